@@ -40,9 +40,9 @@ def listed():
         # the tree workload of the benchmark
         dict(name="sample_tree_batch", op="sample", B=16, N=60, V=128256, depth=6, T=1.0, dtype="bf16"),
         # rows of an odd length, which start at no vector boundary
-        dict(name="sample_odd_vocabulary", op="sample", B=7, N=23, V=32003, depth=4, T=0.8, dtype="bf16"),
+        dict(name="sample_odd_vocabulary", op="sample", B=7, N=23, V=32003, depth=4, T=0.75, dtype="bf16"),
         # a serving batch with float32 logits and the largest vocabulary
-        dict(name="sample_large_f32", op="sample", B=64, N=32, V=151936, depth=8, T=0.7, dtype="f32"),
+        dict(name="sample_large_f32", op="sample", B=64, N=32, V=151936, depth=8, T=0.625, dtype="f32"),
         # a short chat turn with a small chain of drafts, heads not shared
         dict(name="attention_short_chain", op="attention", B=1, N=5, Hkv=8, G=1, D=64, ctx=300, P=0, chain=True),
         # plain decoding: one token of every sequence
@@ -74,7 +74,7 @@ def draw(rng):
             V = max(8, V // 8 * 8)
         N = _log_int(rng, 1, 64)
         return dict(op=op, B=min(_log_int(rng, 1, 64), max(1, 300_000_000 // (N * V))), N=N, V=V, depth=rng.randint(1, 8),
-                    T=round(rng.uniform(0.5, 1.3), 2), dtype=rng.choice(["bf16", "f32"]))
+                    T=rng.randint(16, 40) / 32, dtype=rng.choice(["bf16", "f32"]))
     G, Hkv, D = rng.choice([1, 2, 3, 4, 5, 8]), rng.choice([1, 2, 4, 8]), rng.choice([64, 128])
     B, N = _log_int(rng, 1, 64), _log_int(rng, 1, 64)
     if op == "attention":
