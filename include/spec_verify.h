@@ -92,7 +92,9 @@ typedef enum {
   SPEC_MODE_KV_COMMIT = 4, /* spec_kv_commit_path: the flag header only */
   SPEC_MODE_LM_HEAD_GREEDY = 5, /* spec_lm_head_verify_greedy (k_or_N = k) */
   SPEC_MODE_TREE_GROW = 6,      /* spec_tree_grow (k_or_N = K children per node) */
-  SPEC_MODE_LM_HEAD_SAMPLE = 7  /* spec_lm_head_verify_sample (k_or_N = k, d <= SPEC_LM_MAX_D) */
+  SPEC_MODE_LM_HEAD_SAMPLE = 7, /* spec_lm_head_verify_sample (k_or_N = k, d <= SPEC_LM_MAX_D) */
+  SPEC_MODE_TREE_SAMPLE = 8,    /* spec_verify_tree_sample: the flag header only */
+  SPEC_MODE_TREE_QKV = 10       /* spec_tree_qkv_rope: the flag header only */
 } spec_mode_t;
 
 /* Bits of the workspace flag word (sticky until read with clear != 0). */
@@ -108,7 +110,11 @@ typedef enum {
                                           not start at node 0, names a node
                                           outside [1, N), is longer than
                                           max_depth, or a tree that does not fit
-                                          the cache; that sequence is untouched */
+                                          the cache; that sequence is untouched.
+                                          spec_tree_qkv_rope, spec_tree_attention:
+                                          a tree that does not fit the cache */
+#define SPEC_FLAG_EMPTY_ROW 64u        /* spec_verify_tree_sample: a row on the walk
+                                          without a finite logit; no token drawn */
 
 /* Limits checked on the host. */
 #define SPEC_MAX_V (1 << 26)
@@ -204,6 +210,50 @@ SPEC_API spec_status_t spec_verify_tree_greedy(const void* target_logits, int dt
                                       size_t workspace_bytes, void* stream);
 
 /*
+ * Sampling verification of B draft trees ("EAGLE-3 speculative decoding
+ * review", "Does Using a Small Model's Answer Reduce Quality?", with drafts
+ * that are points: the children that spec_tree_grow picks are the draft's most
+ * probable tokens, not draws from it, so a child x is taken with probability
+ * p(x) and a miss leaves p without the children).  The walk starts at the root.
+ * At a node of depth d with target row z it draws
+ *   x = the smallest j with u_sample[b, d] * R < C_j,
+ * C_j the inclusive prefix sum and R the total of the weights exp(z_j / T),
+ * moves to the lowest-numbered child whose token is x, or ends there.  The
+ * emitted tokens are those that drawing one at a time from softmax(z / T)
+ * with the same uniforms gives, whatever the tree; the tree decides only how
+ * many of them one call emits.
+ *   target_logits [B, N, V]   row v: the target's logits after the path root..v;
+ *                             -inf is a token of probability 0
+ *   node_tokens   int32 [B, N] (node 0's entry is ignored)
+ *   parents       int32 [B, N]  as spec_verify_tree_greedy
+ *   u_sample      float [B, max_depth + 1] in [0, 1)
+ *   temperature   > 0, finite
+ *   max_depth     0..SPEC_MAX_TREE_DEPTH; deeper nodes are not taken
+ * Outputs (device, written in full):
+ *   accepted_len  int32 [B]              depth of the last node of the walk
+ *   path_nodes    int32 [B, max_depth+1] 0, ..., that node, then -1
+ *   out_tokens    int32 [B, max_depth+1] the tokens drawn at those nodes (the
+ *                                        last one is the new token), then -1
+ *   out_probs     float [B, max_depth+1] their probabilities, then 0
+ * so that spec_kv_commit_path takes accepted_len and path_nodes as they are.
+ * Prefix sums are exact 64-bit integers of weights held to 2^-45 of the
+ * largest.  A row without a finite logit draws nothing (token -1, probability
+ * 0, SPEC_FLAG_EMPTY_ROW) and ends the walk.  Malformed nodes are never taken
+ * (SPEC_FLAG_BAD_PARENT, SPEC_FLAG_TOKEN_RANGE); SPEC_FLAG_DEPTH is set when
+ * the walk would have gone below max_depth.  Only the rows on the walk are
+ * read.  One launch of a cluster of up to 16 CTAs per sequence.  Workspace:
+ * spec_verify_workspace_bytes(SPEC_MODE_TREE_SAMPLE, ...) bytes (the flag
+ * header).
+ */
+SPEC_API spec_status_t spec_verify_tree_sample(const void* target_logits, int dtype,
+                                               const int32_t* node_tokens, const int32_t* parents,
+                                               const float* u_sample, float temperature, int B,
+                                               int N, int V, int max_depth, int32_t* accepted_len,
+                                               int32_t* path_nodes, int32_t* out_tokens,
+                                               float* out_probs, void* workspace,
+                                               size_t workspace_bytes, void* stream);
+
+/*
  * Tree attention mask of B draft trees ("EAGLE-3 speculative decoding
  * review", "EAGLE-2: Does Every Context Need the Same Draft Tree?" and "Must
  * the Feature Be Predicted Exactly?": each node sees the shared prefix and
@@ -226,6 +276,81 @@ SPEC_API spec_status_t spec_verify_tree_greedy(const void* target_logits, int dt
 SPEC_API spec_status_t spec_tree_attention_mask(const int32_t* parents, int B, int N,
                                                 uint32_t* mask, int32_t* depth, void* workspace,
                                                 size_t workspace_bytes, void* stream);
+
+/*
+ * Query, key and value heads of the tree's nodes, ready for spec_tree_attention
+ * ("EAGLE-3 speculative decoding review", "The Complete EAGLE-3 Inference
+ * Process" step 3: the target scores all nodes in one pass).  Node v of
+ * sequence b stands at position pos_offset + base_len[b] - 1 + depth[b, v] (the
+ * root is the last committed token).  Query and key heads are normalised,
+ *   y = x / sqrt(mean(x^2) + eps) * w   (a null w: no norm),
+ * and their first rot_dim elements rotated in pairs by position * inv_freq[i],
+ *   (a, b) -> (a cos - b sin, b cos + a sin),
+ * in float32 (positions and angles exactly), rounded once.  Queries go to
+ * q_out; keys and values go to cache position base_len[b] - 1 + v, where
+ * spec_kv_commit_path expects them.
+ *   qkv           bf16 [B, N, Hq + 2 Hkv, D]: query, key, value heads
+ *   q_norm,k_norm bf16 [D] or NULL
+ *   inv_freq      float [rot_dim / 2] (NULL when rot_dim = 0), finite
+ *   rot_dim       even, 0..D;  interleaved: 0 pairs (i, i + rot_dim / 2),
+ *                 else (2i, 2i + 1)
+ *   pos_offset    >= 0 (the length of a prefix shared by the batch)
+ *   base_len      int32 [B]; depth int32 [B, N] or NULL (a chain: node v at
+ *                 depth v); a negative depth counts as 0 and raises
+ *                 SPEC_FLAG_BAD_PARENT
+ *   q_out         bf16 [B, N, Hq, D]
+ *   k_cache, v_cache bf16: sequence b's position t starts seq_stride * b +
+ *                 t * Hkv * D * 2 bytes in; L positions per sequence
+ * D is 64 or 128; qkv, q_out, the norms and the caches 16-byte aligned,
+ * seq_stride a multiple of 16.  A sequence whose tree does not fit the cache
+ * (base_len < 1 or base_len + N - 1 > L) writes no key or value, gets queries
+ * of 0 and raises SPEC_FLAG_BAD_PATH.  One launch.  Workspace:
+ * spec_verify_workspace_bytes(SPEC_MODE_TREE_QKV, ...) bytes (the flag header).
+ */
+SPEC_API spec_status_t spec_tree_qkv_rope(const void* qkv, const void* q_norm, const void* k_norm,
+                                          float eps, const float* inv_freq, int rot_dim,
+                                          int interleaved, long long pos_offset,
+                                          const int32_t* base_len, const int32_t* depth, int B,
+                                          int N, int Hq, int Hkv, int D, int L,
+                                          long long seq_stride, void* q_out, void* k_cache,
+                                          void* v_cache, void* workspace, size_t workspace_bytes,
+                                          void* stream);
+
+/*
+ * Attention of the tree's nodes over the KV cache ("EAGLE-3 speculative
+ * decoding review", "EAGLE-2: Does Every Context Need the Same Draft Tree?":
+ * a node sees the committed prefix and its own ancestors).  Query head
+ * h G + g (G = Hq / Hkv) reads key-value head h:
+ *   out = sum_j softmax_j(scale q . k_j) v_j
+ * over j in
+ *   - the shared prefix: prefix_k/v entries [0, P), one copy for the batch;
+ *   - the sequence's own positions [0, base_len[b] - 1);
+ *   - the tree's entries base_len[b] - 1 + u for the set bits u < N of the
+ *     node's mask row (spec_tree_attention_mask; NULL: u <= v, a chain).
+ * Entries that a node does not see are never used, whatever they hold.  A
+ * node that sees nothing gets out = 0 and lse = -inf.
+ *   q          bf16 [B, N, Hq, D]
+ *   k_cache, v_cache bf16, layout as in spec_tree_qkv_rope
+ *   prefix_k, prefix_v bf16 [P, Hkv, D] (NULL when P = 0)
+ *   mask       uint32 [B, N, ceil(N/32)] or NULL
+ *   base_len   int32 [B]; scale > 0, finite
+ *   out        bf16 [B, N, Hq, D]
+ *   lse        float [B, N, Hq] or NULL: ln sum_j exp(scale q . k_j)
+ * N = 1 without a mask is plain decoding.  D is 64 or 128, Hq a multiple of
+ * Hkv, G at most 128, N at most SPEC_ATTN_MAX_NODES; q, out, the caches and
+ * prefixes 16-byte aligned, seq_stride a multiple of 16.  A sequence whose
+ * tree does not fit the cache (base_len < 1 or base_len + N - 1 > L) gets out
+ * = 0, lse = -inf and raises SPEC_FLAG_BAD_PATH.  Workspace: at least
+ * spec_tree_attention_workspace_bytes() bytes.
+ */
+#define SPEC_ATTN_MAX_NODES 4096
+SPEC_API size_t spec_tree_attention_workspace_bytes(int B, int N, int Hq, int Hkv, int D, int P);
+SPEC_API spec_status_t spec_tree_attention(const void* q, const void* k_cache, const void* v_cache,
+                                           long long seq_stride, int L, const void* prefix_k,
+                                           const void* prefix_v, int P, const uint32_t* mask,
+                                           const int32_t* base_len, int B, int N, int Hq, int Hkv,
+                                           int D, float scale, void* out, float* lse,
+                                           void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * KV commit of the accepted path ("EAGLE-3 speculative decoding review",

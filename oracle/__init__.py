@@ -77,6 +77,12 @@ def _bind(lib):
     lib.oracle_lm_head_greedy.restype = I
     lib.oracle_tree_grow.argtypes = [P, I, I, I, I, I, D, I, P, P, P, P, P]
     lib.oracle_tree_grow.restype = I
+    lib.oracle_verify_tree_sample.argtypes = [P, I, P, P, P, I, I, I, I, D, P, P, P, P, P]
+    lib.oracle_verify_tree_sample.restype = I
+    lib.oracle_tree_qkv.argtypes = [P, P, P, D, P, I, I, LL, P, P, I, I, I, I, I, I, P, P, P]
+    lib.oracle_tree_qkv.restype = I
+    lib.oracle_tree_attention.argtypes = [P, P, P, P, P, I, P, P, I, I, I, I, I, I, D, P, P]
+    lib.oracle_tree_attention.restype = I
     lib.oracle_expected_tokens.argtypes = [D, I]
     lib.oracle_expected_tokens.restype = D
     lib.oracle_speedup_model.argtypes = [D, I, D]
@@ -350,6 +356,75 @@ def tree_grow(logits, temperature, M, dtype="bf16", lib=None):
                               _ptr(out["values"]), _ptr(out["min_gap"]))
     _check(rc)
     return out
+
+
+def verify_tree_sample(target, tokens, parents, u, temperature, max_depth, dtype="bf16", lib=None):
+    """Sampling verification of draft trees (reading R14 of spec_oracle.c).
+    ``margin`` [B]: how near the walk's draws came to a border of their token."""
+    lib = lib or _load()
+    target = _logits(target, dtype)
+    B, N, V = target.shape
+    W = max_depth + 1
+    tokens = np.ascontiguousarray(tokens, dtype=np.int32).reshape(B, N)
+    parents = np.ascontiguousarray(parents, dtype=np.int32).reshape(B, N)
+    u = np.ascontiguousarray(u, dtype=np.float32).reshape(B, W)
+    out = dict(accepted_len=np.zeros(B, np.int32), path_nodes=np.zeros((B, W), np.int32),
+               out_tokens=np.zeros((B, W), np.int32), out_probs=np.zeros((B, W)),
+               margin=np.zeros(B))
+    _check(lib.oracle_verify_tree_sample(_ptr(target), _dtype_code(dtype), _ptr(tokens),
+                                         _ptr(parents), _ptr(u), B, N, V, int(max_depth),
+                                         float(temperature), _ptr(out["accepted_len"]),
+                                         _ptr(out["path_nodes"]), _ptr(out["out_tokens"]),
+                                         _ptr(out["out_probs"]), _ptr(out["margin"])))
+    return out
+
+
+def _opt(a):
+    return None if a is None else _ptr(a)
+
+
+def tree_qkv(qkv, q_norm, k_norm, eps, inv_freq, base_len, depth, Hkv, L, offset=0,
+             interleaved=False, lib=None):
+    """Head norms, rotation and cache positions (reading R16): ``qkv`` bf16 bits
+    [B, N, H, D].  Returns float64 (q [B, N, Hq, D], k, v [B, L, Hkv, D], NaN
+    where nothing is written)."""
+    lib = lib or _load()
+    qkv = np.ascontiguousarray(qkv, dtype=np.uint16)
+    B, N, H, D = qkv.shape
+    Hq = H - 2 * Hkv
+    q_norm, k_norm = (None if w is None else np.ascontiguousarray(w, dtype=np.uint16)
+                      for w in (q_norm, k_norm))
+    inv_freq = np.ascontiguousarray(inv_freq, dtype=np.float32)
+    base_len = np.ascontiguousarray(base_len, dtype=np.int32)
+    depth = None if depth is None else np.ascontiguousarray(depth, dtype=np.int32)
+    assert ((base_len >= 1) & (base_len + N - 1 <= L)).all()
+    q = np.full((B, N, Hq, D), np.nan)
+    k, v = np.full((B, L, Hkv, D), np.nan), np.full((B, L, Hkv, D), np.nan)
+    _check(lib.oracle_tree_qkv(_ptr(qkv), _opt(q_norm), _opt(k_norm), float(eps), _ptr(inv_freq),
+                               2 * len(inv_freq), int(interleaved), int(offset), _ptr(base_len),
+                               _opt(depth), B, N, Hq, Hkv, D, L, _ptr(q), _ptr(k), _ptr(v)))
+    return q, k, v
+
+
+def tree_attention(q, k, v, mask, base_len, scale, prefix_k=None, prefix_v=None, lib=None):
+    """Attention of the tree's nodes (reading R15) on bf16 bits: q [B, N, Hq, D],
+    k, v [B, L, Hkv, D], prefix_k, prefix_v [P, Hkv, D]; returns float64
+    (out [B, N, Hq, D], lse [B, N, Hq])."""
+    lib = lib or _load()
+    q, k, v = (np.ascontiguousarray(a, dtype=np.uint16) for a in (q, k, v))
+    B, N, Hq, D = q.shape
+    L, Hkv = k.shape[1:3]
+    P = 0 if prefix_k is None else len(prefix_k)
+    prefix_k, prefix_v = (None if a is None else np.ascontiguousarray(a, dtype=np.uint16)
+                          for a in (prefix_k, prefix_v))
+    mask = None if mask is None else np.ascontiguousarray(mask).view(np.uint32)
+    base_len = np.ascontiguousarray(base_len, dtype=np.int32)
+    assert ((base_len >= 1) & (base_len + N - 1 <= L)).all()
+    out, lse = np.zeros((B, N, Hq, D)), np.zeros((B, N, Hq))
+    _check(lib.oracle_tree_attention(_ptr(q), _ptr(k), _ptr(v), _opt(prefix_k), _opt(prefix_v), P,
+                                     _opt(mask), _ptr(base_len), B, N, Hq, Hkv, D, L, float(scale),
+                                     _ptr(out), _ptr(lse)))
+    return out, lse
 
 
 def expected_tokens(alpha: float, gamma: int, lib=None) -> float:

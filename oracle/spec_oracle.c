@@ -69,7 +69,20 @@
  *      with parents renumbered.  A child never outranks its parent (ln q
  *      <= 0 and the parent was created first), so the tree is closed under
  *      ancestors.
- *   Non-finite logits are outside the method's domain (rejected here).
+ *   R14 Tree sampling: at node v (the root first) of depth d the next token is
+ *      the inverse-CDF draw (R5) of softmax(z_v / T) with u[b, d]; the walk
+ *      goes on to the lowest-numbered child holding that token, if there is
+ *      one and d < max_depth, and else ends with the token as its last.  A
+ *      logit of -inf is a token of probability 0; a row of only those draws
+ *      nothing (token -1, probability 0) and ends the walk.
+ *   R15 Tree attention: node v sees the shared prefix, its sequence's first
+ *      base - 1 positions, and the tree entries base - 1 + u whose bit u is
+ *      set in its mask row (no mask: u <= v).  What it does not see is not
+ *      read.  Nothing visible: output 0, log-sum -inf.
+ *   R16 Positions: node v stands at offset + base - 1 + depth(v); its key and
+ *      value entries are cache position base - 1 + v.
+ *   Non-finite logits are outside the method's domain (rejected here; R14
+ *   admits -inf).
  */
 #include <math.h>
 #include <stdint.h>
@@ -537,6 +550,162 @@ int oracle_verify_tree_greedy(const void* target, int dtype, const int32_t* node
   free(depth);
   free(ok);
   return rc;
+}
+
+/*
+ * Tree sampling verification.  [REVIEW] "Does Using a Small Model's Answer
+ * Reduce Quality?" (accept test and residual, for drafts that are points);
+ * [MATH] "EAGLE-2: dynamic draft trees".  Reading R14.
+ *
+ * target [B, N, V], node_tokens, parents [B, N], u [B, max_depth + 1].
+ * Outputs: accepted_len [B]; path_nodes, out_tokens, probs [B, max_depth + 1]
+ * (unused -1, -1, 0); margin [B] (may be NULL): smallest distance of u R to
+ * the borders of the drawn token, over R, along the walk.
+ */
+int oracle_verify_tree_sample(const void* target, int dtype, const int32_t* node_tokens,
+                              const int32_t* parents, const float* u, int B, int N, int V,
+                              int max_depth, double T, int32_t* accepted_len, int32_t* path_nodes,
+                              int32_t* out_tokens, double* probs, double* margin) {
+  if (B < 0 || N < 1 || V < 1 || max_depth < 0 || !(T > 0)) return OR_ERR_ARG;
+  const int W = max_depth + 1;
+  double* w = (double*)malloc(sizeof(double) * (size_t)V);
+  if (!w) return OR_ERR_NOMEM;
+  for (int b = 0; b < B; ++b) {
+    const int32_t* par = parents + (size_t)b * N;
+    const int32_t* tok = node_tokens + (size_t)b * N;
+    for (int i = 0; i < W; ++i) {
+      path_nodes[(size_t)b * W + i] = -1;
+      out_tokens[(size_t)b * W + i] = -1;
+      probs[(size_t)b * W + i] = 0.0;
+    }
+    if (margin) margin[b] = INFINITY;
+    int cur = 0, d = 0;
+    for (;;) {
+      const size_t off = ((size_t)b * N + cur) * (size_t)V;
+      double m = -INFINITY, R = 0.0, edge = INFINITY;
+      for (int j = 0; j < V; ++j) {
+        double z = logit_at(target, dtype, off + (size_t)j);
+        if (z > m) m = z;
+      }
+      for (int j = 0; j < V; ++j)
+        w[j] = isinf(m) ? 0.0 : exp((logit_at(target, dtype, off + (size_t)j) - m) / T);
+      path_nodes[(size_t)b * W + d] = cur;
+      int x = -1;
+      if (!isinf(m)) x = inverse_cdf(w, V, (double)u[(size_t)b * W + d], &R, &edge);
+      out_tokens[(size_t)b * W + d] = x;
+      if (x >= 0) probs[(size_t)b * W + d] = w[x] / R;
+      if (margin && edge < margin[b]) margin[b] = edge;
+      int child = -1;
+      for (int v = cur + 1; v < N && child < 0; ++v)
+        if (par[v] == cur && tok[v] == x && x >= 0) child = v;
+      if (child < 0 || d == max_depth) break;
+      cur = child;
+      ++d;
+    }
+    accepted_len[b] = d;
+  }
+  free(w);
+  return OR_OK;
+}
+
+/*
+ * Head norms, rotation and cache write of the tree's nodes.  Reading R16;
+ * [REVIEW] "The Complete EAGLE-3 Inference Process" step 3.
+ *
+ * qkv bf16 [B, N, Hq + 2 Hkv, D]; qn, kn bf16 [D] or NULL; inv_freq [rot/2];
+ * depth [B, N] or NULL; q_out float64 [B, N, Hq, D]; k_out, v_out float64
+ * [B, L, Hkv, D], of which only the written positions change.
+ */
+int oracle_tree_qkv(const uint16_t* qkv, const uint16_t* qn, const uint16_t* kn, double eps,
+                    const float* inv_freq, int rot, int interleaved, long long offset,
+                    const int32_t* base, const int32_t* depth, int B, int N, int Hq, int Hkv,
+                    int D, int L, double* q_out, double* k_out, double* v_out) {
+  const int H = Hq + 2 * Hkv;
+  double x[1024];
+  if (D > 1024) return OR_ERR_ARG;
+  for (int b = 0; b < B; ++b)
+    for (int v = 0; v < N; ++v)
+      for (int h = 0; h < H; ++h) {
+        const size_t row = (((size_t)b * N + v) * H + h) * (size_t)D;
+        for (int i = 0; i < D; ++i) x[i] = logit_at(qkv, OR_BF16, row + (size_t)i);
+        const int is_v = h >= Hq + Hkv;
+        if (!is_v) {
+          const uint16_t* w = h < Hq ? qn : kn;
+          if (w) {
+            double s = 0.0;
+            for (int i = 0; i < D; ++i) s += x[i] * x[i];
+            s = 1.0 / sqrt(s / D + eps);
+            for (int i = 0; i < D; ++i) x[i] *= s * logit_at(w, OR_BF16, (size_t)i);
+          }
+          const double pos = (double)(offset + base[b] - 1 + (depth ? depth[(size_t)b * N + v] : v));
+          for (int i = 0; i < rot / 2; ++i) {
+            const int a = interleaved ? 2 * i : i, c = interleaved ? 2 * i + 1 : i + rot / 2;
+            const double t = pos * (double)inv_freq[i], xa = x[a], xc = x[c];
+            x[a] = xa * cos(t) - xc * sin(t);
+            x[c] = xc * cos(t) + xa * sin(t);
+          }
+        }
+        const size_t at = ((size_t)b * L + (size_t)(base[b] - 1 + v)) * Hkv;
+        double* dst = h < Hq ? q_out + (((size_t)b * N + v) * Hq + h) * (size_t)D
+                             : (is_v ? v_out + (at + (size_t)(h - Hq - Hkv)) * D
+                                     : k_out + (at + (size_t)(h - Hq)) * D);
+        for (int i = 0; i < D; ++i) dst[i] = x[i];
+      }
+  return OR_OK;
+}
+
+/*
+ * Attention of the tree's nodes.  Reading R15; [REVIEW] "EAGLE-2: Does Every
+ * Context Need the Same Draft Tree?".
+ *
+ * q bf16 [B, N, Hq, D]; k, v bf16 [B, L, Hkv, D]; pk, pv bf16 [P, Hkv, D];
+ * mask [B, N, W] or NULL; out float64 [B, N, Hq, D], lse float64 [B, N, Hq].
+ */
+int oracle_tree_attention(const uint16_t* q, const uint16_t* k, const uint16_t* v,
+                          const uint16_t* pk, const uint16_t* pv, int P, const uint32_t* mask,
+                          const int32_t* base, int B, int N, int Hq, int Hkv, int D, int L,
+                          double scale, double* out, double* lse) {
+  const int G = Hq / Hkv, W = (N + 31) / 32;
+  double* s = (double*)malloc(sizeof(double) * (size_t)(P + L + 1));
+  size_t* at = (size_t*)malloc(sizeof(size_t) * (size_t)(P + L + 1));
+  if (!s || !at) { free(s); free(at); return OR_ERR_NOMEM; }
+  for (int b = 0; b < B; ++b)
+    for (int n = 0; n < N; ++n)
+      for (int h = 0; h < Hq; ++h) {
+        const size_t qo = (((size_t)b * N + n) * Hq + h) * (size_t)D;
+        const int hk = h / G;
+        int cnt = 0;
+        for (int j = 0; j < P; ++j) at[cnt++] = ((size_t)j * Hkv + hk) * (size_t)D;
+        for (int t = 0; t < base[b] - 1 + N; ++t) {
+          const int u = t - (base[b] - 1);
+          if (u >= 0) {
+            const int sees = mask ? (mask[((size_t)b * N + n) * W + u / 32] >> (u % 32)) & 1 : u <= n;
+            if (!sees) continue;
+          }
+          at[cnt++] = (((size_t)b * L + t) * Hkv + hk) * (size_t)D;
+        }
+        double m = -INFINITY, total = 0.0;
+        for (int j = 0; j < cnt; ++j) {
+          double dot = 0.0;
+          for (int i = 0; i < D; ++i)
+            dot += logit_at(q, OR_BF16, qo + i) * logit_at(j < P ? pk : k, OR_BF16, at[j] + i);
+          s[j] = scale * dot;
+          if (s[j] > m) m = s[j];
+        }
+        for (int j = 0; j < cnt; ++j) {
+          s[j] = exp(s[j] - m);
+          total += s[j];
+        }
+        for (int i = 0; i < D; ++i) {
+          double o = 0.0;
+          for (int j = 0; j < cnt; ++j) o += s[j] * logit_at(j < P ? pv : v, OR_BF16, at[j] + i);
+          out[qo + i] = cnt ? o / total : 0.0;
+        }
+        lse[((size_t)b * N + n) * Hq + h] = cnt ? m + log(total) : -INFINITY;
+      }
+  free(s);
+  free(at);
+  return OR_OK;
 }
 
 /*

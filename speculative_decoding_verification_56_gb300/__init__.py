@@ -15,12 +15,18 @@ Entry points (same names as the C ABI):
 * :func:`spec_lm_head_verify_greedy` -- LM head (tcgen05 GEMM) fused with greedy verification
 * :func:`spec_lm_head_verify_sample` -- LM head (tcgen05 GEMM) fused with sampling verification
 * :func:`spec_tree_grow`          -- EAGLE-2 dynamic draft-tree growth
-* :func:`spec_verify_workspace_bytes`, :func:`spec_verify_read_flags`,
+* :func:`spec_tree_qkv_rope`      -- head norms, rotation and cache write of the tree's nodes
+* :func:`spec_tree_attention`     -- attention of the tree's nodes over the cache and a shared prefix
+* :func:`spec_verify_tree_sample` -- sampling verification of draft trees
+* :func:`spec_verify_workspace_bytes`, :func:`spec_tree_attention_workspace_bytes`,
+  :func:`spec_verify_read_flags`,
   :func:`spec_verify_launch_count`, :func:`spec_status_string`
 
 Convenience wrappers that also allocate outputs and a workspace with torch:
 :func:`verify_sample`, :func:`verify_greedy`, :func:`verify_tree_greedy`,
-:func:`tree_attention_mask`.
+:func:`tree_attention_mask`, :func:`lm_head_verify_greedy`,
+:func:`lm_head_verify_sample`, :func:`tree_grow`, :func:`tree_qkv_rope`,
+:func:`tree_attention`, :func:`verify_tree_sample`.
 """
 from __future__ import annotations
 
@@ -48,6 +54,9 @@ SPEC_MODE_KV_COMMIT = 4
 SPEC_MODE_LM_HEAD_GREEDY = 5
 SPEC_MODE_TREE_GROW = 6
 SPEC_MODE_LM_HEAD_SAMPLE = 7
+SPEC_MODE_TREE_SAMPLE = 8
+SPEC_MODE_TREE_QKV = 10
+SPEC_ATTN_MAX_NODES = 4096
 SPEC_LM_MAX_D = 8192
 SPEC_FLAG_TOKEN_RANGE = 1
 SPEC_FLAG_BAD_PARENT = 2
@@ -55,6 +64,7 @@ SPEC_FLAG_DEPTH = 4
 SPEC_FLAG_RESIDUAL_FALLBACK = 8
 SPEC_FLAG_TIMEOUT = 16
 SPEC_FLAG_BAD_PATH = 32
+SPEC_FLAG_EMPTY_ROW = 64
 
 _lock = threading.Lock()
 _lib = None
@@ -102,6 +112,16 @@ def load_library(path: str = LIB_PATH):
         lib.spec_lm_head_verify_sample.restype = I
         lib.spec_tree_grow.argtypes = [P, I, F, I, I, I, I, I, P, P, P, P, P, Z, P]
         lib.spec_tree_grow.restype = I
+        lib.spec_verify_tree_sample.argtypes = [P, I, P, P, P, F, I, I, I, I, P, P, P, P, P, Z, P]
+        lib.spec_verify_tree_sample.restype = I
+        lib.spec_tree_qkv_rope.argtypes = [P, P, P, F, P, I, I, LL, P, P, I, I, I, I, I, I, LL, P,
+                                           P, P, P, Z, P]
+        lib.spec_tree_qkv_rope.restype = I
+        lib.spec_tree_attention_workspace_bytes.argtypes = [I, I, I, I, I, I]
+        lib.spec_tree_attention_workspace_bytes.restype = Z
+        lib.spec_tree_attention.argtypes = [P, P, P, LL, I, P, P, I, P, P, I, I, I, I, I, F, P, P,
+                                            P, Z, P]
+        lib.spec_tree_attention.restype = I
         lib.spec_verify_read_flags.argtypes = [P, ctypes.POINTER(ctypes.c_uint32), I, P]
         lib.spec_verify_read_flags.restype = I
         lib.spec_verify_launch_count.argtypes = []
@@ -147,6 +167,52 @@ def _dev(t, name, dtype=None, optional=False):
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     return t.data_ptr()
+
+
+def _arg(t, name, dtype, shape, device):
+    """Pointer of a contiguous CUDA tensor of the given type and shape on the
+    call's device."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on cuda:{device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _call_device(t, name):
+    """Index of the CUDA device that a call runs on: its tensors' device, which
+    has to be the current one."""
+    torch = _torch()
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{name} is on cuda:{dev}, which is not the current device")
+    return dev
+
+
+def _cache_args(k_cache, v_cache, Hkv, D, B, device):
+    """Pointers, byte stride between sequences and positions of a layer's key
+    and value cache [B, L, Hkv, D] (sequences may lie further apart)."""
+    torch = _torch()
+    L = k_cache.shape[1] if k_cache.dim() == 4 else 0
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        if t.dtype != torch.bfloat16:
+            raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
+        if t.shape != (B, L, Hkv, D):
+            raise ValueError(f"{name} must be [{B}, L, {Hkv}, {D}], got {list(t.shape)}")
+        if t.get_device() != device:
+            raise ValueError(f"{name} must be on cuda:{device}")
+        if t.stride()[1:] != (Hkv * D, D, 1) and t.numel() > 0:
+            raise ValueError(f"{name}: the positions of a sequence must be contiguous")
+    s = max(k_cache.stride(0), L * Hkv * D) if B <= 1 else k_cache.stride(0)
+    if B > 1 and v_cache.stride(0) != s:
+        raise ValueError("k_cache and v_cache must have the same strides")
+    return k_cache.data_ptr(), v_cache.data_ptr(), s * 2, L
 
 
 def _stream_ptr(stream):
@@ -376,6 +442,99 @@ def spec_tree_grow(draft_logits, temperature, M, tokens, parents, depth, values,
     _check(st, "spec_tree_grow")
 
 
+def spec_verify_tree_sample(target_logits, node_tokens, parents, u_sample, temperature, max_depth,
+                            accepted_len, path_nodes, out_tokens, out_probs, workspace,
+                            stream=None):
+    """Sampling verification of draft trees (C ABI ``spec_verify_tree_sample``).
+
+    target_logits [B, N, V] (bf16 or fp32); node_tokens, parents int32 [B, N];
+    u_sample float32 [B, max_depth+1].  Outputs: accepted_len int32 [B];
+    path_nodes, out_tokens int32 and out_probs float32 [B, max_depth+1].
+    """
+    torch = _torch()
+    dev = _call_device(target_logits, "target_logits")
+    B, N, V = target_logits.shape
+    W = int(max_depth) + 1
+    i32, f32 = torch.int32, torch.float32
+    st = load_library().spec_verify_tree_sample(
+        _dev(target_logits, "target_logits"), _dtype_code(target_logits),
+        _arg(node_tokens, "node_tokens", i32, (B, N), dev),
+        _arg(parents, "parents", i32, (B, N), dev), _arg(u_sample, "u_sample", f32, (B, W), dev),
+        float(temperature), B, N, V, W - 1, _arg(accepted_len, "accepted_len", i32, (B,), dev),
+        _arg(path_nodes, "path_nodes", i32, (B, W), dev),
+        _arg(out_tokens, "out_tokens", i32, (B, W), dev),
+        _arg(out_probs, "out_probs", f32, (B, W), dev), _dev(workspace, "workspace"),
+        workspace.numel() * workspace.element_size(), _stream_ptr(stream))
+    _check(st, "spec_verify_tree_sample")
+
+
+def spec_tree_qkv_rope(qkv, q_norm, k_norm, eps, inv_freq, base_len, depth, q_out, k_cache,
+                       v_cache, workspace, pos_offset=0, interleaved=False, stream=None):
+    """Head norms, rotation and cache write of the tree's nodes (C ABI
+    ``spec_tree_qkv_rope``).
+
+    qkv bf16 [B, N, Hq + 2 Hkv, D]; q_norm, k_norm bf16 [D] or None; inv_freq
+    float32 [rot_dim / 2]; base_len int32 [B]; depth int32 [B, N] or None (a
+    chain); q_out bf16 [B, N, Hq, D]; k_cache, v_cache bf16 [B, L, Hkv, D],
+    written at positions base_len - 1 + node.
+    """
+    torch = _torch()
+    dev = _call_device(qkv, "qkv")
+    B, N, H, D = qkv.shape
+    Hkv = k_cache.shape[2] if k_cache.dim() == 4 else 0
+    Hq = H - 2 * Hkv
+    bf16 = torch.bfloat16
+    kp, vp, stride, L = _cache_args(k_cache, v_cache, Hkv, D, B, dev)
+    st = load_library().spec_tree_qkv_rope(
+        _arg(qkv, "qkv", bf16, (B, N, H, D), dev),
+        None if q_norm is None else _arg(q_norm, "q_norm", bf16, (D,), dev),
+        None if k_norm is None else _arg(k_norm, "k_norm", bf16, (D,), dev), float(eps),
+        _arg(inv_freq, "inv_freq", torch.float32, (inv_freq.numel(),), dev), 2 * inv_freq.numel(),
+        1 if interleaved else 0, int(pos_offset),
+        _arg(base_len, "base_len", torch.int32, (B,), dev),
+        None if depth is None else _arg(depth, "depth", torch.int32, (B, N), dev), B, N, Hq, Hkv,
+        D, L, stride, _arg(q_out, "q_out", bf16, (B, N, Hq, D), dev), kp, vp,
+        _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(),
+        _stream_ptr(stream))
+    _check(st, "spec_tree_qkv_rope")
+
+
+def spec_tree_attention_workspace_bytes(B: int, N: int, Hq: int, Hkv: int, D: int,
+                                        P: int = 0) -> int:
+    return int(load_library().spec_tree_attention_workspace_bytes(B, N, Hq, Hkv, D, P))
+
+
+def spec_tree_attention(q, k_cache, v_cache, mask, base_len, scale, out, lse, workspace,
+                        prefix_k=None, prefix_v=None, stream=None):
+    """Attention of the tree's nodes (C ABI ``spec_tree_attention``).
+
+    q, out bf16 [B, N, Hq, D]; k_cache, v_cache bf16 [B, L, Hkv, D]; mask
+    int32 [B, N, ceil(N/32)] (:func:`tree_attention_mask`) or None for a
+    chain; base_len int32 [B]; lse float32 [B, N, Hq] or None; prefix_k,
+    prefix_v bf16 [P, Hkv, D], a prefix that the whole batch shares, or None.
+    """
+    torch = _torch()
+    dev = _call_device(q, "q")
+    B, N, Hq, D = q.shape
+    Hkv = k_cache.shape[2] if k_cache.dim() == 4 else 0
+    bf16 = torch.bfloat16
+    kp, vp, stride, L = _cache_args(k_cache, v_cache, Hkv, D, B, dev)
+    if (prefix_k is None) != (prefix_v is None):
+        raise ValueError("prefix_k and prefix_v go together")
+    P = 0 if prefix_k is None else prefix_k.shape[0]
+    st = load_library().spec_tree_attention(
+        _arg(q, "q", bf16, (B, N, Hq, D), dev), kp, vp, stride, L,
+        _arg(prefix_k, "prefix_k", bf16, (P, Hkv, D), dev) if P else None,
+        _arg(prefix_v, "prefix_v", bf16, (P, Hkv, D), dev) if P else None, P,
+        None if mask is None else _arg(mask, "mask", torch.int32, (B, N, (N + 31) // 32), dev),
+        _arg(base_len, "base_len", torch.int32, (B,), dev), B, N, Hq, Hkv, D, float(scale),
+        _arg(out, "out", bf16, (B, N, Hq, D), dev),
+        None if lse is None else _arg(lse, "lse", torch.float32, (B, N, Hq), dev),
+        _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(),
+        _stream_ptr(stream))
+    _check(st, "spec_tree_attention")
+
+
 def spec_verify_read_flags(workspace, clear: bool = True, stream=None) -> int:
     """Device flag bits recorded in ``workspace`` (synchronises the stream)."""
     out = ctypes.c_uint32(0)
@@ -513,6 +672,72 @@ def tree_grow(draft_logits, temperature, M, workspace=None, stream=None):
     spec_tree_grow(draft_logits, temperature, M, out["tokens"], out["parents"], out["depth"],
                    out["values"], workspace, stream)
     return out
+
+
+def verify_tree_sample(target_logits, node_tokens, parents, u_sample, temperature, max_depth,
+                       workspace=None, stream=None):
+    """Sampling verification of B draft trees; returns dict(accepted_len,
+    path_nodes, out_tokens, out_probs)."""
+    torch = _torch()
+    B, N, V = target_logits.shape
+    dev = target_logits.device
+    if workspace is None:
+        workspace = alloc_workspace(SPEC_MODE_TREE_SAMPLE, B, N, V, _dtype_code(target_logits),
+                                    dev)
+    W = int(max_depth) + 1
+    i32 = dict(dtype=torch.int32, device=dev)
+    out = dict(accepted_len=torch.empty(B, **i32), path_nodes=torch.empty(B, W, **i32),
+               out_tokens=torch.empty(B, W, **i32),
+               out_probs=torch.empty(B, W, dtype=torch.float32, device=dev))
+    spec_verify_tree_sample(target_logits, node_tokens, parents, u_sample, temperature, max_depth,
+                            out["accepted_len"], out["path_nodes"], out["out_tokens"],
+                            out["out_probs"], workspace, stream)
+    return out
+
+
+def tree_qkv_rope(qkv, q_norm, k_norm, eps, inv_freq, base_len, depth, k_cache, v_cache,
+                  pos_offset=0, interleaved=False, workspace=None, stream=None):
+    """Normalise and rotate the tree's query and key heads and write its keys
+    and values into the cache; returns the queries [B, N, Hq, D]."""
+    torch = _torch()
+    B, N, H, D = qkv.shape
+    if workspace is None:
+        workspace = alloc_workspace(SPEC_MODE_TREE_QKV, B, N, 1, SPEC_DTYPE_BF16, qkv.device)
+    q = torch.empty(B, N, H - 2 * k_cache.shape[2], D, dtype=qkv.dtype, device=qkv.device)
+    spec_tree_qkv_rope(qkv, q_norm, k_norm, eps, inv_freq, base_len, depth, q, k_cache, v_cache,
+                       workspace, pos_offset, interleaved, stream)
+    return q
+
+
+def alloc_tree_attention_workspace(q, k_cache, prefix_k=None):
+    """Workspace of :func:`spec_tree_attention` for these shapes (its flag word
+    is zero; the rest needs no value)."""
+    torch = _torch()
+    B, N, Hq, D = q.shape
+    n = spec_tree_attention_workspace_bytes(B, N, Hq, k_cache.shape[2], D,
+                                            0 if prefix_k is None else prefix_k.shape[0])
+    if n == 0:
+        raise ValueError("shape outside the library's limits")
+    ws = torch.empty(n, dtype=torch.uint8, device=q.device)
+    ws[:256].zero_()
+    return ws
+
+
+def tree_attention(q, k_cache, v_cache, mask, base_len, scale=None, prefix_k=None, prefix_v=None,
+                   workspace=None, stream=None):
+    """Attention of the tree's nodes over a shared prefix, the cached positions
+    and their ancestors; returns ``(out, lse)``.  ``scale`` defaults to
+    1 / sqrt(D)."""
+    torch = _torch()
+    if workspace is None:
+        workspace = alloc_tree_attention_workspace(q, k_cache, prefix_k)
+    if scale is None:
+        scale = q.shape[3] ** -0.5
+    out = torch.empty_like(q)
+    lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+    spec_tree_attention(q, k_cache, v_cache, mask, base_len, scale, out, lse, workspace,
+                        prefix_k, prefix_v, stream)
+    return out, lse
 
 
 def to_device_logits(arr, dtype: str, device="cuda"):

@@ -22,6 +22,9 @@
 #include "sv_tree.cuh"
 #include "sv_lmhead.cuh"
 #include "sv_grow.cuh"
+#include "sv_rope.cuh"
+#include "sv_attn.cuh"
+#include "sv_treesample.cuh"
 
 static_assert(sv::kMaxDraft == SPEC_MAX_K, "finish kernel buffers are sized for SPEC_MAX_K");
 
@@ -55,7 +58,8 @@ struct Layout {
 
 // Returns false for arguments outside the documented limits.
 bool make_layout(int mode, int B, int kN, int V, int dtype, Layout* L) {
-  if (mode == SPEC_MODE_TREE_MASK || mode == SPEC_MODE_KV_COMMIT) {  // the flag header only
+  if (mode == SPEC_MODE_TREE_MASK || mode == SPEC_MODE_KV_COMMIT ||
+      mode == SPEC_MODE_TREE_SAMPLE || mode == SPEC_MODE_TREE_QKV) {  // the flag header only
     if (B < 0 || kN < 1 || kN > SPEC_MAX_TREE_NODES) return false;
     L->bytes = kHeaderBytes;
     return true;
@@ -292,9 +296,10 @@ spec_status_t persistent_grid(int items, int* grid) {
   return SPEC_OK;
 }
 
-// Dynamic shared-memory opt-in for a kernel, once per device context.
+// Dynamic shared-memory opt-in for a kernel (and, for clusters of more than
+// eight CTAs, the opt-in to those), once per device context.
 template <auto kernel>
-spec_status_t ensure_smem(size_t bytes) {
+spec_status_t ensure_smem(size_t bytes, bool big_clusters = false) {
   static bool done[kMaxDevices] = {false};
   static unsigned long long done_ctx[kMaxDevices] = {0};
   int dev = 0;
@@ -304,6 +309,9 @@ spec_status_t ensure_smem(size_t bytes) {
   if (!done[dev] || done_ctx[dev] != ctx) {
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) !=
         cudaSuccess)
+      return SPEC_ERR_CUDA;
+    if (big_clusters && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed,
+                                             1) != cudaSuccess)
       return SPEC_ERR_CUDA;
     done[dev] = true;
     done_ctx[dev] = ctx;
@@ -500,6 +508,24 @@ spec_status_t noalloc_scratch(void** addr) {
   }
   *addr = g_noalloc_addr[dev];
   return SPEC_OK;
+}
+
+constexpr size_t kTsMaxSmem = 192 * 1024;
+
+// Tree sampling: a cluster of CTAs per sequence (16 are more than the portable
+// 8); the dynamic shared memory holds the sums of the warps' steps.
+template <auto kernel>
+spec_status_t launch_tree_sample(const sv::TreeSampleParams& prm, int B, int cluster, size_t smem,
+                                 void* stream) {
+  const spec_status_t st = ensure_smem<kernel>(kTsMaxSmem, true);
+  if (st != SPEC_OK) return st;
+  return launch(kernel, B * cluster, smem, prm, stream, true, cluster, sv::kTsThreads);
+}
+
+bool attn_shape_ok(int B, int N, int Hq, int Hkv, int D, int P) {
+  return B >= 0 && N >= 1 && N <= SPEC_ATTN_MAX_NODES && Hkv >= 1 && Hq >= Hkv && Hq <= 65536 &&
+         Hq % Hkv == 0 && Hq / Hkv <= 128 && (D == 64 || D == 128) && P >= 0 &&
+         (long long)B * N * Hkv <= INT32_MAX;
 }
 
 }  // namespace
@@ -915,6 +941,165 @@ spec_status_t spec_lm_head_verify_sample(
   // the recomputed rows), as spec_verify_sample's
   if (vec_ok(lbuf, V, SPEC_DTYPE_F32)) return run_finish<sv::F32, true>(prm, stream);
   return run_finish<sv::F32, false>(prm, stream);
+}
+
+spec_status_t spec_verify_tree_sample(const void* target_logits, int dtype,
+                                      const int32_t* node_tokens, const int32_t* parents,
+                                      const float* u_sample, float temperature, int B, int N,
+                                      int V, int max_depth, int32_t* accepted_len,
+                                      int32_t* path_nodes, int32_t* out_tokens, float* out_probs,
+                                      void* workspace, size_t workspace_bytes, void* stream) {
+  if (dtype != SPEC_DTYPE_F32 && dtype != SPEC_DTYPE_BF16) return SPEC_ERR_INVALID_ARG;
+  if (B < 0 || N < 1 || N > SPEC_MAX_TREE_NODES || V < 1 || V > SPEC_MAX_V || max_depth < 0 ||
+      max_depth > SPEC_MAX_TREE_DEPTH || !(temperature > 0.0f) || !std::isfinite(temperature))
+    return SPEC_ERR_INVALID_ARG;
+  if ((long long)B * sv::kTsMaxCluster > INT32_MAX) return SPEC_ERR_INVALID_ARG;
+  if (B == 0) return SPEC_OK;
+  if (!target_logits || !node_tokens || !parents || !u_sample || !accepted_len || !path_nodes ||
+      !out_tokens || !out_probs)
+    return SPEC_ERR_INVALID_ARG;
+  if (!aligned(target_logits, elem_bytes(dtype)) || !aligned(node_tokens, 4) ||
+      !aligned(parents, 4) || !aligned(u_sample, 4) || !aligned(accepted_len, 4) ||
+      !aligned(path_nodes, 4) || !aligned(out_tokens, 4) || !aligned(out_probs, 4))
+    return SPEC_ERR_ALIGNMENT;
+  if (!workspace || workspace_bytes < kHeaderBytes) return SPEC_ERR_WORKSPACE;
+  if (!aligned(workspace, kAlign)) return SPEC_ERR_ALIGNMENT;
+  const double scale = 1.4426950408889634 / (double)temperature;
+  sv::TreeSampleParams prm;
+  std::memset(&prm, 0, sizeof prm);
+  prm.logits = target_logits;
+  prm.tokens = node_tokens;
+  prm.parents = parents;
+  prm.u = u_sample;
+  prm.c_hi = (float)scale;
+  prm.c_lo = (float)(scale - (double)prm.c_hi);
+  prm.N = N;
+  prm.V = V;
+  prm.max_depth = max_depth;
+  for (int bits = 17; bits < 31 && (1 << bits) < V; ++bits) prm.extra = bits - 16;
+  prm.accepted_len = accepted_len;
+  prm.path = path_nodes;
+  prm.out = out_tokens;
+  prm.probs = out_probs;
+  prm.flags = reinterpret_cast<unsigned*>(workspace);
+  constexpr int kCtaStep = sv::kTsWarps * sv::kTsStep;  // elements of a CTA's step
+  int cluster = 1;
+  while (cluster < (V > (1 << 20) ? 16 : 8) && cluster * kCtaStep < V) cluster *= 2;
+  prm.nsteps = (V + cluster * kCtaStep - 1) / (cluster * kCtaStep);
+  const size_t smem = (size_t)sv::kTsWarps * prm.nsteps * sizeof(unsigned long long);
+  // 16-byte loads: whole groups of 8 elements at 16-byte boundaries
+  const bool vec = aligned(target_logits, 16) && V % 8 == 0;
+  if (dtype == SPEC_DTYPE_BF16)
+    return vec ? launch_tree_sample<sv::tree_sample_kernel<sv::BF16, true>>(prm, B, cluster, smem, stream)
+               : launch_tree_sample<sv::tree_sample_kernel<sv::BF16, false>>(prm, B, cluster, smem, stream);
+  return vec ? launch_tree_sample<sv::tree_sample_kernel<sv::F32, true>>(prm, B, cluster, smem, stream)
+             : launch_tree_sample<sv::tree_sample_kernel<sv::F32, false>>(prm, B, cluster, smem, stream);
+}
+
+spec_status_t spec_tree_qkv_rope(const void* qkv, const void* q_norm, const void* k_norm, float eps,
+                                 const float* inv_freq, int rot_dim, int interleaved,
+                                 long long pos_offset, const int32_t* base_len,
+                                 const int32_t* depth, int B, int N, int Hq, int Hkv, int D, int L,
+                                 long long seq_stride, void* q_out, void* k_cache, void* v_cache,
+                                 void* workspace, size_t workspace_bytes, void* stream) {
+  if (B < 0 || N < 1 || N > SPEC_MAX_TREE_NODES || Hq < 1 || Hkv < 1 || Hq > 65536 ||
+      Hkv > 65536 || (D != 64 && D != 128) || L < 1 || rot_dim < 0 || rot_dim > D || rot_dim % 2 ||
+      pos_offset < 0 || !(eps >= 0.0f) || !std::isfinite(eps) ||
+      (long long)B * N > INT32_MAX)
+    return SPEC_ERR_INVALID_ARG;
+  if (seq_stride < (long long)L * Hkv * D * 2) return SPEC_ERR_INVALID_ARG;
+  if (B == 0) return SPEC_OK;
+  if (!qkv || !base_len || !q_out || !k_cache || !v_cache || (rot_dim > 0 && !inv_freq))
+    return SPEC_ERR_INVALID_ARG;
+  if (!aligned(qkv, 16) || !aligned(q_out, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+      !aligned(q_norm, 16) || !aligned(k_norm, 16) || seq_stride % 16 || !aligned(base_len, 4) ||
+      !aligned(depth, 4) || !aligned(inv_freq, 4))
+    return SPEC_ERR_ALIGNMENT;
+  if (!workspace || workspace_bytes < kHeaderBytes) return SPEC_ERR_WORKSPACE;
+  if (!aligned(workspace, kAlign)) return SPEC_ERR_ALIGNMENT;
+  sv::RopeParams prm;
+  std::memset(&prm, 0, sizeof prm);
+  prm.qkv = static_cast<const uint16_t*>(qkv);
+  prm.q_norm = static_cast<const uint16_t*>(q_norm);
+  prm.k_norm = static_cast<const uint16_t*>(k_norm);
+  prm.inv_freq = inv_freq;
+  prm.base_len = base_len;
+  prm.depth = depth;
+  prm.q_out = static_cast<uint16_t*>(q_out);
+  prm.k_cache = static_cast<uint16_t*>(k_cache);
+  prm.v_cache = static_cast<uint16_t*>(v_cache);
+  prm.flags = reinterpret_cast<unsigned*>(workspace);
+  prm.seq_stride = seq_stride / 2;
+  prm.pos_offset = pos_offset;
+  prm.eps = eps;
+  prm.N = N;
+  prm.Hq = Hq;
+  prm.Hkv = Hkv;
+  prm.L = L;
+  prm.rot = rot_dim;
+  prm.interleaved = interleaved != 0;
+  // both members of every pair in one thread: adjacent elements, or halves a
+  // whole number of 8-element vectors apart
+  const bool vec = interleaved || rot_dim % 16 == 0;
+  const int grid = B * N;
+  if (D == 128)
+    return vec ? launch(sv::tree_qkv_rope_kernel<128, true>, grid, 0, prm, stream, true, 1, sv::kRopeThreads)
+               : launch(sv::tree_qkv_rope_kernel<128, false>, grid, 0, prm, stream, true, 1, sv::kRopeThreads);
+  return vec ? launch(sv::tree_qkv_rope_kernel<64, true>, grid, 0, prm, stream, true, 1, sv::kRopeThreads)
+             : launch(sv::tree_qkv_rope_kernel<64, false>, grid, 0, prm, stream, true, 1, sv::kRopeThreads);
+}
+
+size_t spec_tree_attention_workspace_bytes(int B, int N, int Hq, int Hkv, int D, int P) {
+  if (!attn_shape_ok(B, N, Hq, Hkv, D, P)) return 0;
+  return kHeaderBytes;
+}
+
+spec_status_t spec_tree_attention(const void* q, const void* k_cache, const void* v_cache,
+                                  long long seq_stride, int L, const void* prefix_k,
+                                  const void* prefix_v, int P, const uint32_t* mask,
+                                  const int32_t* base_len, int B, int N, int Hq, int Hkv, int D,
+                                  float scale, void* out, float* lse, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
+  if (!attn_shape_ok(B, N, Hq, Hkv, D, P) || L < 1 || !(scale > 0.0f) || !std::isfinite(scale))
+    return SPEC_ERR_INVALID_ARG;
+  if (seq_stride < (long long)L * Hkv * D * 2) return SPEC_ERR_INVALID_ARG;
+  if (B == 0) return SPEC_OK;
+  if (!q || !k_cache || !v_cache || !base_len || !out || (P > 0 && (!prefix_k || !prefix_v)))
+    return SPEC_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) ||
+      seq_stride % 16 || (P > 0 && (!aligned(prefix_k, 16) || !aligned(prefix_v, 16))) ||
+      !aligned(mask, 4) || !aligned(base_len, 4) || !aligned(lse, 4))
+    return SPEC_ERR_ALIGNMENT;
+  if (!workspace || workspace_bytes < spec_tree_attention_workspace_bytes(B, N, Hq, Hkv, D, P))
+    return SPEC_ERR_WORKSPACE;
+  if (!aligned(workspace, kAlign)) return SPEC_ERR_ALIGNMENT;
+  sv::AttnParams prm;
+  std::memset(&prm, 0, sizeof prm);
+  prm.q = static_cast<const uint16_t*>(q);
+  prm.k = static_cast<const uint16_t*>(k_cache);
+  prm.v = static_cast<const uint16_t*>(v_cache);
+  prm.pk = static_cast<const uint16_t*>(prefix_k);
+  prm.pv = static_cast<const uint16_t*>(prefix_v);
+  prm.mask = mask;
+  prm.base_len = base_len;
+  prm.out = static_cast<uint16_t*>(out);
+  prm.lse = lse;
+  prm.flags = reinterpret_cast<unsigned*>(workspace);
+  prm.seq_stride = seq_stride / 2;
+  prm.scale_log2 = (float)(1.4426950408889634 * (double)scale);
+  prm.B = B;
+  prm.N = N;
+  prm.Hq = Hq;
+  prm.Hkv = Hkv;
+  prm.G = Hq / Hkv;
+  prm.W = (N + 31) / 32;
+  prm.L = L;
+  prm.P = P;
+  const long long items = (long long)B * N * Hkv;
+  const int per = sv::kAtFinThreads / 32;
+  const int grid = (int)((items + per - 1) / per);
+  return D == 128 ? launch(sv::tree_attn_finish_kernel<128>, grid, 0, prm, stream, true, 1, sv::kAtFinThreads)
+                  : launch(sv::tree_attn_finish_kernel<64>, grid, 0, prm, stream, true, 1, sv::kAtFinThreads);
 }
 
 spec_status_t spec_tree_grow(const void* draft_logits, int dtype, float temperature, int B,
