@@ -319,14 +319,16 @@ spec_status_t ensure_smem(size_t bytes, bool big_clusters = false) {
   return SPEC_OK;
 }
 
-// TMA descriptor of a row-major bf16 matrix [outer, inner] read as K-major
-// boxes of 64 x box_outer with 128-byte swizzle (out-of-range rows and
-// columns read as zero).  The driver's encoder is looked up once.
+// TMA descriptors of bf16 arrays (innermost dimension first; strides in bytes,
+// of the outer dimensions) read in boxes 64 elements wide with 128-byte
+// swizzle, out-of-range elements as zero; encode_bf16_kmajor: a row-major
+// matrix [outer, inner] in boxes of 64 x box_outer.  The driver's encoder is
+// looked up once.
 std::mutex g_encode_mu;
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 
-spec_status_t encode_bf16_kmajor(CUtensorMap* map, const void* base, int inner, int outer,
-                                 int box_outer) {
+spec_status_t encode_bf16(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims,
+                          const cuuint64_t* strides, const cuuint32_t* box) {
   {
     std::lock_guard<std::mutex> lock(g_encode_mu);
     if (!g_encode) {
@@ -339,15 +341,20 @@ spec_status_t encode_bf16_kmajor(CUtensorMap* map, const void* base, int inner, 
       g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
     }
   }
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUresult r =
+      g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(base),
+               dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? SPEC_OK : SPEC_ERR_INVALID_ARG;
+}
+
+spec_status_t encode_bf16_kmajor(CUtensorMap* map, const void* base, int inner, int outer,
+                                 int box_outer) {
   const cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)outer};
   const cuuint64_t strides[1] = {(cuuint64_t)inner * 2};
   const cuuint32_t box[2] = {(cuuint32_t)sv::kLmBK, (cuuint32_t)box_outer};
-  const cuuint32_t estr[2] = {1, 1};
-  const CUresult r =
-      g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides,
-               box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? SPEC_OK : SPEC_ERR_INVALID_ARG;
+  return encode_bf16(map, base, 2, dims, strides, box);
 }
 
 // Row groups of an LM-head GEMM: at most kLmMaxRows rows each, split evenly,
@@ -522,10 +529,73 @@ spec_status_t launch_tree_sample(const sv::TreeSampleParams& prm, int B, int clu
   return launch(kernel, B * cluster, smem, prm, stream, true, cluster, sv::kTsThreads);
 }
 
+// Tiles and partial slots of spec_tree_attention for one call shape.
+struct AttnPlan {
+  int tok = 0, pair_s = 0, pair_o = 0, mg_s = 0, mg_o = 0, half_rows = 0, slot_rows = 0;
+  size_t off_ml = 0, off_part = 0, bytes = 0;
+};
+
+// Rows of an item: the G query heads of `tok` nodes fill one 128-row half;
+// an item with more nodes takes two halves, with fewer one (both halves of
+// the kernel then share it by alternate tiles).
+AttnPlan attn_plan(int B, int N, int Hq, int Hkv, int D, int P) {
+  AttnPlan a;
+  const int G = Hq / Hkv;
+  a.tok = sv::kAtRows / G;
+  const long long all = (long long)B * N;
+  a.pair_o = N > a.tok;
+  a.mg_o = (N + (a.tok << a.pair_o) - 1) / (a.tok << a.pair_o);
+  if (P > 0) {
+    a.pair_s = all > a.tok;
+    a.mg_s = (int)((all + (a.tok << a.pair_s) - 1) / (a.tok << a.pair_s));
+  }
+  a.half_rows = (int)std::min<long long>(a.tok, P > 0 ? all : N) * G;
+  a.slot_rows = a.half_rows << std::max(a.pair_s, a.pair_o);
+  const size_t slots = (size_t)Hkv * a.mg_s + (size_t)B * Hkv * a.mg_o + sv::kAtMaxCtas;
+  a.off_ml = align_up(kDataOffset + (size_t)(B + 1) * sizeof(long long));
+  a.off_part = align_up(a.off_ml + slots * a.slot_rows * sizeof(float2));
+  a.bytes = align_up(a.off_part + slots * a.slot_rows * D * sizeof(float));
+  return a;
+}
+
+// Multiprocessors of the current device, once per device context.
+spec_status_t sm_count(int* sms) {
+  static int cached[kMaxDevices] = {0};
+  static unsigned long long cached_ctx[kMaxDevices] = {0};
+  int dev = 0;
+  unsigned long long ctx = 0;
+  if (current_context(&dev, &ctx) != SPEC_OK) return SPEC_ERR_CUDA;
+  std::lock_guard<std::mutex> lock(g_shape_mu);
+  if (cached[dev] == 0 || cached_ctx[dev] != ctx) {
+    if (cudaDeviceGetAttribute(&cached[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+      return SPEC_ERR_CUDA;
+    cached_ctx[dev] = ctx;
+  }
+  *sms = cached[dev];
+  return SPEC_OK;
+}
+
+template <int D>
+spec_status_t run_attention(const sv::AttnParams& prm, const CUtensorMap (&map)[5], void* stream) {
+  spec_status_t st = ensure_smem<sv::tree_attn_kernel<D>>((size_t)sv::at_smem<D>());
+  if (st != SPEC_OK) return st;
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr[1];
+  pdl_config(&cfg, attr, dim3((unsigned)prm.nctas), dim3(sv::kAtThreads), sv::at_smem<D>(), stream);
+  if (cudaLaunchKernelEx(&cfg, sv::tree_attn_kernel<D>, map[0], map[1], map[2], map[3], map[4],
+                         prm) != cudaSuccess)
+    return SPEC_ERR_CUDA;
+  g_launches.fetch_add(1, std::memory_order_relaxed);
+  const long long items = (long long)prm.B * prm.N * prm.Hkv;
+  constexpr int kPer = sv::kAtFinThreads / 32;
+  return launch(sv::tree_attn_finish_kernel<D>, (int)((items + kPer - 1) / kPer), 0, prm, stream,
+                true, 1, sv::kAtFinThreads);
+}
+
 bool attn_shape_ok(int B, int N, int Hq, int Hkv, int D, int P) {
   return B >= 0 && N >= 1 && N <= SPEC_ATTN_MAX_NODES && Hkv >= 1 && Hq >= Hkv && Hq <= 65536 &&
          Hq % Hkv == 0 && Hq / Hkv <= 128 && (D == 64 || D == 128) && P >= 0 &&
-         (long long)B * N * Hkv <= INT32_MAX;
+         (long long)B * N <= INT32_MAX / 128 && (long long)B * N * Hkv <= INT32_MAX;
 }
 
 }  // namespace
@@ -1051,7 +1121,7 @@ spec_status_t spec_tree_qkv_rope(const void* qkv, const void* q_norm, const void
 
 size_t spec_tree_attention_workspace_bytes(int B, int N, int Hq, int Hkv, int D, int P) {
   if (!attn_shape_ok(B, N, Hq, Hkv, D, P)) return 0;
-  return kHeaderBytes;
+  return attn_plan(B, N, Hq, Hkv, D, P).bytes;
 }
 
 spec_status_t spec_tree_attention(const void* q, const void* k_cache, const void* v_cache,
@@ -1070,16 +1140,19 @@ spec_status_t spec_tree_attention(const void* q, const void* k_cache, const void
       seq_stride % 16 || (P > 0 && (!aligned(prefix_k, 16) || !aligned(prefix_v, 16))) ||
       !aligned(mask, 4) || !aligned(base_len, 4) || !aligned(lse, 4))
     return SPEC_ERR_ALIGNMENT;
-  if (!workspace || workspace_bytes < spec_tree_attention_workspace_bytes(B, N, Hq, Hkv, D, P))
-    return SPEC_ERR_WORKSPACE;
+  if (!workspace) return SPEC_ERR_WORKSPACE;
   if (!aligned(workspace, kAlign)) return SPEC_ERR_ALIGNMENT;
+  const AttnPlan plan = attn_plan(B, N, Hq, Hkv, D, P);
+  if (workspace_bytes < plan.bytes) return SPEC_ERR_WORKSPACE;
+  int sms = 0;
+  spec_status_t st = sm_count(&sms);
+  if (st != SPEC_OK) return st;
+  char* ws = static_cast<char*>(workspace);
   sv::AttnParams prm;
   std::memset(&prm, 0, sizeof prm);
   prm.q = static_cast<const uint16_t*>(q);
   prm.k = static_cast<const uint16_t*>(k_cache);
   prm.v = static_cast<const uint16_t*>(v_cache);
-  prm.pk = static_cast<const uint16_t*>(prefix_k);
-  prm.pv = static_cast<const uint16_t*>(prefix_v);
   prm.mask = mask;
   prm.base_len = base_len;
   prm.out = static_cast<uint16_t*>(out);
@@ -1095,11 +1168,45 @@ spec_status_t spec_tree_attention(const void* q, const void* k_cache, const void
   prm.W = (N + 31) / 32;
   prm.L = L;
   prm.P = P;
-  const long long items = (long long)B * N * Hkv;
-  const int per = sv::kAtFinThreads / 32;
-  const int grid = (int)((items + per - 1) / per);
-  return D == 128 ? launch(sv::tree_attn_finish_kernel<128>, grid, 0, prm, stream, true, 1, sv::kAtFinThreads)
-                  : launch(sv::tree_attn_finish_kernel<64>, grid, 0, prm, stream, true, 1, sv::kAtFinThreads);
+  prm.tok = plan.tok;
+  prm.pair_s = plan.pair_s;
+  prm.pair_o = plan.pair_o;
+  prm.mg_s = plan.mg_s;
+  prm.mg_o = plan.mg_o;
+  prm.tiles_s = P / sv::kAtKeys + (P % sv::kAtKeys != 0);
+  prm.half_rows = plan.half_rows;
+  prm.slot_rows = plan.slot_rows;
+  prm.nctas = std::min(sms, sv::kAtMaxCtas);
+  prm.tstart = reinterpret_cast<long long*>(ws + kDataOffset);
+  prm.ml = reinterpret_cast<float2*>(ws + plan.off_ml);
+  prm.opart = reinterpret_cast<float*>(ws + plan.off_part);
+  // queries: boxes of 64 elements x the heads of one key-value head x nodes;
+  // caches: 64 elements x one head x 128 positions
+  CUtensorMap map[5];
+  {
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)Hq, (cuuint64_t)B * N};
+    const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)Hq * D * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)prm.G, (cuuint32_t)prm.tok};
+    st = encode_bf16(&map[0], q, 3, dims, strides, box);
+    if (st != SPEC_OK) return st;
+  }
+  const cuuint32_t box[4] = {64, 1, (cuuint32_t)sv::kAtKeys, 1};
+  const cuuint64_t row = (cuuint64_t)Hkv * D * 2;
+  for (int i = 0; i < 2; ++i) {
+    const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)Hkv, (cuuint64_t)L, (cuuint64_t)B};
+    const cuuint64_t strides[3] = {(cuuint64_t)D * 2, row, (cuuint64_t)seq_stride};
+    st = encode_bf16(&map[1 + i], i == 0 ? k_cache : v_cache, 4, dims, strides, box);
+    if (st != SPEC_OK) return st;
+    if (P == 0) {
+      map[3 + i] = map[1 + i];  // never read
+      continue;
+    }
+    const cuuint64_t pdims[4] = {(cuuint64_t)D, (cuuint64_t)Hkv, (cuuint64_t)P, 1};
+    const cuuint64_t pstrides[3] = {(cuuint64_t)D * 2, row, row * P};
+    st = encode_bf16(&map[3 + i], i == 0 ? prefix_k : prefix_v, 4, pdims, pstrides, box);
+    if (st != SPEC_OK) return st;
+  }
+  return D == 128 ? run_attention<128>(prm, map, stream) : run_attention<64>(prm, map, stream);
 }
 
 spec_status_t spec_tree_grow(const void* draft_logits, int dtype, float temperature, int B,

@@ -9,6 +9,20 @@
 // over j in the prefix shared by the batch (P entries, one copy), the
 // sequence's own positions [0, base_len - 1), and the tree entries
 // base_len - 1 + u with bit u of the node's mask row set (mask null: u <= v).
+//
+// Two kernels.  The prefixes, where every node sees every entry, are matrix
+// products: tree_attn_kernel runs them on the tensor cores, the nodes' query
+// heads of one key-value head as the rows (a sequence's nodes for its own
+// prefix, the whole batch's nodes for the shared one, so that its entries are
+// read once for all), 128 entries of the cache at a time, and leaves
+// unnormalised partial sums.  tree_attn_finish_kernel adds each node's few
+// ancestors one by one, reading nothing that the node does not see, and joins
+// the partials.
+//
+// The work is cut into equal runs of (rows, 128 entries) tiles, one run per
+// SM, whatever the lengths: the tiles of all items (shared prefix first, then
+// sequence by sequence) stand in one line, CTA c takes [c T / n, (c+1) T / n),
+// and an item that is cut leaves one partial per CTA, in slot item + c.
 #pragma once
 
 #include "sv_lmhead.cuh"
@@ -16,15 +30,27 @@
 
 namespace sv {
 
+constexpr int kAtRows = 128;     // rows of a half (UMMA M, tensor-memory lanes)
+constexpr int kAtKeys = 128;     // cache entries per tile
+constexpr int kAtThreads = 384;  // producer, MMA issuer, 2 idle warps, 2 x 4 softmax warps
+constexpr int kAtMaxStages = 8;
+constexpr int kAtMaxCtas = 160;  // partial slots are laid out for at most this many CTAs
+constexpr float kAtLazy = 8.0f;  // a row's reference grows only past 2^8
 constexpr int kAtFinThreads = 128;
 constexpr int kAtFinHeads = 8;  // query heads of a key-value head held by a warp at once
+
+template <int D>
+__host__ __device__ constexpr int at_tile_bytes() { return kAtKeys * D * 2; }
+// K and V tiles in flight beside the two query tiles, in 195 KB
+template <int D>
+__host__ __device__ constexpr int at_stages() { return D == 128 ? 4 : 8; }
+template <int D>
+__host__ __device__ constexpr int at_smem() { return (2 + at_stages<D>()) * at_tile_bytes<D>() + 1024; }
 
 struct AttnParams {
   const uint16_t* q;        // [B, N, Hq, D]
   const uint16_t* k;        // [B, L, Hkv, D], sequences seq_stride elements apart
   const uint16_t* v;
-  const uint16_t* pk;       // [P, Hkv, D]
-  const uint16_t* pv;
   const uint32_t* mask;     // [B, N, W] or null (a chain)
   const int32_t* base_len;  // [B]
   uint16_t* out;            // [B, N, Hq, D]
@@ -33,29 +59,628 @@ struct AttnParams {
   long long seq_stride;     // elements
   float scale_log2;         // scale * log2(e)
   int B, N, Hq, Hkv, G, W, L, P;
+  // the prefixes' tiles
+  int tok;                  // nodes per half: floor(128 / G)
+  int pair_s, pair_o;       // shared / own items: two halves of rows (else one, by alternate tiles)
+  int mg_s, mg_o;           // items per key-value head (and sequence)
+  int tiles_s;              // ceil(P / 128)
+  int half_rows;            // rows stored per half
+  int slot_rows;            // rows stored per slot
+  int nctas;
+  float* opart;             // [slot][D / 4][slot_rows][4]
+  float2* ml;               // [slot][slot_rows]: reference (log2) and sum
+  long long* tstart;        // [B + 1]: tiles of the sequences before b, per item
 };
 
 __device__ __forceinline__ bool attn_seq_ok(const AttnParams& p, int base) {
   return base >= 1 && (long long)base + p.N - 1 <= p.L;
 }
+// 128-entry tiles of a sequence's own prefix
+__device__ __forceinline__ int attn_tiles(const AttnParams& p, int b) {
+  const int base = __ldg(p.base_len + b);
+  return attn_seq_ok(p, base) ? (base - 1 + kAtKeys - 1) / kAtKeys : 0;
+}
 
-// One warp per (node, key-value head): running softmax over the visible
-// entries in float32, kAtFinHeads query heads at a time; a lane holds D / 32
-// elements of the head.
+// A CTA's run of tiles, item by item.
+struct AttnSeg {
+  long long slot;     // of the partial: item + CTA
+  int b, mg, h;       // b < 0: the shared prefix
+  int t0, n, kvlen;   // tiles [t0, t0 + n) of an item with kvlen entries
+};
+struct AttnWalk {
+  long long pos, hi, bstart;  // bstart: first tile of sequence b in the line
+  int b;
+  __device__ __forceinline__ bool next(const AttnParams& p, AttnSeg* s) {
+    if (pos >= hi) return false;
+    const long long items_s = (long long)p.Hkv * p.mg_s;
+    const long long shared = items_s * p.tiles_s;
+    long long it;
+    int tiles;
+    if (pos < shared) {
+      it = pos / p.tiles_s;
+      tiles = p.tiles_s;
+      s->t0 = (int)(pos - it * tiles);
+      s->b = -1;
+      s->kvlen = p.P;
+      s->slot = it + blockIdx.x;
+    } else {
+      const int per = p.Hkv * p.mg_o;
+      tiles = attn_tiles(p, b);
+      while (pos >= bstart + (long long)per * tiles) {
+        bstart += (long long)per * tiles;
+        tiles = attn_tiles(p, ++b);
+      }
+      it = (pos - bstart) / tiles;
+      s->t0 = (int)(pos - bstart - it * tiles);
+      s->b = b;
+      s->kvlen = __ldg(p.base_len + b) - 1;
+      s->slot = items_s + (long long)b * per + it + blockIdx.x;
+    }
+    s->mg = (int)(it / p.Hkv);
+    s->h = (int)(it - (long long)s->mg * p.Hkv);
+    s->n = (int)min((long long)(tiles - s->t0), hi - pos);
+    pos += s->n;
+    return true;
+  }
+};
+
+// --- tcgen05 / TMA forms of one CTA (see sv_lmhead.cuh for the pair's) -------
+
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int x, int y, int z,
+                                            int w, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar))
+      : "memory");
+}
+// D (tensor memory) = or += A B with both operands in shared memory
+__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                        uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// the same with A in tensor memory (two bf16 per column)
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                        uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void umma_commit(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+          smem_addr(bar))
+      : "memory");
+}
+// 32 columns from registers, the store side of tmem_ld32 (no wait)
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
+      "%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
+      "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
+      "r"(r[30]), "r"(r[31]), "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+// Shared-memory descriptor of V [keys, D] as the product's second operand
+// with D contiguous (MN-major, 128-byte swizzle): 64-wide column blocks 128
+// rows x 128 bytes apart (leading-byte offset), 8-key groups 1024 bytes apart
+// (stride-byte offset).  A step of 16 keys advances the start by 2048 bytes.
+__device__ __forceinline__ uint64_t umma_desc_mn_sw128(uint32_t smem_byte_addr) {
+  return umma_desc_sw128(smem_byte_addr) | ((uint64_t)((kAtKeys * 128) >> 4) << 16);
+}
+
+// Warp 0 copies (TMA), warp 1 issues the MMAs, warps 4-7 and 8-11 are the
+// softmax of half 0 and 1.  A half is 128 rows with its own score and output
+// accumulators in tensor memory (S0 | S1 | O0 | O1) and its own running
+// reference and sums.  With more rows than one tile holds (pair), the halves
+// are two row tiles over the same entries; otherwise both take the same rows
+// and alternate tiles, and are joined at the end of an item.  Either way one
+// half's softmax runs beside the other's products:
+//   S = Q K^T -> registers -> P = 2^(S c - m), bf16, over S in tensor memory
+//   O += P V   (P from tensor memory)
+// The reference m of a row follows the row's maximum only when that has grown
+// by more than 2^8 (P then stays below 2^8, harmless in bf16 and float32), so
+// that O is rarely rescaled.
+template <int D>
+__global__ void __launch_bounds__(kAtThreads, 1)
+    tree_attn_kernel(const __grid_constant__ CUtensorMap map_q,
+                     const __grid_constant__ CUtensorMap map_k,
+                     const __grid_constant__ CUtensorMap map_v,
+                     const __grid_constant__ CUtensorMap map_pk,
+                     const __grid_constant__ CUtensorMap map_pv, const AttnParams p) {
+  constexpr int kTile = at_tile_bytes<D>();
+  constexpr int S = at_stages<D>();
+  constexpr int kSub = D / 64;  // 64-element column blocks of a tile (128 rows x 128 bytes)
+  extern __shared__ uint8_t at_raw[];
+  __shared__ uint64_t full[kAtMaxStages], empty[kAtMaxStages];
+  __shared__ uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], drain;
+  __shared__ uint32_t tmem_holder;
+  __shared__ int s_abort, s_b;
+  __shared__ long long s_bstart, s_sum[kAtThreads / 32];
+  __shared__ float2 s_ml[2][kAtRows];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(at_raw) + 1023) & ~(uintptr_t)1023);
+  uint8_t* ring = smem + 2 * kTile;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(&q_full, 1);
+    mbar_init(&q_empty, 1);
+    for (int w = 0; w < 2; ++w) {
+      mbar_init(&s_full[w], 1);
+      mbar_init(&p_full[w], 4);
+      mbar_init(&o_full[w], 1);
+    }
+    mbar_init(&drain, 1);
+    s_abort = 0;
+    s_b = 0;
+    s_bstart = 0;
+    mbar_init_fence();
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_addr(&tmem_holder)),
+                 "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  // a programmatic dependent of the kernel before it in the stream: nothing of
+  // global memory is touched before that grid has finished
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+  // the run [lo, hi) of this CTA and the sequence it starts in
+  const int per = p.Hkv * p.mg_o;
+  const long long shared = (long long)p.Hkv * p.mg_s * p.tiles_s;
+  long long own = 0;
+  for (int b = threadIdx.x; b < p.B; b += kAtThreads) own += attn_tiles(p, b);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) own += __shfl_xor_sync(0xffffffffu, own, o);
+  if (lane == 0) s_sum[warp] = own;
+  tmem_fence_before();
+  __syncthreads();
+  tmem_fence_after();
+  own = 0;
+  for (int w = 0; w < kAtThreads / 32; ++w) own += s_sum[w];
+  const long long total = shared + own * per;
+  const long long lo = total * blockIdx.x / p.nctas, hi = total * (blockIdx.x + 1) / p.nctas;
+  {
+    long long run = 0;
+    for (int b0 = 0; b0 < p.B; b0 += kAtThreads) {
+      const int b = b0 + threadIdx.x;
+      const long long mine = b < p.B ? attn_tiles(p, b) : 0;
+      long long incl = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      __syncthreads();
+      if (lane == 31) s_sum[warp] = incl;
+      __syncthreads();
+      long long before = run;
+      for (int w = 0; w < kAtThreads / 32; ++w) {
+        if (w < warp) before += s_sum[w];
+        run += s_sum[w];
+      }
+      const long long excl = before + incl - mine;
+      if (b < p.B) {
+        if (blockIdx.x == 0) p.tstart[b] = excl;
+        if (lo >= shared && lo - shared >= excl * per && lo - shared < (excl + mine) * per) {
+          s_b = b;
+          s_bstart = shared + excl * per;
+        }
+      }
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0) p.tstart[p.B] = run;
+  }
+  if (threadIdx.x == 0 && lo < shared) s_bstart = shared;
+  __syncthreads();
+  const uint32_t tmem = tmem_holder;
+  AttnWalk walk{lo, hi, s_bstart, s_b};
+  AttnSeg seg;
+  auto fail = [&]() {
+    s_abort = 1;
+    set_flag(p.flags, kFlagTimeout);
+  };
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ---------------- copies ----------------
+      int stage = 0, issued = 0;
+      unsigned phase = 0, nq = 0;
+      bool ok = true;
+      while (ok && walk.next(p, &seg)) {
+        const bool sh = seg.b < 0;
+        const int pair = sh ? p.pair_s : p.pair_o;
+        const int cap = p.tok << pair;
+        const int tok0 = (sh ? 0 : seg.b * p.N) + seg.mg * cap;
+        if (*(volatile int*)&s_abort || !mbar_wait_bounded(&q_empty, (nq & 1) ^ 1u)) {
+          fail();
+          break;
+        }
+        mbar_expect_tx(&q_full, (unsigned)((1 + pair) * kSub * p.tok * p.G * 128));
+        for (int w = 0; w <= pair; ++w)
+          for (int c = 0; c < kSub; ++c)
+            tma_load_3d(smem + w * kTile + c * (kAtRows * 128), &map_q, c * 64, seg.h * p.G,
+                        tok0 + w * p.tok, &q_full);
+        ++nq;
+        const CUtensorMap* mk = sh ? &map_pk : &map_k;
+        const CUtensorMap* mv = sh ? &map_pv : &map_v;
+        auto put = [&](const CUtensorMap* m, int t) {
+          if (*(volatile int*)&s_abort || !mbar_wait_bounded(&empty[stage], phase ^ 1u)) {
+            ok = false;
+            fail();
+            return;
+          }
+          mbar_expect_tx(&full[stage], kTile);
+          for (int c = 0; c < kSub; ++c)
+            tma_load_4d(ring + stage * kTile + c * (kAtKeys * 128), m, c * 64, seg.h,
+                        (seg.t0 + t) * kAtKeys, sh ? 0 : seg.b, &full[stage]);
+          ++issued;
+          if (++stage == S) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        };
+        // in the order of use: each V tile, then the K tile `ahead` further on
+        const int ahead = 2 - pair;
+        for (int t = 0; ok && t < seg.n + ahead; ++t) {
+          if (t >= ahead) put(mv, t - ahead);
+          if (ok && t < seg.n) put(mk, t);
+        }
+      }
+      // every copy has landed before the CTA can leave
+      for (int j = max(0, issued - S); j < issued; ++j)
+        mbar_wait_bounded(&full[j % S], (unsigned)((j / S) & 1));
+      if (nq) mbar_wait_bounded(&q_full, (nq - 1) & 1);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      // ---------------- MMAs ----------------
+      const uint32_t id_qk = umma_idesc_bf16_f32(kAtRows, kAtKeys);
+      const uint32_t id_pv = umma_idesc_bf16_f32(kAtRows, D) | (1u << 16);  // V: MN-major
+      const uint64_t qdesc = umma_desc_sw128(smem_addr(smem));
+      const uint64_t kdesc = umma_desc_sw128(smem_addr(ring));
+      const uint64_t vdesc = umma_desc_mn_sw128(smem_addr(ring));
+      int stage = 0;
+      unsigned phase = 0, nq = 0, np[2] = {0, 0};
+      bool ok = true;
+      auto wait = [&](uint64_t* bar, unsigned parity) {
+        if (ok && (*(volatile int*)&s_abort || !mbar_wait_bounded(bar, parity))) {
+          ok = false;
+          fail();
+        }
+        tmem_fence_after();
+        return ok;
+      };
+      auto advance = [&]() {
+        if (++stage == S) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      };
+      // scores of half w from the K tile in the current stage, query tile qt
+      auto scores = [&](int w, int qt) {
+        const uint64_t a = qdesc + (uint64_t)(qt * kTile >> 4);
+        const uint64_t b = kdesc + (uint64_t)(stage * kTile >> 4);
+#pragma unroll
+        for (int c = 0; c < kSub; ++c)
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            const uint64_t o = (uint64_t)((c * kAtKeys * 128 + kk * 32) >> 4);
+            umma_ss(tmem + w * kAtKeys, a + o, b + o, id_qk, (c | kk) ? 1u : 0u);
+          }
+        umma_commit(&s_full[w]);
+      };
+      // output of half w from the V tile in stage st
+      auto output = [&](int w, int st, bool first) {
+        const uint64_t b = vdesc + (uint64_t)(st * kTile >> 4);
+#pragma unroll
+        for (int kk = 0; kk < kAtKeys / 16; ++kk)
+          umma_ts(tmem + 2 * kAtKeys + w * D, tmem + w * kAtKeys + kk * 8,
+                  b + (uint64_t)(kk * 2048 >> 4), id_pv, (!first || kk) ? 1u : 0u);
+      };
+      while (ok && walk.next(p, &seg)) {
+        const int pair = seg.b < 0 ? p.pair_s : p.pair_o;
+        const int n = seg.n;
+        if (!wait(&q_full, nq & 1)) break;
+        ++nq;
+        if (pair) {
+          if (!wait(&full[stage], phase)) break;
+          scores(0, 0);
+          scores(1, 1);
+          umma_commit(&empty[stage]);
+          if (n == 1) umma_commit(&q_empty);
+          advance();
+          for (int t = 0; t < n; ++t) {
+            const int vst = stage;
+            if (!wait(&full[stage], phase)) break;
+            advance();
+            if (!wait(&p_full[0], np[0]++ & 1)) break;
+            output(0, vst, t == 0);
+            if (t + 1 < n) {
+              if (!wait(&full[stage], phase)) break;
+              scores(0, 0);
+            } else {
+              umma_commit(&o_full[0]);
+            }
+            if (!wait(&p_full[1], np[1]++ & 1)) break;
+            output(1, vst, t == 0);
+            umma_commit(&empty[vst]);
+            if (t + 1 < n) {
+              scores(1, 1);
+              umma_commit(&empty[stage]);
+              if (t + 2 == n) umma_commit(&q_empty);
+              advance();
+            } else {
+              umma_commit(&o_full[1]);
+            }
+          }
+        } else {
+          for (int t = 0; t < min(2, n); ++t) {
+            if (!wait(&full[stage], phase)) break;
+            scores(t, 0);
+            umma_commit(&empty[stage]);
+            if (t + 1 == n) umma_commit(&q_empty);
+            advance();
+          }
+          for (int t = 0; ok && t < n; ++t) {
+            const int w = t & 1, vst = stage;
+            if (!wait(&full[stage], phase)) break;
+            advance();
+            if (!wait(&p_full[w], np[w]++ & 1)) break;
+            output(w, vst, t < 2);
+            umma_commit(&empty[vst]);
+            if (t + 2 < n) {
+              if (!wait(&full[stage], phase)) break;
+              scores(w, 0);
+              umma_commit(&empty[stage]);
+              if (t + 3 == n) umma_commit(&q_empty);
+              advance();
+            } else {
+              umma_commit(&o_full[w]);
+            }
+          }
+        }
+      }
+      // every MMA has completed before tensor memory is freed
+      umma_commit(&drain);
+      mbar_wait_bounded(&drain, 0);
+    }
+    __syncwarp();
+  } else if (warp >= 4) {
+    // ---------------- softmax ----------------
+    const int w = (warp - 4) >> 2;                // half
+    const int quad = warp & 3;                    // tensor-memory lanes 32 quad ..
+    const int r = quad * 32 + lane;               // row of the half
+    const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
+    const uint32_t sbase = lanes + w * kAtKeys;
+    unsigned ns = 0, no = 0;  // uses of s_full / o_full so far
+    long long ring0 = 0;      // ring uses before this segment
+    bool dead = false;        // a wait gave up: only the barriers are kept up
+    auto wait = [&](uint64_t* bar, unsigned parity) {
+      if (!dead && (*(volatile int*)&s_abort || !mbar_wait_bounded(bar, parity))) {
+        dead = true;
+        fail();
+      }
+      dead = __any_sync(0xffffffffu, dead);  // the warp decides as one
+      tmem_fence_after();
+    };
+    while (walk.next(p, &seg)) {
+      const bool sh = seg.b < 0;
+      const int pair = sh ? p.pair_s : p.pair_o;
+      const int cap = p.tok << pair;
+      const int ntok = (sh ? p.B * p.N : p.N) - seg.mg * cap - (pair ? w * p.tok : 0);
+      const int nrows = max(0, min(p.tok, ntok)) * p.G;  // rows of this half in use
+      const bool busy = quad * 32 < nrows;               // whole warps of unused rows only wait
+      const int nt = pair ? seg.n : (seg.n + 1 - w) / 2;
+      float m = -INFINITY, l = 0.0f;
+      for (int i = 0; i < nt; ++i) {
+        const int t = pair ? i : 2 * i + w;
+        const int valid = seg.kvlen - (seg.t0 + t) * kAtKeys;  // entries of the tile
+        wait(&s_full[w], ns++ & 1);
+        if (!dead && valid < kAtKeys && (!pair || w == 0)) {
+          // the tile's last rows are beyond the prefix: whatever they hold,
+          // their products with weights of 0 have to be 0
+          const long long u = ring0 + 2 * seg.n - 1;  // the segment's last ring use
+          const int st = (int)(u % S);
+          wait(&full[st], (unsigned)((u / S) & 1));
+          if (r >= valid) {
+            uint8_t* row = ring + st * kTile + r * 128;
+#pragma unroll
+            for (int c = 0; c < kSub; ++c)
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                *reinterpret_cast<uint4*>(row + c * (kAtKeys * 128) + j * 16) =
+                    make_uint4(0, 0, 0, 0);
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
+        if (busy && !dead) {
+          uint32_t s0[32], s1[32], s2[32], s3[32];
+          tmem_ld32_async(sbase, s0);
+          tmem_ld32_async(sbase + 32, s1);
+          tmem_ld32_async(sbase + 64, s2);
+          tmem_ld32_async(sbase + 96, s3);
+          tmem_wait_ld(s0);
+          tmem_wait_ld(s1);
+          tmem_wait_ld(s2);
+          tmem_wait_ld(s3);
+          if (valid < kAtKeys) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              if (j >= valid) s0[j] = 0xFF800000u;
+              if (j + 32 >= valid) s1[j] = 0xFF800000u;
+              if (j + 64 >= valid) s2[j] = 0xFF800000u;
+              if (j + 96 >= valid) s3[j] = 0xFF800000u;
+            }
+          }
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            mx[0] = fmaxf(mx[0], __uint_as_float(s0[j]));
+            mx[1] = fmaxf(mx[1], __uint_as_float(s1[j]));
+            mx[2] = fmaxf(mx[2], __uint_as_float(s2[j]));
+            mx[3] = fmaxf(mx[3], __uint_as_float(s3[j]));
+          }
+          const float top = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2,
+                                  -1e30f);
+          if (i == 0) {
+            m = top;
+          } else if (__any_sync(0xffffffffu, top > m + kAtLazy)) {
+            // rescale this row's output; the tile before this one is in it
+            // (its product was issued before this tile's scores)
+            const float mn = fmaxf(m, top), f = ex2(m - mn);
+            m = mn;
+            l *= f;
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+              uint32_t o[32];
+              const uint32_t at = lanes + 2 * kAtKeys + w * D + c;
+              tmem_ld32(at, o);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+              tmem_st32(at, o);
+            }
+          }
+          const float nm = -m;
+          float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          auto weights = [&](const uint32_t (&a)[32], const uint32_t (&b)[32], uint32_t at) {
+            uint32_t pk[32];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const float x = ex2(__fmaf_rn(__uint_as_float(a[2 * j]), p.scale_log2, nm));
+              const float y = ex2(__fmaf_rn(__uint_as_float(a[2 * j + 1]), p.scale_log2, nm));
+              const float z = ex2(__fmaf_rn(__uint_as_float(b[2 * j]), p.scale_log2, nm));
+              const float u = ex2(__fmaf_rn(__uint_as_float(b[2 * j + 1]), p.scale_log2, nm));
+              sum[0] += x;
+              sum[1] += y;
+              sum[2] += z;
+              sum[3] += u;
+              pk[j] = pack_bf16(x, y);
+              pk[16 + j] = pack_bf16(z, u);
+            }
+            tmem_st32(at, pk);
+          };
+          weights(s0, s1, sbase);
+          weights(s2, s3, sbase + 32);
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          tmem_wait_st();
+        }
+        tmem_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[w]);
+      }
+      ring0 += 2 * seg.n;
+      // the partial: [D / 4][slot_rows][4], so that a warp's lanes (rows) store
+      // 512 consecutive bytes
+      if (nt > 0) wait(&o_full[w], no++ & 1);
+      float* slot = p.opart + seg.slot * (long long)p.slot_rows * D;
+      if (pair) {
+        const int row = w * p.half_rows + r;
+        if (busy && !dead) {
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            uint32_t o[32];
+            tmem_ld32(lanes + 2 * kAtKeys + w * D + c, o);
+            if (r < nrows) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                *reinterpret_cast<uint4*>(slot + ((c / 4 + j) * p.slot_rows + row) * 4) =
+                    make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+            }
+          }
+          if (r < nrows) p.ml[seg.slot * p.slot_rows + row] = make_float2(m, l);
+        }
+        tmem_fence_before();
+      } else {
+        // join the two halves; each takes half of the columns
+        s_ml[w][r] = make_float2(m, l);
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        tmem_fence_after();
+        if (busy && !dead) {
+          const float2 a = s_ml[0][r], b = s_ml[1][r];  // half 0 has at least one tile
+          const float mm = fmaxf(a.x, b.x);
+          const float fa = ex2(a.x - mm), fb = ex2(b.x - mm);
+#pragma unroll 1
+          for (int c = w * (D / 2); c < (w + 1) * (D / 2); c += 32) {
+            uint32_t o[32];
+            tmem_ld32(lanes + 2 * kAtKeys + c, o);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * fa);
+            if (seg.n > 1) {
+              uint32_t o1[32];
+              tmem_ld32(lanes + 2 * kAtKeys + D + c, o1);
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                o[j] = __float_as_uint(
+                    __fmaf_rn(__uint_as_float(o1[j]), fb, __uint_as_float(o[j])));
+            }
+            if (r < nrows) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                *reinterpret_cast<uint4*>(slot + ((c / 4 + j) * p.slot_rows + r) * 4) =
+                    make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+            }
+          }
+          if (w == 0 && r < nrows)
+            p.ml[seg.slot * p.slot_rows + r] = make_float2(mm, a.y * fa + b.y * fb);
+        }
+        // neither half's accumulators are written again before both are read
+        tmem_fence_before();
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+      }
+    }
+  }
+  tmem_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tmem_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512)
+                 : "memory");
+  }
+}
+
+// One warp per (node, key-value head): the node's ancestors one by one, in
+// float32, kAtFinHeads query heads at a time (a lane holds D / 32 elements of
+// the head), then the prefixes' partials.  The ancestors need nothing of the
+// kernel before this one and overlap its end.
 template <int D>
 __global__ void __launch_bounds__(kAtFinThreads) tree_attn_finish_kernel(const AttnParams p) {
   constexpr int kE = D / 32;  // elements per lane
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long item = (long long)blockIdx.x * (kAtFinThreads / 32) + warp;
-  if (item >= (long long)p.B * p.N * p.Hkv) return;
+  const bool live = item < (long long)p.B * p.N * p.Hkv;
   const int h = (int)(item % p.Hkv);
   const long long node = item / p.Hkv;
   const int b = (int)(node / p.N), n = (int)(node - (long long)b * p.N);
-  const int base = __ldg(p.base_len + b);
-  const bool ok = attn_seq_ok(p, base);
-  if (!ok && n == 0 && h == 0 && lane == 0) set_flag(p.flags, kFlagBadPath);
+  const int base = live ? __ldg(p.base_len + b) : 0;
+  const bool ok = live && attn_seq_ok(p, base);
+  if (live && !ok && n == 0 && h == 0 && lane == 0) set_flag(p.flags, kFlagBadPath);
   const int prefix = base - 1;
   const uint16_t* kseq = p.k + (long long)b * p.seq_stride + h * D;
   const uint16_t* vseq = p.v + (long long)b * p.seq_stride + h * D;
@@ -68,42 +693,21 @@ __global__ void __launch_bounds__(kAtFinThreads) tree_attn_finish_kernel(const A
       x[0] = bf16_lo(w); x[1] = bf16_hi(w);
     }
   };
+  bool waited = false;
   for (int g0 = 0; g0 < p.G; g0 += kAtFinHeads) {
     const int ng = min(kAtFinHeads, p.G - g0);
     float q[kAtFinHeads][kE], acc[kAtFinHeads][kE], m[kAtFinHeads], l[kAtFinHeads];
     const uint16_t* qrow = p.q + ((size_t)node * p.Hq + h * p.G + g0) * D;
 #pragma unroll
     for (int g = 0; g < kAtFinHeads; ++g) {
-      m[g] = -INFINITY;
+      m[g] = -1e30f;
       l[g] = 0.0f;
 #pragma unroll
       for (int e = 0; e < kE; ++e) acc[g][e] = q[g][e] = 0.0f;
-      if (g < ng) load(qrow + (size_t)g * D, q[g]);
+      if (ok && g < ng) load(qrow + (size_t)g * D, q[g]);
     }
-    auto visit = [&](const uint16_t* krow, const uint16_t* vrow) {
-      float kx[kE], vx[kE];
-      load(krow, kx);
-      load(vrow, vx);
-#pragma unroll
-      for (int g = 0; g < kAtFinHeads; ++g) {
-        if (g < ng) {
-          float s = 0.0f;
-#pragma unroll
-          for (int e = 0; e < kE; ++e) s = __fmaf_rn(q[g][e], kx[e], s);
-          s = warp_sum_f(s) * p.scale_log2;
-          const float mn = fmaxf(m[g], s);
-          const float a = ex2(m[g] - mn), w = ex2(s - mn);
-          m[g] = mn;
-          l[g] = __fmaf_rn(l[g], a, w);
-#pragma unroll
-          for (int e = 0; e < kE; ++e) acc[g][e] = __fmaf_rn(acc[g][e], a, w * vx[e]);
-        }
-      }
-    };
     const size_t es = (size_t)p.Hkv * D;
     if (ok) {
-      for (int j = 0; j < p.P; ++j) visit(p.pk + j * es + h * D, p.pv + j * es + h * D);
-      for (int j = 0; j < prefix; ++j) visit(kseq + j * es, vseq + j * es);
       const uint32_t* mrow = p.mask ? p.mask + (size_t)node * p.W : nullptr;
       for (int w = 0; w < p.W; ++w) {
         uint32_t bits;
@@ -117,21 +721,99 @@ __global__ void __launch_bounds__(kAtFinThreads) tree_attn_finish_kernel(const A
         while (bits) {
           const int u = 32 * w + __ffs(bits) - 1;
           bits &= bits - 1;
-          visit(kseq + (size_t)(prefix + u) * es, vseq + (size_t)(prefix + u) * es);
+          float kx[kE], vx[kE];
+          load(kseq + (size_t)(prefix + u) * es, kx);
+          load(vseq + (size_t)(prefix + u) * es, vx);
+#pragma unroll
+          for (int g = 0; g < kAtFinHeads; ++g) {
+            if (g < ng) {
+              float s = 0.0f;
+#pragma unroll
+              for (int e = 0; e < kE; ++e) s = __fmaf_rn(q[g][e], kx[e], s);
+              s = warp_sum_f(s) * p.scale_log2;
+              const float mn = fmaxf(m[g], s);
+              const float a = ex2(m[g] - mn), wgt = ex2(s - mn);
+              m[g] = mn;
+              l[g] = __fmaf_rn(l[g], a, wgt);
+#pragma unroll
+              for (int e = 0; e < kE; ++e) acc[g][e] = __fmaf_rn(acc[g][e], a, wgt * vx[e]);
+            }
+          }
+        }
+      }
+    }
+    if (!waited) {
+      asm volatile("griddepcontrol.wait;" ::: "memory");
+      asm volatile("griddepcontrol.launch_dependents;");
+      waited = true;
+    }
+    if (!live) return;
+    if (ok) {
+      const long long items_s = (long long)p.Hkv * p.mg_s, per = (long long)p.Hkv * p.mg_o;
+      const long long shared = items_s * p.tiles_s;
+      const long long total = shared + p.tstart[p.B] * per;
+      const long long at_b = p.tstart[b];
+      const int tiles_o = (int)(p.tstart[b + 1] - at_b);
+#pragma unroll 1
+      for (int cls = 0; cls < 2; ++cls) {
+        const int tiles = cls == 0 ? p.tiles_s : tiles_o;
+        if (tiles == 0) continue;
+        const int pair = cls == 0 ? p.pair_s : p.pair_o;
+        const int cap = p.tok << pair;
+        const int tokn = cls == 0 ? (int)node : n;
+        const int mg = tokn / cap, in = tokn - mg * cap;
+        const int half = in / p.tok;
+        const int row = half * p.half_rows + (in - half * p.tok) * p.G + g0;
+        const long long it = cls == 0 ? (long long)mg * p.Hkv + h
+                                      : items_s + (long long)b * per + (long long)mg * p.Hkv + h;
+        const long long s0 = cls == 0 ? it * tiles
+                                      : shared + at_b * per + ((long long)mg * p.Hkv + h) * tiles;
+        // the CTAs whose runs [c T / n, (c+1) T / n) meet the item's tiles
+        int c = (int)(s0 * p.nctas / total);
+        while (c + 1 < p.nctas && total * (c + 1) / p.nctas <= s0) ++c;
+        for (; c < p.nctas && total * c / p.nctas < s0 + tiles; ++c) {
+          if (total * c / p.nctas == total * (c + 1) / p.nctas) continue;  // an empty run
+          const long long slot = it + c;
+          const float* part = p.opart + slot * (long long)p.slot_rows * D;
+#pragma unroll
+          for (int g = 0; g < kAtFinHeads; ++g) {
+            if (g < ng) {
+              const float2 ml = p.ml[slot * p.slot_rows + row + g];
+              const float mn = fmaxf(m[g], ml.x);
+              const float fa = ex2(m[g] - mn), fb = ex2(ml.x - mn);
+              m[g] = mn;
+              l[g] = l[g] * fa + ml.y * fb;
+              if constexpr (kE == 4) {
+                const float4 o = *reinterpret_cast<const float4*>(
+                    part + ((size_t)lane * p.slot_rows + row + g) * 4);
+                acc[g][0] = acc[g][0] * fa + o.x * fb;
+                acc[g][1] = acc[g][1] * fa + o.y * fb;
+                acc[g][2] = acc[g][2] * fa + o.z * fb;
+                acc[g][3] = acc[g][3] * fa + o.w * fb;
+              } else {
+                const float2 o = *reinterpret_cast<const float2*>(
+                    part + ((size_t)(lane >> 1) * p.slot_rows + row + g) * 4 + (lane & 1) * 2);
+                acc[g][0] = acc[g][0] * fa + o.x * fb;
+                acc[g][1] = acc[g][1] * fa + o.y * fb;
+              }
+            }
+          }
         }
       }
     }
 #pragma unroll
     for (int g = 0; g < kAtFinHeads; ++g) {
       if (g < ng) {
-        const float r = l[g] > 0.0f ? 1.0f / l[g] : (l[g] == 0.0f ? 0.0f : l[g]);
+        // nothing visible: 0 and -inf
+        const float rl = l[g] == 0.0f ? 0.0f : 1.0f / l[g];
         uint16_t* orow = p.out + ((size_t)node * p.Hq + h * p.G + g0 + g) * D;
         if constexpr (kE == 4) {
           *reinterpret_cast<uint2*>(orow + lane * 4) =
-              make_uint2(pack_bf16(acc[g][0] * r, acc[g][1] * r),
-                         pack_bf16(acc[g][2] * r, acc[g][3] * r));
+              make_uint2(pack_bf16(acc[g][0] * rl, acc[g][1] * rl),
+                         pack_bf16(acc[g][2] * rl, acc[g][3] * rl));
         } else {
-          *reinterpret_cast<uint32_t*>(orow + lane * 2) = pack_bf16(acc[g][0] * r, acc[g][1] * r);
+          *reinterpret_cast<uint32_t*>(orow + lane * 2) =
+              pack_bf16(acc[g][0] * rl, acc[g][1] * rl);
         }
         if (p.lse && lane == 0)
           p.lse[(size_t)node * p.Hq + h * p.G + g0 + g] =
