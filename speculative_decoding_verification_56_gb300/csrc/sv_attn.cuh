@@ -10,19 +10,17 @@
 // sequence's own positions [0, base_len - 1), and the tree entries
 // base_len - 1 + u with bit u of the node's mask row set (mask null: u <= v).
 //
-// Two kernels.  The prefixes, where every node sees every entry, are matrix
-// products: tree_attn_kernel runs them on the tensor cores, the nodes' query
-// heads of one key-value head as the rows (a sequence's nodes for its own
-// prefix, the whole batch's nodes for the shared one, so that its entries are
-// read once for all), 128 entries of the cache at a time, and leaves
-// unnormalised partial sums.  tree_attn_finish_kernel adds each node's few
-// ancestors one by one, reading nothing that the node does not see, and joins
-// the partials.
+// The entries are taken 128 at a time by matrix products on the tensor cores,
+// with the nodes' query heads of one key-value head as the rows: a sequence's
+// nodes for its own entries (the tree's stand right behind the prefix, and
+// only their tiles look at the mask), the whole batch's nodes for the shared
+// prefix, so that its entries are read once for all.
 //
 // The work is cut into equal runs of (rows, 128 entries) tiles, one run per
 // SM, whatever the lengths: the tiles of all items (shared prefix first, then
 // sequence by sequence) stand in one line, CTA c takes [c T / n, (c+1) T / n),
-// and an item that is cut leaves one partial per CTA, in slot item + c.
+// and an item that is cut (or has a shared prefix to be joined with) leaves one
+// partial per CTA, in slot item + c, for tree_attn_finish_kernel to join.
 #pragma once
 
 #include "sv_lmhead.cuh"
@@ -37,7 +35,7 @@ constexpr int kAtMaxStages = 8;
 constexpr int kAtMaxCtas = 160;  // partial slots are laid out for at most this many CTAs
 constexpr float kAtLazy = 8.0f;  // a row's reference grows only past 2^8
 constexpr int kAtFinThreads = 128;
-constexpr int kAtFinHeads = 8;  // query heads of a key-value head held by a warp at once
+constexpr int kAtFinHeads = 4;  // query heads of a key-value head held by a warp at once
 
 template <int D>
 __host__ __device__ constexpr int at_tile_bytes() { return kAtKeys * D * 2; }
@@ -75,17 +73,25 @@ struct AttnParams {
 __device__ __forceinline__ bool attn_seq_ok(const AttnParams& p, int base) {
   return base >= 1 && (long long)base + p.N - 1 <= p.L;
 }
-// 128-entry tiles of a sequence's own prefix
+// 128-entry tiles of a sequence's own entries, prefix and tree
 __device__ __forceinline__ int attn_tiles(const AttnParams& p, int b) {
   const int base = __ldg(p.base_len + b);
-  return attn_seq_ok(p, base) ? (base - 1 + kAtKeys - 1) / kAtKeys : 0;
+  return attn_seq_ok(p, base) ? (base - 1 + p.N + kAtKeys - 1) / kAtKeys : 0;
+}
+
+// 1 / l and the log-sum; nothing visible (l = 0): output 0, log-sum -inf.
+__device__ __forceinline__ float attn_norm(float l) { return l == 0.0f ? 0.0f : 1.0f / l; }
+__device__ __forceinline__ float attn_lse(float m, float l) {
+  return l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
 // A CTA's run of tiles, item by item.
 struct AttnSeg {
   long long slot;     // of the partial: item + CTA
   int b, mg, h;       // b < 0: the shared prefix
-  int t0, n, kvlen;   // tiles [t0, t0 + n) of an item with kvlen entries
+  int t0, n, kvlen;   // tiles [t0, t0 + n) of an item with kvlen entries,
+  int plen;           // the first plen of them seen by all nodes
+  bool whole;         // all that the item's rows attend to
 };
 struct AttnWalk {
   long long pos, hi, bstart;  // bstart: first tile of sequence b in the line
@@ -101,7 +107,7 @@ struct AttnWalk {
       tiles = p.tiles_s;
       s->t0 = (int)(pos - it * tiles);
       s->b = -1;
-      s->kvlen = p.P;
+      s->kvlen = s->plen = p.P;
       s->slot = it + blockIdx.x;
     } else {
       const int per = p.Hkv * p.mg_o;
@@ -113,12 +119,14 @@ struct AttnWalk {
       it = (pos - bstart) / tiles;
       s->t0 = (int)(pos - bstart - it * tiles);
       s->b = b;
-      s->kvlen = __ldg(p.base_len + b) - 1;
+      s->plen = __ldg(p.base_len + b) - 1;
+      s->kvlen = s->plen + p.N;
       s->slot = items_s + (long long)b * per + it + blockIdx.x;
     }
     s->mg = (int)(it / p.Hkv);
     s->h = (int)(it - (long long)s->mg * p.Hkv);
     s->n = (int)min((long long)(tiles - s->t0), hi - pos);
+    s->whole = s->n == tiles && p.tiles_s == 0;
     pos += s->n;
     return true;
   }
@@ -166,16 +174,23 @@ __device__ __forceinline__ void umma_commit(uint64_t* bar) {
           smem_addr(bar))
       : "memory");
 }
-// 32 columns from registers, the store side of tmem_ld32 (no wait)
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+// 16 columns to and from registers; a store's wait is tmem_wait_st
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
-      "%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
+      "%13,%14,%15};" ::"r"(r[0]),
       "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
-      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
-      "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
-      "r"(r[30]), "r"(r[31]), "r"(taddr)
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
+      "%13,%14,%15}, [%16];\ntcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() {
@@ -218,6 +233,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   __shared__ int s_abort, s_b;
   __shared__ long long s_bstart, s_sum[kAtThreads / 32];
   __shared__ float2 s_ml[2][kAtRows];
+  __shared__ uint32_t s_bad[2][2][4];  // tree entries of a tile whose V is not finite: by
+                                       // turns, half
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(at_raw) + 1023) & ~(uintptr_t)1023);
   uint8_t* ring = smem + 2 * kTile;
@@ -498,27 +515,79 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       const int nrows = max(0, min(p.tok, ntok)) * p.G;  // rows of this half in use
       const bool busy = quad * 32 < nrows;               // whole warps of unused rows only wait
       const int nt = pair ? seg.n : (seg.n + 1 - w) / 2;
+      const int node = seg.mg * cap + (pair ? w * p.tok : 0) + r / p.G;  // own items: the row's
       float m = -INFINITY, l = 0.0f;
       for (int i = 0; i < nt; ++i) {
         const int t = pair ? i : 2 * i + w;
-        const int valid = seg.kvlen - (seg.t0 + t) * kAtKeys;  // entries of the tile
+        const int key0 = (seg.t0 + t) * kAtKeys;
+        const bool edge = key0 + kAtKeys > seg.plen;  // not all of the tile is seen by all
         wait(&s_full[w], ns++ & 1);
-        if (!dead && valid < kAtKeys && (!pair || w == 0)) {
-          // the tile's last rows are beyond the prefix: whatever they hold,
-          // their products with weights of 0 have to be 0
-          const long long u = ring0 + 2 * seg.n - 1;  // the segment's last ring use
-          const int st = (int)(u % S);
-          wait(&full[st], (unsigned)((u / S) & 1));
-          if (r >= valid) {
-            uint8_t* row = ring + st * kTile + r * 128;
+        uint32_t see[4];
+        bool spoilt = false;
+        if (edge) {
+          // V entries beyond the last are zeroed, whatever they hold: their
+          // products with weights of 0 have to be 0.  So are tree entries that
+          // are not finite, and the rows that see them become NaN.
+          if (!pair || w == 0) {
+            const long long u = ring0 + min(seg.n, t + 2 - pair) + t;  // V tile's ring use
+            const int st = (int)(u % S);
+            wait(&full[st], (unsigned)((u / S) & 1));
+            const int at = key0 + r;
+            bool bad = false;
+            if (!dead && at >= seg.plen) {
+              uint8_t* row = ring + st * kTile + r * 128;
+              if (at < seg.kvlen) {
 #pragma unroll
-            for (int c = 0; c < kSub; ++c)
+                for (int c = 0; c < kSub; ++c)
 #pragma unroll
-              for (int j = 0; j < 8; ++j)
-                *reinterpret_cast<uint4*>(row + c * (kAtKeys * 128) + j * 16) =
-                    make_uint4(0, 0, 0, 0);
+                  for (int j = 0; j < 8; ++j) {
+                    const uint4 x = lds128(row + c * (kAtKeys * 128) + j * 16);
+                    auto inf = [](uint32_t y) {
+                      return (y & 0x7F80u) == 0x7F80u || (y & 0x7F800000u) == 0x7F800000u;
+                    };
+                    bad |= inf(x.x) | inf(x.y) | inf(x.z) | inf(x.w);
+                  }
+              }
+              if (bad || at >= seg.kvlen) {
+#pragma unroll
+                for (int c = 0; c < kSub; ++c)
+#pragma unroll
+                  for (int j = 0; j < 8; ++j)
+                    *reinterpret_cast<uint4*>(row + c * (kAtKeys * 128) + j * 16) =
+                        make_uint4(0, 0, 0, 0);
+              }
+            }
+            const unsigned any = __ballot_sync(0xffffffffu, bad);
+            if (lane == 0) s_bad[i & 1][w][quad] = any;
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           }
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          if (pair)
+            asm volatile("bar.sync 2, 256;" ::: "memory");
+          else
+            asm volatile("bar.sync %0, 128;" ::"r"(3 + w) : "memory");
+          // the row's view of the tile, 32 entries per word
+          const int tree0 = key0 - seg.plen;  // tree number of the tile's first entry
+          const uint32_t* mrow = !sh && p.mask && node < p.N
+                                     ? p.mask + ((size_t)seg.b * p.N + node) * p.W : nullptr;
+          auto word = [&](int j) -> uint32_t {  // tree entries 32 j .. that the node sees
+            if (j < 0) return 0xFFFFFFFFu;
+            if (sh || j >= p.W) return 0u;
+            uint32_t x;
+            if (p.mask) {
+              x = mrow ? __ldg(mrow + j) : 0u;
+            } else {
+              const int c = node + 1 - 32 * j;
+              x = c >= 32 ? 0xFFFFFFFFu : c <= 0 ? 0u : (1u << c) - 1u;
+            }
+            const int left = p.N - 32 * j;
+            return left < 32 ? x & ((1u << left) - 1u) : x;
+          };
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int u = tree0 + 32 * c;
+            see[c] = __funnelshift_r(word(u >> 5), word((u >> 5) + 1), u & 31);
+            spoilt |= (see[c] & s_bad[i & 1][pair ? 0 : w][c]) != 0;
+          }
         }
         if (busy && !dead) {
           uint32_t s0[32], s1[32], s2[32], s3[32];
@@ -530,22 +599,22 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           tmem_wait_ld(s1);
           tmem_wait_ld(s2);
           tmem_wait_ld(s3);
-          if (valid < kAtKeys) {
+          if (edge) {
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
-              if (j >= valid) s0[j] = 0xFF800000u;
-              if (j + 32 >= valid) s1[j] = 0xFF800000u;
-              if (j + 64 >= valid) s2[j] = 0xFF800000u;
-              if (j + 96 >= valid) s3[j] = 0xFF800000u;
+              if (!((see[0] >> j) & 1)) s0[j] = 0xFF800000u;
+              if (!((see[1] >> j) & 1)) s1[j] = 0xFF800000u;
+              if (!((see[2] >> j) & 1)) s2[j] = 0xFF800000u;
+              if (!((see[3] >> j) & 1)) s3[j] = 0xFF800000u;
             }
           }
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            mx[0] = fmaxf(mx[0], __uint_as_float(s0[j]));
-            mx[1] = fmaxf(mx[1], __uint_as_float(s1[j]));
-            mx[2] = fmaxf(mx[2], __uint_as_float(s2[j]));
-            mx[3] = fmaxf(mx[3], __uint_as_float(s3[j]));
+          for (int j = 0; j < 32; j += 2) {
+            mx[0] = fmaxf(fmaxf(mx[0], __uint_as_float(s0[j])), __uint_as_float(s0[j + 1]));
+            mx[1] = fmaxf(fmaxf(mx[1], __uint_as_float(s1[j])), __uint_as_float(s1[j + 1]));
+            mx[2] = fmaxf(fmaxf(mx[2], __uint_as_float(s2[j])), __uint_as_float(s2[j + 1]));
+            mx[3] = fmaxf(fmaxf(mx[3], __uint_as_float(s3[j])), __uint_as_float(s3[j + 1]));
           }
           const float top = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2,
                                   -1e30f);
@@ -558,37 +627,43 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             m = mn;
             l *= f;
 #pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-              uint32_t o[32];
+            for (int c = 0; c < D; c += 16) {
+              uint32_t o[16];
               const uint32_t at = lanes + 2 * kAtKeys + w * D + c;
-              tmem_ld32(at, o);
+              tmem_ld16(at, o);
 #pragma unroll
-              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-              tmem_st32(at, o);
+              for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+              tmem_st16(at, o);
             }
           }
-          const float nm = -m;
-          float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-          auto weights = [&](const uint32_t (&a)[32], const uint32_t (&b)[32], uint32_t at) {
-            uint32_t pk[32];
+          // weights of 16 entries at a time, into 8 columns
+          const unsigned long long c2 = f2pack(p.scale_log2, p.scale_log2), nm2 = f2pack(-m, -m);
+          unsigned long long sum0 = 0, sum1 = 0;
+          auto weights = [&](const uint32_t (&a)[32], uint32_t at) {
+            uint32_t pk[16];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const float x = ex2(__fmaf_rn(__uint_as_float(a[2 * j]), p.scale_log2, nm));
-              const float y = ex2(__fmaf_rn(__uint_as_float(a[2 * j + 1]), p.scale_log2, nm));
-              const float z = ex2(__fmaf_rn(__uint_as_float(b[2 * j]), p.scale_log2, nm));
-              const float u = ex2(__fmaf_rn(__uint_as_float(b[2 * j + 1]), p.scale_log2, nm));
-              sum[0] += x;
-              sum[1] += y;
-              sum[2] += z;
-              sum[3] += u;
+            for (int j = 0; j < 16; j += 2) {
+              float x, y, z, u;
+              f2unpack(fma2(f2pack(__uint_as_float(a[2 * j]), __uint_as_float(a[2 * j + 1])), c2, nm2), x, y);
+              f2unpack(fma2(f2pack(__uint_as_float(a[2 * j + 2]), __uint_as_float(a[2 * j + 3])), c2, nm2), z, u);
+              x = ex2(x);
+              y = ex2(y);
+              z = ex2(z);
+              u = ex2(u);
+              sum0 = add2(sum0, f2pack(x, y));
+              sum1 = add2(sum1, f2pack(z, u));
               pk[j] = pack_bf16(x, y);
-              pk[16 + j] = pack_bf16(z, u);
+              pk[j + 1] = pack_bf16(z, u);
             }
-            tmem_st32(at, pk);
+            tmem_st16(at, pk);
           };
-          weights(s0, s1, sbase);
-          weights(s2, s3, sbase + 32);
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          weights(s0, sbase);
+          weights(s1, sbase + 16);
+          weights(s2, sbase + 32);
+          weights(s3, sbase + 48);
+          float a0, a1;
+          f2unpack(add2(sum0, sum1), a0, a1);
+          l += spoilt ? NAN : a0 + a1;
           tmem_wait_st();
         }
         tmem_fence_before();
@@ -596,25 +671,47 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         if (lane == 0) mbar_arrive(&p_full[w]);
       }
       ring0 += 2 * seg.n;
-      // the partial: [D / 4][slot_rows][4], so that a warp's lanes (rows) store
-      // 512 consecutive bytes
+      // the item's output, or its partial as [D / 4][slot_rows][4], so that a
+      // warp's lanes (rows) store 512 consecutive bytes
       if (nt > 0) wait(&o_full[w], no++ & 1);
+      const bool mine = r < nrows;
       float* slot = p.opart + seg.slot * (long long)p.slot_rows * D;
-      if (pair) {
-        const int row = w * p.half_rows + r;
-        if (busy && !dead) {
-#pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            uint32_t o[32];
-            tmem_ld32(lanes + 2 * kAtKeys + w * D + c, o);
-            if (r < nrows) {
+      const int row = (pair ? w * p.half_rows : 0) + r;
+      const size_t orow = ((size_t)max(seg.b, 0) * p.N + node) * p.Hq + seg.h * p.G + r % p.G;
+      auto put = [&](int c, const uint32_t (&o)[16], float norm) {
+        if (!mine) return;
+        if (seg.whole) {
+          uint32_t x[8];
 #pragma unroll
-              for (int j = 0; j < 8; ++j)
-                *reinterpret_cast<uint4*>(slot + ((c / 4 + j) * p.slot_rows + row) * 4) =
-                    make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
-            }
+          for (int j = 0; j < 8; ++j)
+            x[j] = pack_bf16(__uint_as_float(o[2 * j]) * norm, __uint_as_float(o[2 * j + 1]) * norm);
+          uint4* dst = reinterpret_cast<uint4*>(p.out + orow * D + c);
+          dst[0] = make_uint4(x[0], x[1], x[2], x[3]);
+          dst[1] = make_uint4(x[4], x[5], x[6], x[7]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<uint4*>(slot + ((c / 4 + j) * p.slot_rows + row) * 4) =
+                make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+        }
+      };
+      auto put_ml = [&](float mm, float ll) {
+        if (!mine) return;
+        if (!seg.whole)
+          p.ml[seg.slot * p.slot_rows + row] = make_float2(mm, ll);
+        else if (p.lse)
+          p.lse[orow] = attn_lse(mm, ll);
+      };
+      if (pair) {
+        if (busy && !dead) {
+          const float norm = attn_norm(l);
+#pragma unroll 1
+          for (int c = 0; c < D; c += 16) {
+            uint32_t o[16];
+            tmem_ld16(lanes + 2 * kAtKeys + w * D + c, o);
+            put(c, o, norm);
           }
-          if (r < nrows) p.ml[seg.slot * p.slot_rows + row] = make_float2(m, l);
+          put_ml(m, l);
         }
         tmem_fence_before();
       } else {
@@ -626,29 +723,23 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           const float2 a = s_ml[0][r], b = s_ml[1][r];  // half 0 has at least one tile
           const float mm = fmaxf(a.x, b.x);
           const float fa = ex2(a.x - mm), fb = ex2(b.x - mm);
+          const float ll = seg.n > 1 ? a.y * fa + b.y * fb : a.y;
+          const float norm = attn_norm(ll);
 #pragma unroll 1
-          for (int c = w * (D / 2); c < (w + 1) * (D / 2); c += 32) {
-            uint32_t o[32];
-            tmem_ld32(lanes + 2 * kAtKeys + c, o);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * fa);
+          for (int c = w * (D / 2); c < (w + 1) * (D / 2); c += 16) {
+            uint32_t o[16];
+            tmem_ld16(lanes + 2 * kAtKeys + c, o);
             if (seg.n > 1) {
-              uint32_t o1[32];
-              tmem_ld32(lanes + 2 * kAtKeys + D + c, o1);
+              uint32_t o1[16];
+              tmem_ld16(lanes + 2 * kAtKeys + D + c, o1);
 #pragma unroll
-              for (int j = 0; j < 32; ++j)
+              for (int j = 0; j < 16; ++j)
                 o[j] = __float_as_uint(
-                    __fmaf_rn(__uint_as_float(o1[j]), fb, __uint_as_float(o[j])));
+                    __fmaf_rn(__uint_as_float(o1[j]), fb, __uint_as_float(o[j]) * fa));
             }
-            if (r < nrows) {
-#pragma unroll
-              for (int j = 0; j < 8; ++j)
-                *reinterpret_cast<uint4*>(slot + ((c / 4 + j) * p.slot_rows + r) * 4) =
-                    make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
-            }
+            put(c, o, norm);
           }
-          if (w == 0 && r < nrows)
-            p.ml[seg.slot * p.slot_rows + r] = make_float2(mm, a.y * fa + b.y * fb);
+          if (w == 0) put_ml(mm, ll);
         }
         // neither half's accumulators are written again before both are read
         tmem_fence_before();
@@ -665,138 +756,89 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   }
 }
 
-// One warp per (node, key-value head): the node's ancestors one by one, in
-// float32, kAtFinHeads query heads at a time (a lane holds D / 32 elements of
-// the head), then the prefixes' partials.  The ancestors need nothing of the
-// kernel before this one and overlap its end.
+// Joins the partials of items that several CTAs share or that have a shared
+// prefix; other rows are done.  One warp per (node, key-value head),
+// kAtFinHeads query heads at a time, a lane holding D / 32 elements of a head.
 template <int D>
 __global__ void __launch_bounds__(kAtFinThreads) tree_attn_finish_kernel(const AttnParams p) {
   constexpr int kE = D / 32;  // elements per lane
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long item = (long long)blockIdx.x * (kAtFinThreads / 32) + warp;
-  const bool live = item < (long long)p.B * p.N * p.Hkv;
+  if (item >= (long long)p.B * p.N * p.Hkv) return;
   const int h = (int)(item % p.Hkv);
   const long long node = item / p.Hkv;
   const int b = (int)(node / p.N), n = (int)(node - (long long)b * p.N);
-  const int base = live ? __ldg(p.base_len + b) : 0;
-  const bool ok = live && attn_seq_ok(p, base);
-  if (live && !ok && n == 0 && h == 0 && lane == 0) set_flag(p.flags, kFlagBadPath);
-  const int prefix = base - 1;
-  const uint16_t* kseq = p.k + (long long)b * p.seq_stride + h * D;
-  const uint16_t* vseq = p.v + (long long)b * p.seq_stride + h * D;
-  auto load = [&](const uint16_t* src, float (&x)[kE]) {
-    if constexpr (kE == 4) {
-      const uint2 w = *reinterpret_cast<const uint2*>(src + lane * 4);
-      x[0] = bf16_lo(w.x); x[1] = bf16_hi(w.x); x[2] = bf16_lo(w.y); x[3] = bf16_hi(w.y);
-    } else {
-      const uint32_t w = *reinterpret_cast<const uint32_t*>(src + lane * 2);
-      x[0] = bf16_lo(w); x[1] = bf16_hi(w);
+  const bool ok = attn_seq_ok(p, __ldg(p.base_len + b));
+  if (!ok && n == 0 && h == 0 && lane == 0) set_flag(p.flags, kFlagBadPath);
+  // per class (shared prefix, own entries): the partials' first slot, the run
+  // of CTAs, and the row in the slot
+  long long it[2], total = 1;
+  int c0[2] = {0, 0}, c1[2] = {0, 0}, row[2];
+  if (ok) {
+    const long long items_s = (long long)p.Hkv * p.mg_s, per = (long long)p.Hkv * p.mg_o;
+    const long long shared = items_s * p.tiles_s;
+    total = shared + p.tstart[p.B] * per;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const long long tiles = k == 0 ? p.tiles_s : p.tstart[b + 1] - p.tstart[b];
+      if (tiles == 0) continue;
+      const int cap = p.tok << (k == 0 ? p.pair_s : p.pair_o);
+      const int tokn = k == 0 ? (int)node : n;
+      const int mg = tokn / cap, in = tokn - mg * cap;
+      const int half = in / p.tok;
+      const int index = mg * p.Hkv + h;
+      row[k] = half * p.half_rows + (in - half * p.tok) * p.G;
+      it[k] = k == 0 ? index : items_s + (long long)b * per + index;
+      const long long s0 = k == 0 ? index * tiles
+                                  : shared + p.tstart[b] * per + (long long)index * tiles;
+      // the CTAs whose runs [c T / n, (c+1) T / n) meet the item's tiles
+      int c = (int)(s0 * p.nctas / total);
+      while (total * (c + 1) / p.nctas <= s0) ++c;
+      c0[k] = c;
+      while (c < p.nctas && total * c / p.nctas < s0 + tiles) ++c;
+      c1[k] = c;
     }
-  };
-  bool waited = false;
+    if (p.tiles_s == 0 && c1[1] - c0[1] == 1) return;  // written by its only CTA
+  }
   for (int g0 = 0; g0 < p.G; g0 += kAtFinHeads) {
     const int ng = min(kAtFinHeads, p.G - g0);
-    float q[kAtFinHeads][kE], acc[kAtFinHeads][kE], m[kAtFinHeads], l[kAtFinHeads];
-    const uint16_t* qrow = p.q + ((size_t)node * p.Hq + h * p.G + g0) * D;
+    float acc[kAtFinHeads][kE], m[kAtFinHeads], l[kAtFinHeads];
 #pragma unroll
     for (int g = 0; g < kAtFinHeads; ++g) {
       m[g] = -1e30f;
       l[g] = 0.0f;
 #pragma unroll
-      for (int e = 0; e < kE; ++e) acc[g][e] = q[g][e] = 0.0f;
-      if (ok && g < ng) load(qrow + (size_t)g * D, q[g]);
+      for (int e = 0; e < kE; ++e) acc[g][e] = 0.0f;
     }
-    const size_t es = (size_t)p.Hkv * D;
-    if (ok) {
-      const uint32_t* mrow = p.mask ? p.mask + (size_t)node * p.W : nullptr;
-      for (int w = 0; w < p.W; ++w) {
-        uint32_t bits;
-        if (mrow) {
-          bits = __ldg(mrow + w);
-        } else {
-          const int c = n + 1 - 32 * w;
-          bits = c >= 32 ? 0xFFFFFFFFu : c <= 0 ? 0u : (1u << c) - 1u;
-        }
-        if (p.N - 32 * w < 32) bits &= (1u << (p.N - 32 * w)) - 1u;
-        while (bits) {
-          const int u = 32 * w + __ffs(bits) - 1;
-          bits &= bits - 1;
-          float kx[kE], vx[kE];
-          load(kseq + (size_t)(prefix + u) * es, kx);
-          load(vseq + (size_t)(prefix + u) * es, vx);
 #pragma unroll
-          for (int g = 0; g < kAtFinHeads; ++g) {
-            if (g < ng) {
-              float s = 0.0f;
+    for (int k = 0; k < 2; ++k) {
+      for (int c = c0[k]; c < c1[k]; ++c) {
+        if (total * c / p.nctas == total * (c + 1) / p.nctas) continue;  // an empty run
+        const long long slot = it[k] + c;
+        const float* part = p.opart + slot * (long long)p.slot_rows * D;
+        const float2* ml = p.ml + slot * p.slot_rows + row[k] + g0;
 #pragma unroll
-              for (int e = 0; e < kE; ++e) s = __fmaf_rn(q[g][e], kx[e], s);
-              s = warp_sum_f(s) * p.scale_log2;
-              const float mn = fmaxf(m[g], s);
-              const float a = ex2(m[g] - mn), wgt = ex2(s - mn);
-              m[g] = mn;
-              l[g] = __fmaf_rn(l[g], a, wgt);
-#pragma unroll
-              for (int e = 0; e < kE; ++e) acc[g][e] = __fmaf_rn(acc[g][e], a, wgt * vx[e]);
+        for (int g = 0; g < kAtFinHeads; ++g) {
+          if (g < ng) {
+            const float2 x = ml[g];
+            float o[kE];
+            if constexpr (kE == 4) {
+              const float4 y = *reinterpret_cast<const float4*>(
+                  part + ((size_t)lane * p.slot_rows + row[k] + g0 + g) * 4);
+              o[0] = y.x; o[1] = y.y; o[2] = y.z; o[3] = y.w;
+            } else {
+              const float2 y = *reinterpret_cast<const float2*>(
+                  part + ((size_t)(lane >> 1) * p.slot_rows + row[k] + g0 + g) * 4 + (lane & 1) * 2);
+              o[0] = y.x; o[1] = y.y;
             }
-          }
-        }
-      }
-    }
-    if (!waited) {
-      asm volatile("griddepcontrol.wait;" ::: "memory");
-      asm volatile("griddepcontrol.launch_dependents;");
-      waited = true;
-    }
-    if (!live) return;
-    if (ok) {
-      const long long items_s = (long long)p.Hkv * p.mg_s, per = (long long)p.Hkv * p.mg_o;
-      const long long shared = items_s * p.tiles_s;
-      const long long total = shared + p.tstart[p.B] * per;
-      const long long at_b = p.tstart[b];
-      const int tiles_o = (int)(p.tstart[b + 1] - at_b);
-#pragma unroll 1
-      for (int cls = 0; cls < 2; ++cls) {
-        const int tiles = cls == 0 ? p.tiles_s : tiles_o;
-        if (tiles == 0) continue;
-        const int pair = cls == 0 ? p.pair_s : p.pair_o;
-        const int cap = p.tok << pair;
-        const int tokn = cls == 0 ? (int)node : n;
-        const int mg = tokn / cap, in = tokn - mg * cap;
-        const int half = in / p.tok;
-        const int row = half * p.half_rows + (in - half * p.tok) * p.G + g0;
-        const long long it = cls == 0 ? (long long)mg * p.Hkv + h
-                                      : items_s + (long long)b * per + (long long)mg * p.Hkv + h;
-        const long long s0 = cls == 0 ? it * tiles
-                                      : shared + at_b * per + ((long long)mg * p.Hkv + h) * tiles;
-        // the CTAs whose runs [c T / n, (c+1) T / n) meet the item's tiles
-        int c = (int)(s0 * p.nctas / total);
-        while (c + 1 < p.nctas && total * (c + 1) / p.nctas <= s0) ++c;
-        for (; c < p.nctas && total * c / p.nctas < s0 + tiles; ++c) {
-          if (total * c / p.nctas == total * (c + 1) / p.nctas) continue;  // an empty run
-          const long long slot = it + c;
-          const float* part = p.opart + slot * (long long)p.slot_rows * D;
+            const float mn = fmaxf(m[g], x.x);
+            const float fa = ex2(m[g] - mn), fb = ex2(x.x - mn);
+            m[g] = mn;
+            l[g] = l[g] * fa + x.y * fb;
 #pragma unroll
-          for (int g = 0; g < kAtFinHeads; ++g) {
-            if (g < ng) {
-              const float2 ml = p.ml[slot * p.slot_rows + row + g];
-              const float mn = fmaxf(m[g], ml.x);
-              const float fa = ex2(m[g] - mn), fb = ex2(ml.x - mn);
-              m[g] = mn;
-              l[g] = l[g] * fa + ml.y * fb;
-              if constexpr (kE == 4) {
-                const float4 o = *reinterpret_cast<const float4*>(
-                    part + ((size_t)lane * p.slot_rows + row + g) * 4);
-                acc[g][0] = acc[g][0] * fa + o.x * fb;
-                acc[g][1] = acc[g][1] * fa + o.y * fb;
-                acc[g][2] = acc[g][2] * fa + o.z * fb;
-                acc[g][3] = acc[g][3] * fa + o.w * fb;
-              } else {
-                const float2 o = *reinterpret_cast<const float2*>(
-                    part + ((size_t)(lane >> 1) * p.slot_rows + row + g) * 4 + (lane & 1) * 2);
-                acc[g][0] = acc[g][0] * fa + o.x * fb;
-                acc[g][1] = acc[g][1] * fa + o.y * fb;
-              }
-            }
+            for (int e = 0; e < kE; ++e) acc[g][e] = acc[g][e] * fa + o[e] * fb;
           }
         }
       }
@@ -804,20 +846,17 @@ __global__ void __launch_bounds__(kAtFinThreads) tree_attn_finish_kernel(const A
 #pragma unroll
     for (int g = 0; g < kAtFinHeads; ++g) {
       if (g < ng) {
-        // nothing visible: 0 and -inf
-        const float rl = l[g] == 0.0f ? 0.0f : 1.0f / l[g];
-        uint16_t* orow = p.out + ((size_t)node * p.Hq + h * p.G + g0 + g) * D;
+        const float rl = attn_norm(l[g]);
+        const size_t at = (size_t)node * p.Hq + h * p.G + g0 + g;
         if constexpr (kE == 4) {
-          *reinterpret_cast<uint2*>(orow + lane * 4) =
+          *reinterpret_cast<uint2*>(p.out + at * D + lane * 4) =
               make_uint2(pack_bf16(acc[g][0] * rl, acc[g][1] * rl),
                          pack_bf16(acc[g][2] * rl, acc[g][3] * rl));
         } else {
-          *reinterpret_cast<uint32_t*>(orow + lane * 2) =
+          *reinterpret_cast<uint32_t*>(p.out + at * D + lane * 2) =
               pack_bf16(acc[g][0] * rl, acc[g][1] * rl);
         }
-        if (p.lse && lane == 0)
-          p.lse[(size_t)node * p.Hq + h * p.G + g0 + g] =
-              l[g] == 0.0f ? -INFINITY : (m[g] + log2f(l[g])) * 0.6931471805599453f;
+        if (p.lse && lane == 0) p.lse[at] = attn_lse(m[g], l[g]);
       }
     }
   }

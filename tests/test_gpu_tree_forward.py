@@ -262,6 +262,89 @@ def test_attention_hidden_branches_may_hold_anything():
         assert (out[0, n] == clean[0, n]).all() and (lse[0, n] == clean_lse[0, n]).all()
 
 
+def test_attention_entries_that_are_not_finite_stay_with_their_nodes():
+    """An infinite value or key of a tree entry spoils the nodes that see it and
+    no other, whatever tile or half they are in."""
+    B, N, Hq, Hkv, D, base = 2, 150, 4, 2, 64, 101
+    rng = np.random.default_rng(6)
+    par = parents_of(rng, B, N)
+    mask = oracle.tree_mask(par)[0]
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    q, kc = randn(gen, B, N, Hq, D), randn(gen, B, 300, Hkv, D)
+    vc = randn(gen, B, 300, Hkv, D)
+    maskd = torch.from_numpy(mask.view(np.int32)).cuda()
+    based = torch.tensor([base, base + 77], dtype=torch.int32, device="cuda")
+    clean, clean_lse = sv.tree_attention(q, kc, vc, maskd, based)
+    for what, u in (("v", 40), ("v", 120), ("k", 130), ("v", 149)):
+        k2, v2 = kc.clone(), vc.clone()
+        (v2 if what == "v" else k2)[0, base - 1 + u, 1, 3] = float("inf")
+        out, lse = sv.tree_attention(q, k2, v2, maskd, based)
+        torch.cuda.synchronize()
+        sees = torch.from_numpy((mask[0, :, u // 32] >> (u % 32)) & 1 != 0)
+        assert 0 < sees.sum() < N
+        assert (out[1] == clean[1]).all() and (lse[1] == clean_lse[1]).all()
+        assert (out[0, :, :2] == clean[0, :, :2]).all()          # heads of the other key head
+        assert (out[0, ~sees] == clean[0, ~sees]).all()
+        # a score of -inf (an infinite key against a negative query element) is a
+        # weight of 0; every other case spoils the head
+        none = (q[0, :, 2:, 3] < 0) & (what == "k")
+        assert (torch.isfinite(out[0, :, 2:]).all(dim=-1) == none)[sees].all()
+
+
+def reference_attention(q, k, v, see, scale, pk=None, pv=None):
+    """float64 on the GPU, sequence by sequence; `see` [B, N, L] truth values."""
+    B, N, Hq, D = q.shape
+    Hkv = k.shape[2]
+    out, lse = torch.zeros(B, N, Hq, D, dtype=torch.float64), torch.zeros(B, N, Hq, dtype=torch.float64)
+    big = torch.zeros(B, N, Hq, D, dtype=torch.float64)
+    for b in range(B):
+        for h in range(Hq):
+            kk, vv, ss = k[b, :, h // (Hq // Hkv)].double(), v[b, :, h // (Hq // Hkv)].double(), see[b]
+            if pk is not None:
+                kk = torch.cat([pk[:, h // (Hq // Hkv)].double(), kk])
+                vv = torch.cat([pv[:, h // (Hq // Hkv)].double(), vv])
+                ss = torch.cat([torch.ones(N, len(pk), dtype=torch.bool, device=ss.device), ss], 1)
+            z = (q[b, :, h].double() @ kk.T * scale).masked_fill(~ss, float("-inf"))
+            w = torch.softmax(z, 1)
+            out[b, :, h], big[b, :, h], lse[b, :, h] = (w @ vv).cpu(), (w @ vv.abs()).cpu(), torch.logsumexp(z, 1).cpu()
+    return out, big, lse
+
+
+@pytest.mark.parametrize("B,N,Hq,Hkv,D,ctx,P,chain", [
+    (24, 1, 16, 4, 128, 4000, 0, True),      # decoding: runs of tiles over several sequences
+    (9, 60, 32, 8, 128, 2500, 0, False),     # rows of two tiles, items cut anywhere
+    (33, 12, 8, 8, 64, 1700, 1000, False),   # a shared prefix beside own ones
+    (300, 2, 8, 1, 64, 90, 0, True),         # many short sequences
+    (2, 500, 8, 2, 128, 3000, 0, True),      # long chains: several items per sequence
+])
+def test_attention_many_tiles(B, N, Hq, Hkv, D, ctx, P, chain):
+    rng = np.random.default_rng(B)
+    gen = torch.Generator(device="cuda").manual_seed(B)
+    base = torch.from_numpy(rng.integers(1, ctx + 1, B).astype(np.int32)).cuda()
+    L = ctx + N
+    q, k, v = randn(gen, B, N, Hq, D), randn(gen, B, L, Hkv, D), randn(gen, B, L, Hkv, D)
+    pk = randn(gen, P, Hkv, D) if P else None
+    pv = randn(gen, P, Hkv, D) if P else None
+    node = torch.arange(N, device="cuda")
+    mask, tree = None, (node[None] <= node[:, None]).expand(B, N, N)
+    if not chain:
+        words, _, _ = oracle.tree_mask(parents_of(rng, B, N))
+        mask = torch.from_numpy(words.view(np.int32)).cuda()
+        tree = ((mask.long()[:, :, node // 32] >> (node % 32)) & 1) != 0
+    see = torch.zeros(B, N, L, dtype=torch.bool, device="cuda")
+    for b in range(B):
+        p0 = int(base[b]) - 1
+        see[b, :, :p0] = True
+        see[b, :, p0:p0 + N] = tree[b]
+    out, lse = sv.tree_attention(q, k, v, mask, base, prefix_k=pk, prefix_v=pv)
+    torch.cuda.synchronize()
+    want, big, wl = reference_attention(q, k, v, see, D ** -0.5, pk, pv)
+    eps = F32 * (2 * D * D ** -0.5 * float(q.float().abs().sum(-1).max()) * 6 + 2 * (ctx + P + N))
+    err = (out.double().cpu() - want).abs()
+    assert (err <= BF16 * (want.abs() + big) * (1 + 2.0 ** -6) + 2 * eps * big).all(), err.max()
+    assert ((lse.double().cpu() - wl).abs() <= eps + 2 * F32 * wl.abs()).all()
+
+
 def test_attention_tree_that_does_not_fit():
     B, N, Hq, Hkv, D, L = 4, 6, 4, 2, 64, 300
     gen = torch.Generator(device="cuda").manual_seed(1)
