@@ -552,7 +552,7 @@ AttnPlan attn_plan(int B, int N, int Hq, int Hkv, int D, int P) {
   a.half_rows = (int)std::min<long long>(a.tok, P > 0 ? all : N) * G;
   a.slot_rows = a.half_rows << std::max(a.pair_s, a.pair_o);
   const size_t slots = (size_t)Hkv * a.mg_s + (size_t)B * Hkv * a.mg_o + sv::kAtMaxCtas;
-  a.off_ml = align_up(kDataOffset + (size_t)(B + 1) * sizeof(long long));
+  a.off_ml = align_up(kDataOffset + slots * sizeof(int2));
   a.off_part = align_up(a.off_ml + slots * a.slot_rows * sizeof(float2));
   a.bytes = align_up(a.off_part + slots * a.slot_rows * D * sizeof(float));
   return a;
@@ -586,16 +586,16 @@ spec_status_t run_attention(const sv::AttnParams& prm, const CUtensorMap (&map)[
                          prm) != cudaSuccess)
     return SPEC_ERR_CUDA;
   g_launches.fetch_add(1, std::memory_order_relaxed);
-  const long long items = (long long)prm.B * prm.N * prm.Hkv;
-  constexpr int kPer = sv::kAtFinThreads / 32;
-  return launch(sv::tree_attn_finish_kernel<D>, (int)((items + kPer - 1) / kPer), 0, prm, stream,
-                true, 1, sv::kAtFinThreads);
+  const long long rows = (long long)prm.B * prm.N * prm.Hq;
+  const long long blocks = (rows + sv::kAtFinThreads - 1) / sv::kAtFinThreads;
+  return launch(sv::tree_attn_finish_kernel<D>, (int)(blocks * (D / 16)), 0, prm, stream, true, 1,
+                sv::kAtFinThreads);
 }
 
 bool attn_shape_ok(int B, int N, int Hq, int Hkv, int D, int P) {
   return B >= 0 && N >= 1 && N <= SPEC_ATTN_MAX_NODES && Hkv >= 1 && Hq >= Hkv && Hq <= 65536 &&
          Hq % Hkv == 0 && Hq / Hkv <= 128 && (D == 64 || D == 128) && P >= 0 &&
-         (long long)B * N <= INT32_MAX / 128 && (long long)B * N * Hkv <= INT32_MAX;
+         (long long)B * N <= INT32_MAX / 128 && (long long)B * N * Hq <= INT32_MAX;
 }
 
 }  // namespace
@@ -1177,7 +1177,7 @@ spec_status_t spec_tree_attention(const void* q, const void* k_cache, const void
   prm.half_rows = plan.half_rows;
   prm.slot_rows = plan.slot_rows;
   prm.nctas = std::min(sms, sv::kAtMaxCtas);
-  prm.tstart = reinterpret_cast<long long*>(ws + kDataOffset);
+  prm.span = reinterpret_cast<int2*>(ws + kDataOffset);
   prm.ml = reinterpret_cast<float2*>(ws + plan.off_ml);
   prm.opart = reinterpret_cast<float*>(ws + plan.off_part);
   // queries: boxes of 64 elements x the heads of one key-value head x nodes;

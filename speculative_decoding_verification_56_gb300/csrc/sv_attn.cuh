@@ -18,7 +18,7 @@
 //
 // The work is cut into equal runs of (rows, 128 entries) tiles, one run per
 // SM, whatever the lengths: the tiles of all items (shared prefix first, then
-// sequence by sequence) stand in one line, CTA c takes [c T / n, (c+1) T / n),
+// sequence by sequence) stand in one line of T, CTA c takes [c T / n, (c+1) T / n),
 // and an item that is cut (or has a shared prefix to be joined with) leaves one
 // partial per CTA, in slot item + c, for tree_attn_finish_kernel to join.
 #pragma once
@@ -33,9 +33,10 @@ constexpr int kAtKeys = 128;     // cache entries per tile
 constexpr int kAtThreads = 384;  // producer, MMA issuer, 2 idle warps, 2 x 4 softmax warps
 constexpr int kAtMaxStages = 8;
 constexpr int kAtMaxCtas = 160;  // partial slots are laid out for at most this many CTAs
-constexpr float kAtLazy = 8.0f;  // a row's reference grows only past 2^8
-constexpr int kAtFinThreads = 128;
-constexpr int kAtFinHeads = 4;  // query heads of a key-value head held by a warp at once
+constexpr float kAtLazy = 4096.0f;  // a tile's largest sum of a row's weights before its
+                                    // reference is renewed
+constexpr int kAtFinThreads = 256;
+constexpr int kAtSegs = 4;       // segment descriptors ahead of their use
 
 template <int D>
 __host__ __device__ constexpr int at_tile_bytes() { return kAtKeys * D * 2; }
@@ -67,15 +68,14 @@ struct AttnParams {
   int nctas;
   float* opart;             // [slot][D / 4][slot_rows][4]
   float2* ml;               // [slot][slot_rows]: reference (log2) and sum
-  long long* tstart;        // [B + 1]: tiles of the sequences before b, per item
+  int2* span;               // [items]: first and last CTA that holds a part of the item
 };
 
 __device__ __forceinline__ bool attn_seq_ok(const AttnParams& p, int base) {
   return base >= 1 && (long long)base + p.N - 1 <= p.L;
 }
 // 128-entry tiles of a sequence's own entries, prefix and tree
-__device__ __forceinline__ int attn_tiles(const AttnParams& p, int b) {
-  const int base = __ldg(p.base_len + b);
+__device__ __forceinline__ int attn_tiles_of(const AttnParams& p, int base) {
   return attn_seq_ok(p, base) ? (base - 1 + p.N + kAtKeys - 1) / kAtKeys : 0;
 }
 
@@ -85,50 +85,61 @@ __device__ __forceinline__ float attn_lse(float m, float l) {
   return l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
-// A CTA's run of tiles, item by item.
+// A CTA's run of tiles is cut into segments, one per item it meets.
 struct AttnSeg {
   long long slot;     // of the partial: item + CTA
-  int b, mg, h;       // b < 0: the shared prefix
-  int t0, n, kvlen;   // tiles [t0, t0 + n) of an item with kvlen entries,
-  int plen;           // the first plen of them seen by all nodes
-  bool whole;         // all that the item's rows attend to
+  int b, h;           // sequence (0 for the shared prefix), key-value head
+  int node0, ntok;    // first node and number of nodes of the item's rows: of all nodes of the
+                      // batch for the shared prefix, else of the sequence's
+  int t0, n;          // tiles [t0, t0 + n) of the item; n = 0: no more segments
+  int kvlen, plen;    // entries, and the first of them that not every node sees
+  int shared, pair, whole;  // whole: all that the item's rows attend to
 };
 struct AttnWalk {
   long long pos, hi, bstart;  // bstart: first tile of sequence b in the line
   int b;
-  __device__ __forceinline__ bool next(const AttnParams& p, AttnSeg* s) {
-    if (pos >= hi) return false;
+  __device__ __forceinline__ void next(const AttnParams& p, AttnSeg* s) {
+    s->n = 0;
+    if (pos >= hi) return;
     const long long items_s = (long long)p.Hkv * p.mg_s;
     const long long shared = items_s * p.tiles_s;
     long long it;
     int tiles;
-    if (pos < shared) {
+    s->shared = pos < shared;
+    if (s->shared) {
       it = pos / p.tiles_s;
       tiles = p.tiles_s;
       s->t0 = (int)(pos - it * tiles);
-      s->b = -1;
+      s->b = 0;
       s->kvlen = s->plen = p.P;
       s->slot = it + blockIdx.x;
+      s->pair = p.pair_s;
     } else {
       const int per = p.Hkv * p.mg_o;
-      tiles = attn_tiles(p, b);
+      int base = __ldg(p.base_len + b);
+      tiles = attn_tiles_of(p, base);
       while (pos >= bstart + (long long)per * tiles) {
         bstart += (long long)per * tiles;
-        tiles = attn_tiles(p, ++b);
+        base = __ldg(p.base_len + ++b);
+        tiles = attn_tiles_of(p, base);
       }
       it = (pos - bstart) / tiles;
       s->t0 = (int)(pos - bstart - it * tiles);
       s->b = b;
-      s->plen = __ldg(p.base_len + b) - 1;
+      s->plen = base - 1;
       s->kvlen = s->plen + p.N;
       s->slot = items_s + (long long)b * per + it + blockIdx.x;
+      s->pair = p.pair_o;
     }
-    s->mg = (int)(it / p.Hkv);
-    s->h = (int)(it - (long long)s->mg * p.Hkv);
+    const int mg = (int)it / p.Hkv;
+    s->h = (int)it - mg * p.Hkv;
+    s->node0 = mg * (p.tok << s->pair);
+    s->ntok = min(p.tok << s->pair, (s->shared ? p.B * p.N : p.N) - s->node0);
     s->n = (int)min((long long)(tiles - s->t0), hi - pos);
     s->whole = s->n == tiles && p.tiles_s == 0;
+    if (s->t0 == 0) p.span[s->slot - blockIdx.x].x = blockIdx.x;
+    if (s->t0 + s->n == tiles) p.span[s->slot - blockIdx.x].y = blockIdx.x;
     pos += s->n;
-    return true;
   }
 };
 
@@ -204,18 +215,43 @@ __device__ __forceinline__ uint64_t umma_desc_mn_sw128(uint32_t smem_byte_addr) 
   return umma_desc_sw128(smem_byte_addr) | ((uint64_t)((kAtKeys * 128) >> 4) << 16);
 }
 
-// Warp 0 copies (TMA), warp 1 issues the MMAs, warps 4-7 and 8-11 are the
-// softmax of half 0 and 1.  A half is 128 rows with its own score and output
-// accumulators in tensor memory (S0 | S1 | O0 | O1) and its own running
-// reference and sums.  With more rows than one tile holds (pair), the halves
-// are two row tiles over the same entries; otherwise both take the same rows
-// and alternate tiles, and are joined at the end of an item.  Either way one
-// half's softmax runs beside the other's products:
+// A wait in the kernel below.  The first test sleeps up to 1 ms in the
+// instruction; past that, the wait ends when it has taken kWaitLimitNs or
+// another role of the CTA has given up.
+__device__ __forceinline__ bool at_wait_slow(uint64_t* bar, unsigned parity, const int* abort) {
+  const uint64_t t0 = global_ns();
+  for (unsigned it = 0; it < (1u << 30); ++it) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*(const volatile int*)abort || global_ns() - t0 > kWaitLimitNs) return false;
+  }
+  return false;
+}
+__device__ __forceinline__ bool at_wait(uint64_t* bar, unsigned parity, const int* abort) {
+  return mbar_try_wait(bar, parity) || at_wait_slow(bar, parity, abort);
+}
+// the same for a whole warp, with one answer
+__device__ __forceinline__ bool at_wait_warp(uint64_t* bar, unsigned parity, const int* abort) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return __all_sync(0xffffffffu, at_wait_slow(bar, parity, abort));
+}
+
+// Warp 0 copies (TMA), warp 1 issues the MMAs, warp 2 lists the CTA's
+// segments, warps 4-7 and 8-11 are the softmax of half 0 and 1.  A half is
+// 128 rows with its own score and output accumulators in tensor memory
+// (S0 | S1 | O0 | O1) and its own running reference and sums.  With more rows
+// than one tile holds (pair), the halves are two row tiles over the same
+// entries; otherwise both take the same rows and alternate tiles, and are
+// joined at the end of an item.  Either way one half's softmax runs beside
+// the other's products:
 //   S = Q K^T -> registers -> P = 2^(S c - m), bf16, over S in tensor memory
 //   O += P V   (P from tensor memory)
-// The reference m of a row follows the row's maximum only when that has grown
-// by more than 2^8 (P then stays below 2^8, harmless in bf16 and float32), so
-// that O is rarely rescaled.
+// The reference m of a row is the maximum of the first tile, and is renewed
+// only by a tile whose weights add up to more than 2^12 (up to there they are
+// harmless in bf16 and float32): the maximum of a tile is not looked for, the
+// sum that softmax needs anyway shows whether the reference still serves, and
+// the weights are kept back until it is known.
+//   Every wait between the roles is a bounded one on an mbarrier; a role
+// that gives up leaves, and the others follow.
 template <int D>
 __global__ void __launch_bounds__(kAtThreads, 1)
     tree_attn_kernel(const __grid_constant__ CUtensorMap map_q,
@@ -226,12 +262,15 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   constexpr int kTile = at_tile_bytes<D>();
   constexpr int S = at_stages<D>();
   constexpr int kSub = D / 64;  // 64-element column blocks of a tile (128 rows x 128 bytes)
+  constexpr int kWarps = kAtThreads / 32;
   extern __shared__ uint8_t at_raw[];
   __shared__ uint64_t full[kAtMaxStages], empty[kAtMaxStages];
   __shared__ uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], drain;
+  __shared__ uint64_t seg_full[kAtSegs], seg_empty[kAtSegs], half_bar[2], pair_bar;
+  __shared__ AttnSeg s_seg[kAtSegs];
   __shared__ uint32_t tmem_holder;
   __shared__ int s_abort, s_b;
-  __shared__ long long s_bstart, s_sum[kAtThreads / 32];
+  __shared__ long long s_bstart, s_sum[kWarps];
   __shared__ float2 s_ml[2][kAtRows];
   __shared__ uint32_t s_bad[2][2][4];  // tree entries of a tile whose V is not finite: by
                                        // turns, half
@@ -250,6 +289,12 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       mbar_init(&s_full[w], 1);
       mbar_init(&p_full[w], 4);
       mbar_init(&o_full[w], 1);
+      mbar_init(&half_bar[w], 4);
+    }
+    mbar_init(&pair_bar, 8);
+    for (int s = 0; s < kAtSegs; ++s) {
+      mbar_init(&seg_full[s], 1);
+      mbar_init(&seg_empty[s], 10);  // copies, MMAs, eight softmax warps
     }
     mbar_init(&drain, 1);
     s_abort = 0;
@@ -268,11 +313,14 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   // global memory is touched before that grid has finished
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
-  // the run [lo, hi) of this CTA and the sequence it starts in
+  // the run [lo, hi) of this CTA and the sequence it starts in: a scan of the
+  // sequences' tile counts, kAtThreads sequences at a time
   const int per = p.Hkv * p.mg_o;
   const long long shared = (long long)p.Hkv * p.mg_s * p.tiles_s;
-  long long own = 0;
-  for (int b = threadIdx.x; b < p.B; b += kAtThreads) own += attn_tiles(p, b);
+  int mine = (int)threadIdx.x < p.B ? attn_tiles_of(p, __ldg(p.base_len + threadIdx.x)) : 0;
+  long long own = mine;
+  for (int b = threadIdx.x + kAtThreads; b < p.B; b += kAtThreads)
+    own += attn_tiles_of(p, __ldg(p.base_len + b));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) own += __shfl_xor_sync(0xffffffffu, own, o);
   if (lane == 0) s_sum[warp] = own;
@@ -280,14 +328,18 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   __syncthreads();
   tmem_fence_after();
   own = 0;
-  for (int w = 0; w < kAtThreads / 32; ++w) own += s_sum[w];
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) own += s_sum[w];
   const long long total = shared + own * per;
-  const long long lo = total * blockIdx.x / p.nctas, hi = total * (blockIdx.x + 1) / p.nctas;
+  const int n = (int)min((long long)p.nctas, total);  // no run is empty; other CTAs have none
+  const long long lo = (int)blockIdx.x < n ? total * blockIdx.x / n : 0;
+  const long long hi = (int)blockIdx.x < n ? total * (blockIdx.x + 1) / n : 0;
+  if (threadIdx.x == 0 && lo < shared) s_bstart = shared;
   {
     long long run = 0;
     for (int b0 = 0; b0 < p.B; b0 += kAtThreads) {
       const int b = b0 + threadIdx.x;
-      const long long mine = b < p.B ? attn_tiles(p, b) : 0;
+      if (b0 > 0) mine = b < p.B ? attn_tiles_of(p, __ldg(p.base_len + b)) : 0;
       long long incl = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -298,56 +350,72 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       if (lane == 31) s_sum[warp] = incl;
       __syncthreads();
       long long before = run;
-      for (int w = 0; w < kAtThreads / 32; ++w) {
+      for (int w = 0; w < kWarps; ++w) {
         if (w < warp) before += s_sum[w];
         run += s_sum[w];
       }
       const long long excl = before + incl - mine;
-      if (b < p.B) {
-        if (blockIdx.x == 0) p.tstart[b] = excl;
-        if (lo >= shared && lo - shared >= excl * per && lo - shared < (excl + mine) * per) {
-          s_b = b;
-          s_bstart = shared + excl * per;
-        }
+      if (lo >= shared && lo - shared >= excl * per && lo - shared < (excl + mine) * per) {
+        s_b = b;
+        s_bstart = shared + excl * per;
       }
     }
-    if (blockIdx.x == 0 && threadIdx.x == 0) p.tstart[p.B] = run;
   }
-  if (threadIdx.x == 0 && lo < shared) s_bstart = shared;
   __syncthreads();
   const uint32_t tmem = tmem_holder;
-  AttnWalk walk{lo, hi, s_bstart, s_b};
-  AttnSeg seg;
+  const int* abort = &s_abort;
   auto fail = [&]() {
     s_abort = 1;
     set_flag(p.flags, kFlagTimeout);
   };
 
-  if (warp == 0) {
+  if (warp == 2) {
+    if (lane == 0) {
+      // ---------------- segments ----------------
+      AttnWalk walk{lo, hi, s_bstart, s_b};
+      for (unsigned k = 0;; ++k) {
+        AttnSeg seg;
+        walk.next(p, &seg);
+        const unsigned at = k % kAtSegs;
+        if (!at_wait(&seg_empty[at], ((k / kAtSegs) & 1) ^ 1u, abort)) {
+          fail();
+          break;
+        }
+        s_seg[at] = seg;
+        mbar_arrive(&seg_full[at]);
+        if (seg.n == 0) break;
+      }
+    }
+    __syncwarp();
+  } else if (warp == 0) {
     if (lane == 0) {
       // ---------------- copies ----------------
       int stage = 0, issued = 0;
       unsigned phase = 0, nq = 0;
-      bool ok = true;
-      while (ok && walk.next(p, &seg)) {
-        const bool sh = seg.b < 0;
-        const int pair = sh ? p.pair_s : p.pair_o;
-        const int cap = p.tok << pair;
-        const int tok0 = (sh ? 0 : seg.b * p.N) + seg.mg * cap;
-        if (*(volatile int*)&s_abort || !mbar_wait_bounded(&q_empty, (nq & 1) ^ 1u)) {
+      for (bool ok = true; ok;) {
+        const unsigned at = nq % kAtSegs;
+        if (!at_wait(&seg_full[at], (nq / kAtSegs) & 1, abort)) {
           fail();
           break;
         }
-        mbar_expect_tx(&q_full, (unsigned)((1 + pair) * kSub * p.tok * p.G * 128));
-        for (int w = 0; w <= pair; ++w)
+        const AttnSeg seg = s_seg[at];
+        mbar_arrive(&seg_empty[at]);
+        if (seg.n == 0) break;
+        if (!at_wait(&q_empty, (nq & 1) ^ 1u, abort)) {
+          fail();
+          break;
+        }
+        ++nq;
+        const int tok0 = seg.b * p.N + seg.node0;
+        mbar_expect_tx(&q_full, (unsigned)((1 + seg.pair) * kSub * p.tok * p.G * 128));
+        for (int w = 0; w <= seg.pair; ++w)
           for (int c = 0; c < kSub; ++c)
             tma_load_3d(smem + w * kTile + c * (kAtRows * 128), &map_q, c * 64, seg.h * p.G,
                         tok0 + w * p.tok, &q_full);
-        ++nq;
-        const CUtensorMap* mk = sh ? &map_pk : &map_k;
-        const CUtensorMap* mv = sh ? &map_pv : &map_v;
+        const CUtensorMap* mk = seg.shared ? &map_pk : &map_k;
+        const CUtensorMap* mv = seg.shared ? &map_pv : &map_v;
         auto put = [&](const CUtensorMap* m, int t) {
-          if (*(volatile int*)&s_abort || !mbar_wait_bounded(&empty[stage], phase ^ 1u)) {
+          if (!at_wait(&empty[stage], phase ^ 1u, abort)) {
             ok = false;
             fail();
             return;
@@ -355,7 +423,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           mbar_expect_tx(&full[stage], kTile);
           for (int c = 0; c < kSub; ++c)
             tma_load_4d(ring + stage * kTile + c * (kAtKeys * 128), m, c * 64, seg.h,
-                        (seg.t0 + t) * kAtKeys, sh ? 0 : seg.b, &full[stage]);
+                        (seg.t0 + t) * kAtKeys, seg.b, &full[stage]);
           ++issued;
           if (++stage == S) {
             stage = 0;
@@ -363,7 +431,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           }
         };
         // in the order of use: each V tile, then the K tile `ahead` further on
-        const int ahead = 2 - pair;
+        const int ahead = 2 - seg.pair;
         for (int t = 0; ok && t < seg.n + ahead; ++t) {
           if (t >= ahead) put(mv, t - ahead);
           if (ok && t < seg.n) put(mk, t);
@@ -384,10 +452,10 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       const uint64_t kdesc = umma_desc_sw128(smem_addr(ring));
       const uint64_t vdesc = umma_desc_mn_sw128(smem_addr(ring));
       int stage = 0;
-      unsigned phase = 0, nq = 0, np[2] = {0, 0};
+      unsigned phase = 0, nq = 0, np0 = 0, np1 = 0;
       bool ok = true;
       auto wait = [&](uint64_t* bar, unsigned parity) {
-        if (ok && (*(volatile int*)&s_abort || !mbar_wait_bounded(bar, parity))) {
+        if (!at_wait(bar, parity & 1, abort)) {
           ok = false;
           fail();
         }
@@ -421,11 +489,12 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           umma_ts(tmem + 2 * kAtKeys + w * D, tmem + w * kAtKeys + kk * 8,
                   b + (uint64_t)(kk * 2048 >> 4), id_pv, (!first || kk) ? 1u : 0u);
       };
-      while (ok && walk.next(p, &seg)) {
-        const int pair = seg.b < 0 ? p.pair_s : p.pair_o;
-        const int n = seg.n;
-        if (!wait(&q_full, nq & 1)) break;
-        ++nq;
+      while (ok) {
+        const unsigned at = nq % kAtSegs;
+        if (!wait(&seg_full[at], nq / kAtSegs)) break;
+        const int n = s_seg[at].n, pair = s_seg[at].pair;
+        mbar_arrive(&seg_empty[at]);
+        if (n == 0 || !wait(&q_full, nq++)) break;
         if (pair) {
           if (!wait(&full[stage], phase)) break;
           scores(0, 0);
@@ -437,18 +506,18 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             const int vst = stage;
             if (!wait(&full[stage], phase)) break;
             advance();
-            if (!wait(&p_full[0], np[0]++ & 1)) break;
+            const bool more = t + 1 < n;
+            if (more && !wait(&full[stage], phase)) break;
+            if (!wait(&p_full[0], np0++)) break;
             output(0, vst, t == 0);
-            if (t + 1 < n) {
-              if (!wait(&full[stage], phase)) break;
+            if (more)
               scores(0, 0);
-            } else {
+            else
               umma_commit(&o_full[0]);
-            }
-            if (!wait(&p_full[1], np[1]++ & 1)) break;
+            if (!wait(&p_full[1], np1++)) break;
             output(1, vst, t == 0);
             umma_commit(&empty[vst]);
-            if (t + 1 < n) {
+            if (more) {
               scores(1, 1);
               umma_commit(&empty[stage]);
               if (t + 2 == n) umma_commit(&q_empty);
@@ -469,11 +538,12 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             const int w = t & 1, vst = stage;
             if (!wait(&full[stage], phase)) break;
             advance();
-            if (!wait(&p_full[w], np[w]++ & 1)) break;
+            const bool more = t + 2 < n;
+            if (more && !wait(&full[stage], phase)) break;
+            if (!wait(&p_full[w], w ? np1++ : np0++)) break;
             output(w, vst, t < 2);
             umma_commit(&empty[vst]);
-            if (t + 2 < n) {
-              if (!wait(&full[stage], phase)) break;
+            if (more) {
               scores(w, 0);
               umma_commit(&empty[stage]);
               if (t + 3 == n) umma_commit(&q_empty);
@@ -494,35 +564,68 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     const int w = (warp - 4) >> 2;                // half
     const int quad = warp & 3;                    // tensor-memory lanes 32 quad ..
     const int r = quad * 32 + lane;               // row of the half
+    const int rtok = r / p.G, rhead = r - rtok * p.G;
     const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
     const uint32_t sbase = lanes + w * kAtKeys;
-    unsigned ns = 0, no = 0;  // uses of s_full / o_full so far
-    long long ring0 = 0;      // ring uses before this segment
-    bool dead = false;        // a wait gave up: only the barriers are kept up
-    auto wait = [&](uint64_t* bar, unsigned parity) {
-      if (!dead && (*(volatile int*)&s_abort || !mbar_wait_bounded(bar, parity))) {
-        dead = true;
-        fail();
-      }
-      dead = __any_sync(0xffffffffu, dead);  // the warp decides as one
-      tmem_fence_after();
+    unsigned ns = 0, no = 0, nh = 0, npair = 0;  // uses of the barriers so far
+    long long ring0 = 0;                         // ring uses before this segment
+    // all warps of a half, or of both halves, meet
+    auto meet = [&](uint64_t* bar, unsigned& uses) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar);
+      return at_wait_warp(bar, uses++ & 1, abort);
     };
-    while (walk.next(p, &seg)) {
-      const bool sh = seg.b < 0;
-      const int pair = sh ? p.pair_s : p.pair_o;
-      const int cap = p.tok << pair;
-      const int ntok = (sh ? p.B * p.N : p.N) - seg.mg * cap - (pair ? w * p.tok : 0);
-      const int nrows = max(0, min(p.tok, ntok)) * p.G;  // rows of this half in use
-      const bool busy = quad * 32 < nrows;               // whole warps of unused rows only wait
+    bool ok = true;
+    for (unsigned k = 0; ok; ++k) {
+      if (!at_wait_warp(&seg_full[k % kAtSegs], (k / kAtSegs) & 1, abort)) {
+        ok = false;
+        break;
+      }
+      const AttnSeg seg = s_seg[k % kAtSegs];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&seg_empty[k % kAtSegs]);
+      if (seg.n == 0) break;
+      const int pair = seg.pair;
+      const int node = seg.node0 + (pair ? w * p.tok : 0) + rtok;
+      const int nrows = max(0, min(p.tok, seg.ntok - (pair ? w * p.tok : 0))) * p.G;
+      const bool busy = quad * 32 < nrows;  // whole warps of unused rows only wait
       const int nt = pair ? seg.n : (seg.n + 1 - w) / 2;
-      const int node = seg.mg * cap + (pair ? w * p.tok : 0) + r / p.G;  // own items: the row's
-      float m = -INFINITY, l = 0.0f;
+      float m = -1e30f, l = 0.0f;
       for (int i = 0; i < nt; ++i) {
         const int t = pair ? i : 2 * i + w;
         const int key0 = (seg.t0 + t) * kAtKeys;
         const bool edge = key0 + kAtKeys > seg.plen;  // not all of the tile is seen by all
-        wait(&s_full[w], ns++ & 1);
         uint32_t see[4];
+        if (edge) {
+          // the row's view of the tile, 32 entries per word
+          const int tree0 = key0 - seg.plen;  // tree number of the tile's first entry
+          const uint32_t* mrow = !seg.shared && p.mask && node < p.N
+                                     ? p.mask + ((size_t)seg.b * p.N + node) * p.W : nullptr;
+          auto word = [&](int j) -> uint32_t {  // tree entries 32 j .. that the node sees
+            if (j < 0) return 0xFFFFFFFFu;
+            if (seg.shared || j >= p.W) return 0u;
+            uint32_t x;
+            if (p.mask) {
+              x = mrow ? __ldg(mrow + j) : 0u;
+            } else {
+              const int c = node + 1 - 32 * j;
+              x = c >= 32 ? 0xFFFFFFFFu : c <= 0 ? 0u : (1u << c) - 1u;
+            }
+            const int left = p.N - 32 * j;
+            return left < 32 ? x & ((1u << left) - 1u) : x;
+          };
+          const int j0 = tree0 >> 5;
+          uint32_t x[5];
+#pragma unroll
+          for (int c = 0; c < 5; ++c) x[c] = word(j0 + c);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) see[c] = __funnelshift_r(x[c], x[c + 1], tree0 & 31);
+        }
+        if (!at_wait_warp(&s_full[w], ns++ & 1, abort)) {
+          ok = false;
+          break;
+        }
+        tmem_fence_after();
         bool spoilt = false;
         if (edge) {
           // V entries beyond the last are zeroed, whatever they hold: their
@@ -531,17 +634,20 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           if (!pair || w == 0) {
             const long long u = ring0 + min(seg.n, t + 2 - pair) + t;  // V tile's ring use
             const int st = (int)(u % S);
-            wait(&full[st], (unsigned)((u / S) & 1));
+            if (!at_wait_warp(&full[st], (unsigned)((u / S) & 1), abort)) {
+              ok = false;
+              break;
+            }
             const int at = key0 + r;
             bool bad = false;
-            if (!dead && at >= seg.plen) {
+            if (at >= seg.plen) {
               uint8_t* row = ring + st * kTile + r * 128;
               if (at < seg.kvlen) {
 #pragma unroll
                 for (int c = 0; c < kSub; ++c)
 #pragma unroll
-                  for (int j = 0; j < 8; ++j) {
-                    const uint4 x = lds128(row + c * (kAtKeys * 128) + j * 16);
+                  for (int j = 0; j < 8; ++j) {  // by turns, so that rows meet other banks
+                    const uint4 x = lds128(row + c * (kAtKeys * 128) + ((j + r) & 7) * 16);
                     auto inf = [](uint32_t y) {
                       return (y & 0x7F80u) == 0x7F80u || (y & 0x7F800000u) == 0x7F800000u;
                     };
@@ -553,7 +659,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                 for (int c = 0; c < kSub; ++c)
 #pragma unroll
                   for (int j = 0; j < 8; ++j)
-                    *reinterpret_cast<uint4*>(row + c * (kAtKeys * 128) + j * 16) =
+                    *reinterpret_cast<uint4*>(row + c * (kAtKeys * 128) + ((j + r) & 7) * 16) =
                         make_uint4(0, 0, 0, 0);
               }
             }
@@ -561,192 +667,213 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             if (lane == 0) s_bad[i & 1][w][quad] = any;
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           }
-          if (pair)
-            asm volatile("bar.sync 2, 256;" ::: "memory");
-          else
-            asm volatile("bar.sync %0, 128;" ::"r"(3 + w) : "memory");
-          // the row's view of the tile, 32 entries per word
-          const int tree0 = key0 - seg.plen;  // tree number of the tile's first entry
-          const uint32_t* mrow = !sh && p.mask && node < p.N
-                                     ? p.mask + ((size_t)seg.b * p.N + node) * p.W : nullptr;
-          auto word = [&](int j) -> uint32_t {  // tree entries 32 j .. that the node sees
-            if (j < 0) return 0xFFFFFFFFu;
-            if (sh || j >= p.W) return 0u;
-            uint32_t x;
-            if (p.mask) {
-              x = mrow ? __ldg(mrow + j) : 0u;
-            } else {
-              const int c = node + 1 - 32 * j;
-              x = c >= 32 ? 0xFFFFFFFFu : c <= 0 ? 0u : (1u << c) - 1u;
-            }
-            const int left = p.N - 32 * j;
-            return left < 32 ? x & ((1u << left) - 1u) : x;
-          };
+          ok = pair ? meet(&pair_bar, npair) : meet(&half_bar[w], nh);
+          if (!ok) break;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int u = tree0 + 32 * c;
-            see[c] = __funnelshift_r(word(u >> 5), word((u >> 5) + 1), u & 31);
-            spoilt |= (see[c] & s_bad[i & 1][pair ? 0 : w][c]) != 0;
-          }
+          for (int c = 0; c < 4; ++c) spoilt |= (see[c] & s_bad[i & 1][pair ? 0 : w][c]) != 0;
         }
-        if (busy && !dead) {
-          uint32_t s0[32], s1[32], s2[32], s3[32];
-          tmem_ld32_async(sbase, s0);
-          tmem_ld32_async(sbase + 32, s1);
-          tmem_ld32_async(sbase + 64, s2);
-          tmem_ld32_async(sbase + 96, s3);
-          tmem_wait_ld(s0);
-          tmem_wait_ld(s1);
-          tmem_wait_ld(s2);
-          tmem_wait_ld(s3);
-          if (edge) {
+        if (busy) {
+          const unsigned long long c2 = f2pack(p.scale_log2, p.scale_log2);
+          unsigned long long sum0, sum1, nm2;
+          auto hide = [&](uint32_t (&a)[32], uint32_t bits) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              if (!((see[0] >> j) & 1)) s0[j] = 0xFF800000u;
-              if (!((see[1] >> j) & 1)) s1[j] = 0xFF800000u;
-              if (!((see[2] >> j) & 1)) s2[j] = 0xFF800000u;
-              if (!((see[3] >> j) & 1)) s3[j] = 0xFF800000u;
-            }
-          }
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int j = 0; j < 32; j += 2) {
-            mx[0] = fmaxf(fmaxf(mx[0], __uint_as_float(s0[j])), __uint_as_float(s0[j + 1]));
-            mx[1] = fmaxf(fmaxf(mx[1], __uint_as_float(s1[j])), __uint_as_float(s1[j + 1]));
-            mx[2] = fmaxf(fmaxf(mx[2], __uint_as_float(s2[j])), __uint_as_float(s2[j + 1]));
-            mx[3] = fmaxf(fmaxf(mx[3], __uint_as_float(s3[j])), __uint_as_float(s3[j + 1]));
-          }
-          const float top = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2,
-                                  -1e30f);
-          if (i == 0) {
-            m = top;
-          } else if (__any_sync(0xffffffffu, top > m + kAtLazy)) {
-            // rescale this row's output; the tile before this one is in it
-            // (its product was issued before this tile's scores)
-            const float mn = fmaxf(m, top), f = ex2(m - mn);
-            m = mn;
-            l *= f;
-#pragma unroll 1
-            for (int c = 0; c < D; c += 16) {
-              uint32_t o[16];
-              const uint32_t at = lanes + 2 * kAtKeys + w * D + c;
-              tmem_ld16(at, o);
-#pragma unroll
-              for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-              tmem_st16(at, o);
-            }
-          }
-          // weights of 16 entries at a time, into 8 columns
-          const unsigned long long c2 = f2pack(p.scale_log2, p.scale_log2), nm2 = f2pack(-m, -m);
-          unsigned long long sum0 = 0, sum1 = 0;
-          auto weights = [&](const uint32_t (&a)[32], uint32_t at) {
-            uint32_t pk[16];
+            for (int j = 0; j < 32; ++j)
+              if (!((bits >> j) & 1)) a[j] = 0xFF800000u;
+          };
+          // weights of 32 entries, two to a word
+          auto weights = [&](const uint32_t (&a)[32], uint32_t (&pk)[16]) {
 #pragma unroll
             for (int j = 0; j < 16; j += 2) {
-              float x, y, z, u;
-              f2unpack(fma2(f2pack(__uint_as_float(a[2 * j]), __uint_as_float(a[2 * j + 1])), c2, nm2), x, y);
-              f2unpack(fma2(f2pack(__uint_as_float(a[2 * j + 2]), __uint_as_float(a[2 * j + 3])), c2, nm2), z, u);
-              x = ex2(x);
-              y = ex2(y);
-              z = ex2(z);
-              u = ex2(u);
-              sum0 = add2(sum0, f2pack(x, y));
-              sum1 = add2(sum1, f2pack(z, u));
-              pk[j] = pack_bf16(x, y);
-              pk[j + 1] = pack_bf16(z, u);
+              float e0, e1, e2, e3;
+              f2unpack(fma2(f2pack(__uint_as_float(a[2 * j]), __uint_as_float(a[2 * j + 1])), c2,
+                            nm2), e0, e1);
+              f2unpack(fma2(f2pack(__uint_as_float(a[2 * j + 2]), __uint_as_float(a[2 * j + 3])),
+                            c2, nm2), e2, e3);
+              e0 = ex2(e0);
+              e1 = ex2(e1);
+              e2 = ex2(e2);
+              e3 = ex2(e3);
+              sum0 = add2(sum0, f2pack(e0, e1));
+              sum1 = add2(sum1, f2pack(e2, e3));
+              pk[j] = pack_bf16(e0, e1);
+              pk[j + 1] = pack_bf16(e2, e3);
             }
-            tmem_st16(at, pk);
           };
-          weights(s0, sbase);
-          weights(s1, sbase + 16);
-          weights(s2, sbase + 32);
-          weights(s3, sbase + 48);
-          float a0, a1;
-          f2unpack(add2(sum0, sum1), a0, a1);
-          l += spoilt ? NAN : a0 + a1;
+          auto total = [&]() {
+            float x, y;
+            f2unpack(add2(sum0, sum1), x, y);
+            return x + y;
+          };
+          bool good = false;
+          if (i > 0) {
+            uint32_t sa[32], sb[32], p0[16], p1[16], p2[16], p3[16];
+            nm2 = f2pack(-m, -m);
+            sum0 = sum1 = 0;
+            tmem_ld32_async(sbase, sa);
+            tmem_wait_ld(sa);
+            tmem_ld32_async(sbase + 32, sb);
+            if (edge) hide(sa, see[0]);
+            weights(sa, p0);
+            tmem_wait_ld(sb);
+            tmem_ld32_async(sbase + 64, sa);
+            if (edge) hide(sb, see[1]);
+            weights(sb, p1);
+            tmem_wait_ld(sa);
+            tmem_ld32_async(sbase + 96, sb);
+            if (edge) hide(sa, see[2]);
+            weights(sa, p2);
+            tmem_wait_ld(sb);
+            if (edge) hide(sb, see[3]);
+            weights(sb, p3);
+            good = __all_sync(0xffffffffu, total() <= kAtLazy);
+            if (good) {
+              tmem_st16(sbase, p0);
+              tmem_st16(sbase + 16, p1);
+              tmem_st16(sbase + 32, p2);
+              tmem_st16(sbase + 48, p3);
+            }
+          }
+          if (!good) {
+            // the first tile, or a sum that shows the reference to be too old:
+            // the row's maximum first
+            float x = -INFINITY, y = -INFINITY;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              uint32_t a[32];
+              tmem_ld32(sbase + 32 * c, a);
+              if (edge) hide(a, c == 0 ? see[0] : c == 1 ? see[1] : c == 2 ? see[2] : see[3]);
+#pragma unroll
+              for (int j = 0; j < 32; j += 4) {
+                x = fmaxf(fmaxf(x, __uint_as_float(a[j])), __uint_as_float(a[j + 1]));
+                y = fmaxf(fmaxf(y, __uint_as_float(a[j + 2])), __uint_as_float(a[j + 3]));
+              }
+            }
+            const float mn = fmaxf(m, fmaxf(x, y) * p.scale_log2), f = ex2(m - mn);
+            m = mn;
+            l *= f;
+            if (i > 0) {  // the tile before this one is in the output: its product was
+                          // issued before this tile's scores
+#pragma unroll 1
+              for (int c = 0; c < D; c += 16) {
+                uint32_t o[16];
+                const uint32_t at = lanes + 2 * kAtKeys + w * D + c;
+                tmem_ld16(at, o);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                tmem_st16(at, o);
+              }
+            }
+            nm2 = f2pack(-m, -m);
+            sum0 = sum1 = 0;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {  // P of a chunk goes over scores already taken
+              uint32_t a[32], pk[16];
+              tmem_ld32(sbase + 32 * c, a);
+              if (edge) hide(a, c == 0 ? see[0] : c == 1 ? see[1] : c == 2 ? see[2] : see[3]);
+              weights(a, pk);
+              tmem_st16(sbase + 16 * c, pk);
+            }
+          }
+          l += spoilt ? NAN : total();
           tmem_wait_st();
         }
         tmem_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[w]);
       }
+      if (!ok) break;
       ring0 += 2 * seg.n;
       // the item's output, or its partial as [D / 4][slot_rows][4], so that a
       // warp's lanes (rows) store 512 consecutive bytes
-      if (nt > 0) wait(&o_full[w], no++ & 1);
-      const bool mine = r < nrows;
+      if (nt > 0 && !at_wait_warp(&o_full[w], no++ & 1, abort)) {
+        ok = false;
+        break;
+      }
+      tmem_fence_after();
+      const bool mine_row = r < nrows;
       float* slot = p.opart + seg.slot * (long long)p.slot_rows * D;
       const int row = (pair ? w * p.half_rows : 0) + r;
-      const size_t orow = ((size_t)max(seg.b, 0) * p.N + node) * p.Hq + seg.h * p.G + r % p.G;
-      auto put = [&](int c, const uint32_t (&o)[16], float norm) {
-        if (!mine) return;
+      const size_t orow = ((size_t)seg.b * p.N + node) * p.Hq + seg.h * p.G + rhead;
+      auto put = [&](int c, const uint32_t (&o)[32], float norm) {
+        if (!mine_row) return;
         if (seg.whole) {
-          uint32_t x[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            x[j] = pack_bf16(__uint_as_float(o[2 * j]) * norm, __uint_as_float(o[2 * j + 1]) * norm);
           uint4* dst = reinterpret_cast<uint4*>(p.out + orow * D + c);
-          dst[0] = make_uint4(x[0], x[1], x[2], x[3]);
-          dst[1] = make_uint4(x[4], x[5], x[6], x[7]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t x[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              x[e] = pack_bf16(__uint_as_float(o[8 * j + 2 * e]) * norm,
+                               __uint_as_float(o[8 * j + 2 * e + 1]) * norm);
+            dst[j] = make_uint4(x[0], x[1], x[2], x[3]);
+          }
         } else {
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
+          for (int j = 0; j < 8; ++j)
             *reinterpret_cast<uint4*>(slot + ((c / 4 + j) * p.slot_rows + row) * 4) =
                 make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
         }
       };
       auto put_ml = [&](float mm, float ll) {
-        if (!mine) return;
+        if (!mine_row) return;
         if (!seg.whole)
           p.ml[seg.slot * p.slot_rows + row] = make_float2(mm, ll);
         else if (p.lse)
           p.lse[orow] = attn_lse(mm, ll);
       };
+      const uint32_t obase = lanes + 2 * kAtKeys;
       if (pair) {
-        if (busy && !dead) {
+        if (busy) {
           const float norm = attn_norm(l);
-#pragma unroll 1
-          for (int c = 0; c < D; c += 16) {
-            uint32_t o[16];
-            tmem_ld16(lanes + 2 * kAtKeys + w * D + c, o);
-            put(c, o, norm);
-          }
           put_ml(m, l);
+#pragma unroll 1
+          for (int c = 0; c < D; c += 64) {
+            uint32_t o0[32], o1[32];
+            tmem_ld32_async(obase + w * D + c, o0);
+            tmem_ld32_async(obase + w * D + c + 32, o1);
+            tmem_wait_ld(o0);
+            tmem_wait_ld(o1);
+            put(c, o0, norm);
+            put(c + 32, o1, norm);
+          }
         }
         tmem_fence_before();
       } else {
         // join the two halves; each takes half of the columns
         s_ml[w][r] = make_float2(m, l);
-        asm volatile("bar.sync 1, 256;" ::: "memory");
+        if (!(ok = meet(&pair_bar, npair))) break;
         tmem_fence_after();
-        if (busy && !dead) {
+        if (busy) {
           const float2 a = s_ml[0][r], b = s_ml[1][r];  // half 0 has at least one tile
           const float mm = fmaxf(a.x, b.x);
           const float fa = ex2(a.x - mm), fb = ex2(b.x - mm);
           const float ll = seg.n > 1 ? a.y * fa + b.y * fb : a.y;
           const float norm = attn_norm(ll);
+          if (w == 0) put_ml(mm, ll);
 #pragma unroll 1
-          for (int c = w * (D / 2); c < (w + 1) * (D / 2); c += 16) {
-            uint32_t o[16];
-            tmem_ld16(lanes + 2 * kAtKeys + c, o);
+          for (int c = w * (D / 2); c < (w + 1) * (D / 2); c += 32) {
+            uint32_t o[32], o1[32];
+            tmem_ld32_async(obase + c, o);
+            if (seg.n > 1) tmem_ld32_async(obase + D + c, o1);
+            tmem_wait_ld(o);
             if (seg.n > 1) {
-              uint32_t o1[16];
-              tmem_ld16(lanes + 2 * kAtKeys + D + c, o1);
+              tmem_wait_ld(o1);
 #pragma unroll
-              for (int j = 0; j < 16; ++j)
+              for (int j = 0; j < 32; ++j)
                 o[j] = __float_as_uint(
                     __fmaf_rn(__uint_as_float(o1[j]), fb, __uint_as_float(o[j]) * fa));
             }
             put(c, o, norm);
           }
-          if (w == 0) put_ml(mm, ll);
         }
         // neither half's accumulators are written again before both are read
         tmem_fence_before();
-        asm volatile("bar.sync 1, 256;" ::: "memory");
+        ok = meet(&pair_bar, npair);
       }
     }
+    if (!ok) fail();
   }
+  __syncwarp();
   tmem_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -757,109 +884,75 @@ __global__ void __launch_bounds__(kAtThreads, 1)
 }
 
 // Joins the partials of items that several CTAs share or that have a shared
-// prefix; other rows are done.  One warp per (node, key-value head),
-// kAtFinHeads query heads at a time, a lane holding D / 32 elements of a head.
+// prefix; other rows are done.  A thread takes 16 elements of a row (a node's
+// query head), neighbouring lanes neighbouring rows of a key-value head, as
+// the partials lie.
 template <int D>
 __global__ void __launch_bounds__(kAtFinThreads) tree_attn_finish_kernel(const AttnParams p) {
-  constexpr int kE = D / 32;  // elements per lane
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long item = (long long)blockIdx.x * (kAtFinThreads / 32) + warp;
-  if (item >= (long long)p.B * p.N * p.Hkv) return;
-  const int h = (int)(item % p.Hkv);
-  const long long node = item / p.Hkv;
-  const int b = (int)(node / p.N), n = (int)(node - (long long)b * p.N);
+  const unsigned rows = (unsigned)p.B * p.N * p.Hq;  // at most 2^31
+  const unsigned blocks = (rows + kAtFinThreads - 1) / kAtFinThreads;
+  const unsigned part = blockIdx.x / blocks;  // 16 elements: part < D / 16
+  const unsigned at = (blockIdx.x - part * blocks) * kAtFinThreads + threadIdx.x;
+  if (at >= rows) return;
+  // row = ((b Hkv + h) N + n) G + g
+  const unsigned ng = (unsigned)p.N * p.G, bh = at / ng, in_bh = at - bh * ng;
+  const int n = (int)(in_bh / p.G), g = (int)(in_bh - (unsigned)n * p.G);
+  const int b = (int)(bh / p.Hkv), h = (int)(bh - (unsigned)b * p.Hkv);
   const bool ok = attn_seq_ok(p, __ldg(p.base_len + b));
-  if (!ok && n == 0 && h == 0 && lane == 0) set_flag(p.flags, kFlagBadPath);
-  // per class (shared prefix, own entries): the partials' first slot, the run
-  // of CTAs, and the row in the slot
-  long long it[2], total = 1;
-  int c0[2] = {0, 0}, c1[2] = {0, 0}, row[2];
+  float m = -1e30f, l = 0.0f, acc[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) acc[e] = 0.0f;
   if (ok) {
-    const long long items_s = (long long)p.Hkv * p.mg_s, per = (long long)p.Hkv * p.mg_o;
-    const long long shared = items_s * p.tiles_s;
-    total = shared + p.tstart[p.B] * per;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const long long tiles = k == 0 ? p.tiles_s : p.tstart[b + 1] - p.tstart[b];
-      if (tiles == 0) continue;
+#pragma unroll 1
+    for (int k = p.tiles_s == 0 ? 1 : 0; k < 2; ++k) {  // shared prefix, own entries
       const int cap = p.tok << (k == 0 ? p.pair_s : p.pair_o);
-      const int tokn = k == 0 ? (int)node : n;
-      const int mg = tokn / cap, in = tokn - mg * cap;
-      const int half = in / p.tok;
-      const int index = mg * p.Hkv + h;
-      row[k] = half * p.half_rows + (in - half * p.tok) * p.G;
-      it[k] = k == 0 ? index : items_s + (long long)b * per + index;
-      const long long s0 = k == 0 ? index * tiles
-                                  : shared + p.tstart[b] * per + (long long)index * tiles;
-      // the CTAs whose runs [c T / n, (c+1) T / n) meet the item's tiles
-      int c = (int)(s0 * p.nctas / total);
-      while (total * (c + 1) / p.nctas <= s0) ++c;
-      c0[k] = c;
-      while (c < p.nctas && total * c / p.nctas < s0 + tiles) ++c;
-      c1[k] = c;
-    }
-    if (p.tiles_s == 0 && c1[1] - c0[1] == 1) return;  // written by its only CTA
-  }
-  for (int g0 = 0; g0 < p.G; g0 += kAtFinHeads) {
-    const int ng = min(kAtFinHeads, p.G - g0);
-    float acc[kAtFinHeads][kE], m[kAtFinHeads], l[kAtFinHeads];
+      const int node = k == 0 ? b * p.N + n : n;
+      const int mg = node / cap, in = node - mg * cap, half = in / p.tok;
+      const int row = half * p.half_rows + (in - half * p.tok) * p.G + g;
+      const long long it = k == 0 ? mg * p.Hkv + h
+                                  : (long long)p.Hkv * p.mg_s +
+                                        ((long long)b * p.mg_o + mg) * p.Hkv + h;
+      const int2 span = p.span[it];
+      if (p.tiles_s == 0 && span.x == span.y) return;  // written by its only CTA
+#pragma unroll 2
+      for (int c = span.x; c <= span.y; ++c) {
+        const long long slot = it + c;
+        const float2 x = p.ml[slot * p.slot_rows + row];
+        const float4* o = reinterpret_cast<const float4*>(p.opart + slot * (long long)p.slot_rows * D) +
+                          part * 4 * p.slot_rows + row;
+        float4 y[4];
 #pragma unroll
-    for (int g = 0; g < kAtFinHeads; ++g) {
-      m[g] = -1e30f;
-      l[g] = 0.0f;
+        for (int j = 0; j < 4; ++j) y[j] = o[j * p.slot_rows];
+        const float mn = fmaxf(m, x.x);
+        const float fa = ex2(m - mn), fb = ex2(x.x - mn);
+        m = mn;
+        l = l * fa + x.y * fb;
 #pragma unroll
-      for (int e = 0; e < kE; ++e) acc[g][e] = 0.0f;
-    }
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      for (int c = c0[k]; c < c1[k]; ++c) {
-        if (total * c / p.nctas == total * (c + 1) / p.nctas) continue;  // an empty run
-        const long long slot = it[k] + c;
-        const float* part = p.opart + slot * (long long)p.slot_rows * D;
-        const float2* ml = p.ml + slot * p.slot_rows + row[k] + g0;
-#pragma unroll
-        for (int g = 0; g < kAtFinHeads; ++g) {
-          if (g < ng) {
-            const float2 x = ml[g];
-            float o[kE];
-            if constexpr (kE == 4) {
-              const float4 y = *reinterpret_cast<const float4*>(
-                  part + ((size_t)lane * p.slot_rows + row[k] + g0 + g) * 4);
-              o[0] = y.x; o[1] = y.y; o[2] = y.z; o[3] = y.w;
-            } else {
-              const float2 y = *reinterpret_cast<const float2*>(
-                  part + ((size_t)(lane >> 1) * p.slot_rows + row[k] + g0 + g) * 4 + (lane & 1) * 2);
-              o[0] = y.x; o[1] = y.y;
-            }
-            const float mn = fmaxf(m[g], x.x);
-            const float fa = ex2(m[g] - mn), fb = ex2(x.x - mn);
-            m[g] = mn;
-            l[g] = l[g] * fa + x.y * fb;
-#pragma unroll
-            for (int e = 0; e < kE; ++e) acc[g][e] = acc[g][e] * fa + o[e] * fb;
-          }
+        for (int j = 0; j < 4; ++j) {
+          acc[4 * j] = acc[4 * j] * fa + y[j].x * fb;
+          acc[4 * j + 1] = acc[4 * j + 1] * fa + y[j].y * fb;
+          acc[4 * j + 2] = acc[4 * j + 2] * fa + y[j].z * fb;
+          acc[4 * j + 3] = acc[4 * j + 3] * fa + y[j].w * fb;
         }
       }
     }
-#pragma unroll
-    for (int g = 0; g < kAtFinHeads; ++g) {
-      if (g < ng) {
-        const float rl = attn_norm(l[g]);
-        const size_t at = (size_t)node * p.Hq + h * p.G + g0 + g;
-        if constexpr (kE == 4) {
-          *reinterpret_cast<uint2*>(p.out + at * D + lane * 4) =
-              make_uint2(pack_bf16(acc[g][0] * rl, acc[g][1] * rl),
-                         pack_bf16(acc[g][2] * rl, acc[g][3] * rl));
-        } else {
-          *reinterpret_cast<uint32_t*>(p.out + at * D + lane * 2) =
-              pack_bf16(acc[g][0] * rl, acc[g][1] * rl);
-        }
-        if (p.lse && lane == 0) p.lse[at] = attn_lse(m[g], l[g]);
-      }
-    }
+  } else if (n == 0 && h == 0 && g == 0 && part == 0) {
+    set_flag(p.flags, kFlagBadPath);
   }
+  const float norm = attn_norm(l);
+  const size_t orow = ((size_t)b * p.N + n) * p.Hq + h * p.G + g;
+  uint4* out = reinterpret_cast<uint4*>(p.out + orow * D + part * 16);
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    uint32_t x[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      x[e] = pack_bf16(acc[8 * j + 2 * e] * norm, acc[8 * j + 2 * e + 1] * norm);
+    out[j] = make_uint4(x[0], x[1], x[2], x[3]);
+  }
+  if (p.lse && part == 0) p.lse[orow] = attn_lse(m, l);
 }
 
 }  // namespace sv
