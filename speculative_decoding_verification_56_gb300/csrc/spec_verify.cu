@@ -1177,6 +1177,7 @@ spec_status_t spec_tree_attention(const void* q, const void* k_cache, const void
   prm.half_rows = plan.half_rows;
   prm.slot_rows = plan.slot_rows;
   prm.nctas = std::min(sms, sv::kAtMaxCtas);
+  prm.q_tiles = 1 + std::max(plan.pair_s, plan.pair_o);
   prm.span = reinterpret_cast<int2*>(ws + kDataOffset);
   prm.ml = reinterpret_cast<float2*>(ws + plan.off_ml);
   prm.opart = reinterpret_cast<float*>(ws + plan.off_part);

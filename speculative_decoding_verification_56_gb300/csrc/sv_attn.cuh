@@ -31,7 +31,7 @@ namespace sv {
 constexpr int kAtRows = 128;     // rows of a half (UMMA M, tensor-memory lanes)
 constexpr int kAtKeys = 128;     // cache entries per tile
 constexpr int kAtThreads = 384;  // producer, MMA issuer, 2 idle warps, 2 x 4 softmax warps
-constexpr int kAtMaxStages = 8;
+constexpr int kAtMaxStages = 13;
 constexpr int kAtMaxCtas = 160;  // partial slots are laid out for at most this many CTAs
 constexpr float kAtLazy = 4096.0f;  // a tile's largest sum of a row's weights before its
                                     // reference is renewed
@@ -40,11 +40,12 @@ constexpr int kAtSegs = 4;       // segment descriptors ahead of their use
 
 template <int D>
 __host__ __device__ constexpr int at_tile_bytes() { return kAtKeys * D * 2; }
-// K and V tiles in flight beside the two query tiles, in 195 KB
+// Query tiles (one, or two where items are pairs) and as many K and V tiles as
+// fit beside them: with the static arrays, all of an SM's 227 KB.
 template <int D>
-__host__ __device__ constexpr int at_stages() { return D == 128 ? 4 : 8; }
+__host__ __device__ constexpr int at_tiles() { return D == 128 ? 7 : 14; }
 template <int D>
-__host__ __device__ constexpr int at_smem() { return (2 + at_stages<D>()) * at_tile_bytes<D>() + 1024; }
+__host__ __device__ constexpr int at_smem() { return at_tiles<D>() * at_tile_bytes<D>(); }
 
 struct AttnParams {
   const uint16_t* q;        // [B, N, Hq, D]
@@ -66,6 +67,7 @@ struct AttnParams {
   int half_rows;            // rows stored per half
   int slot_rows;            // rows stored per slot
   int nctas;
+  int q_tiles;              // 2 if any item is a pair
   float* opart;             // [slot][D / 4][slot_rows][4]
   float2* ml;               // [slot][slot_rows]: reference (log2) and sum
   int2* span;               // [items]: first and last CTA that holds a part of the item
@@ -260,10 +262,10 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                      const __grid_constant__ CUtensorMap map_pk,
                      const __grid_constant__ CUtensorMap map_pv, const AttnParams p) {
   constexpr int kTile = at_tile_bytes<D>();
-  constexpr int S = at_stages<D>();
   constexpr int kSub = D / 64;  // 64-element column blocks of a tile (128 rows x 128 bytes)
   constexpr int kWarps = kAtThreads / 32;
-  extern __shared__ uint8_t at_raw[];
+  extern __shared__ __align__(1024) uint8_t smem[];
+  static_assert(at_tiles<D>() - 1 <= kAtMaxStages, "ring barriers");
   __shared__ uint64_t full[kAtMaxStages], empty[kAtMaxStages];
   __shared__ uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], drain;
   __shared__ uint64_t seg_full[kAtSegs], seg_empty[kAtSegs], half_bar[2], pair_bar;
@@ -274,10 +276,13 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   __shared__ float2 s_ml[2][kAtRows];
   __shared__ uint32_t s_bad[2][2][4];  // tree entries of a tile whose V is not finite: by
                                        // turns, half
-  uint8_t* smem = reinterpret_cast<uint8_t*>(
-      (reinterpret_cast<uintptr_t>(at_raw) + 1023) & ~(uintptr_t)1023);
-  uint8_t* ring = smem + 2 * kTile;
+  uint8_t* ring = smem + p.q_tiles * kTile;
+  const int S = at_tiles<D>() - p.q_tiles;  // ring stages
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (smem_addr(smem) & 1023) {  // swizzled tiles start at 1024-byte boundaries; never expected
+    if (threadIdx.x == 0) set_flag(p.flags, kFlagTimeout);
+    return;
+  }
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(&full[s], 1);
@@ -725,7 +730,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             tmem_wait_ld(sb);
             if (edge) hide(sb, see[3]);
             weights(sb, p3);
-            good = __all_sync(0xffffffffu, total() <= kAtLazy);
+            good = __all_sync(0xffffffffu, total() <= kAtLazy || r >= nrows);
             if (good) {
               tmem_st16(sbase, p0);
               tmem_st16(sbase + 16, p1);
