@@ -504,7 +504,6 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           if (!wait(&full[stage], phase)) break;
           scores(0, 0);
           scores(1, 1);
-          umma_commit(&empty[stage]);
           if (n == 1) umma_commit(&q_empty);
           advance();
           for (int t = 0; t < n; ++t) {
@@ -521,10 +520,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
               umma_commit(&o_full[0]);
             if (!wait(&p_full[1], np1++)) break;
             output(1, vst, t == 0);
-            umma_commit(&empty[vst]);
             if (more) {
               scores(1, 1);
-              umma_commit(&empty[stage]);
               if (t + 2 == n) umma_commit(&q_empty);
               advance();
             } else {
@@ -535,7 +532,6 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           for (int t = 0; t < min(2, n); ++t) {
             if (!wait(&full[stage], phase)) break;
             scores(t, 0);
-            umma_commit(&empty[stage]);
             if (t + 1 == n) umma_commit(&q_empty);
             advance();
           }
@@ -547,10 +543,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             if (more && !wait(&full[stage], phase)) break;
             if (!wait(&p_full[w], w ? np1++ : np0++)) break;
             output(w, vst, t < 2);
-            umma_commit(&empty[vst]);
             if (more) {
               scores(w, 0);
-              umma_commit(&empty[stage]);
               if (t + 3 == n) umma_commit(&q_empty);
               advance();
             } else {
@@ -573,7 +567,20 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
     const uint32_t sbase = lanes + w * kAtKeys;
     unsigned ns = 0, no = 0, nh = 0, npair = 0;  // uses of the barriers so far
-    long long ring0 = 0;                         // ring uses before this segment
+    unsigned ring0 = 0;                          // ring uses before this segment
+    // Ring uses of a segment, in the order of the copies: K tile t and V tile t
+    // (pair: K0 V0 K1 V1 ..; else K0 K1 V0 K2 V1 K3 ..).
+    auto k_use = [&](int pair, int t) { return pair ? 2 * t : t < 2 ? t : 2 * t - 1; };
+    auto v_use = [&](int pair, int t, int n) { return min(n, t + 2 - pair) + t; };
+    // A half whose scores or outputs are complete frees the tiles that made
+    // them (of a pair, half 1, whose products come last).
+    auto slot_of = [&](int use) {
+      const unsigned u = ring0 + use;
+      return p.q_tiles == 2 ? u % (at_tiles<D>() - 2) : u % (at_tiles<D>() - 1);
+    };
+    auto release = [&](int use) {
+      if (quad == 0 && lane == 0) mbar_arrive(&empty[slot_of(use)]);
+    };
     // all warps of a half, or of both halves, meet
     auto meet = [&](uint64_t* bar, unsigned& uses) {
       __syncwarp();
@@ -631,15 +638,19 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           break;
         }
         tmem_fence_after();
+        if (!pair || w == 1) {
+          release(k_use(pair, t));
+          if (i > 0) release(v_use(pair, t - (2 - pair), seg.n));
+        }
         bool spoilt = false;
         if (edge) {
           // V entries beyond the last are zeroed, whatever they hold: their
           // products with weights of 0 have to be 0.  So are tree entries that
           // are not finite, and the rows that see them become NaN.
           if (!pair || w == 0) {
-            const long long u = ring0 + min(seg.n, t + 2 - pair) + t;  // V tile's ring use
-            const int st = (int)(u % S);
-            if (!at_wait_warp(&full[st], (unsigned)((u / S) & 1), abort)) {
+            const int use = v_use(pair, t, seg.n);
+            const int st = slot_of(use);
+            if (!at_wait_warp(&full[st], ((ring0 + use) / S) & 1, abort)) {
               ok = false;
               break;
             }
@@ -787,7 +798,6 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         if (lane == 0) mbar_arrive(&p_full[w]);
       }
       if (!ok) break;
-      ring0 += 2 * seg.n;
       // the item's output, or its partial as [D / 4][slot_rows][4], so that a
       // warp's lanes (rows) store 512 consecutive bytes
       if (nt > 0 && !at_wait_warp(&o_full[w], no++ & 1, abort)) {
@@ -795,6 +805,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         break;
       }
       tmem_fence_after();
+      if (nt > 0 && (!pair || w == 1)) release(v_use(pair, pair ? nt - 1 : 2 * (nt - 1) + w, seg.n));
+      ring0 += 2 * seg.n;
       const bool mine_row = r < nrows;
       float* slot = p.opart + seg.slot * (long long)p.slot_rows * D;
       const int row = (pair ? w * p.half_rows : 0) + r;
