@@ -68,6 +68,7 @@ SPEC_FLAG_EMPTY_ROW = 64
 
 _lock = threading.Lock()
 _lib = None
+_torch_module = None
 
 
 class SpecVerifyError(RuntimeError):
@@ -79,6 +80,8 @@ class SpecVerifyError(RuntimeError):
 def load_library(path: str = LIB_PATH):
     """Load the compiled C-ABI library (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -141,8 +144,11 @@ def load_library(path: str = LIB_PATH):
 # ---------------------------------------------------------------------------
 
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _dtype_code(t) -> int:
@@ -172,25 +178,25 @@ def _dev(t, name, dtype=None, optional=False):
 def _arg(t, name, dtype, shape, device):
     """Pointer of a contiguous CUDA tensor of the given type and shape on the
     call's device."""
-    if t.dtype != dtype:
+    if (t.dtype is dtype and t.shape == shape and t.get_device() == device
+            and t.is_contiguous()):
+        return t.data_ptr()
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     if t.get_device() != device:
         raise ValueError(f"{name} must be on cuda:{device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _call_device(t, name):
     """Index of the CUDA device that a call runs on: its tensors' device, which
     has to be the current one."""
-    torch = _torch()
     dev = t.get_device()
     if dev < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if dev != torch.cuda.current_device():
+    if dev != _torch().cuda.current_device():
         raise ValueError(f"{name} is on cuda:{dev}, which is not the current device")
     return dev
 
@@ -198,21 +204,37 @@ def _call_device(t, name):
 def _cache_args(k_cache, v_cache, Hkv, D, B, device):
     """Pointers, byte stride between sequences and positions of a layer's key
     and value cache [B, L, Hkv, D] (sequences may lie further apart)."""
-    torch = _torch()
-    L = k_cache.shape[1] if k_cache.dim() == 4 else 0
-    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if t.dtype != torch.bfloat16:
-            raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
-        if t.shape != (B, L, Hkv, D):
-            raise ValueError(f"{name} must be [{B}, L, {Hkv}, {D}], got {list(t.shape)}")
-        if t.get_device() != device:
-            raise ValueError(f"{name} must be on cuda:{device}")
-        if t.stride()[1:] != (Hkv * D, D, 1) and t.numel() > 0:
-            raise ValueError(f"{name}: the positions of a sequence must be contiguous")
-    s = max(k_cache.stride(0), L * Hkv * D) if B <= 1 else k_cache.stride(0)
-    if B > 1 and v_cache.stride(0) != s:
-        raise ValueError("k_cache and v_cache must have the same strides")
-    return k_cache.data_ptr(), v_cache.data_ptr(), s * 2, L
+    bf16 = _torch().bfloat16
+    shape, stride = k_cache.shape, k_cache.stride()
+    if not (k_cache.dtype is bf16 and v_cache.dtype is bf16 and len(shape) == 4
+            and shape[0] == B and shape[2] == Hkv and shape[3] == D and v_cache.shape == shape
+            and k_cache.get_device() == device and v_cache.get_device() == device
+            and stride[1:] == (Hkv * D, D, 1) and v_cache.stride() == stride):
+        for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+            if t.dtype is not bf16:
+                raise TypeError(f"{name} must be {bf16}, got {t.dtype}")
+            if t.get_device() != device:
+                raise ValueError(f"{name} must be on cuda:{device}")
+            if t.dim() != 4 or t.shape != (B, shape[1], Hkv, D):
+                raise ValueError(f"{name} must be [{B}, L, {Hkv}, {D}], got {list(t.shape)}")
+        raise ValueError("k_cache and v_cache must have the same strides, with the positions of "
+                         "a sequence contiguous")
+    L = shape[1]
+    step = stride[0] if B > 1 else max(stride[0], L * Hkv * D)
+    return k_cache.data_ptr(), v_cache.data_ptr(), 2 * step, L
+
+
+def _workspace(t, device):
+    if t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{device}")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def _stream_of(stream, device):
+    """_stream_ptr for a call on a known device (the current one)."""
+    if stream is not None:
+        return _stream_ptr(stream)
+    return _torch()._C._cuda_getCurrentRawStream(device)
 
 
 def _stream_ptr(stream):
@@ -463,8 +485,8 @@ def spec_verify_tree_sample(target_logits, node_tokens, parents, u_sample, tempe
         float(temperature), B, N, V, W - 1, _arg(accepted_len, "accepted_len", i32, (B,), dev),
         _arg(path_nodes, "path_nodes", i32, (B, W), dev),
         _arg(out_tokens, "out_tokens", i32, (B, W), dev),
-        _arg(out_probs, "out_probs", f32, (B, W), dev), _dev(workspace, "workspace"),
-        workspace.numel() * workspace.element_size(), _stream_ptr(stream))
+        _arg(out_probs, "out_probs", f32, (B, W), dev), *_workspace(workspace, dev),
+        _stream_of(stream, dev))
     _check(st, "spec_verify_tree_sample")
 
 
@@ -494,8 +516,7 @@ def spec_tree_qkv_rope(qkv, q_norm, k_norm, eps, inv_freq, base_len, depth, q_ou
         _arg(base_len, "base_len", torch.int32, (B,), dev),
         None if depth is None else _arg(depth, "depth", torch.int32, (B, N), dev), B, N, Hq, Hkv,
         D, L, stride, _arg(q_out, "q_out", bf16, (B, N, Hq, D), dev), kp, vp,
-        _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(),
-        _stream_ptr(stream))
+        *_workspace(workspace, dev), _stream_of(stream, dev))
     _check(st, "spec_tree_qkv_rope")
 
 
@@ -530,8 +551,7 @@ def spec_tree_attention(q, k_cache, v_cache, mask, base_len, scale, out, lse, wo
         _arg(base_len, "base_len", torch.int32, (B,), dev), B, N, Hq, Hkv, D, float(scale),
         _arg(out, "out", bf16, (B, N, Hq, D), dev),
         None if lse is None else _arg(lse, "lse", torch.float32, (B, N, Hq), dev),
-        _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(),
-        _stream_ptr(stream))
+        *_workspace(workspace, dev), _stream_of(stream, dev))
     _check(st, "spec_tree_attention")
 
 
