@@ -517,7 +517,8 @@ spec_status_t noalloc_scratch(void** addr) {
   return SPEC_OK;
 }
 
-constexpr size_t kTsMaxSmem = 192 * 1024;
+constexpr int kTsMaxSteps = 1024;  // of a warp, whose sums are held in shared memory
+constexpr size_t kTsMaxSmem = (size_t)sv::kTsWarps * kTsMaxSteps * sizeof(unsigned long long);
 
 // Tree sampling: a cluster of CTAs per sequence (16 are more than the portable
 // 8); the dynamic shared memory holds the sums of the warps' steps.
@@ -1053,8 +1054,14 @@ spec_status_t spec_verify_tree_sample(const void* target_logits, int dtype,
   prm.probs = out_probs;
   prm.flags = reinterpret_cast<unsigned*>(workspace);
   constexpr int kCtaStep = sv::kTsWarps * sv::kTsStep;  // elements of a CTA's step
+  int most = 1;  // CTAs per sequence
+  while (most < sv::kTsMaxCluster && 2 * most * B <= 304) most *= 2;
+#ifdef TS_CLUSTER
+  most = TS_CLUSTER;
+#endif
   int cluster = 1;
-  while (cluster < (V > (1 << 20) ? 16 : 8) && cluster * kCtaStep < V) cluster *= 2;
+  while (cluster < most && cluster * kCtaStep < V) cluster *= 2;
+  while ((long long)cluster * kCtaStep * kTsMaxSteps < V) cluster *= 2;
   prm.nsteps = (V + cluster * kCtaStep - 1) / (cluster * kCtaStep);
   const size_t smem = (size_t)sv::kTsWarps * prm.nsteps * sizeof(unsigned long long);
   // 16-byte loads: whole groups of 8 elements at 16-byte boundaries

@@ -19,11 +19,20 @@
 // up their sums, once to learn the token.
 //
 // A token must fall on the right side of every border C_j, also of the
-// hundred thousand unlikely ones, so sums are exact: weights are fixed-point
-// 64-bit integers (2^-45 of the largest, from a double-float evaluation of
-// 2^x), whose sums depend on no order.  Each CTA scales by its own largest
-// logit, rounded up to a power of two, so that one pass needs no exchange of
-// maxima and the sums of two CTAs are brought together by shifts.
+// hundred thousand unlikely ones, which no float32 sum can promise.  So a step
+// first screens the row in float32, in one pass: every 256 elements are summed
+// as 2^(z_j c - ref) with a power of two near their largest as the reference,
+// those sums are brought together as fixed-point integers, and the token of
+// t = u R is taken if t is further than R / 2^17 from both of its borders.  The
+// error of such sums is bounded: 2^-22.4 of a weight from ex2.approx, 1.5 |r|
+// 2^-24 ln 2 from its argument r (its rounding and that of c), where the mean
+// of |r| over the row's mass is at most log2(V) + 1, and 13 float additions:
+// together below 2.7e-6 R for V = 2^26, of t and of a border.  Otherwise (a
+// draw among tokens of probability below 1e-5, for the most part) the row is
+// summed again exactly: weights as fixed-point 64-bit integers (2^-45 of the
+// largest, from a double-float evaluation of 2^x), whose sums depend on no
+// order.  No float64 arithmetic is on the way: it runs at two operations per
+// clock and SM here, and the sums of 16 CTAs alone took 16 us of a step.
 #pragma once
 
 #include "sv_lmhead.cuh"
@@ -53,10 +62,19 @@ struct TreeSampleParams {
   unsigned* flags;
 };
 
-// z * log2(e) / T as a double-float.
-__device__ __forceinline__ void ts_exponent(const TreeSampleParams& p, float z, float* hi, float* lo) {
-  *hi = __fmul_rn(z, p.c_hi);
-  *lo = __fmaf_rn(z, p.c_lo, __fmaf_rn(z, p.c_hi, -*hi));
+// z * log2(e) / T - ref as a normalised double-float: the product's two parts,
+// the difference to the reference with its rounding error (two-sum), and a
+// renormalisation, so that large logits lose nothing to their common size.
+__device__ __forceinline__ void ts_exponent(const TreeSampleParams& p, float z, float ref,
+                                            float* hi, float* lo) {
+  const float y = __fmul_rn(z, p.c_hi);
+  const float y_lo = __fmaf_rn(z, p.c_lo, __fmaf_rn(z, p.c_hi, -y));
+  const float d = __fsub_rn(y, ref);
+  const float t = __fsub_rn(d, y);  // two-sum of y and -ref
+  const float err = __fsub_rn(__fsub_rn(y, __fsub_rn(d, t)), __fadd_rn(ref, t));
+  const float l = __fadd_rn(err, y_lo);
+  *hi = __fadd_rn(d, l);
+  *lo = __fsub_rn(l, __fsub_rn(*hi, d));
 }
 
 // Mantissa of 2^(y_hi + y_lo) in fixed point (2^45 stands for 1) and its
@@ -98,11 +116,11 @@ __device__ __forceinline__ long long ts_mantissa(float y_hi, float y_lo, const l
 __device__ __forceinline__ unsigned long long ts_weight(const TreeSampleParams& p, float z, int ref,
                                                         const long long* tab_i, const float2* tab_f) {
   float hi, lo;
-  ts_exponent(p, z, &hi, &lo);
-  if (!(hi > (float)(ref - kTsFrac - 3))) return 0;  // too small, -inf or NaN
+  ts_exponent(p, z, (float)ref, &hi, &lo);
+  if (!(hi > -(float)(kTsFrac + 3))) return 0;  // too small, -inf or NaN
   int n;
   const long long m = ts_mantissa(hi, lo, tab_i, tab_f, &n);
-  const int sh = ref - n + p.extra;
+  const int sh = p.extra - n;
   if (sh <= 0) return (unsigned long long)m;
   return ((unsigned long long)m + (1ull << (sh - 1))) >> sh;
 }
@@ -158,23 +176,53 @@ __device__ __forceinline__ void ts_load(const typename E::storage* row, long lon
   }
 }
 
-struct TsPart {  // a CTA's part of a row, as every CTA of the cluster holds it
-  unsigned long long sum;
+// A CTA's part of a row, as every CTA of the cluster holds it.
+struct TsPart {
+  unsigned long long sum;  // of fixed-point weights relative to 2^ref
   int ref;
   int pad;
 };
 
+__device__ __forceinline__ void cluster_st64(uint32_t at, unsigned long long x) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(at), "l"(x) : "memory");
+}
+__device__ __forceinline__ void cluster_st32(uint32_t at, uint32_t x) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(x) : "memory");
+}
+
+constexpr int kTsScreenShift = 17;  // draws nearer than R / 2^17 to a border are decided exactly
+constexpr int kTsScreenFrac = 36;   // fraction bits of the screen's sums
+constexpr int kTsTreeSmem = 1024;   // trees of up to so many nodes are held in shared memory
+constexpr int kTsNone = -1, kTsUnclear = -2;
+constexpr int kTsRefBad = 1 << 30;  // of a sum that is not finite
+
+__device__ __forceinline__ unsigned long long ts_shift(unsigned long long x, int sh) {
+  return sh < 64 ? x >> sh : 0ull;
+}
+
+// The first lane whose inclusive sum of x exceeds t (-1: none); t becomes the
+// rest inside that lane.  Every lane gets the answer.
+__device__ __forceinline__ int ts_pick(unsigned long long x, unsigned long long* t) {
+  const unsigned long long incl = warp_scan_u64(x);
+  const unsigned past = __ballot_sync(0xffffffffu, *t < incl);
+  if (past == 0) return -1;
+  const int at = __ffs(past) - 1;
+  *t -= __shfl_sync(0xffffffffu, incl - x, at);
+  return at;
+}
+
 template <typename E, bool kVec>
-__global__ void __launch_bounds__(kTsThreads) tree_sample_kernel(const TreeSampleParams p) {
+__global__ void __launch_bounds__(kTsThreads, 2) tree_sample_kernel(const TreeSampleParams p) {
   extern __shared__ unsigned long long ts_steps[];  // [kTsWarps][nsteps]: sums of the steps
   __shared__ long long tab_i[64];
   __shared__ float2 tab_f[64];
-  __shared__ TsPart s_part[2][kTsMaxCluster];
+  __shared__ TsPart s_part[2][kTsMaxCluster];  // the cluster's, by turns
+  __shared__ TsPart s_warp[kTsWarps];
   __shared__ int s_tok[2];
   __shared__ float s_prob[2];
-  __shared__ float s_max[kTsWarps];
-  __shared__ unsigned long long s_wsum[kTsWarps];
+  __shared__ int s_max[kTsWarps];
   __shared__ int s_child;
+  __shared__ int2 s_tree[kTsTreeSmem];  // parent, token
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint32_t C;
   asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(C));
@@ -192,92 +240,200 @@ __global__ void __launch_bounds__(kTsThreads) tree_sample_kernel(const TreeSampl
   const int32_t* par = p.parents + (size_t)b * p.N;
   const int32_t* tok = p.tokens + (size_t)b * p.N;
   const int W = p.max_depth + 1;
-  if (rank == 0) {
+  const bool held = p.N <= kTsTreeSmem;
+  if (held || rank == 0) {
     unsigned bad = 0;
     for (int v = threadIdx.x; v < p.N; v += kTsThreads) {
+      const int pa = par[v], to = tok[v];
       if (v > 0) {
-        if (par[v] < 0 || par[v] >= v) bad |= kFlagBadParent;
-        if (tok[v] < 0 || tok[v] >= p.V) bad |= kFlagTokenRange;
+        if (pa < 0 || pa >= v) bad |= kFlagBadParent;
+        if (to < 0 || to >= p.V) bad |= kFlagTokenRange;
       }
+      if (held) s_tree[v] = make_int2(pa, to);
     }
-    if (bad) set_flag(p.flags, bad);
+    if (bad && rank == 0) set_flag(p.flags, bad);
   }
-  __syncthreads();
   const long long span = (long long)p.nsteps * kTsStep;  // elements of a warp
   const long long w0 = ((long long)rank * kTsWarps + warp) * span + lane * 8;
   unsigned long long* steps = ts_steps + (size_t)warp * p.nsteps;
-  int cur = 0, d = 0;
-  for (;; ++d) {
-    const int par_ = d & 1;
-    const typename E::storage* row =
-        static_cast<const typename E::storage*>(p.logits) + ((size_t)b * p.N + cur) * (size_t)p.V;
-    // the CTA's largest logit: the power of two its weights are relative to
-    float m = -INFINITY;
-    for (int s = 0; s < p.nsteps; ++s) {
-      float z[8];
-      ts_load<E, kVec>(row, w0 + (long long)s * kTsStep, p.V, z);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) m = fmaxf(m, z[e]);
-    }
-    m = warp_max_f(m);
-    if (lane == 0) s_max[warp] = m;
-    if (threadIdx.x == 0) s_child = 0x7FFFFFFF;
-    __syncthreads();
-    m = s_max[lane & (kTsWarps - 1)];
-    m = warp_max_f(m);
-    const int ref = exp_ref(m, p.c_hi);
-    // sums of the weights
-    unsigned long long sum = 0;
-    for (int s = 0; s < p.nsteps; ++s) {
-      float z[8];
-      ts_load<E, kVec>(row, w0 + (long long)s * kTsStep, p.V, z);
-      unsigned long long part = 0;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) part += ts_weight(p, z[e], ref, tab_i, tab_f);
-      part = warp_sum_u64(part);
-      if (lane == 0) steps[s] = part;
-      sum += part;
-    }
-    if (lane == 0) s_wsum[warp] = sum;
-    __syncthreads();
+  int2* raw = reinterpret_cast<int2*>(steps);
+  unsigned meet = 0;  // exchanges so far: their buffers alternate
+
+  // Adds up the warps' sums (s_warp), tells the cluster, and finds the warp
+  // with t = floor(u R): the same answer in every CTA for the owner; in the
+  // owner, its warp `own` and the rest t in that warp's units.
+  unsigned long long R;
+  int gref, owner, own;
+  unsigned long long t;
+  int shift;  // of the owning warp's units
+  auto exchange = [&](float u) {
+    __syncthreads();  // s_warp is complete
+    const TsPart mine = lane < kTsWarps ? s_warp[lane] : TsPart{0ull, kRefEmpty, 0};
+    const int top = __reduce_max_sync(0xffffffffu, mine.ref);
+    const unsigned long long x = ts_shift(mine.sum, top - mine.ref);
     if (warp == 0) {
-      unsigned long long t = warp_sum_u64(lane < kTsWarps ? s_wsum[lane] : 0ull);
+      const unsigned long long sum = warp_sum_u64(x);
       if (lane < (int)C) {  // into every CTA of the cluster
-        const uint32_t at = cluster_addr(&s_part[par_][rank], lane);
-        asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(at), "l"(t) : "memory");
-        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at + 8), "r"(ref) : "memory");
+        const uint32_t at = cluster_addr(&s_part[meet & 1][rank], lane);
+        cluster_st64(at, sum);
+        cluster_st32(at + 8, (uint32_t)top);
       }
     }
     cluster_sync_all();
-    // the total, and the CTA that holds the drawn token
-    int gref = kRefEmpty;
-    for (int c = 0; c < (int)C; ++c) gref = max(gref, s_part[par_][c].ref);
-    unsigned long long R = 0;
-    for (int c = 0; c < (int)C; ++c) {
-      const int sh = gref - s_part[par_][c].ref;
-      R += sh < 64 ? s_part[par_][c].sum >> sh : 0ull;
-    }
-    unsigned long long t = R ? ts_threshold(p.u[(size_t)b * W + d], R) : 0;
-    int owner = -1, shift = 0;
-    if (R) {
-      for (int c = 0; c < (int)C; ++c) {
-        const int sh = gref - s_part[par_][c].ref;
-        const unsigned long long part = sh < 64 ? s_part[par_][c].sum >> sh : 0ull;
-        if (t < part) {
-          owner = c;
-          shift = sh;
-          break;
-        }
-        t -= part;
+    const TsPart part = lane < (int)C ? s_part[meet & 1][lane] : TsPart{0ull, kRefEmpty, 0};
+    gref = __reduce_max_sync(0xffffffffu, part.ref);
+    const unsigned long long y = ts_shift(part.sum, gref - part.ref);
+    R = warp_sum_u64(y);
+    owner = kTsNone;
+    if (gref == kTsRefBad) {
+      owner = kTsUnclear;
+    } else if (R) {
+      t = ts_threshold(u, R);
+      owner = ts_pick(y, &t);
+      if (owner == (int)rank) {
+        t <<= gref - top;  // in the CTA's own units: below its sum
+        own = ts_pick(x, &t);
+        const int r = __shfl_sync(0xffffffffu, mine.ref, own);
+        t <<= top - r;
+        shift = gref - r;
       }
     }
-    if (owner == (int)rank) {
-      t <<= shift;  // in the CTA's own units: below its sum
-      int own = 0;
-      for (; own < kTsWarps - 1 && t >= s_wsum[own]; ++own) t -= s_wsum[own];
-      if (warp == own) {
-        int s = 0;
-        for (; s < p.nsteps - 1 && t >= steps[s]; ++s) t -= steps[s];
+  };
+  // the step of the owning warp that holds t
+  auto find_step = [&]() {
+    int at = p.nsteps - 1;
+    for (int s0 = 0; s0 < p.nsteps; s0 += 32) {
+      const unsigned long long x = s0 + lane < p.nsteps ? steps[s0 + lane] : 0ull;
+      const int k = ts_pick(x, &t);
+      if (k >= 0) {
+        at = s0 + k;
+        break;
+      }
+      t -= warp_sum_u64(x);
+    }
+    return at;
+  };
+  auto tell = [&](int token, float prob) {  // one thread, to every CTA
+    for (int c = 0; c < (int)C; ++c) {
+      cluster_st32(cluster_addr(&s_tok[meet & 1], c), (uint32_t)token);
+      cluster_st32(cluster_addr(&s_prob[meet & 1], c), __float_as_uint(prob));
+    }
+  };
+
+  int cur = 0, d = 0;
+  for (;; ++d) {
+    const typename E::storage* row =
+        static_cast<const typename E::storage*>(p.logits) + ((size_t)b * p.N + cur) * (size_t)p.V;
+    const float u = p.u[(size_t)b * W + d];
+    if (threadIdx.x == 0) s_child = 0x7FFFFFFF;
+    // ---- screen: float32 sums in one pass
+#pragma unroll 4
+    for (int s = 0; s < p.nsteps; ++s) {
+      float z[8];
+      ts_load<E, kVec>(row, w0 + (long long)s * kTsStep, p.V, z);
+      const float m = fmaxf(fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])),
+                            fmaxf(fmaxf(z[4], z[5]), fmaxf(z[6], z[7])));
+      const int ref = __reduce_max_sync(0xffffffffu, exp_ref(m, p.c_hi));
+      const float nref = -(float)ref;
+      float x = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x += ex2(__fmaf_rn(z[e], p.c_hi, nref));
+      x = warp_sum_f(x);
+      if (lane == 0) raw[s] = x <= 512.0f ? make_int2(ref, __float_as_int(x)) : make_int2(kTsRefBad, 0);
+    }
+    __syncwarp();
+    {
+      int top = kRefEmpty;
+      for (int s = lane; s < p.nsteps; s += 32) top = max(top, raw[s].x);
+      top = __reduce_max_sync(0xffffffffu, top);
+      unsigned long long sum = 0;
+      for (int s = lane; s < p.nsteps; s += 32) {
+        const int2 r = raw[s];
+        const int e = kTsScreenFrac + r.x - top;  // bring to the warp's reference
+        const unsigned long long q =
+            e > -20 ? __float2ull_rn(__int_as_float(r.y) * __int_as_float((e + 127) << 23)) : 0ull;
+        steps[s] = q;
+        sum += q;
+      }
+      sum = warp_sum_u64(sum);
+      if (lane == 0) s_warp[warp] = TsPart{sum, top, 0};
+    }
+    exchange(u);
+    if (owner == (int)rank && warp == own) {
+      const int s = find_step();
+      const int ref = s_warp[warp].ref;
+      float z[8];
+      ts_load<E, kVec>(row, w0 + (long long)s * kTsStep, p.V, z);
+      const float nref = -(float)ref;
+      unsigned long long w[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float x = ex2(__fmaf_rn(z[e], p.c_hi, nref));
+        w[e] = __float2ull_rn(x * 68719476736.0f);  // 2^36
+      }
+      unsigned long long part = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) part += w[e];
+      const int at = ts_pick(part, &t);
+      const unsigned long long eps = R >> kTsScreenShift;
+      if (lane == max(at, 0)) {
+        unsigned long long lo = 0, hi = 0;
+        int x = 0;
+        bool found = false;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          if (!found) {
+            lo = hi;
+            hi += w[e];
+            x = e;
+            found = t < hi;
+          }
+        }
+        // distances to the borders, in the cluster's units
+        const bool clear = at >= 0 && found && ((t - lo) >> min(shift, 63)) > eps &&
+                           ((hi - t) >> min(shift, 63)) > eps;
+        const int token = clear ? (int)(w0 + (long long)s * kTsStep) + x : kTsUnclear;
+        tell(token, (float)(hi - lo) / (float)R * pow2i_f(-min(shift, 200)));
+      }
+    }
+    int x = owner;
+    float prob = 0.0f;
+    if (owner >= 0) {
+      cluster_sync_all();
+      x = s_tok[meet & 1];
+      prob = s_prob[meet & 1];
+    }
+    ++meet;
+    if (x == kTsUnclear) {
+      // ---- exact: fixed-point sums relative to the CTA's largest logit
+      int ref = kRefEmpty;
+      for (int s = 0; s < p.nsteps; ++s) {
+        float z[8], m = -INFINITY;
+        ts_load<E, kVec>(row, w0 + (long long)s * kTsStep, p.V, z);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m = fmaxf(m, z[e]);
+        ref = max(ref, exp_ref(m, p.c_hi));
+      }
+      ref = __reduce_max_sync(0xffffffffu, ref);
+      if (lane == 0) s_max[warp] = ref;
+      __syncthreads();
+      ref = __reduce_max_sync(0xffffffffu, s_max[lane & (kTsWarps - 1)]);
+      if (ref == kTsRefBad) ref = kTsRefBad - 1;  // (an infinite logit: unspecified)
+      unsigned long long sum = 0;
+      for (int s = 0; s < p.nsteps; ++s) {
+        float z[8];
+        ts_load<E, kVec>(row, w0 + (long long)s * kTsStep, p.V, z);
+        unsigned long long part = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) part += ts_weight(p, z[e], ref, tab_i, tab_f);
+        part = warp_sum_u64(part);
+        if (lane == 0) steps[s] = part;
+        sum += part;
+      }
+      if (lane == 0) s_warp[warp] = TsPart{sum, ref, 0};
+      exchange(u);
+      if (owner == (int)rank && warp == own) {
+        const int s = find_step();
         float z[8];
         unsigned long long w[8], part = 0;
         ts_load<E, kVec>(row, w0 + (long long)s * kTsStep, p.V, z);
@@ -286,58 +442,66 @@ __global__ void __launch_bounds__(kTsThreads) tree_sample_kernel(const TreeSampl
           w[e] = ts_weight(p, z[e], ref, tab_i, tab_f);
           part += w[e];
         }
-        const unsigned long long incl = warp_scan_u64(part);
-        unsigned long long left = incl - part;
-        if (t >= left && t < incl) {  // one lane
-          int x = 0;
+        if (lane == ts_pick(part, &t)) {
+          unsigned long long left = 0;
+          int e0 = 0;
           float zx = z[0];
           bool found = false;
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            if (!found && t < left + w[e]) {
+            left += w[e];
+            if (!found && t < left) {
               found = true;
-              x = e;
+              e0 = e;
               zx = z[e];
             }
-            left += w[e];
           }
-          const int token = (int)(w0 + (long long)s * kTsStep) + x;
           float hi, lo;
           int n;
-          ts_exponent(p, zx, &hi, &lo);
-          const double mant = (double)ts_mantissa(hi, lo, tab_i, tab_f, &n);
-          const float prob = (float)(mant * exp2((double)(n - gref - p.extra)) / (double)R);
-          for (int c = 0; c < (int)C; ++c) {
-            const uint32_t at = cluster_addr(&s_tok[par_], c), ap = cluster_addr(&s_prob[par_], c);
-            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(token) : "memory");
-            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(ap), "f"(prob) : "memory");
-          }
+          ts_exponent(p, zx, (float)ref, &hi, &lo);
+          const float mant = (float)ts_mantissa(hi, lo, tab_i, tab_f, &n);
+          tell((int)(w0 + (long long)s * kTsStep) + e0,
+               mant / (float)R * pow2i_f(min(n + ref - gref - p.extra, 0)));
         }
       }
+      cluster_sync_all();
+      x = owner < 0 ? kTsNone : s_tok[meet & 1];
+      prob = owner < 0 ? 0.0f : s_prob[meet & 1];
+      ++meet;
     }
-    cluster_sync_all();
-    const int x = owner < 0 ? -1 : s_tok[par_];
     if (rank == 0 && threadIdx.x == 0) {
       p.path[(size_t)b * W + d] = cur;
       p.out[(size_t)b * W + d] = x;
-      p.probs[(size_t)b * W + d] = owner < 0 ? 0.0f : s_prob[par_];
-      if (owner < 0) set_flag(p.flags, kFlagEmptyRow);
+      p.probs[(size_t)b * W + d] = prob;
+      if (x < 0) set_flag(p.flags, kFlagEmptyRow);
     }
     // the lowest-numbered child that holds the token (children come after
     // their parent, so the walk ends)
-    if (x >= 0) {
-      for (int v = cur + 1 + threadIdx.x; v < p.N; v += kTsThreads)
-        if (__ldg(par + v) == cur && __ldg(tok + v) == x) atomicMin(&s_child, v);
+    int child = 0x7FFFFFFF;
+    if (held) {  // every warp for itself
+      for (int v = cur + 1; x >= 0 && v < p.N; v += 32) {
+        const int2 node = v + lane < p.N ? s_tree[v + lane] : make_int2(-1, -1);
+        const unsigned hit = __ballot_sync(0xffffffffu, node.x == cur && node.y == x);
+        if (hit) {
+          child = v + __ffs(hit) - 1;
+          break;
+        }
+      }
+    } else {
+      if (x >= 0) {
+        for (int v = cur + 1 + threadIdx.x; v < p.N; v += kTsThreads)
+          if (__ldg(par + v) == cur && __ldg(tok + v) == x) atomicMin(&s_child, v);
+      }
+      __syncthreads();
+      child = s_child;
+      __syncthreads();  // s_child is read before the next step resets it
     }
-    __syncthreads();
-    const int child = s_child;
     if (child == 0x7FFFFFFF) break;
     if (d == p.max_depth) {
       if (rank == 0 && threadIdx.x == 0) set_flag(p.flags, kFlagDepth);
       break;
     }
     cur = child;
-    __syncthreads();  // s_child is read before the next step resets it
   }
   if (rank == 0) {
     if (threadIdx.x == 0) p.accepted_len[b] = d;

@@ -424,7 +424,8 @@ def check_sample(logits, host, tok, par, u, T, depth, dtype):
     for key in ("accepted_len", "path_nodes", "out_tokens"):
         assert (r[key].cpu().numpy() == o[key]).all(), key
     got = r["out_probs"].double().cpu().numpy()
-    assert (np.abs(got - o["out_probs"]) <= 2 * F32 * o["out_probs"]).all()
+    # a weight and the total, each within 2.7e-6 of the total's float32 sum, and a rounding
+    assert (np.abs(got - o["out_probs"]) <= (2 * 2.7e-6 + F32) * o["out_probs"]).all()
     return o, sv.spec_verify_read_flags(ws)
 
 
@@ -499,6 +500,48 @@ def test_sample_twin_children_take_the_first():
     tok = torch.tensor([[0, 4, 4, 3, 2]], dtype=torch.int32, device="cuda")
     r = sv.verify_tree_sample(z, tok, par, torch.full((1, 4), 0.3, device="cuda"), 1.0, 3)
     assert r["path_nodes"].tolist() == [[0, 1, 4, -1]]
+
+
+@pytest.mark.parametrize("V,dtype", [(64, "f32"), (1024, "bf16"), (65536, "bf16")])
+def test_sample_draws_on_and_next_to_the_borders(V, dtype):
+    """Equal logits: the borders are the multiples of 1 / V, and a uniform on one
+    of them, or the floats beside it, falls where exact arithmetic says."""
+    rng = np.random.default_rng(V)
+    j = np.concatenate([[0, 1, V - 1], rng.integers(0, V, 60)])
+    u = (j / V).astype(np.float32)
+    assert (u.astype(np.float64) * V == j).all()      # V is a power of two: exact
+    u = np.concatenate([u, np.nextafter(u, np.float32(1)), np.nextafter(u, np.float32(0))])
+    n = len(u)
+    logits = torch.full((n, 1, V), -3.25, device="cuda",
+                        dtype=torch.float32 if dtype == "f32" else torch.bfloat16)
+    one = torch.zeros(n, 1, dtype=torch.int32, device="cuda")
+    r = sv.verify_tree_sample(logits, one, one - 1, torch.from_numpy(u[:, None]).cuda(), 0.75, 0)
+    torch.cuda.synchronize()
+    want = np.floor(u.astype(np.float64) * V).astype(np.int32)
+    assert (r["out_tokens"].cpu().numpy()[:, 0] == want).all()
+
+
+def test_sample_spread_out_logits():
+    """Ranges of the logits far apart from one part of the row to the next, where
+    references of the float32 sums lie hundreds of powers of two apart."""
+    rng = np.random.default_rng(12)
+    B, V = 12, 70000
+    z = rng.standard_normal((B, 1, V)).astype(np.float32)
+    at = np.arange(V)
+    z[0:3] += 300.0 * np.sin(at / 9000.0)          # smooth, peaks of many near-equal weights
+    z[3:6] += -4000.0 * (at // 4096 != 7)          # one part holds all the mass
+    z[6] = -1e6 + 0.01 * z[6]
+    z[7] = 2e6 + np.round(z[7])
+    z[8, 0, ::2] = -np.inf
+    z[9, 0, 5:] = -np.inf
+    z[10, 0, :4096] += 30.0                        # the first elements are the largest
+    z[11, 0, 300:] += 150.0                        # the first elements are far too small
+    u = rng.random((B, 1)).astype(np.float32)
+    u[u >= 1] = 0.5
+    one = np.zeros((B, 1), np.int32)
+    logits = torch.from_numpy(z).cuda()
+    o, flags = check_sample(logits, z, one, one - 1, u, 1.0, 0, "f32")
+    assert flags == 0
 
 
 def test_sample_law_of_the_first_token():
