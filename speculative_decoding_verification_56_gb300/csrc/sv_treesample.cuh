@@ -22,13 +22,14 @@
 // hundred thousand unlikely ones, which no float32 sum can promise.  So a step
 // first screens the row in float32, in one pass: every 256 elements are summed
 // as 2^(z_j c - ref) with a power of two near their largest as the reference,
-// those sums are brought together as fixed-point integers, and the token of
-// t = u R is taken if t is further than R / 2^17 from both of its borders.  The
-// error of such sums is bounded: 2^-22.4 of a weight from ex2.approx, 1.5 |r|
-// 2^-24 ln 2 from its argument r (its rounding and that of c), where the mean
-// of |r| over the row's mass is at most log2(V) + 1, and 13 float additions:
-// together below 2.7e-6 R for V = 2^26, of t and of a border.  Otherwise (a
-// draw among tokens of probability below 1e-5, for the most part) the row is
+// those sums are added up in turn, and the token of t = u R is taken if t is
+// further than R / 2^15 from both of its borders.  The error of such sums is
+// bounded: 2^-22.4 of a weight from ex2.approx, 1.5 |r| 2^-24 ln 2 from its
+// argument r (its rounding and that of c), where the mean of |r| over the
+// row's mass is at most log2(V) + 1, and up to 13 float additions in a step, 37
+// over a warp's 1024 steps, 5 over the warps, 5 over the CTAs and 5 in the
+// search: together below 6e-6 R for V = 2^26, of t and of a border.  Otherwise
+// (a draw among tokens of probability below 6e-5, for the most part) the row is
 // summed again exactly: weights as fixed-point 64-bit integers (2^-45 of the
 // largest, from a double-float evaluation of 2^x), whose sums depend on no
 // order.  No float64 arithmetic is on the way: it runs at two operations per
@@ -45,6 +46,60 @@ constexpr int kTsStep = 256;          // elements of a warp's step: 8 per lane
 constexpr int kTsMaxCluster = 16;
 constexpr int kTsFrac = 45;           // fraction bits of a weight
 constexpr unsigned kFlagEmptyRow = 64u;
+
+// 2^(k/64): in units of 2^-45, and as two floats (nearest to the exact values).
+__constant__ long long kTsPow[64] = {
+    0x200000000000ll, 0x2059347cef01ll, 0x20b361a62b0bll, 0x210e8a30eb38ll,
+    0x216ab0d9f312ll, 0x21c7d865a7a3ll, 0x222603a024b7ll, 0x2285355d525cll,
+    0x22e57078faa3ll, 0x2346b7d6df97ll, 0x23a90e62d173ll, 0x240c7710c51all,
+    0x2470f4dceac4ll, 0x24d68acbc4fall, 0x253d3bea3fbell, 0x25a50b4dc806ll,
+    0x260dfc14636ell, 0x26781164c82ell, 0x26e34e6e7554ll, 0x274fb669cb40ll,
+    0x27bd4c982468ll, 0x282c1443ee5cll, 0x289c10c0c312ll, 0x290d456b827all,
+    0x297fb5aa6c54ll, 0x29f364ed3a59ll, 0x2a6856ad3a9fll, 0x2ade8e6d6a50ll,
+    0x2b560fba90a8ll, 0x2bcede2b5a43ll, 0x2c48fd6074abll, 0x2cc47104aa44ll,
+    0x2d413cccfe78ll, 0x2dbf6478ca34ll, 0x2e3eebd1d8bfll, 0x2ebfd6ac84d0ll,
+    0x2f4228e7d603ll, 0x2fc5e66d9e9dll, 0x304b1332999cll, 0x30d1b3368926ll,
+    0x3159ca845542ll, 0x31e35d322aeell, 0x326e6f619b8cll, 0x32fb053fbc9dll,
+    0x3389230547e1ll, 0x3418ccf6bbcbll, 0x34aa07647c4bll, 0x353cd6aaf3fbll,
+    0x35d13f32b5a7ll, 0x366745709e2cll, 0x36feede5f6bdll, 0x37983d209784ll,
+    0x383337bb0aa5ll, 0x38cfe25cafa3ll, 0x396e41b9df21ll, 0x3a0e5a940f13ll,
+    0x3ab031b9f749ll, 0x3b53cc07b665ll, 0x3bf92e66f737ll, 0x3ca05dcf1680ll,
+    0x3d495f454922ll, 0x3df437dcc2b4ll, 0x3ea0ecb6dc8bll, 0x3f4f83033d22ll,
+};
+__constant__ float2 kTsPowF[64] = {
+    {0x1.0000000000000p+0f, 0x0.0p+0f}, {0x1.02c9a40000000p+0f, -0x1.887fa00000000p-28f},
+    {0x1.059b0e0000000p+0f, -0x1.9d4f520000000p-25f}, {0x1.0874520000000p+0f, -0x1.e2990e0000000p-26f},
+    {0x1.0b55860000000p+0f, 0x1.9f31220000000p-25f}, {0x1.0e3ec40000000p+0f, -0x1.a585cc0000000p-25f},
+    {0x1.11301e0000000p+0f, -0x1.fdb4960000000p-25f}, {0x1.1429aa0000000p+0f, 0x1.d525bc0000000p-25f},
+    {0x1.172b840000000p+0f, -0x1.c157420000000p-27f}, {0x1.1a35be0000000p+0f, 0x1.6df96e0000000p-25f},
+    {0x1.1d48740000000p+0f, -0x1.d2e8ca0000000p-25f}, {0x1.2063b80000000p+0f, 0x1.0c519a0000000p-25f},
+    {0x1.2387a60000000p+0f, 0x1.ceac480000000p-25f}, {0x1.26b4560000000p+0f, 0x1.789f380000000p-26f},
+    {0x1.29e9e00000000p+0f, -0x1.5c04240000000p-25f}, {0x1.2d285a0000000p+0f, 0x1.b900c20000000p-26f},
+    {0x1.306fe00000000p+0f, 0x1.4636e20000000p-25f}, {0x1.33c08c0000000p+0f, -0x1.b37d200000000p-25f},
+    {0x1.371a740000000p+0f, -0x1.18aac60000000p-25f}, {0x1.3a7db40000000p+0f, -0x1.634c020000000p-25f},
+    {0x1.3dea640000000p+0f, 0x1.8246840000000p-25f}, {0x1.4160a20000000p+0f, 0x1.f72e2a0000000p-28f},
+    {0x1.44e0860000000p+0f, 0x1.8624b40000000p-30f}, {0x1.486a2c0000000p+0f, -0x1.47d8660000000p-25f},
+    {0x1.4bfdae0000000p+0f, -0x1.593abc0000000p-25f}, {0x1.4f9b280000000p+0f, -0x1.2c5a6c0000000p-25f},
+    {0x1.5342b60000000p+0f, -0x1.2c56100000000p-25f}, {0x1.56f4740000000p+0f, -0x1.295b040000000p-25f},
+    {0x1.5ab07e0000000p+0f, -0x1.5bd5ec0000000p-27f}, {0x1.5e76f20000000p+0f, -0x1.4a5bd60000000p-25f},
+    {0x1.6247ec0000000p+0f, -0x1.f8b5500000000p-25f}, {0x1.6623880000000p+0f, 0x1.2a91120000000p-27f},
+    {0x1.6a09e60000000p+0f, 0x1.9fcef40000000p-26f}, {0x1.6dfb240000000p+0f, -0x1.cd72e80000000p-27f},
+    {0x1.71f75e0000000p+0f, 0x1.1d8bee0000000p-25f}, {0x1.75feb60000000p+0f, -0x1.37b3060000000p-25f},
+    {0x1.7a11480000000p+0f, -0x1.829fd00000000p-25f}, {0x1.7e2f340000000p+0f, -0x1.2616340000000p-25f},
+    {0x1.82589a0000000p+0f, -0x1.accc7c0000000p-26f}, {0x1.868d9a0000000p+0f, -0x1.2edb440000000p-26f},
+    {0x1.8ace540000000p+0f, 0x1.15506e0000000p-27f}, {0x1.8f1aea0000000p+0f, -0x1.baa2320000000p-26f},
+    {0x1.93737c0000000p+0f, -0x1.e647440000000p-25f}, {0x1.97d82a0000000p+0f, -0x1.0d8d840000000p-31f},
+    {0x1.9c49180000000p+0f, 0x1.51f8480000000p-27f}, {0x1.a0c6680000000p+0f, -0x1.2886a60000000p-26f},
+    {0x1.a5503c0000000p+0f, -0x1.b83b540000000p-25f}, {0x1.a9e6b60000000p+0f, -0x1.50c0480000000p-25f},
+    {0x1.ae89fa0000000p+0f, -0x1.a94b140000000p-26f}, {0x1.b33a2c0000000p+0f, -0x1.ec3a820000000p-26f},
+    {0x1.b7f7700000000p+0f, -0x1.a094380000000p-25f}, {0x1.bcc1ea0000000p+0f, -0x1.f687c60000000p-25f},
+    {0x1.c199be0000000p+0f, -0x1.3d56b20000000p-27f}, {0x1.c67f120000000p+0f, 0x1.cafa2a0000000p-25f},
+    {0x1.cb720e0000000p+0f, -0x1.8837cc0000000p-27f}, {0x1.d072d40000000p+0f, 0x1.40f1300000000p-25f},
+    {0x1.d5818e0000000p+0f, -0x1.822dbc0000000p-27f}, {0x1.da9e600000000p+0f, 0x1.ed99420000000p-27f},
+    {0x1.dfc9740000000p+0f, -0x1.908c940000000p-25f}, {0x1.e502ee0000000p+0f, 0x1.e2cffe0000000p-26f},
+    {0x1.ea4afa0000000p+0f, 0x1.52486c0000000p-27f}, {0x1.efa1be0000000p+0f, 0x1.cc2b440000000p-25f},
+    {0x1.f507660000000p+0f, -0x1.246eb00000000p-26f}, {0x1.fa7c180000000p+0f, 0x1.9e90d80000000p-28f},
+};
 
 struct TreeSampleParams {
   const void* logits;         // [B, N, V]
@@ -178,9 +233,9 @@ __device__ __forceinline__ void ts_load(const typename E::storage* row, long lon
 
 // A CTA's part of a row, as every CTA of the cluster holds it.
 struct TsPart {
-  unsigned long long sum;  // of fixed-point weights relative to 2^ref
+  unsigned long long sum;  // exact: of fixed-point weights relative to 2^ref
   int ref;
-  int pad;
+  float fsum;              // screened: of weights relative to 2^ref
 };
 
 __device__ __forceinline__ void cluster_st64(uint32_t at, unsigned long long x) {
@@ -190,8 +245,7 @@ __device__ __forceinline__ void cluster_st32(uint32_t at, uint32_t x) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(x) : "memory");
 }
 
-constexpr int kTsScreenShift = 17;  // draws nearer than R / 2^17 to a border are decided exactly
-constexpr int kTsScreenFrac = 36;   // fraction bits of the screen's sums
+constexpr float kTsScreen = 1.0f / 32768.0f;  // of R: draws nearer to a border are decided exactly
 constexpr int kTsTreeSmem = 1024;   // trees of up to so many nodes are held in shared memory
 constexpr int kTsNone = -1, kTsUnclear = -2;
 constexpr int kTsRefBad = 1 << 30;  // of a sum that is not finite
@@ -209,6 +263,28 @@ __device__ __forceinline__ int ts_pick(unsigned long long x, unsigned long long*
   const int at = __ffs(past) - 1;
   *t -= __shfl_sync(0xffffffffu, incl - x, at);
   return at;
+}
+
+// The same for float sums (behind all of them: the last lane that is not 0).
+__device__ __forceinline__ float warp_scan_f(float v) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const float y = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += y;
+  }
+  return v;
+}
+__device__ __forceinline__ int ts_pick_f(float x, float incl, float* t) {
+  const unsigned past = __ballot_sync(0xffffffffu, *t < incl && x > 0.0f);
+  const unsigned some = __ballot_sync(0xffffffffu, x > 0.0f);
+  const int at = past ? __ffs(past) - 1 : some ? 31 - __clz(some) : 0;
+  *t = fmaxf(*t - __shfl_sync(0xffffffffu, incl - x, at), 0.0f);
+  return at;
+}
+// 2^d, 0 for d < -126 (d <= 127)
+__device__ __forceinline__ float ts_pow2(int d) {
+  return d < -126 ? 0.0f : __int_as_float((min(d, 127) + 127) << 23);
 }
 
 template <typename E, bool kVec>
@@ -229,9 +305,8 @@ __global__ void __launch_bounds__(kTsThreads, 2) tree_sample_kernel(const TreeSa
   const uint32_t rank = cluster_rank();
   const int b = blockIdx.x / C;
   if (threadIdx.x < 64) {
-    const double m = exp2((double)threadIdx.x / 64.0);
-    tab_i[threadIdx.x] = __double2ll_rn(m * 35184372088832.0);  // 2^45
-    tab_f[threadIdx.x] = make_float2((float)m, (float)(m - (double)(float)m));
+    tab_i[threadIdx.x] = kTsPow[threadIdx.x];
+    tab_f[threadIdx.x] = kTsPowF[threadIdx.x];
   }
   // a programmatic dependent of the kernel before it in the stream: nothing
   // of global memory is touched before that grid has finished
@@ -259,16 +334,15 @@ __global__ void __launch_bounds__(kTsThreads, 2) tree_sample_kernel(const TreeSa
   int2* raw = reinterpret_cast<int2*>(steps);
   unsigned meet = 0;  // exchanges so far: their buffers alternate
 
-  // Adds up the warps' sums (s_warp), tells the cluster, and finds the warp
-  // with t = floor(u R): the same answer in every CTA for the owner; in the
-  // owner, its warp `own` and the rest t in that warp's units.
+  // Exact: adds up the warps' sums (s_warp), tells the cluster, and finds the
+  // CTA with t = floor(u R) -- the same answer everywhere -- and in that CTA
+  // the warp `own` and the rest t.
   unsigned long long R;
   int gref, owner, own;
   unsigned long long t;
-  int shift;  // of the owning warp's units
   auto exchange = [&](float u) {
     __syncthreads();  // s_warp is complete
-    const TsPart mine = lane < kTsWarps ? s_warp[lane] : TsPart{0ull, kRefEmpty, 0};
+    const TsPart mine = lane < kTsWarps ? s_warp[lane] : TsPart{0ull, kRefEmpty, 0.0f};
     const int top = __reduce_max_sync(0xffffffffu, mine.ref);
     const unsigned long long x = ts_shift(mine.sum, top - mine.ref);
     if (warp == 0) {
@@ -280,22 +354,17 @@ __global__ void __launch_bounds__(kTsThreads, 2) tree_sample_kernel(const TreeSa
       }
     }
     cluster_sync_all();
-    const TsPart part = lane < (int)C ? s_part[meet & 1][lane] : TsPart{0ull, kRefEmpty, 0};
+    const TsPart part = lane < (int)C ? s_part[meet & 1][lane] : TsPart{0ull, kRefEmpty, 0.0f};
     gref = __reduce_max_sync(0xffffffffu, part.ref);
     const unsigned long long y = ts_shift(part.sum, gref - part.ref);
     R = warp_sum_u64(y);
     owner = kTsNone;
-    if (gref == kTsRefBad) {
-      owner = kTsUnclear;
-    } else if (R) {
+    if (R) {
       t = ts_threshold(u, R);
       owner = ts_pick(y, &t);
       if (owner == (int)rank) {
-        t <<= gref - top;  // in the CTA's own units: below its sum
-        own = ts_pick(x, &t);
-        const int r = __shfl_sync(0xffffffffu, mine.ref, own);
-        t <<= top - r;
-        shift = gref - r;
+        t <<= gref - top;      // in the CTA's own units: below its sum
+        own = ts_pick(x, &t);  // (a CTA's warps have one reference)
       }
     }
   };
@@ -313,10 +382,12 @@ __global__ void __launch_bounds__(kTsThreads, 2) tree_sample_kernel(const TreeSa
     }
     return at;
   };
-  auto tell = [&](int token, float prob) {  // one thread, to every CTA
-    for (int c = 0; c < (int)C; ++c) {
-      cluster_st32(cluster_addr(&s_tok[meet & 1], c), (uint32_t)token);
-      cluster_st32(cluster_addr(&s_prob[meet & 1], c), __float_as_uint(prob));
+  auto tell = [&](int from, int token, float prob) {  // lane `from`'s, to every CTA
+    token = __shfl_sync(0xffffffffu, token, from);
+    prob = __shfl_sync(0xffffffffu, prob, from);
+    if (lane < (int)C) {
+      cluster_st32(cluster_addr(&s_tok[meet & 1], lane), (uint32_t)token);
+      cluster_st32(cluster_addr(&s_prob[meet & 1], lane), __float_as_uint(prob));
     }
   };
 
@@ -346,55 +417,81 @@ __global__ void __launch_bounds__(kTsThreads, 2) tree_sample_kernel(const TreeSa
       int top = kRefEmpty;
       for (int s = lane; s < p.nsteps; s += 32) top = max(top, raw[s].x);
       top = __reduce_max_sync(0xffffffffu, top);
-      unsigned long long sum = 0;
-      for (int s = lane; s < p.nsteps; s += 32) {
-        const int2 r = raw[s];
-        const int e = kTsScreenFrac + r.x - top;  // bring to the warp's reference
-        const unsigned long long q =
-            e > -20 ? __float2ull_rn(__int_as_float(r.y) * __int_as_float((e + 127) << 23)) : 0ull;
-        steps[s] = q;
-        sum += q;
+      float sum = 0.0f;
+      for (int s = lane; s < p.nsteps; s += 32) {  // brought to the warp's reference
+        const float y = __int_as_float(raw[s].y) * ts_pow2(raw[s].x - top);
+        raw[s].y = __float_as_int(y);
+        sum += y;
       }
-      sum = warp_sum_u64(sum);
-      if (lane == 0) s_warp[warp] = TsPart{sum, top, 0};
+      sum = warp_sum_f(sum);
+      if (lane == 0) s_warp[warp] = TsPart{0ull, top, sum};
     }
-    exchange(u);
+    __syncthreads();
+    float R_f = 0.0f, t_f = 0.0f;
+    {
+      const TsPart mine = lane < kTsWarps ? s_warp[lane] : TsPart{0ull, kRefEmpty, 0.0f};
+      const int top = __reduce_max_sync(0xffffffffu, mine.ref);
+      if (warp == 0) {
+        const float sum = warp_sum_f(mine.fsum * ts_pow2(mine.ref - top));
+        if (lane < (int)C)  // into every CTA of the cluster
+          cluster_st64(cluster_addr(&s_part[meet & 1][rank].ref, lane),
+                       (unsigned long long)__float_as_uint(sum) << 32 | (uint32_t)top);
+      }
+      cluster_sync_all();
+      const TsPart part = lane < (int)C ? s_part[meet & 1][lane] : TsPart{0ull, kRefEmpty, 0.0f};
+      gref = __reduce_max_sync(0xffffffffu, part.ref);
+      const float y = part.fsum * ts_pow2(part.ref - gref);
+      const float incl = warp_scan_f(y);
+      R_f = __shfl_sync(0xffffffffu, incl, 31);
+      owner = gref == kTsRefBad ? kTsUnclear : kTsNone;
+      if (gref != kTsRefBad && R_f > 0.0f) {
+        t_f = fminf(fmaxf(u, 0.0f), 0.99999994f) * R_f;
+        owner = ts_pick_f(y, incl, &t_f);
+        if (owner == (int)rank) {
+          const float x = mine.fsum * ts_pow2(mine.ref - gref);
+          own = ts_pick_f(x, warp_scan_f(x), &t_f);
+        }
+      }
+    }
     if (owner == (int)rank && warp == own) {
-      const int s = find_step();
       const int ref = s_warp[warp].ref;
-      float z[8];
+      const float unit = ts_pow2(ref - gref);  // of the warp's sums
+      int s = 0;
+      for (int s0 = 0; s0 < p.nsteps; s0 += 32) {
+        const float y = s0 + lane < p.nsteps ? __int_as_float(raw[s0 + lane].y) * unit : 0.0f;
+        const float incl = warp_scan_f(y);
+        const float all = __shfl_sync(0xffffffffu, incl, 31);
+        if (t_f < all || s0 + 32 >= p.nsteps) {
+          s = s0 + ts_pick_f(y, incl, &t_f);
+          break;
+        }
+        t_f -= all;
+      }
+      float z[8], w[8], sum = 0.0f;
       ts_load<E, kVec>(row, w0 + (long long)s * kTsStep, p.V, z);
       const float nref = -(float)ref;
-      unsigned long long w[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float x = ex2(__fmaf_rn(z[e], p.c_hi, nref));
-        w[e] = __float2ull_rn(x * 68719476736.0f);  // 2^36
+        w[e] = ex2(__fmaf_rn(z[e], p.c_hi, nref)) * unit;
+        sum += w[e];
       }
-      unsigned long long part = 0;
+      const int at = ts_pick_f(sum, warp_scan_f(sum), &t_f);
+      float lo = 0.0f, hi = 0.0f, wx = 0.0f;  // (of the lane that holds t)
+      int x = 0;
+      bool found = false;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) part += w[e];
-      const int at = ts_pick(part, &t);
-      const unsigned long long eps = R >> kTsScreenShift;
-      if (lane == max(at, 0)) {
-        unsigned long long lo = 0, hi = 0;
-        int x = 0;
-        bool found = false;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          if (!found) {
-            lo = hi;
-            hi += w[e];
-            x = e;
-            found = t < hi;
-          }
+      for (int e = 0; e < 8; ++e) {
+        if (!found) {
+          lo = hi;
+          hi += w[e];
+          wx = w[e];
+          x = e;
+          found = t_f < hi;
         }
-        // distances to the borders, in the cluster's units
-        const bool clear = at >= 0 && found && ((t - lo) >> min(shift, 63)) > eps &&
-                           ((hi - t) >> min(shift, 63)) > eps;
-        const int token = clear ? (int)(w0 + (long long)s * kTsStep) + x : kTsUnclear;
-        tell(token, (float)(hi - lo) / (float)R * pow2i_f(-min(shift, 200)));
       }
+      const float eps = R_f * kTsScreen;
+      const bool clear = found && t_f - lo > eps && hi - t_f > eps;
+      tell(at, clear ? (int)(w0 + (long long)s * kTsStep) + x : kTsUnclear, wx / R_f);
     }
     int x = owner;
     float prob = 0.0f;
@@ -430,7 +527,7 @@ __global__ void __launch_bounds__(kTsThreads, 2) tree_sample_kernel(const TreeSa
         if (lane == 0) steps[s] = part;
         sum += part;
       }
-      if (lane == 0) s_warp[warp] = TsPart{sum, ref, 0};
+      if (lane == 0) s_warp[warp] = TsPart{sum, ref, 0.0f};
       exchange(u);
       if (owner == (int)rank && warp == own) {
         const int s = find_step();
@@ -442,27 +539,26 @@ __global__ void __launch_bounds__(kTsThreads, 2) tree_sample_kernel(const TreeSa
           w[e] = ts_weight(p, z[e], ref, tab_i, tab_f);
           part += w[e];
         }
-        if (lane == ts_pick(part, &t)) {
-          unsigned long long left = 0;
-          int e0 = 0;
-          float zx = z[0];
-          bool found = false;
+        const int at = ts_pick(part, &t);
+        unsigned long long left = 0;
+        int e0 = 0;
+        float zx = z[0];
+        bool found = false;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            left += w[e];
-            if (!found && t < left) {
-              found = true;
-              e0 = e;
-              zx = z[e];
-            }
+        for (int e = 0; e < 8; ++e) {
+          left += w[e];
+          if (!found && t < left) {
+            found = true;
+            e0 = e;
+            zx = z[e];
           }
-          float hi, lo;
-          int n;
-          ts_exponent(p, zx, (float)ref, &hi, &lo);
-          const float mant = (float)ts_mantissa(hi, lo, tab_i, tab_f, &n);
-          tell((int)(w0 + (long long)s * kTsStep) + e0,
-               mant / (float)R * pow2i_f(min(n + ref - gref - p.extra, 0)));
         }
+        float hi, lo;
+        int n;
+        ts_exponent(p, zx, (float)ref, &hi, &lo);
+        const float mant = (float)ts_mantissa(hi, lo, tab_i, tab_f, &n);
+        tell(max(at, 0), (int)(w0 + (long long)s * kTsStep) + e0,
+             mant / (float)R * pow2i_f(min(n + ref - gref - p.extra, 0)));
       }
       cluster_sync_all();
       x = owner < 0 ? kTsNone : s_tok[meet & 1];

@@ -424,8 +424,8 @@ def check_sample(logits, host, tok, par, u, T, depth, dtype):
     for key in ("accepted_len", "path_nodes", "out_tokens"):
         assert (r[key].cpu().numpy() == o[key]).all(), key
     got = r["out_probs"].double().cpu().numpy()
-    # a weight and the total, each within 2.7e-6 of the total's float32 sum, and a rounding
-    assert (np.abs(got - o["out_probs"]) <= (2 * 2.7e-6 + F32) * o["out_probs"]).all()
+    # a weight and the total, each within 6e-6 of the total's float32 sum, and a rounding
+    assert (np.abs(got - o["out_probs"]) <= (2 * 6e-6 + F32) * o["out_probs"]).all()
     return o, sv.spec_verify_read_flags(ws)
 
 
