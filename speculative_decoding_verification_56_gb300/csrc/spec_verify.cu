@@ -1055,7 +1055,7 @@ spec_status_t spec_verify_tree_sample(const void* target_logits, int dtype,
   prm.flags = reinterpret_cast<unsigned*>(workspace);
   constexpr int kCtaStep = sv::kTsWarps * sv::kTsStep;  // elements of a CTA's step
   int most = 1;  // CTAs per sequence
-  while (most < sv::kTsMaxCluster && 2 * most * B <= 304) most *= 2;
+  while (most < sv::kTsMaxCluster && 2 * most * B <= 1216) most *= 2;
 #ifdef TS_CLUSTER
   most = TS_CLUSTER;
 #endif

@@ -40,7 +40,7 @@
 
 namespace sv {
 
-constexpr int kTsThreads = 512;
+constexpr int kTsThreads = 256;
 constexpr int kTsWarps = kTsThreads / 32;
 constexpr int kTsStep = 256;          // elements of a warp's step: 8 per lane
 constexpr int kTsMaxCluster = 16;
@@ -288,7 +288,7 @@ __device__ __forceinline__ float ts_pow2(int d) {
 }
 
 template <typename E, bool kVec>
-__global__ void __launch_bounds__(kTsThreads, 2) tree_sample_kernel(const TreeSampleParams p) {
+__global__ void __launch_bounds__(kTsThreads, 4) tree_sample_kernel(const TreeSampleParams p) {
   extern __shared__ unsigned long long ts_steps[];  // [kTsWarps][nsteps]: sums of the steps
   __shared__ long long tab_i[64];
   __shared__ float2 tab_f[64];
@@ -514,7 +514,7 @@ __global__ void __launch_bounds__(kTsThreads, 2) tree_sample_kernel(const TreeSa
       ref = __reduce_max_sync(0xffffffffu, ref);
       if (lane == 0) s_max[warp] = ref;
       __syncthreads();
-      ref = __reduce_max_sync(0xffffffffu, s_max[lane & (kTsWarps - 1)]);
+      ref = __reduce_max_sync(0xffffffffu, s_max[lane % kTsWarps]);
       if (ref == kTsRefBad) ref = kTsRefBad - 1;  // (an infinite logit: unspecified)
       unsigned long long sum = 0;
       for (int s = 0; s < p.nsteps; ++s) {
