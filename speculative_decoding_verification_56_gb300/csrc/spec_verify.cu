@@ -593,6 +593,18 @@ spec_status_t run_attention(const sv::AttnParams& prm, const CUtensorMap (&map)[
                 sv::kAtFinThreads);
 }
 
+template <int D>
+spec_status_t run_rope(const sv::RopeParams& prm, int mode, int nodes, void* stream) {
+  if (mode == sv::kRopeHalves)
+    return launch(sv::tree_qkv_rope_kernel<D, sv::kRopeHalves>, nodes, 0, prm, stream, true, 1,
+                  sv::kRopeThreads);
+  if (mode == sv::kRopePairs)
+    return launch(sv::tree_qkv_rope_kernel<D, sv::kRopePairs>, nodes, 0, prm, stream, true, 1,
+                  sv::kRopeThreads);
+  return launch(sv::tree_qkv_rope_kernel<D, sv::kRopeOdd>, nodes, 0, prm, stream, true, 1,
+                sv::kRopeThreads);
+}
+
 bool attn_shape_ok(int B, int N, int Hq, int Hkv, int D, int P) {
   return B >= 0 && N >= 1 && N <= SPEC_ATTN_MAX_NODES && Hkv >= 1 && Hq >= Hkv && Hq <= 65536 &&
          Hq % Hkv == 0 && Hq / Hkv <= 128 && (D == 64 || D == 128) && P >= 0 &&
@@ -1115,15 +1127,8 @@ spec_status_t spec_tree_qkv_rope(const void* qkv, const void* q_norm, const void
   prm.L = L;
   prm.rot = rot_dim;
   prm.interleaved = interleaved != 0;
-  // both members of every pair in one thread: adjacent elements, or halves a
-  // whole number of 8-element vectors apart
-  const bool vec = interleaved || rot_dim % 16 == 0;
-  const int grid = B * N;
-  if (D == 128)
-    return vec ? launch(sv::tree_qkv_rope_kernel<128, true>, grid, 0, prm, stream, true, 1, sv::kRopeThreads)
-               : launch(sv::tree_qkv_rope_kernel<128, false>, grid, 0, prm, stream, true, 1, sv::kRopeThreads);
-  return vec ? launch(sv::tree_qkv_rope_kernel<64, true>, grid, 0, prm, stream, true, 1, sv::kRopeThreads)
-             : launch(sv::tree_qkv_rope_kernel<64, false>, grid, 0, prm, stream, true, 1, sv::kRopeThreads);
+  const int mode = interleaved ? sv::kRopePairs : rot_dim % 16 == 0 ? sv::kRopeHalves : sv::kRopeOdd;
+  return D == 128 ? run_rope<128>(prm, mode, B * N, stream) : run_rope<64>(prm, mode, B * N, stream);
 }
 
 size_t spec_tree_attention_workspace_bytes(int B, int N, int Hq, int Hkv, int D, int P) {

@@ -11,18 +11,21 @@
 //   (a, b) -> (a cos - b sin, b cos + a sin)    angle = pos * inv_freq[i]
 //
 // in float32, rounded to bf16 once at the end.  Memory-bound: every element
-// is read once and written once.  One CTA per node: its first rot/2 threads
-// make the node's sines and cosines while the first heads' loads are in
-// flight, and D/16 threads share a head, each holding the two 8-element
-// vectors that a rotation pairs, so that the rotation needs no exchange and
-// the norm a butterfly over 4 or 8 lanes.
+// is read once and written once, so what counts is that the arithmetic in
+// between stays below the loads: D/16 threads share a head, each holding the
+// two 8-element vectors that a rotation pairs, which needs no exchange (the
+// norm is a butterfly over 4 or 8 lanes), and a thread keeps its sines,
+// cosines and norm weights in registers over all the heads of the node that
+// it takes, as pairs for the two-wide float instructions.  One CTA per node;
+// the first threads make the sines and cosines while the first heads' loads
+// are in flight.
 #pragma once
 
 #include "sv_device.cuh"
 
 namespace sv {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 64;  // at least D / 2: they make the sines
 
 struct RopeParams {
   const uint16_t* qkv;     // [B, N, Hq + 2 Hkv, D] bf16
@@ -48,15 +51,6 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-__device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8]) {
-  x[0] = bf16_lo(v.x); x[1] = bf16_hi(v.x); x[2] = bf16_lo(v.y); x[3] = bf16_hi(v.y);
-  x[4] = bf16_lo(v.z); x[5] = bf16_hi(v.z); x[6] = bf16_lo(v.w); x[7] = bf16_hi(v.w);
-}
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-  return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
-                    pack_bf16(x[6], x[7]));
-}
-
 // Sine and cosine of pos * f for an integer position and a float frequency.
 // The turns per position f / (2 pi) are held to 2^-64 of a turn (the product
 // as a double-float, about 2^-48 relative), multiplied by pos modulo one turn
@@ -79,10 +73,40 @@ __device__ __forceinline__ void turn_sincos(long long pos, float f, float* sn, f
   *sn *= sign;
 }
 
-// kVec: the vector layout holds both members of every pair in one thread
-// (pairs side by side, or halves a whole number of 8-element vectors apart);
-// otherwise each thread finds an element's partner in memory.
-template <int D, bool kVec>
+// mul.rn on both floats of a pair
+__device__ __forceinline__ unsigned long long mul2(unsigned long long a, unsigned long long b) {
+  unsigned long long d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+// a vector of 8 bf16 as 4 pairs of floats, and back
+__device__ __forceinline__ void unpack_pairs(const uint4& v, unsigned long long (&x)[4]) {
+  x[0] = f2pack(bf16_lo(v.x), bf16_hi(v.x));
+  x[1] = f2pack(bf16_lo(v.y), bf16_hi(v.y));
+  x[2] = f2pack(bf16_lo(v.z), bf16_hi(v.z));
+  x[3] = f2pack(bf16_lo(v.w), bf16_hi(v.w));
+}
+__device__ __forceinline__ uint32_t pack_pair(unsigned long long x) {
+  float lo, hi;
+  f2unpack(x, lo, hi);
+  return pack_bf16(lo, hi);
+}
+__device__ __forceinline__ uint4 pack_pairs(const unsigned long long (&x)[4]) {
+  return make_uint4(pack_pair(x[0]), pack_pair(x[1]), pack_pair(x[2]), pack_pair(x[3]));
+}
+__device__ __forceinline__ unsigned long long swap_pair(unsigned long long x) {
+  float lo, hi;
+  f2unpack(x, lo, hi);
+  return f2pack(hi, lo);
+}
+
+// Where a rotation finds its two elements: in the halves of the rotated part,
+// a whole number of 8-element vectors apart, or side by side (in either case
+// in one thread); or in halves that are not whole vectors, where each thread
+// reads an element's partner from memory.
+enum RopeMode : int { kRopeHalves = 0, kRopePairs = 1, kRopeOdd = 2 };
+
+template <int D, int kMode>
 __global__ void __launch_bounds__(kRopeThreads) tree_qkv_rope_kernel(const RopeParams p) {
   constexpr int kLanes = D / 16;                  // threads per head
   constexpr int kHeads = kRopeThreads / kLanes;   // heads in flight per CTA
@@ -91,14 +115,6 @@ __global__ void __launch_bounds__(kRopeThreads) tree_qkv_rope_kernel(const RopeP
   asm volatile("griddepcontrol.launch_dependents;");
   const int node = blockIdx.x;
   const int b = node / p.N, v = node - b * p.N;
-  const int base = __ldg(p.base_len + b);
-  const bool ok = base >= 1 && (long long)base + p.N - 1 <= p.L;
-  int dep = p.depth ? __ldg(p.depth + node) : v;
-  if (threadIdx.x == 0) {
-    if (!ok && v == 0) set_flag(p.flags, kFlagBadPath);
-    if (dep < 0) set_flag(p.flags, kFlagBadParent);
-  }
-  if (dep < 0) dep = 0;
   const int H = p.Hq + 2 * p.Hkv;
   const int sub = threadIdx.x % kLanes;
   const int half = p.rot / 2;
@@ -106,7 +122,8 @@ __global__ void __launch_bounds__(kRopeThreads) tree_qkv_rope_kernel(const RopeP
   // the thread's two 8-element vectors: a rotated pair of vectors first, then
   // what is left of the head in order
   int c0 = 2 * sub, c1 = 2 * sub + 1;
-  if (kVec && !p.interleaved && sub < p.rot / 16) {
+  const bool turns = kMode == kRopeHalves && sub < p.rot / 16;
+  if (turns) {
     c0 = sub;
     c1 = sub + p.rot / 16;
   }
@@ -114,20 +131,59 @@ __global__ void __launch_bounds__(kRopeThreads) tree_qkv_rope_kernel(const RopeP
   int h = threadIdx.x / kLanes;
   uint4 r0, r1;
   if (h < H) {
-    r0 = *reinterpret_cast<const uint4*>(src + (size_t)h * D + c0 * 8);
-    r1 = *reinterpret_cast<const uint4*>(src + (size_t)h * D + c1 * 8);
+    r0 = ldg_stream(src + (size_t)h * D + c0 * 8);
+    r1 = ldg_stream(src + (size_t)h * D + c1 * 8);
   }
+  const int base = __ldg(p.base_len + b);
+  int dep = p.depth ? __ldg(p.depth + node) : v;
+  const bool ok = base >= 1 && (long long)base + p.N - 1 <= p.L;
+  if (threadIdx.x == 0) {
+    if (!ok && v == 0) set_flag(p.flags, kFlagBadPath);
+    if (dep < 0) set_flag(p.flags, kFlagBadParent);
+  }
+  if (dep < 0) dep = 0;
   if (threadIdx.x < half) {
     const long long pos = p.pos_offset + base - 1 + dep;
     turn_sincos(pos, __ldg(p.inv_freq + threadIdx.x), &s_sin[threadIdx.x], &s_cos[threadIdx.x]);
   }
+  unsigned long long wq[8];  // the query norm's weights of the thread's elements
+  if (p.q_norm) {
+    unsigned long long t[4];
+    unpack_pairs(__ldg(reinterpret_cast<const uint4*>(p.q_norm + c0 * 8)), t);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) wq[i] = t[i];
+    unpack_pairs(__ldg(reinterpret_cast<const uint4*>(p.q_norm + c1 * 8)), t);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) wq[4 + i] = t[i];
+  }
   __syncthreads();
+  // halves: cosines and sines of the vector's elements, two to a word; pairs:
+  // (c, c) and (-s, s) of the 8 pairs of both vectors
+  unsigned long long cs[8], sn[8];
+  if (turns) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int e = c0 * 8 + 2 * i;
+      cs[i] = f2pack(s_cos[e], s_cos[e + 1]);
+      sn[i] = f2pack(s_sin[e], s_sin[e + 1]);
+      sn[4 + i] = f2pack(-s_sin[e], -s_sin[e + 1]);
+    }
+  } else if (kMode == kRopePairs) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int e = (i < 4 ? c0 : c1) * 4 + (i & 3);  // the pair's number
+      const bool in = e < half;
+      const float c = in ? s_cos[e] : 1.0f, s = in ? s_sin[e] : 0.0f;
+      cs[i] = f2pack(c, c);
+      sn[i] = f2pack(-s, s);
+    }
+  }
   for (; h < H; h += kHeads) {
     const uint4 a = r0, c = r1;
     const int hn = h + kHeads;
     if (hn < H) {  // the next head's loads
-      r0 = *reinterpret_cast<const uint4*>(src + (size_t)hn * D + c0 * 8);
-      r1 = *reinterpret_cast<const uint4*>(src + (size_t)hn * D + c1 * 8);
+      r0 = ldg_stream(src + (size_t)hn * D + c0 * 8);
+      r1 = ldg_stream(src + (size_t)hn * D + c1 * 8);
     }
     const bool is_q = h < p.Hq, is_v = h >= p.Hq + p.Hkv;
     uint16_t* dst = nullptr;
@@ -143,52 +199,53 @@ __global__ void __launch_bounds__(kRopeThreads) tree_qkv_rope_kernel(const RopeP
       o0 = o1 = make_uint4(0, 0, 0, 0);
     } else if (!is_v) {
       const uint16_t* w = is_q ? p.q_norm : p.k_norm;
-      float x[8], y[8];
-      unpack8(a, x);
-      unpack8(c, y);
+      unsigned long long x[4], y[4];
+      unpack_pairs(a, x);
+      unpack_pairs(c, y);
       float r = 1.0f;
-      {
-        float ss = 0.0f;
+      if (w) {
+        unsigned long long s2 = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss = __fmaf_rn(x[i], x[i], __fmaf_rn(y[i], y[i], ss));
+        for (int i = 0; i < 4; ++i) s2 = fma2(x[i], x[i], fma2(y[i], y[i], s2));
+        float lo, hi;
+        f2unpack(s2, lo, hi);
+        float ss = lo + hi;
         // butterfly over the head's own lanes (other heads of the warp may be values)
 #pragma unroll
         for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(head_lanes, ss, o);
-        if (w) r = rsqrtf(ss * (1.0f / D) + p.eps);
-      }
-      if (w) {
-        float wx[8], wy[8];
-        unpack8(__ldg(reinterpret_cast<const uint4*>(w + c0 * 8)), wx);
-        unpack8(__ldg(reinterpret_cast<const uint4*>(w + c1 * 8)), wy);
+        r = rsqrtf(ss * (1.0f / D) + p.eps);
+        const unsigned long long r2 = f2pack(r, r);
+        if (is_q) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          x[i] = x[i] * r * wx[i];
-          y[i] = y[i] * r * wy[i];
+          for (int i = 0; i < 4; ++i) {
+            x[i] = mul2(x[i], mul2(r2, wq[i]));
+            y[i] = mul2(y[i], mul2(r2, wq[4 + i]));
+          }
+        } else {
+          unsigned long long t[4];
+          unpack_pairs(__ldg(reinterpret_cast<const uint4*>(w + c0 * 8)), t);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[i] = mul2(x[i], mul2(r2, t[i]));
+          unpack_pairs(__ldg(reinterpret_cast<const uint4*>(w + c1 * 8)), t);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) y[i] = mul2(y[i], mul2(r2, t[i]));
         }
       }
-      if constexpr (kVec) {
-        if (p.interleaved) {
+      if constexpr (kMode == kRopeHalves) {
+        if (turns) {
 #pragma unroll
-          for (int i = 0; i < 8; i += 2) {
-            const int ex = c0 * 8 + i, ey = c1 * 8 + i;
-            if (ex < p.rot) {
-              const float cs = s_cos[ex / 2], sn = s_sin[ex / 2], u = x[i], t = x[i + 1];
-              x[i] = u * cs - t * sn;
-              x[i + 1] = t * cs + u * sn;
-            }
-            if (ey < p.rot) {
-              const float cs = s_cos[ey / 2], sn = s_sin[ey / 2], u = y[i], t = y[i + 1];
-              y[i] = u * cs - t * sn;
-              y[i + 1] = t * cs + u * sn;
-            }
+          for (int i = 0; i < 4; ++i) {
+            const unsigned long long u = x[i];
+            x[i] = fma2(u, cs[i], mul2(y[i], sn[4 + i]));
+            y[i] = fma2(y[i], cs[i], mul2(u, sn[i]));
           }
-        } else if (sub < p.rot / 16) {
+        }
+      } else if constexpr (kMode == kRopePairs) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float cs = s_cos[c0 * 8 + i], sn = s_sin[c0 * 8 + i], u = x[i], t = y[i];
-            x[i] = u * cs - t * sn;
-            y[i] = t * cs + u * sn;
-          }
+        for (int i = 0; i < 8; ++i) {
+          unsigned long long& u = i < 4 ? x[i] : y[i - 4];
+          const unsigned long long t = fma2(u, cs[i], mul2(swap_pair(u), sn[i]));
+          if ((i < 4 ? c0 : c1) * 4 + (i & 3) < half) u = t;
         }
       } else {
         // halves that are not whole vectors: the partner read from memory
@@ -202,12 +259,15 @@ __global__ void __launch_bounds__(kRopeThreads) tree_qkv_rope_kernel(const RopeP
         };
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          x[i] = turned(c0 * 8 + i, x[i]);
-          y[i] = turned(c1 * 8 + i, y[i]);
+          unsigned long long& u = i < 4 ? x[i] : y[i - 4];
+          const int e = (i < 4 ? c0 : c1) * 8 + 2 * (i & 3);
+          float lo, hi;
+          f2unpack(u, lo, hi);
+          u = f2pack(turned(e, lo), turned(e + 1, hi));
         }
       }
-      o0 = pack8(x);
-      o1 = pack8(y);
+      o0 = pack_pairs(x);
+      o1 = pack_pairs(y);
     }
     if (dst) {
       *reinterpret_cast<uint4*>(dst + c0 * 8) = o0;
