@@ -337,7 +337,7 @@ SPEC_API spec_status_t spec_tree_qkv_rope(const void* qkv, const void* q_norm, c
  *   out        bf16 [B, N, Hq, D]
  *   lse        float [B, N, Hq] or NULL: ln sum_j exp(scale q . k_j)
  * N = 1 without a mask is plain decoding.  D is 64 or 128, Hq a multiple of
- * Hkv, G at most 128, N at most SPEC_ATTN_MAX_NODES; q, out, the caches and
+ * Hkv, G at most 128, N at most SPEC_ATTN_MAX_NODES, L at most 2^31 - 257; q, out, the caches and
  * prefixes 16-byte aligned, seq_stride a multiple of 16.  A sequence whose
  * tree does not fit the cache (base_len < 1 or base_len + N - 1 > L) gets out
  * = 0, lse = -inf and raises SPEC_FLAG_BAD_PATH.  Workspace: at least

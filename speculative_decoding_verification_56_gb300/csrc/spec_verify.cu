@@ -1142,7 +1142,7 @@ spec_status_t spec_tree_attention(const void* q, const void* k_cache, const void
                                   const int32_t* base_len, int B, int N, int Hq, int Hkv, int D,
                                   float scale, void* out, float* lse, void* workspace,
                                   size_t workspace_bytes, void* stream) {
-  if (!attn_shape_ok(B, N, Hq, Hkv, D, P) || L < 1 || !(scale > 0.0f) || !std::isfinite(scale))
+  if (!attn_shape_ok(B, N, Hq, Hkv, D, P) || L < 1 || L > INT32_MAX - 256 || !(scale > 0.0f) || !std::isfinite(scale))
     return SPEC_ERR_INVALID_ARG;
   if (seq_stride < (long long)L * Hkv * D * 2) return SPEC_ERR_INVALID_ARG;
   if (B == 0) return SPEC_OK;

@@ -473,17 +473,15 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           phase ^= 1u;
         }
       };
-      // scores of half w from the K tile in the current stage, query tile qt
-      auto scores = [&](int w, int qt) {
+      // scores of half w from the K tile in stage st, query tile qt
+      auto scores = [&](int w, int qt, int st) {
         const uint64_t a = qdesc + (uint64_t)(qt * kTile >> 4);
-        const uint64_t b = kdesc + (uint64_t)(stage * kTile >> 4);
+        const uint64_t b = kdesc + (uint64_t)(st * kTile >> 4);
 #pragma unroll
-        for (int c = 0; c < kSub; ++c)
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            const uint64_t o = (uint64_t)((c * kAtKeys * 128 + kk * 32) >> 4);
-            umma_ss(tmem + w * kAtKeys, a + o, b + o, id_qk, (c | kk) ? 1u : 0u);
-          }
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint64_t o = (uint64_t)((kk >> 2) * (kAtKeys * 128 >> 4) + (kk & 3) * 2);
+          umma_ss(tmem + w * kAtKeys, a + o, b + o, id_qk, kk ? 1u : 0u);
+        }
         umma_commit(&s_full[w]);
       };
       // output of half w from the V tile in stage st
@@ -492,7 +490,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
 #pragma unroll
         for (int kk = 0; kk < kAtKeys / 16; ++kk)
           umma_ts(tmem + 2 * kAtKeys + w * D, tmem + w * kAtKeys + kk * 8,
-                  b + (uint64_t)(kk * 2048 >> 4), id_pv, (!first || kk) ? 1u : 0u);
+                  b + (uint64_t)(kk * (2048 >> 4)), id_pv, (!first || kk) ? 1u : 0u);
       };
       while (ok) {
         const unsigned at = nq % kAtSegs;
@@ -501,29 +499,37 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         mbar_arrive(&seg_empty[at]);
         if (n == 0 || !wait(&q_full, nq++)) break;
         if (pair) {
+          // ring: K0, V0, K1, V1, ...; each tile is waited for as late as its use
+          // allows, and where the tensor cores have work
           if (!wait(&full[stage], phase)) break;
-          scores(0, 0);
-          scores(1, 1);
+          scores(0, 0, stage);
+          scores(1, 1, stage);
           if (n == 1) umma_commit(&q_empty);
           advance();
+          int vst = stage;
+          if (!wait(&full[stage], phase)) break;
+          advance();
+#pragma unroll 1
           for (int t = 0; t < n; ++t) {
-            const int vst = stage;
-            if (!wait(&full[stage], phase)) break;
-            advance();
             const bool more = t + 1 < n;
+            const int v = vst, k = stage;
             if (more && !wait(&full[stage], phase)) break;
             if (!wait(&p_full[0], np0++)) break;
-            output(0, vst, t == 0);
-            if (more)
-              scores(0, 0);
-            else
-              umma_commit(&o_full[0]);
-            if (!wait(&p_full[1], np1++)) break;
-            output(1, vst, t == 0);
+            output(0, v, t == 0);
             if (more) {
-              scores(1, 1);
-              if (t + 2 == n) umma_commit(&q_empty);
+              scores(0, 0, k);
               advance();
+              vst = stage;
+              if (!wait(&full[stage], phase)) break;
+              advance();
+            } else {
+              umma_commit(&o_full[0]);
+            }
+            if (!wait(&p_full[1], np1++)) break;
+            output(1, v, t == 0);
+            if (more) {
+              scores(1, 1, k);
+              if (t + 2 == n) umma_commit(&q_empty);
             } else {
               umma_commit(&o_full[1]);
             }
@@ -531,20 +537,20 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         } else {
           for (int t = 0; t < min(2, n); ++t) {
             if (!wait(&full[stage], phase)) break;
-            scores(t, 0);
+            scores(t, 0, stage);
             if (t + 1 == n) umma_commit(&q_empty);
             advance();
           }
+#pragma unroll 1
           for (int t = 0; ok && t < n; ++t) {
             const int w = t & 1, vst = stage;
             if (!wait(&full[stage], phase)) break;
             advance();
-            const bool more = t + 2 < n;
-            if (more && !wait(&full[stage], phase)) break;
             if (!wait(&p_full[w], w ? np1++ : np0++)) break;
             output(w, vst, t < 2);
-            if (more) {
-              scores(w, 0);
+            if (t + 2 < n) {
+              if (!wait(&full[stage], phase)) break;
+              scores(w, 0, stage);
               if (t + 3 == n) umma_commit(&q_empty);
               advance();
             } else {
