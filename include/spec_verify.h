@@ -236,8 +236,9 @@ SPEC_API spec_status_t spec_verify_tree_greedy(const void* target_logits, int dt
  *                                        last one is the new token), then -1
  *   out_probs     float [B, max_depth+1] their probabilities, then 0
  * so that spec_kv_commit_path takes accepted_len and path_nodes as they are.
- * Prefix sums are exact 64-bit integers of weights held to 2^-45 of the
- * largest.  A row without a finite logit draws nothing (token -1, probability
+ * Draws are decided by float32 sums with a bounded error and, next to a border
+ * C_j, by exact 64-bit integer sums of weights held to 2^-45 of the largest;
+ * out_probs is within 2e-5 of its value.  A row without a finite logit draws nothing (token -1, probability
  * 0, SPEC_FLAG_EMPTY_ROW) and ends the walk.  Malformed nodes are never taken
  * (SPEC_FLAG_BAD_PARENT, SPEC_FLAG_TOKEN_RANGE); SPEC_FLAG_DEPTH is set when
  * the walk would have gone below max_depth.  Only the rows on the walk are
@@ -294,7 +295,7 @@ SPEC_API spec_status_t spec_tree_attention_mask(const int32_t* parents, int B, i
  *   inv_freq      float [rot_dim / 2] (NULL when rot_dim = 0), finite
  *   rot_dim       even, 0..D;  interleaved: 0 pairs (i, i + rot_dim / 2),
  *                 else (2i, 2i + 1)
- *   pos_offset    >= 0 (the length of a prefix shared by the batch)
+ *   pos_offset    0..2^31 - 1 (the length of a prefix shared by the batch)
  *   base_len      int32 [B]; depth int32 [B, N] or NULL (a chain: node v at
  *                 depth v); a negative depth counts as 0 and raises
  *                 SPEC_FLAG_BAD_PARENT
@@ -340,8 +341,14 @@ SPEC_API spec_status_t spec_tree_qkv_rope(const void* qkv, const void* q_norm, c
  * Hkv, G at most 128, N at most SPEC_ATTN_MAX_NODES, L at most 2^31 - 257; q, out, the caches and
  * prefixes 16-byte aligned, seq_stride a multiple of 16.  A sequence whose
  * tree does not fit the cache (base_len < 1 or base_len + N - 1 > L) gets out
- * = 0, lse = -inf and raises SPEC_FLAG_BAD_PATH.  Workspace: at least
- * spec_tree_attention_workspace_bytes() bytes.
+ * = 0, lse = -inf and raises SPEC_FLAG_BAD_PATH.  A node that sees an entry
+ * whose value is not finite gets NaN.  Outputs must not overlap inputs.
+ * Two launches: the attention of equal runs of 128-entry tiles, one run per
+ * SM, on the tensor cores (weights rounded to bf16, sums in float32), which
+ * takes most of each SM's shared and tensor memory until it ends, and the join
+ * of items that were cut; the cut, and so the last bits, depend on base_len and
+ * the number of SMs alone.  Workspace: at least
+ * spec_tree_attention_workspace_bytes() bytes (the partials of cut items).
  */
 #define SPEC_ATTN_MAX_NODES 4096
 SPEC_API size_t spec_tree_attention_workspace_bytes(int B, int N, int Hq, int Hkv, int D, int P);

@@ -496,7 +496,7 @@ def spec_tree_qkv_rope(qkv, q_norm, k_norm, eps, inv_freq, base_len, depth, q_ou
     ``spec_tree_qkv_rope``).
 
     qkv bf16 [B, N, Hq + 2 Hkv, D]; q_norm, k_norm bf16 [D] or None; inv_freq
-    float32 [rot_dim / 2]; base_len int32 [B]; depth int32 [B, N] or None (a
+    float32 [rot_dim / 2] or None (no rotation); base_len int32 [B]; depth int32 [B, N] or None (a
     chain); q_out bf16 [B, N, Hq, D]; k_cache, v_cache bf16 [B, L, Hkv, D],
     written at positions base_len - 1 + node.
     """
@@ -511,7 +511,9 @@ def spec_tree_qkv_rope(qkv, q_norm, k_norm, eps, inv_freq, base_len, depth, q_ou
         _arg(qkv, "qkv", bf16, (B, N, H, D), dev),
         None if q_norm is None else _arg(q_norm, "q_norm", bf16, (D,), dev),
         None if k_norm is None else _arg(k_norm, "k_norm", bf16, (D,), dev), float(eps),
-        _arg(inv_freq, "inv_freq", torch.float32, (inv_freq.numel(),), dev), 2 * inv_freq.numel(),
+        None if inv_freq is None else _arg(inv_freq, "inv_freq", torch.float32,
+                                           (inv_freq.numel(),), dev),
+        0 if inv_freq is None else 2 * inv_freq.numel(),
         1 if interleaved else 0, int(pos_offset),
         _arg(base_len, "base_len", torch.int32, (B,), dev),
         None if depth is None else _arg(depth, "depth", torch.int32, (B, N), dev), B, N, Hq, Hkv,

@@ -517,7 +517,7 @@ spec_status_t noalloc_scratch(void** addr) {
   return SPEC_OK;
 }
 
-constexpr int kTsMaxSteps = 1024;  // of a warp, whose sums are held in shared memory
+constexpr int kTsMaxSteps = 2048;  // of a warp, whose sums are held in shared memory
 constexpr size_t kTsMaxSmem = (size_t)sv::kTsWarps * kTsMaxSteps * sizeof(unsigned long long);
 
 // Tree sampling: a cluster of CTAs per sequence (16 are more than the portable
@@ -607,7 +607,7 @@ spec_status_t run_rope(const sv::RopeParams& prm, int mode, int nodes, void* str
 
 bool attn_shape_ok(int B, int N, int Hq, int Hkv, int D, int P) {
   return B >= 0 && N >= 1 && N <= SPEC_ATTN_MAX_NODES && Hkv >= 1 && Hq >= Hkv && Hq <= 65536 &&
-         Hq % Hkv == 0 && Hq / Hkv <= 128 && (D == 64 || D == 128) && P >= 0 &&
+         Hq % Hkv == 0 && Hq / Hkv <= 128 && (D == 64 || D == 128) && P >= 0 && P <= INT32_MAX - 256 &&
          (long long)B * N <= INT32_MAX / 128 && (long long)B * N * Hq <= INT32_MAX;
 }
 
@@ -1066,11 +1066,12 @@ spec_status_t spec_verify_tree_sample(const void* target_logits, int dtype,
   prm.probs = out_probs;
   prm.flags = reinterpret_cast<unsigned*>(workspace);
   constexpr int kCtaStep = sv::kTsWarps * sv::kTsStep;  // elements of a CTA's step
-  int most = 1;  // CTAs per sequence
+  // CTAs per sequence: as many as keep all sequences resident (1216 CTAs of 256
+  // threads).  V = 128256 bf16, walks of 2.7 rows: B = 16 with 16 CTAs 26.8 us,
+  // with 8 30.9; B = 128 with 8 66.9, with 16 79.6; B = 256 with 4 99.8, with
+  // 16 141.
+  int most = 1;
   while (most < sv::kTsMaxCluster && 2 * most * B <= 1216) most *= 2;
-#ifdef TS_CLUSTER
-  most = TS_CLUSTER;
-#endif
   int cluster = 1;
   while (cluster < most && cluster * kCtaStep < V) cluster *= 2;
   while ((long long)cluster * kCtaStep * kTsMaxSteps < V) cluster *= 2;
@@ -1093,7 +1094,8 @@ spec_status_t spec_tree_qkv_rope(const void* qkv, const void* q_norm, const void
                                  void* workspace, size_t workspace_bytes, void* stream) {
   if (B < 0 || N < 1 || N > SPEC_MAX_TREE_NODES || Hq < 1 || Hkv < 1 || Hq > 65536 ||
       Hkv > 65536 || (D != 64 && D != 128) || L < 1 || rot_dim < 0 || rot_dim > D || rot_dim % 2 ||
-      pos_offset < 0 || !(eps >= 0.0f) || !std::isfinite(eps) ||
+      pos_offset < 0 ||
+      pos_offset > INT32_MAX || !(eps >= 0.0f) || !std::isfinite(eps) ||
       (long long)B * N > INT32_MAX)
     return SPEC_ERR_INVALID_ARG;
   if (seq_stride < (long long)L * Hkv * D * 2) return SPEC_ERR_INVALID_ARG;

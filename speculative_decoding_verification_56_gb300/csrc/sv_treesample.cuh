@@ -26,9 +26,9 @@
 // further than R / 2^15 from both of its borders.  The error of such sums is
 // bounded: 2^-22.4 of a weight from ex2.approx, 1.5 |r| 2^-24 ln 2 from its
 // argument r (its rounding and that of c), where the mean of |r| over the
-// row's mass is at most log2(V) + 1, and up to 13 float additions in a step, 37
-// over a warp's 1024 steps, 5 over the warps, 5 over the CTAs and 5 in the
-// search: together below 6e-6 R for V = 2^26, of t and of a border.  Otherwise
+// row's mass is at most log2(V) + 1, and up to 13 float additions in a step, 69
+// over a warp's 2048 steps, 5 over the warps, 5 over the CTAs and 5 in the
+// search: together below 8e-6 R for V = 2^26, of t and of a border.  Otherwise
 // (a draw among tokens of probability below 6e-5, for the most part) the row is
 // summed again exactly: weights as fixed-point 64-bit integers (2^-45 of the
 // largest, from a double-float evaluation of 2^x), whose sums depend on no

@@ -215,6 +215,11 @@ def test_attention(B, N, Hq, Hkv, D, base, P, chain):
     assert flags == 0
 
 
+def test_attention_cache_of_one_position():
+    check_attention(1, 1, 8, 4, 128, [1], L=1, chain=True)
+    check_attention(3, 2, 2, 2, 64, [1, 1, 1], L=2, chain=True)
+
+
 def test_attention_large_logits():
     # weights from 1 down to nothing: running maxima grow far over many tiles
     check_attention(2, 6, 8, 2, 128, [900, 411], spread=24.0, seed=9)
@@ -424,8 +429,8 @@ def check_sample(logits, host, tok, par, u, T, depth, dtype):
     for key in ("accepted_len", "path_nodes", "out_tokens"):
         assert (r[key].cpu().numpy() == o[key]).all(), key
     got = r["out_probs"].double().cpu().numpy()
-    # a weight and the total, each within 6e-6 of the total's float32 sum, and a rounding
-    assert (np.abs(got - o["out_probs"]) <= (2 * 6e-6 + F32) * o["out_probs"]).all()
+    # a weight and the total, each within 8e-6 of the total's float32 sum, and a rounding
+    assert (np.abs(got - o["out_probs"]) <= (2 * 8e-6 + F32) * o["out_probs"]).all()
     return o, sv.spec_verify_read_flags(ws)
 
 
@@ -434,7 +439,7 @@ def check_sample(logits, host, tok, par, u, T, depth, dtype):
     (4, 20, 1001, "bf16", 1.0), (4, 20, 1003, "f32", 0.75), (3, 33, 4096, "f32", 1.5),
     (3, 12, 32003, "bf16", 1.0), (2, 12, 40000, "bf16", 1.0), (2, 10, 128256, "bf16", 0.75),
     (2, 5, 151937, "f32", 1.0), (1, 2, 400000, "bf16", 1.0), (1, 2, 1100000, "bf16", 1.0),
-    (150, 6, 500, "f32", 1.0),
+    (150, 6, 500, "f32", 1.0), (2, 1500, 30, "f32", 1.0),
 ])
 def test_sample(B, N, V, dtype, T):
     c = tree_case(B, N, V, dtype, T=T, seed=B + N + V)
@@ -442,6 +447,15 @@ def test_sample(B, N, V, dtype, T):
     assert flags == 0
     if B >= 3 and N >= 8:
         assert 0 < o["accepted_len"].sum()
+
+
+def test_sample_largest_vocabulary():
+    V = 1 << 26
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    logits = randn(gen, 1, 1, V) * 3
+    one = np.zeros((1, 1), np.int32)
+    for u in (0.123, 0.987654):
+        check_sample(logits, bits(logits), one, one - 1, np.array([[u]], np.float32), 1.0, 0, "bf16")
 
 
 def test_sample_uniforms_at_the_ends():
@@ -700,6 +714,47 @@ def test_forward_on_a_side_stream_and_in_a_graph():
     step()
     torch.cuda.synchronize()
     assert (got == out).all() and not (got == want[1]).all()
+
+
+def test_two_streams_at_once():
+    """Calls that overlap on the GPU, each with a workspace of its own."""
+    gen = torch.Generator(device="cuda").manual_seed(11)
+    cases = []
+    for B, N, ctx, D in ((20, 30, 1500, 128), (7, 61, 900, 64)):
+        q, kc, vc = randn(gen, B, N, 8, D), randn(gen, B, ctx + N, 2, D), randn(gen, B, ctx + N, 2, D)
+        base = torch.randint(1, ctx, (B,), generator=gen, device="cuda", dtype=torch.int32)
+        z = randn(gen, B, N, 5000)
+        tok = torch.randint(0, 5000, (B, N), generator=gen, device="cuda", dtype=torch.int32)
+        par = torch.arange(-1, N - 1, device="cuda", dtype=torch.int32).expand(B, N).contiguous()
+        u = torch.rand(B, N, generator=gen, device="cuda")
+        cases.append((q, kc, vc, base, z, tok, par, u))
+
+    def run(c, stream=None):
+        q, kc, vc, base, z, tok, par, u = c
+        out, lse = sv.tree_attention(q, kc, vc, None, base, stream=stream)
+        r = sv.verify_tree_sample(z, tok, par, u, 1.0, u.shape[1] - 1, stream=stream)
+        return [out, lse, *r.values()]
+    want = [run(c) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    for _ in range(5):
+        got = [run(c, s) for c, s in zip(cases, streams)]
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            assert all(torch.equal(a, b) for a, b in zip(g, w))
+
+
+def test_empty_batches_are_no_ops():
+    kc = torch.zeros(0, 9, 2, 64, dtype=torch.bfloat16, device="cuda")
+    base = torch.zeros(0, dtype=torch.int32, device="cuda")
+    q = sv.tree_qkv_rope(torch.zeros(0, 3, 8, 64, dtype=torch.bfloat16, device="cuda"), None, None, 1e-6, None,
+                         base, None, kc, kc)
+    assert q.shape == (0, 3, 4, 64)
+    out, lse = sv.tree_attention(q, kc, kc, None, base)
+    assert out.shape == q.shape and lse.shape == (0, 3, 4)
+    i = torch.zeros(0, 3, dtype=torch.int32, device="cuda")
+    r = sv.verify_tree_sample(torch.zeros(0, 3, 50, device="cuda"), i, i, torch.zeros(0, 3, device="cuda"), 1.0, 2)
+    assert r["out_tokens"].shape == (0, 3)
 
 
 def test_wrappers_refuse_what_does_not_fit():

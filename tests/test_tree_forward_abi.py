@@ -1,0 +1,105 @@
+"""CPU checks of the tree's verification forward: workspace sizes and the host's
+refusals (every call below fails validation or is the B = 0 no-op, before any
+CUDA call), and the Python wrappers' refusals that need no GPU."""
+import pytest
+
+import speculative_decoding_verification_56_gb300 as sv
+from speculative_decoding_verification_56_gb300 import build
+
+FAKE = 0x10000          # 64 KiB-aligned fake device address, never dereferenced
+OK, INVALID, ALIGN, WORKSPACE = 0, 1, 2, 3
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build.build_library()
+    return sv.load_library()
+
+
+def caller(fn, **defaults):
+    def call(**over):
+        assert not set(over) - set(defaults)
+        return fn(*{**defaults, **over}.values())
+    return call
+
+
+def test_workspace_sizes(lib):
+    ws = sv.spec_verify_workspace_bytes
+    assert ws(sv.SPEC_MODE_TREE_SAMPLE, 16, 60, 128256, sv.SPEC_DTYPE_BF16) == 256
+    assert ws(sv.SPEC_MODE_TREE_QKV, 16, 60, 1, sv.SPEC_DTYPE_BF16) == 256
+    assert ws(sv.SPEC_MODE_TREE_SAMPLE, 16, 0, 10, 0) == 0
+    at = sv.spec_tree_attention_workspace_bytes
+    a, b = at(16, 60, 32, 8, 128), at(32, 60, 32, 8, 128)
+    assert 0 < a < b and a % 256 == 0
+    assert at(16, 60, 32, 8, 128, 8192) > a          # partials of the shared prefix
+    assert at(64, 1, 32, 8, 128) < 16 << 20           # decoding keeps few rows a slot
+    for bad in ((-1, 60, 32, 8, 128, 0), (1, 0, 32, 8, 128, 0), (1, 4097, 32, 8, 128, 0),
+                (1, 1, 30, 8, 128, 0), (1, 1, 8, 0, 128, 0), (1, 1, 129, 1, 128, 0),
+                (1, 1, 32, 8, 96, 0), (1, 1, 32, 8, 128, -1), (1 << 24, 4096, 32, 8, 128, 0)):
+        assert at(*bad) == 0, bad
+
+
+def test_tree_sample_validation(lib):
+    call = caller(lib.spec_verify_tree_sample, z=FAKE, dtype=1, tok=FAKE, par=FAKE, u=FAKE, T=1.0, B=2, N=8,
+                  V=100, md=4, n=FAKE, path=FAKE, out=FAKE, probs=FAKE, ws=FAKE, wsb=256, stream=None)
+    for over in (dict(dtype=2), dict(T=0.0), dict(T=-1.0), dict(T=float("nan")), dict(T=float("inf")),
+                 dict(B=-1), dict(N=0), dict(N=65537), dict(V=0), dict(V=(1 << 26) + 1), dict(md=-1),
+                 dict(md=1025), dict(B=1 << 28), dict(z=None), dict(tok=None), dict(par=None),
+                 dict(u=None), dict(n=None), dict(path=None), dict(out=None), dict(probs=None)):
+        assert call(**over) == INVALID, over
+    for over in (dict(z=FAKE + 1), dict(dtype=0, z=FAKE + 2), dict(tok=FAKE + 2), dict(u=FAKE + 1),
+                 dict(probs=FAKE + 2), dict(ws=FAKE + 16)):
+        assert call(**over) == ALIGN, over
+    assert call(ws=None) == WORKSPACE and call(wsb=255) == WORKSPACE
+    assert call(B=0, z=None, tok=None, ws=None, wsb=0) == OK
+
+
+def test_tree_qkv_validation(lib):
+    call = caller(lib.spec_tree_qkv_rope, qkv=FAKE, qn=FAKE, kn=None, eps=1e-6, freq=FAKE, rot=64, inter=0,
+                  off=0, base=FAKE, depth=None, B=2, N=8, Hq=8, Hkv=2, D=64, L=100, stride=100 * 2 * 64 * 2,
+                  q=FAKE, k=FAKE, v=FAKE, ws=FAKE, wsb=256, stream=None)
+    for over in (dict(B=-1), dict(N=0), dict(N=65537), dict(Hq=0), dict(Hkv=0), dict(D=96), dict(L=0),
+                 dict(rot=-2), dict(rot=66), dict(rot=7), dict(off=-1), dict(off=1 << 31), dict(eps=-1e-6),
+                 dict(eps=float("nan")), dict(stride=100 * 2 * 64 * 2 - 16), dict(B=1 << 20, N=65536),
+                 dict(qkv=None), dict(base=None), dict(q=None), dict(k=None), dict(v=None), dict(freq=None)):
+        assert call(**over) == INVALID, over
+    for over in (dict(qkv=FAKE + 8), dict(q=FAKE + 8), dict(k=FAKE + 4), dict(v=FAKE + 8), dict(qn=FAKE + 2),
+                 dict(kn=FAKE + 8), dict(stride=100 * 2 * 64 * 2 + 8), dict(base=FAKE + 1),
+                 dict(depth=FAKE + 2), dict(ws=FAKE + 16)):
+        assert call(**over) == ALIGN, over
+    assert call(ws=None) == WORKSPACE and call(wsb=255) == WORKSPACE
+    assert call(B=0, qkv=None, ws=None) == OK
+    assert call(rot=0, freq=None, wsb=16) == WORKSPACE   # no frequencies are needed then
+
+
+def test_tree_attention_validation(lib):
+    call = caller(lib.spec_tree_attention, q=FAKE, k=FAKE, v=FAKE, stride=100 * 2 * 64 * 2, L=100, pk=None,
+                  pv=None, P=0, mask=None, base=FAKE, B=2, N=8, Hq=8, Hkv=2, D=64, scale=0.125, out=FAKE,
+                  lse=None, ws=FAKE, wsb=1 << 30, stream=None)
+    for over in (dict(B=-1), dict(N=0), dict(N=4097), dict(Hq=7), dict(Hq=1), dict(Hkv=0), dict(D=32),
+                 dict(Hq=258), dict(L=0), dict(L=2 ** 31 - 100), dict(P=-1), dict(scale=0.0),
+                 dict(scale=-1.0), dict(scale=float("inf")), dict(scale=float("nan")),
+                 dict(stride=100 * 2 * 64 * 2 - 16), dict(P=5), dict(P=5, pk=FAKE), dict(q=None),
+                 dict(k=None), dict(v=None), dict(base=None), dict(out=None)):
+        assert call(**over) == INVALID, over
+    for over in (dict(q=FAKE + 8), dict(k=FAKE + 8), dict(v=FAKE + 2), dict(out=FAKE + 8),
+                 dict(stride=100 * 2 * 64 * 2 + 8), dict(P=5, pk=FAKE, pv=FAKE + 8), dict(mask=FAKE + 2),
+                 dict(base=FAKE + 2), dict(lse=FAKE + 1), dict(ws=FAKE + 16)):
+        assert call(**over) == ALIGN, over
+    need = sv.spec_tree_attention_workspace_bytes(2, 8, 8, 2, 64)
+    assert call(ws=None) == WORKSPACE and call(wsb=need - 1) == WORKSPACE
+    assert call(B=0, q=None, ws=None, wsb=0) == OK
+
+
+def test_wrappers_refuse_host_tensors():
+    torch = pytest.importorskip("torch")
+    z = torch.zeros(1, 2, 8)
+    i = torch.zeros(1, 2, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        sv.spec_verify_tree_sample(z, i, i, torch.zeros(1, 3), 1.0, 2, i, i, i, z, i)
+    q = torch.zeros(1, 2, 4, 64, dtype=torch.bfloat16)
+    kc = torch.zeros(1, 9, 2, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        sv.spec_tree_attention(q, kc, kc, None, i[0], 1.0, q, None, i)
+    with pytest.raises(ValueError):
+        sv.spec_tree_qkv_rope(q, None, None, 1e-6, z, i, None, q, kc, kc, i)
