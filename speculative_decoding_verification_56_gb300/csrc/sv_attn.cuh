@@ -939,25 +939,35 @@ __global__ void __launch_bounds__(kAtFinThreads) tree_attn_finish_kernel(const A
                                         ((long long)b * p.mg_o + mg) * p.Hkv + h;
       const int2 span = p.span[it];
       if (p.tiles_s == 0 && span.x == span.y) return;  // written by its only CTA
-#pragma unroll 2
-      for (int c = span.x; c <= span.y; ++c) {
-        const long long slot = it + c;
-        const float2 x = p.ml[slot * p.slot_rows + row];
-        const float4* o = reinterpret_cast<const float4*>(p.opart + slot * (long long)p.slot_rows * D) +
-                          part * 4 * p.slot_rows + row;
-        float4 y[4];
+      const float* base = p.opart + (size_t)part * 16 * p.slot_rows + (size_t)row * 4;
+      for (int c = span.x; c <= span.y; c += 4) {
+        float2 x[4];
+        float4 y[4][4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) y[j] = o[j * p.slot_rows];
-        const float mn = fmaxf(m, x.x);
-        const float fa = ex2(m - mn), fb = ex2(x.x - mn);
-        m = mn;
-        l = l * fa + x.y * fb;
+        for (int i = 0; i < 4; ++i) {
+          if (c + i <= span.y) {
+            const size_t slot = (size_t)(it + c + i) * p.slot_rows;
+            x[i] = p.ml[slot + row];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          acc[4 * j] = acc[4 * j] * fa + y[j].x * fb;
-          acc[4 * j + 1] = acc[4 * j + 1] * fa + y[j].y * fb;
-          acc[4 * j + 2] = acc[4 * j + 2] * fa + y[j].z * fb;
-          acc[4 * j + 3] = acc[4 * j + 3] * fa + y[j].w * fb;
+            for (int j = 0; j < 4; ++j)
+              y[i][j] = *reinterpret_cast<const float4*>(base + slot * D + (size_t)j * 4 * p.slot_rows);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (c + i <= span.y) {
+            const float mn = fmaxf(m, x[i].x);
+            const float fa = ex2(m - mn), fb = ex2(x[i].x - mn);
+            m = mn;
+            l = l * fa + x[i].y * fb;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              acc[4 * j] = acc[4 * j] * fa + y[i][j].x * fb;
+              acc[4 * j + 1] = acc[4 * j + 1] * fa + y[i][j].y * fb;
+              acc[4 * j + 2] = acc[4 * j + 2] * fa + y[i][j].z * fb;
+              acc[4 * j + 3] = acc[4 * j + 3] * fa + y[i][j].w * fb;
+            }
+          }
         }
       }
     }
