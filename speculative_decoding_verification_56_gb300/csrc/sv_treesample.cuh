@@ -238,6 +238,13 @@ struct TsPart {
   float fsum;              // screened: of weights relative to 2^ref
 };
 
+// All threads of the cluster.  The aligned barrier wants whole warps, so lanes
+// that took different ways come together first.
+__device__ __forceinline__ void ts_cluster_sync() {
+  __syncwarp();
+  cluster_sync_all();
+}
+
 __device__ __forceinline__ void cluster_st64(uint32_t at, unsigned long long x) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(at), "l"(x) : "memory");
 }
@@ -308,6 +315,7 @@ __global__ void __launch_bounds__(kTsThreads, 4) tree_sample_kernel(const TreeSa
     tab_i[threadIdx.x] = kTsPow[threadIdx.x];
     tab_f[threadIdx.x] = kTsPowF[threadIdx.x];
   }
+  ts_cluster_sync();  // every CTA runs before its shared memory is written to
   // a programmatic dependent of the kernel before it in the stream: nothing
   // of global memory is touched before that grid has finished
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -353,7 +361,7 @@ __global__ void __launch_bounds__(kTsThreads, 4) tree_sample_kernel(const TreeSa
         cluster_st32(at + 8, (uint32_t)top);
       }
     }
-    cluster_sync_all();
+    ts_cluster_sync();
     const TsPart part = lane < (int)C ? s_part[meet & 1][lane] : TsPart{0ull, kRefEmpty, 0.0f};
     gref = __reduce_max_sync(0xffffffffu, part.ref);
     const unsigned long long y = ts_shift(part.sum, gref - part.ref);
@@ -437,7 +445,7 @@ __global__ void __launch_bounds__(kTsThreads, 4) tree_sample_kernel(const TreeSa
           cluster_st64(cluster_addr(&s_part[meet & 1][rank].ref, lane),
                        (unsigned long long)__float_as_uint(sum) << 32 | (uint32_t)top);
       }
-      cluster_sync_all();
+      ts_cluster_sync();
       const TsPart part = lane < (int)C ? s_part[meet & 1][lane] : TsPart{0ull, kRefEmpty, 0.0f};
       gref = __reduce_max_sync(0xffffffffu, part.ref);
       const float y = part.fsum * ts_pow2(part.ref - gref);
@@ -496,7 +504,7 @@ __global__ void __launch_bounds__(kTsThreads, 4) tree_sample_kernel(const TreeSa
     int x = owner;
     float prob = 0.0f;
     if (owner >= 0) {
-      cluster_sync_all();
+      ts_cluster_sync();
       x = s_tok[meet & 1];
       prob = s_prob[meet & 1];
     }
@@ -560,7 +568,7 @@ __global__ void __launch_bounds__(kTsThreads, 4) tree_sample_kernel(const TreeSa
         tell(max(at, 0), (int)(w0 + (long long)s * kTsStep) + e0,
              mant / (float)R * pow2i_f(min(n + ref - gref - p.extra, 0)));
       }
-      cluster_sync_all();
+      ts_cluster_sync();
       x = owner < 0 ? kTsNone : s_tok[meet & 1];
       prob = owner < 0 ? 0.0f : s_prob[meet & 1];
       ++meet;
