@@ -238,8 +238,9 @@ SPEC_API spec_status_t spec_verify_tree_greedy(const void* target_logits, int dt
  * so that spec_kv_commit_path takes accepted_len and path_nodes as they are.
  * Draws are decided by float32 sums with a bounded error and, next to a border
  * C_j, by exact 64-bit integer sums of weights held to 2^-45 of the largest;
- * out_probs is within 2e-5 of its value.  A row without a finite logit draws nothing (token -1, probability
- * 0, SPEC_FLAG_EMPTY_ROW) and ends the walk.  Malformed nodes are never taken
+ * out_probs is within 2e-5 of its value.  A row without a finite logit draws
+ * nothing (token -1, probability 0, SPEC_FLAG_EMPTY_ROW) and ends the walk.
+ * Malformed nodes are never taken
  * (SPEC_FLAG_BAD_PARENT, SPEC_FLAG_TOKEN_RANGE); SPEC_FLAG_DEPTH is set when
  * the walk would have gone below max_depth.  Only the rows on the walk are
  * read.  One launch of a cluster of up to 16 CTAs per sequence.  Workspace:
@@ -287,7 +288,8 @@ SPEC_API spec_status_t spec_tree_attention_mask(const int32_t* parents, int B, i
  *   y = x / sqrt(mean(x^2) + eps) * w   (a null w: no norm),
  * and their first rot_dim elements rotated in pairs by position * inv_freq[i],
  *   (a, b) -> (a cos - b sin, b cos + a sin),
- * in float32 (positions and angles exactly), rounded once.  Queries go to
+ * in float32, rounded once (angles are reduced to one turn in 64-bit integers:
+ * at position 2^31 they are off by less than 1e-5 of a turn).  Queries go to
  * q_out; keys and values go to cache position base_len[b] - 1 + v, where
  * spec_kv_commit_path expects them.
  *   qkv           bf16 [B, N, Hq + 2 Hkv, D]: query, key, value heads
@@ -334,12 +336,13 @@ SPEC_API spec_status_t spec_tree_qkv_rope(const void* qkv, const void* q_norm, c
  *   k_cache, v_cache bf16, layout as in spec_tree_qkv_rope
  *   prefix_k, prefix_v bf16 [P, Hkv, D] (NULL when P = 0)
  *   mask       uint32 [B, N, ceil(N/32)] or NULL
- *   base_len   int32 [B]; scale > 0, finite
+ *   base_len   int32 [B]; scale > 0, below 2^127, scores |scale q . k| below 2^24
  *   out        bf16 [B, N, Hq, D]
  *   lse        float [B, N, Hq] or NULL: ln sum_j exp(scale q . k_j)
  * N = 1 without a mask is plain decoding.  D is 64 or 128, Hq a multiple of
- * Hkv, G at most 128, N at most SPEC_ATTN_MAX_NODES, L at most 2^31 - 257; q, out, the caches and
- * prefixes 16-byte aligned, seq_stride a multiple of 16.  A sequence whose
+ * Hkv, G at most 128, N at most SPEC_ATTN_MAX_NODES, L and P at most
+ * 2^31 - 257; q, out, the caches and prefixes 16-byte aligned, seq_stride a
+ * multiple of 16.  A sequence whose
  * tree does not fit the cache (base_len < 1 or base_len + N - 1 > L) gets out
  * = 0, lse = -inf and raises SPEC_FLAG_BAD_PATH.  A node that sees an entry
  * whose value is not finite gets NaN.  Outputs must not overlap inputs.

@@ -696,10 +696,24 @@ def tree_grow(draft_logits, temperature, M, workspace=None, stream=None):
     return out
 
 
+def _allocating_on(stream, device):
+    """Context in which what a convenience allocates belongs to the stream that
+    its call runs on: the allocator then hands a workspace that goes out of use
+    to that stream's later work only."""
+    cuda = _torch().cuda
+    if isinstance(stream, int):
+        stream = cuda.ExternalStream(stream, device=device) if stream else cuda.default_stream(device)
+    return cuda.stream(stream)
+
+
 def verify_tree_sample(target_logits, node_tokens, parents, u_sample, temperature, max_depth,
                        workspace=None, stream=None):
     """Sampling verification of B draft trees; returns dict(accepted_len,
     path_nodes, out_tokens, out_probs)."""
+    if stream is not None:
+        with _allocating_on(stream, target_logits.device):
+            return verify_tree_sample(target_logits, node_tokens, parents, u_sample, temperature,
+                                      max_depth, workspace)
     torch = _torch()
     B, N, V = target_logits.shape
     dev = target_logits.device
@@ -721,6 +735,10 @@ def tree_qkv_rope(qkv, q_norm, k_norm, eps, inv_freq, base_len, depth, k_cache, 
                   pos_offset=0, interleaved=False, workspace=None, stream=None):
     """Normalise and rotate the tree's query and key heads and write its keys
     and values into the cache; returns the queries [B, N, Hq, D]."""
+    if stream is not None:
+        with _allocating_on(stream, qkv.device):
+            return tree_qkv_rope(qkv, q_norm, k_norm, eps, inv_freq, base_len, depth, k_cache,
+                                 v_cache, pos_offset, interleaved, workspace)
     torch = _torch()
     B, N, H, D = qkv.shape
     if workspace is None:
@@ -750,6 +768,10 @@ def tree_attention(q, k_cache, v_cache, mask, base_len, scale=None, prefix_k=Non
     """Attention of the tree's nodes over a shared prefix, the cached positions
     and their ancestors; returns ``(out, lse)``.  ``scale`` defaults to
     1 / sqrt(D)."""
+    if stream is not None:
+        with _allocating_on(stream, q.device):
+            return tree_attention(q, k_cache, v_cache, mask, base_len, scale, prefix_k, prefix_v,
+                                  workspace)
     torch = _torch()
     if workspace is None:
         workspace = alloc_tree_attention_workspace(q, k_cache, prefix_k)

@@ -1094,8 +1094,7 @@ spec_status_t spec_tree_qkv_rope(const void* qkv, const void* q_norm, const void
                                  void* workspace, size_t workspace_bytes, void* stream) {
   if (B < 0 || N < 1 || N > SPEC_MAX_TREE_NODES || Hq < 1 || Hkv < 1 || Hq > 65536 ||
       Hkv > 65536 || (D != 64 && D != 128) || L < 1 || rot_dim < 0 || rot_dim > D || rot_dim % 2 ||
-      pos_offset < 0 ||
-      pos_offset > INT32_MAX || !(eps >= 0.0f) || !std::isfinite(eps) ||
+      pos_offset < 0 || pos_offset > INT32_MAX || !(eps >= 0.0f) || !std::isfinite(eps) ||
       (long long)B * N > INT32_MAX)
     return SPEC_ERR_INVALID_ARG;
   if (seq_stride < (long long)L * Hkv * D * 2) return SPEC_ERR_INVALID_ARG;
@@ -1144,7 +1143,8 @@ spec_status_t spec_tree_attention(const void* q, const void* k_cache, const void
                                   const int32_t* base_len, int B, int N, int Hq, int Hkv, int D,
                                   float scale, void* out, float* lse, void* workspace,
                                   size_t workspace_bytes, void* stream) {
-  if (!attn_shape_ok(B, N, Hq, Hkv, D, P) || L < 1 || L > INT32_MAX - 256 || !(scale > 0.0f) || !std::isfinite(scale))
+  if (!attn_shape_ok(B, N, Hq, Hkv, D, P) || L < 1 || L > INT32_MAX - 256 || !(scale > 0.0f) ||
+      !(scale < 1.7014118e38f))  // 2^127: scale * log2(e) stays finite
     return SPEC_ERR_INVALID_ARG;
   if (seq_stride < (long long)L * Hkv * D * 2) return SPEC_ERR_INVALID_ARG;
   if (B == 0) return SPEC_OK;

@@ -30,7 +30,7 @@ namespace sv {
 
 constexpr int kAtRows = 128;     // rows of a half (UMMA M, tensor-memory lanes)
 constexpr int kAtKeys = 128;     // cache entries per tile
-constexpr int kAtThreads = 384;  // producer, MMA issuer, 2 idle warps, 2 x 4 softmax warps
+constexpr int kAtThreads = 384;  // copies, MMAs, segments, an idle warp, 2 x 4 softmax warps
 constexpr int kAtMaxStages = 13;
 constexpr int kAtMaxCtas = 160;  // partial slots are laid out for at most this many CTAs
 constexpr float kAtLazy = 4096.0f;  // a tile's largest sum of a row's weights before its
@@ -937,8 +937,11 @@ __global__ void __launch_bounds__(kAtFinThreads) tree_attn_finish_kernel(const A
       const long long it = k == 0 ? mg * p.Hkv + h
                                   : (long long)p.Hkv * p.mg_s +
                                         ((long long)b * p.mg_o + mg) * p.Hkv + h;
-      const int2 span = p.span[it];
+      int2 span = p.span[it];
       if (p.tiles_s == 0 && span.x == span.y) return;  // written by its only CTA
+      // slots of the workspace, whatever an overlapping call made of the span
+      span.x = max(span.x, 0);
+      span.y = min(span.y, p.nctas - 1);
       const float* base = p.opart + (size_t)part * 16 * p.slot_rows + (size_t)row * 4;
       for (int c = span.x; c <= span.y; c += 4) {
         float2 x[4];

@@ -65,8 +65,9 @@ __device__ __forceinline__ void turn_sincos(long long pos, float f, float* sn, f
   const float hi = __fmul_rn(f, inv2pi_hi);
   const float lo = __fmaf_rn(f, inv2pi_lo, __fmaf_rn(f, inv2pi_hi, -hi));
   const float frac = hi - floorf(hi);  // exact; in [0, 1)
+  const float rest = lo - rintf(lo);   // exact; whole turns only past 2^23
   const unsigned long long step = __float2ull_rn(frac * 18446744073709551616.0f) +
-                                  (unsigned long long)__float2ll_rn(lo * 18446744073709551616.0f);
+                                  (unsigned long long)__float2ll_rn(rest * 18446744073709551616.0f);
   const unsigned long long turns = step * (unsigned long long)pos;
   const float t = (float)(int)(turns >> 32) * 2.3283064365386963e-10f;  // [-1/2, 1/2] turns
   sincospif(2.0f * t, sn, cs);

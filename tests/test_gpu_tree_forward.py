@@ -783,3 +783,72 @@ def test_wrappers_refuse_what_does_not_fit():
         sv.verify_tree_sample(z, i.long(), i, torch.zeros(2, 4, device="cuda"), 1.0, 3)
     with pytest.raises(ValueError):
         sv.verify_tree_sample(z, i, i.cpu(), torch.zeros(2, 4, device="cuda"), 1.0, 3)
+
+
+def test_qkv_frequencies_of_many_turns():
+    # more than 2^23 turns a position: the float below the product's first one
+    # holds whole turns too.  At position 1 the angle is off by 2^-47 of it
+    # (8e7 turns: 6e-7 of a turn, 4e-6), far below the roundings counted here
+    N, D = 2, 64
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    qkv = randn(gen, 1, N, 3, D)
+    inv = torch.linspace(6e7, 5e8, D // 2)
+    kc, vc = randn(gen, 1, 9, 1, D), randn(gen, 1, 9, 1, D)
+    base = np.array([1], np.int32)
+    q = sv.tree_qkv_rope(qkv, None, None, 1e-6, inv.cuda(), torch.from_numpy(base).cuda(), None, kc,
+                         vc)
+    torch.cuda.synchronize()
+    qo, ko, _ = oracle.tree_qkv(bits(qkv), None, None, np.float32(1e-6), inv.numpy(), base, None, 1, 9)
+    pair = 2 * float(qkv.float().abs().max())
+    eps = (4e-6 + 2.0 ** -20) * pair
+    assert (np.abs(q.double().cpu().numpy() - qo) <= BF16 * np.abs(qo) + eps).all()
+    kn = kc.double().cpu().numpy()[:, :N]
+    assert (np.abs(kn - ko[:, :N]) <= BF16 * np.abs(ko[:, :N]) + eps).all()
+
+
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("N,ctx", [(1, 5), (1, 700), (40, 300)])
+def test_attention_scores_far_from_zero(N, ctx, sign):
+    # every score is +-2^23 (64 products of 2^17): equal weights, so the output
+    # is the mean of V, and the log-sum the score plus ln of their number
+    D, Hkv, Hq = 64, 2, 4
+    gen = torch.Generator(device="cuda").manual_seed(ctx)
+    q = torch.full((1, N, Hq, D), 2.0 ** 8, dtype=torch.bfloat16, device="cuda")
+    kc = torch.full((1, ctx + N, Hkv, D), sign * 2.0 ** 9, dtype=torch.bfloat16, device="cuda")
+    vc = randn(gen, 1, ctx + N, Hkv, D)
+    base = torch.tensor([ctx + 1], dtype=torch.int32, device="cuda")
+    out, lse = sv.tree_attention(q, kc, vc, None, base, scale=1.0)
+    torch.cuda.synchronize()
+    v = vc.double().cpu().numpy()[0]
+    for n in range(N):
+        seen = v[: ctx + 1 + n]
+        mean = seen.mean(axis=0).repeat(Hq // Hkv, axis=0)
+        mag = np.abs(seen).mean(axis=0).repeat(Hq // Hkv, axis=0)
+        got = out[0, n].double().cpu().numpy()
+        # a weight rounds to bf16 (all of them alike, 2^-8 of it), the output
+        # once more; float32 sums of ctx + N terms
+        tol = BF16 * (np.abs(mean) + mag) * (1 + 2.0 ** -6) + 2 * (ctx + N) * F32 * mag
+        assert (np.abs(got - mean) <= tol).all()
+        # the reference, its sum with log2 and the product with ln 2 round
+        want = sign * 2.0 ** 23 + np.log(len(seen))
+        assert (np.abs(lse[0, n].double().cpu().numpy() - want) <= 4 * F32 * 2.0 ** 23).all()
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_conveniences_allocate_on_the_stream_of_the_call(raw):
+    """A workspace that goes out of use when its call returns is not handed to
+    another stream while the call is still to run."""
+    gen = torch.Generator(device="cuda").manual_seed(12)
+    B, N, ctx = 3, 20, 1500
+    q, kc, vc = randn(gen, B, N, 8, 64), randn(gen, B, ctx + N, 2, 64), randn(gen, B, ctx + N, 2, 64)
+    base = torch.tensor([ctx, 3, 900], dtype=torch.int32, device="cuda")
+    want, want_lse = sv.tree_attention(q, kc, vc, None, base)
+    nbytes = sv.spec_tree_attention_workspace_bytes(B, N, 8, 2, 64)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)  # about 10 ms
+    out, lse = sv.tree_attention(q, kc, vc, None, base, stream=side.cuda_stream if raw else side)
+    held = [torch.full((nbytes,), 0x7F, dtype=torch.uint8, device="cuda") for _ in range(3)]
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and torch.equal(lse, want_lse) and len(held) == 3

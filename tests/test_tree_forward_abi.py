@@ -103,3 +103,12 @@ def test_wrappers_refuse_host_tensors():
         sv.spec_tree_attention(q, kc, kc, None, i[0], 1.0, q, None, i)
     with pytest.raises(ValueError):
         sv.spec_tree_qkv_rope(q, None, None, 1e-6, z, i, None, q, kc, kc, i)
+
+
+def test_tree_attention_scale_stays_finite(lib):
+    call = caller(lib.spec_tree_attention, q=FAKE, k=FAKE, v=FAKE, stride=100 * 2 * 64 * 2, L=100, pk=None,
+                  pv=None, P=0, mask=None, base=FAKE, B=2, N=8, Hq=8, Hkv=2, D=64, scale=0.125, out=FAKE,
+                  lse=None, ws=FAKE, wsb=0, stream=None)
+    assert call(scale=2.0 ** 127) == INVALID and call(scale=3e38) == INVALID
+    assert call(scale=float("inf")) == INVALID and call(scale=float("nan")) == INVALID
+    assert call(scale=1.5 * 2.0 ** 126) == WORKSPACE and call(scale=1e-45) == WORKSPACE
