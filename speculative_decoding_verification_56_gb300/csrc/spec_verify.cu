@@ -538,7 +538,10 @@ struct AttnPlan {
 
 // Rows of an item: the G query heads of `tok` nodes fill one 128-row half;
 // an item with more nodes takes two halves, with fewer one (both halves of
-// the kernel then share it by alternate tiles).
+// the kernel then share it by alternate tiles).  Items of one half throughout:
+// 79.6 us instead of 69.4 (16 trees of 60), 181 instead of 133 (65536 cached),
+// 254 instead of 184 (a shared prefix); two halves throughout: decoding 154.8
+// instead of 136.3 us.
 AttnPlan attn_plan(int B, int N, int Hq, int Hkv, int D, int P) {
   AttnPlan a;
   const int G = Hq / Hkv;
@@ -589,8 +592,16 @@ spec_status_t run_attention(const sv::AttnParams& prm, const CUtensorMap (&map)[
   g_launches.fetch_add(1, std::memory_order_relaxed);
   const long long rows = (long long)prm.B * prm.N * prm.Hq;
   const long long blocks = (rows + sv::kAtFinThreads - 1) / sv::kAtFinThreads;
-  return launch(sv::tree_attn_finish_kernel<D>, (int)(blocks * (D / 16)), 0, prm, stream, true, 1,
-                sv::kAtFinThreads);
+  // Parts of an item: about 1 + CTAs / items.  Many (3 sequences of 65536, 24
+  // items): 8 elements a thread of 8 parts at once 132 us, 16 of 4 134, 16 of 2
+  // 137; few (16 trees of 60, 128 items): 16 of 2 68.5 us, 16 of 4 69.9, 8 of 8
+  // 74.9; a shared prefix (640 items) 181, 183.5 and 194.
+  const long long items = (long long)prm.Hkv * (prm.mg_s + (long long)prm.B * prm.mg_o);
+  if (2 * items >= prm.nctas)
+    return launch(sv::tree_attn_finish_kernel<D, 16, 2>, (int)(blocks * (D / 16)), 0, prm, stream,
+                  true, 1, sv::kAtFinThreads);
+  return launch(sv::tree_attn_finish_kernel<D, 8, 8>, (int)(blocks * (D / 8)), 0, prm, stream, true,
+                1, sv::kAtFinThreads);
 }
 
 template <int D>
@@ -1066,18 +1077,28 @@ spec_status_t spec_verify_tree_sample(const void* target_logits, int dtype,
   prm.probs = out_probs;
   prm.flags = reinterpret_cast<unsigned*>(workspace);
   constexpr int kCtaStep = sv::kTsWarps * sv::kTsStep;  // elements of a CTA's step
-  // CTAs per sequence: as many as keep all sequences resident (1216 CTAs of 256
-  // threads).  V = 128256 bf16, walks of 2.7 rows: B = 16 with 16 CTAs 26.8 us,
-  // with 8 30.9; B = 128 with 8 66.9, with 16 79.6; B = 256 with 4 99.8, with
-  // 16 141.
+  // CTAs per sequence.  608 CTAs are resident (four on an SM); clusters beyond
+  // that start as others end, which pays where rows are long.  Measured with 4,
+  // 8 and 16 CTAs: V = 32000 bf16, B = 40 24.2, 22.1, 22.0 us; 56 26.5, 24.1,
+  // 27.7; 112 26.5, 33.6, 50.2; V = 128256 bf16, B = 24 35.6, 23.9, 21.1; 40
+  // 53.1, 34.7, 29.6; 80 64.8, 45.7, 52.3; 112 70.2, 57.3, 70.9; 250 101, 102,
+  // 138; V = 151936 float32, B = 40 80.7, 55.4, 40.9; 112 87.2, 71.8, 84.3; and 2
+  // CTAs at B = 250 44.6, 127 and 170 us against 39.8, 101 and 131 with 4.
+  const long long row_bytes = (long long)V * elem_bytes(dtype);
   int most = 1;
-  while (most < sv::kTsMaxCluster && 2 * most * B <= 1216) most *= 2;
+  while (most < sv::kTsMaxCluster) {
+    const long long beyond = most < 4 ? 608 : row_bytes * (most == 4 ? 12 : 4) / 5120;
+    if (2ll * most * B > 608 + std::min(beyond, 608ll)) break;
+    most *= 2;
+  }
   int cluster = 1;
   while (cluster < most && cluster * kCtaStep < V) cluster *= 2;
   while ((long long)cluster * kCtaStep * kTsMaxSteps < V) cluster *= 2;
   prm.nsteps = (V + cluster * kCtaStep - 1) / (cluster * kCtaStep);
   const size_t smem = (size_t)sv::kTsWarps * prm.nsteps * sizeof(unsigned long long);
-  // 16-byte loads: whole groups of 8 elements at 16-byte boundaries
+  // 16-byte loads: whole groups of 8 elements at 16-byte boundaries (element by
+  // element 15.5 us become 18.1 at one stream of V = 128256 bf16, 62.0 become
+  // 78.4 at 64 of V = 151936 float32)
   const bool vec = aligned(target_logits, 16) && V % 8 == 0;
   if (dtype == SPEC_DTYPE_BF16)
     return vec ? launch_tree_sample<sv::tree_sample_kernel<sv::BF16, true>>(prm, B, cluster, smem, stream)
@@ -1128,6 +1149,9 @@ spec_status_t spec_tree_qkv_rope(const void* qkv, const void* q_norm, const void
   prm.L = L;
   prm.rot = rot_dim;
   prm.interleaved = interleaved != 0;
+  // an element's partner in the thread's registers where the halves are whole
+  // vectors (128 trees of 60, D = 128: 34.8 us; 100.8 with the partner read from
+  // memory, as other rotations have to)
   const int mode = interleaved ? sv::kRopePairs : rot_dim % 16 == 0 ? sv::kRopeHalves : sv::kRopeOdd;
   return D == 128 ? run_rope<128>(prm, mode, B * N, stream) : run_rope<64>(prm, mode, B * N, stream);
 }

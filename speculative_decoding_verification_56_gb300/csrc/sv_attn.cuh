@@ -907,16 +907,19 @@ __global__ void __launch_bounds__(kAtThreads, 1)
 }
 
 // Joins the partials of items that several CTAs share or that have a shared
-// prefix; other rows are done.  A thread takes 16 elements of a row (a node's
+// prefix; other rows are done.  A thread takes E elements of a row (a node's
 // query head), neighbouring lanes neighbouring rows of a key-value head, as
-// the partials lie.
-template <int D>
-__global__ void __launch_bounds__(kAtFinThreads) tree_attn_finish_kernel(const AttnParams p) {
+// the partials lie, and reads A partials at once: the kernel is a chain of
+// loads (lengths, span, partials), and what counts is how few times a thread
+// waits (few items in many parts) or how many threads are resident (many items).
+template <int D, int E, int A>
+__global__ void __launch_bounds__(kAtFinThreads, E * A <= 32 ? 3 : 2)
+    tree_attn_finish_kernel(const AttnParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
   const unsigned rows = (unsigned)p.B * p.N * p.Hq;  // at most 2^31
   const unsigned blocks = (rows + kAtFinThreads - 1) / kAtFinThreads;
-  const unsigned part = blockIdx.x / blocks;  // 16 elements: part < D / 16
+  const unsigned part = blockIdx.x / blocks;  // E elements: part < D / E
   const unsigned at = (blockIdx.x - part * blocks) * kAtFinThreads + threadIdx.x;
   if (at >= rows) return;
   // row = ((b Hkv + h) N + n) G + g
@@ -924,9 +927,9 @@ __global__ void __launch_bounds__(kAtFinThreads) tree_attn_finish_kernel(const A
   const int n = (int)(in_bh / p.G), g = (int)(in_bh - (unsigned)n * p.G);
   const int b = (int)(bh / p.Hkv), h = (int)(bh - (unsigned)b * p.Hkv);
   const bool ok = attn_seq_ok(p, __ldg(p.base_len + b));
-  float m = -1e30f, l = 0.0f, acc[16];
+  float m = -1e30f, l = 0.0f, acc[E];
 #pragma unroll
-  for (int e = 0; e < 16; ++e) acc[e] = 0.0f;
+  for (int e = 0; e < E; ++e) acc[e] = 0.0f;
   if (ok) {
 #pragma unroll 1
     for (int k = p.tiles_s == 0 ? 1 : 0; k < 2; ++k) {  // shared prefix, own entries
@@ -942,29 +945,29 @@ __global__ void __launch_bounds__(kAtFinThreads) tree_attn_finish_kernel(const A
       // slots of the workspace, whatever an overlapping call made of the span
       span.x = max(span.x, 0);
       span.y = min(span.y, p.nctas - 1);
-      const float* base = p.opart + (size_t)part * 16 * p.slot_rows + (size_t)row * 4;
-      for (int c = span.x; c <= span.y; c += 4) {
-        float2 x[4];
-        float4 y[4][4];
+      const float* base = p.opart + (size_t)part * E * p.slot_rows + (size_t)row * 4;
+      for (int c = span.x; c <= span.y; c += A) {
+        float2 x[A];
+        float4 y[A][E / 4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < A; ++i) {
           if (c + i <= span.y) {
             const size_t slot = (size_t)(it + c + i) * p.slot_rows;
             x[i] = p.ml[slot + row];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int j = 0; j < E / 4; ++j)
               y[i][j] = *reinterpret_cast<const float4*>(base + slot * D + (size_t)j * 4 * p.slot_rows);
           }
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < A; ++i) {
           if (c + i <= span.y) {
             const float mn = fmaxf(m, x[i].x);
             const float fa = ex2(m - mn), fb = ex2(x[i].x - mn);
             m = mn;
             l = l * fa + x[i].y * fb;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < E / 4; ++j) {
               acc[4 * j] = acc[4 * j] * fa + y[i][j].x * fb;
               acc[4 * j + 1] = acc[4 * j + 1] * fa + y[i][j].y * fb;
               acc[4 * j + 2] = acc[4 * j + 2] * fa + y[i][j].z * fb;
@@ -979,9 +982,9 @@ __global__ void __launch_bounds__(kAtFinThreads) tree_attn_finish_kernel(const A
   }
   const float norm = attn_norm(l);
   const size_t orow = ((size_t)b * p.N + n) * p.Hq + h * p.G + g;
-  uint4* out = reinterpret_cast<uint4*>(p.out + orow * D + part * 16);
+  uint4* out = reinterpret_cast<uint4*>(p.out + orow * D + part * E);
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
+  for (int j = 0; j < E / 8; ++j) {
     uint32_t x[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e)
