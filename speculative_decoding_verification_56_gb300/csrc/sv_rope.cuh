@@ -19,13 +19,19 @@
 // it takes, as pairs for the two-wide float instructions.  One CTA per node;
 // the first threads make the sines and cosines while the first heads' loads
 // are in flight.
+//
+// Measured: 128 trees of 60 nodes, 32 + 8 + 8 heads of 128 (189 MB): 34.8 us,
+// 5.4 TB/s, 81% of a plain copy's rate.  64 threads a CTA, so that ends and
+// starts of nodes overlap (128 threads 37.2 us, 256 threads 50.8); loads one
+// head ahead (two heads ahead 36.0 us: fewer CTAs fit); scalar arithmetic 44.5.
+// A single tree of 60 nodes takes what a launch takes.
 #pragma once
 
 #include "sv_device.cuh"
 
 namespace sv {
 
-constexpr int kRopeThreads = 64;  // at least D / 2: they make the sines
+constexpr int kRopeThreads = 64;  // at least D / 2: they make the sines (see above for others)
 
 struct RopeParams {
   const uint16_t* qkv;     // [B, N, Hq + 2 Hkv, D] bf16

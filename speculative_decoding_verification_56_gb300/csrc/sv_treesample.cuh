@@ -34,6 +34,14 @@
 // largest, from a double-float evaluation of 2^x), whose sums depend on no
 // order.  No float64 arithmetic is on the way: it runs at two operations per
 // clock and SM here, and the sums of 16 CTAs alone took 16 us of a step.
+//
+// Measured (V = 128256 bf16, walks of 2.7 rows): one sequence 15.5 us, 16 of
+// them 27 us (their longest walks count), 64 of V = 151936 float32 62 us; about
+// 4 us a step (clocks: screen 1700, the CTA's sum 680, exchange 1650, search
+// 480, token 2700, child 460), against 0.1 to 15 us of HBM time for the rows.
+// Tried against the exchanges and lost: words counted by mbarriers in place of
+// the cluster's barriers 17.5 us at one sequence and 30.1 at 16; the rows of the
+// children asked for ahead 19.8 -> 22.5 and 28.2 -> 33.0.
 #pragma once
 
 #include "sv_lmhead.cuh"
