@@ -852,3 +852,53 @@ def test_conveniences_allocate_on_the_stream_of_the_call(raw):
     held = [torch.full((nbytes,), 0x7F, dtype=torch.uint8, device="cuda") for _ in range(3)]
     torch.cuda.synchronize()
     assert torch.equal(out, want) and torch.equal(lse, want_lse) and len(held) == 3
+
+
+@pytest.mark.parametrize("B,N,Hq,Hkv,D,ctx,P", [
+    (900, 2, 2, 1, 64, 60, 0),       # more sequences than one scan of the lengths takes
+    (900, 1, 4, 2, 64, 150, 130),
+    (1, 4096, 1, 1, 64, 100, 0),     # the largest tree
+])
+def test_attention_many_sequences_and_nodes(B, N, Hq, Hkv, D, ctx, P):
+    base = np.random.default_rng(B + N).integers(1, ctx + 1, B)
+    _, _, flags = check_attention(B, N, Hq, Hkv, D, base, P, chain=N < 3, seed=B, junk=False)
+    assert flags == 0
+
+
+def test_cache_offsets_past_32_bits():
+    # two sequences 2^31 + 2^20 elements apart give what a compact cache gives
+    B, N, Hq, Hkv, D, L = 2, 9, 8, 2, 64, 700
+    step = (1 << 31) + (1 << 20)
+    gen = torch.Generator(device="cuda").manual_seed(21)
+    small = [randn(gen, B, L, Hkv, D) for _ in range(2)]
+    far = []
+    for t in small:
+        flat = torch.empty(step + L * Hkv * D, dtype=torch.bfloat16, device="cuda")
+        far.append(flat.as_strided((B, L, Hkv, D), (step, Hkv * D, D, 1)))
+        far[-1].copy_(t)
+    qkv = randn(gen, B, N, Hq + 2 * Hkv, D)
+    inv = torch.linspace(1.0, 1e-4, D // 2, device="cuda")
+    base = torch.tensor([33, 651], dtype=torch.int32, device="cuda")
+    res = []
+    for k, v in (small, far):
+        q = sv.tree_qkv_rope(qkv, None, None, 1e-6, inv, base, None, k, v)
+        res.append((q, *sv.tree_attention(q, k, v, None, base)))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(*res))
+    assert torch.equal(small[0], far[0]) and torch.equal(small[1], far[1])
+
+
+def test_sample_rows_past_32_bits():
+    # row 599 of V = 2^22 starts 2.5e9 elements in
+    N, V = 600, 1 << 22
+    z = torch.zeros(1, N, V, dtype=torch.bfloat16, device="cuda")
+    z[0, 0, 12345] = z[0, N - 1, 777] = 40.0   # e^40 against 4e6: probability 1 to 2e-11
+    tok = torch.arange(N, dtype=torch.int32, device="cuda")[None].contiguous()
+    tok[0, N - 1] = 12345
+    par = torch.zeros(1, N, dtype=torch.int32, device="cuda")
+    u = torch.full((1, 2), 0.5, device="cuda")
+    r = sv.verify_tree_sample(z, tok, par, u, 1.0, 1)
+    torch.cuda.synchronize()
+    assert r["accepted_len"].tolist() == [1] and r["path_nodes"].tolist() == [[0, N - 1]]
+    assert r["out_tokens"].tolist() == [[12345, 777]]
+    assert (r["out_probs"] - 1).abs().max() < 2e-5
