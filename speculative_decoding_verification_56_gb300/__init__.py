@@ -196,7 +196,7 @@ def _call_device(t, name):
     dev = t.get_device()
     if dev < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if dev != _torch().cuda.current_device():
+    if dev != _torch()._C._cuda_getDevice():  # (CUDA is initialised: t is there)
         raise ValueError(f"{name} is on cuda:{dev}, which is not the current device")
     return dev
 
@@ -206,28 +206,28 @@ def _cache_args(k_cache, v_cache, Hkv, D, B, device):
     and value cache [B, L, Hkv, D] (sequences may lie further apart)."""
     bf16 = _torch().bfloat16
     shape, stride = k_cache.shape, k_cache.stride()
-    if not (k_cache.dtype is bf16 and v_cache.dtype is bf16 and len(shape) == 4
-            and shape[0] == B and shape[2] == Hkv and shape[3] == D and v_cache.shape == shape
+    if (k_cache.dtype is bf16 and v_cache.dtype is bf16 and len(shape) == 4
+            and shape == (B, shape[1], Hkv, D) and v_cache.shape == shape
             and k_cache.get_device() == device and v_cache.get_device() == device
-            and stride[1:] == (Hkv * D, D, 1) and v_cache.stride() == stride):
-        for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-            if t.dtype is not bf16:
-                raise TypeError(f"{name} must be {bf16}, got {t.dtype}")
-            if t.get_device() != device:
-                raise ValueError(f"{name} must be on cuda:{device}")
-            if t.dim() != 4 or t.shape != (B, shape[1], Hkv, D):
-                raise ValueError(f"{name} must be [{B}, L, {Hkv}, {D}], got {list(t.shape)}")
-        raise ValueError("k_cache and v_cache must have the same strides, with the positions of "
-                         "a sequence contiguous")
-    L = shape[1]
-    step = stride[0] if B > 1 else max(stride[0], L * Hkv * D)
-    return k_cache.data_ptr(), v_cache.data_ptr(), 2 * step, L
+            and stride == (stride[0], Hkv * D, D, 1) and v_cache.stride() == stride):
+        L = shape[1]
+        step = stride[0] if B > 1 else max(stride[0], L * Hkv * D)
+        return k_cache.data_ptr(), v_cache.data_ptr(), 2 * step, L
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        if t.dtype is not bf16:
+            raise TypeError(f"{name} must be {bf16}, got {t.dtype}")
+        if t.get_device() != device:
+            raise ValueError(f"{name} must be on cuda:{device}")
+        if t.dim() != 4 or t.shape != (B, t.shape[1], Hkv, D):
+            raise ValueError(f"{name} must be [{B}, L, {Hkv}, {D}], got {list(t.shape)}")
+    raise ValueError("k_cache and v_cache must have the same shape and strides, with the positions "
+                     "of a sequence contiguous")
 
 
 def _workspace(t, device):
     if t.get_device() != device or not t.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on cuda:{device}")
-    return t.data_ptr(), t.numel() * t.element_size()
+    return t.data_ptr(), t.nbytes
 
 
 def _stream_of(stream, device):
