@@ -35,7 +35,8 @@
 // long / shared prefix, us, then 69 / 137 / 182): one issuing warp per half 79 /
 // 199 / 197; P handed over in two parts 78 / 153 / 233; scores loaded 64 or 128
 // columns at once 81 / 145 / 184 and 78 / 141 / 177 (the products with V slow
-// down beside long loads).
+// down beside long loads); two softmax warps for 32 rows, 64 entries each, 112 /
+// 236 / 277 (96 registers a thread are too few).
 #pragma once
 
 #include "sv_lmhead.cuh"
