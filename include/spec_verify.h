@@ -301,7 +301,7 @@ SPEC_API spec_status_t spec_tree_attention_mask(const int32_t* parents, int B, i
  *   base_len      int32 [B]; depth int32 [B, N] or NULL (a chain: node v at
  *                 depth v); a negative depth counts as 0 and raises
  *                 SPEC_FLAG_BAD_PARENT
- *   q_out         bf16 [B, N, Hq, D]
+ *   q_out         bf16 [B, N, Hq, D]; outputs must not overlap inputs
  *   k_cache, v_cache bf16: sequence b's position t starts seq_stride * b +
  *                 t * Hkv * D * 2 bytes in; L positions per sequence
  * D is 64 or 128; qkv, q_out, the norms and the caches 16-byte aligned,
