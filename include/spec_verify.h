@@ -351,7 +351,8 @@ SPEC_API spec_status_t spec_tree_qkv_rope(const void* qkv, const void* q_norm, c
  * takes most of each SM's shared and tensor memory until it ends, and the join
  * of items that were cut; the cut, and so the last bits, depend on base_len and
  * the number of SMs alone.  Workspace: at least
- * spec_tree_attention_workspace_bytes() bytes (the partials of cut items).
+ * spec_tree_attention_workspace_bytes() bytes (float32 partials: of cut items,
+ * two per SM at most, or of every item behind a shared prefix).
  */
 #define SPEC_ATTN_MAX_NODES 4096
 SPEC_API size_t spec_tree_attention_workspace_bytes(int B, int N, int Hq, int Hkv, int D, int P);

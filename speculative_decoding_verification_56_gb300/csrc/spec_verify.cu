@@ -532,7 +532,8 @@ spec_status_t launch_tree_sample(const sv::TreeSampleParams& prm, int B, int clu
 
 // Tiles and partial slots of spec_tree_attention for one call shape.
 struct AttnPlan {
-  int tok = 0, pair_s = 0, pair_o = 0, mg_s = 0, mg_o = 0, half_rows = 0, slot_rows = 0;
+  int tok = 0, pair_s = 0, pair_o = 0, mg_s = 0, mg_o = 0, rows_s = 0, rows_o = 0, by_cta = 0;
+  long long own0 = 0;  // rows of the shared items' slots, which come first
   size_t off_ml = 0, off_part = 0, bytes = 0;
 };
 
@@ -542,6 +543,11 @@ struct AttnPlan {
 // 79.6 us instead of 69.4 (16 trees of 60), 181 instead of 133 (65536 cached),
 // 254 instead of 184 (a shared prefix); two halves throughout: decoding 154.8
 // instead of 136.3 us.
+// Slots: shared and own items have slots of their own sizes.  Behind a shared
+// prefix every own item leaves a partial, and each cut one more: items + CTAs
+// slots.  Without one, only cut items do, at most two a CTA (the item that it
+// begins with and the one that it ends with), which is less from kAtMaxCtas
+// items on (by_cta).
 AttnPlan attn_plan(int B, int N, int Hq, int Hkv, int D, int P) {
   AttnPlan a;
   const int G = Hq / Hkv;
@@ -549,16 +555,24 @@ AttnPlan attn_plan(int B, int N, int Hq, int Hkv, int D, int P) {
   const long long all = (long long)B * N;
   a.pair_o = N > a.tok;
   a.mg_o = (N + (a.tok << a.pair_o) - 1) / (a.tok << a.pair_o);
+  a.rows_o = std::min(N, a.tok << a.pair_o) * G;
+  const size_t items_o = (size_t)B * Hkv * a.mg_o;
+  size_t items_s = 0, slots_s = 0, slots_o = items_o + sv::kAtMaxCtas;
   if (P > 0) {
     a.pair_s = all > a.tok;
     a.mg_s = (int)((all + (a.tok << a.pair_s) - 1) / (a.tok << a.pair_s));
+    a.rows_s = (int)std::min<long long>(all, a.tok << a.pair_s) * G;
+    items_s = (size_t)Hkv * a.mg_s;
+    slots_s = items_s + sv::kAtMaxCtas;
+  } else if (items_o > (size_t)sv::kAtMaxCtas) {
+    a.by_cta = 1;
+    slots_o = 2 * (size_t)sv::kAtMaxCtas;
   }
-  a.half_rows = (int)std::min<long long>(a.tok, P > 0 ? all : N) * G;
-  a.slot_rows = a.half_rows << std::max(a.pair_s, a.pair_o);
-  const size_t slots = (size_t)Hkv * a.mg_s + (size_t)B * Hkv * a.mg_o + sv::kAtMaxCtas;
-  a.off_ml = align_up(kDataOffset + slots * sizeof(int2));
-  a.off_part = align_up(a.off_ml + slots * a.slot_rows * sizeof(float2));
-  a.bytes = align_up(a.off_part + slots * a.slot_rows * D * sizeof(float));
+  a.own0 = (long long)slots_s * a.rows_s;
+  const size_t rows = (size_t)a.own0 + slots_o * a.rows_o;
+  a.off_ml = align_up(kDataOffset + (items_s + items_o) * sizeof(int2));
+  a.off_part = align_up(a.off_ml + rows * sizeof(float2));
+  a.bytes = align_up(a.off_part + rows * D * sizeof(float));
   return a;
 }
 
@@ -1212,8 +1226,10 @@ spec_status_t spec_tree_attention(const void* q, const void* k_cache, const void
   prm.mg_s = plan.mg_s;
   prm.mg_o = plan.mg_o;
   prm.tiles_s = P / sv::kAtKeys + (P % sv::kAtKeys != 0);
-  prm.half_rows = plan.half_rows;
-  prm.slot_rows = plan.slot_rows;
+  prm.rows_s = plan.rows_s;
+  prm.rows_o = plan.rows_o;
+  prm.by_cta = plan.by_cta;
+  prm.own0 = plan.own0;
   prm.nctas = std::min(sms, sv::kAtMaxCtas);
   prm.q_tiles = 1 + std::max(plan.pair_s, plan.pair_o);
   prm.span = reinterpret_cast<int2*>(ws + kDataOffset);

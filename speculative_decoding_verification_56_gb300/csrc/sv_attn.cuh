@@ -20,7 +20,10 @@
 // SM, whatever the lengths: the tiles of all items (shared prefix first, then
 // sequence by sequence) stand in one line of T, CTA c takes [c T / n, (c+1) T / n),
 // and an item that is cut (or has a shared prefix to be joined with) leaves one
-// partial per CTA, in slot item + c, for tree_attn_finish_kernel to join.
+// partial per CTA for tree_attn_finish_kernel to join: in slot item + c, or,
+// where many items of which only cut ones leave partials would take too many
+// slots, 2 c (+ 1 if the item begins in CTA c).  Shared and own items have
+// slots of their own sizes.
 //
 // Measured (32 query heads of 8, D = 128): plain decoding of 64 sequences of
 // about 3000 entries 136 us, 5.9 TB/s, bound by HBM; 16 trees of 60 nodes over
@@ -80,12 +83,13 @@ struct AttnParams {
   int pair_s, pair_o;       // shared / own items: two halves of rows (else one, by alternate tiles)
   int mg_s, mg_o;           // items per key-value head (and sequence)
   int tiles_s;              // ceil(P / 128)
-  int half_rows;            // rows stored per half
-  int slot_rows;            // rows stored per slot
+  int rows_s, rows_o;       // rows of a slot of a shared / own item
+  int by_cta;               // own items' slots by CTA (else by item)
+  long long own0;           // first row of the own items' slots
   int nctas;
   int q_tiles;              // 2 if any item is a pair
-  float* opart;             // [slot][D / 4][slot_rows][4]
-  float2* ml;               // [slot][slot_rows]: reference (log2) and sum
+  float* opart;             // [slot][D / 4][rows][4]
+  float2* ml;               // [slot][rows]: reference (log2) and sum
   int2* span;               // [items]: first and last CTA that holds a part of the item
 };
 
@@ -105,7 +109,7 @@ __device__ __forceinline__ float attn_lse(float m, float l) {
 
 // A CTA's run of tiles is cut into segments, one per item it meets.
 struct AttnSeg {
-  long long slot;     // of the partial: item + CTA
+  long long slot;     // first row of the partial's slot
   int b, h;           // sequence (0 for the shared prefix), key-value head
   int node0, ntok;    // first node and number of nodes of the item's rows: of all nodes of the
                       // batch for the shared prefix, else of the sequence's
@@ -121,7 +125,7 @@ struct AttnWalk {
     if (pos >= hi) return;
     const long long items_s = (long long)p.Hkv * p.mg_s;
     const long long shared = items_s * p.tiles_s;
-    long long it;
+    long long it, item;  // item: among all, the shared ones first
     int tiles;
     s->shared = pos < shared;
     if (s->shared) {
@@ -130,7 +134,8 @@ struct AttnWalk {
       s->t0 = (int)(pos - it * tiles);
       s->b = 0;
       s->kvlen = s->plen = p.P;
-      s->slot = it + blockIdx.x;
+      item = it;
+      s->slot = (it + blockIdx.x) * p.rows_s;
       s->pair = p.pair_s;
     } else {
       const int per = p.Hkv * p.mg_o;
@@ -146,7 +151,9 @@ struct AttnWalk {
       s->b = b;
       s->plen = base - 1;
       s->kvlen = s->plen + p.N;
-      s->slot = items_s + (long long)b * per + it + blockIdx.x;
+      item = items_s + (long long)b * per + it;
+      s->slot = p.own0 + (p.by_cta ? 2ll * blockIdx.x + (s->t0 == 0)
+                                   : (long long)b * per + it + blockIdx.x) * p.rows_o;
       s->pair = p.pair_o;
     }
     const int mg = (int)it / p.Hkv;
@@ -155,8 +162,8 @@ struct AttnWalk {
     s->ntok = min(p.tok << s->pair, (s->shared ? p.B * p.N : p.N) - s->node0);
     s->n = (int)min((long long)(tiles - s->t0), hi - pos);
     s->whole = s->n == tiles && p.tiles_s == 0;
-    if (s->t0 == 0) p.span[s->slot - blockIdx.x].x = blockIdx.x;
-    if (s->t0 + s->n == tiles) p.span[s->slot - blockIdx.x].y = blockIdx.x;
+    if (s->t0 == 0) p.span[item].x = blockIdx.x;
+    if (s->t0 + s->n == tiles) p.span[item].y = blockIdx.x;
     pos += s->n;
   }
 };
@@ -820,7 +827,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         if (lane == 0) mbar_arrive(&p_full[w]);
       }
       if (!ok) break;
-      // the item's output, or its partial as [D / 4][slot_rows][4], so that a
+      // the item's output, or its partial as [D / 4][rows][4], so that a
       // warp's lanes (rows) store 512 consecutive bytes
       if (nt > 0 && !at_wait_warp(&o_full[w], no++ & 1, abort)) {
         ok = false;
@@ -830,8 +837,9 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       if (nt > 0 && (!pair || w == 1)) release(v_use(pair, pair ? nt - 1 : 2 * (nt - 1) + w, seg.n));
       ring0 += 2 * seg.n;
       const bool mine_row = r < nrows;
-      float* slot = p.opart + seg.slot * (long long)p.slot_rows * D;
-      const int row = (pair ? w * p.half_rows : 0) + r;
+      float* slot = p.opart + seg.slot * D;
+      const int rows = seg.shared ? p.rows_s : p.rows_o;
+      const int row = (pair ? w * p.tok * p.G : 0) + r;
       const size_t orow = ((size_t)seg.b * p.N + node) * p.Hq + seg.h * p.G + rhead;
       auto put = [&](int c, const uint32_t (&o)[32], float norm) {
         if (!mine_row) return;
@@ -849,14 +857,14 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         } else {
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            *reinterpret_cast<uint4*>(slot + ((c / 4 + j) * p.slot_rows + row) * 4) =
+            *reinterpret_cast<uint4*>(slot + ((c / 4 + j) * rows + row) * 4) =
                 make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
         }
       };
       auto put_ml = [&](float mm, float ll) {
         if (!mine_row) return;
         if (!seg.whole)
-          p.ml[seg.slot * p.slot_rows + row] = make_float2(mm, ll);
+          p.ml[seg.slot + row] = make_float2(mm, ll);
         else if (p.lse)
           p.lse[orow] = attn_lse(mm, ll);
       };
@@ -951,28 +959,31 @@ __global__ void __launch_bounds__(kAtFinThreads, E * A <= 32 ? 3 : 2)
     for (int k = p.tiles_s == 0 ? 1 : 0; k < 2; ++k) {  // shared prefix, own entries
       const int cap = p.tok << (k == 0 ? p.pair_s : p.pair_o);
       const int node = k == 0 ? b * p.N + n : n;
-      const int mg = node / cap, in = node - mg * cap, half = in / p.tok;
-      const int row = half * p.half_rows + (in - half * p.tok) * p.G + g;
-      const long long it = k == 0 ? mg * p.Hkv + h
-                                  : (long long)p.Hkv * p.mg_s +
-                                        ((long long)b * p.mg_o + mg) * p.Hkv + h;
-      int2 span = p.span[it];
+      const int mg = node / cap;
+      const int row = (node - mg * cap) * p.G + g;  // (half 1 stands behind the tok G of half 0)
+      const long long it = ((k == 0 ? 0ll : (long long)b * p.mg_o) + mg) * p.Hkv + h;
+      int2 span = p.span[k == 0 ? it : (long long)p.Hkv * p.mg_s + it];
       if (p.tiles_s == 0 && span.x == span.y) return;  // written by its only CTA
       // slots of the workspace, whatever an overlapping call made of the span
       span.x = max(span.x, 0);
       span.y = min(span.y, p.nctas - 1);
-      const float* base = p.opart + (size_t)part * E * p.slot_rows + (size_t)row * 4;
+      const int slot_rows = k == 0 ? p.rows_s : p.rows_o;
+      const bool by_cta = k == 1 && p.by_cta;
+      const long long slot0 = (k == 0 ? 0ll : p.own0) + (by_cta ? 0ll : it * slot_rows);
+      const int first = span.x;
+      const float* base = p.opart + (size_t)part * E * slot_rows + (size_t)row * 4;
       for (int c = span.x; c <= span.y; c += A) {
         float2 x[A];
         float4 y[A][E / 4];
 #pragma unroll
         for (int i = 0; i < A; ++i) {
           if (c + i <= span.y) {
-            const size_t slot = (size_t)(it + c + i) * p.slot_rows;
+            const int at_c = by_cta ? 2 * (c + i) + (c + i == first) : c + i;
+            const size_t slot = (size_t)(slot0 + (long long)at_c * slot_rows);
             x[i] = p.ml[slot + row];
 #pragma unroll
             for (int j = 0; j < E / 4; ++j)
-              y[i][j] = *reinterpret_cast<const float4*>(base + slot * D + (size_t)j * 4 * p.slot_rows);
+              y[i][j] = *reinterpret_cast<const float4*>(base + slot * D + (size_t)j * 4 * slot_rows);
           }
         }
 #pragma unroll

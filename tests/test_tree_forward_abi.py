@@ -112,3 +112,28 @@ def test_tree_attention_scale_stays_finite(lib):
     assert call(scale=2.0 ** 127) == INVALID and call(scale=3e38) == INVALID
     assert call(scale=float("inf")) == INVALID and call(scale=float("nan")) == INVALID
     assert call(scale=1.5 * 2.0 ** 126) == WORKSPACE and call(scale=1e-45) == WORKSPACE
+
+
+@pytest.mark.parametrize("B,N,Hq,Hkv,D,P", [
+    (64, 1, 32, 8, 128, 0), (64, 1, 32, 8, 128, 1), (1024, 1, 32, 8, 128, 1), (256, 60, 32, 8, 128, 0),
+    (256, 60, 32, 8, 128, 8192), (1, 5, 8, 8, 64, 0), (20, 1, 8, 8, 64, 0), (3, 200, 71, 1, 64, 129),
+])
+def test_attention_workspace_holds_what_the_join_reads(lib, B, N, Hq, Hkv, D, P):
+    """Slots of an item's own rows: one part of every item behind a shared prefix
+    and one more a CTA; without a prefix two a CTA at most."""
+    ctas, tok = 160, 128 // (Hq // Hkv)
+
+    def items_and_rows(nodes):
+        per = 2 * tok if nodes > tok else tok
+        return -(-nodes // per), min(nodes, per) * (Hq // Hkv)
+
+    mg, rows = items_and_rows(N)
+    items = B * Hkv * mg
+    held = (items + ctas if P else min(items + ctas, 2 * ctas)) * rows
+    if P:
+        mg, rows = items_and_rows(B * N)
+        held += (Hkv * mg + ctas) * rows
+        items += Hkv * mg
+    need = 256 + items * 8 + held * (4 * D + 8)     # flags, spans; row: D floats, reference and sum
+    got = sv.spec_tree_attention_workspace_bytes(B, N, Hq, Hkv, D, P)
+    assert need <= got < need + 4 * 256             # parts start at multiples of 256
