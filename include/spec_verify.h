@@ -344,8 +344,12 @@ SPEC_API spec_status_t spec_tree_qkv_rope(const void* qkv, const void* q_norm, c
  * 2^31 - 257; q, out, the caches and prefixes 16-byte aligned, seq_stride a
  * multiple of 16.  A sequence whose
  * tree does not fit the cache (base_len < 1 or base_len + N - 1 > L) gets out
- * = 0, lse = -inf and raises SPEC_FLAG_BAD_PATH.  A node that sees an entry
- * whose value is not finite gets NaN.  Outputs must not overlap inputs.
+ * = 0, lse = -inf and raises SPEC_FLAG_BAD_PATH.  Values that are not finite:
+ * an element of a tree entry (the root's or a node's) makes all of out NaN for
+ * the query heads that read it, of the nodes that see the entry alone; an
+ * element of the prefix or of the committed positions, which all nodes see,
+ * makes its own column of out infinite or NaN, as in the sum.  lse does not
+ * depend on values.  Outputs must not overlap inputs.
  * Two launches: the attention of equal runs of 128-entry tiles, one run per
  * SM, on the tensor cores (weights rounded to bf16, sums in float32), which
  * takes most of each SM's shared and tensor memory until it ends, and the join

@@ -299,6 +299,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   __shared__ float2 s_ml[2][kAtRows];
   __shared__ uint32_t s_bad[2][2][4];  // tree entries of a tile whose V is not finite: by
                                        // turns, half
+  __shared__ uint32_t s_spoilt[2][4];  // rows of a half that see one in this segment
   uint8_t* ring = smem + p.q_tiles * kTile;
   const int S = at_tiles<D>() - p.q_tiles;  // ring stages
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -632,6 +633,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       const bool busy = quad * 32 < nrows;  // whole warps of unused rows only wait
       const int nt = pair ? seg.n : (seg.n + 1 - w) / 2;
       float m = -1e30f, l = 0.0f;
+      if (lane == 0) s_spoilt[w][quad] = 0;
       for (int i = 0; i < nt; ++i) {
         const int t = pair ? i : 2 * i + w;
         const int key0 = (seg.t0 + t) * kAtKeys;
@@ -671,11 +673,11 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           release(k_use(pair, t));
           if (i > 0) release(v_use(pair, t - (2 - pair), seg.n));
         }
-        bool spoilt = false;
         if (edge) {
           // V entries beyond the last are zeroed, whatever they hold: their
           // products with weights of 0 have to be 0.  So are tree entries that
-          // are not finite, and the rows that see them become NaN.
+          // are not finite, and the outputs of rows that see them become NaN
+          // (not their log-sums, which V has no part in).
           if (!pair || w == 0) {
             const int use = v_use(pair, t, seg.n);
             const int st = slot_of(use);
@@ -714,8 +716,11 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           }
           ok = pair ? meet(&pair_bar, npair) : meet(&half_bar[w], nh);
           if (!ok) break;
+          uint32_t bad = 0;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) spoilt |= (see[c] & s_bad[i & 1][pair ? 0 : w][c]) != 0;
+          for (int c = 0; c < 4; ++c) bad |= see[c] & s_bad[i & 1][pair ? 0 : w][c];
+          const unsigned rows_bad = __ballot_sync(0xffffffffu, bad != 0);
+          if (rows_bad && lane == 0) s_spoilt[w][quad] |= rows_bad;
         }
         if (busy) {
           const unsigned long long c2 = f2pack(p.scale_log2, p.scale_log2);
@@ -819,7 +824,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
               tmem_st16(sbase + 16 * c, pk);
             }
           }
-          l += spoilt ? NAN : total();
+          l += total();
           tmem_wait_st();
         }
         tmem_fence_before();
@@ -861,6 +866,18 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                 make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
         }
       };
+      // NaN over the columns [c0, c1) that put stored, in a spoilt row
+      auto spoil = [&](int c0, int c1, uint32_t rows_bad) {
+        if (!((rows_bad >> lane) & 1) || !mine_row) return;
+        const uint32_t x = seg.whole ? 0x7FC07FC0u : 0x7FC00000u;
+#pragma unroll 1
+        for (int c = c0; c < c1; c += 4) {
+          if (!seg.whole)
+            *reinterpret_cast<uint4*>(slot + (c / 4 * rows + row) * 4) = make_uint4(x, x, x, x);
+          else
+            *reinterpret_cast<uint2*>(p.out + orow * D + c) = make_uint2(x, x);
+        }
+      };
       auto put_ml = [&](float mm, float ll) {
         if (!mine_row) return;
         if (!seg.whole)
@@ -883,6 +900,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             put(c, o0, norm);
             put(c + 32, o1, norm);
           }
+          __syncwarp();
+          spoil(0, D, s_spoilt[w][quad]);
         }
         tmem_fence_before();
       } else {
@@ -912,6 +931,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             }
             put(c, o, norm);
           }
+          spoil(w * (D / 2), (w + 1) * (D / 2), s_spoilt[0][quad] | s_spoilt[1][quad]);
         }
         // neither half's accumulators are written again before both are read
         tmem_fence_before();

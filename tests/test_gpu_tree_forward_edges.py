@@ -56,3 +56,63 @@ def test_attention_keeps_to_its_workspace(monkeypatch, B, N, Hq, Hkv, D, base, P
     _, _, flags = check_attention(B, N, Hq, Hkv, D, base, P, chain=N == 1, seed=B + N)
     buf, n = held[0]
     assert flags == 0 and len(held) == 1 and (buf[n:] == 0xFF).all()
+
+
+# ---------------------------------------------------------------------------
+# values that are not finite
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("N,D,P,base", [
+    (9, 64, 0, [40, 3]),        # one tile: written by its only CTA
+    (9, 128, 0, [700, 300]),    # halves by alternate tiles, items cut
+    (70, 64, 0, [333, 900]),    # rows of two tiles
+    (9, 64, 200, [150, 20]),    # joined with a shared prefix
+    (70, 128, 130, [100, 1]),
+])
+@pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan")])
+def test_attention_values_that_are_not_finite(N, D, P, base, value):
+    """One element of V: of a tree entry it makes the whole output NaN for the
+    nodes that see it; of a committed entry or the prefix, its own column for all
+    nodes.  The log-sums, which V has no part in, keep their bits."""
+    rng = np.random.default_rng(N + D)
+    gen = torch.Generator(device="cuda").manual_seed(N + D)
+    B, Hq, Hkv, L, col, head = 2, 4, 2, 1000, 5, 1
+
+    def randn(*shape):
+        return torch.randn(*shape, generator=gen, dtype=torch.bfloat16, device="cuda")
+
+    q, kc, vc = randn(B, N, Hq, D), randn(B, L, Hkv, D), randn(B, L, Hkv, D)
+    pk, pv = (randn(P, Hkv, D), randn(P, Hkv, D)) if P else (None, None)
+    par = np.stack([np.concatenate([[-1], [rng.integers(0, v) for v in range(1, N)]]) for _ in range(B)])
+    mask = oracle.tree_mask(par.astype(np.int32))[0]
+    maskd = torch.from_numpy(mask.view(np.int32)).cuda()
+    based = torch.tensor(base, dtype=torch.int32, device="cuda")
+    clean, lse0 = sv.tree_attention(q, kc, vc, maskd, based, prefix_k=pk, prefix_v=pv)
+    heads = slice(head * Hq // Hkv, (head + 1) * Hq // Hkv)
+    for b in range(B):
+        at = [base[b] - 1 + u for u in (0, N // 2, N - 1)] + [t for t in (0, base[b] - 2) if 0 <= t < base[b] - 1]
+        for t in at:
+            v2 = vc.clone()
+            v2[b, t, head, col] = value
+            out, lse = sv.tree_attention(q, kc, v2, maskd, based, prefix_k=pk, prefix_v=pv)
+            want = clean.clone()
+            u = t - (base[b] - 1)
+            if u >= 0:
+                sees = torch.from_numpy(mask[b, :, u // 32] >> (u % 32) & 1 != 0).cuda()
+                assert sees.any()
+                want[b, sees, heads] = float("nan")
+            else:
+                want[b, :, heads, col] = float("nan")
+            spoilt = torch.isnan(want)
+            assert torch.equal(lse, lse0)
+            assert torch.equal(out[~spoilt], clean[~spoilt])
+            assert not torch.isfinite(out[spoilt]).any()
+            if u >= 0:
+                assert torch.isnan(out[spoilt]).all()
+    if P:
+        p2 = pv.clone()
+        p2[P - 1, head, col] = value
+        out, lse = sv.tree_attention(q, kc, vc, maskd, based, prefix_k=pk, prefix_v=p2)
+        assert torch.equal(lse, lse0) and not torch.isfinite(out[:, :, heads, col]).any()
+        out[:, :, heads, col] = clean[:, :, heads, col]
+        assert torch.equal(out, clean)
