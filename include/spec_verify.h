@@ -237,7 +237,10 @@ SPEC_API spec_status_t spec_verify_tree_greedy(const void* target_logits, int dt
  *   out_probs     float [B, max_depth+1] their probabilities, then 0
  * so that spec_kv_commit_path takes accepted_len and path_nodes as they are.
  * Draws are decided by float32 sums with a bounded error and, next to a border
- * C_j, by exact 64-bit integer sums of weights held to 2^-45 of the largest;
+ * C_j, by integer sums of weights rounded to 2^-50 of the largest, each off by
+ * 2^-40 of itself and another |z_j / T| 2^-46 of itself: a border of such sums
+ * is off by less than V 2^-51 + 2^-28 of R (2^-24 at the largest V; a token
+ * below 2^-51 of the largest is never drawn) where all |z_j / T| < 2^16;
  * out_probs is within 2e-5 of its value.  A row without a finite logit draws
  * nothing (token -1, probability 0, SPEC_FLAG_EMPTY_ROW) and ends the walk.
  * Malformed nodes are never taken

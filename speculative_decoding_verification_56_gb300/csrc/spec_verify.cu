@@ -1084,7 +1084,8 @@ spec_status_t spec_verify_tree_sample(const void* target_logits, int dtype,
   prm.N = N;
   prm.V = V;
   prm.max_depth = max_depth;
-  for (int bits = 17; bits < 31 && (1 << bits) < V; ++bits) prm.extra = bits - 16;
+  // the largest weight is below 2^(kTsFrac + 1/2): the sum of 2^bits of them stays below 2^63
+  for (int bits = 12; bits < 31 && (1 << bits) < V; ++bits) prm.extra = bits - 11;
   prm.accepted_len = accepted_len;
   prm.path = path_nodes;
   prm.out = out_tokens;

@@ -30,9 +30,15 @@
 // over a warp's 2048 steps, 5 over the warps, 5 over the CTAs and 5 in the
 // search: together below 8e-6 R for V = 2^26, of t and of a border.  Otherwise
 // (a draw among tokens of probability below 6e-5, for the most part) the row is
-// summed again exactly: weights as fixed-point 64-bit integers (2^-45 of the
-// largest, from a double-float evaluation of 2^x), whose sums depend on no
-// order.  No float64 arithmetic is on the way: it runs at two operations per
+// summed again in integers, whose sums depend on no order: weights in units of
+// 2^-50 of the largest, from a double-float evaluation of 2^x (off by 2^-40 of
+// itself, and by |z / T| 2^-46 of itself for the argument's rounding).  The
+// roundings to the unit can all go one way (equal tokens), which moves a border
+// by V 2^-51; the sums of a warp's 256-element steps are kept whole, and only
+// the warps' sums are cut to 2^(extra-50) (so that the row's fit 64 bits), 128 of
+// them at most: 2^-29 at V = 2^26.  Together a border is off by less than 2^-24
+// of R for every V up to 2^26, one step of a float32 uniform.
+// No float64 arithmetic is on the way: it runs at two operations per
 // clock and SM here, and the sums of 16 CTAs alone took 16 us of a step.
 //
 // Measured (V = 128256 bf16, walks of 2.7 rows): one sequence 15.5 us, 16 of
@@ -52,7 +58,8 @@ constexpr int kTsThreads = 256;
 constexpr int kTsWarps = kTsThreads / 32;
 constexpr int kTsStep = 256;          // elements of a warp's step: 8 per lane
 constexpr int kTsMaxCluster = 16;
-constexpr int kTsFrac = 45;           // fraction bits of a weight
+constexpr int kTsMant = 45;           // fraction bits of a mantissa in [1, 2)
+constexpr int kTsFrac = 50;           // and of a weight: 32 steps' sums stay below 2^64
 constexpr unsigned kFlagEmptyRow = 64u;
 
 // 2^(k/64): in units of 2^-45, and as two floats (nearest to the exact values).
@@ -117,7 +124,7 @@ struct TreeSampleParams {
   float c_hi, c_lo;           // log2(e) / T as a double-float
   int N, V, max_depth;
   int nsteps;                 // steps of kTsStep elements per warp
-  int extra;                  // further right shift of the weights: V > 2^17
+  int extra;                  // right shift of the warps' sums: V > 2^12
   int32_t* accepted_len;      // [B]
   int32_t* path;              // [B, max_depth + 1]
   int32_t* out;               // [B, max_depth + 1]
@@ -140,7 +147,7 @@ __device__ __forceinline__ void ts_exponent(const TreeSampleParams& p, float z, 
   *lo = __fsub_rn(l, __fsub_rn(*hi, d));
 }
 
-// Mantissa of 2^(y_hi + y_lo) in fixed point (2^45 stands for 1) and its
+// Mantissa of 2^(y_hi + y_lo) in fixed point (2^kTsMant stands for 1) and its
 // binary exponent *n.  y = n + k/64 + r with |r| <= 1/128: the table gives
 // 2^(k/64) (as the integer and as two floats), e^(r ln 2) - 1 is s + s^2/2 + ...
 // with s held as a double-float; its product with the table's value is
@@ -175,7 +182,7 @@ __device__ __forceinline__ long long ts_mantissa(float y_hi, float y_lo, const l
   return tab_i[k] + ((long long)i1 << 23) + 2ll * i2;
 }
 
-// Weight of logit z relative to 2^ref, in units of 2^-kTsFrac (2^-extra more).
+// Weight of logit z relative to 2^ref, in units of 2^-kTsFrac, rounded.
 __device__ __forceinline__ unsigned long long ts_weight(const TreeSampleParams& p, float z, int ref,
                                                         const long long* tab_i, const float2* tab_f) {
   float hi, lo;
@@ -183,22 +190,27 @@ __device__ __forceinline__ unsigned long long ts_weight(const TreeSampleParams& 
   if (!(hi > -(float)(kTsFrac + 3))) return 0;  // too small, -inf or NaN
   int n;
   const long long m = ts_mantissa(hi, lo, tab_i, tab_f, &n);
-  const int sh = p.extra - n;
-  if (sh <= 0) return (unsigned long long)m;
+  const int sh = kTsMant - kTsFrac - n;
+  if (sh <= 0) return (unsigned long long)m << min(-sh, kTsFrac - kTsMant);
   return ((unsigned long long)m + (1ull << (sh - 1))) >> sh;
 }
 
-// floor(u * R) for u in [0, 1): below R, so that u R < C means floor < C.
-__device__ __forceinline__ unsigned long long ts_threshold(float u, unsigned long long R) {
+// floor(u * R) for u in [0, 1): below R, so that u R < C means floor < C; and the
+// next `extra` bits of u * R, for the warps' uncut sums.
+__device__ __forceinline__ unsigned long long ts_threshold(float u, unsigned long long R, int extra,
+                                                           unsigned* frac) {
+  const unsigned mask = (1u << extra) - 1u;
+  *frac = 0;
   if (!(u > 0.0f)) return 0;
+  *frac = mask;
   if (u >= 1.0f) return R - 1;
   const unsigned bits = __float_as_uint(u);
   const int ex = (int)(bits >> 23);
-  const unsigned long long man = ex ? (bits & 0x7FFFFFu) | 0x800000u : (bits & 0x7FFFFFu);
-  const int sh = 150 - (ex ? ex : 1);  // u = man * 2^-sh, sh in [24, 149]
-  const unsigned long long lo = man * R, hi = __umul64hi(man, R);
-  if (sh < 64) return (hi << (64 - sh)) | (lo >> sh);
-  return sh < 128 ? hi >> (sh - 64) : 0;
+  const unsigned man = ex ? (bits & 0x7FFFFFu) | 0x800000u : (bits & 0x7FFFFFu);
+  const int sh = 150 - (ex ? ex : 1) - extra;  // u = man * 2^-(sh + extra); sh in [9, 149]
+  const unsigned __int128 x = sh < 128 ? (unsigned __int128)man * R >> sh : 0;
+  *frac = (unsigned)x & mask;
+  return (unsigned long long)(x >> extra);
 }
 
 __device__ __forceinline__ unsigned long long warp_sum_u64(unsigned long long v) {
@@ -241,7 +253,7 @@ __device__ __forceinline__ void ts_load(const typename E::storage* row, long lon
 
 // A CTA's part of a row, as every CTA of the cluster holds it.
 struct TsPart {
-  unsigned long long sum;  // exact: of fixed-point weights relative to 2^ref
+  unsigned long long sum;  // exact: of weights relative to 2^ref, in units of 2^(extra-kTsFrac)
   int ref;
   float fsum;              // screened: of weights relative to 2^ref
 };
@@ -356,6 +368,7 @@ __global__ void __launch_bounds__(kTsThreads, 4) tree_sample_kernel(const TreeSa
   unsigned long long R;
   int gref, owner, own;
   unsigned long long t;
+  unsigned t_frac;  // bits of t below the unit of the cut sums
   auto exchange = [&](float u) {
     __syncthreads();  // s_warp is complete
     const TsPart mine = lane < kTsWarps ? s_warp[lane] : TsPart{0ull, kRefEmpty, 0.0f};
@@ -376,7 +389,7 @@ __global__ void __launch_bounds__(kTsThreads, 4) tree_sample_kernel(const TreeSa
     R = warp_sum_u64(y);
     owner = kTsNone;
     if (R) {
-      t = ts_threshold(u, R);
+      t = ts_threshold(u, R, p.extra, &t_frac);
       owner = ts_pick(y, &t);
       if (owner == (int)rank) {
         t <<= gref - top;      // in the CTA's own units: below its sum
@@ -384,19 +397,21 @@ __global__ void __launch_bounds__(kTsThreads, 4) tree_sample_kernel(const TreeSa
       }
     }
   };
-  // the step of the owning warp that holds t
+  // the step of the owning warp that holds t, which becomes the rest in it (in
+  // the weights' units; a warp's 2048 steps may add up to more than 64 bits)
   auto find_step = [&]() {
-    int at = p.nsteps - 1;
+    unsigned __int128 left = (unsigned __int128)t << p.extra | t_frac;
+    t = 0;
     for (int s0 = 0; s0 < p.nsteps; s0 += 32) {
       const unsigned long long x = s0 + lane < p.nsteps ? steps[s0 + lane] : 0ull;
-      const int k = ts_pick(x, &t);
-      if (k >= 0) {
-        at = s0 + k;
-        break;
+      const unsigned long long all = warp_sum_u64(x);
+      if (left < all) {
+        t = (unsigned long long)left;
+        return s0 + ts_pick(x, &t);
       }
-      t -= warp_sum_u64(x);
+      left -= all;
     }
-    return at;
+    return p.nsteps - 1;  // never: t is below the steps' sum
   };
   auto tell = [&](int from, int token, float prob) {  // lane `from`'s, to every CTA
     token = __shfl_sync(0xffffffffu, token, from);
@@ -532,7 +547,7 @@ __global__ void __launch_bounds__(kTsThreads, 4) tree_sample_kernel(const TreeSa
       __syncthreads();
       ref = __reduce_max_sync(0xffffffffu, s_max[lane % kTsWarps]);
       if (ref == kTsRefBad) ref = kTsRefBad - 1;  // (an infinite logit: unspecified)
-      unsigned long long sum = 0;
+      unsigned __int128 sum = 0;
       for (int s = 0; s < p.nsteps; ++s) {
         float z[8];
         ts_load<E, kVec>(row, w0 + (long long)s * kTsStep, p.V, z);
@@ -543,7 +558,7 @@ __global__ void __launch_bounds__(kTsThreads, 4) tree_sample_kernel(const TreeSa
         if (lane == 0) steps[s] = part;
         sum += part;
       }
-      if (lane == 0) s_warp[warp] = TsPart{sum, ref, 0.0f};
+      if (lane == 0) s_warp[warp] = TsPart{(unsigned long long)(sum >> p.extra), ref, 0.0f};
       exchange(u);
       if (owner == (int)rank && warp == own) {
         const int s = find_step();
@@ -574,7 +589,8 @@ __global__ void __launch_bounds__(kTsThreads, 4) tree_sample_kernel(const TreeSa
         ts_exponent(p, zx, (float)ref, &hi, &lo);
         const float mant = (float)ts_mantissa(hi, lo, tab_i, tab_f, &n);
         tell(max(at, 0), (int)(w0 + (long long)s * kTsStep) + e0,
-             mant / (float)R * pow2i_f(min(n + ref - gref - p.extra, 0)));
+             mant * (float)(1 << (kTsFrac - kTsMant)) / (float)R *
+                 pow2i_f(min(n + ref - gref, 0) - p.extra));
       }
       ts_cluster_sync();
       x = owner < 0 ? kTsNone : s_tok[meet & 1];

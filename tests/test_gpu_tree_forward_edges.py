@@ -116,3 +116,56 @@ def test_attention_values_that_are_not_finite(N, D, P, base, value):
         assert torch.equal(lse, lse0) and not torch.isfinite(out[:, :, heads, col]).any()
         out[:, :, heads, col] = clean[:, :, heads, col]
         assert torch.equal(out, clean)
+
+
+# ---------------------------------------------------------------------------
+# tree sampling: draws among very unlikely tokens
+# ---------------------------------------------------------------------------
+
+def draw_first(logits, u, T=1.0):
+    """The tokens that uniforms u draw from the one row `logits`."""
+    rows = logits.expand(len(u), -1)[:, None].contiguous()
+    one = torch.zeros(len(u), 1, dtype=torch.int32, device="cuda")
+    r = sv.verify_tree_sample(rows, one, one - 1, torch.tensor(u, dtype=torch.float32, device="cuda")[:, None], T, 0)
+    torch.cuda.synchronize()
+    return r["out_tokens"].cpu().numpy()[:, 0].astype(np.float64), r["out_probs"].double().cpu().numpy()[:, 0]
+
+
+@pytest.mark.parametrize("V,z,dtype", [
+    (1 << 26, -24.625, torch.bfloat16),   # 1.4 times 2^-36 of the largest each, 1.4e-3 of it together
+    (1 << 26, -27.5, torch.bfloat16),
+    ((1 << 24) + 3, -26.25, torch.float32),
+    (1 << 22, -27.5, torch.float32),      # 0.6 of 2^-39
+])
+@pytest.mark.parametrize("first", [True, False])
+def test_sample_a_flat_tail_of_a_large_vocabulary(V, z, dtype, first):
+    """One likely token and V - 1 alike: the borders are an arithmetic series, and
+    a draw falls within V 2^-51 + 2^-28 of the total of where it should."""
+    row = torch.full((1, V), z, dtype=dtype, device="cuda")
+    row[0, 0 if first else V - 1] = 0.0
+    w = float(np.exp(z))                    # (bf16 holds these z exactly)
+    R = 1.0 + (V - 1) * w
+    part = np.array([0.1, 0.37, 0.5, 0.93])
+    u = ((1.0 + part * (R - 1)) / R if first else part * (R - 1) / R).astype(np.float32)
+    x, p = draw_first(row, u)
+    t = u.astype(np.float64) * R
+    lo = np.where(x == 0, 0.0, 1.0 + (x - 1) * w) if first else x * w
+    hi = 1.0 + x * w if first else np.where(x == V - 1, R, (x + 1) * w)
+    off = (V * 2.0 ** -51 + 2.0 ** -28) * R
+    assert (lo - off <= t).all() and (t < hi + off).all(), (lo - t, hi - t)
+    likely = x == (0 if first else V - 1)
+    want = np.where(likely, 1.0, w) / R
+    assert (np.abs(p - want) <= 2e-5 * want).all()
+
+
+@pytest.mark.parametrize("V", [1 << 20, 1 << 26])
+def test_sample_borders_of_a_large_vocabulary(V):
+    """Equal logits: a uniform on a border, or the float beside it, falls where
+    exact arithmetic says (every sum is a multiple of one weight)."""
+    rng = np.random.default_rng(V)
+    j = np.array([1, V // 2, V - 64, *(rng.integers(0, 1 << 20, 4) * (V >> 20))])
+    u = (j / V).astype(np.float32)
+    assert (u.astype(np.float64) * V == j).all()
+    for v in (u, np.nextafter(u, np.float32(1)), np.nextafter(u, np.float32(0))):
+        x, _ = draw_first(torch.full((1, V), -3.25, dtype=torch.bfloat16, device="cuda"), v, T=0.75)
+        assert (x == np.floor(v.astype(np.float64) * V)).all()
