@@ -104,8 +104,10 @@ typedef enum {
 #define SPEC_FLAG_RESIDUAL_FALLBACK 8u /* residual mass was 0 after a rejection;
                                           that position was sampled from p */
 #define SPEC_FLAG_TIMEOUT 16u          /* a kernel gave up waiting for its own
-                                          bulk copies (outputs of that call are
-                                          unspecified); never expected */
+                                          bulk copies or matrix products, or one
+                                          of its roles for another (outputs of
+                                          that call are unspecified); never
+                                          expected */
 #define SPEC_FLAG_BAD_PATH 32u         /* spec_kv_commit_path: a path that does
                                           not start at node 0, names a node
                                           outside [1, N), is longer than
@@ -519,17 +521,19 @@ SPEC_API uint64_t spec_verify_launch_count(void);
 /*
  * Diagnostic control of the bounded waits (no counterpart in the pages).
  *
- * Every wait of the verification kernels on their own bulk copies gives up
- * after a limit (0.2 s by default): the CTA then sets SPEC_FLAG_TIMEOUT,
- * stops copying, waits (with the default limit) for the copies it has in
- * flight and finishes its control flow, so the call completes with
- * unspecified outputs and the flag raised instead of hanging.  This sets the
- * limit used by calls of spec_verify_sample, spec_verify_greedy,
- * spec_verify_tree_greedy and spec_verify_greedy_noalloc enqueued afterwards,
- * process-wide; limit_ns = 0 restores the default.  limit_ns = 1 gives up
- * whenever a copy has not landed at the first look, which is how a test
- * exercises that path (other limits below a microsecond are rounded up by
- * the resolution of the GPU's global timer).  Not for production use.
+ * Every wait of the verification kernels on their own bulk copies, and every
+ * wait between the roles of a CTA of spec_tree_attention (copies, products,
+ * softmax), gives up after a limit (0.2 s by default): the CTA then sets
+ * SPEC_FLAG_TIMEOUT, stops copying, waits (with the default limit) for the
+ * copies and products it has in flight and finishes its control flow, so the
+ * call completes with unspecified outputs and the flag raised instead of
+ * hanging.  This sets the limit used by calls of spec_verify_sample,
+ * spec_verify_greedy, spec_verify_tree_greedy, spec_verify_greedy_noalloc and
+ * spec_tree_attention enqueued afterwards, process-wide; limit_ns = 0 restores
+ * the default.  limit_ns = 1 gives up whenever a copy has not landed (a role
+ * has not answered) at the first look, which is how a test exercises that path
+ * (other limits below a microsecond are rounded up by the resolution of the
+ * GPU's global timer).  Not for production use.
  */
 SPEC_API void spec_verify_set_wait_limit_ns(uint64_t limit_ns);
 

@@ -274,9 +274,10 @@ def spec_verify_abi_version() -> int:
 
 
 def spec_verify_set_wait_limit_ns(limit_ns: int) -> None:
-    """Limit of the verification kernels' waits on their bulk copies for calls
-    enqueued afterwards (0 restores the default 0.2 s); a diagnostic control
-    for testing the timeout path."""
+    """Limit of the verification kernels' waits on their bulk copies, and of the
+    tree attention's waits between its roles, for calls enqueued afterwards (0
+    restores the default 0.2 s); a diagnostic control for testing the timeout
+    path."""
     load_library().spec_verify_set_wait_limit_ns(int(limit_ns))
 
 

@@ -31,8 +31,8 @@ static_assert(sv::kMaxDraft == SPEC_MAX_K, "finish kernel buffers are sized for 
 namespace {
 
 std::atomic<uint64_t> g_launches{0};
-// limit of the verification kernels' waits on their bulk copies
-// (spec_verify_set_wait_limit_ns)
+// limit of the verification kernels' waits on their bulk copies and of the tree
+// attention's between its roles (spec_verify_set_wait_limit_ns)
 std::atomic<uint64_t> g_wait_limit_ns{sv::kWaitLimitNs};
 
 constexpr size_t kAlign = 256;
@@ -593,17 +593,27 @@ spec_status_t sm_count(int* sms) {
   return SPEC_OK;
 }
 
-template <int D>
-spec_status_t run_attention(const sv::AttnParams& prm, const CUtensorMap (&map)[5], void* stream) {
-  spec_status_t st = ensure_smem<sv::tree_attn_kernel<D>>((size_t)sv::at_smem<D>());
+template <int D, bool kSet>
+spec_status_t launch_attention(const sv::AttnParams& prm, const CUtensorMap (&map)[5],
+                               void* stream) {
+  const spec_status_t st = ensure_smem<sv::tree_attn_kernel<D, kSet>>((size_t)sv::at_smem<D>());
   if (st != SPEC_OK) return st;
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[1];
   pdl_config(&cfg, attr, dim3((unsigned)prm.nctas), dim3(sv::kAtThreads), sv::at_smem<D>(), stream);
-  if (cudaLaunchKernelEx(&cfg, sv::tree_attn_kernel<D>, map[0], map[1], map[2], map[3], map[4],
-                         prm) != cudaSuccess)
+  if (cudaLaunchKernelEx(&cfg, sv::tree_attn_kernel<D, kSet>, map[0], map[1], map[2], map[3],
+                         map[4], prm) != cudaSuccess)
     return SPEC_ERR_CUDA;
   g_launches.fetch_add(1, std::memory_order_relaxed);
+  return SPEC_OK;
+}
+
+template <int D>
+spec_status_t run_attention(const sv::AttnParams& prm, const CUtensorMap (&map)[5], void* stream) {
+  const spec_status_t st = prm.wait_ns == sv::kWaitLimitNs
+                               ? launch_attention<D, false>(prm, map, stream)
+                               : launch_attention<D, true>(prm, map, stream);
+  if (st != SPEC_OK) return st;
   const long long rows = (long long)prm.B * prm.N * prm.Hq;
   const long long blocks = (rows + sv::kAtFinThreads - 1) / sv::kAtFinThreads;
   // Parts of an item: about 1 + CTAs / items.  Many (3 sequences of 65536, 24
@@ -1234,6 +1244,7 @@ spec_status_t spec_tree_attention(const void* q, const void* k_cache, const void
   prm.nctas = std::min(sms, sv::kAtMaxCtas);
   prm.q_tiles = 1 + std::max(plan.pair_s, plan.pair_o);
   prm.span = reinterpret_cast<int2*>(ws + kDataOffset);
+  prm.wait_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
   prm.ml = reinterpret_cast<float2*>(ws + plan.off_ml);
   prm.opart = reinterpret_cast<float*>(ws + plan.off_part);
   // queries: boxes of 64 elements x the heads of one key-value head x nodes;

@@ -90,6 +90,8 @@ struct AttnParams {
   int q_tiles;              // 2 if any item is a pair
   float* opart;             // [slot][D / 4][rows][4]
   float2* ml;               // [slot][rows]: reference (log2) and sum
+  unsigned long long wait_ns;  // limit of each wait between the roles, where it was set (else
+                               // kWaitLimitNs), as a test does to exercise the timeout path
   int2* span;               // [items]: first and last CTA that holds a part of the item
 };
 
@@ -241,23 +243,39 @@ __device__ __forceinline__ uint64_t umma_desc_mn_sw128(uint32_t smem_byte_addr) 
 }
 
 // A wait in the kernel below.  The first test sleeps up to 1 ms in the
-// instruction; past that, the wait ends when it has taken kWaitLimitNs or
-// another role of the CTA has given up.
-__device__ __forceinline__ bool at_wait_slow(uint64_t* bar, unsigned parity, const int* abort) {
+// instruction; past that, the wait ends when it has taken its limit or another
+// role of the CTA has given up.  As in mbar_wait_bounded, a limit of 1 ns gives
+// up as soon as one test finds the phase incomplete.  kSet: the limit is p's
+// (instantiations of their own, since a limit that is not a constant makes the
+// softmax loop slower: a shared prefix 180 -> 207 us).
+template <bool kSet>
+__device__ __forceinline__ bool at_try(const AttnParams& p, uint64_t* bar, unsigned parity) {
+  if (!kSet) return mbar_try_wait(bar, parity);
+  return mbar_try_wait(bar, parity, (uint32_t)min(p.wait_ns, (unsigned long long)kSuspendHintNs));
+}
+template <bool kSet>
+__device__ __forceinline__ bool at_wait_slow(const AttnParams& p, uint64_t* bar, unsigned parity,
+                                             const int* abort) {
+  const uint64_t limit = kSet ? p.wait_ns : kWaitLimitNs;
+  if (limit <= 1) return false;
   const uint64_t t0 = global_ns();
   for (unsigned it = 0; it < (1u << 30); ++it) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if (*(const volatile int*)abort || global_ns() - t0 > kWaitLimitNs) return false;
+    if (at_try<kSet>(p, bar, parity)) return true;
+    if (*(const volatile int*)abort || global_ns() - t0 > limit) return false;
   }
   return false;
 }
-__device__ __forceinline__ bool at_wait(uint64_t* bar, unsigned parity, const int* abort) {
-  return mbar_try_wait(bar, parity) || at_wait_slow(bar, parity, abort);
+template <bool kSet>
+__device__ __forceinline__ bool at_wait(const AttnParams& p, uint64_t* bar, unsigned parity,
+                                        const int* abort) {
+  return at_try<kSet>(p, bar, parity) || at_wait_slow<kSet>(p, bar, parity, abort);
 }
 // the same for a whole warp, with one answer
-__device__ __forceinline__ bool at_wait_warp(uint64_t* bar, unsigned parity, const int* abort) {
-  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-  return __all_sync(0xffffffffu, at_wait_slow(bar, parity, abort));
+template <bool kSet>
+__device__ __forceinline__ bool at_wait_warp(const AttnParams& p, uint64_t* bar, unsigned parity,
+                                             const int* abort) {
+  if (__all_sync(0xffffffffu, at_try<kSet>(p, bar, parity))) return true;
+  return __all_sync(0xffffffffu, at_wait_slow<kSet>(p, bar, parity, abort));
 }
 
 // Warp 0 copies (TMA), warp 1 issues the MMAs, warp 2 lists the CTA's
@@ -277,7 +295,7 @@ __device__ __forceinline__ bool at_wait_warp(uint64_t* bar, unsigned parity, con
 // the weights are kept back until it is known.
 //   Every wait between the roles is a bounded one on an mbarrier; a role
 // that gives up leaves, and the others follow.
-template <int D>
+template <int D, bool kSet>
 __global__ void __launch_bounds__(kAtThreads, 1)
     tree_attn_kernel(const __grid_constant__ CUtensorMap map_q,
                      const __grid_constant__ CUtensorMap map_k,
@@ -406,7 +424,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         AttnSeg seg;
         walk.next(p, &seg);
         const unsigned at = k % kAtSegs;
-        if (!at_wait(&seg_empty[at], ((k / kAtSegs) & 1) ^ 1u, abort)) {
+        if (!at_wait<kSet>(p, &seg_empty[at], ((k / kAtSegs) & 1) ^ 1u, abort)) {
           fail();
           break;
         }
@@ -423,14 +441,14 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       unsigned phase = 0, nq = 0;
       for (bool ok = true; ok;) {
         const unsigned at = nq % kAtSegs;
-        if (!at_wait(&seg_full[at], (nq / kAtSegs) & 1, abort)) {
+        if (!at_wait<kSet>(p, &seg_full[at], (nq / kAtSegs) & 1, abort)) {
           fail();
           break;
         }
         const AttnSeg seg = s_seg[at];
         mbar_arrive(&seg_empty[at]);
         if (seg.n == 0) break;
-        if (!at_wait(&q_empty, (nq & 1) ^ 1u, abort)) {
+        if (!at_wait<kSet>(p, &q_empty, (nq & 1) ^ 1u, abort)) {
           fail();
           break;
         }
@@ -444,7 +462,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         const CUtensorMap* mk = seg.shared ? &map_pk : &map_k;
         const CUtensorMap* mv = seg.shared ? &map_pv : &map_v;
         auto put = [&](const CUtensorMap* m, int t) {
-          if (!at_wait(&empty[stage], phase ^ 1u, abort)) {
+          if (!at_wait<kSet>(p, &empty[stage], phase ^ 1u, abort)) {
             ok = false;
             fail();
             return;
@@ -484,7 +502,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       unsigned phase = 0, nq = 0, np0 = 0, np1 = 0;
       bool ok = true;
       auto wait = [&](uint64_t* bar, unsigned parity) {
-        if (!at_wait(bar, parity & 1, abort)) {
+        if (!at_wait<kSet>(p, bar, parity & 1, abort)) {
           ok = false;
           fail();
         }
@@ -615,11 +633,11 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     auto meet = [&](uint64_t* bar, unsigned& uses) {
       __syncwarp();
       if (lane == 0) mbar_arrive(bar);
-      return at_wait_warp(bar, uses++ & 1, abort);
+      return at_wait_warp<kSet>(p, bar, uses++ & 1, abort);
     };
     bool ok = true;
     for (unsigned k = 0; ok; ++k) {
-      if (!at_wait_warp(&seg_full[k % kAtSegs], (k / kAtSegs) & 1, abort)) {
+      if (!at_wait_warp<kSet>(p, &seg_full[k % kAtSegs], (k / kAtSegs) & 1, abort)) {
         ok = false;
         break;
       }
@@ -664,7 +682,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
 #pragma unroll
           for (int c = 0; c < 4; ++c) see[c] = __funnelshift_r(x[c], x[c + 1], tree0 & 31);
         }
-        if (!at_wait_warp(&s_full[w], ns++ & 1, abort)) {
+        if (!at_wait_warp<kSet>(p, &s_full[w], ns++ & 1, abort)) {
           ok = false;
           break;
         }
@@ -681,7 +699,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           if (!pair || w == 0) {
             const int use = v_use(pair, t, seg.n);
             const int st = slot_of(use);
-            if (!at_wait_warp(&full[st], ((ring0 + use) / S) & 1, abort)) {
+            if (!at_wait_warp<kSet>(p, &full[st], ((ring0 + use) / S) & 1, abort)) {
               ok = false;
               break;
             }
@@ -834,7 +852,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       if (!ok) break;
       // the item's output, or its partial as [D / 4][rows][4], so that a
       // warp's lanes (rows) store 512 consecutive bytes
-      if (nt > 0 && !at_wait_warp(&o_full[w], no++ & 1, abort)) {
+      if (nt > 0 && !at_wait_warp<kSet>(p, &o_full[w], no++ & 1, abort)) {
         ok = false;
         break;
       }

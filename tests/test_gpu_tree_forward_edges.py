@@ -169,3 +169,50 @@ def test_sample_borders_of_a_large_vocabulary(V):
     for v in (u, np.nextafter(u, np.float32(1)), np.nextafter(u, np.float32(0))):
         x, _ = draw_first(torch.full((1, V), -3.25, dtype=torch.bfloat16, device="cuda"), v, T=0.75)
         assert (x == np.floor(v.astype(np.float64) * V)).all()
+
+
+# ---------------------------------------------------------------------------
+# the attention's waits
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("B,N,Hq,Hkv,D,ctx,P", [
+    (20, 1, 8, 2, 128, 3000, 0),      # halves by alternate tiles
+    (9, 60, 16, 4, 128, 2000, 0),     # rows of two tiles
+    (16, 9, 8, 2, 64, 500, 1500),     # and a shared prefix
+])
+def test_attention_waits_that_run_out(B, N, Hq, Hkv, D, ctx, P):
+    """A wait that takes longer than its limit ends the call with the flag set (1 ns:
+    at the first wait that is not over at its first look; longer limits let the
+    roles get further), and the next call is right."""
+    gen = torch.Generator(device="cuda").manual_seed(B)
+
+    def randn(*shape):
+        return torch.randn(*shape, generator=gen, dtype=torch.bfloat16, device="cuda")
+
+    q, kc, vc = randn(B, N, Hq, D), randn(B, ctx + N, Hkv, D), randn(B, ctx + N, Hkv, D)
+    pk, pv = (randn(P, Hkv, D), randn(P, Hkv, D)) if P else (None, None)
+    base = torch.randint(1, ctx, (B,), generator=gen, device="cuda", dtype=torch.int32)
+    ws = sv.alloc_tree_attention_workspace(q, kc, pk)
+
+    def call():
+        out, lse = sv.tree_attention(q, kc, vc, None, base, prefix_k=pk, prefix_v=pv, workspace=ws)
+        torch.cuda.synchronize()
+        return out, lse, sv.spec_verify_read_flags(ws)
+
+    want = call()
+    assert want[2] == 0
+    flush = torch.empty(256 << 20, dtype=torch.uint8, device="cuda")
+    for limit in (1, 300, 1000, 3000, 10000, 10 ** 9):
+        flush.fill_(1)                       # the copies come from memory, not from L2
+        sv.spec_verify_set_wait_limit_ns(limit)
+        try:
+            out, lse, flags = call()
+        finally:
+            sv.spec_verify_set_wait_limit_ns(0)
+        assert flags == (sv.SPEC_FLAG_TIMEOUT if limit == 1 else flags & sv.SPEC_FLAG_TIMEOUT)
+        if limit == 10 ** 9:
+            assert flags == 0
+        if flags == 0:
+            assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+        again = call()
+        assert again[2] == 0 and torch.equal(again[0], want[0]) and torch.equal(again[1], want[1])
