@@ -56,6 +56,7 @@ constexpr float kAtLazy = 4096.0f;  // a tile's largest sum of a row's weights b
                                     // reference is renewed
 constexpr int kAtFinThreads = 256;
 constexpr int kAtSegs = 4;       // segment descriptors ahead of their use
+constexpr unsigned kAtTileNs = 20000;  // more than a tile takes (about 2000)
 
 template <int D>
 __host__ __device__ constexpr int at_tile_bytes() { return kAtKeys * D * 2; }
@@ -255,8 +256,8 @@ __device__ __forceinline__ bool at_try(const AttnParams& p, uint64_t* bar, unsig
 }
 template <bool kSet>
 __device__ __forceinline__ bool at_wait_slow(const AttnParams& p, uint64_t* bar, unsigned parity,
-                                             const int* abort) {
-  const uint64_t limit = kSet ? p.wait_ns : kWaitLimitNs;
+                                             const int* abort, uint64_t more_ns = 0) {
+  const uint64_t limit = (kSet ? p.wait_ns : kWaitLimitNs) + more_ns;
   if (limit <= 1) return false;
   const uint64_t t0 = global_ns();
   for (unsigned it = 0; it < (1u << 30); ++it) {
@@ -267,8 +268,8 @@ __device__ __forceinline__ bool at_wait_slow(const AttnParams& p, uint64_t* bar,
 }
 template <bool kSet>
 __device__ __forceinline__ bool at_wait(const AttnParams& p, uint64_t* bar, unsigned parity,
-                                        const int* abort) {
-  return at_try<kSet>(p, bar, parity) || at_wait_slow<kSet>(p, bar, parity, abort);
+                                        const int* abort, uint64_t more_ns = 0) {
+  return at_try<kSet>(p, bar, parity) || at_wait_slow<kSet>(p, bar, parity, abort, more_ns);
 }
 // the same for a whole warp, with one answer
 template <bool kSet>
@@ -424,7 +425,10 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         AttnSeg seg;
         walk.next(p, &seg);
         const unsigned at = k % kAtSegs;
-        if (!at_wait<kSet>(p, &seg_empty[at], ((k / kAtSegs) & 1) ^ 1u, abort)) {
+        // (the only wait that lasts as long as an item: until the one four before
+        // this is begun, so up to the run's length)
+        if (!at_wait<kSet>(p, &seg_empty[at], ((k / kAtSegs) & 1) ^ 1u, abort,
+                           (uint64_t)(hi - lo) * kAtTileNs)) {
           fail();
           break;
         }

@@ -216,3 +216,25 @@ def test_attention_waits_that_run_out(B, N, Hq, Hkv, D, ctx, P):
             assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
         again = call()
         assert again[2] == 0 and torch.equal(again[0], want[0]) and torch.equal(again[1], want[1])
+
+
+def test_attention_runs_of_long_items_are_not_given_up():
+    """Each CTA has seven items of half a million entries, several ms each, one
+    after the other: no role may take the time of a whole item for a wait that
+    has run out (limit 1 ms)."""
+    N, Hq, D, ctx = 2200, 128, 64, 512 * 1024
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    q = torch.randn(1, N, Hq, D, generator=gen, dtype=torch.bfloat16, device="cuda")
+    kc, vc = (torch.randn(1, ctx + N, 1, D, generator=gen, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    base = torch.tensor([ctx], dtype=torch.int32, device="cuda")
+    ws = sv.alloc_tree_attention_workspace(q, kc)
+    want = sv.tree_attention(q, kc, vc, None, base, workspace=ws)
+    assert sv.spec_verify_read_flags(ws) == 0
+    sv.spec_verify_set_wait_limit_ns(1_000_000)
+    try:
+        out, lse = sv.tree_attention(q, kc, vc, None, base, workspace=ws)
+        torch.cuda.synchronize()
+    finally:
+        sv.spec_verify_set_wait_limit_ns(0)
+    assert sv.spec_verify_read_flags(ws) == 0
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
