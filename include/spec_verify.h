@@ -25,7 +25,8 @@
  *     whose byte length is a multiple of 16 starting at a 16-byte aligned base
  *     take the vectorised path, others a scalar path with identical results.
  *   - Logits must be finite with |logit / T| < 2^23; other values give
- *     unspecified (but memory-safe) outputs.
+ *     unspecified (but memory-safe) outputs.  spec_verify_tree_sample also
+ *     takes -inf, a token of probability 0.
  *   - `workspace`: device scratch of at least spec_verify_workspace_bytes()
  *     bytes, 256-byte aligned.  Its contents on entry do not matter: every
  *     record a kernel reads is written earlier in the same call, so one
@@ -49,10 +50,14 @@
  *     kernels of spec_verify_greedy, spec_verify_tree_greedy and (for short
  *     per-CTA ranges) spec_verify_sample start reading their logits (and
  *     sampling its draft tokens) before that wait, while the call before
- *     them on the stream is finishing.  So the inputs of a call must not be
- *     written by the library call issued just before it on the same stream
- *     (a kernel of the caller's own, issued between two calls, has always
- *     finished before the next call's kernels start).
+ *     them on the stream is finishing.  So the logits and draft tokens of
+ *     these three must not be written by the library call issued just before
+ *     them on the same stream (a kernel of the caller's own, issued between
+ *     two calls, has always finished before the next call's kernels start).
+ *     All other calls read nothing before that wait, and may take what the
+ *     call before them writes: spec_tree_grow, spec_tree_attention_mask,
+ *     spec_tree_qkv_rope, spec_tree_attention, spec_verify_tree_sample and
+ *     spec_kv_commit_path can be issued one after the other.
  */
 #ifndef SPEC_VERIFY_H_
 #define SPEC_VERIFY_H_

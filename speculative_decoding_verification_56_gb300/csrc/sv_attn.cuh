@@ -142,11 +142,11 @@ struct AttnWalk {
       s->pair = p.pair_s;
     } else {
       const int per = p.Hkv * p.mg_o;
-      int base = __ldg(p.base_len + b);
+      int base = p.base_len[b];
       tiles = attn_tiles_of(p, base);
       while (pos >= bstart + (long long)per * tiles) {
         bstart += (long long)per * tiles;
-        base = __ldg(p.base_len + ++b);
+        base = p.base_len[++b];
         tiles = attn_tiles_of(p, base);
       }
       it = (pos - bstart) / tiles;
@@ -361,14 +361,17 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   // global memory is touched before that grid has finished
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
+  // (lengths and masks, which the call before this one may have written, are read
+  // with ordinary loads: those that may be taken out of order are for data that
+  // stays as it is while a kernel lives)
   // the run [lo, hi) of this CTA and the sequence it starts in: a scan of the
   // sequences' tile counts, kAtThreads sequences at a time
   const int per = p.Hkv * p.mg_o;
   const long long shared = (long long)p.Hkv * p.mg_s * p.tiles_s;
-  int mine = (int)threadIdx.x < p.B ? attn_tiles_of(p, __ldg(p.base_len + threadIdx.x)) : 0;
+  int mine = (int)threadIdx.x < p.B ? attn_tiles_of(p, p.base_len[threadIdx.x]) : 0;
   long long own = mine;
   for (int b = threadIdx.x + kAtThreads; b < p.B; b += kAtThreads)
-    own += attn_tiles_of(p, __ldg(p.base_len + b));
+    own += attn_tiles_of(p, p.base_len[b]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) own += __shfl_xor_sync(0xffffffffu, own, o);
   if (lane == 0) s_sum[warp] = own;
@@ -387,7 +390,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     long long run = 0;
     for (int b0 = 0; b0 < p.B; b0 += kAtThreads) {
       const int b = b0 + threadIdx.x;
-      if (b0 > 0) mine = b < p.B ? attn_tiles_of(p, __ldg(p.base_len + b)) : 0;
+      if (b0 > 0) mine = b < p.B ? attn_tiles_of(p, p.base_len[b]) : 0;
       long long incl = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -671,7 +674,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             if (seg.shared || j >= p.W) return 0u;
             uint32_t x;
             if (p.mask) {
-              x = mrow ? __ldg(mrow + j) : 0u;
+              x = mrow ? mrow[j] : 0u;
             } else {
               const int c = node + 1 - 32 * j;
               x = c >= 32 ? 0xFFFFFFFFu : c <= 0 ? 0u : (1u << c) - 1u;
@@ -992,7 +995,7 @@ __global__ void __launch_bounds__(kAtFinThreads, E * A <= 32 ? 3 : 2)
   const unsigned ng = (unsigned)p.N * p.G, bh = at / ng, in_bh = at - bh * ng;
   const int n = (int)(in_bh / p.G), g = (int)(in_bh - (unsigned)n * p.G);
   const int b = (int)(bh / p.Hkv), h = (int)(bh - (unsigned)b * p.Hkv);
-  const bool ok = attn_seq_ok(p, __ldg(p.base_len + b));
+  const bool ok = attn_seq_ok(p, p.base_len[b]);
   float m = -1e30f, l = 0.0f, acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.0f;

@@ -141,8 +141,9 @@ __global__ void __launch_bounds__(kRopeThreads) tree_qkv_rope_kernel(const RopeP
     r0 = ldg_stream(src + (size_t)h * D + c0 * 8);
     r1 = ldg_stream(src + (size_t)h * D + c1 * 8);
   }
-  const int base = __ldg(p.base_len + b);
-  int dep = p.depth ? __ldg(p.depth + node) : v;
+  // (ordinary loads: the call before this one may have written them)
+  const int base = p.base_len[b];
+  int dep = p.depth ? p.depth[node] : v;
   const bool ok = base >= 1 && (long long)base + p.N - 1 <= p.L;
   if (threadIdx.x == 0) {
     if (!ok && v == 0) set_flag(p.flags, kFlagBadPath);

@@ -618,7 +618,7 @@ __global__ void __launch_bounds__(kTsThreads, 4) tree_sample_kernel(const TreeSa
     } else {
       if (x >= 0) {
         for (int v = cur + 1 + threadIdx.x; v < p.N; v += kTsThreads)
-          if (__ldg(par + v) == cur && __ldg(tok + v) == x) atomicMin(&s_child, v);
+          if (par[v] == cur && tok[v] == x) atomicMin(&s_child, v);
       }
       __syncthreads();
       child = s_child;

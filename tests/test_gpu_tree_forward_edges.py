@@ -238,3 +238,64 @@ def test_attention_runs_of_long_items_are_not_given_up():
         sv.spec_verify_set_wait_limit_ns(0)
     assert sv.spec_verify_read_flags(ws) == 0
     assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+# ---------------------------------------------------------------------------
+# calls that take what the call before them writes
+# ---------------------------------------------------------------------------
+
+def test_calls_chained_without_a_pause():
+    """Mask, heads, attention, sampling and KV commit, each on the outputs of the
+    one before, step after step with other trees and lengths and nothing in
+    between: what the same calls give with a pause after each."""
+    B, N, Hq, Hkv, D, L, V, depth, steps = 5, 24, 8, 2, 64, 400, 900, 6, 40
+    rng = np.random.default_rng(3)
+    gen = torch.Generator(device="cuda").manual_seed(3)
+
+    def randn(*shape, dtype=torch.bfloat16):
+        return torch.randn(*shape, generator=gen, dtype=dtype, device="cuda")
+
+    def ints(*shape):
+        return torch.empty(*shape, dtype=torch.int32, device="cuda")
+
+    par = torch.from_numpy(np.stack([[[-1] + [rng.integers(0, v) for v in range(1, N)] for _ in range(B)]
+                                     for _ in range(steps)]).astype(np.int32)).cuda()
+    tok = torch.from_numpy(rng.integers(0, 3, (steps, B, N)).astype(np.int32)).cuda()
+    base = torch.from_numpy(rng.integers(1, L - N, (steps, B)).astype(np.int32)).cuda()
+    qkv = randn(steps, B, N, Hq + 2 * Hkv, D)
+    z = randn(steps, B, N, V, dtype=torch.float32)
+    z[..., :3] += 8.0                      # the three tokens that nodes hold
+    u = torch.rand(steps, B, depth + 1, generator=gen, device="cuda")
+    inv = torch.linspace(1.0, 1e-3, D // 2, device="cuda")
+    cache0 = randn(2, B, L, Hkv, D)
+
+    def run(pause):
+        cache, got = cache0.clone(), []
+        ws = torch.zeros(max(sv.spec_tree_attention_workspace_bytes(B, N, Hq, Hkv, D), 256),
+                         dtype=torch.uint8, device="cuda")
+        mask, dep, q = ints(B, N, 1), ints(B, N), torch.empty(B, N, Hq, D, dtype=torch.bfloat16, device="cuda")
+        n, path, out_tok, new_len = ints(B), ints(B, depth + 1), ints(B, depth + 1), ints(B)
+        prob = torch.empty(B, depth + 1, device="cuda")
+        outs = torch.empty(steps, B, N, Hq, D, dtype=torch.bfloat16, device="cuda")
+        lens = ints(steps, B)
+        for s in range(steps):
+            calls = (lambda: sv.spec_tree_attention_mask(par[s], mask, dep, ws),
+                     lambda: sv.spec_tree_qkv_rope(qkv[s], None, None, 1e-6, inv, base[s], dep, q, cache[0],
+                                                   cache[1], ws),
+                     lambda: sv.spec_tree_attention(q, cache[0], cache[1], mask, base[s], 0.125, outs[s], None, ws),
+                     lambda: sv.spec_verify_tree_sample(z[s], tok[s], par[s], u[s], 1.0, depth, n, path, out_tok,
+                                                        prob, ws),
+                     lambda: sv.spec_kv_commit_path(cache, base[s], n, path, N, lens[s], ws))
+            for call in calls:
+                call()
+                if pause:
+                    torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        return outs, lens, cache, sv.spec_verify_read_flags(ws)
+
+    want = run(True)
+    assert want[3] & ~sv.SPEC_FLAG_DEPTH == 0 and (want[1] > base).any()
+    for _ in range(3):
+        got = run(False)
+        assert got[3] == want[3]
+        assert all(torch.equal(a, b) for a, b in zip(got[:3], want[:3]))
