@@ -299,7 +299,8 @@ SPEC_API spec_status_t spec_tree_attention_mask(const int32_t* parents, int B, i
  * and their first rot_dim elements rotated in pairs by position * inv_freq[i],
  *   (a, b) -> (a cos - b sin, b cos + a sin),
  * in float32, rounded once (angles are reduced to one turn in 64-bit integers:
- * at position 2^31 they are off by less than 1e-5 of a turn).  Queries go to
+ * an angle of A turns is off by less than A 2^-47 + 2^-24 of a turn, which at
+ * position 2^31 is 3e-6 for a frequency of 1).  Queries go to
  * q_out; keys and values go to cache position base_len[b] - 1 + v, where
  * spec_kv_commit_path expects them.
  *   qkv           bf16 [B, N, Hq + 2 Hkv, D]: query, key, value heads

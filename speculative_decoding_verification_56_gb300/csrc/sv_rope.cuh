@@ -58,11 +58,12 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return r;
 }
 // Sine and cosine of pos * f for an integer position and a float frequency.
-// The turns per position f / (2 pi) are held to 2^-64 of a turn (the product
-// as a double-float, about 2^-48 relative), multiplied by pos modulo one turn
-// in 64-bit integers, and only the remaining fraction of a turn is rounded to
-// float: far positions lose no more than near ones, and no float64
-// arithmetic (two operations per clock and SM here) is needed.
+// The turns per position f / (2 pi) are a double-float product (off by less
+// than 2^-47 of itself: the rounding of its low part and of 1 / (2 pi)), held to
+// 2^-64 of a turn, multiplied by pos modulo one turn in 64-bit integers, and
+// only the remaining fraction of a turn is rounded to float (2^-26): an angle of
+// A turns is off by A 2^-47 + 2^-25 of a turn, and no float64 arithmetic (two
+// operations per clock and SM here) is needed.
 __device__ __forceinline__ void turn_sincos(long long pos, float f, float* sn, float* cs) {
   const float inv2pi_hi = 0.15915494f;                       // nearest float to 1 / (2 pi)
   const float inv2pi_lo = 6.4206383e-09f;                    // 1 / (2 pi) - inv2pi_hi

@@ -1,6 +1,8 @@
 """Edges of the tree's verification forward on the GPU: workspaces of exactly the
 size asked for, values that are not finite, draws among very unlikely tokens,
 waits that run out, and calls that the documentation allows at its limits."""
+from fractions import Fraction
+
 import numpy as np
 import pytest
 import torch
@@ -299,3 +301,39 @@ def test_calls_chained_without_a_pause():
         got = run(False)
         assert got[3] == want[3]
         assert all(torch.equal(a, b) for a, b in zip(got[:3], want[:3]))
+
+
+# ---------------------------------------------------------------------------
+# angles of far positions
+# ---------------------------------------------------------------------------
+
+PI = Fraction(314159265358979323846264338327950288419716939937510582097494459, 10 ** 62)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_qkv_angles_are_as_exact_as_the_header_says(interleaved):
+    """Pairs (1, 0) turn into (cos, sin) of position * frequency; an angle of A
+    turns may be off by A 2^-47 + 2^-24 of a turn, and the outputs are rounded."""
+    D, Hkv = 64, 1
+    freq = np.exp(np.random.default_rng(5).uniform(np.log(1e-5), np.log(3000.0), D // 2)).astype(np.float32)
+    freq[:4] = 1.0, 0.5, 100.0, 1e-4
+    offset = 2 ** 31 - 1
+    depth = torch.tensor([[0, 1, 2, 3, 77, 1000, 123456, 2 ** 31 - 1]], dtype=torch.int32, device="cuda")
+    N = depth.shape[1]
+    qkv = torch.zeros(1, N, 1 + 2 * Hkv, D, dtype=torch.bfloat16, device="cuda")
+    qkv[..., 0::2 if interleaved else 1][..., : D // 2] = 1.0
+    kc = torch.zeros(1, N + 1, Hkv, D, dtype=torch.bfloat16, device="cuda")
+    base = torch.tensor([2], dtype=torch.int32, device="cuda")
+    q = sv.tree_qkv_rope(qkv, None, None, 1e-6, torch.from_numpy(freq).cuda(), base, depth, kc, kc.clone(),
+                         pos_offset=offset, interleaved=interleaved).double().cpu().numpy()[0, :, 0]
+    cos, sin = (q[:, 0::2], q[:, 1::2]) if interleaved else (q[:, : D // 2], q[:, D // 2:])
+    for n in range(N):
+        pos = offset + 1 + int(depth[0, n])
+        for i, f in enumerate(freq):
+            turns = pos * Fraction(float(f)) / (2 * PI)
+            angle = 2 * np.pi * float(turns - round(turns))
+            off = 2 * np.pi * (float(turns) * 2.0 ** -47 + 2.0 ** -24)
+            # a rounding to bf16, and the float32 sine and cosine's own 2 ulp
+            tol = 2.0 ** -8 + 2.0 ** -22
+            for got, want in ((cos[n, i], np.cos(angle)), (sin[n, i], np.sin(angle))):
+                assert abs(got - want) <= off + tol * (abs(want) + off), (n, i, got, want, off)
