@@ -69,6 +69,7 @@ SPEC_FLAG_EMPTY_ROW = 64
 _lock = threading.Lock()
 _lib = None
 _torch_module = None
+_current_device = _raw_stream = None
 
 
 class SpecVerifyError(RuntimeError):
@@ -144,11 +145,22 @@ def load_library(path: str = LIB_PATH):
 # ---------------------------------------------------------------------------
 
 def _torch():
-    global _torch_module
+    global _torch_module, _current_device, _raw_stream
     if _torch_module is None:
         import torch
+        _current_device, _raw_stream = _device_getters(torch)
         _torch_module = torch
     return _torch_module
+
+
+def _device_getters(torch):
+    """Functions that give the current device's index and a device's current
+    stream as an integer: torch's internal ones (a small rotation's call takes
+    10.6 us with them, 11.4 with the public device getter) or, where a torch
+    does not have them, the public ones."""
+    device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return device, stream or (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _dtype_code(t) -> int:
@@ -196,7 +208,8 @@ def _call_device(t, name):
     dev = t.get_device()
     if dev < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if dev != _torch()._C._cuda_getDevice():  # (CUDA is initialised: t is there)
+    _torch()
+    if dev != _current_device():  # (CUDA is initialised: t is there)
         raise ValueError(f"{name} is on cuda:{dev}, which is not the current device")
     return dev
 
@@ -234,7 +247,8 @@ def _stream_of(stream, device):
     """_stream_ptr for a call on a known device (the current one)."""
     if stream is not None:
         return _stream_ptr(stream)
-    return _torch()._C._cuda_getCurrentRawStream(device)
+    _torch()
+    return _raw_stream(device)
 
 
 def _stream_ptr(stream):

@@ -137,3 +137,13 @@ def test_attention_workspace_holds_what_the_join_reads(lib, B, N, Hq, Hkv, D, P)
     need = 256 + items * 8 + held * (4 * D + 8)     # flags, spans; row: D floats, reference and sum
     got = sv.spec_tree_attention_workspace_bytes(B, N, Hq, Hkv, D, P)
     assert need <= got < need + 4 * 256             # parts start at multiples of 256
+
+
+def test_device_getters_without_torch_internals():
+    from types import SimpleNamespace as NS
+    public = NS(_C=NS(), cuda=NS(current_device=lambda: 3, current_stream=lambda i: NS(cuda_stream=100 + i)))
+    device, stream = sv._device_getters(public)
+    assert device() == 3 and stream(2) == 102
+    public._C = NS(_cuda_getDevice=lambda: 1, _cuda_getCurrentRawStream=lambda i: 200 + i)
+    device, stream = sv._device_getters(public)
+    assert device() == 1 and stream(2) == 202
