@@ -237,6 +237,14 @@ def _cache_args(k_cache, v_cache, Hkv, D, B, device):
                      "of a sequence contiguous")
 
 
+def _cache_heads(k_cache):
+    """Key-value heads of a cache, for the conveniences, which size their
+    allocations by it before the call checks its arguments."""
+    if k_cache.dim() != 4:
+        raise ValueError(f"k_cache must be [B, L, heads, D], got {list(k_cache.shape)}")
+    return k_cache.shape[2]
+
+
 def _workspace(t, device):
     if t.get_device() != device or not t.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on cuda:{device}")
@@ -756,9 +764,12 @@ def tree_qkv_rope(qkv, q_norm, k_norm, eps, inv_freq, base_len, depth, k_cache, 
                                  v_cache, pos_offset, interleaved, workspace)
     torch = _torch()
     B, N, H, D = qkv.shape
+    Hq = H - 2 * _cache_heads(k_cache)
+    if Hq < 1:
+        raise ValueError(f"qkv holds {H} heads, of which {H - Hq} are keys and values: no query head")
     if workspace is None:
         workspace = alloc_workspace(SPEC_MODE_TREE_QKV, B, N, 1, SPEC_DTYPE_BF16, qkv.device)
-    q = torch.empty(B, N, H - 2 * k_cache.shape[2], D, dtype=qkv.dtype, device=qkv.device)
+    q = torch.empty(B, N, Hq, D, dtype=qkv.dtype, device=qkv.device)
     spec_tree_qkv_rope(qkv, q_norm, k_norm, eps, inv_freq, base_len, depth, q, k_cache, v_cache,
                        workspace, pos_offset, interleaved, stream)
     return q
@@ -769,7 +780,7 @@ def alloc_tree_attention_workspace(q, k_cache, prefix_k=None):
     is zero; the rest needs no value)."""
     torch = _torch()
     B, N, Hq, D = q.shape
-    n = spec_tree_attention_workspace_bytes(B, N, Hq, k_cache.shape[2], D,
+    n = spec_tree_attention_workspace_bytes(B, N, Hq, _cache_heads(k_cache), D,
                                             0 if prefix_k is None else prefix_k.shape[0])
     if n == 0:
         raise ValueError("shape outside the library's limits")

@@ -147,3 +147,18 @@ def test_device_getters_without_torch_internals():
     public._C = NS(_cuda_getDevice=lambda: 1, _cuda_getCurrentRawStream=lambda i: 200 + i)
     device, stream = sv._device_getters(public)
     assert device() == 1 and stream(2) == 202
+
+
+def test_conveniences_refuse_caches_of_another_rank(lib):
+    torch = pytest.importorskip("torch")
+    bf16 = dict(dtype=torch.bfloat16)
+    qkv, q = torch.zeros(1, 2, 8, 64, **bf16), torch.zeros(1, 2, 4, 64, **bf16)
+    one = torch.ones(1, dtype=torch.int32)
+    for cache in (torch.zeros(9, 64, **bf16), torch.zeros(1, 9, 64, **bf16), torch.zeros(1, 1, 9, 2, 64, **bf16)):
+        with pytest.raises(ValueError, match="k_cache"):
+            sv.tree_qkv_rope(qkv, None, None, 1e-6, None, one, None, cache, cache)
+        with pytest.raises(ValueError, match="k_cache"):
+            sv.tree_attention(q, cache, cache, None, one)
+    four = torch.zeros(1, 9, 4, 64, **bf16)
+    with pytest.raises(ValueError, match="no query head"):
+        sv.tree_qkv_rope(qkv, None, None, 1e-6, None, one, None, four, four)
