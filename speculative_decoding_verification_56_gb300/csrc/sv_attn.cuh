@@ -25,16 +25,21 @@
 // slots, 2 c (+ 1 if the item begins in CTA c).  Shared and own items have
 // slots of their own sizes.
 //
-// Measured (32 query heads of 8, D = 128): plain decoding of 64 sequences of
-// about 3000 entries 136 us, 5.9 TB/s, bound by HBM; 16 trees of 60 nodes over
-// as many 68.5 us (a floor of 33 us of HBM time); 3 trees of 33 (40 heads) over
-// 49000 entries 132 us under the power cap (91 us); 64 trees of 16 behind a
-// shared prefix of 8192 181 us (77 us of tensor time).  Trees are bound by the
-// hand-over between softmax and products: a pair of halves takes about 3400
-// clocks a tile, 2048 of them products (16 of K = 16 for S, as many for O, 64
-// clocks each and half), because one half's chain -- its scores 490, softmax
-// 1600, its product with V 630 and the hand-overs -- is longer than the other
-// half's products beside it.  What was tried against it and lost (16 trees /
+// Measured (32 query heads of 8, D = 128; ranges over boxes): plain decoding of
+// 64 sequences of about 3000 entries 132-139 us, 5.9 TB/s, bound by HBM; 16 trees
+// of 60 nodes over as many 65-71 us (a floor of 33 us of HBM time); 3 trees of 33
+// (40 heads) over 49000 entries 121-145 us under the power cap (91 us); 64 trees
+// of 16 behind a shared prefix of 8192 180-185 us (77 us of tensor time).  In the
+// loop trees are bound by the hand-over between softmax and products: a pair of
+// halves takes 3200-3600 clocks a tile, 2048 of them products (16 of K = 16 for
+// S, as many for O, 64 clocks each and half), because one half's chain -- its
+// scores 490, softmax 1600, its product with V 630 and the hand-overs -- is longer
+// than the other half's products beside it.  Outside the loop: start, fills and
+// stores 9 of the 16 trees' 70 us, CTAs of unequal length 6, the wait for the
+// join 8 and the join 10; behind a shared prefix the CTAs of short own items (15
+// items of 4-5 tiles, 20500 clocks each) end at 184 us, those of the prefix at
+// 120-153.  D = 64 (half the bytes and products): 107, 56, 114 and 155 us.  What
+// was tried against it and lost (16 trees /
 // long / shared prefix, us, then 69 / 137 / 182): one issuing warp per half 79 /
 // 199 / 197; P handed over in two parts 78 / 153 / 233; scores loaded 64 or 128
 // columns at once 81 / 145 / 184 and 78 / 141 / 177 (the products with V slow

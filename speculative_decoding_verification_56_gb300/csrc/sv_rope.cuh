@@ -24,7 +24,10 @@
 // 5.4 TB/s, 81% of a plain copy's rate.  64 threads a CTA, so that ends and
 // starts of nodes overlap (128 threads 37.2 us, 256 threads 50.8); loads one
 // head ahead (two heads ahead 36.0 us: fewer CTAs fit); scalar arithmetic 44.5.
-// A single tree of 60 nodes takes what a launch takes.
+// A single tree of 60 nodes takes what a launch takes.  Other forms at that size:
+// pairs side by side 37.2 us; halves that are not whole vectors, whose partners
+// are read from memory, 77 us (3 elements) to 103 (60); D = 64 18.5 and, side by
+// side, 19.1 (95 MB).
 #pragma once
 
 #include "sv_device.cuh"

@@ -41,9 +41,10 @@
 // No float64 arithmetic is on the way: it runs at two operations per
 // clock and SM here, and the sums of 16 CTAs alone took 16 us of a step.
 //
-// Measured (V = 128256 bf16, walks of 2.7 rows): one sequence 15.5 us, 16 of
-// them 27 us (their longest walks count), 64 of V = 151936 float32 62 us; about
-// 4 us a step (clocks: screen 1700, the CTA's sum 680, exchange 1650, search
+// Measured (V = 128256 bf16): one sequence 8-21 us by the length of its walk, 16
+// of them 21-31 (their longest walks count: 5 rows 21, 7 rows 28), 64 of
+// V = 151936 float32 60-70 us; about 4.2 us a step (5.8 where V = 128257 has rows
+// read element by element) (clocks: screen 1700, the CTA's sum 680, exchange 1650, search
 // 480, token 2700, child 460), against 0.1 to 15 us of HBM time for the rows.
 // Tried against the exchanges and lost: words counted by mbarriers in place of
 // the cluster's barriers 17.5 us at one sequence and 30.1 at 16; the rows of the
