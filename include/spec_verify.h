@@ -47,8 +47,9 @@
  *     stream to finish (and its writes to be visible) before it writes
  *     memory or reads anything but its logits, and the last kernel of a call
  *     lets the next kernel in the stream be scheduled early.  The streaming
- *     kernels of spec_verify_greedy, spec_verify_tree_greedy and (for short
- *     per-CTA ranges) spec_verify_sample start reading their logits (and
+ *     kernels of spec_verify_greedy (and its _noalloc form),
+ *     spec_verify_tree_greedy and (for short per-CTA ranges)
+ *     spec_verify_sample start reading their logits (and
  *     sampling its draft tokens) before that wait, while the call before
  *     them on the stream is finishing.  So the logits and draft tokens of
  *     these three must not be written by the library call issued just before

@@ -533,7 +533,7 @@ spec_status_t launch_tree_sample(const sv::TreeSampleParams& prm, int B, int clu
 // Tiles and partial slots of spec_tree_attention for one call shape.
 struct AttnPlan {
   int tok = 0, pair_s = 0, pair_o = 0, mg_s = 0, mg_o = 0, rows_s = 0, rows_o = 0, by_cta = 0;
-  long long own0 = 0;  // rows of the shared items' slots, which come first
+  long long own0 = 0;  // row of the own items' slot 0, behind the shared ones
   size_t off_ml = 0, off_part = 0, bytes = 0;
 };
 
@@ -544,10 +544,13 @@ struct AttnPlan {
 // 254 instead of 184 (a shared prefix); two halves throughout: decoding 154.8
 // instead of 136.3 us.
 // Slots: shared and own items have slots of their own sizes.  Behind a shared
-// prefix every own item leaves a partial, and each cut one more: items + CTAs
-// slots.  Without one, only cut items do, at most two a CTA (the item that it
-// begins with and the one that it ends with), which is less from kAtMaxCtas
-// items on (by_cta).
+// prefix every item leaves a partial, and each cut one more: items + CTAs slots
+// in all.  If CTA c holds the last shared tile, the shared items' slots (item +
+// CTA) end below row (items_s + c) rows_s, and the own items' begin at own0 +
+// c rows_o, so own0 = items_s rows_s + CTAs (rows_s - rows_o) keeps them apart
+// for every c.  Without a prefix, only cut items leave partials, at most two a
+// CTA (the item that it begins with and the one that it ends with), which is
+// less from kAtMaxCtas items on (by_cta).
 AttnPlan attn_plan(int B, int N, int Hq, int Hkv, int D, int P) {
   AttnPlan a;
   const int G = Hq / Hkv;
@@ -557,18 +560,17 @@ AttnPlan attn_plan(int B, int N, int Hq, int Hkv, int D, int P) {
   a.mg_o = (N + (a.tok << a.pair_o) - 1) / (a.tok << a.pair_o);
   a.rows_o = std::min(N, a.tok << a.pair_o) * G;
   const size_t items_o = (size_t)B * Hkv * a.mg_o;
-  size_t items_s = 0, slots_s = 0, slots_o = items_o + sv::kAtMaxCtas;
+  size_t items_s = 0, slots_o = items_o + sv::kAtMaxCtas;
   if (P > 0) {
     a.pair_s = all > a.tok;
     a.mg_s = (int)((all + (a.tok << a.pair_s) - 1) / (a.tok << a.pair_s));
     a.rows_s = (int)std::min<long long>(all, a.tok << a.pair_s) * G;
     items_s = (size_t)Hkv * a.mg_s;
-    slots_s = items_s + sv::kAtMaxCtas;
+    a.own0 = (long long)items_s * a.rows_s + (long long)sv::kAtMaxCtas * (a.rows_s - a.rows_o);
   } else if (items_o > (size_t)sv::kAtMaxCtas) {
     a.by_cta = 1;
     slots_o = 2 * (size_t)sv::kAtMaxCtas;
   }
-  a.own0 = (long long)slots_s * a.rows_s;
   const size_t rows = (size_t)a.own0 + slots_o * a.rows_o;
   a.off_ml = align_up(kDataOffset + (items_s + items_o) * sizeof(int2));
   a.off_part = align_up(a.off_ml + rows * sizeof(float2));

@@ -91,7 +91,7 @@ struct AttnParams {
   int tiles_s;              // ceil(P / 128)
   int rows_s, rows_o;       // rows of a slot of a shared / own item
   int by_cta;               // own items' slots by CTA (else by item)
-  long long own0;           // first row of the own items' slots
+  long long own0;           // row of the own items' slot 0
   int nctas;
   int q_tiles;              // 2 if any item is a pair
   float* opart;             // [slot][D / 4][rows][4]

@@ -120,7 +120,7 @@ def test_tree_attention_scale_stays_finite(lib):
 ])
 def test_attention_workspace_holds_what_the_join_reads(lib, B, N, Hq, Hkv, D, P):
     """Slots of an item's own rows: one part of every item behind a shared prefix
-    and one more a CTA; without a prefix two a CTA at most."""
+    and one more a CTA (of the larger kind); without a prefix two a CTA at most."""
     ctas, tok = 160, 128 // (Hq // Hkv)
 
     def items_and_rows(nodes):
@@ -132,7 +132,7 @@ def test_attention_workspace_holds_what_the_join_reads(lib, B, N, Hq, Hkv, D, P)
     held = (items + ctas if P else min(items + ctas, 2 * ctas)) * rows
     if P:
         mg, rows = items_and_rows(B * N)
-        held += (Hkv * mg + ctas) * rows
+        held += Hkv * mg * rows + ctas * (rows - min(N, 2 * tok if N > tok else tok) * (Hq // Hkv))
         items += Hkv * mg
     need = 256 + items * 8 + held * (4 * D + 8)     # flags, spans; row: D floats, reference and sum
     got = sv.spec_tree_attention_workspace_bytes(B, N, Hq, Hkv, D, P)
@@ -162,3 +162,19 @@ def test_conveniences_refuse_caches_of_another_rank(lib):
     four = torch.zeros(1, 9, 4, 64, **bf16)
     with pytest.raises(ValueError, match="no query head"):
         sv.tree_qkv_rope(qkv, None, None, 1e-6, None, one, None, four, four)
+
+
+def test_attention_workspace_is_never_more_than_slots_of_one_size(lib):
+    """items + CTAs slots that all hold the largest kind's rows."""
+    for B in (1, 2, 17, 64, 1000):
+        for N in (1, 5, 33, 60, 500):
+            for Hq, Hkv in ((8, 8), (32, 8), (71, 1), (15, 3)):
+                for P in (0, 1, 5000):
+                    G, tok = Hq // Hkv, 128 // (Hq // Hkv)
+
+                    def per(nodes):
+                        return 2 * tok if nodes > tok else tok
+                    items = B * Hkv * -(-N // per(N)) + (Hkv * -(-B * N // per(B * N)) if P else 0)
+                    rows = min(tok, B * N if P else N) * G * (2 if max(N, B * N if P else 0) > tok else 1)
+                    most = 256 + items * 8 + (items + 160) * rows * (4 * 128 + 8) + 4 * 256
+                    assert sv.spec_tree_attention_workspace_bytes(B, N, Hq, Hkv, 128, P) <= most, (B, N, Hq, Hkv, P)
