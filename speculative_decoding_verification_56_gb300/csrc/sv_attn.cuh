@@ -25,7 +25,7 @@
 // slots, 2 c (+ 1 if the item begins in CTA c).  Shared and own items have
 // slots of their own sizes.
 //
-// Measured (32 query heads of 8, D = 128; ranges over boxes): plain decoding of
+// Measured (32 query heads of 8, D = 128; ranges over several runs): plain decoding of
 // 64 sequences of about 3000 entries 132-139 us, 5.9 TB/s, bound by HBM; 16 trees
 // of 60 nodes over as many 65-71 us (a floor of 33 us of HBM time); 3 trees of 33
 // (40 heads) over 49000 entries 121-145 us under the power cap (91 us); 64 trees
