@@ -98,8 +98,8 @@ def draw(rng):
 
 
 # ---------------------------------------------------------------------------
-# the pages' format: of one head, codes of the keys [page, D / 2], their scales
-# [page, D / 16], codes of the values, their scales
+# the pages' format: of one head, 16 positions after 16 positions, codes of the
+# keys [16, D / 2], their scales [16, D / 16], codes of the values, their scales
 # ---------------------------------------------------------------------------
 
 def _block_bytes(case):
@@ -107,11 +107,12 @@ def _block_bytes(case):
 
 
 def _parts(pages, page, D):
-    """Views of the pages' four parts, [..., heads, page, bytes]."""
+    """Views of the pages' four parts, [..., heads, page / 16, 16, bytes]."""
     out, at = [], 0
+    pages = pages.unflatten(-1, (page // 16, 18 * D))
     for width in (D // 2, D // BLOCK) * 2:
-        out.append(pages[..., at: at + page * width].unflatten(-1, (page, width)))
-        at += page * width
+        out.append(pages[..., at: at + 16 * width].unflatten(-1, (16, width)))
+        at += 16 * width
     return out
 
 
@@ -239,7 +240,7 @@ def prepare(case, seed):
             n = min(512, n_pages - p0)
             for c, sc, j in ((kc, ks, 0), (vc, vs, 1)):
                 code, scale = _encode(normal(n, Hkv, page, D).float() * (1.0 if j == 0 else 0.5), exps[layer, j])
-                c[layer, p0: p0 + n], sc[layer, p0: p0 + n] = code, scale
+                c[layer, p0: p0 + n], sc[layer, p0: p0 + n] = code.unflatten(2, (-1, 16)), scale.unflatten(2, (-1, 16))
     chain = case.get("chain", not case.get("path", False))
     par, dep, anc = _trees(rng, B, N, 8, chain) if not chain else (None, None, None)
     s.update(pages=pages, table=table, base=cuda(base), exps=exps)
@@ -340,8 +341,8 @@ def _gathered(s, layer):
     at = s["table"].long()
 
     def take(codes, scales, e):
-        y = _decode(codes[at], scales[at], e)  # [B, W, Hkv, page, D]
-        return y.permute(0, 1, 3, 2, 4).flatten(1, 2)
+        y = _decode(codes[at], scales[at], e)  # [B, W, Hkv, page / 16, 16, D]
+        return y.permute(0, 1, 3, 4, 2, 5).flatten(1, 3)
 
     return take(kc, ks, s["exps"][layer, 0]), take(vc, vs, s["exps"][layer, 1])
 
@@ -389,8 +390,8 @@ def _plain_store(s):
     for layer in range(layers):
         for j, x in ((0, s["nk"]), (1, s["nv"])):
             code, scale = _encode(x[layer][rows, node].float(), s["exps"][layer, j])
-            parts[2 * j][layer].transpose(1, 2)[pid, slot] = code
-            parts[2 * j + 1][layer].transpose(1, 2)[pid, slot] = scale
+            parts[2 * j][layer].permute(0, 2, 3, 1, 4)[pid, slot // 16, slot % 16] = code
+            parts[2 * j + 1][layer].permute(0, 2, 3, 1, 4)[pid, slot // 16, slot % 16] = scale
         for y, out in zip(_gathered(s, layer), (s["k"], s["v"])):
             out[layer] = torch.where(seen, y[:, :L].to(torch.bfloat16), out[layer])
     return dict(new_len=new_len, k=s["k"], v=s["v"])
@@ -530,9 +531,9 @@ def _exact_values(c, s, layer, b, n, j):
     """Keys (j = 0) or values of positions [0, n) of a sequence, float64 [n, Hkv, D]."""
     page, D = c["page"], c["D"]
     block = s["pages"][layer][s["table"][b, : -(-n // page)].long()].long()
-    at = j * page * D * 9 // 16
-    codes = block[..., at: at + page * D // 2].reshape(*block.shape[:2], page, D // 2)
-    scales = block[..., at + page * D // 2: at + page * D * 9 // 16].reshape(*block.shape[:2], page, D // 16)
+    block = block.reshape(*block.shape[:2], page // 16, 2, 9 * D)[:, :, :, j]
+    codes = block[..., : 8 * D].reshape(*block.shape[:2], page, D // 2)
+    scales = block[..., 8 * D:].reshape(*block.shape[:2], page, D // 16)
     x = torch.empty(*codes.shape[:3], D, dtype=torch.float64, device="cuda")
     for k in (0, 1):
         y = (codes >> (4 * k)) & 15
