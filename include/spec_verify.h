@@ -58,7 +58,8 @@
  *     All other calls read nothing before that wait, and may take what the
  *     call before them writes: spec_tree_grow, spec_tree_attention_mask,
  *     spec_tree_qkv_rope, spec_tree_attention, spec_verify_tree_sample and
- *     spec_kv_commit_path can be issued one after the other.
+ *     spec_kv_commit_path can be issued one after the other, and so can the
+ *     calls on the 4-bit cache, on pages and on beams.
  */
 #ifndef SPEC_VERIFY_H_
 #define SPEC_VERIFY_H_
@@ -100,7 +101,8 @@ typedef enum {
   SPEC_MODE_TREE_GROW = 6,      /* spec_tree_grow (k_or_N = K children per node) */
   SPEC_MODE_LM_HEAD_SAMPLE = 7, /* spec_lm_head_verify_sample (k_or_N = k, d <= SPEC_LM_MAX_D) */
   SPEC_MODE_TREE_SAMPLE = 8,    /* spec_verify_tree_sample: the flag header only */
-  SPEC_MODE_TREE_QKV = 10       /* spec_tree_qkv_rope: the flag header only */
+  SPEC_MODE_TREE_QKV = 10,      /* spec_tree_qkv_rope: the flag header only */
+  SPEC_MODE_KV4 = 11            /* spec_kv4_commit_path, spec_kv4_read: the flag header only */
 } spec_mode_t;
 
 /* Bits of the workspace flag word (sticky until read with clear != 0). */
@@ -120,9 +122,13 @@ typedef enum {
                                           max_depth, or a tree that does not fit
                                           the cache; that sequence is untouched.
                                           spec_tree_qkv_rope, spec_tree_attention:
-                                          a tree that does not fit the cache */
+                                          a tree that does not fit the cache;
+                                          the calls on pages: a length outside
+                                          the table (see each call) */
 #define SPEC_FLAG_EMPTY_ROW 64u        /* spec_verify_tree_sample: a row on the walk
                                           without a finite logit; no token drawn */
+#define SPEC_FLAG_BAD_PAGE 128u        /* an entry of a page table that is needed names no page */
+#define SPEC_FLAG_NO_PAGE 256u         /* spec_kv_pages_fork: no free page left */
 
 /* Limits checked on the host. */
 #define SPEC_MAX_V (1 << 26)
@@ -505,6 +511,216 @@ SPEC_API spec_status_t spec_tree_grow(const void* draft_logits, int dtype, float
                                       int B, int D, int K, int V, int M, int32_t* tokens,
                                       int32_t* parents, int32_t* depth, float* values,
                                       void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * spec_tree_qkv_rope for a cache in pages: the same norms, rotation and
+ * queries, but node v's key and value go to place v of k_out and v_out
+ * (bf16 [B, N, Hkv, D], 16-byte aligned), where spec_tree_attention_kv4 and
+ * spec_kv4_commit_path take them.  A sequence with base_len < 1 gets queries of
+ * 0, writes no key or value and raises SPEC_FLAG_BAD_PATH.  One launch;
+ * workspace as spec_tree_qkv_rope.
+ */
+SPEC_API spec_status_t spec_tree_qkv_rope_nodes(const void* qkv, const void* q_norm,
+                                                const void* k_norm, float eps,
+                                                const float* inv_freq, int rot_dim,
+                                                int interleaved, long long pos_offset,
+                                                const int32_t* base_len, const int32_t* depth,
+                                                int B, int N, int Hq, int Hkv, int D, void* q_out,
+                                                void* k_out, void* v_out, void* workspace,
+                                                size_t workspace_bytes, void* stream);
+
+/*
+ * A key-value cache in pages of 4-bit values (a deployment format: the pages
+ * cited above fix only which entries a node sees and which are kept, "The
+ * Complete EAGLE-3 Inference Process" steps 3 and 5).
+ *
+ *   pages       uint8 [layers, n_pages, Hkv, block], 16-byte aligned: a page
+ *               holds page_size positions (16, 32, 64 or 128) of one layer.  The
+ *               block of a head is 9 page_size D / 8 bytes: for each 16
+ *               positions key codes [16, D/2], key scales [16, D/16], value
+ *               codes, value scales
+ *   page_table  int32 [B, W]: position t of sequence b stands in page
+ *               page_table[b, t / page_size], at place t % page_size, in every
+ *               layer; sequences may share pages
+ *   kv_exp      int32 [layers, 2] or NULL (all 0): exponents e of a layer's keys
+ *               and values (beyond +-64 taken as that)
+ * 16 channels of a head share a scale: with a = max |x|,
+ *   s = e4m3(min(448, a / 6 * 2^-e)),  code = e2m1(x / (s 2^e)),
+ *   value = code * s * 2^e,
+ * both to nearest even, codes saturating at 6 (all codes 0 where s is 0), the
+ * even channel in a byte's low half.  Values are exact in bf16.  A good e keeps
+ * s between 2^-6 and 448: a between 0.1 * 2^e and 2688 * 2^e.
+ *
+ * spec_kv4_commit_path writes the accepted path of B sequences into the pages
+ * of all layers.  For the path 0, v_1, ..., v_d (d = accepted_len[b]) node
+ * v_i's key and value go to position base_len[b] - 1 + i (the root, node 0, is
+ * the last committed token: its entry is written too), and new_len[b] =
+ * base_len[b] + d, the number of positions that hold entries.
+ *   node_k, node_v  bf16 [layers, B, N, Hkv, D], finite
+ *   base_len        int32 [B], at least 1
+ *   accepted_len    int32 [B], 0..min(max_depth, N - 1); NULL: N - 1
+ *   path_nodes      int32 [B, max_depth + 1], needs accepted_len; or NULL: a
+ *                   chain, v_i = i (max_depth is not looked at).  With neither,
+ *                   all N nodes are written: a prompt, or a part of one
+ * All positions' table entries must name pages that no other sequence reads
+ * there (spec_kv_pages_fork sees to that).  A sequence with a malformed path
+ * (SPEC_FLAG_BAD_PATH) or a needed table entry that names no page
+ * (SPEC_FLAG_BAD_PAGE) is left untouched, with new_len = max(base_len - 1, 0).
+ * Elements that are not finite give unspecified values of their scale's 16.
+ * One launch.  Workspace: spec_verify_workspace_bytes(SPEC_MODE_KV4, ...) bytes
+ * (the flag header).  D is 64 or 128, N at most SPEC_MAX_TREE_NODES, W at most
+ * SPEC_KV_MAX_TABLE.
+ */
+#define SPEC_KV_MAX_TABLE (1 << 20)
+#define SPEC_KV_MAX_PAGES (1 << 24) /* of spec_kv_pages_fork and _compact */
+SPEC_API spec_status_t spec_kv4_commit_path(void* pages, int layers, long long n_pages,
+                                            int page_size, int Hkv, int D,
+                                            const int32_t* page_table, int W, const void* node_k,
+                                            const void* node_v, const int32_t* base_len,
+                                            const int32_t* accepted_len, const int32_t* path_nodes,
+                                            int max_depth, const int32_t* kv_exp, int B, int N,
+                                            int32_t* new_len, void* workspace,
+                                            size_t workspace_bytes, void* stream);
+
+/*
+ * The first length[b] positions of B sequences, all layers, back in bf16 (a
+ * prefix for spec_tree_attention, or another consumer's cache).
+ *   length        int32 [B], 0..L (others are cut to that and raise
+ *                 SPEC_FLAG_BAD_PATH)
+ *   k_out, v_out  bf16: position t of sequence b and layer l starts l *
+ *                 layer_stride + b * seq_stride + t * Hkv * D * 2 bytes in; both
+ *                 strides multiples of 16, the arrays 16-byte aligned.  Positions
+ *                 from length[b] on keep their contents
+ * Positions whose table entry names no page read as 0 (SPEC_FLAG_BAD_PAGE).
+ * One launch; workspace as spec_kv4_commit_path.
+ */
+SPEC_API spec_status_t spec_kv4_read(const void* pages, int layers, long long n_pages,
+                                     int page_size, int Hkv, int D, const int32_t* page_table,
+                                     int W, const int32_t* length, const int32_t* kv_exp, int B,
+                                     int L, void* k_out, void* v_out, long long layer_stride,
+                                     long long seq_stride, void* workspace, size_t workspace_bytes,
+                                     void* stream);
+
+/*
+ * spec_tree_attention over one layer of a 4-bit cache in pages: query head
+ * h G + g of node v of sequence b attends to
+ *   - the committed positions [0, base_len[b] - 1), in the pages;
+ *   - the tree's nodes u < N of the node's mask row (NULL: u <= v, a chain),
+ *     whose keys and values are still bf16.
+ *   q, out          bf16 [B, N, Hq, D];  lse float [B, N, Hq] or NULL
+ *   pages           uint8 [n_pages, Hkv, block] (one layer, see above)
+ *   node_k, node_v  bf16 [B, N, Hkv, D]; magnitudes beyond 65504 * 2^e count as
+ *                   that (the cache itself holds up to 2688 * 2^e)
+ *   mask, base_len, scale  as spec_tree_attention;  kv_exp int32 [2] or NULL
+ * N = 1 without a mask is plain decoding.  A node that sees nothing gets out = 0
+ * and lse = -inf.  Entries that a node does not see are never used, whatever
+ * they hold; a node's entry with an element that is not finite makes out and
+ * lse NaN for the query heads that see it, and so does a query element that is
+ * not finite for its own head.  Positions whose table entry names no page are
+ * not seen (SPEC_FLAG_BAD_PAGE); a sequence with base_len < 1 or more than W *
+ * page_size committed positions gets out = 0, lse = -inf and raises
+ * SPEC_FLAG_BAD_PATH.
+ * Queries and weights are rounded to fp16 (queries at a power of two that
+ * brings a head's largest element to 2^14, weights at 2^7: both have at least
+ * bf16's 8 bits down to 2^-24 of the largest), the cached values are exact in
+ * fp16, sums are float32.  Limits as spec_tree_attention (D 64 or 128, G at most
+ * 128, N at most SPEC_ATTN_MAX_NODES); W * page_size at most 2^31 - 257.  Two
+ * launches; the cut of the work, and so the last bits, depend on base_len and
+ * the number of SMs alone.  Workspace: at least
+ * spec_tree_attention_kv4_workspace_bytes() bytes.
+ */
+SPEC_API size_t spec_tree_attention_kv4_workspace_bytes(int B, int N, int Hq, int Hkv, int D);
+SPEC_API spec_status_t spec_tree_attention_kv4(const void* q, const void* pages, long long n_pages,
+                                               int page_size, const int32_t* page_table, int W,
+                                               const void* node_k, const void* node_v,
+                                               const uint32_t* mask, const int32_t* base_len,
+                                               const int32_t* kv_exp, int B, int N, int Hq,
+                                               int Hkv, int D, float scale, void* out, float* lse,
+                                               void* workspace, size_t workspace_bytes,
+                                               void* stream);
+
+/*
+ * Forks of sequences whose pages a table names (any cache in pages: a page is
+ * page_bytes bytes in each of `planes` planes).  New sequence j goes on from
+ * old sequence parent[j], several from one if need be (beams, samples of one
+ * prompt), or is empty (parent[j] = -1):
+ *   - new_len[j] = length[parent[j]]; the pages that are full up to there are
+ *     shared;
+ *   - the unfinished page is taken over by the lowest j that has it, unless a
+ *     sequence holds it as a full one; the others get a copy of it (all planes);
+ *   - fresh pages follow up to need[j] positions (at least new_len[j]), the free
+ *     pages with the lowest ids first, in the order of j and of places; pages
+ *     that no new sequence holds are free (entries of page_table behind a
+ *     sequence's length are not looked at).
+ * So every position from new_len[j] on stands in a page that j alone holds.
+ *   pages       planes plane_stride bytes apart, each n_pages * page_bytes;
+ *               16-byte aligned, strides and page_bytes multiples of 16
+ *   page_table  int32 [B, W]; length int32 [B], 0..W page_size
+ *   parent      int32 [B2], or NULL (j's own, B2 <= B: growth alone)
+ *   need        int32 [B2], or NULL (new_len)
+ * Outputs: new_table int32 [B2, W] (-1 behind a sequence's pages), new_len
+ * int32 [B2], used int32 [1] (pages held).  new_table and new_len must not
+ * overlap the inputs.  No page left: -1 (SPEC_FLAG_NO_PAGE).  A needed entry
+ * that names no page stays -1, an unfinished one gets a fresh page without a
+ * copy (SPEC_FLAG_BAD_PAGE); a parent outside [-1, B) counts as -1
+ * (SPEC_FLAG_BAD_PARENT); a length outside its range counts as 0, a need beyond
+ * W page_size as that (SPEC_FLAG_BAD_PATH).
+ * Two launches.  Workspace: spec_kv_pages_workspace_bytes(n_pages, B2) bytes.
+ */
+SPEC_API size_t spec_kv_pages_workspace_bytes(long long n_pages, int rows);
+SPEC_API spec_status_t spec_kv_pages_fork(void* pages, int planes, long long plane_stride,
+                                          long long n_pages, long long page_bytes, int page_size,
+                                          const int32_t* page_table, const int32_t* length, int B,
+                                          const int32_t* parent, const int32_t* need, int B2,
+                                          int W, int32_t* new_table, int32_t* new_len,
+                                          int32_t* used, void* workspace, size_t workspace_bytes,
+                                          void* stream);
+
+/*
+ * Compaction: the n pages that a table names move to the places [0, n), so that
+ * the pages from n on can be given back.  A page below n stays; those from n on
+ * move to the free places below n, in ascending order both.
+ *   page_table  int32 [B, W], negative: no page (others outside [0, n_pages)
+ *               become -1, SPEC_FLAG_BAD_PAGE)
+ * Outputs: new_table int32 [B, W] (may be page_table itself), used int32 [1] (n).
+ * Two launches.  Other arguments as spec_kv_pages_fork; workspace:
+ * spec_kv_pages_workspace_bytes(n_pages, B) bytes.
+ */
+SPEC_API spec_status_t spec_kv_pages_compact(void* pages, int planes, long long plane_stride,
+                                             long long n_pages, long long page_bytes,
+                                             const int32_t* page_table, int B, int W,
+                                             int32_t* new_table, int32_t* used, void* workspace,
+                                             size_t workspace_bytes, void* stream);
+
+/*
+ * Beam search's selection (no counterpart in the pages: a decoder beside the
+ * draft trees): the M best continuations of each request over its K beams and
+ * V tokens,
+ *   total[b, k, v] = scores[b, k] + z_v / T - ln sum_j exp(z_j / T),
+ * z = logits[b, k, :]; a finished beam has the single candidate (eos, its
+ * score).  Larger totals first, then lower beams, then lower tokens.
+ *   logits    [B, K, V] dtype; -inf is a token of probability 0
+ *   scores    float [B, K]; -inf (or NaN): the beam has no candidate
+ *   finished  int32 [B, K] (not 0: finished) or NULL
+ *   eos       the token that ends a beam, or -1
+ *   K         1..64;  M 1..16;  ceil(V / chunk) M <= 2048 (chunk = 16384 bf16 /
+ *             8192 fp32 elements)
+ * Outputs [B, M]: out_scores float (the totals), out_parents int32 (rows b K +
+ * k: what spec_kv_pages_fork takes), out_tokens int32, out_finished int32 (the
+ * parent was finished, or the token is eos).  Places without a candidate:
+ * -inf, -1, -1, 1.
+ * Totals are ordered in float64 from float32 exponentials: they are off by less
+ * than 2^-21 (1 + |z_v / T|); within a beam the order is that of the logits,
+ * and beams with the same logits and scores tie.
+ * Two launches.  Workspace: spec_beam_select_workspace_bytes() bytes.
+ */
+SPEC_API size_t spec_beam_select_workspace_bytes(int B, int K, int V, int M, int dtype);
+SPEC_API spec_status_t spec_beam_select(const void* logits, int dtype, const float* scores,
+                                        const int32_t* finished, int eos, float temperature, int B,
+                                        int K, int V, int M, float* out_scores,
+                                        int32_t* out_parents, int32_t* out_tokens,
+                                        int32_t* out_finished, void* workspace,
+                                        size_t workspace_bytes, void* stream);
 
 /*
  * Copy the workspace's flag word to *host_flags (synchronises `stream`); with

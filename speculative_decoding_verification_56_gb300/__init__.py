@@ -18,7 +18,16 @@ Entry points (same names as the C ABI):
 * :func:`spec_tree_qkv_rope`      -- head norms, rotation and cache write of the tree's nodes
 * :func:`spec_tree_attention`     -- attention of the tree's nodes over the cache and a shared prefix
 * :func:`spec_verify_tree_sample` -- sampling verification of draft trees
+* :func:`spec_tree_qkv_rope_nodes` -- the same with keys and values beside the cache
+* :func:`spec_kv4_commit_path`    -- the accepted path's entries into 4-bit pages
+* :func:`spec_kv4_read`           -- 4-bit pages back to bf16
+* :func:`spec_tree_attention_kv4` -- attention of the tree's nodes over 4-bit pages
+* :func:`spec_kv_pages_fork`      -- sequences that go on from others' pages
+* :func:`spec_kv_pages_compact`   -- the pages in use to the lowest places
+* :func:`spec_beam_select`        -- the best continuations over beams and vocabulary
 * :func:`spec_verify_workspace_bytes`, :func:`spec_tree_attention_workspace_bytes`,
+  :func:`spec_tree_attention_kv4_workspace_bytes`, :func:`spec_kv_pages_workspace_bytes`,
+  :func:`spec_beam_select_workspace_bytes`,
   :func:`spec_verify_read_flags`,
   :func:`spec_verify_launch_count`, :func:`spec_status_string`
 
@@ -26,7 +35,10 @@ Convenience wrappers that also allocate outputs and a workspace with torch:
 :func:`verify_sample`, :func:`verify_greedy`, :func:`verify_tree_greedy`,
 :func:`tree_attention_mask`, :func:`lm_head_verify_greedy`,
 :func:`lm_head_verify_sample`, :func:`tree_grow`, :func:`tree_qkv_rope`,
-:func:`tree_attention`, :func:`verify_tree_sample`.
+:func:`tree_attention`, :func:`verify_tree_sample`, :func:`tree_qkv_rope_nodes`,
+:func:`kv4_commit_path`, :func:`kv4_read`, :func:`tree_attention_kv4`,
+:func:`kv_pages_fork`, :func:`kv_pages_compact`, :func:`beam_select`; and
+:func:`alloc_kv4_pages`.
 """
 from __future__ import annotations
 
@@ -56,7 +68,10 @@ SPEC_MODE_TREE_GROW = 6
 SPEC_MODE_LM_HEAD_SAMPLE = 7
 SPEC_MODE_TREE_SAMPLE = 8
 SPEC_MODE_TREE_QKV = 10
+SPEC_MODE_KV4 = 11
 SPEC_ATTN_MAX_NODES = 4096
+SPEC_KV_MAX_TABLE = 1 << 20
+SPEC_KV_MAX_PAGES = 1 << 24
 SPEC_LM_MAX_D = 8192
 SPEC_FLAG_TOKEN_RANGE = 1
 SPEC_FLAG_BAD_PARENT = 2
@@ -65,6 +80,8 @@ SPEC_FLAG_RESIDUAL_FALLBACK = 8
 SPEC_FLAG_TIMEOUT = 16
 SPEC_FLAG_BAD_PATH = 32
 SPEC_FLAG_EMPTY_ROW = 64
+SPEC_FLAG_BAD_PAGE = 128
+SPEC_FLAG_NO_PAGE = 256
 
 _lock = threading.Lock()
 _lib = None
@@ -126,6 +143,30 @@ def load_library(path: str = LIB_PATH):
         lib.spec_tree_attention.argtypes = [P, P, P, LL, I, P, P, I, P, P, I, I, I, I, I, F, P, P,
                                             P, Z, P]
         lib.spec_tree_attention.restype = I
+        lib.spec_tree_qkv_rope_nodes.argtypes = [P, P, P, F, P, I, I, LL, P, P, I, I, I, I, I, P,
+                                                 P, P, P, Z, P]
+        lib.spec_tree_qkv_rope_nodes.restype = I
+        lib.spec_kv4_commit_path.argtypes = [P, I, LL, I, I, I, P, I, P, P, P, P, P, I, P, I, I,
+                                             P, P, Z, P]
+        lib.spec_kv4_commit_path.restype = I
+        lib.spec_kv4_read.argtypes = [P, I, LL, I, I, I, P, I, P, P, I, I, P, P, LL, LL, P, Z, P]
+        lib.spec_kv4_read.restype = I
+        lib.spec_tree_attention_kv4_workspace_bytes.argtypes = [I, I, I, I, I]
+        lib.spec_tree_attention_kv4_workspace_bytes.restype = Z
+        lib.spec_tree_attention_kv4.argtypes = [P, P, LL, I, P, I, P, P, P, P, P, I, I, I, I, I,
+                                                F, P, P, P, Z, P]
+        lib.spec_tree_attention_kv4.restype = I
+        lib.spec_kv_pages_workspace_bytes.argtypes = [LL, I]
+        lib.spec_kv_pages_workspace_bytes.restype = Z
+        lib.spec_kv_pages_fork.argtypes = [P, I, LL, LL, LL, I, P, P, I, P, P, I, I, P, P, P, P,
+                                           Z, P]
+        lib.spec_kv_pages_fork.restype = I
+        lib.spec_kv_pages_compact.argtypes = [P, I, LL, LL, LL, P, I, I, P, P, P, Z, P]
+        lib.spec_kv_pages_compact.restype = I
+        lib.spec_beam_select_workspace_bytes.argtypes = [I, I, I, I, I]
+        lib.spec_beam_select_workspace_bytes.restype = Z
+        lib.spec_beam_select.argtypes = [P, I, P, P, I, F, I, I, I, I, P, P, P, P, P, Z, P]
+        lib.spec_beam_select.restype = I
         lib.spec_verify_read_flags.argtypes = [P, ctypes.POINTER(ctypes.c_uint32), I, P]
         lib.spec_verify_read_flags.restype = I
         lib.spec_verify_launch_count.argtypes = []
@@ -580,6 +621,242 @@ def spec_tree_attention(q, k_cache, v_cache, mask, base_len, scale, out, lse, wo
     _check(st, "spec_tree_attention")
 
 
+def spec_tree_qkv_rope_nodes(qkv, q_norm, k_norm, eps, inv_freq, base_len, depth, q_out, k_out,
+                             v_out, workspace, pos_offset=0, interleaved=False, stream=None):
+    """:func:`spec_tree_qkv_rope` with keys and values at their nodes' places (C
+    ABI ``spec_tree_qkv_rope_nodes``): k_out, v_out bf16 [B, N, Hkv, D]."""
+    torch = _torch()
+    dev = _call_device(qkv, "qkv")
+    B, N, H, D = qkv.shape
+    Hkv = k_out.shape[2] if k_out.dim() == 4 else 0
+    Hq = H - 2 * Hkv
+    bf16 = torch.bfloat16
+    st = load_library().spec_tree_qkv_rope_nodes(
+        _arg(qkv, "qkv", bf16, (B, N, H, D), dev),
+        None if q_norm is None else _arg(q_norm, "q_norm", bf16, (D,), dev),
+        None if k_norm is None else _arg(k_norm, "k_norm", bf16, (D,), dev), float(eps),
+        None if inv_freq is None else _arg(inv_freq, "inv_freq", torch.float32,
+                                           (inv_freq.numel(),), dev),
+        0 if inv_freq is None else 2 * inv_freq.numel(),
+        1 if interleaved else 0, int(pos_offset),
+        _arg(base_len, "base_len", torch.int32, (B,), dev),
+        None if depth is None else _arg(depth, "depth", torch.int32, (B, N), dev), B, N, Hq, Hkv,
+        D, _arg(q_out, "q_out", bf16, (B, N, Hq, D), dev),
+        _arg(k_out, "k_out", bf16, (B, N, Hkv, D), dev),
+        _arg(v_out, "v_out", bf16, (B, N, Hkv, D), dev), *_workspace(workspace, dev),
+        _stream_of(stream, dev))
+    _check(st, "spec_tree_qkv_rope_nodes")
+
+
+def _kv4_args(pages, layered, D, device):
+    """Pointer, layers, pages, positions per page and heads of a 4-bit cache
+    uint8 [layers, n_pages, Hkv, block] (without layers: one layer)."""
+    shape = pages.shape
+    if (pages.dtype is not _torch().uint8 or len(shape) != (4 if layered else 3)
+            or pages.get_device() != device or not pages.is_contiguous()):
+        raise ValueError("pages must be a contiguous uint8 tensor "
+                         f"[{'layers, ' if layered else ''}n_pages, heads, block] on cuda:{device}")
+    page_size, rest = divmod(8 * shape[-1], 9 * D)
+    if rest:
+        raise ValueError(f"a head's block of {shape[-1]} bytes holds no whole positions of D = {D}")
+    return pages.data_ptr(), shape[0] if layered else 1, shape[-3], page_size, shape[-2]
+
+
+def _page_table(t, rows, device, name="page_table"):
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be [{rows}, W], got {list(t.shape)}")
+    return _arg(t, name, _torch().int32, (rows, t.shape[1]), device), t.shape[1]
+
+
+def _kv_exp(t, shape, device):
+    return None if t is None else _arg(t, "kv_exp", _torch().int32, shape, device)
+
+
+def spec_kv4_commit_path(pages, page_table, node_k, node_v, base_len, accepted_len, path_nodes,
+                         new_len, workspace, kv_exp=None, stream=None):
+    """The accepted path's entries into 4-bit pages (C ABI
+    ``spec_kv4_commit_path``).
+
+    pages uint8 [layers, n_pages, Hkv, block] (:func:`alloc_kv4_pages`);
+    page_table int32 [B, W]; node_k, node_v bf16 [layers, B, N, Hkv, D];
+    base_len int32 [B]; accepted_len int32 [B] or None (all nodes); path_nodes
+    int32 [B, max_depth+1] or None (a chain); new_len int32 [B] out; kv_exp
+    int32 [layers, 2] or None.
+    """
+    torch = _torch()
+    dev = _call_device(node_k, "node_k")
+    layers, B, N, Hkv, D = node_k.shape
+    bf16, i32 = torch.bfloat16, torch.int32
+    pp, pl, n_pages, page_size, heads = _kv4_args(pages, True, D, dev)
+    if (pl, heads) != (layers, Hkv):
+        raise ValueError(f"pages hold {pl} layers of {heads} heads, node_k {layers} of {Hkv}")
+    tp, W = _page_table(page_table, B, dev)
+    if path_nodes is not None and path_nodes.dim() != 2:
+        raise ValueError(f"path_nodes must be [{B}, max_depth + 1], got {list(path_nodes.shape)}")
+    shape = (layers, B, N, Hkv, D)
+    st = load_library().spec_kv4_commit_path(
+        pp, layers, n_pages, page_size, Hkv, D, tp, W, _arg(node_k, "node_k", bf16, shape, dev),
+        _arg(node_v, "node_v", bf16, shape, dev), _arg(base_len, "base_len", i32, (B,), dev),
+        None if accepted_len is None else _arg(accepted_len, "accepted_len", i32, (B,), dev),
+        None if path_nodes is None else _arg(path_nodes, "path_nodes", i32,
+                                             (B, path_nodes.shape[1]), dev),
+        0 if path_nodes is None else path_nodes.shape[1] - 1, _kv_exp(kv_exp, (layers, 2), dev), B,
+        N, _arg(new_len, "new_len", i32, (B,), dev), *_workspace(workspace, dev),
+        _stream_of(stream, dev))
+    _check(st, "spec_kv4_commit_path")
+
+
+def spec_kv4_read(pages, page_table, length, k_out, v_out, workspace, kv_exp=None, stream=None):
+    """4-bit pages back to bf16 (C ABI ``spec_kv4_read``): the first length[b]
+    positions into k_out, v_out bf16 [layers, B, L, Hkv, D] (positions of a
+    sequence contiguous), the rest of which stays as it is."""
+    torch = _torch()
+    dev = _call_device(k_out, "k_out")
+    bf16 = torch.bfloat16
+    layers, B, L, Hkv, D = k_out.shape
+    pp, pl, n_pages, page_size, heads = _kv4_args(pages, True, D, dev)
+    if (pl, heads) != (layers, Hkv):
+        raise ValueError(f"pages hold {pl} layers of {heads} heads, k_out {layers} of {Hkv}")
+    tp, W = _page_table(page_table, B, dev)
+    stride = k_out.stride()
+    for t, name in ((k_out, "k_out"), (v_out, "v_out")):
+        if t.dtype is not bf16:
+            raise TypeError(f"{name} must be {bf16}, got {t.dtype}")
+        if t.get_device() != dev:
+            raise ValueError(f"{name} must be on cuda:{dev}")
+    if v_out.shape != k_out.shape or v_out.stride() != stride or stride[2:] != (Hkv * D, D, 1):
+        raise ValueError("k_out and v_out must have the same shape and strides, with the positions "
+                         "of a sequence contiguous")
+    # (strides of dimensions of one element are not looked at)
+    seq = stride[1] if B > 1 else max(stride[1], L * Hkv * D)
+    layer = stride[0] if layers > 1 else max(stride[0], B * seq)
+    st = load_library().spec_kv4_read(
+        pp, layers, n_pages, page_size, Hkv, D, tp, W,
+        _arg(length, "length", torch.int32, (B,), dev), _kv_exp(kv_exp, (layers, 2), dev), B, L,
+        k_out.data_ptr(), v_out.data_ptr(), 2 * layer, 2 * seq, *_workspace(workspace, dev),
+        _stream_of(stream, dev))
+    _check(st, "spec_kv4_read")
+
+
+def spec_tree_attention_kv4_workspace_bytes(B: int, N: int, Hq: int, Hkv: int, D: int) -> int:
+    return int(load_library().spec_tree_attention_kv4_workspace_bytes(B, N, Hq, Hkv, D))
+
+
+def spec_tree_attention_kv4(q, pages, page_table, node_k, node_v, mask, base_len, scale, out, lse,
+                            workspace, kv_exp=None, stream=None):
+    """Attention of the tree's nodes over 4-bit pages and their ancestors (C
+    ABI ``spec_tree_attention_kv4``).
+
+    q, out bf16 [B, N, Hq, D]; pages uint8 [n_pages, Hkv, block], one layer;
+    page_table int32 [B, W]; node_k, node_v bf16 [B, N, Hkv, D]; mask int32
+    [B, N, ceil(N/32)] or None for a chain; base_len int32 [B]; lse float32
+    [B, N, Hq] or None; kv_exp int32 [2] or None.
+    """
+    torch = _torch()
+    dev = _call_device(q, "q")
+    B, N, Hq, D = q.shape
+    bf16, i32 = torch.bfloat16, torch.int32
+    pp, _, n_pages, page_size, Hkv = _kv4_args(pages, False, D, dev)
+    tp, W = _page_table(page_table, B, dev)
+    st = load_library().spec_tree_attention_kv4(
+        _arg(q, "q", bf16, (B, N, Hq, D), dev), pp, n_pages, page_size, tp, W,
+        _arg(node_k, "node_k", bf16, (B, N, Hkv, D), dev),
+        _arg(node_v, "node_v", bf16, (B, N, Hkv, D), dev),
+        None if mask is None else _arg(mask, "mask", i32, (B, N, (N + 31) // 32), dev),
+        _arg(base_len, "base_len", i32, (B,), dev), _kv_exp(kv_exp, (2,), dev), B, N, Hq, Hkv, D,
+        float(scale), _arg(out, "out", bf16, (B, N, Hq, D), dev),
+        None if lse is None else _arg(lse, "lse", torch.float32, (B, N, Hq), dev),
+        *_workspace(workspace, dev), _stream_of(stream, dev))
+    _check(st, "spec_tree_attention_kv4")
+
+
+def _plane_args(pages, device):
+    """Pointer, planes, plane stride, pages and bytes of a page of any cache
+    [planes, n_pages, ...]."""
+    if pages.dim() < 3 or pages.get_device() != device or not pages.is_contiguous():
+        raise ValueError(f"pages must be a contiguous tensor [planes, n_pages, ...] on cuda:{device}")
+    planes, n_pages = pages.shape[:2]
+    if planes < 1 or n_pages < 1:
+        raise ValueError("pages must hold a page")
+    page_bytes = pages.nbytes // (planes * n_pages)
+    return pages.data_ptr(), planes, n_pages * page_bytes, n_pages, page_bytes
+
+
+def spec_kv_pages_workspace_bytes(n_pages: int, rows: int) -> int:
+    return int(load_library().spec_kv_pages_workspace_bytes(n_pages, rows))
+
+
+def spec_kv_pages_fork(pages, page_table, length, parent, need, page_size, new_table, new_len,
+                       used, workspace, stream=None):
+    """Sequences that go on from others' pages (C ABI ``spec_kv_pages_fork``).
+
+    pages: any cache [planes, n_pages, ...], page_size positions to a page;
+    page_table int32 [B, W]; length int32 [B]; parent int32 [B2] (-1: empty) or
+    None (each its own); need int32 [B2], positions to have pages for, or None.
+    Outputs: new_table int32 [B2, W], new_len int32 [B2], used int32 [1].
+    """
+    i32 = _torch().int32
+    dev = _call_device(pages, "pages")
+    pp, planes, stride, n_pages, page_bytes = _plane_args(pages, dev)
+    B = length.numel()
+    B2 = new_len.numel()
+    tp, W = _page_table(page_table, B, dev)
+    st = load_library().spec_kv_pages_fork(
+        pp, planes, stride, n_pages, page_bytes, int(page_size), tp,
+        _arg(length, "length", i32, (B,), dev), B,
+        None if parent is None else _arg(parent, "parent", i32, (B2,), dev),
+        None if need is None else _arg(need, "need", i32, (B2,), dev), B2, W,
+        _arg(new_table, "new_table", i32, (B2, W), dev), _arg(new_len, "new_len", i32, (B2,), dev),
+        _arg(used, "used", i32, (1,), dev), *_workspace(workspace, dev), _stream_of(stream, dev))
+    _check(st, "spec_kv_pages_fork")
+
+
+def spec_kv_pages_compact(pages, page_table, new_table, used, workspace, stream=None):
+    """The pages that a table names to the lowest places (C ABI
+    ``spec_kv_pages_compact``): new_table int32 [B, W] (may be page_table), used
+    int32 [1]."""
+    i32 = _torch().int32
+    dev = _call_device(pages, "pages")
+    pp, planes, stride, n_pages, page_bytes = _plane_args(pages, dev)
+    B = page_table.shape[0]
+    tp, W = _page_table(page_table, B, dev)
+    st = load_library().spec_kv_pages_compact(
+        pp, planes, stride, n_pages, page_bytes, tp, B, W,
+        _arg(new_table, "new_table", i32, (B, W), dev), _arg(used, "used", i32, (1,), dev),
+        *_workspace(workspace, dev), _stream_of(stream, dev))
+    _check(st, "spec_kv_pages_compact")
+
+
+def spec_beam_select_workspace_bytes(B: int, K: int, V: int, M: int, dtype: int) -> int:
+    return int(load_library().spec_beam_select_workspace_bytes(B, K, V, M, dtype))
+
+
+def spec_beam_select(logits, scores, finished, eos, temperature, out_scores, out_parents,
+                     out_tokens, out_finished, workspace, stream=None):
+    """The best continuations over beams and vocabulary (C ABI
+    ``spec_beam_select``).
+
+    logits [B, K, V] bf16 or fp32; scores float32 [B, K]; finished int32 [B, K]
+    or None; eos: the token that ends a beam, or -1.  Outputs [B, M]:
+    out_scores float32, out_parents (rows b K + beam), out_tokens and
+    out_finished int32.
+    """
+    torch = _torch()
+    dev = _call_device(logits, "logits")
+    B, K, V = logits.shape
+    M = out_scores.shape[-1]
+    i32, f32 = torch.int32, torch.float32
+    st = load_library().spec_beam_select(
+        _dev(logits, "logits"), _dtype_code(logits), _arg(scores, "scores", f32, (B, K), dev),
+        None if finished is None else _arg(finished, "finished", i32, (B, K), dev), int(eos),
+        float(temperature), B, K, V, M, _arg(out_scores, "out_scores", f32, (B, M), dev),
+        _arg(out_parents, "out_parents", i32, (B, M), dev),
+        _arg(out_tokens, "out_tokens", i32, (B, M), dev),
+        _arg(out_finished, "out_finished", i32, (B, M), dev), *_workspace(workspace, dev),
+        _stream_of(stream, dev))
+    _check(st, "spec_beam_select")
+
+
 def spec_verify_read_flags(workspace, clear: bool = True, stream=None) -> int:
     """Device flag bits recorded in ``workspace`` (synchronises the stream)."""
     out = ctypes.c_uint32(0)
@@ -808,6 +1085,175 @@ def tree_attention(q, k_cache, v_cache, mask, base_len, scale=None, prefix_k=Non
     spec_tree_attention(q, k_cache, v_cache, mask, base_len, scale, out, lse, workspace,
                         prefix_k, prefix_v, stream)
     return out, lse
+
+
+def tree_qkv_rope_nodes(qkv, Hkv, q_norm, k_norm, eps, inv_freq, base_len, depth, pos_offset=0,
+                        interleaved=False, workspace=None, stream=None):
+    """:func:`tree_qkv_rope` for a cache in pages (Hkv key-value heads); returns
+    queries [B, N, Hq, D], keys and values [B, N, Hkv, D]."""
+    if stream is not None:
+        with _allocating_on(stream, qkv.device):
+            return tree_qkv_rope_nodes(qkv, Hkv, q_norm, k_norm, eps, inv_freq, base_len, depth,
+                                       pos_offset, interleaved, workspace)
+    torch = _torch()
+    B, N, H, D = qkv.shape
+    Hq = H - 2 * Hkv
+    if Hq < 1 or Hkv < 1:
+        raise ValueError(f"qkv holds {H} heads, of which {2 * Hkv} are keys and values")
+    if workspace is None:
+        workspace = alloc_workspace(SPEC_MODE_TREE_QKV, B, N, 1, SPEC_DTYPE_BF16, qkv.device)
+    q = torch.empty(B, N, Hq, D, dtype=qkv.dtype, device=qkv.device)
+    k = torch.empty(B, N, Hkv, D, dtype=qkv.dtype, device=qkv.device)
+    v = torch.empty_like(k)
+    spec_tree_qkv_rope_nodes(qkv, q_norm, k_norm, eps, inv_freq, base_len, depth, q, k, v,
+                             workspace, pos_offset, interleaved)
+    return q, k, v
+
+
+def alloc_kv4_pages(layers: int, n_pages: int, Hkv: int, page_size: int, D: int, device="cuda"):
+    """Pages of a 4-bit cache, all zero: uint8 [layers, n_pages, Hkv, 9 page_size D / 8]."""
+    if page_size not in (16, 32, 64, 128) or D not in (64, 128):
+        raise ValueError("page_size must be 16, 32, 64 or 128 and D 64 or 128")
+    return _torch().zeros(layers, n_pages, Hkv, 9 * page_size * D // 8, dtype=_torch().uint8,
+                          device=device)
+
+
+def kv4_commit_path(pages, page_table, node_k, node_v, base_len, accepted_len=None,
+                    path_nodes=None, kv_exp=None, workspace=None, stream=None):
+    """Write the accepted path's entries into 4-bit pages, in place; returns
+    new_len int32 [B]."""
+    if stream is not None:
+        with _allocating_on(stream, node_k.device):
+            return kv4_commit_path(pages, page_table, node_k, node_v, base_len, accepted_len,
+                                   path_nodes, kv_exp, workspace)
+    B = base_len.shape[0]
+    if workspace is None:
+        workspace = alloc_workspace(SPEC_MODE_KV4, B, 1, 1, SPEC_DTYPE_BF16, node_k.device)
+    new_len = _torch().empty_like(base_len)
+    spec_kv4_commit_path(pages, page_table, node_k, node_v, base_len, accepted_len, path_nodes,
+                         new_len, workspace, kv_exp)
+    return new_len
+
+
+def kv4_read(pages, page_table, length, L, D, kv_exp=None, workspace=None, stream=None):
+    """The first length[b] positions of 4-bit pages in bf16; returns keys and
+    values [layers, B, L, Hkv, D], 0 behind a sequence's length."""
+    if stream is not None:
+        with _allocating_on(stream, pages.device):
+            return kv4_read(pages, page_table, length, L, D, kv_exp, workspace)
+    torch = _torch()
+    if pages.dim() != 4:
+        raise ValueError(f"pages must be [layers, n_pages, heads, block], got {list(pages.shape)}")
+    B = length.shape[0]
+    if workspace is None:
+        workspace = alloc_workspace(SPEC_MODE_KV4, B, 1, 1, SPEC_DTYPE_BF16, pages.device)
+    k = torch.zeros(pages.shape[0], B, L, pages.shape[2], D, dtype=torch.bfloat16,
+                    device=pages.device)
+    v = torch.zeros_like(k)
+    spec_kv4_read(pages, page_table, length, k, v, workspace, kv_exp)
+    return k, v
+
+
+def _alloc_flagged(n, device):
+    """Workspace whose flag word is zero (the rest needs no value)."""
+    if n == 0:
+        raise ValueError("shape outside the library's limits")
+    ws = _torch().empty(n, dtype=_torch().uint8, device=device)
+    ws[:256].zero_()
+    return ws
+
+
+def alloc_tree_attention_kv4_workspace(q, pages):
+    """Workspace of :func:`spec_tree_attention_kv4` for these shapes."""
+    B, N, Hq, D = q.shape
+    return _alloc_flagged(spec_tree_attention_kv4_workspace_bytes(B, N, Hq, pages.shape[-2], D),
+                          q.device)
+
+
+def tree_attention_kv4(q, pages, page_table, node_k, node_v, mask, base_len, scale=None,
+                       kv_exp=None, workspace=None, stream=None):
+    """Attention of the tree's nodes over 4-bit pages and their ancestors;
+    returns ``(out, lse)``.  ``scale`` defaults to 1 / sqrt(D)."""
+    if stream is not None:
+        with _allocating_on(stream, q.device):
+            return tree_attention_kv4(q, pages, page_table, node_k, node_v, mask, base_len, scale,
+                                      kv_exp, workspace)
+    torch = _torch()
+    if workspace is None:
+        workspace = alloc_tree_attention_kv4_workspace(q, pages)
+    if scale is None:
+        scale = q.shape[3] ** -0.5
+    out = torch.empty_like(q)
+    lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+    spec_tree_attention_kv4(q, pages, page_table, node_k, node_v, mask, base_len, scale, out, lse,
+                            workspace, kv_exp)
+    return out, lse
+
+
+def alloc_kv_pages_workspace(pages, rows: int, W: int = 1):
+    """Workspace of :func:`spec_kv_pages_fork` and :func:`spec_kv_pages_compact`
+    for tables of up to ``rows`` sequences (of any width)."""
+    return _alloc_flagged(spec_kv_pages_workspace_bytes(pages.shape[1], rows), pages.device)
+
+
+def kv_pages_fork(pages, page_table, length, parent, need, page_size, workspace=None, stream=None):
+    """Fork sequences (see :func:`spec_kv_pages_fork`); returns ``(new_table,
+    new_len, used)``."""
+    if stream is not None:
+        with _allocating_on(stream, pages.device):
+            return kv_pages_fork(pages, page_table, length, parent, need, page_size, workspace)
+    torch = _torch()
+    like = length if parent is None else parent
+    B2 = like.numel()
+    if workspace is None:
+        workspace = alloc_kv_pages_workspace(pages, B2)
+    new_table = torch.empty(B2, page_table.shape[1], dtype=torch.int32, device=pages.device)
+    new_len = torch.empty(B2, dtype=torch.int32, device=pages.device)
+    used = torch.empty(1, dtype=torch.int32, device=pages.device)
+    spec_kv_pages_fork(pages, page_table, length, parent, need, page_size, new_table, new_len, used,
+                       workspace)
+    return new_table, new_len, used
+
+
+def kv_pages_compact(pages, page_table, workspace=None, stream=None):
+    """Move the pages in use to the lowest places; returns ``(new_table, used)``."""
+    if stream is not None:
+        with _allocating_on(stream, pages.device):
+            return kv_pages_compact(pages, page_table, workspace)
+    torch = _torch()
+    if workspace is None:
+        workspace = alloc_kv_pages_workspace(pages, page_table.shape[0])
+    new_table = torch.empty_like(page_table)
+    used = torch.empty(1, dtype=torch.int32, device=pages.device)
+    spec_kv_pages_compact(pages, page_table, new_table, used, workspace)
+    return new_table, used
+
+
+def alloc_beam_select_workspace(logits, M: int):
+    """Workspace of :func:`spec_beam_select` for these shapes."""
+    B, K, V = logits.shape
+    return _alloc_flagged(spec_beam_select_workspace_bytes(B, K, V, M, _dtype_code(logits)),
+                          logits.device)
+
+
+def beam_select(logits, scores, M, finished=None, eos=-1, temperature=1.0, workspace=None,
+                stream=None):
+    """The M best continuations of each request; returns dict(scores, parents,
+    tokens, finished) [B, M]."""
+    if stream is not None:
+        with _allocating_on(stream, logits.device):
+            return beam_select(logits, scores, M, finished, eos, temperature, workspace)
+    torch = _torch()
+    B = logits.shape[0]
+    if workspace is None:
+        workspace = alloc_beam_select_workspace(logits, M)
+    i32 = dict(dtype=torch.int32, device=logits.device)
+    out = dict(scores=torch.empty(B, M, dtype=torch.float32, device=logits.device),
+               parents=torch.empty(B, M, **i32), tokens=torch.empty(B, M, **i32),
+               finished=torch.empty(B, M, **i32))
+    spec_beam_select(logits, scores, finished, eos, temperature, out["scores"], out["parents"],
+                     out["tokens"], out["finished"], workspace)
+    return out
 
 
 def to_device_logits(arr, dtype: str, device="cuda"):

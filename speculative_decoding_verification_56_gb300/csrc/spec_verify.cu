@@ -25,6 +25,10 @@
 #include "sv_rope.cuh"
 #include "sv_attn.cuh"
 #include "sv_treesample.cuh"
+#include "sv_kv4.cuh"
+#include "sv_attn4.cuh"
+#include "sv_pages.cuh"
+#include "sv_beam.cuh"
 
 static_assert(sv::kMaxDraft == SPEC_MAX_K, "finish kernel buffers are sized for SPEC_MAX_K");
 
@@ -59,7 +63,8 @@ struct Layout {
 // Returns false for arguments outside the documented limits.
 bool make_layout(int mode, int B, int kN, int V, int dtype, Layout* L) {
   if (mode == SPEC_MODE_TREE_MASK || mode == SPEC_MODE_KV_COMMIT ||
-      mode == SPEC_MODE_TREE_SAMPLE || mode == SPEC_MODE_TREE_QKV) {  // the flag header only
+      mode == SPEC_MODE_TREE_SAMPLE || mode == SPEC_MODE_TREE_QKV ||
+      mode == SPEC_MODE_KV4) {  // the flag header only
     if (B < 0 || kN < 1 || kN > SPEC_MAX_TREE_NODES) return false;
     L->bytes = kHeaderBytes;
     return true;
@@ -648,6 +653,178 @@ bool attn_shape_ok(int B, int N, int Hq, int Hkv, int D, int P) {
          (long long)B * N <= INT32_MAX / 128 && (long long)B * N * Hq <= INT32_MAX;
 }
 
+// --- the 4-bit cache in pages --------------------------------------------------
+
+int log2_of(int x) {  // of a power of two
+  int n = 0;
+  while ((1 << n) < x) ++n;
+  return n;
+}
+
+bool kv4_shape_ok(long long n_pages, int page_size, int Hkv, int D, int W) {
+  return n_pages >= 1 && n_pages <= INT32_MAX && Hkv >= 1 && Hkv <= 65536 &&
+         (D == 64 || D == 128) && W >= 1 && W <= SPEC_KV_MAX_TABLE &&
+         (page_size == 16 || page_size == 32 || page_size == 64 || page_size == 128);
+}
+
+// Items and partial slots of spec_tree_attention_kv4 for one call shape.
+struct Attn4Plan {
+  int nt = 1, rows = 0, groups = 0;
+  size_t off_ml = 0, off_part = 0, bytes = 0;
+};
+
+Attn4Plan attn4_plan(int B, int N, int Hq, int Hkv, int D) {
+  Attn4Plan a;
+  const long long all = (long long)N * (Hq / Hkv);
+  a.nt = all <= 8 ? 1 : all <= 16 ? 2 : 3;
+  a.groups = (int)((all + 8 * a.nt - 1) / (8 * a.nt));
+  a.rows = (int)std::min<long long>(all, 8 * a.nt);
+  const size_t items = (size_t)B * Hkv * a.groups;
+  const size_t rows = (size_t)2 * sv::kA4MaxCtas * a.rows;
+  a.off_ml = align_up(kDataOffset + items * sizeof(int2));
+  a.off_part = align_up(a.off_ml + rows * sizeof(float2));
+  a.bytes = align_up(a.off_part + rows * D * sizeof(float));
+  return a;
+}
+
+bool attn4_shape_ok(int B, int N, int Hq, int Hkv, int D) {
+  if (B < 0 || N < 1 || N > SPEC_ATTN_MAX_NODES || Hkv < 1 || Hq < Hkv || Hq > 65536 ||
+      Hq % Hkv || (D != 64 && D != 128) || Hq / Hkv > 128)
+    return false;
+  return (long long)B * N * Hq * (D / 4) <= (long long)INT32_MAX * 128;
+}
+
+template <int D, int NT>
+spec_status_t launch_attn4(sv::Attn4Params prm, int sms, void* stream) {
+  constexpr size_t smem = sv::a4_smem<D, NT>();
+  prm.nctas = std::min(sms * sv::a4_per_sm<NT>(), sv::kA4MaxCtas);
+  const spec_status_t st = ensure_smem<sv::kv4_attn_rows_kernel<D, NT>>(smem);
+  if (st != SPEC_OK) return st;
+  const spec_status_t st2 = launch(sv::kv4_attn_rows_kernel<D, NT>, prm.nctas, smem, prm, stream,
+                                   true, 1, sv::kA4Threads);
+  if (st2 != SPEC_OK) return st2;
+  const long long threads = (long long)prm.B * prm.N * prm.Hq * (D / 4);
+  return launch(sv::kv4_attn_finish_kernel<D>, (int)((threads + 255) / 256), 0, prm, stream, true,
+                1, 256);
+}
+
+template <int D>
+spec_status_t run_attn4(const sv::Attn4Params& prm, int nt, int sms, void* stream) {
+  if (nt == 1) return launch_attn4<D, 1>(prm, sms, stream);
+  if (nt == 2) return launch_attn4<D, 2>(prm, sms, stream);
+  return launch_attn4<D, 3>(prm, sms, stream);
+}
+
+// Blocks of a (layer, sequence) of the commit and read kernels: enough for its
+// most places, and no more than fill the GPU several times.
+int kv4_blocks(long long places, int Hkv, int D, int layers, int B) {
+  const long long threads = places * Hkv * (D / 16) * 2;
+  const long long most = std::max(1ll, 9728ll / ((long long)layers * B));
+  return (int)std::max(1ll, std::min((threads + sv::kKv4Threads - 1) / sv::kKv4Threads, most));
+}
+
+struct PagesLayout {
+  size_t off_bits = 0, off_mark = 0, off_free = 0, off_off = 0, off_copies = 0, bytes = 0;
+};
+bool pages_layout(long long n_pages, long long rows, PagesLayout* L) {
+  if (n_pages < 1 || n_pages > SPEC_KV_MAX_PAGES || rows < 0 || rows > SPEC_KV_MAX_TABLE)
+    return false;
+  size_t off = kDataOffset;  // (word 4 of the header's space holds the number of copies)
+  L->off_bits = off;
+  off = align_up(off + (size_t)((n_pages + 31) / 32) * 4);
+  L->off_mark = off;
+  off = align_up(off + (size_t)n_pages * 4);
+  L->off_free = off;
+  off = align_up(off + (size_t)n_pages * 4);
+  L->off_off = off;
+  off = align_up(off + (size_t)rows * 4);
+  L->off_copies = off;
+  off = align_up(off + (size_t)std::max(n_pages, rows) * sizeof(int2));
+  L->bytes = off;
+  return true;
+}
+
+// Arguments that both calls on pages share, checked and laid out.
+spec_status_t pages_params(void* pages, int planes, long long plane_stride, long long n_pages,
+                           long long page_bytes, const int32_t* table, int B, int rows, int W,
+                           int32_t* new_table, int32_t* used, void* workspace,
+                           size_t workspace_bytes, sv::PagesParams* prm) {
+  PagesLayout L;
+  if (planes < 1 || planes > 65535 || page_bytes < 16 || B < 0 || W < 1 ||
+      W > SPEC_KV_MAX_TABLE || B > SPEC_KV_MAX_TABLE || !pages_layout(n_pages, rows, &L) ||
+      page_bytes > INT64_MAX / n_pages ||
+      (planes > 1 && plane_stride < n_pages * page_bytes))
+    return SPEC_ERR_INVALID_ARG;
+  if (!pages || !used || (B > 0 && !table) || (rows > 0 && !new_table)) return SPEC_ERR_INVALID_ARG;
+  if (!aligned(pages, 16) || page_bytes % 16 || plane_stride % 16 || !aligned(table, 4) ||
+      !aligned(new_table, 4) || !aligned(used, 4))
+    return SPEC_ERR_ALIGNMENT;
+  if (!workspace || workspace_bytes < L.bytes) return SPEC_ERR_WORKSPACE;
+  if (!aligned(workspace, kAlign)) return SPEC_ERR_ALIGNMENT;
+  char* ws = static_cast<char*>(workspace);
+  std::memset(prm, 0, sizeof *prm);
+  prm->pages = static_cast<uint8_t*>(pages);
+  prm->table = table;
+  prm->new_table = new_table;
+  prm->used = used;
+  prm->flags = reinterpret_cast<unsigned*>(ws);
+  prm->ncopies = reinterpret_cast<int32_t*>(ws + 16);
+  prm->bits = reinterpret_cast<uint32_t*>(ws + L.off_bits);
+  prm->mark = reinterpret_cast<int32_t*>(ws + L.off_mark);
+  prm->free_ids = reinterpret_cast<int32_t*>(ws + L.off_free);
+  prm->off = reinterpret_cast<int32_t*>(ws + L.off_off);
+  prm->copies = reinterpret_cast<int2*>(ws + L.off_copies);
+  prm->plane_stride = plane_stride;
+  prm->page_bytes = page_bytes;
+  prm->planes = planes;
+  prm->n_pages = (int)n_pages;
+  prm->B = B;
+  prm->B2 = rows;
+  prm->W = W;
+  prm->words = (int)((n_pages + 31) / 32);
+  return SPEC_OK;
+}
+
+spec_status_t run_pages(void (*plan)(sv::PagesParams), const sv::PagesParams& prm, void* stream) {
+  // CTAs of the plan: one per 8192 table entries or 1024 words of the bitmap
+  const long long entries = (long long)std::max(prm.B, prm.B2) * prm.W;
+  int cluster = 1;
+  while (cluster < sv::kPgMaxCluster &&
+         (entries > 8192ll * cluster || prm.words > sv::kPgThreads * cluster))
+    cluster *= 2;
+  spec_status_t st = launch(plan, cluster, 0, prm, stream, true, cluster, sv::kPgThreads);
+  if (st != SPEC_OK) return st;
+  int sms = 0;
+  st = sm_count(&sms);
+  if (st != SPEC_OK) return st;
+  return launch(sv::pages_copy_kernel, sms * 8, 0, prm, stream, true, 1, sv::kPgCopyThreads);
+}
+
+struct BeamLayout {
+  int nchunks = 0;
+  size_t bytes = 0;
+};
+bool beam_layout(int B, int K, int V, int M, int dtype, BeamLayout* L) {
+  if (B < 0 || K < 1 || K > sv::kBeamMaxK || M < 1 || M > sv::kGrowMaxK || V < 1 ||
+      V > SPEC_MAX_V || (dtype != SPEC_DTYPE_F32 && dtype != SPEC_DTYPE_BF16))
+    return false;
+  const int C = (V + chunk_elems(dtype) - 1) / chunk_elems(dtype);
+  if (C * M > sv::kGrowMaxCand || (long long)B * K * C > INT32_MAX) return false;
+  L->nchunks = C;
+  L->bytes = align_up(kDataOffset + (size_t)B * K * C * sizeof(sv::GrowRec));
+  return true;
+}
+
+template <typename E>
+spec_status_t run_beam_rows(const sv::GrowParams& prm, bool vec, void* stream) {
+  if (!vec)
+    return launch(sv::grow_topk_kernel<E, false, true>, prm.items, 0, prm, stream, true);
+  int grid = 0;
+  const spec_status_t st = persistent_grid<sv::grow_topk_stream_kernel<E, true>>(prm.items, &grid);
+  if (st != SPEC_OK) return st;
+  return launch(sv::grow_topk_stream_kernel<E, true>, grid, kStreamSmem, prm, stream, true);
+}
+
 }  // namespace
 
 extern "C" {
@@ -1134,12 +1311,15 @@ spec_status_t spec_verify_tree_sample(const void* target_logits, int dtype,
              : launch_tree_sample<sv::tree_sample_kernel<sv::F32, false>>(prm, B, cluster, smem, stream);
 }
 
-spec_status_t spec_tree_qkv_rope(const void* qkv, const void* q_norm, const void* k_norm, float eps,
-                                 const float* inv_freq, int rot_dim, int interleaved,
-                                 long long pos_offset, const int32_t* base_len,
-                                 const int32_t* depth, int B, int N, int Hq, int Hkv, int D, int L,
-                                 long long seq_stride, void* q_out, void* k_cache, void* v_cache,
-                                 void* workspace, size_t workspace_bytes, void* stream) {
+namespace {
+
+// spec_tree_qkv_rope and, with to_nodes, spec_tree_qkv_rope_nodes
+spec_status_t tree_qkv_rope(const void* qkv, const void* q_norm, const void* k_norm, float eps,
+                            const float* inv_freq, int rot_dim, int interleaved,
+                            long long pos_offset, const int32_t* base_len, const int32_t* depth,
+                            int B, int N, int Hq, int Hkv, int D, int L, long long seq_stride,
+                            void* q_out, void* k_cache, void* v_cache, bool to_nodes,
+                            void* workspace, size_t workspace_bytes, void* stream) {
   if (B < 0 || N < 1 || N > SPEC_MAX_TREE_NODES || Hq < 1 || Hkv < 1 || Hq > 65536 ||
       Hkv > 65536 || (D != 64 && D != 128) || L < 1 || rot_dim < 0 || rot_dim > D || rot_dim % 2 ||
       pos_offset < 0 || pos_offset > INT32_MAX || !(eps >= 0.0f) || !std::isfinite(eps) ||
@@ -1176,11 +1356,37 @@ spec_status_t spec_tree_qkv_rope(const void* qkv, const void* q_norm, const void
   prm.L = L;
   prm.rot = rot_dim;
   prm.interleaved = interleaved != 0;
+  prm.to_nodes = to_nodes;
   // an element's partner in the thread's registers where the halves are whole
   // vectors (128 trees of 60, D = 128: 34.8 us; 100.8 with the partner read from
   // memory, as other rotations have to)
   const int mode = interleaved ? sv::kRopePairs : rot_dim % 16 == 0 ? sv::kRopeHalves : sv::kRopeOdd;
   return D == 128 ? run_rope<128>(prm, mode, B * N, stream) : run_rope<64>(prm, mode, B * N, stream);
+}
+
+}  // namespace
+
+spec_status_t spec_tree_qkv_rope(const void* qkv, const void* q_norm, const void* k_norm, float eps,
+                                 const float* inv_freq, int rot_dim, int interleaved,
+                                 long long pos_offset, const int32_t* base_len,
+                                 const int32_t* depth, int B, int N, int Hq, int Hkv, int D, int L,
+                                 long long seq_stride, void* q_out, void* k_cache, void* v_cache,
+                                 void* workspace, size_t workspace_bytes, void* stream) {
+  return tree_qkv_rope(qkv, q_norm, k_norm, eps, inv_freq, rot_dim, interleaved, pos_offset,
+                       base_len, depth, B, N, Hq, Hkv, D, L, seq_stride, q_out, k_cache, v_cache,
+                       false, workspace, workspace_bytes, stream);
+}
+
+spec_status_t spec_tree_qkv_rope_nodes(const void* qkv, const void* q_norm, const void* k_norm,
+                                       float eps, const float* inv_freq, int rot_dim,
+                                       int interleaved, long long pos_offset,
+                                       const int32_t* base_len, const int32_t* depth, int B, int N,
+                                       int Hq, int Hkv, int D, void* q_out, void* k_out,
+                                       void* v_out, void* workspace, size_t workspace_bytes,
+                                       void* stream) {
+  return tree_qkv_rope(qkv, q_norm, k_norm, eps, inv_freq, rot_dim, interleaved, pos_offset,
+                       base_len, depth, B, N, Hq, Hkv, D, N, (long long)N * Hkv * D * 2, q_out,
+                       k_out, v_out, true, workspace, workspace_bytes, stream);
 }
 
 size_t spec_tree_attention_workspace_bytes(int B, int N, int Hq, int Hkv, int D, int P) {
@@ -1320,6 +1526,7 @@ spec_status_t spec_tree_grow(const void* draft_logits, int dtype, float temperat
   prm.flags = reinterpret_cast<unsigned*>(ws);
   // every draft row the growth reads, reduced in one streaming launch
   prm.rows_per_tree = 1 + (D - 1) * K;
+  prm.slots = K;
   if ((long long)B * prm.rows_per_tree * prm.nchunks > INT32_MAX) return SPEC_ERR_INVALID_ARG;
   prm.items = B * prm.rows_per_tree * prm.nchunks;
   const bool vec = vec_ok(draft_logits, V, dtype);  // whole 16-byte vectors per row
@@ -1347,6 +1554,261 @@ spec_status_t spec_tree_grow(const void* draft_logits, int dtype, float temperat
   return launch(sv::grow_tree_kernel, B * sv::kGrowTreeCluster,
                 sv::grow_tree_smem(L.nchunks, K, prm.rows_per_tree, nnodes), prm, stream,
                 true, sv::kGrowTreeCluster, sv::kGrowTreeThreads);
+}
+
+spec_status_t spec_kv4_commit_path(void* pages, int layers, long long n_pages, int page_size,
+                                   int Hkv, int D, const int32_t* page_table, int W,
+                                   const void* node_k, const void* node_v,
+                                   const int32_t* base_len, const int32_t* accepted_len,
+                                   const int32_t* path_nodes, int max_depth, const int32_t* kv_exp,
+                                   int B, int N, int32_t* new_len, void* workspace,
+                                   size_t workspace_bytes, void* stream) {
+  if (!kv4_shape_ok(n_pages, page_size, Hkv, D, W) || layers < 1 || layers > 65535 || B < 0 ||
+      N < 1 || N > SPEC_MAX_TREE_NODES ||
+      (path_nodes && (max_depth < 0 || max_depth > SPEC_MAX_TREE_DEPTH || !accepted_len)) ||
+      (long long)B * layers > INT32_MAX / 64)
+    return SPEC_ERR_INVALID_ARG;
+  if (B == 0) return SPEC_OK;
+  if (!pages || !page_table || !node_k || !node_v || !base_len || !new_len)
+    return SPEC_ERR_INVALID_ARG;
+  if (!aligned(pages, 16) || !aligned(node_k, 16) || !aligned(node_v, 16) ||
+      !aligned(page_table, 4) || !aligned(base_len, 4) || !aligned(accepted_len, 4) ||
+      !aligned(path_nodes, 4) || !aligned(kv_exp, 4) || !aligned(new_len, 4))
+    return SPEC_ERR_ALIGNMENT;
+  if (!workspace || workspace_bytes < kHeaderBytes) return SPEC_ERR_WORKSPACE;
+  if (!aligned(workspace, kAlign)) return SPEC_ERR_ALIGNMENT;
+  sv::Kv4Params prm;
+  std::memset(&prm, 0, sizeof prm);
+  prm.pages = static_cast<uint8_t*>(pages);
+  prm.table = page_table;
+  prm.node_k = static_cast<const uint16_t*>(node_k);
+  prm.node_v = static_cast<const uint16_t*>(node_v);
+  prm.base_len = base_len;
+  prm.accepted = accepted_len;
+  prm.path = path_nodes;
+  prm.exps = kv_exp;
+  prm.new_len = new_len;
+  prm.flags = reinterpret_cast<unsigned*>(workspace);
+  prm.n_pages = n_pages;
+  prm.B = B;
+  prm.N = N;
+  prm.Hkv = Hkv;
+  prm.W = W;
+  prm.lg = log2_of(page_size);
+  prm.max_depth = max_depth;
+  prm.layers = layers;
+  prm.blocks = kv4_blocks(path_nodes ? std::min(max_depth + 1, N) : N, Hkv, D, layers, B);
+  const int grid = layers * B * prm.blocks;
+  return D == 128 ? launch(sv::kv4_commit_kernel<128>, grid, 0, prm, stream, true, 1, sv::kKv4Threads)
+                  : launch(sv::kv4_commit_kernel<64>, grid, 0, prm, stream, true, 1, sv::kKv4Threads);
+}
+
+spec_status_t spec_kv4_read(const void* pages, int layers, long long n_pages, int page_size,
+                            int Hkv, int D, const int32_t* page_table, int W,
+                            const int32_t* length, const int32_t* kv_exp, int B, int L,
+                            void* k_out, void* v_out, long long layer_stride,
+                            long long seq_stride, void* workspace, size_t workspace_bytes,
+                            void* stream) {
+  if (!kv4_shape_ok(n_pages, page_size, Hkv, D, W) || layers < 1 || layers > 65535 || B < 0 ||
+      L < 1 || (long long)B * layers > INT32_MAX / 64)
+    return SPEC_ERR_INVALID_ARG;
+  if (seq_stride < (long long)L * Hkv * D * 2 ||
+      (layers > 1 && (B > 1 ? seq_stride > INT64_MAX / B : false)) ||
+      (layers > 1 && layer_stride < (long long)std::max(B - 1, 0) * seq_stride + (long long)L * Hkv * D * 2))
+    return SPEC_ERR_INVALID_ARG;
+  if (B == 0) return SPEC_OK;
+  if (!pages || !page_table || !length || !k_out || !v_out) return SPEC_ERR_INVALID_ARG;
+  if (!aligned(pages, 16) || !aligned(k_out, 16) || !aligned(v_out, 16) || layer_stride % 16 ||
+      seq_stride % 16 || !aligned(page_table, 4) || !aligned(length, 4) || !aligned(kv_exp, 4))
+    return SPEC_ERR_ALIGNMENT;
+  if (!workspace || workspace_bytes < kHeaderBytes) return SPEC_ERR_WORKSPACE;
+  if (!aligned(workspace, kAlign)) return SPEC_ERR_ALIGNMENT;
+  sv::Kv4Params prm;
+  std::memset(&prm, 0, sizeof prm);
+  prm.pages = static_cast<uint8_t*>(const_cast<void*>(pages));
+  prm.table = page_table;
+  prm.length = length;
+  prm.exps = kv_exp;
+  prm.k_out = static_cast<uint16_t*>(k_out);
+  prm.v_out = static_cast<uint16_t*>(v_out);
+  prm.flags = reinterpret_cast<unsigned*>(workspace);
+  prm.n_pages = n_pages;
+  prm.out_layer = layer_stride / 2;
+  prm.out_seq = seq_stride / 2;
+  prm.B = B;
+  prm.Hkv = Hkv;
+  prm.W = W;
+  prm.lg = log2_of(page_size);
+  prm.L = L;
+  prm.layers = layers;
+  prm.blocks = kv4_blocks(L, Hkv, D, layers, B);
+  const int grid = layers * B * prm.blocks;
+  return D == 128 ? launch(sv::kv4_read_kernel<128>, grid, 0, prm, stream, true, 1, sv::kKv4Threads)
+                  : launch(sv::kv4_read_kernel<64>, grid, 0, prm, stream, true, 1, sv::kKv4Threads);
+}
+
+size_t spec_tree_attention_kv4_workspace_bytes(int B, int N, int Hq, int Hkv, int D) {
+  if (!attn4_shape_ok(B, N, Hq, Hkv, D)) return 0;
+  return attn4_plan(B, N, Hq, Hkv, D).bytes;
+}
+
+spec_status_t spec_tree_attention_kv4(const void* q, const void* pages, long long n_pages,
+                                      int page_size, const int32_t* page_table, int W,
+                                      const void* node_k, const void* node_v,
+                                      const uint32_t* mask, const int32_t* base_len,
+                                      const int32_t* kv_exp, int B, int N, int Hq, int Hkv, int D,
+                                      float scale, void* out, float* lse, void* workspace,
+                                      size_t workspace_bytes, void* stream) {
+  if (!attn4_shape_ok(B, N, Hq, Hkv, D) || !kv4_shape_ok(n_pages, page_size, Hkv, D, W) ||
+      (long long)W * page_size > INT32_MAX - 256 || !(scale > 0.0f) ||
+      !(scale < 1.7014118e38f))  // 2^127: scale * log2(e) stays finite
+    return SPEC_ERR_INVALID_ARG;
+  if (B == 0) return SPEC_OK;
+  if (!q || !pages || !page_table || !node_k || !node_v || !base_len || !out)
+    return SPEC_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(pages, 16) || !aligned(node_k, 16) || !aligned(node_v, 16) ||
+      !aligned(out, 16) || !aligned(page_table, 4) || !aligned(mask, 4) || !aligned(base_len, 4) ||
+      !aligned(kv_exp, 4) || !aligned(lse, 4))
+    return SPEC_ERR_ALIGNMENT;
+  if (!workspace) return SPEC_ERR_WORKSPACE;
+  if (!aligned(workspace, kAlign)) return SPEC_ERR_ALIGNMENT;
+  const Attn4Plan plan = attn4_plan(B, N, Hq, Hkv, D);
+  if (workspace_bytes < plan.bytes) return SPEC_ERR_WORKSPACE;
+  int sms = 0;
+  const spec_status_t st = sm_count(&sms);
+  if (st != SPEC_OK) return st;
+  char* ws = static_cast<char*>(workspace);
+  sv::Attn4Params prm;
+  std::memset(&prm, 0, sizeof prm);
+  prm.q = static_cast<const uint16_t*>(q);
+  prm.pages = static_cast<const uint8_t*>(pages);
+  prm.table = page_table;
+  prm.nk = static_cast<const uint16_t*>(node_k);
+  prm.nv = static_cast<const uint16_t*>(node_v);
+  prm.mask = mask;
+  prm.base_len = base_len;
+  prm.exps = kv_exp;
+  prm.out = static_cast<uint16_t*>(out);
+  prm.lse = lse;
+  prm.flags = reinterpret_cast<unsigned*>(ws);
+  prm.span = reinterpret_cast<int2*>(ws + kDataOffset);
+  prm.ml = reinterpret_cast<float2*>(ws + plan.off_ml);
+  prm.opart = reinterpret_cast<float*>(ws + plan.off_part);
+  prm.wait_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
+  prm.n_pages = n_pages;
+  prm.scale_log2 = (float)(1.4426950408889634 * (double)scale);
+  prm.B = B;
+  prm.N = N;
+  prm.Hq = Hq;
+  prm.Hkv = Hkv;
+  prm.G = Hq / Hkv;
+  prm.W = W;
+  prm.Wm = (N + 31) / 32;
+  prm.lg = log2_of(page_size);
+  prm.rows = plan.rows;
+  prm.groups = plan.groups;
+  return D == 128 ? run_attn4<128>(prm, plan.nt, sms, stream)
+                  : run_attn4<64>(prm, plan.nt, sms, stream);
+}
+
+size_t spec_kv_pages_workspace_bytes(long long n_pages, int rows) {
+  PagesLayout L;
+  return pages_layout(n_pages, rows, &L) ? L.bytes : 0;
+}
+
+spec_status_t spec_kv_pages_fork(void* pages, int planes, long long plane_stride,
+                                 long long n_pages, long long page_bytes, int page_size,
+                                 const int32_t* page_table, const int32_t* length, int B,
+                                 const int32_t* parent, const int32_t* need, int B2, int W,
+                                 int32_t* new_table, int32_t* new_len, int32_t* used,
+                                 void* workspace, size_t workspace_bytes, void* stream) {
+  if (page_size < 1 || B2 < 0 || B2 > SPEC_KV_MAX_TABLE || (long long)W * page_size > INT32_MAX ||
+      (!parent && B2 > B))
+    return SPEC_ERR_INVALID_ARG;
+  sv::PagesParams prm;
+  const spec_status_t st = pages_params(pages, planes, plane_stride, n_pages, page_bytes,
+                                        page_table, B, B2, W, new_table, used, workspace,
+                                        workspace_bytes, &prm);
+  if (st != SPEC_OK) return st;
+  if ((B > 0 && !length) || (B2 > 0 && !new_len)) return SPEC_ERR_INVALID_ARG;
+  if (!aligned(length, 4) || !aligned(parent, 4) || !aligned(need, 4) || !aligned(new_len, 4))
+    return SPEC_ERR_ALIGNMENT;
+  prm.length = length;
+  prm.parent = parent;
+  prm.need = need;
+  prm.new_len = new_len;
+  prm.page = page_size;
+  return run_pages(sv::pages_fork_kernel, prm, stream);
+}
+
+spec_status_t spec_kv_pages_compact(void* pages, int planes, long long plane_stride,
+                                    long long n_pages, long long page_bytes,
+                                    const int32_t* page_table, int B, int W, int32_t* new_table,
+                                    int32_t* used, void* workspace, size_t workspace_bytes,
+                                    void* stream) {
+  sv::PagesParams prm;
+  const spec_status_t st = pages_params(pages, planes, plane_stride, n_pages, page_bytes,
+                                        page_table, B, B, W, new_table, used, workspace,
+                                        workspace_bytes, &prm);
+  if (st != SPEC_OK) return st;
+  return run_pages(sv::pages_compact_kernel, prm, stream);
+}
+
+size_t spec_beam_select_workspace_bytes(int B, int K, int V, int M, int dtype) {
+  BeamLayout L;
+  return beam_layout(B, K, V, M, dtype, &L) ? L.bytes : 0;
+}
+
+spec_status_t spec_beam_select(const void* logits, int dtype, const float* scores,
+                               const int32_t* finished, int eos, float temperature, int B, int K,
+                               int V, int M, float* out_scores, int32_t* out_parents,
+                               int32_t* out_tokens, int32_t* out_finished, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+  BeamLayout L;
+  if (!beam_layout(B, K, V, M, dtype, &L) || eos < -1 || eos >= V || !(temperature > 0.0f) ||
+      !std::isfinite(temperature))
+    return SPEC_ERR_INVALID_ARG;
+  if (B == 0) return SPEC_OK;
+  if (!logits || !scores || !out_scores || !out_parents || !out_tokens || !out_finished)
+    return SPEC_ERR_INVALID_ARG;
+  if (!aligned(logits, elem_bytes(dtype)) || !aligned(scores, 4) || !aligned(finished, 4) ||
+      !aligned(out_scores, 4) || !aligned(out_parents, 4) || !aligned(out_tokens, 4) ||
+      !aligned(out_finished, 4))
+    return SPEC_ERR_ALIGNMENT;
+  if (!workspace || workspace_bytes < L.bytes) return SPEC_ERR_WORKSPACE;
+  if (!aligned(workspace, kAlign)) return SPEC_ERR_ALIGNMENT;
+  char* ws = static_cast<char*>(workspace);
+  sv::BeamParams prm;
+  std::memset(&prm, 0, sizeof prm);
+  prm.rows.logits = logits;
+  prm.rows.scale = (float)(1.4426950408889634 / (double)temperature);
+  prm.rows.B = B * K;
+  prm.rows.D = 1;
+  prm.rows.K = M;
+  prm.rows.V = V;
+  prm.rows.nchunks = L.nchunks;
+  prm.rows.rows_per_tree = 1;
+  prm.rows.slots = 1;
+  prm.rows.items = B * K * L.nchunks;
+  prm.rows.rec = reinterpret_cast<sv::GrowRec*>(ws + kDataOffset);
+  prm.rows.flags = reinterpret_cast<unsigned*>(ws);
+  prm.score = scores;
+  prm.finished = finished;
+  prm.out_score = out_scores;
+  prm.out_parent = out_parents;
+  prm.out_token = out_tokens;
+  prm.out_finished = out_finished;
+  prm.B = B;
+  prm.K = K;
+  prm.M = M;
+  prm.eos = eos;
+  const bool vec = vec_ok(logits, V, dtype);
+  const spec_status_t st = dtype == SPEC_DTYPE_BF16
+                               ? run_beam_rows<sv::BF16>(prm.rows, vec, stream)
+                               : run_beam_rows<sv::F32>(prm.rows, vec, stream);
+  if (st != SPEC_OK) return st;
+  const size_t smem = (size_t)K * M * 12 + (size_t)sv::kBeamWarps * L.nchunks;
+  return launch(sv::beam_select_kernel, B, smem, prm, stream, true, 1, sv::kBeamThreads);
 }
 
 spec_status_t spec_verify_read_flags(void* workspace, uint32_t* host_flags, int clear,

@@ -1,0 +1,236 @@
+// sv_kv4.cuh -- a key-value cache in pages of 4-bit values: its format, the
+// commit of an accepted path into it, and the way back to bf16.
+//
+// A page holds `page` positions of all key-value heads of one layer, head by
+// head, and a head's positions in groups of 16, each contiguous:
+//   key codes [16, D/2], key scales [16, D/16], value codes, value scales
+// (18 D bytes), so that whatever the page, one copy brings a warp of the
+// attention all that it needs for one matrix product's 16 entries.  16 channels
+// of a head share a scale:
+//   a = max |x|,  s = e4m3(min(448, a / 6 2^-e)),  code = e2m1(x / (s 2^e)),
+//   value = code s 2^e,
+// both rounded to nearest even (codes saturate at 6), channel 2 i in the low
+// half of byte i; e is one exponent per layer for keys and one for values.
+// Codes have 2 significant bits and scales 4, so a value is exact in bf16 and,
+// without 2^e, in fp16; and x / (s 2^e) next to a border of two codes is
+// decided exactly in float32 (x has 8 bits, border times scale at most 7).
+#pragma once
+
+#include "sv_rope.cuh"
+
+namespace sv {
+
+constexpr unsigned kFlagBadPage = 128u;
+constexpr int kKv4MaxExp = 64;  // exponents beyond are taken as this
+constexpr int kKv4Threads = 256;
+
+// Bytes of a group of 16 positions, and of a head's block.
+__host__ __device__ constexpr int kv4_group(int D) { return 18 * D; }
+__host__ __device__ constexpr int kv4_block(int page, int D) { return page / 16 * kv4_group(D); }
+// Byte offset in a block of the key (value) half of place `slot`'s group
+__device__ __forceinline__ int kv4_half(int slot, int is_v, int D) {
+  return (slot >> 4) * kv4_group(D) + is_v * (kv4_group(D) / 2);
+}
+
+__device__ __forceinline__ int kv4_exp(const int32_t* e, int i) {
+  return e ? min(max(e[i], -kKv4MaxExp), kKv4MaxExp) : 0;
+}
+// 2^e for |e| <= 126
+__device__ __forceinline__ float pow2_small(int e) { return __int_as_float((e + 127) << 23); }
+
+// 8 codes (a word) as 4 pairs of fp16, in channel order
+__device__ __forceinline__ void kv4_unpack(uint32_t w, uint32_t (&h)[4]) {
+  asm("{\n .reg .b8 a, b, c, d;\n mov.b32 {a, b, c, d}, %4;\n"
+      " cvt.rn.f16x2.e2m1x2 %0, a;\n cvt.rn.f16x2.e2m1x2 %1, b;\n"
+      " cvt.rn.f16x2.e2m1x2 %2, c;\n cvt.rn.f16x2.e2m1x2 %3, d;\n}\n"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+}
+// two scales (low byte first) as a pair of fp16
+__device__ __forceinline__ uint32_t kv4_scales(uint32_t two) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)two));
+  return r;
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ float2 half2_to_float2(uint32_t h) {
+  float2 f;
+  asm("{\n .reg .f16 a, b;\n mov.b32 {a, b}, %2;\n cvt.f32.f16 %0, a;\n cvt.f32.f16 %1, b;\n}\n"
+      : "=f"(f.x), "=f"(f.y)
+      : "r"(h));
+  return f;
+}
+// e4m3 of a float in [0, 448], to nearest even
+__device__ __forceinline__ uint32_t to_e4m3(float x) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.0f), "f"(x));
+  return r & 0xFFu;
+}
+// a byte of two codes, lo in the low half, to nearest even, saturating
+__device__ __forceinline__ uint32_t to_e2m1x2(float hi, float lo) {
+  uint32_t r;
+  asm("{\n .reg .b8 t;\n cvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n mov.b32 %0, {t, t, t, t};\n}\n"
+      : "=r"(r)
+      : "f"(hi), "f"(lo));
+  return r & 0xFFu;
+}
+
+struct Kv4Params {
+  uint8_t* pages;           // [layers, n_pages, Hkv, block]
+  const int32_t* table;     // [B, W]
+  const uint16_t* node_k;   // commit: [layers, B, N, Hkv, D] bf16
+  const uint16_t* node_v;
+  const int32_t* base_len;  // commit: [B]
+  const int32_t* accepted;  // commit: [B] or null (all nodes)
+  const int32_t* path;      // commit: [B, max_depth + 1] or null (a chain)
+  const int32_t* length;    // read: [B]
+  const int32_t* exps;      // [layers, 2] or null
+  int32_t* new_len;         // commit: [B]
+  uint16_t* k_out;          // read: [layers, B, L, Hkv, D] bf16
+  uint16_t* v_out;
+  unsigned* flags;
+  long long n_pages, out_layer, out_seq;  // (elements)
+  int B, N, Hkv, W, lg, max_depth, L, layers;
+  int places;               // places of a sequence that the grid covers: blocks of
+  int blocks;               // kKv4Threads threads for each (layer, sequence)
+};
+
+// Page of position t of sequence b, or -1 (outside the table, or no page).
+__device__ __forceinline__ long long kv4_page_of(const Kv4Params& p, int b, long long t) {
+  const long long i = t >> p.lg;
+  if (i < 0 || i >= p.W) return -1;
+  const int id = p.table[(size_t)b * p.W + i];
+  return id >= 0 && id < p.n_pages ? id : -1;
+}
+
+// Number of entries that sequence b commits; 0 for one that is malformed
+// (flagged).  The whole block takes part.
+__device__ __forceinline__ int kv4_commit_count(const Kv4Params& p, int b) {
+  const int base = p.base_len[b];
+  const int acc = p.accepted ? p.accepted[b] : p.N - 1;
+  const int most = p.path ? min(p.max_depth, p.N - 1) : p.N - 1;
+  bool ok = base >= 1 && acc >= 0 && acc <= most;
+  bool paged = true;
+  if (ok) {
+    if (p.path) {
+      const int32_t* path = p.path + (size_t)b * (p.max_depth + 1);
+      for (int i = threadIdx.x; i <= acc; i += blockDim.x)
+        ok &= i == 0 ? path[0] == 0 : path[i] >= 1 && path[i] < p.N;
+    }
+    const long long first = (base - 1) >> p.lg, last = ((long long)base - 1 + acc) >> p.lg;
+    for (long long i = first + threadIdx.x; i <= last; i += blockDim.x)
+      paged &= kv4_page_of(p, b, i << p.lg) >= 0;
+  }
+  ok = __syncthreads_and(ok);
+  paged = __syncthreads_and(paged);
+  if (ok && paged) return acc + 1;
+  if (threadIdx.x == 0) set_flag(p.flags, ok ? kFlagBadPage : kFlagBadPath);
+  return 0;
+}
+
+// Commit: a thread takes 16 channels of one entry's key or value -- two loads
+// of 16 bytes, one store of 8 and one of a byte.  Blocks run over (layer,
+// sequence, part of the sequence's places x heads x channel groups x {key,
+// value}); how many places a sequence has is known only to the device.
+template <int D>
+__global__ void __launch_bounds__(kKv4Threads) kv4_commit_kernel(const Kv4Params p) {
+  constexpr int kBlocks = D / 16;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+  const unsigned lb = blockIdx.x / p.blocks, part = blockIdx.x - lb * p.blocks;
+  const int layer = (int)(lb / p.B), b = (int)(lb - (unsigned)layer * p.B);
+  const int count = kv4_commit_count(p, b);
+  const int base = p.base_len[b];
+  if (layer == 0 && part == 0 && threadIdx.x == 0)
+    p.new_len[b] = count ? base - 1 + count : max(base - 1, 0);
+  const int per = p.Hkv * kBlocks * 2;  // threads of an entry
+  const long long work = (long long)count * per;
+  const int page = 1 << p.lg;
+  const float ke = pow2_small(kv4_exp(p.exps, 2 * layer)), ve = pow2_small(kv4_exp(p.exps, 2 * layer + 1));
+  for (long long i = (long long)part * kKv4Threads + threadIdx.x; i < work;
+       i += (long long)p.blocks * kKv4Threads) {
+    const int at = (int)(i / per), r = (int)(i - (long long)at * per);
+    const int is_v = r >= per / 2, hb = r - is_v * (per / 2);
+    const int node = p.path ? p.path[(size_t)b * (p.max_depth + 1) + at] : at;
+    const uint16_t* src = (is_v ? p.node_v : p.node_k) +
+                          ((((size_t)layer * p.B + b) * p.N + node) * p.Hkv * kBlocks + hb) * 16;
+    const uint4 x0 = ldg_stream(src), x1 = ldg_stream(src + 8);
+    const uint32_t x[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+    uint32_t a = 0;  // largest magnitude, as bits
+#pragma unroll
+    for (int j = 0; j < 8; ++j) a = max(a, max(x[j] & 0x7FFFu, (x[j] >> 16) & 0x7FFFu));
+    const float unit = is_v ? ve : ke;
+    const uint32_t sb = to_e4m3(fminf(__fdiv_rn(__uint_as_float(a << 16), 6.0f) / unit, 448.0f));
+    const float step = half2_to_float2(kv4_scales(sb)).x * unit;
+    uint32_t code[2] = {0, 0};
+    if (step > 0.0f) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        code[j >> 2] |= to_e2m1x2(__fdiv_rn(bf16_hi(x[j]), step), __fdiv_rn(bf16_lo(x[j]), step))
+                        << (8 * (j & 3));
+    }
+    const long long t = (long long)base - 1 + at;
+    const int slot = (int)t & (page - 1);
+    const int h = hb / kBlocks, c = hb - h * kBlocks;
+    uint8_t* block = p.pages + (((size_t)layer * p.n_pages + kv4_page_of(p, b, t)) * p.Hkv + h) *
+                                   kv4_block(page, D) + kv4_half(slot, is_v, D);
+    *reinterpret_cast<uint2*>(block + (slot & 15) * (D / 2) + c * 8) = make_uint2(code[0], code[1]);
+    block[8 * D + (slot & 15) * kBlocks + c] = (uint8_t)sb;
+  }
+}
+
+// Read: a thread takes 16 channels of one position's key or value.
+template <int D>
+__global__ void __launch_bounds__(kKv4Threads) kv4_read_kernel(const Kv4Params p) {
+  constexpr int kBlocks = D / 16;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+  const unsigned lb = blockIdx.x / p.blocks, part = blockIdx.x - lb * p.blocks;
+  const int layer = (int)(lb / p.B), b = (int)(lb - (unsigned)layer * p.B);
+  const int len = p.length[b];
+  const int count = max(0, min(len, p.L));
+  if ((len < 0 || len > p.L) && layer == 0 && part == 0 && threadIdx.x == 0)
+    set_flag(p.flags, kFlagBadPath);
+  const int per = p.Hkv * kBlocks * 2;
+  const long long work = (long long)count * per;
+  const int page = 1 << p.lg;
+  const float ke = pow2_small(kv4_exp(p.exps, 2 * layer)), ve = pow2_small(kv4_exp(p.exps, 2 * layer + 1));
+  for (long long i = (long long)part * kKv4Threads + threadIdx.x; i < work;
+       i += (long long)p.blocks * kKv4Threads) {
+    const int t = (int)(i / per), r = (int)(i - (long long)t * per);
+    const int is_v = r >= per / 2, hb = r - is_v * (per / 2);
+    const long long id = kv4_page_of(p, b, t);
+    uint32_t o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (id >= 0) {
+      const int slot = t & (page - 1);
+      const int h = hb / kBlocks, c = hb - h * kBlocks;
+      const uint8_t* block = p.pages + (((size_t)layer * p.n_pages + id) * p.Hkv + h) *
+                                           kv4_block(page, D) + kv4_half(slot, is_v, D);
+      const uint2 code = *reinterpret_cast<const uint2*>(block + (slot & 15) * (D / 2) + c * 8);
+      const float s = half2_to_float2(kv4_scales(block[8 * D + (slot & 15) * kBlocks + c])).x *
+                      (is_v ? ve : ke);
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        uint32_t h4[4];
+        kv4_unpack(w ? code.y : code.x, h4);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 f = half2_to_float2(h4[j]);
+          o[4 * w + j] = pack_bf16(f.x * s, f.y * s);
+        }
+      }
+    } else if (r == 0) {
+      set_flag(p.flags, kFlagBadPage);
+    }
+    uint16_t* dst = (is_v ? p.v_out : p.k_out) + layer * p.out_layer + b * p.out_seq +
+                    ((size_t)t * p.Hkv * kBlocks + hb) * 16;
+    *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
+    *reinterpret_cast<uint4*>(dst + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+  }
+}
+
+}  // namespace sv

@@ -51,6 +51,7 @@ struct RopeParams {
   long long pos_offset;
   float eps;
   int N, Hq, Hkv, L, rot, interleaved;
+  int to_nodes;            // keys and values at place v of [B, N, Hkv, D], not behind the prefix
 };
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
@@ -148,7 +149,7 @@ __global__ void __launch_bounds__(kRopeThreads) tree_qkv_rope_kernel(const RopeP
   // (ordinary loads: the call before this one may have written them)
   const int base = p.base_len[b];
   int dep = p.depth ? p.depth[node] : v;
-  const bool ok = base >= 1 && (long long)base + p.N - 1 <= p.L;
+  const bool ok = base >= 1 && (p.to_nodes || (long long)base + p.N - 1 <= p.L);
   if (threadIdx.x == 0) {
     if (!ok && v == 0) set_flag(p.flags, kFlagBadPath);
     if (dep < 0) set_flag(p.flags, kFlagBadParent);
@@ -204,7 +205,7 @@ __global__ void __launch_bounds__(kRopeThreads) tree_qkv_rope_kernel(const RopeP
     } else if (ok) {
       const int hk = h - p.Hq - (is_v ? p.Hkv : 0);
       dst = (is_v ? p.v_cache : p.k_cache) + (long long)b * p.seq_stride +
-            ((long long)(base - 1 + v) * p.Hkv + hk) * D;
+            ((long long)(p.to_nodes ? v : base - 1 + v) * p.Hkv + hk) * D;
     }
     uint4 o0 = a, o1 = c;
     if (!ok) {
