@@ -27,6 +27,7 @@
 #include "sv_treesample.cuh"
 #include "sv_kv4.cuh"
 #include "sv_attn4.cuh"
+#include "sv_attn4t.cuh"
 #include "sv_pages.cuh"
 #include "sv_beam.cuh"
 
@@ -615,12 +616,9 @@ spec_status_t launch_attention(const sv::AttnParams& prm, const CUtensorMap (&ma
   return SPEC_OK;
 }
 
+// The join of cut items.
 template <int D>
-spec_status_t run_attention(const sv::AttnParams& prm, const CUtensorMap (&map)[5], void* stream) {
-  const spec_status_t st = prm.wait_ns == sv::kWaitLimitNs
-                               ? launch_attention<D, false>(prm, map, stream)
-                               : launch_attention<D, true>(prm, map, stream);
-  if (st != SPEC_OK) return st;
+spec_status_t finish_attention(const sv::AttnParams& prm, void* stream) {
   const long long rows = (long long)prm.B * prm.N * prm.Hq;
   const long long blocks = (rows + sv::kAtFinThreads - 1) / sv::kAtFinThreads;
   // Parts of an item: about 1 + CTAs / items.  Many (3 sequences of 65536, 24
@@ -633,6 +631,15 @@ spec_status_t run_attention(const sv::AttnParams& prm, const CUtensorMap (&map)[
                   true, 1, sv::kAtFinThreads);
   return launch(sv::tree_attn_finish_kernel<D, 8, 8>, (int)(blocks * (D / 8)), 0, prm, stream, true,
                 1, sv::kAtFinThreads);
+}
+
+template <int D>
+spec_status_t run_attention(const sv::AttnParams& prm, const CUtensorMap (&map)[5], void* stream) {
+  const spec_status_t st = prm.wait_ns == sv::kWaitLimitNs
+                               ? launch_attention<D, false>(prm, map, stream)
+                               : launch_attention<D, true>(prm, map, stream);
+  if (st != SPEC_OK) return st;
+  return finish_attention<D>(prm, stream);
 }
 
 template <int D>
@@ -669,13 +676,22 @@ bool kv4_shape_ok(long long n_pages, int page_size, int Hkv, int D, int W) {
 
 // Items and partial slots of spec_tree_attention_kv4 for one call shape.
 struct Attn4Plan {
+  bool tiles = false;  // more rows than the kernel for few serves
+  AttnPlan t;          // tiles: items and slots as spec_tree_attention's
   int nt = 1, rows = 0, groups = 0;
   size_t off_ml = 0, off_part = 0, bytes = 0;
 };
+constexpr int kA4MaxRows = 24;
 
 Attn4Plan attn4_plan(int B, int N, int Hq, int Hkv, int D) {
   Attn4Plan a;
   const long long all = (long long)N * (Hq / Hkv);
+  if (all > kA4MaxRows) {
+    a.tiles = true;
+    a.t = attn_plan(B, N, Hq, Hkv, D, 0);
+    a.bytes = a.t.bytes;
+    return a;
+  }
   a.nt = all <= 8 ? 1 : all <= 16 ? 2 : 3;
   a.groups = (int)((all + 8 * a.nt - 1) / (8 * a.nt));
   a.rows = (int)std::min<long long>(all, 8 * a.nt);
@@ -713,6 +729,23 @@ spec_status_t run_attn4(const sv::Attn4Params& prm, int nt, int sms, void* strea
   if (nt == 1) return launch_attn4<D, 1>(prm, sms, stream);
   if (nt == 2) return launch_attn4<D, 2>(prm, sms, stream);
   return launch_attn4<D, 3>(prm, sms, stream);
+}
+
+template <int D, bool kSet>
+spec_status_t launch_attn4_tiles(const sv::AttnQParams& prm, void* stream) {
+  const spec_status_t st = ensure_smem<sv::kv4_attn_tiles_kernel<D, kSet>>((size_t)sv::atq_smem<D>());
+  if (st != SPEC_OK) return st;
+  return launch(sv::kv4_attn_tiles_kernel<D, kSet>, prm.nctas, sv::atq_smem<D>(), prm, stream, true,
+                1, sv::kAtqThreads);
+}
+
+template <int D>
+spec_status_t run_attn4_tiles(const sv::AttnQParams& prm, void* stream) {
+  const spec_status_t st = prm.wait_ns == sv::kWaitLimitNs
+                               ? launch_attn4_tiles<D, false>(prm, stream)
+                               : launch_attn4_tiles<D, true>(prm, stream);
+  if (st != SPEC_OK) return st;
+  return finish_attention<D>(prm, stream);
 }
 
 // Blocks of a (layer, sequence) of the commit and read kernels: enough for its
@@ -1678,6 +1711,46 @@ spec_status_t spec_tree_attention_kv4(const void* q, const void* pages, long lon
   const spec_status_t st = sm_count(&sms);
   if (st != SPEC_OK) return st;
   char* ws = static_cast<char*>(workspace);
+  if (plan.tiles) {
+    sv::AttnQParams t;
+    std::memset(&t, 0, sizeof t);
+    t.q = static_cast<const uint16_t*>(q);
+    t.mask = mask;
+    t.base_len = base_len;
+    t.out = static_cast<uint16_t*>(out);
+    t.lse = lse;
+    t.flags = reinterpret_cast<unsigned*>(ws);
+    t.scale_log2 = (float)(1.4426950408889634 * (double)scale);
+    t.B = B;
+    t.N = N;
+    t.Hq = Hq;
+    t.Hkv = Hkv;
+    t.G = Hq / Hkv;
+    t.W = (N + 31) / 32;
+    // positions that a sequence may have: W pages of committed ones, and its nodes
+    t.L = (int)std::min<long long>((long long)W * page_size + N, INT32_MAX - 256);
+    t.tok = plan.t.tok;
+    t.pair_o = plan.t.pair_o;
+    t.mg_o = plan.t.mg_o;
+    t.rows_o = plan.t.rows_o;
+    t.by_cta = plan.t.by_cta;
+    t.own0 = plan.t.own0;
+    t.nctas = std::min(sms, sv::kAtMaxCtas);
+    t.q_tiles = 1 + plan.t.pair_o;
+    t.span = reinterpret_cast<int2*>(ws + kDataOffset);
+    t.ml = reinterpret_cast<float2*>(ws + plan.t.off_ml);
+    t.opart = reinterpret_cast<float*>(ws + plan.t.off_part);
+    t.wait_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
+    t.pages = static_cast<const uint8_t*>(pages);
+    t.table = page_table;
+    t.nk = static_cast<const uint16_t*>(node_k);
+    t.nv = static_cast<const uint16_t*>(node_v);
+    t.exps = kv_exp;
+    t.n_pages = n_pages;
+    t.Wt = W;
+    t.lg = log2_of(page_size);
+    return D == 128 ? run_attn4_tiles<128>(t, stream) : run_attn4_tiles<64>(t, stream);
+  }
   sv::Attn4Params prm;
   std::memset(&prm, 0, sizeof prm);
   prm.q = static_cast<const uint16_t*>(q);

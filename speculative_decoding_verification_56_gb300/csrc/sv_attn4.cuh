@@ -90,6 +90,12 @@ struct Attn4Walk {
   }
 };
 
+// scale 2^e, kept finite and above 0 (where it would not be, products are 0 or
+// scores beyond their limit), so that its products with 0 and -inf are right
+__device__ __forceinline__ float score_unit(float scale, int e) {
+  return fminf(fmaxf(ldexpf(scale, e), 1.2e-38f), 1e38f);
+}
+
 __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -300,7 +306,7 @@ __global__ void __launch_bounds__(kA4Threads, a4_per_sm<NT>())
       for (int j = 0; j < D / 64; ++j)
         *reinterpret_cast<uint32_t*>(s_q + r * kQStride + (j * 64 + lane * 2) * 2) =
             pack_half(ldexpf(bf16_lo(x[j]), e) + bad, ldexpf(bf16_hi(x[j]), e) + bad);
-      if (lane == 0) s_fac[r] = ldexpf(p.scale_log2, kexp - e);
+      if (lane == 0) s_fac[r] = score_unit(p.scale_log2, kexp - e);
     }
     meet();
     uint32_t qf[NT][kSteps][2];
