@@ -1743,8 +1743,22 @@ spec_status_t spec_tree_attention_kv4(const void* q, const void* pages, long lon
     t.wait_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
     t.pages = static_cast<const uint8_t*>(pages);
     t.table = page_table;
-    t.nk = static_cast<const uint16_t*>(node_k);
-    t.nv = static_cast<const uint16_t*>(node_v);
+    {
+      const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)Hq, (cuuint64_t)B * N};
+      const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)Hq * D * 2};
+      const cuuint32_t box[3] = {64, (cuuint32_t)t.G, (cuuint32_t)t.tok};
+      const spec_status_t e = encode_bf16(&t.map_q, q, 3, dims, strides, box);
+      if (e != SPEC_OK) return e;
+    }
+    for (int i = 0; i < 2; ++i) {
+      const cuuint64_t row = (cuuint64_t)Hkv * D * 2;
+      const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)Hkv, (cuuint64_t)N, (cuuint64_t)B};
+      const cuuint64_t strides[3] = {(cuuint64_t)D * 2, row, row * N};
+      const cuuint32_t box[4] = {64, 1, (cuuint32_t)sv::kAtKeys, 1};
+      const spec_status_t e = encode_bf16(i == 0 ? &t.map_k : &t.map_v, i == 0 ? node_k : node_v,
+                                          4, dims, strides, box);
+      if (e != SPEC_OK) return e;
+    }
     t.exps = kv_exp;
     t.n_pages = n_pages;
     t.Wt = W;

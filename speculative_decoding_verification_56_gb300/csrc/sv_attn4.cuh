@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(kA4Threads, a4_per_sm<NT>())
   constexpr int kQStride = D * 2 + 16;  // bytes of a query row: neighbouring rows in other banks
   constexpr int kGroup = kv4_group(D);
   constexpr int kStages = a4_stages<D, NT>();
-  extern __shared__ __align__(128) uint8_t smem[];
+  extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ uint64_t full[kA4Warps][kStages];
   __shared__ int s_nopage[kA4Warps][kStages];  // the group's table entry names no page
   __shared__ Attn4Walk s_walk[kA4Warps];       // of the copies

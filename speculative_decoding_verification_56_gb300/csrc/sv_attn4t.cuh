@@ -33,14 +33,42 @@ __host__ __device__ constexpr int atq_smem() {
 }
 
 struct AttnQParams : AttnParams {
+  alignas(64) CUtensorMap map_q;  // [B N, Hq, D]
+  CUtensorMap map_k, map_v;       // the nodes' [B, N, Hkv, D]
   const uint8_t* pages;  // [n_pages, Hkv, block]
   const int32_t* table;  // [B, Wt]
-  const uint16_t* nk;    // [B, N, Hkv, D]
-  const uint16_t* nv;
   const int32_t* exps;   // [2] or null
   long long n_pages;
   int Wt, lg;            // the table's width; log2 of the page size
 };
+
+// Put i of a segment of n tiles into the ring, in the order of use: pairs K0 V0
+// K1 V1 .., else K0 K1 V0 K2 V1 K3 .. (see the softmax's k_use and v_use).
+__device__ __forceinline__ void atq_put(int pair, int n, int i, int* t, int* is_v) {
+  if (pair) {
+    *t = i >> 1;
+    *is_v = i & 1;
+  } else if (i < 2) {
+    *is_v = i >= n;  // (n = 1: K0 V0)
+    *t = *is_v ? 0 : i;
+  } else {
+    const int tk = (i + 1) >> 1;
+    *is_v = !(i & 1) || tk >= n;
+    *t = (i & 1) ? min(tk, n - 1) : (i - 2) >> 1;
+  }
+}
+
+// Whether a phase is complete, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, unsigned parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(done)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return done != 0;
+}
 
 // fp16 operands, fp32 accumulator (formats 0 of bits 7-9 and 10-12)
 __host__ __device__ constexpr uint32_t umma_idesc_f16_f32(int M, int N) {
@@ -58,7 +86,7 @@ __global__ void __launch_bounds__(kAtqThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem[];
   static_assert(atq_tiles<D>() - 1 <= kAtMaxStages, "ring barriers");
   __shared__ uint64_t full[kAtMaxStages], empty[kAtMaxStages];
-  __shared__ uint64_t raw_full[kRaw], raw_empty[kRaw];
+  __shared__ uint64_t raw_full[kRaw], raw_empty[kRaw], node_full[kAtqTurns], q_raw;
   __shared__ uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], drain;
   __shared__ uint64_t seg_full[kAtSegs], seg_empty[kAtSegs], pair_bar;
   __shared__ AttnSeg s_seg[kAtSegs];
@@ -73,7 +101,7 @@ __global__ void __launch_bounds__(kAtqThreads, 1)
   // still look at a tile that its first warp has given back): positions without
   // a page, and tree entries that are not finite
   __shared__ unsigned s_hole[kAtqTurns];
-  __shared__ uint32_t s_bad[kAtqTurns][4];
+  __shared__ uint32_t s_bad[kAtqTurns][2][4];   // (of keys, of values)
   uint8_t* ring = smem + p.q_tiles * kTile;
   const int S = atq_tiles<D>() - p.q_tiles;  // ring stages
   uint8_t* raw = smem + atq_tiles<D>() * kTile;
@@ -91,6 +119,8 @@ __global__ void __launch_bounds__(kAtqThreads, 1)
       mbar_init(&raw_full[s], 1);
       mbar_init(&raw_empty[s], 4);
     }
+    for (int s = 0; s < kAtqTurns; ++s) mbar_init(&node_full[s], 1);
+    mbar_init(&q_raw, 1);
     mbar_init(&q_full, 4);
     mbar_init(&q_empty, 1);
     for (int w = 0; w < 2; ++w) {
@@ -219,18 +249,29 @@ __global__ void __launch_bounds__(kAtqThreads, 1)
       if (lane == 0) mbar_arrive(&seg_empty[at]);
       if (seg.n == 0) break;
       const int32_t* row = p.table + (size_t)seg.b * p.Wt;
-      auto page_of = [&](int t) {  // of this lane's positions of tile t: -2 none wanted, -1 no page
+      auto page_of = [&](int i) {  // of this lane's positions of put i: -2 none wanted, -1 no page
+        if (lane >= 8 || i >= 2 * seg.n) return -2;
+        int t, is_v;
+        atq_put(seg.pair, seg.n, i, &t, &is_v);
         const int pos = (seg.t0 + t) * kAtKeys + lane * 16;
-        if (lane >= 8 || pos >= seg.plen) return -2;
+        if (pos >= seg.plen) return -2;
         const int id = row[pos >> p.lg];
         return id >= 0 && id < p.n_pages ? id : -1;
       };
-      auto put = [&](int t, int is_v, int id) {
+      // (pages are looked up two puts early)
+      int id0 = page_of(0), id1 = page_of(1);
+#pragma unroll 1
+      for (int i = 0; i < 2 * seg.n; ++i) {
+        int t, is_v;
+        atq_put(seg.pair, seg.n, i, &t, &is_v);
+        const int id = id0;
+        id0 = id1;
+        id1 = page_of(i + 2);
         const int key0 = (seg.t0 + t) * kAtKeys;
-        if (key0 >= seg.plen) return;  // nodes alone: not in the pages
+        if (key0 >= seg.plen) continue;  // nodes alone: not in the pages
         if (!at_wait_warp<kSet>(p, &raw_empty[stage], phase ^ 1u, abort)) {
           ok = false;
-          return;
+          break;
         }
         const unsigned some = __ballot_sync(0xffffffffu, id >= 0);
         const unsigned none = __ballot_sync(0xffffffffu, id == -1);
@@ -250,18 +291,6 @@ __global__ void __launch_bounds__(kAtqThreads, 1)
           stage = 0;
           phase ^= 1u;
         }
-      };
-      // in the order of use (see the softmax): each V tile, then the K tile `ahead`
-      // further on; the pages of a tile are looked up one tile early
-      const int ahead = 2 - seg.pair;
-      int idv[3] = {-2, -2, page_of(0)};  // of the tiles t - 2 .. t
-      for (int t = 0; ok && t < seg.n + ahead; ++t) {
-        const int next = t + 1 < seg.n ? page_of(t + 1) : -2;
-        if (t >= ahead) put(t - ahead, 1, seg.pair ? idv[1] : idv[0]);
-        if (ok && t < seg.n) put(t, 0, idv[2]);
-        idv[0] = idv[1];
-        idv[1] = idv[2];
-        idv[2] = next;
       }
     }
     if (!ok && lane == 0) fail();
@@ -390,12 +419,14 @@ __global__ void __launch_bounds__(kAtqThreads, 1)
   } else if (warp >= 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     // ---------------- unpacking ----------------
-    // thread r: query row r of each half, and entry r of each tile
+    // thread r: query row r of each half, and entry r of each tile.  (One copy of
+    // the code for keys and values: five roles share the instruction caches.)
     const int r = (int)threadIdx.x - 384;
-    const float kinv = pow2_small(-kv4_exp(p.exps, 0)), vinv = pow2_small(-kv4_exp(p.exps, 1));
     const int kexp = kv4_exp(p.exps, 0);
-    int stage = 0, rst = 0;
-    unsigned phase = 0, rphase = 0, kput = 0;  // kput: K tiles so far
+    const float kinv = pow2_small(-kexp), vinv = pow2_small(-kv4_exp(p.exps, 1));
+    int rst = 0;
+    unsigned rphase = 0, use = 0, nput = 0, kput = 0, vput = 0;  // ring uses, node tiles, K and V tiles so far
+    unsigned nq = 0, nasked = 0;  // thread 384: queries and node tiles asked for
     bool ok = true;
     // the tiles' rows of 128 bytes: 16-byte chunk c of row r stands at c ^ (r & 7)
     auto chunk = [&](uint8_t* tile, int c) {  // of D / 8
@@ -412,21 +443,35 @@ __global__ void __launch_bounds__(kAtqThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&seg_empty[at]);
       if (seg.n == 0) break;
-      // queries as fp16, each row times a power of two that brings its largest
-      // element to [2^14, 2^15)
-      if (!at_wait_warp<kSet>(p, &q_empty, (k & 1) ^ 1u, abort)) {
+      // the segment's queries and nodes come as bf16 tiles, for one thread to ask
+      // for; the queries become fp16 in place, each row times a power of two that
+      // brings its largest element to [2^14, 2^15)
+      if (threadIdx.x == 384) {
+        if (at_wait<kSet>(p, &q_empty, (k & 1) ^ 1u, abort)) {
+          const int tok0 = seg.b * p.N + seg.node0;
+          mbar_expect_tx(&q_raw, (unsigned)((1 + seg.pair) * kSub * p.tok * p.G * 128));
+          for (int w = 0; w <= seg.pair; ++w)
+            for (int c = 0; c < kSub; ++c)
+              tma_load_3d(smem + w * kTile + c * (kAtRows * 128), &p.map_q, c * 64, seg.h * p.G,
+                          tok0 + w * p.tok, &q_raw);
+          ++nq;
+        } else {
+          fail();
+        }
+      }
+      __syncwarp();
+      if (!at_wait_warp<kSet>(p, &q_raw, k & 1, abort)) {
         ok = false;
         break;
       }
+#pragma unroll 1
       for (int w = 0; w <= seg.pair; ++w) {
-        const int tk = w * p.tok + r / p.G;
-        if (r >= p.tok * p.G || tk >= seg.ntok) continue;
-        const uint4* src = reinterpret_cast<const uint4*>(
-            p.q + (((size_t)seg.b * p.N + seg.node0 + tk) * p.Hq + seg.h * p.G + r % p.G) * D);
+        if (r >= p.tok * p.G) continue;  // (rows of no node: whatever the copy brought)
+        uint8_t* tile = smem + w * kTile;
         uint32_t a = 0;
-#pragma unroll
+#pragma unroll 4
         for (int c = 0; c < D / 8; ++c) {
-          const uint4 x = src[c];
+          const uint4 x = lds128(chunk(tile, c));
           const uint32_t y[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) a = max(a, max(y[e] & 0x7FFFu, (y[e] >> 16) & 0x7FFFu));
@@ -434,39 +479,68 @@ __global__ void __launch_bounds__(kAtqThreads, 1)
         const int e2 = a == 0 || a >= 0x7F80u ? 0 : 14 - ilogbf(__uint_as_float(a << 16));
         const float nan = a >= 0x7F80u ? __int_as_float(0x7FC00000) : 0.0f;
         s_fac[k & 1][w][r] = score_unit(p.scale_log2, kexp - e2);
-        const float f0 = ldexpf(1.0f, e2 / 2), f1 = ldexpf(1.0f, e2 - e2 / 2);  // (2^e2 may overflow)
-#pragma unroll
+        const float f0 = pow2_small(e2 / 2), f1 = pow2_small(e2 - e2 / 2);  // (2^e2 may overflow)
+#pragma unroll 2
         for (int c = 0; c < D / 8; ++c) {
-          const uint4 x = src[c];
+          uint4* at_c = chunk(tile, c);
+          const uint4 x = lds128(at_c);
           const uint32_t y[4] = {x.x, x.y, x.z, x.w};
           uint32_t z[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             z[e] = pack_half(bf16_lo(y[e]) * f0 * f1 + nan, bf16_hi(y[e]) * f0 * f1 + nan);
-          *chunk(smem + w * kTile, c) = make_uint4(z[0], z[1], z[2], z[3]);
+          *at_c = make_uint4(z[0], z[1], z[2], z[3]);
         }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_full);
-      auto put = [&](int t, int is_v) {
-        const int key0 = (seg.t0 + t) * kAtKeys, key = key0 + r;
-        uint8_t* tile = ring + stage * kTile;
-        if (!at_wait_warp<kSet>(p, &empty[stage], phase ^ 1u, abort)) {
-          ok = false;
-          return;
+      int asked = 0;  // puts of the segment whose nodes are asked for
+#pragma unroll 1
+      for (int i = 0; i < 2 * seg.n; ++i, ++use) {
+        if (threadIdx.x == 384) {  // this put's nodes, and the next one's if its place is free
+          for (; asked <= i + 1 && asked < 2 * seg.n; ++asked) {
+            int t, is_v;
+            atq_put(seg.pair, seg.n, asked, &t, &is_v);
+            const int node0 = (seg.t0 + t) * kAtKeys - seg.plen;
+            if (node0 + kAtKeys <= 0) continue;
+            const unsigned u = use + (asked - i), st = u % S, par = ((u / S) & 1) ^ 1u;
+            if (asked > i && !mbar_test(&empty[st], par)) break;
+            if (!at_wait<kSet>(p, &empty[st], par, abort)) {
+              fail();
+              break;
+            }
+            uint64_t* bar = &node_full[nasked++ % kAtqTurns];
+            mbar_expect_tx(bar, kTile);
+            for (int c = 0; c < kSub; ++c)
+              tma_load_4d(ring + st * kTile + c * (kAtKeys * 128), is_v ? &p.map_v : &p.map_k, c * 64,
+                          seg.h, node0, seg.b, bar);
+          }
         }
+        __syncwarp();
+        int t, is_v;
+        atq_put(seg.pair, seg.n, i, &t, &is_v);
+        const int key0 = (seg.t0 + t) * kAtKeys, key = key0 + r;
+        const int stage = use % S;
+        uint8_t* tile = ring + stage * kTile;
+        // a tile with nodes: they are in it already (and 0 behind the last)
+        const bool nodes = key0 + kAtKeys > seg.plen, paged = key0 < seg.plen;
+        if (!(nodes ? at_wait_warp<kSet>(p, &node_full[nput % kAtqTurns], (nput / kAtqTurns) & 1, abort)
+                    : at_wait_warp<kSet>(p, &empty[stage], ((use / S) & 1) ^ 1u, abort))) {
+          ok = false;
+          break;
+        }
+        nput += nodes;
         unsigned hole = 0;
-        const bool paged = key0 < seg.plen;
         if (paged) {
           if (!at_wait_warp<kSet>(p, &raw_full[rst], rphase, abort)) {
             ok = false;
-            return;
+            break;
           }
           hole = s_nopage[rst];
         }
-        bool bad = false;
-        if (key < seg.plen && !((hole >> (r >> 4)) & 1)) {
+        const bool mine = key < seg.plen;
+        if (mine && !((hole >> (r >> 4)) & 1)) {
           // 32 channels at a time, neighbouring rows in other orders, so that
           // they meet other banks
           const uint8_t* src = raw + rst * kHalf + (r >> 4) * (kHalf / 8);
@@ -479,7 +553,7 @@ __global__ void __launch_bounds__(kAtqThreads, 1)
           } else {
             sc[0] = *reinterpret_cast<const uint32_t*>(src + 8 * D + (r & 15) * (D / 16));
           }
-#pragma unroll
+#pragma unroll 2
           for (int j = 0; j < D / 32; ++j) {
             const int cc = (j + (D == 128 ? r >> 1 : r >> 2)) & (D / 32 - 1);
             const uint4 x = lds128(codes + cc * 16);
@@ -497,67 +571,51 @@ __global__ void __launch_bounds__(kAtqThreads, 1)
                   make_uint4(hmul2(h[0], s), hmul2(h[1], s), hmul2(h[2], s), hmul2(h[3], s));
             }
           }
-        } else if (key >= seg.plen && key < seg.kvlen) {
-          // a node: bf16 to fp16; a value is 0 where the entry is not finite
-          const size_t node = ((size_t)seg.b * p.N + (key - seg.plen)) * p.Hkv + seg.h;
-          const uint4* kr = reinterpret_cast<const uint4*>(p.nk + node * D);
-          const uint4* vr = reinterpret_cast<const uint4*>(p.nv + node * D);
-          auto look = [&](const uint4* row) {
-#pragma unroll 4
-            for (int c = 0; c < D / 8; ++c) {
-              const uint4 x = row[c];
-              const uint32_t y[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                bad |= (y[e] & 0x7F80u) == 0x7F80u || (y[e] & 0x7F800000u) == 0x7F800000u;
-            }
-          };
-          look(kr);
-          look(vr);
-          bool dummy = false;
-#pragma unroll 4
-          for (int c = 0; c < D / 8; ++c) {
-            uint4 x = (is_v ? vr : kr)[c];
+        }
+        bool bad = false;
+        if (nodes || hole) {
+          // nodes, bf16 to fp16 in place; 0 if an element is not finite, and where
+          // there is no page
+          bool zero = mine && ((hole >> (r >> 4)) & 1);
+          if (!mine && key < seg.kvlen) {
             const float f = is_v ? vinv : kinv;
-            x = bad ? make_uint4(0, 0, 0, 0)
-                    : make_uint4(node_half2(x.x, f, dummy), node_half2(x.y, f, dummy),
-                                 node_half2(x.z, f, dummy), node_half2(x.w, f, dummy));
-            *chunk(tile, c) = x;
+#pragma unroll 2
+            for (int c = 0; c < D / 8; ++c) {
+              uint4* at_c = chunk(tile, c);
+              const uint4 x = lds128(at_c);
+              *at_c = make_uint4(node_half2(x.x, f, bad), node_half2(x.y, f, bad),
+                                 node_half2(x.z, f, bad), node_half2(x.w, f, bad));
+            }
           }
-        } else {
-          // nothing there: a weight of 0 times it has to be 0
-#pragma unroll 4
-          for (int c = 0; c < D / 8; ++c) *chunk(tile, c) = make_uint4(0, 0, 0, 0);
+          if (zero || bad)
+#pragma unroll 1
+            for (int c = 0; c < D / 8; ++c) *chunk(tile, c) = make_uint4(0, 0, 0, 0);
         }
         const unsigned any = __ballot_sync(0xffffffffu, bad);
-        if (!is_v && lane == 0) {
-          const unsigned turn = kput % kAtqTurns;
-          s_bad[turn][warp - 12] = any;
-          if (warp == 12) s_hole[turn] = hole;
+        const unsigned turn = (is_v ? vput++ : kput++) % kAtqTurns;
+        if (lane == 0) {
+          s_bad[turn][is_v][warp - 12] = any;
+          if (warp == 12 && !is_v) s_hole[turn] = hole;
         }
-        if (!is_v) ++kput;
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(&full[stage]);
           if (paged) mbar_arrive(&raw_empty[rst]);
         }
-        if (++stage == S) {
-          stage = 0;
-          phase ^= 1u;
-        }
         if (paged && ++rst == kRaw) {
           rst = 0;
           rphase ^= 1u;
         }
-      };
-      const int ahead = 2 - seg.pair;
-      for (int t = 0; ok && t < seg.n + ahead; ++t) {
-        if (t >= ahead) put(t - ahead, 1);
-        if (ok && t < seg.n) put(t, 0);
       }
     }
     if (!ok && lane == 0) fail();
+    if (threadIdx.x == 384) {  // every copy has landed before the CTA can leave
+      for (unsigned j = nasked > kAtqTurns ? nasked - kAtqTurns : 0; j < nasked; ++j)
+        mbar_wait_bounded(&node_full[j % kAtqTurns], (j / kAtqTurns) & 1);
+      if (nq) mbar_wait_bounded(&q_raw, (nq - 1) & 1);
+    }
+    __syncwarp();
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
     // ---------------- softmax ----------------
@@ -608,7 +666,7 @@ __global__ void __launch_bounds__(kAtqThreads, 1)
         const int t = pair ? i : 2 * i + w;
         const int key0 = (seg.t0 + t) * kAtKeys;
         bool edge = key0 + kAtKeys > seg.plen;  // not all of the tile is seen by all
-        uint32_t see[4], bad[4] = {0, 0, 0, 0};
+        uint32_t see[4];
         if (edge) {
           // the row's view of the tile, 32 entries per word
           const int tree0 = key0 - seg.plen;  // tree number of the tile's first entry
@@ -641,17 +699,26 @@ __global__ void __launch_bounds__(kAtqThreads, 1)
         }
         tmem_fence_after();
         if (i == 0) fac = s_fac[k & 1][pair ? w : 0][r];
-        // positions without a page are hidden from all; tree entries that are
-        // not finite turn the scores of the rows that see them to NaN (their
-        // values are 0 in the tile)
+        // positions without a page are hidden from all
         const unsigned hole = s_hole[turn];
-        if (edge || hole) {
+        bool spoilt = false;
+        if (edge) {
+          // tree entries that are not finite are 0 in the tiles, and the sums of
+          // the rows that see them become NaN
+          const int use = v_use(pair, t, seg.n);
+          if (!at_wait_warp<kSet>(p, &full[slot_of(use)], ((ring0 + use) / S) & 1, abort)) {
+            ok = false;
+            break;
+          }
+#pragma unroll
+          for (int c = 0; c < 4; ++c) spoilt |= ((s_bad[turn][0][c] | s_bad[turn][1][c]) & see[c]) != 0;
+        }
+        if (hole) {
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            if (!edge) see[c] = 0xFFFFFFFFu;
             const unsigned two = hole >> (2 * c);
-            see[c] &= ~((two & 1 ? 0xFFFFu : 0u) | (two & 2 ? 0xFFFF0000u : 0u));
-            bad[c] = s_bad[turn][c] & see[c];
+            see[c] = (edge ? see[c] : 0xFFFFFFFFu) &
+                     ~((two & 1 ? 0xFFFFu : 0u) | (two & 2 ? 0xFFFF0000u : 0u));
           }
           edge = true;
         }
@@ -665,14 +732,9 @@ __global__ void __launch_bounds__(kAtqThreads, 1)
           unsigned long long sum0, sum1, nm2;
           auto hide = [&](uint32_t (&a)[32], int c) {
             const uint32_t bits = c == 0 ? see[0] : c == 1 ? see[1] : c == 2 ? see[2] : see[3];
-            const uint32_t nan = c == 0 ? bad[0] : c == 1 ? bad[1] : c == 2 ? bad[2] : bad[3];
 #pragma unroll
             for (int j = 0; j < 32; ++j)
               if (!((bits >> j) & 1)) a[j] = 0xFF800000u;
-            if (nan)
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if ((nan >> j) & 1) a[j] = 0x7FC00000u;
           };
           // weights of 32 entries, two to a word
           auto weights = [&](const uint32_t (&a)[32], uint32_t (&pk)[16]) {
@@ -768,7 +830,7 @@ __global__ void __launch_bounds__(kAtqThreads, 1)
               tmem_st16(sbase + 16 * c, pk);
             }
           }
-          l += total();
+          l += spoilt ? __int_as_float(0x7FC00000) : total();
           tmem_wait_st();
         }
         tmem_fence_before();
