@@ -419,7 +419,7 @@ __global__ void __launch_bounds__(kAtqThreads, 1)
   } else if (warp >= 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     // ---------------- unpacking ----------------
-    // thread r: query row r of each half, and entry r of each tile.  (One copy of
+    // thread r: query row r of each half, and node r of each tile.  (One copy of
     // the code for keys and values: five roles share the instruction caches.)
     const int r = (int)threadIdx.x - 384;
     const int kexp = kv4_exp(p.exps, 0);
@@ -433,6 +433,15 @@ __global__ void __launch_bounds__(kAtqThreads, 1)
       return reinterpret_cast<uint4*>(tile + (c >> 3) * (kAtRows * 128) + r * 128 +
                                       (((c & 7) ^ (r & 7)) << 4));
     };
+    // Unpacking: lane 4 s + c (D = 64: 2 s + c) takes channels 32 c .. of entries s,
+    // s + kRows, ..: 16 bytes of codes, four chunks of fp16, which start at chunk
+    // 4 (c & 1) of column block c >> 1 and lie at places xor s & 7.  Lanes of the
+    // second column block store their chunks in the order 2 3 0 1.
+    constexpr int kRows = 32 * 32 / D;
+    const int ucc = lane % (D / 32), usub = lane / (D / 32);
+    const bool uswap = ucc >= 2;
+    const int udst = (ucc >> 1) * (kAtRows * 128) + ((warp - 12) * 32 + usub) * 128;
+    const int ulow = ((4 * (ucc & 1) + (uswap ? 2 : 0)) ^ (usub & 7)) * 16;
     for (unsigned k = 0; ok; ++k) {
       const unsigned at = k % kAtSegs;
       if (!at_wait_warp<kSet>(p, &seg_full[at], (k / kAtSegs) & 1, abort)) {
@@ -539,39 +548,36 @@ __global__ void __launch_bounds__(kAtqThreads, 1)
           }
           hole = s_nopage[rst];
         }
-        const bool mine = key < seg.plen;
-        if (mine && !((hole >> (r >> 4)) & 1)) {
-          // 32 channels at a time, neighbouring rows in other orders, so that
-          // they meet other banks
-          const uint8_t* src = raw + rst * kHalf + (r >> 4) * (kHalf / 8);
-          const uint8_t* codes = src + (r & 15) * (D / 2);
-          uint32_t sc[D / 64];
-          if constexpr (D == 128) {
-            const uint2 s2 = *reinterpret_cast<const uint2*>(src + 8 * D + (r & 15) * (D / 16));
-            sc[0] = s2.x;
-            sc[1] = s2.y;
-          } else {
-            sc[0] = *reinterpret_cast<const uint32_t*>(src + 8 * D + (r & 15) * (D / 16));
-          }
-#pragma unroll 2
-          for (int j = 0; j < D / 32; ++j) {
-            const int cc = (j + (D == 128 ? r >> 1 : r >> 2)) & (D / 32 - 1);
-            const uint4 x = lds128(codes + cc * 16);
-            uint32_t word = sc[0];
-            if (D == 128 && cc >= 2) word = sc[D / 64 - 1];
-            const uint32_t s01 = kv4_scales((cc & 1 ? word >> 16 : word) & 0xFFFFu);
-            const uint32_t s0 = prmt(s01, 0, 0x1010), s1 = prmt(s01, 0, 0x3232);
+        // the warp's 32 entries, kRows at a time: every load is of whole groups and
+        // every store meets other banks
+        {
+          const uint8_t* src = raw + rst * kHalf + (warp - 12) * (kHalf / 4);
+          const uint8_t* codes = src + usub * (D / 2) + ucc * 16;
+          const uint8_t* scales = src + 8 * D + usub * (D / 16) + ucc * 2;
+          uint8_t* dst = tile + udst;
+          const int left = seg.plen - key0 - (warp - 12) * 32 - usub;  // positions from this one on
+#pragma unroll
+          for (int j = 0; j < 32 / kRows; ++j) {
+            const int group = j * kRows / 16, place = j * kRows % 16;
+            if (j * kRows >= left || ((hole >> ((warp - 12) * 2 + group)) & 1)) continue;
+            uint4 x = lds128(codes + group * (kHalf / 8) + place * (D / 2));
+            const uint32_t s01 =
+                kv4_scales(*reinterpret_cast<const uint16_t*>(scales + group * (kHalf / 8) + place * (D / 16)));
+            const uint32_t s0 = prmt(s01, 0, uswap ? 0x3232 : 0x1010);
+            const uint32_t s1 = prmt(s01, 0, uswap ? 0x1010 : 0x3232);
+            if (uswap) x = make_uint4(x.z, x.w, x.x, x.y);
             const uint32_t y[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               uint32_t h[4];
               kv4_unpack(y[e], h);
               const uint32_t s = e < 2 ? s0 : s1;
-              *chunk(tile, 4 * cc + e) =
+              *reinterpret_cast<uint4*>(dst + j * kRows * 128 + (ulow ^ (e * 16))) =
                   make_uint4(hmul2(h[0], s), hmul2(h[1], s), hmul2(h[2], s), hmul2(h[3], s));
             }
           }
         }
+        const bool mine = key < seg.plen;
         bool bad = false;
         if (nodes || hole) {
           // nodes, bf16 to fp16 in place; 0 if an element is not finite, and where
