@@ -731,19 +731,12 @@ spec_status_t run_attn4(const sv::Attn4Params& prm, int nt, int sms, void* strea
   return launch_attn4<D, 3>(prm, sms, stream);
 }
 
-template <int D, bool kSet>
-spec_status_t launch_attn4_tiles(const sv::AttnQParams& prm, void* stream) {
-  const spec_status_t st = ensure_smem<sv::kv4_attn_tiles_kernel<D, kSet>>((size_t)sv::atq_smem<D>());
-  if (st != SPEC_OK) return st;
-  return launch(sv::kv4_attn_tiles_kernel<D, kSet>, prm.nctas, sv::atq_smem<D>(), prm, stream, true,
-                1, sv::kAtqThreads);
-}
-
 template <int D>
 spec_status_t run_attn4_tiles(const sv::AttnQParams& prm, void* stream) {
-  const spec_status_t st = prm.wait_ns == sv::kWaitLimitNs
-                               ? launch_attn4_tiles<D, false>(prm, stream)
-                               : launch_attn4_tiles<D, true>(prm, stream);
+  spec_status_t st = ensure_smem<sv::kv4_attn_tiles_kernel<D>>((size_t)sv::atq_smem<D>());
+  if (st != SPEC_OK) return st;
+  st = launch(sv::kv4_attn_tiles_kernel<D>, prm.nctas, sv::atq_smem<D>(), prm, stream, true, 1,
+              sv::kAtqThreads);
   if (st != SPEC_OK) return st;
   return finish_attention<D>(prm, stream);
 }
@@ -1740,7 +1733,9 @@ spec_status_t spec_tree_attention_kv4(const void* q, const void* pages, long lon
     t.span = reinterpret_cast<int2*>(ws + kDataOffset);
     t.ml = reinterpret_cast<float2*>(ws + plan.t.off_ml);
     t.opart = reinterpret_cast<float*>(ws + plan.t.off_part);
-    t.wait_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
+    const uint64_t limit = g_wait_limit_ns.load(std::memory_order_relaxed);
+    t.sleep_ns = (unsigned)std::min<uint64_t>(limit, sv::kSuspendHintNs);
+    t.tries = (int)std::min<uint64_t>(limit / sv::kSuspendHintNs + 1, 1000000);
     t.pages = static_cast<const uint8_t*>(pages);
     t.table = page_table;
     {

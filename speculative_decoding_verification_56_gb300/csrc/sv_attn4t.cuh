@@ -19,7 +19,7 @@ namespace sv {
 constexpr int kAtqThreads = 512;  // copies, MMAs, segments, an idle warp; 2 x 4 softmax warps;
                                   // 4 that unpack
 constexpr int kAtqTurns = 16;
-constexpr float kAtqLazy = 32768.0f;  // largest sum of a row's weights in a tile before its
+constexpr float kAtqLazy = 32768.0f;  // largest sum of a row's weights in 32 entries before its
                                       // reference is renewed: 2^8 times 2^kA4Off, within fp16
 
 // Query and unpacked tiles, and half tiles (keys or values) of packed groups.
@@ -40,6 +40,8 @@ struct AttnQParams : AttnParams {
   const int32_t* exps;   // [2] or null
   long long n_pages;
   int Wt, lg;            // the table's width; log2 of the page size
+  int tries;             // of a wait before it is given up, each a sleep of up to
+  unsigned sleep_ns;     // this
 };
 
 // Put i of a segment of n tiles into the ring, in the order of use: pairs K0 V0
@@ -70,12 +72,35 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, unsigned parity) {
   return done != 0;
 }
 
+// Waits between the roles: a number of tries that sleep in the instruction until
+// the phase completes, so that a wait is a few instructions (what the roles
+// share here is the instruction caches, see below).
+__device__ __forceinline__ bool atq_wait(const AttnQParams& p, uint64_t* bar, unsigned parity,
+                                         const int* abort, int more = 0) {
+#pragma unroll 1
+  for (int i = p.tries + more; i > 0; --i) {
+    if (mbar_try_wait(bar, parity, p.sleep_ns)) return true;
+    if (*(const volatile int*)abort) break;
+  }
+  return false;
+}
+// the same for a whole warp, with one answer
+__device__ __forceinline__ bool atq_wait_warp(const AttnQParams& p, uint64_t* bar, unsigned parity,
+                                              const int* abort) {
+#pragma unroll 1
+  for (int i = p.tries; i > 0; --i) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity, p.sleep_ns))) return true;
+    if (__any_sync(0xffffffffu, *(const volatile int*)abort)) break;
+  }
+  return false;
+}
+
 // fp16 operands, fp32 accumulator (formats 0 of bits 7-9 and 10-12)
 __host__ __device__ constexpr uint32_t umma_idesc_f16_f32(int M, int N) {
   return umma_idesc_bf16_f32(M, N) & ~((1u << 7) | (1u << 10));
 }
 
-template <int D, bool kSet>
+template <int D>
 __global__ void __launch_bounds__(kAtqThreads, 1)
     kv4_attn_tiles_kernel(const __grid_constant__ AttnQParams p) {
   constexpr int kTile = at_tile_bytes<D>();
@@ -220,8 +245,8 @@ __global__ void __launch_bounds__(kAtqThreads, 1)
         const unsigned at = k % kAtSegs;
         // (the only wait that lasts as long as an item: until the one four before
         // this is begun, so up to the run's length)
-        if (!at_wait<kSet>(p, &seg_empty[at], ((k / kAtSegs) & 1) ^ 1u, abort,
-                           (uint64_t)(hi - lo) * kAtTileNs)) {
+        if (!atq_wait(p, &seg_empty[at], ((k / kAtSegs) & 1) ^ 1u, abort,
+                      (int)min(hi - lo, 1000000ll))) {
           fail();
           break;
         }
@@ -240,7 +265,7 @@ __global__ void __launch_bounds__(kAtqThreads, 1)
     const int page = 1 << p.lg;
     for (unsigned k = 0; ok; ++k) {
       const unsigned at = k % kAtSegs;
-      if (!at_wait_warp<kSet>(p, &seg_full[at], (k / kAtSegs) & 1, abort)) {
+      if (!atq_wait_warp(p, &seg_full[at], (k / kAtSegs) & 1, abort)) {
         ok = false;
         break;
       }
@@ -269,7 +294,7 @@ __global__ void __launch_bounds__(kAtqThreads, 1)
         id1 = page_of(i + 2);
         const int key0 = (seg.t0 + t) * kAtKeys;
         if (key0 >= seg.plen) continue;  // nodes alone: not in the pages
-        if (!at_wait_warp<kSet>(p, &raw_empty[stage], phase ^ 1u, abort)) {
+        if (!atq_wait_warp(p, &raw_empty[stage], phase ^ 1u, abort)) {
           ok = false;
           break;
         }
@@ -307,10 +332,10 @@ __global__ void __launch_bounds__(kAtqThreads, 1)
       const uint64_t kdesc = umma_desc_sw128(smem_addr(ring));
       const uint64_t vdesc = umma_desc_mn_sw128(smem_addr(ring));
       int stage = 0;
-      unsigned phase = 0, nq = 0, np0 = 0, np1 = 0;
+      unsigned phase = 0, nq = 0, np = 0, np1 = 0;
       bool ok = true;
       auto wait = [&](uint64_t* bar, unsigned parity) {
-        if (!at_wait<kSet>(p, bar, parity & 1, abort)) {
+        if (!atq_wait(p, bar, parity & 1, abort)) {
           ok = false;
           fail();
         }
@@ -353,38 +378,36 @@ __global__ void __launch_bounds__(kAtqThreads, 1)
           // ring: K0, V0, K1, V1, ...; each tile is waited for as late as its use
           // allows, and where the tensor cores have work
           if (!wait(&full[stage], phase)) break;
-          scores(0, 0, stage);
-          scores(1, 1, stage);
+#pragma unroll 1
+          for (int w = 0; w < 2; ++w) scores(w, w, stage);
           if (n == 1) umma_commit(&q_empty);
           advance();
           int vst = stage;
           if (!wait(&full[stage], phase)) break;
           advance();
 #pragma unroll 1
-          for (int t = 0; t < n; ++t) {
+          for (int t = 0; ok && t < n; ++t, ++np) {
             const bool more = t + 1 < n;
             const int v = vst, k = stage;
             if (more && !wait(&full[stage], phase)) break;
-            if (!wait(&p_full[0], np0++)) break;
-            output(0, v, t == 0);
-            if (more) {
-              scores(0, 0, k);
-              advance();
-              vst = stage;
-              if (!wait(&full[stage], phase)) break;
-              advance();
-            } else {
-              umma_commit(&o_full[0]);
+#pragma unroll 1
+            for (int w = 0; w < 2; ++w) {
+              if (!wait(&p_full[w], np)) break;
+              output(w, v, t == 0);
+              if (more)
+                scores(w, w, k);
+              else
+                umma_commit(&o_full[w]);
+              if (more && w == 0) {
+                advance();
+                vst = stage;
+                if (!wait(&full[stage], phase)) break;
+                advance();
+              }
             }
-            if (!wait(&p_full[1], np1++)) break;
-            output(1, v, t == 0);
-            if (more) {
-              scores(1, 1, k);
-              if (t + 2 == n) umma_commit(&q_empty);
-            } else {
-              umma_commit(&o_full[1]);
-            }
+            if (t + 2 == n) umma_commit(&q_empty);
           }
+          np1 = np;
         } else {
           for (int t = 0; t < min(2, n); ++t) {
             if (!wait(&full[stage], phase)) break;
@@ -397,7 +420,7 @@ __global__ void __launch_bounds__(kAtqThreads, 1)
             const int w = t & 1, vst = stage;
             if (!wait(&full[stage], phase)) break;
             advance();
-            if (!wait(&p_full[w], w ? np1++ : np0++)) break;
+            if (!wait(&p_full[w], w ? np1++ : np++)) break;
             output(w, vst, t < 2);
             if (t + 2 < n) {
               if (!wait(&full[stage], phase)) break;
@@ -444,7 +467,7 @@ __global__ void __launch_bounds__(kAtqThreads, 1)
     const int ulow = ((4 * (ucc & 1) + (uswap ? 2 : 0)) ^ (usub & 7)) * 16;
     for (unsigned k = 0; ok; ++k) {
       const unsigned at = k % kAtSegs;
-      if (!at_wait_warp<kSet>(p, &seg_full[at], (k / kAtSegs) & 1, abort)) {
+      if (!atq_wait_warp(p, &seg_full[at], (k / kAtSegs) & 1, abort)) {
         ok = false;
         break;
       }
@@ -456,7 +479,7 @@ __global__ void __launch_bounds__(kAtqThreads, 1)
       // for; the queries become fp16 in place, each row times a power of two that
       // brings its largest element to [2^14, 2^15)
       if (threadIdx.x == 384) {
-        if (at_wait<kSet>(p, &q_empty, (k & 1) ^ 1u, abort)) {
+        if (atq_wait(p, &q_empty, (k & 1) ^ 1u, abort)) {
           const int tok0 = seg.b * p.N + seg.node0;
           mbar_expect_tx(&q_raw, (unsigned)((1 + seg.pair) * kSub * p.tok * p.G * 128));
           for (int w = 0; w <= seg.pair; ++w)
@@ -469,7 +492,7 @@ __global__ void __launch_bounds__(kAtqThreads, 1)
         }
       }
       __syncwarp();
-      if (!at_wait_warp<kSet>(p, &q_raw, k & 1, abort)) {
+      if (!atq_wait_warp(p, &q_raw, k & 1, abort)) {
         ok = false;
         break;
       }
@@ -515,7 +538,7 @@ __global__ void __launch_bounds__(kAtqThreads, 1)
             if (node0 + kAtKeys <= 0) continue;
             const unsigned u = use + (asked - i), st = u % S, par = ((u / S) & 1) ^ 1u;
             if (asked > i && !mbar_test(&empty[st], par)) break;
-            if (!at_wait<kSet>(p, &empty[st], par, abort)) {
+            if (!atq_wait(p, &empty[st], par, abort)) {
               fail();
               break;
             }
@@ -534,15 +557,15 @@ __global__ void __launch_bounds__(kAtqThreads, 1)
         uint8_t* tile = ring + stage * kTile;
         // a tile with nodes: they are in it already (and 0 behind the last)
         const bool nodes = key0 + kAtKeys > seg.plen, paged = key0 < seg.plen;
-        if (!(nodes ? at_wait_warp<kSet>(p, &node_full[nput % kAtqTurns], (nput / kAtqTurns) & 1, abort)
-                    : at_wait_warp<kSet>(p, &empty[stage], ((use / S) & 1) ^ 1u, abort))) {
+        if (!(nodes ? atq_wait_warp(p, &node_full[nput % kAtqTurns], (nput / kAtqTurns) & 1, abort)
+                    : atq_wait_warp(p, &empty[stage], ((use / S) & 1) ^ 1u, abort))) {
           ok = false;
           break;
         }
         nput += nodes;
         unsigned hole = 0;
         if (paged) {
-          if (!at_wait_warp<kSet>(p, &raw_full[rst], rphase, abort)) {
+          if (!atq_wait_warp(p, &raw_full[rst], rphase, abort)) {
             ok = false;
             break;
           }
@@ -650,11 +673,11 @@ __global__ void __launch_bounds__(kAtqThreads, 1)
     auto meet = [&](uint64_t* bar, unsigned& uses) {
       __syncwarp();
       if (lane == 0) mbar_arrive(bar);
-      return at_wait_warp<kSet>(p, bar, uses++ & 1, abort);
+      return atq_wait_warp(p, bar, uses++ & 1, abort);
     };
     bool ok = true;
     for (unsigned k = 0; ok; ++k) {
-      if (!at_wait_warp<kSet>(p, &seg_full[k % kAtSegs], (k / kAtSegs) & 1, abort)) {
+      if (!atq_wait_warp(p, &seg_full[k % kAtSegs], (k / kAtSegs) & 1, abort)) {
         ok = false;
         break;
       }
@@ -699,7 +722,7 @@ __global__ void __launch_bounds__(kAtqThreads, 1)
           for (int c = 0; c < 4; ++c) see[c] = __funnelshift_r(x[c], x[c + 1], tree0 & 31);
         }
         const unsigned turn = (ring0 / 2 + t) % kAtqTurns;
-        if (!at_wait_warp<kSet>(p, &s_full[w], ns++ & 1, abort)) {
+        if (!atq_wait_warp(p, &s_full[w], ns++ & 1, abort)) {
           ok = false;
           break;
         }
@@ -712,7 +735,7 @@ __global__ void __launch_bounds__(kAtqThreads, 1)
           // tree entries that are not finite are 0 in the tiles, and the sums of
           // the rows that see them become NaN
           const int use = v_use(pair, t, seg.n);
-          if (!at_wait_warp<kSet>(p, &full[slot_of(use)], ((ring0 + use) / S) & 1, abort)) {
+          if (!atq_wait_warp(p, &full[slot_of(use)], ((ring0 + use) / S) & 1, abort)) {
             ok = false;
             break;
           }
@@ -766,41 +789,12 @@ __global__ void __launch_bounds__(kAtqThreads, 1)
             f2unpack(add2(sum0, sum1), x, y);
             return x + y;
           };
-          bool good = false;
-          if (i > 0) {
-            uint32_t sa[32], sb[32], p0[16], p1[16], p2[16], p3[16];
-            nm2 = f2pack(kA4Off - m, kA4Off - m);
-            sum0 = sum1 = 0;
-            tmem_ld32_async(sbase, sa);
-            tmem_wait_ld(sa);
-            tmem_ld32_async(sbase + 32, sb);
-            if (edge) hide(sa, 0);
-            weights(sa, p0);
-            tmem_wait_ld(sb);
-            tmem_ld32_async(sbase + 64, sa);
-            if (edge) hide(sb, 1);
-            weights(sb, p1);
-            tmem_wait_ld(sa);
-            tmem_ld32_async(sbase + 96, sb);
-            if (edge) hide(sa, 2);
-            weights(sa, p2);
-            tmem_wait_ld(sb);
-            if (edge) hide(sb, 3);
-            weights(sb, p3);
-            good = __all_sync(0xffffffffu, total() <= kAtqLazy || r >= nrows);
-            if (good) {
-              tmem_st16(sbase, p0);
-              tmem_st16(sbase + 16, p1);
-              tmem_st16(sbase + 32, p2);
-              tmem_st16(sbase + 48, p3);
-            }
-          }
-          if (!good) {
-            // the first tile, or a sum that shows the reference to be too old:
-            // the row's maximum first
+          // the row's maximum over the chunks from c0 on becomes its reference; what
+          // there is of sums, output and weights follows
+          auto renew = [&](int c0) {
             float x = -INFINITY, y = -INFINITY;
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
+            for (int c = c0; c < 4; ++c) {
               uint32_t a[32];
               tmem_ld32(sbase + 32 * c, a);
               if (edge) hide(a, c);
@@ -825,18 +819,42 @@ __global__ void __launch_bounds__(kAtqThreads, 1)
                 tmem_st16(at, o);
               }
             }
+            const uint32_t f2 = pack_half(f, f);
+#pragma unroll 1
+            for (int c = 0; c < c0; ++c) {  // weights that are stored already
+              uint32_t o[16];
+              tmem_ld16(sbase + 16 * c, o);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) o[j] = hmul2(o[j], f2);
+              tmem_st16(sbase + 16 * c, o);
+            }
+            tmem_wait_st();
+          };
+          int c = 0;
+          bool old = i > 0, stale = i == 0;  // the reference may be too old; it is
+#pragma unroll 1
+          while (c < 4) {  // weights of a chunk go over scores already taken
+            if (stale) renew(c);
+            stale = false;
+            uint32_t a[32], pk[16];
+            tmem_ld32(sbase + 32 * c, a);
+            if (edge) hide(a, c);
             nm2 = f2pack(kA4Off - m, kA4Off - m);
             sum0 = sum1 = 0;
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {  // P of a chunk goes over scores already taken
-              uint32_t a[32], pk[16];
-              tmem_ld32(sbase + 32 * c, a);
-              if (edge) hide(a, c);
-              weights(a, pk);
-              tmem_st16(sbase + 16 * c, pk);
+            weights(a, pk);
+            const float sum = total();
+            // a sum that shows the reference to be too old: once more with the
+            // maximum of what is left, which serves to the tile's end
+            if (old && __any_sync(0xffffffffu, sum > kAtqLazy && r < nrows)) {
+              stale = true;
+              old = false;
+              continue;
             }
+            l += sum;
+            tmem_st16(sbase + 16 * c, pk);
+            ++c;
           }
-          l += spoilt ? __int_as_float(0x7FC00000) : total();
+          if (spoilt) l = __int_as_float(0x7FC00000);
           tmem_wait_st();
         }
         tmem_fence_before();
@@ -846,7 +864,7 @@ __global__ void __launch_bounds__(kAtqThreads, 1)
       if (!ok) break;
       // the item's output, or its partial as [D / 4][rows][4], so that a
       // warp's lanes (rows) store 512 consecutive bytes
-      if (nt > 0 && !at_wait_warp<kSet>(p, &o_full[w], no++ & 1, abort)) {
+      if (nt > 0 && !atq_wait_warp(p, &o_full[w], no++ & 1, abort)) {
         ok = false;
         break;
       }
