@@ -1735,7 +1735,8 @@ spec_status_t spec_tree_attention_kv4(const void* q, const void* pages, long lon
     t.opart = reinterpret_cast<float*>(ws + plan.t.off_part);
     const uint64_t limit = g_wait_limit_ns.load(std::memory_order_relaxed);
     t.sleep_ns = (unsigned)std::min<uint64_t>(limit, sv::kSuspendHintNs);
-    t.tries = (int)std::min<uint64_t>(limit / sv::kSuspendHintNs + 1, 1000000);
+    t.polls = limit > 1 ? 128 : 1;
+    t.tries = limit > 1 ? (int)std::min<uint64_t>(limit / 10000 + 1, 1000000) : 1;
     t.pages = static_cast<const uint8_t*>(pages);
     t.table = page_table;
     {

@@ -40,8 +40,8 @@ struct AttnQParams : AttnParams {
   const int32_t* exps;   // [2] or null
   long long n_pages;
   int Wt, lg;            // the table's width; log2 of the page size
-  int tries;             // of a wait before it is given up, each a sleep of up to
-  unsigned sleep_ns;     // this
+  int tries, polls;      // a wait is given up after tries x polls tests, each a sleep of up to
+  unsigned sleep_ns;     // this (of which the hardware takes some hundred ns)
 };
 
 // Put i of a segment of n tiles into the ring, in the order of use: pairs K0 V0
@@ -79,7 +79,9 @@ __device__ __forceinline__ bool atq_wait(const AttnQParams& p, uint64_t* bar, un
                                          const int* abort, int more = 0) {
 #pragma unroll 1
   for (int i = p.tries + more; i > 0; --i) {
-    if (mbar_try_wait(bar, parity, p.sleep_ns)) return true;
+#pragma unroll 1
+    for (int j = p.polls; j > 0; --j)
+      if (mbar_try_wait(bar, parity, p.sleep_ns)) return true;
     if (*(const volatile int*)abort) break;
   }
   return false;
@@ -89,7 +91,9 @@ __device__ __forceinline__ bool atq_wait_warp(const AttnQParams& p, uint64_t* ba
                                               const int* abort) {
 #pragma unroll 1
   for (int i = p.tries; i > 0; --i) {
-    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity, p.sleep_ns))) return true;
+#pragma unroll 1
+    for (int j = p.polls; j > 0; --j)
+      if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity, p.sleep_ns))) return true;
     if (__any_sync(0xffffffffu, *(const volatile int*)abort)) break;
   }
   return false;
@@ -579,13 +583,13 @@ __global__ void __launch_bounds__(kAtqThreads, 1)
           const uint8_t* scales = src + 8 * D + usub * (D / 16) + ucc * 2;
           uint8_t* dst = tile + udst;
           const int left = seg.plen - key0 - (warp - 12) * 32 - usub;  // positions from this one on
-#pragma unroll
-          for (int j = 0; j < 32 / kRows; ++j) {
+          auto load = [&](int j, uint4& x, uint32_t& two) {
             const int group = j * kRows / 16, place = j * kRows % 16;
-            if (j * kRows >= left || ((hole >> ((warp - 12) * 2 + group)) & 1)) continue;
-            uint4 x = lds128(codes + group * (kHalf / 8) + place * (D / 2));
-            const uint32_t s01 =
-                kv4_scales(*reinterpret_cast<const uint16_t*>(scales + group * (kHalf / 8) + place * (D / 16)));
+            x = lds128(codes + group * (kHalf / 8) + place * (D / 2));
+            two = *reinterpret_cast<const uint16_t*>(scales + group * (kHalf / 8) + place * (D / 16));
+          };
+          auto unpack = [&](int j, uint4 x, uint32_t two) {
+            const uint32_t s01 = kv4_scales(two);
             const uint32_t s0 = prmt(s01, 0, uswap ? 0x3232 : 0x1010);
             const uint32_t s1 = prmt(s01, 0, uswap ? 0x1010 : 0x3232);
             if (uswap) x = make_uint4(x.z, x.w, x.x, x.y);
@@ -597,6 +601,23 @@ __global__ void __launch_bounds__(kAtqThreads, 1)
               const uint32_t s = e < 2 ? s0 : s1;
               *reinterpret_cast<uint4*>(dst + j * kRows * 128 + (ulow ^ (e * 16))) =
                   make_uint4(hmul2(h[0], s), hmul2(h[1], s), hmul2(h[2], s), hmul2(h[3], s));
+            }
+          };
+          if (!nodes && !hole) {  // all of them: loads first, and no branches between
+            uint4 x[32 / kRows];
+            uint32_t two[32 / kRows];
+#pragma unroll
+            for (int j = 0; j < 32 / kRows; ++j) load(j, x[j], two[j]);
+#pragma unroll
+            for (int j = 0; j < 32 / kRows; ++j) unpack(j, x[j], two[j]);
+          } else if (paged) {
+#pragma unroll 1
+            for (int j = 0; j < 32 / kRows; ++j) {
+              if (j * kRows >= left || ((hole >> ((warp - 12) * 2 + j * kRows / 16)) & 1)) continue;
+              uint4 x;
+              uint32_t two;
+              load(j, x, two);
+              unpack(j, x, two);
             }
           }
         }
