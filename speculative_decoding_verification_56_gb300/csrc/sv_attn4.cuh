@@ -7,7 +7,9 @@
 
 namespace sv {
 
-constexpr int kA4Warps = 8;  // 16 positions of a tile of 128 each
+constexpr int kA4Warps = 8;
+constexpr int kA4Step = 32;  // positions that a warp takes at once: two products' 16 entries
+constexpr int kA4Tile = kA4Warps * kA4Step;
 constexpr int kA4Threads = kA4Warps * 32;
 constexpr int kA4MaxCtas = 320;
 constexpr float kA4Off = 7.0f;   // weights are held 2^7 times as large: fp16 then has them down
@@ -47,7 +49,7 @@ __device__ __forceinline__ int attn4_len(const Attn4Params& p, int base) {
 __device__ __forceinline__ int attn4_node_tiles(const Attn4Params& p) { return (p.N + 127) >> 7; }
 __device__ __forceinline__ int attn4_units(const Attn4Params& p, int base) {
   const int len = attn4_len(p, base);
-  return len < 0 ? 0 : attn4_node_tiles(p) - 1 + max(1, (len >> 7) + ((len & 127) != 0));
+  return len < 0 ? 0 : attn4_node_tiles(p) - 1 + max(1, len / kA4Tile + (len % kA4Tile != 0));
 }
 
 // A CTA's run of units is cut into segments, one per item it meets.
@@ -131,17 +133,17 @@ template <int D, int NT>
 __host__ __device__ constexpr int a4_red_bytes() { return kA4Warps / 2 * NT * 8 * D * 4; }
 template <int NT>
 __host__ __device__ constexpr int a4_per_sm() { return NT == 1 ? 2 : 1; }
-// Groups of 16 positions that each warp has in flight: what fits beside the
-// queries, the join's buffer and the static arrays
+// Steps of kA4Step positions that each warp has in shared memory: what fits
+// beside the queries, the join's buffer and the static arrays
 template <int D, int NT>
 __host__ __device__ constexpr int a4_stages() {
   const int room = 232448 / a4_per_sm<NT>() - 1024 - 4096 - a4_q_bytes<D, NT>() - a4_red_bytes<D, NT>();
-  const int fit = room / (kA4Warps * kv4_group(D));
-  return fit < 8 ? fit : 8;
+  const int fit = room / (kA4Warps * 2 * kv4_group(D));
+  return fit < 4 ? fit : 4;
 }
 template <int D, int NT>
 __host__ __device__ constexpr int a4_smem() {
-  return a4_stages<D, NT>() * kA4Warps * kv4_group(D) + a4_q_bytes<D, NT>() + a4_red_bytes<D, NT>();
+  return a4_stages<D, NT>() * kA4Warps * 2 * kv4_group(D) + a4_q_bytes<D, NT>() + a4_red_bytes<D, NT>();
 }
 
 template <int D, int NT>
@@ -153,17 +155,17 @@ __global__ void __launch_bounds__(kA4Threads, a4_per_sm<NT>())
   constexpr int kQStride = D * 2 + 16;  // bytes of a query row: neighbouring rows in other banks
   constexpr int kGroup = kv4_group(D);
   constexpr int kStages = a4_stages<D, NT>();
+  constexpr int kStage = 2 * kGroup;
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ uint64_t full[kA4Warps][kStages];
-  __shared__ int s_nopage[kA4Warps][kStages];  // the group's table entry names no page
   __shared__ Attn4Walk s_walk[kA4Warps];       // of the copies
   __shared__ long long s_sum[kA4Warps], s_bstart;
   __shared__ int s_b;
   __shared__ float s_m[kA4Warps][NT * 8], s_l[kA4Warps][NT * 8];
   __shared__ float s_fac[NT * 8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  uint8_t* ring = smem + warp * (kStages * kGroup);
-  uint8_t* s_q = smem + kA4Warps * kStages * kGroup;
+  uint8_t* ring = smem + warp * (kStages * kStage);
+  uint8_t* s_q = smem + kA4Warps * kStages * kStage;
   float* s_red = reinterpret_cast<float*>(s_q + a4_q_bytes<D, NT>());
   if (lane == 0)
     for (int s = 0; s < kStages; ++s) mbar_init(&full[warp][s], 1);
@@ -226,50 +228,55 @@ __global__ void __launch_bounds__(kA4Threads, a4_per_sm<NT>())
   const int page = 1 << p.lg;
 
   // ---------------- copies ----------------
-  // Each warp brings in its own groups, kStages ahead of their use: nobody
-  // waits for another warp before the end of an item.  c_at: the next group's
-  // first position in the sequence, up to c_end (and below c_len); c_id: its page, read
-  // one group ahead.
+  // Each warp brings in its own steps, kStages ahead of their use: nobody waits
+  // for another warp before the end of an item.  c_at: the next step's first
+  // position in the sequence, up to c_end; lane j < 2 brings in its positions 16 j ..,
+  // whose page c_id was looked up one step ahead.
   int c_at = 0, c_end = 0, c_h = 0, c_id = -1;
   const int32_t* c_row = p.table;
-  unsigned issued = 0, taken = 0;  // groups so far
+  unsigned issued = 0, taken = 0;  // steps so far
+  unsigned holes = 0;              // bits 2 s, 2 s + 1: step s's positions have no page
   bool dead = false;  // a wait was given up: go on without work, so that all barriers are met
   if (lane == 0) s_walk[warp] = walk;
   __syncwarp();
-  auto next_group = [&]() {  // moves c_at on to a group; false: no more
-    if (c_at < c_end) return true;
+  auto look_up = [&]() {  // -2: no position there
+    const int at = c_at + 16 * lane;
+    c_id = lane < 2 && at < c_end ? c_row[at >> p.lg] : -2;
+  };
+  auto next_item = [&]() {  // the next one with a step for this warp; false: none
     Attn4Walk w = s_walk[warp];
     __syncwarp();
     Attn4Seg s;
     bool some = false;
     while (!some && w.next(p, &s, warp == 0 && lane == 0)) {
-      c_at = max(s.t0 - lead, 0) * 128 + warp * 16;
-      c_end = min(s.len, (s.t0 + s.n - lead) * 128);
+      c_at = max(s.t0 - lead, 0) * kA4Tile + warp * kA4Step;
+      c_end = min(s.len, (s.t0 + s.n - lead) * kA4Tile);
       c_h = s.h;
       c_row = p.table + (size_t)s.b * p.W;
       some = c_at < c_end;
     }
     if (lane == 0) s_walk[warp] = w;
     __syncwarp();
-    if (some) c_id = c_row[c_at >> p.lg];
+    if (some) look_up();
     return some;
   };
   auto refill = [&](int st) {
-    if (dead || !next_group()) return;
-    if (lane == 0) {
-      const bool ok = c_id >= 0 && c_id < p.n_pages;
-      s_nopage[warp][st] = !ok;
-      if (!ok) set_flag(p.flags, kFlagBadPage);
-      mbar_expect_tx(&full[warp][st], ok ? kGroup : 0);
-      if (ok)
-        bulk_g2s(ring + st * kGroup,
-                 p.pages + ((size_t)c_id * p.Hkv + c_h) * kv4_block(page, D) +
-                     ((c_at & (page - 1)) >> 4) * kGroup,
-                 kGroup, &full[warp][st]);
-    }
+    if (c_at >= c_end && !next_item()) return;
+    const bool ok = c_id >= 0 && c_id < p.n_pages;
+    const unsigned some = __ballot_sync(0xffffffffu, ok);
+    const unsigned none = __ballot_sync(0xffffffffu, !ok && c_id != -2);
+    if (none && lane == 0) set_flag(p.flags, kFlagBadPage);
+    holes = (holes & ~(3u << (2 * st))) | (none << (2 * st));
+    if (lane == 0) mbar_expect_tx(&full[warp][st], __popc(some) * kGroup);
+    __syncwarp();
+    if (ok)
+      bulk_g2s(ring + st * kStage + lane * kGroup,
+               p.pages + ((size_t)c_id * p.Hkv + c_h) * kv4_block(page, D) +
+                   (((c_at + 16 * lane) & (page - 1)) >> 4) * kGroup,
+               kGroup, &full[warp][st]);
     ++issued;
-    c_at += 128;
-    if (c_at < c_end) c_id = c_row[c_at >> p.lg];
+    c_at += kA4Tile;
+    look_up();
   };
   for (int s = 0; s < kStages; ++s) refill(s);
 
@@ -330,25 +337,35 @@ __global__ void __launch_bounds__(kA4Threads, a4_per_sm<NT>())
         vis[i][c] = (seg.row0 + min(8 * i + 2 * t + c, seg.nrows - 1)) / p.G;
       }
     }
-    // scores of 16 entries (rows of the products g, g + 8), hidden ones already
-    // -inf, to weights; renews references that they outgrow
-    auto weights = [&](float (&s)[NT][4], uint32_t (&w)[NT][2]) {
-      bool over = false;
+    // products of 16 entries a time (rows g, g + 8), hidden ones -inf, to weights;
+    // renews references that their scores outgrow
+    auto weights = [&](auto& s, auto& w) {
+      constexpr int kTimes = sizeof(s) / sizeof(s[0]);
+      float top = -INFINITY;
+      float mo[NT][2];
 #pragma unroll
       for (int i = 0; i < NT; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) over |= s[i][e] > m[i][e & 1] + kA4Lazy;
-      if (__any_sync(0xffffffffu, over)) {
+        for (int c = 0; c < 2; ++c) {
+          mo[i][c] = kA4Off - m[i][c];
+#pragma unroll
+          for (int q = 0; q < kTimes; ++q)
+            top = fmaxf(top, fmaf(fmaxf(s[q][i][c], s[q][i][c + 2]), fac[i][c], mo[i][c]));
+        }
+      if (__any_sync(0xffffffffu, top > kA4Off + kA4Lazy)) {
 #pragma unroll
         for (int i = 0; i < NT; ++i)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            float x = fmaxf(s[i][c], s[i][c + 2]);
+            float x = fmaxf(s[0][i][c], s[0][i][c + 2]);
+#pragma unroll
+            for (int q = 1; q < kTimes; ++q) x = fmaxf(x, fmaxf(s[q][i][c], s[q][i][c + 2]));
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-            const float mn = fmaxf(m[i][c], x);
+            const float mn = fmaxf(m[i][c], x * fac[i][c]);
             const float f = ex2(m[i][c] - mn);
             m[i][c] = mn;
+            mo[i][c] = kA4Off - mn;
             l[i][c] *= f;
 #pragma unroll
             for (int j = 0; j < kSteps; ++j) {
@@ -358,15 +375,17 @@ __global__ void __launch_bounds__(kA4Threads, a4_per_sm<NT>())
           }
       }
 #pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        float e[4];
+      for (int q = 0; q < kTimes; ++q)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) e[c] = ex2(s[i][c] + (kA4Off - m[i][c & 1]));
-        l[i][0] += e[0] + e[2];
-        l[i][1] += e[1] + e[3];
-        w[i][0] = mov_trans(pack_half(e[0], e[1]));
-        w[i][1] = mov_trans(pack_half(e[2], e[3]));
-      }
+        for (int i = 0; i < NT; ++i) {
+          float e[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) e[c] = ex2(fmaf(s[q][i][c], fac[i][c & 1], mo[i][c & 1]));
+          l[i][0] += e[0] + e[2];
+          l[i][1] += e[1] + e[3];
+          w[q][i][0] = mov_trans(pack_half(e[0], e[1]));
+          w[q][i][1] = mov_trans(pack_half(e[2], e[3]));
+        }
     };
 
 #pragma unroll 1
@@ -378,9 +397,9 @@ __global__ void __launch_bounds__(kA4Threads, a4_per_sm<NT>())
         if (u0 < p.N && (p.mask || u0 <= last)) {
           const size_t node0 = (size_t)seg.b * p.N;
           const size_t stride = (size_t)p.Hkv * D;
-          float s[NT][4];
+          float s[1][NT][4];
 #pragma unroll
-          for (int i = 0; i < NT; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.0f;
+          for (int i = 0; i < NT; ++i) s[0][i][0] = s[0][i][1] = s[0][i][2] = s[0][i][3] = 0.0f;
           const int n0 = u0 + pi, n1 = n0 + 8;
           bool bad0 = false, bad1 = false;
           {
@@ -396,8 +415,8 @@ __global__ void __launch_bounds__(kA4Threads, a4_per_sm<NT>())
                                       node_half2(x.w, kinv, bad0), node_half2(y.w, kinv, bad1)};
 #pragma unroll
               for (int i = 0; i < NT; ++i) {
-                mma_16816(s[i], a0, qf[i][j][0], qf[i][j][1]);
-                mma_16816(s[i], a1, qf[i][j + 1][0], qf[i][j + 1][1]);
+                mma_16816(s[0][i], a0, qf[i][j][0], qf[i][j][1]);
+                mma_16816(s[0][i], a1, qf[i][j + 1][0], qf[i][j + 1][1]);
               }
             }
           }
@@ -437,126 +456,143 @@ __global__ void __launch_bounds__(kA4Threads, a4_per_sm<NT>())
               if (see)
                 see = p.mask ? (p.mask[(node0 + v) * p.Wm + (nn >> 5)] >> (nn & 31)) & 1 : nn <= v;
               const bool bad = (badv >> (e < 2 ? pi : pi + 8)) & 1;
-              s[i][e] = !see ? -INFINITY : bad ? __int_as_float(0x7FC00000) : s[i][e] * fac[i][e & 1];
+              if (!see || bad) s[0][i][e] = see ? __int_as_float(0x7FC00000) : -INFINITY;
             }
-          uint32_t w[NT][2];
+          uint32_t w[1][NT][2];
           weights(s, w);
 #pragma unroll
           for (int b = 0; b < kSteps; ++b) {
             const uint32_t a[4] = {prmt(hv[0][b], hv[1][b], 0x5410), prmt(hv[0][b], hv[1][b], 0x7632),
                                    prmt(hv[2][b], hv[3][b], 0x5410), prmt(hv[2][b], hv[3][b], 0x7632)};
 #pragma unroll
-            for (int i = 0; i < NT; ++i) mma_16816(o[i][b], a, w[i][0], w[i][1]);
+            for (int i = 0; i < NT; ++i) mma_16816(o[i][b], a, w[0][i][0], w[0][i][1]);
           }
         }
       }
     }
 
-    // ---- 16 committed positions ----
-    const int end = min(seg.len, (seg.t0 + seg.n - lead) * 128);
+    // ---- 32 committed positions ----
+    const int end = min(seg.len, (seg.t0 + seg.n - lead) * kA4Tile);
 #pragma unroll 1
-    for (int at = max(seg.t0 - lead, 0) * 128 + warp * 16; at < end; at += 128) {
-      if (!dead) {
-        if (mbar_wait_bounded(&full[warp][stage], phase, p.wait_ns)) {
-          ++taken;
-        } else {
-          dead = true;
-          if (lane == 0) set_flag(p.flags, kFlagTimeout);
-        }
-        dead = __any_sync(0xffffffffu, dead);
+    for (int at = max(seg.t0 - lead, 0) * kA4Tile + warp * kA4Step; at < end && !dead; at += kA4Tile) {
+      if (!__all_sync(0xffffffffu, mbar_wait_bounded(&full[warp][stage], phase, p.wait_ns))) {
+        dead = true;
+        if (lane == 0) set_flag(p.flags, kFlagTimeout);
+        break;
       }
+      ++taken;
+      const uint8_t* block = ring + stage * kStage;
+      const bool edge = at + kA4Step > seg.len || ((holes >> (2 * stage)) & 3);
+      float s[2][NT][4];
+      uint32_t w[2][NT][2];
       {
-        if (!dead && !s_nopage[warp][stage]) {
-          const uint8_t* block = ring + stage * kGroup;
-          float s[NT][4];
+        const uint8_t* kc = block + pi * (D / 2) + t * (kCh / 2);
+        const uint8_t* ks = block + 8 * D + pi * (D / 16) + t * (kCh / 16);
+        uint32_t x[2][2][kCh / 8], sc[2][2];
 #pragma unroll
-          for (int i = 0; i < NT; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.0f;
-          {
-            const uint8_t* kc = block + pi * (D / 2) + t * (kCh / 2);
-            const uint8_t* ks = block + 8 * D + pi * (D / 16) + t * (kCh / 16);
-            uint32_t x[2][kCh / 8], sc[2];
+        for (int q = 0; q < 2; ++q)
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              if constexpr (D == 128) {
-                const uint4 y = lds128(kc + r * 8 * (D / 2));
-                x[r][0] = y.x;
-                x[r][1] = y.y;
-                x[r][2] = y.z;
-                x[r][3] = y.w;
-                sc[r] = kv4_scales(*reinterpret_cast<const uint16_t*>(ks + r * 8 * (D / 16)));
-              } else {
-                const uint2 y = *reinterpret_cast<const uint2*>(kc + r * 8 * (D / 2));
-                x[r][0] = y.x;
-                x[r][1] = y.y;
-                sc[r] = kv4_scales(*(ks + r * 8 * (D / 16)));
-              }
-            }
-#pragma unroll
-            for (int c = 0; c < kCh / 8; ++c) {
-              uint32_t h0[4], h1[4];
-              kv4_unpack(x[0][c], h0);
-              kv4_unpack(x[1][c], h1);
-              const uint32_t s0 = prmt(sc[0], 0, c < 2 ? 0x1010 : 0x3232);
-              const uint32_t s1 = prmt(sc[1], 0, c < 2 ? 0x1010 : 0x3232);
-#pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                const uint32_t a[4] = {hmul2(h0[2 * j], s0), hmul2(h1[2 * j], s1),
-                                       hmul2(h0[2 * j + 1], s0), hmul2(h1[2 * j + 1], s1)};
-#pragma unroll
-                for (int i = 0; i < NT; ++i) mma_16816(s[i], a, qf[i][2 * c + j][0], qf[i][2 * c + j][1]);
-              }
+          for (int r = 0; r < 2; ++r) {
+            const uint8_t* kr = kc + q * kGroup + r * 8 * (D / 2);
+            const uint8_t* sr = ks + q * kGroup + r * 8 * (D / 16);
+            if constexpr (D == 128) {
+              const uint4 y = lds128(kr);
+              x[q][r][0] = y.x;
+              x[q][r][1] = y.y;
+              x[q][r][2] = y.z;
+              x[q][r][3] = y.w;
+              sc[q][r] = kv4_scales(*reinterpret_cast<const uint16_t*>(sr));
+            } else {
+              const uint2 y = *reinterpret_cast<const uint2*>(kr);
+              x[q][r][0] = y.x;
+              x[q][r][1] = y.y;
+              sc[q][r] = kv4_scales(*sr);
             }
           }
-          const bool in0 = at + pi < seg.len, in1 = at + pi + 8 < seg.len;
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+          for (int i = 0; i < NT; ++i) s[q][i][0] = s[q][i][1] = s[q][i][2] = s[q][i][3] = 0.0f;
+#pragma unroll
+        for (int c = 0; c < kCh / 8; ++c)
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            uint32_t h0[4], h1[4];
+            kv4_unpack(x[q][0][c], h0);
+            kv4_unpack(x[q][1][c], h1);
+            const uint32_t s0 = prmt(sc[q][0], 0, c < 2 ? 0x1010 : 0x3232);
+            const uint32_t s1 = prmt(sc[q][1], 0, c < 2 ? 0x1010 : 0x3232);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const uint32_t a[4] = {hmul2(h0[2 * j], s0), hmul2(h1[2 * j], s1),
+                                     hmul2(h0[2 * j + 1], s0), hmul2(h1[2 * j + 1], s1)};
+#pragma unroll
+              for (int i = 0; i < NT; ++i)
+                mma_16816(s[q][i], a, qf[i][2 * c + j][0], qf[i][2 * c + j][1]);
+            }
+          }
+      }
+      if (edge) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const bool hole = (holes >> (2 * stage + q)) & 1;
+          const bool in0 = at + 16 * q + pi < seg.len && !hole;
+          const bool in1 = at + 16 * q + pi + 8 < seg.len && !hole;
 #pragma unroll
           for (int i = 0; i < NT; ++i)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              s[i][e] = (e < 2 ? in0 : in1) ? s[i][e] * fac[i][e & 1] : -INFINITY;
-          uint32_t w[NT][2];
-          weights(s, w);
-          {
-            const uint8_t* vc = block + kGroup / 2 + t * (D / 2) + g * (kCv / 2);
-            const uint8_t* vs = block + kGroup / 2 + 8 * D + t * (D / 16) + (g * kCv) / 16;
-            uint32_t x[4][kCv / 8], sc[4];
+              if (!(e < 2 ? in0 : in1)) s[q][i][e] = -INFINITY;
+        }
+      }
+      weights(s, w);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              if constexpr (D == 128) {
-                const uint2 y = *reinterpret_cast<const uint2*>(vc + 4 * i * (D / 2));
-                x[i][0] = y.x;
-                x[i][1] = y.y;
-              } else {
-                x[i][0] = *reinterpret_cast<const uint32_t*>(vc + 4 * i * (D / 2));
-              }
-              // behind the last position anything may stand: 0 times it is 0
-              const uint32_t y = at + 4 * i + t < seg.len ? *(vs + 4 * i * (D / 16)) : 0u;
-              sc[i] = prmt(kv4_scales(y), 0, 0x1010);
-            }
+      for (int q = 0; q < 2; ++q) {
+        const uint8_t* vc = block + q * kGroup + kGroup / 2 + t * (D / 2) + g * (kCv / 2);
+        const uint8_t* vs = block + q * kGroup + kGroup / 2 + 8 * D + t * (D / 16) + (g * kCv) / 16;
+        uint32_t x[4][kCv / 8], sc[4];
 #pragma unroll
-            for (int c = 0; c < kCv / 8; ++c) {
-              uint32_t h[4][4];
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (D == 128) {
+            const uint2 y = *reinterpret_cast<const uint2*>(vc + 4 * i * (D / 2));
+            x[i][0] = y.x;
+            x[i][1] = y.y;
+          } else {
+            x[i][0] = *reinterpret_cast<const uint32_t*>(vc + 4 * i * (D / 2));
+          }
+          sc[i] = vs[4 * i * (D / 16)];
+        }
+        if (edge) {  // behind the last position anything may stand: 0 times it is 0
+          const bool hole = (holes >> (2 * stage + q)) & 1;
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                kv4_unpack(x[i][c], h[i]);
+          for (int i = 0; i < 4; ++i)
+            if (at + 16 * q + 4 * i + t >= seg.len || hole) sc[i] = 0;
+        }
 #pragma unroll
-                for (int j = 0; j < 4; ++j) h[i][j] = hmul2(h[i][j], sc[i]);
-              }
+        for (int i = 0; i < 4; ++i) sc[i] = prmt(kv4_scales(sc[i]), 0, 0x1010);
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const uint32_t a[4] = {prmt(h[0][j], h[1][j], 0x5410), prmt(h[0][j], h[1][j], 0x7632),
-                                       prmt(h[2][j], h[3][j], 0x5410), prmt(h[2][j], h[3][j], 0x7632)};
+        for (int c = 0; c < kCv / 8; ++c) {
+          uint32_t h[4][4];
 #pragma unroll
-                for (int i = 0; i < NT; ++i) mma_16816(o[i][4 * c + j], a, w[i][0], w[i][1]);
-              }
-            }
+          for (int i = 0; i < 4; ++i) {
+            kv4_unpack(x[i][c], h[i]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) h[i][j] = hmul2(h[i][j], sc[i]);
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t a[4] = {prmt(h[0][j], h[1][j], 0x5410), prmt(h[0][j], h[1][j], 0x7632),
+                                   prmt(h[2][j], h[3][j], 0x5410), prmt(h[2][j], h[3][j], 0x7632)};
+#pragma unroll
+            for (int i = 0; i < NT; ++i) mma_16816(o[i][4 * c + j], a, w[q][i][0], w[q][i][1]);
           }
         }
-        __syncwarp();
-        refill(stage);
-        if (++stage == kStages) {
-          stage = 0;
-          phase ^= 1u;
-        }
+      }
+      __syncwarp();
+      refill(stage);
+      if (++stage == kStages) {
+        stage = 0;
+        phase ^= 1u;
       }
     }
 
