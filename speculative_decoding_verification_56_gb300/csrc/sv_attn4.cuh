@@ -119,9 +119,13 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4],
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// whether one of two bf16 is not finite
+__device__ __forceinline__ bool bf16_inf(uint32_t x) {
+  return (x & 0x7F80u) == 0x7F80u || (x & 0x7F800000u) == 0x7F800000u;
+}
 // two bf16 times f (a power of two) as two fp16, saturating; bad: one is not finite
 __device__ __forceinline__ uint32_t node_half2(uint32_t x, float f, bool& bad) {
-  bad |= (x & 0x7F80u) == 0x7F80u || (x & 0x7F800000u) == 0x7F800000u;
+  bad |= bf16_inf(x);
   const float lo = fminf(fmaxf(bf16_lo(x) * f, -65504.0f), 65504.0f);
   const float hi = fminf(fmaxf(bf16_hi(x) * f, -65504.0f), 65504.0f);
   return pack_half(lo, hi);
@@ -158,7 +162,8 @@ __global__ void __launch_bounds__(kA4Threads, a4_per_sm<NT>())
   constexpr int kStage = 2 * kGroup;
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ uint64_t full[kA4Warps][kStages];
-  __shared__ Attn4Walk s_walk[kA4Warps];       // of the copies
+  __shared__ Attn4Walk s_walk[kA4Warps], s_at[kA4Warps];  // of the copies, and of the products
+  __shared__ Attn4Seg s_seg[kA4Warps];
   __shared__ long long s_sum[kA4Warps], s_bstart;
   __shared__ int s_b;
   __shared__ float s_m[kA4Warps][NT * 8], s_l[kA4Warps][NT * 8];
@@ -222,8 +227,6 @@ __global__ void __launch_bounds__(kA4Threads, a4_per_sm<NT>())
     }
   }
   __syncthreads();
-  Attn4Walk walk{lo, hi, s_bstart, s_b};
-  Attn4Seg seg;
   const int lead = attn4_node_tiles(p) - 1;  // units before the first tile of positions
   const int page = 1 << p.lg;
 
@@ -234,10 +237,9 @@ __global__ void __launch_bounds__(kA4Threads, a4_per_sm<NT>())
   // whose page c_id was looked up one step ahead.
   int c_at = 0, c_end = 0, c_h = 0, c_id = -1;
   const int32_t* c_row = p.table;
-  unsigned issued = 0, taken = 0;  // steps so far
-  unsigned holes = 0;              // bits 2 s, 2 s + 1: step s's positions have no page
+  unsigned holes = 0;  // bits 2 s, 2 s + 1: stage s's positions have no page; 16 + s: it is in use
   bool dead = false;  // a wait was given up: go on without work, so that all barriers are met
-  if (lane == 0) s_walk[warp] = walk;
+  if (lane == 0) s_walk[warp] = s_at[warp] = Attn4Walk{lo, hi, s_bstart, s_b};
   __syncwarp();
   auto look_up = [&]() {  // -2: no position there
     const int at = c_at + 16 * lane;
@@ -266,7 +268,7 @@ __global__ void __launch_bounds__(kA4Threads, a4_per_sm<NT>())
     const unsigned some = __ballot_sync(0xffffffffu, ok);
     const unsigned none = __ballot_sync(0xffffffffu, !ok && c_id != -2);
     if (none && lane == 0) set_flag(p.flags, kFlagBadPage);
-    holes = (holes & ~(3u << (2 * st))) | (none << (2 * st));
+    holes = (holes & ~(3u << (2 * st))) | (none << (2 * st)) | (0x10000u << st);
     if (lane == 0) mbar_expect_tx(&full[warp][st], __popc(some) * kGroup);
     __syncwarp();
     if (ok)
@@ -274,7 +276,6 @@ __global__ void __launch_bounds__(kA4Threads, a4_per_sm<NT>())
                p.pages + ((size_t)c_id * p.Hkv + c_h) * kv4_block(page, D) +
                    (((c_at + 16 * lane) & (page - 1)) >> 4) * kGroup,
                kGroup, &full[warp][st]);
-    ++issued;
     c_at += kA4Tile;
     look_up();
   };
@@ -289,7 +290,18 @@ __global__ void __launch_bounds__(kA4Threads, a4_per_sm<NT>())
   unsigned phase = 0;
   auto meet = [&]() { __syncthreads(); };
 
-  while (walk.next(p, &seg, false)) {
+  // (a warp's walk and item stand in shared memory: the loop below has no registers
+  // to spare for them)
+  Attn4Seg& seg = s_seg[warp];
+  for (;;) {
+    __syncwarp();
+    if (lane == 0) {
+      Attn4Walk w = s_at[warp];
+      if (!w.next(p, &seg, false)) seg.n = 0;
+      s_at[warp] = w;
+    }
+    __syncwarp();
+    if (seg.n == 0) break;
     // queries as fp16, each row times a power of two that brings its largest
     // element to [2^14, 2^15)
     for (int r = warp; r < NT * 8; r += kA4Warps) {
@@ -420,21 +432,18 @@ __global__ void __launch_bounds__(kA4Threads, a4_per_sm<NT>())
               }
             }
           }
-          // values: this thread's four nodes 4 i + t of the 16, channels kCv g ..
-          uint32_t hv[4][kCv / 2];
+          // values: this thread's four nodes 4 i + t of the 16, channels kCv g ..;
+          // looked at first, and loaded once more for their product
+          const uint16_t* vrow[4];
           unsigned badv = 0;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int nn = u0 + 4 * i + t;
-            const uint16_t* v0 = p.nv + (node0 + min(nn, p.N - 1)) * stride + seg.h * D + kCv * g;
+            vrow[i] = p.nv + (node0 + min(u0 + 4 * i + t, p.N - 1)) * stride + seg.h * D + kCv * g;
             bool bad = false;
 #pragma unroll
-            for (int c = 0; c < kCv / 2; c += 4) {
-              const uint4 x = *reinterpret_cast<const uint4*>(v0 + 2 * c);
-              hv[i][c] = node_half2(x.x, vinv, bad);
-              hv[i][c + 1] = node_half2(x.y, vinv, bad);
-              hv[i][c + 2] = node_half2(x.z, vinv, bad);
-              hv[i][c + 3] = node_half2(x.w, vinv, bad);
+            for (int c = 0; c < kCv; c += 8) {
+              const uint4 x = *reinterpret_cast<const uint4*>(vrow[i] + c);
+              bad |= bf16_inf(x.x) || bf16_inf(x.y) || bf16_inf(x.z) || bf16_inf(x.w);
             }
             badv |= bad ? 1u << (4 * i + t) : 0u;
           }
@@ -442,11 +451,6 @@ __global__ void __launch_bounds__(kA4Threads, a4_per_sm<NT>())
           // here, and the scores of the rows that see them become NaN
           badv |= (bad0 ? 1u << pi : 0u) | (bad1 ? 1u << (pi + 8) : 0u);
           badv = __reduce_or_sync(0xffffffffu, badv);
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if ((badv >> (4 * i + t)) & 1)
-#pragma unroll
-              for (int c = 0; c < kCv / 2; ++c) hv[i][c] = 0;
 #pragma unroll
           for (int i = 0; i < NT; ++i)
 #pragma unroll
@@ -461,18 +465,32 @@ __global__ void __launch_bounds__(kA4Threads, a4_per_sm<NT>())
           uint32_t w[1][NT][2];
           weights(s, w);
 #pragma unroll
-          for (int b = 0; b < kSteps; ++b) {
-            const uint32_t a[4] = {prmt(hv[0][b], hv[1][b], 0x5410), prmt(hv[0][b], hv[1][b], 0x7632),
-                                   prmt(hv[2][b], hv[3][b], 0x5410), prmt(hv[2][b], hv[3][b], 0x7632)};
+          for (int c = 0; c < kCv; c += 8) {
+            uint32_t h[4][4];
 #pragma unroll
-            for (int i = 0; i < NT; ++i) mma_16816(o[i][b], a, w[0][i][0], w[0][i][1]);
+            for (int i = 0; i < 4; ++i) {
+              uint4 x = *reinterpret_cast<const uint4*>(vrow[i] + c);
+              if ((badv >> (4 * i + t)) & 1) x = make_uint4(0, 0, 0, 0);
+              bool dummy = false;
+              h[i][0] = node_half2(x.x, vinv, dummy);
+              h[i][1] = node_half2(x.y, vinv, dummy);
+              h[i][2] = node_half2(x.z, vinv, dummy);
+              h[i][3] = node_half2(x.w, vinv, dummy);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t a[4] = {prmt(h[0][j], h[1][j], 0x5410), prmt(h[0][j], h[1][j], 0x7632),
+                                     prmt(h[2][j], h[3][j], 0x5410), prmt(h[2][j], h[3][j], 0x7632)};
+#pragma unroll
+              for (int i = 0; i < NT; ++i) mma_16816(o[i][c / 2 + j], a, w[0][i][0], w[0][i][1]);
+            }
           }
         }
       }
     }
 
     // ---- 32 committed positions ----
-    const int end = min(seg.len, (seg.t0 + seg.n - lead) * kA4Tile);
+    const int len = seg.len, end = min(len, (seg.t0 + seg.n - lead) * kA4Tile);
 #pragma unroll 1
     for (int at = max(seg.t0 - lead, 0) * kA4Tile + warp * kA4Step; at < end && !dead; at += kA4Tile) {
       if (!__all_sync(0xffffffffu, mbar_wait_bounded(&full[warp][stage], phase, p.wait_ns))) {
@@ -480,9 +498,9 @@ __global__ void __launch_bounds__(kA4Threads, a4_per_sm<NT>())
         if (lane == 0) set_flag(p.flags, kFlagTimeout);
         break;
       }
-      ++taken;
+      holes &= ~(0x10000u << stage);
       const uint8_t* block = ring + stage * kStage;
-      const bool edge = at + kA4Step > seg.len || ((holes >> (2 * stage)) & 3);
+      const bool edge = at + kA4Step > len || ((holes >> (2 * stage)) & 3);
       float s[2][NT][4];
       uint32_t w[2][NT][2];
       {
@@ -536,8 +554,8 @@ __global__ void __launch_bounds__(kA4Threads, a4_per_sm<NT>())
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           const bool hole = (holes >> (2 * stage + q)) & 1;
-          const bool in0 = at + 16 * q + pi < seg.len && !hole;
-          const bool in1 = at + 16 * q + pi + 8 < seg.len && !hole;
+          const bool in0 = at + 16 * q + pi < len && !hole;
+          const bool in1 = at + 16 * q + pi + 8 < len && !hole;
 #pragma unroll
           for (int i = 0; i < NT; ++i)
 #pragma unroll
@@ -566,7 +584,7 @@ __global__ void __launch_bounds__(kA4Threads, a4_per_sm<NT>())
           const bool hole = (holes >> (2 * stage + q)) & 1;
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if (at + 16 * q + 4 * i + t >= seg.len || hole) sc[i] = 0;
+            if (at + 16 * q + 4 * i + t >= len || hole) sc[i] = 0;
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) sc[i] = prmt(kv4_scales(sc[i]), 0, 0x1010);
@@ -686,8 +704,14 @@ __global__ void __launch_bounds__(kA4Threads, a4_per_sm<NT>())
     }
   }
   // every copy has landed before the CTA can leave
-  for (; taken < issued; ++taken)
-    mbar_wait_bounded(&full[warp][taken % kStages], (taken / kStages) & 1);
+  if (dead)
+    for (int s = 0; s < kStages; ++s, ++stage) {
+      if (stage == kStages) {
+        stage = 0;
+        phase ^= 1u;
+      }
+      if ((holes >> (16 + stage)) & 1) mbar_wait_bounded(&full[warp][stage], phase);
+    }
 }
 
 // Joins the partials of items that several CTAs share; other rows are done.  A
