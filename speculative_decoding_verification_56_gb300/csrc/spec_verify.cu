@@ -811,19 +811,32 @@ spec_status_t pages_params(void* pages, int planes, long long plane_stride, long
   return SPEC_OK;
 }
 
-spec_status_t run_pages(void (*plan)(sv::PagesParams), const sv::PagesParams& prm, void* stream) {
-  // CTAs of the plan: one per 8192 table entries or 1024 words of the bitmap
+spec_status_t run_pages(bool fork, const sv::PagesParams& prm, void* stream) {
+  // one CTA's shared memory where the tables are small, else a cluster with a CTA
+  // per 8192 table entries or 1024 words of the bitmap
   const long long entries = (long long)std::max(prm.B, prm.B2) * prm.W;
-  int cluster = 1;
-  while (cluster < sv::kPgMaxCluster &&
-         (entries > 8192ll * cluster || prm.words > sv::kPgThreads * cluster))
-    cluster *= 2;
-  spec_status_t st = launch(plan, cluster, 0, prm, stream, true, cluster, sv::kPgThreads);
+  spec_status_t st;
+  if (prm.words <= sv::kPgSmallWords && entries <= 65536 && prm.B2 <= sv::kPgSmallRows) {
+    st = launch(fork ? sv::pages_fork_small_kernel : sv::pages_compact_small_kernel, 1, 0, prm,
+                stream, true, 1, sv::kPgThreads);
+  } else {
+    int cluster = 1;
+    while (cluster < sv::kPgMaxCluster &&
+           (entries > 8192ll * cluster || prm.words > sv::kPgThreads * cluster))
+      cluster *= 2;
+    st = launch(fork ? sv::pages_fork_kernel : sv::pages_compact_kernel, cluster, 0, prm, stream,
+                true, cluster, sv::kPgThreads);
+  }
   if (st != SPEC_OK) return st;
   int sms = 0;
   st = sm_count(&sms);
   if (st != SPEC_OK) return st;
-  return launch(sv::pages_copy_kernel, sms * 8, 0, prm, stream, true, 1, sv::kPgCopyThreads);
+  // no more CTAs than the most copies have units
+  const long long unit = 16ll * sv::kPgCopyThreads * sv::kPgCopyVecs;
+  const double units = (double)(fork ? prm.B2 : prm.n_pages) * prm.planes *
+                       (double)((prm.page_bytes + unit - 1) / unit);
+  const int grid = (int)std::max(1.0, std::min((double)sms * 8, units));
+  return launch(sv::pages_copy_kernel, grid, 0, prm, stream, true, 1, sv::kPgCopyThreads);
 }
 
 struct BeamLayout {
@@ -1821,7 +1834,7 @@ spec_status_t spec_kv_pages_fork(void* pages, int planes, long long plane_stride
   prm.need = need;
   prm.new_len = new_len;
   prm.page = page_size;
-  return run_pages(sv::pages_fork_kernel, prm, stream);
+  return run_pages(true, prm, stream);
 }
 
 spec_status_t spec_kv_pages_compact(void* pages, int planes, long long plane_stride,
@@ -1834,7 +1847,7 @@ spec_status_t spec_kv_pages_compact(void* pages, int planes, long long plane_str
                                         page_table, B, B, W, new_table, used, workspace,
                                         workspace_bytes, &prm);
   if (st != SPEC_OK) return st;
-  return run_pages(sv::pages_compact_kernel, prm, stream);
+  return run_pages(false, prm, stream);
 }
 
 size_t spec_beam_select_workspace_bytes(int B, int K, int V, int M, int dtype) {
@@ -1890,7 +1903,12 @@ spec_status_t spec_beam_select(const void* logits, int dtype, const float* score
                                ? run_beam_rows<sv::BF16>(prm.rows, vec, stream)
                                : run_beam_rows<sv::F32>(prm.rows, vec, stream);
   if (st != SPEC_OK) return st;
-  const size_t smem = (size_t)K * M * 12 + (size_t)sv::kBeamWarps * L.nchunks;
+  const int off = (int)(((size_t)K * M * 12 + (size_t)sv::kBeamWarps * L.nchunks + 15) / 16 * 16);
+  // a row's candidates in shared memory, where all warps' fit beside the rest
+  const bool staged = off + (size_t)sv::kBeamWarps * L.nchunks * M * 8 <= 48 << 10;
+  prm.off_stage = off;
+  prm.stage = staged ? L.nchunks * M : 0;
+  const size_t smem = off + (size_t)sv::kBeamWarps * prm.stage * 8;
   return launch(sv::beam_select_kernel, B, smem, prm, stream, true, 1, sv::kBeamThreads);
 }
 

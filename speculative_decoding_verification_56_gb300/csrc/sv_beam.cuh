@@ -29,6 +29,7 @@ struct BeamParams {
   int32_t* out_token;
   int32_t* out_finished;
   int B, K, M, eos;
+  int off_stage, stage;  // shared memory: candidates staged per warp (C M, or 0)
 };
 
 __global__ void __launch_bounds__(kBeamThreads) beam_select_kernel(const BeamParams p) {
@@ -43,27 +44,30 @@ __global__ void __launch_bounds__(kBeamThreads) beam_select_kernel(const BeamPar
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
   uint8_t* head = s_head + warp * C;
+  float* cval = reinterpret_cast<float*>(beam_mem + p.off_stage) + (size_t)warp * 2 * p.stage;
+  int* cidx = reinterpret_cast<int*>(cval + p.stage);
   for (int k = warp; k < K; k += kBeamWarps) {
     const size_t row = (size_t)b * K + k;
     double* tot = s_tot + k * M;
     int* tok = s_tok + k * M;
-    const double score = (double)p.score[row];
-    if (p.finished && p.finished[row]) {
-      for (int r = lane; r < M; r += 32) {
-        tot[r] = r == 0 && score > -INFINITY ? score : -INFINITY;
-        tok[r] = r == 0 ? p.eos : 0x7FFFFFFF;
-      }
-      continue;
-    }
     const GrowRec* rec = p.rows.rec + row * C;
+    // (all loads of a row at once)
+    const float score = p.score[row];
+    const bool done = p.finished && p.finished[row];
     int lref = kRefEmpty;
     FSum acc = FSum::zero();
-    for (int c = lane; c < C; c += 32) {
-      const int gref = __ldcg(&rec[c].ref);
-      FSum v;
-      v.hi = __ldcg(&rec[c].hi);
-      v.lo = __ldcg(&rec[c].lo);
-      head[c] = 0;
+    unsigned live = 0;  // of the first 32 records
+    for (int c0 = 0; c0 < C; c0 += 32) {
+      const int c = c0 + lane;
+      int gref = kRefEmpty;
+      FSum v = FSum::zero();
+      if (c < C) {
+        gref = __ldcg(&rec[c].ref);
+        v.hi = __ldcg(&rec[c].hi);
+        v.lo = __ldcg(&rec[c].lo);
+        head[c] = 0;
+      }
+      if (c0 == 0) live = __ballot_sync(0xffffffffu, gref != kRefEmpty);
       if (gref > lref) {
         acc.scale(pow2i_f(lref - gref));
         lref = gref;
@@ -71,11 +75,61 @@ __global__ void __launch_bounds__(kBeamThreads) beam_select_kernel(const BeamPar
       v.scale(pow2i_f(gref - lref));
       acc = df_add(acc, v);
     }
+    const bool staged = C * M <= p.stage;
+    if (staged)
+      for (int i = lane; i < C * M; i += 32) {
+        const int c = i / M, h = i - c * M;
+        cval[i] = __ldcg(&rec[c].val[h]);
+        cidx[i] = __ldcg(&rec[c].idx[h]);
+      }
+    if (done) {
+      for (int r = lane; r < M; r += 32) {
+        tot[r] = r == 0 && score > -INFINITY ? (double)score : -INFINITY;
+        tok[r] = r == 0 ? p.eos : 0x7FFFFFFF;
+      }
+      __syncwarp();
+      continue;
+    }
     const int R = warp_max_i(lref);
     acc.scale(pow2i_f(lref - R));
     const FSum S = df_norm(warp_sum_df(acc));
     const double ln2 = 0.6931471805599453;
     const double lse = rint(((double)R + log2(S.value())) * ln2 * 4294967296.0) * (1.0 / 4294967296.0);
+    auto put = [&](int r, float v, int i) {
+      const double x = (double)score + ((double)v * (double)p.rows.scale * ln2 - lse);
+      tot[r] = i < p.rows.V && x > -INFINITY ? x : -INFINITY;
+      tok[r] = i;
+    };
+    __syncwarp();
+    const int nl = __popc(live);
+    if (staged && C <= 32 && nl * M <= 32) {
+      // a row's candidates stand in the records of its segments, mostly one or
+      // two: a lane each, ranked against one another by shuffles
+      const int j = lane / M, e = lane - j * M;
+      float v = -INFINITY;
+      int x = 0x7FFFFFFF;
+      if (j < nl) {
+        unsigned m = live;  // drop the j live records before this lane's
+        for (int t = 0; t < j; ++t) m &= m - 1;
+        const int at = (__ffs(m) - 1) * M + e;
+        v = cval[at];
+        x = cidx[at];
+      }
+      int rank = 0;
+#pragma unroll 8
+      for (int u = 0; u < 32; ++u) {
+        const float vu = __shfl_sync(0xffffffffu, v, u);
+        const int xu = __shfl_sync(0xffffffffu, x, u);
+        rank += (xu != 0x7FFFFFFF && grow_better(vu, xu, v, x)) ? 1 : 0;
+      }
+      const bool real = x < p.rows.V;
+      // (with fewer than M real ones, -inf in records marked empty: the rounds below)
+      if (__popc(__ballot_sync(0xffffffffu, real)) >= M) {
+        if (real && rank < M) put(rank, v, x);
+        __syncwarp();
+        continue;
+      }
+    }
     // M rounds over the chunks' sorted lists, list c at lane c mod 32
     float hv = -INFINITY;  // the best head of this lane's lists
     int hi = 0x7FFFFFFF, hc = -1;
@@ -86,8 +140,8 @@ __global__ void __launch_bounds__(kBeamThreads) beam_select_kernel(const BeamPar
       for (int c = lane; c < C; c += 32) {
         const int h = head[c];
         if (h >= M) continue;
-        const float v = __ldcg(&rec[c].val[h]);
-        const int i = __ldcg(&rec[c].idx[h]);
+        const float v = staged ? cval[c * M + h] : __ldcg(&rec[c].val[h]);
+        const int i = staged ? cidx[c * M + h] : __ldcg(&rec[c].idx[h]);
         if (grow_better(v, i, hv, hi)) {
           hv = v;
           hi = i;
@@ -96,20 +150,23 @@ __global__ void __launch_bounds__(kBeamThreads) beam_select_kernel(const BeamPar
       }
     };
     look();
+    float mv = -INFINITY;  // lane r: the r-th best
+    int mi = 0x7FFFFFFF;
     for (int r = 0; r < M; ++r) {
       float v = hv;
       int i = hi;
       grow_warp_best(v, i);
-      if (lane == 0) {
-        const double x = score + ((double)v * (double)p.rows.scale * ln2 - lse);
-        tot[r] = i < p.rows.V && x > -INFINITY ? x : -INFINITY;
-        tok[r] = i;
+      if (lane == r) {
+        mv = v;
+        mi = i;
       }
       if (hc >= 0 && hi == i) {
         ++head[hc];
         look();
       }
     }
+    if (lane < M) put(lane, mv, mi);
+    __syncwarp();
   }
   __syncthreads();
   // rank of each candidate among all: those of other rows are sorted

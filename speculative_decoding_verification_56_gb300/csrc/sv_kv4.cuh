@@ -79,6 +79,28 @@ __device__ __forceinline__ uint32_t to_e2m1x2(float hi, float lo) {
   return r & 0xFFu;
 }
 
+// A thread's way through `work` items of `per` parts each, all threads of a
+// (layer, sequence) together: item at, part r, without a division per step.
+struct Kv4Walk {
+  int at, r, dat, dr;
+  __device__ __forceinline__ Kv4Walk(unsigned part, int blocks, int per) {
+    const long long first = (long long)part * kKv4Threads + threadIdx.x;
+    const long long step = (long long)blocks * kKv4Threads;
+    at = (int)(first / per);
+    r = (int)(first - (long long)at * per);
+    dat = (int)(step / per);
+    dr = (int)(step - (long long)dat * per);
+  }
+  __device__ __forceinline__ void next(int per) {
+    at += dat;
+    r += dr;
+    if (r >= per) {
+      r -= per;
+      ++at;
+    }
+  }
+};
+
 struct Kv4Params {
   uint8_t* pages;           // [layers, n_pages, Hkv, block]
   const int32_t* table;     // [B, W]
@@ -148,12 +170,10 @@ __global__ void __launch_bounds__(kKv4Threads) kv4_commit_kernel(const Kv4Params
   if (layer == 0 && part == 0 && threadIdx.x == 0)
     p.new_len[b] = count ? base - 1 + count : max(base - 1, 0);
   const int per = p.Hkv * kBlocks * 2;  // threads of an entry
-  const long long work = (long long)count * per;
   const int page = 1 << p.lg;
   const float ke = pow2_small(kv4_exp(p.exps, 2 * layer)), ve = pow2_small(kv4_exp(p.exps, 2 * layer + 1));
-  for (long long i = (long long)part * kKv4Threads + threadIdx.x; i < work;
-       i += (long long)p.blocks * kKv4Threads) {
-    const int at = (int)(i / per), r = (int)(i - (long long)at * per);
+  for (Kv4Walk w(part, p.blocks, per); w.at < count; w.next(per)) {
+    const int at = w.at, r = w.r;
     const int is_v = r >= per / 2, hb = r - is_v * (per / 2);
     const int node = p.path ? p.path[(size_t)b * (p.max_depth + 1) + at] : at;
     const uint16_t* src = (is_v ? p.node_v : p.node_k) +
@@ -166,13 +186,17 @@ __global__ void __launch_bounds__(kKv4Threads) kv4_commit_kernel(const Kv4Params
     const float unit = is_v ? ve : ke;
     const uint32_t sb = to_e4m3(fminf(__fdiv_rn(__uint_as_float(a << 16), 6.0f) / unit, 448.0f));
     const float step = half2_to_float2(kv4_scales(sb)).x * unit;
+    // x / step, to 12 bits: a quotient on the border of two codes is exactly that
+    // (borders have 3 bits), and others are further from it than 2^-8 of it: with
+    // whole numbers X < 2^8 and m < 2^4 (of x and s), X against border x m < 2^7
+    const float inv = step > 0.0f ? 1.0f / step : 0.0f;
+    auto quotient = [&](float y) {
+      return __uint_as_float((__float_as_uint(y * inv) + 0x800u) & 0xFFFFF000u);
+    };
     uint32_t code[2] = {0, 0};
-    if (step > 0.0f) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        code[j >> 2] |= to_e2m1x2(__fdiv_rn(bf16_hi(x[j]), step), __fdiv_rn(bf16_lo(x[j]), step))
-                        << (8 * (j & 3));
-    }
+    for (int j = 0; j < 8; ++j)
+      code[j >> 2] |= to_e2m1x2(quotient(bf16_hi(x[j])), quotient(bf16_lo(x[j]))) << (8 * (j & 3));
     const long long t = (long long)base - 1 + at;
     const int slot = (int)t & (page - 1);
     const int h = hb / kBlocks, c = hb - h * kBlocks;
@@ -196,12 +220,10 @@ __global__ void __launch_bounds__(kKv4Threads) kv4_read_kernel(const Kv4Params p
   if ((len < 0 || len > p.L) && layer == 0 && part == 0 && threadIdx.x == 0)
     set_flag(p.flags, kFlagBadPath);
   const int per = p.Hkv * kBlocks * 2;
-  const long long work = (long long)count * per;
   const int page = 1 << p.lg;
   const float ke = pow2_small(kv4_exp(p.exps, 2 * layer)), ve = pow2_small(kv4_exp(p.exps, 2 * layer + 1));
-  for (long long i = (long long)part * kKv4Threads + threadIdx.x; i < work;
-       i += (long long)p.blocks * kKv4Threads) {
-    const int t = (int)(i / per), r = (int)(i - (long long)t * per);
+  for (Kv4Walk w(part, p.blocks, per); w.at < count; w.next(per)) {
+    const int t = w.at, r = w.r;
     const int is_v = r >= per / 2, hb = r - is_v * (per / 2);
     const long long id = kv4_page_of(p, b, t);
     uint32_t o[8] = {0, 0, 0, 0, 0, 0, 0, 0};

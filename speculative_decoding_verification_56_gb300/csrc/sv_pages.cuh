@@ -308,6 +308,160 @@ __global__ void __launch_bounds__(kPgThreads) pages_compact_kernel(const PagesPa
   }
 }
 
+// The same two plans in one CTA's shared memory, where the tables are small: a
+// plan is a chain of dependent loads, and what counts is how few there are
+// (four beams 10.7 -> %FORK% us with the copies, 64 beams of 18 pages each %FORK64%).
+constexpr int kPgSmallRows = 512;     // new sequences
+constexpr int kPgSmallWords = kPgThreads;
+constexpr int kPgSmallFree = 4096;    // free pages listed in shared memory (others in the workspace)
+
+__global__ void __launch_bounds__(kPgThreads) pages_fork_small_kernel(const PagesParams p) {
+  __shared__ int s_warp[32];
+  __shared__ uint32_t s_bits[kPgSmallWords];
+  __shared__ int s_row[kPgSmallRows], s_len[kPgSmallRows], s_full[kPgSmallRows], s_pages[kPgSmallRows];
+  __shared__ int s_open[kPgSmallRows], s_kept[kPgSmallRows], s_before[kPgSmallRows];
+  __shared__ int s_free[kPgSmallFree];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  s_bits[threadIdx.x] = 0;
+  if (threadIdx.x == 0) *p.ncopies = 0;
+  const int j = threadIdx.x;
+  const bool mine = j < p.B2;
+  PgTake t;
+  t.open = -1;
+  if (mine) {
+    t = pg_take(p, j, true);
+    s_row[j] = t.row;
+    s_len[j] = t.len;
+    s_full[j] = t.full;
+    s_pages[j] = t.pages;
+    s_open[j] = t.open;
+  }
+  __syncthreads();
+  for (int k = warp; k < p.B2; k += kPgThreads / 32) {
+    const int32_t* row = p.table + (size_t)max(s_row[k], 0) * p.W;
+    for (int i = lane; i < s_full[k]; i += 32) {
+      const int id = row[i];
+      if (id >= 0 && id < p.n_pages)
+        atomicOr(&s_bits[id >> 5], 1u << (id & 31));
+      else
+        set_flag(p.flags, kFlagBadPage);
+    }
+  }
+  __syncthreads();
+  // of those that take an unfinished page, the lowest may go on in it, unless it
+  // is held as a full one
+  bool keep = mine && t.open >= 0 && !((s_bits[t.open >> 5] >> (t.open & 31)) & 1);
+  if (keep)
+    for (int i = 0; i < j; ++i)
+      if (s_open[i] == t.open) {
+        keep = false;
+        break;
+      }
+  __syncthreads();
+  if (keep) atomicOr(&s_bits[t.open >> 5], 1u << (t.open & 31));
+  int nfresh;
+  const int before = pg_scan(mine ? max(0, t.pages - t.full - keep) : 0, &nfresh, s_warp);
+  if (mine) {
+    s_kept[j] = t.full + keep;
+    s_before[j] = before;
+  }
+  __syncthreads();
+  uint32_t f = j < p.words ? ~s_bits[j] & pg_valid(p, j) : 0u;
+  int nfree;
+  int at = pg_scan(__popc(f), &nfree, s_warp);
+  while (f && at < nfresh) {
+    const int id = 32 * j + __ffs(f) - 1;
+    if (at < kPgSmallFree)
+      s_free[at] = id;
+    else
+      p.free_ids[at] = id;
+    ++at;
+    f &= f - 1;
+  }
+  __syncthreads();
+  for (int k = warp; k < p.B2; k += kPgThreads / 32) {
+    const int32_t* row = p.table + (size_t)max(s_row[k], 0) * p.W;
+    const int kept = s_kept[k], pages = s_pages[k];
+    for (int i = lane; i < p.W; i += 32) {
+      int id = -1;
+      if (i < kept) {
+        id = row[i];
+        if (id < 0 || id >= p.n_pages) id = -1;
+      } else if (i < pages) {
+        const int r = s_before[k] + i - kept;
+        if (r < nfree)
+          id = r < kPgSmallFree ? s_free[r] : __ldcg(p.free_ids + r);
+        else
+          set_flag(p.flags, kFlagNoPage);
+        if (i == s_full[k] && s_open[k] >= 0 && id >= 0)
+          p.copies[atomicAdd(p.ncopies, 1)] = make_int2(s_open[k], id);
+      }
+      p.new_table[(size_t)k * p.W + i] = id;
+    }
+    if (lane == 0) p.new_len[k] = s_len[k];
+  }
+  if (threadIdx.x == 0) *p.used = p.n_pages - nfree + min(nfresh, nfree);
+}
+
+__global__ void __launch_bounds__(kPgThreads) pages_compact_small_kernel(const PagesParams p) {
+  __shared__ int s_warp[32];
+  __shared__ uint32_t s_bits[kPgSmallWords];
+  __shared__ int s_rank[kPgSmallWords];  // pages held before the word
+  __shared__ int s_free[kPgSmallFree];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+  s_bits[threadIdx.x] = 0;
+  __syncthreads();
+  const int entries = p.B * p.W;  // (few)
+  for (int i = threadIdx.x; i < entries; i += kPgThreads) {
+    const int id = p.table[i];
+    if (id >= 0 && id < p.n_pages)
+      atomicOr(&s_bits[id >> 5], 1u << (id & 31));
+    else if (id >= 0)
+      set_flag(p.flags, kFlagBadPage);
+  }
+  __syncthreads();
+  const int w = threadIdx.x;
+  const uint32_t b = s_bits[w];
+  int held;
+  const int before = pg_scan(__popc(b), &held, s_warp);
+  s_rank[w] = before;
+  const int left = held - 32 * w;
+  const uint32_t m = left >= 32 ? 0xFFFFFFFFu : left <= 0 ? 0u : (1u << left) - 1u;
+  // the k-th free place below `held` takes the k-th page from there on
+  uint32_t f = ~b & m;
+  for (int k = 32 * w - before; f; ++k) {
+    const int id = 32 * w + __ffs(f) - 1;
+    if (k < kPgSmallFree) s_free[k] = id;
+    p.copies[k].y = id;
+    f &= f - 1;
+  }
+  int below;
+  pg_scan(__popc(b & m), &below, s_warp);
+  uint32_t up = b & ~m;
+  for (int k = before + __popc(b & m) - below; up; ++k) {
+    p.copies[k].x = 32 * w + __ffs(up) - 1;
+    up &= up - 1;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < entries; i += kPgThreads) {
+    int id = p.table[i];
+    if (id < 0 || id >= p.n_pages) {
+      id = -1;
+    } else if (id >= held) {
+      const int k = s_rank[id >> 5] + __popc(s_bits[id >> 5] & ((1u << (id & 31)) - 1u)) - below;
+      id = k < kPgSmallFree ? s_free[k] : __ldcg(&p.copies[k].y);
+    }
+    p.new_table[i] = id;
+  }
+  if (threadIdx.x == 0) {
+    *p.used = held;
+    *p.ncopies = held - below;
+  }
+}
+
 // The planned copies, over all planes: units of kPgCopyThreads x kPgCopyVecs
 // vectors of a page's plane.
 __global__ void __launch_bounds__(kPgCopyThreads) pages_copy_kernel(const PagesParams p) {
