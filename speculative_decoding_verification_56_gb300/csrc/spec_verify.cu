@@ -741,12 +741,13 @@ spec_status_t run_attn4_tiles(const sv::AttnQParams& prm, void* stream) {
   return finish_attention<D>(prm, stream);
 }
 
-// Blocks of a (layer, sequence) of the commit and read kernels: enough for its
-// most places, and no more than fill the GPU several times.
-int kv4_blocks(long long places, int Hkv, int D, int layers, int B) {
-  const long long threads = places * Hkv * (D / 16) * 2;
-  const long long most = std::max(1ll, 9728ll / ((long long)layers * B));
-  return (int)std::max(1ll, std::min((threads + sv::kKv4Threads - 1) / sv::kKv4Threads, most));
+// Lanes of an entry and blocks of a (layer, sequence) of the commit and read
+// kernels: enough for its most places, and no more than fill the GPU several times.
+void kv4_grid(sv::Kv4Params* prm, long long places, int D) {
+  prm->lg_lanes = std::min(5, log2_of(prm->Hkv * (D / 16)));
+  const long long per_block = sv::kKv4Threads >> prm->lg_lanes;
+  const long long most = std::max(1ll, 4864ll / ((long long)prm->layers * prm->B));
+  prm->blocks = (int)std::max(1ll, std::min((places + per_block - 1) / per_block, most));
 }
 
 struct PagesLayout {
@@ -1636,7 +1637,7 @@ spec_status_t spec_kv4_commit_path(void* pages, int layers, long long n_pages, i
   prm.lg = log2_of(page_size);
   prm.max_depth = max_depth;
   prm.layers = layers;
-  prm.blocks = kv4_blocks(path_nodes ? std::min(max_depth + 1, N) : N, Hkv, D, layers, B);
+  kv4_grid(&prm, path_nodes ? std::min(max_depth + 1, N) : N, D);
   const int grid = layers * B * prm.blocks;
   return D == 128 ? launch(sv::kv4_commit_kernel<128>, grid, 0, prm, stream, true, 1, sv::kKv4Threads)
                   : launch(sv::kv4_commit_kernel<64>, grid, 0, prm, stream, true, 1, sv::kKv4Threads);
@@ -1680,7 +1681,7 @@ spec_status_t spec_kv4_read(const void* pages, int layers, long long n_pages, in
   prm.lg = log2_of(page_size);
   prm.L = L;
   prm.layers = layers;
-  prm.blocks = kv4_blocks(L, Hkv, D, layers, B);
+  kv4_grid(&prm, L, D);
   const int grid = layers * B * prm.blocks;
   return D == 128 ? launch(sv::kv4_read_kernel<128>, grid, 0, prm, stream, true, 1, sv::kKv4Threads)
                   : launch(sv::kv4_read_kernel<64>, grid, 0, prm, stream, true, 1, sv::kKv4Threads);

@@ -79,28 +79,6 @@ __device__ __forceinline__ uint32_t to_e2m1x2(float hi, float lo) {
   return r & 0xFFu;
 }
 
-// A thread's way through `work` items of `per` parts each, all threads of a
-// (layer, sequence) together: item at, part r, without a division per step.
-struct Kv4Walk {
-  int at, r, dat, dr;
-  __device__ __forceinline__ Kv4Walk(unsigned part, int blocks, int per) {
-    const long long first = (long long)part * kKv4Threads + threadIdx.x;
-    const long long step = (long long)blocks * kKv4Threads;
-    at = (int)(first / per);
-    r = (int)(first - (long long)at * per);
-    dat = (int)(step / per);
-    dr = (int)(step - (long long)dat * per);
-  }
-  __device__ __forceinline__ void next(int per) {
-    at += dat;
-    r += dr;
-    if (r >= per) {
-      r -= per;
-      ++at;
-    }
-  }
-};
-
 struct Kv4Params {
   uint8_t* pages;           // [layers, n_pages, Hkv, block]
   const int32_t* table;     // [B, W]
@@ -117,8 +95,8 @@ struct Kv4Params {
   unsigned* flags;
   long long n_pages, out_layer, out_seq;  // (elements)
   int B, N, Hkv, W, lg, max_depth, L, layers;
-  int places;               // places of a sequence that the grid covers: blocks of
-  int blocks;               // kKv4Threads threads for each (layer, sequence)
+  int blocks;               // of each (layer, sequence)
+  int lg_lanes;             // log2 of the lanes that share an entry
 };
 
 // Page of position t of sequence b, or -1 (outside the table, or no page).
@@ -154,10 +132,24 @@ __device__ __forceinline__ int kv4_commit_count(const Kv4Params& p, int b) {
   return 0;
 }
 
-// Commit: a thread takes 16 channels of one entry's key or value -- two loads
-// of 16 bytes, one store of 8 and one of a byte.  Blocks run over (layer,
-// sequence, part of the sequence's places x heads x channel groups x {key,
-// value}); how many places a sequence has is known only to the device.
+// Where a (layer, sequence)'s threads find their entries: 1 << lg_lanes lanes (as
+// many as an entry has groups of 16 channels, a warp at most) share an entry, so
+// that what an entry costs -- its page, its addresses -- is paid once for many
+// channels.
+struct Kv4Lanes {
+  int first, step, lane, lanes;
+  __device__ __forceinline__ Kv4Lanes(const Kv4Params& p, unsigned part) {
+    const int per_block = kKv4Threads >> p.lg_lanes;
+    first = (int)part * per_block + (int)(threadIdx.x >> p.lg_lanes);
+    step = p.blocks * per_block;
+    lanes = 1 << p.lg_lanes;
+    lane = threadIdx.x & (lanes - 1);
+  }
+};
+
+// Commit: a thread takes 16 channels of an entry's key and as many of its value
+// -- loads of 32 bytes, stores of 8 and of one -- in turn over the entry's heads.
+// How many entries a sequence has is known only to the device.
 template <int D>
 __global__ void __launch_bounds__(kKv4Threads) kv4_commit_kernel(const Kv4Params p) {
   constexpr int kBlocks = D / 16;
@@ -169,45 +161,58 @@ __global__ void __launch_bounds__(kKv4Threads) kv4_commit_kernel(const Kv4Params
   const int base = p.base_len[b];
   if (layer == 0 && part == 0 && threadIdx.x == 0)
     p.new_len[b] = count ? base - 1 + count : max(base - 1, 0);
-  const int per = p.Hkv * kBlocks * 2;  // threads of an entry
-  const int page = 1 << p.lg;
-  const float ke = pow2_small(kv4_exp(p.exps, 2 * layer)), ve = pow2_small(kv4_exp(p.exps, 2 * layer + 1));
-  for (Kv4Walk w(part, p.blocks, per); w.at < count; w.next(per)) {
-    const int at = w.at, r = w.r;
-    const int is_v = r >= per / 2, hb = r - is_v * (per / 2);
+  const int blocks = p.Hkv * kBlocks, page = 1 << p.lg;
+  const float unit[2] = {pow2_small(kv4_exp(p.exps, 2 * layer)),
+                         pow2_small(kv4_exp(p.exps, 2 * layer + 1))};
+  const Kv4Lanes w(p, part);
+  for (int at = w.first; at < count; at += w.step) {
     const int node = p.path ? p.path[(size_t)b * (p.max_depth + 1) + at] : at;
-    const uint16_t* src = (is_v ? p.node_v : p.node_k) +
-                          ((((size_t)layer * p.B + b) * p.N + node) * p.Hkv * kBlocks + hb) * 16;
-    const uint4 x0 = ldg_stream(src), x1 = ldg_stream(src + 8);
-    const uint32_t x[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
-    uint32_t a = 0;  // largest magnitude, as bits
-#pragma unroll
-    for (int j = 0; j < 8; ++j) a = max(a, max(x[j] & 0x7FFFu, (x[j] >> 16) & 0x7FFFu));
-    const float unit = is_v ? ve : ke;
-    const uint32_t sb = to_e4m3(fminf(__fdiv_rn(__uint_as_float(a << 16), 6.0f) / unit, 448.0f));
-    const float step = half2_to_float2(kv4_scales(sb)).x * unit;
-    // x / step, to 12 bits: a quotient on the border of two codes is exactly that
-    // (borders have 3 bits), and others are further from it than 2^-8 of it: with
-    // whole numbers X < 2^8 and m < 2^4 (of x and s), X against border x m < 2^7
-    const float inv = step > 0.0f ? 1.0f / step : 0.0f;
-    auto quotient = [&](float y) {
-      return __uint_as_float((__float_as_uint(y * inv) + 0x800u) & 0xFFFFF000u);
-    };
-    uint32_t code[2] = {0, 0};
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      code[j >> 2] |= to_e2m1x2(quotient(bf16_hi(x[j])), quotient(bf16_lo(x[j]))) << (8 * (j & 3));
+    const size_t src = (((size_t)layer * p.B + b) * p.N + node) * (size_t)blocks * 16;
     const long long t = (long long)base - 1 + at;
     const int slot = (int)t & (page - 1);
-    const int h = hb / kBlocks, c = hb - h * kBlocks;
-    uint8_t* block = p.pages + (((size_t)layer * p.n_pages + kv4_page_of(p, b, t)) * p.Hkv + h) *
-                                   kv4_block(page, D) + kv4_half(slot, is_v, D);
-    *reinterpret_cast<uint2*>(block + (slot & 15) * (D / 2) + c * 8) = make_uint2(code[0], code[1]);
-    block[8 * D + (slot & 15) * kBlocks + c] = (uint8_t)sb;
+    uint8_t* dst = p.pages + ((size_t)layer * p.n_pages + kv4_page_of(p, b, t)) * p.Hkv *
+                                 kv4_block(page, D) + kv4_half(slot, 0, D);
+    const int place = slot & 15;
+    for (int hb = w.lane; hb < blocks; hb += w.lanes) {
+      uint4 x4[2][2];
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        const uint16_t* s = (v ? p.node_v : p.node_k) + src + hb * 16;
+        x4[v][0] = ldg_stream(s);
+        x4[v][1] = ldg_stream(s + 8);
+      }
+      const int h = hb / kBlocks, c = hb % kBlocks;
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        const uint32_t x[8] = {x4[v][0].x, x4[v][0].y, x4[v][0].z, x4[v][0].w,
+                               x4[v][1].x, x4[v][1].y, x4[v][1].z, x4[v][1].w};
+        uint32_t a = 0;  // largest magnitude, as bits
+#pragma unroll
+        for (int j = 0; j < 8; ++j) a = max(a, max(x[j] & 0x7FFFu, (x[j] >> 16) & 0x7FFFu));
+        const uint32_t sb = to_e4m3(fminf(__fdiv_rn(__uint_as_float(a << 16), 6.0f) / unit[v], 448.0f));
+        const float step = half2_to_float2(kv4_scales(sb)).x * unit[v];
+        // x / step, to 12 bits: a quotient on the border of two codes is exactly
+        // that (borders have 3 bits), and others are further from it than 2^-8 of
+        // it: with whole numbers X < 2^8 and m < 2^4 (of x and s), X against
+        // border x m < 2^7
+        const float inv = step > 0.0f ? 1.0f / step : 0.0f;
+        auto quotient = [&](float y) {
+          return __uint_as_float((__float_as_uint(y * inv) + 0x800u) & 0xFFFFF000u);
+        };
+        uint32_t code[2] = {0, 0};
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          code[j >> 2] |= to_e2m1x2(quotient(bf16_hi(x[j])), quotient(bf16_lo(x[j]))) << (8 * (j & 3));
+        uint8_t* block = dst + (size_t)h * kv4_block(page, D) + v * (kv4_group(D) / 2);
+        *reinterpret_cast<uint2*>(block + place * (D / 2) + c * 8) = make_uint2(code[0], code[1]);
+        block[8 * D + place * kBlocks + c] = (uint8_t)sb;
+      }
+    }
   }
 }
 
-// Read: a thread takes 16 channels of one position's key or value.
+// Read: a thread takes 16 channels of a position's key and of its value, in turn
+// over the heads.
 template <int D>
 __global__ void __launch_bounds__(kKv4Threads) kv4_read_kernel(const Kv4Params p) {
   constexpr int kBlocks = D / 16;
@@ -219,39 +224,47 @@ __global__ void __launch_bounds__(kKv4Threads) kv4_read_kernel(const Kv4Params p
   const int count = max(0, min(len, p.L));
   if ((len < 0 || len > p.L) && layer == 0 && part == 0 && threadIdx.x == 0)
     set_flag(p.flags, kFlagBadPath);
-  const int per = p.Hkv * kBlocks * 2;
-  const int page = 1 << p.lg;
-  const float ke = pow2_small(kv4_exp(p.exps, 2 * layer)), ve = pow2_small(kv4_exp(p.exps, 2 * layer + 1));
-  for (Kv4Walk w(part, p.blocks, per); w.at < count; w.next(per)) {
-    const int t = w.at, r = w.r;
-    const int is_v = r >= per / 2, hb = r - is_v * (per / 2);
+  const int blocks = p.Hkv * kBlocks, page = 1 << p.lg;
+  const float unit[2] = {pow2_small(kv4_exp(p.exps, 2 * layer)),
+                         pow2_small(kv4_exp(p.exps, 2 * layer + 1))};
+  const Kv4Lanes w(p, part);
+  for (int t = w.first; t < count; t += w.step) {
     const long long id = kv4_page_of(p, b, t);
-    uint32_t o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (id >= 0) {
-      const int slot = t & (page - 1);
-      const int h = hb / kBlocks, c = hb - h * kBlocks;
-      const uint8_t* block = p.pages + (((size_t)layer * p.n_pages + id) * p.Hkv + h) *
-                                           kv4_block(page, D) + kv4_half(slot, is_v, D);
-      const uint2 code = *reinterpret_cast<const uint2*>(block + (slot & 15) * (D / 2) + c * 8);
-      const float s = half2_to_float2(kv4_scales(block[8 * D + (slot & 15) * kBlocks + c])).x *
-                      (is_v ? ve : ke);
+    if (id < 0 && w.lane == 0) set_flag(p.flags, kFlagBadPage);
+    const int slot = t & (page - 1), place = slot & 15;
+    const uint8_t* src = p.pages + ((size_t)layer * p.n_pages + max(id, 0ll)) * p.Hkv *
+                                       kv4_block(page, D) + kv4_half(slot, 0, D);
+    const size_t dst = layer * p.out_layer + b * p.out_seq + (size_t)t * blocks * 16;
+#pragma unroll 2
+    for (int hb = w.lane; hb < blocks; hb += w.lanes) {
+      const int h = hb / kBlocks, c = hb % kBlocks;
+      uint2 code[2];
+      uint32_t sb[2];
 #pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        uint32_t h4[4];
-        kv4_unpack(w ? code.y : code.x, h4);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 f = half2_to_float2(h4[j]);
-          o[4 * w + j] = pack_bf16(f.x * s, f.y * s);
-        }
+      for (int v = 0; v < 2; ++v) {
+        const uint8_t* block = src + (size_t)h * kv4_block(page, D) + v * (kv4_group(D) / 2);
+        code[v] = *reinterpret_cast<const uint2*>(block + place * (D / 2) + c * 8);
+        sb[v] = block[8 * D + place * kBlocks + c];
       }
-    } else if (r == 0) {
-      set_flag(p.flags, kFlagBadPage);
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        const float s = id < 0 ? 0.0f : half2_to_float2(kv4_scales(sb[v])).x * unit[v];
+        uint32_t o[8];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          uint32_t h4[4];
+          kv4_unpack(e ? code[v].y : code[v].x, h4);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 f = half2_to_float2(h4[j]);
+            o[4 * e + j] = id < 0 ? 0u : pack_bf16(f.x * s, f.y * s);
+          }
+        }
+        uint4* out = reinterpret_cast<uint4*>((v ? p.v_out : p.k_out) + dst + hb * 16);
+        out[0] = make_uint4(o[0], o[1], o[2], o[3]);
+        out[1] = make_uint4(o[4], o[5], o[6], o[7]);
+      }
     }
-    uint16_t* dst = (is_v ? p.v_out : p.k_out) + layer * p.out_layer + b * p.out_seq +
-                    ((size_t)t * p.Hkv * kBlocks + hb) * 16;
-    *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
-    *reinterpret_cast<uint4*>(dst + 8) = make_uint4(o[4], o[5], o[6], o[7]);
   }
 }
 
