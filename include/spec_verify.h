@@ -703,7 +703,7 @@ SPEC_API spec_status_t spec_kv_pages_compact(void* pages, int planes, long long 
  *   scores    float [B, K]; -inf (or NaN): the beam has no candidate
  *   finished  int32 [B, K] (not 0: finished) or NULL
  *   eos       the token that ends a beam, or -1
- *   K         1..64;  M 1..16;  ceil(V / chunk) M <= 2048 (chunk = 16384 bf16 /
+ *   K         1..64;  M 1..16;  B K ceil(V / chunk) < 2^25 (chunk = 16384 bf16 /
  *             8192 fp32 elements)
  * Outputs [B, M]: out_scores float (the totals), out_parents int32 (rows b K +
  * k: what spec_kv_pages_fork takes), out_tokens int32, out_finished int32 (the

@@ -842,27 +842,47 @@ spec_status_t run_pages(bool fork, const sv::PagesParams& prm, void* stream) {
 
 struct BeamLayout {
   int nchunks = 0;
-  size_t bytes = 0;
+  size_t off_runs = 0, bytes = 0;
 };
 bool beam_layout(int B, int K, int V, int M, int dtype, BeamLayout* L) {
-  if (B < 0 || K < 1 || K > sv::kBeamMaxK || M < 1 || M > sv::kGrowMaxK || V < 1 ||
+  if (B < 0 || K < 1 || K > sv::kBeamMaxK || M < 1 || M > sv::kBeamMaxM || V < 1 ||
       V > SPEC_MAX_V || (dtype != SPEC_DTYPE_F32 && dtype != SPEC_DTYPE_BF16))
     return false;
   const int C = (V + chunk_elems(dtype) - 1) / chunk_elems(dtype);
-  if (C * M > sv::kGrowMaxCand || (long long)B * K * C > INT32_MAX) return false;
+  if ((long long)B * K * C > INT32_MAX / 64) return false;
+  const size_t items = (size_t)B * K * C;
   L->nchunks = C;
-  L->bytes = align_up(kDataOffset + (size_t)B * K * C * sizeof(sv::GrowRec));
+  L->off_runs = align_up(kDataOffset + items * sv::kWarps * sizeof(float2));
+  L->bytes = align_up(L->off_runs + items * sv::kBeamRuns * sizeof(float));
   return true;
 }
 
 template <typename E>
-spec_status_t run_beam_rows(const sv::GrowParams& prm, bool vec, void* stream) {
-  if (!vec)
-    return launch(sv::grow_topk_kernel<E, false, true>, prm.items, 0, prm, stream, true);
-  int grid = 0;
-  const spec_status_t st = persistent_grid<sv::grow_topk_stream_kernel<E, true>>(prm.items, &grid);
+spec_status_t run_beam(const sv::BeamParams& prm, bool vec, void* stream) {
+  spec_status_t st;
+  if (vec) {
+    int grid = 0;
+    st = persistent_grid<sv::beam_rows_stream_kernel<E>>(prm.items, &grid);
+    if (st == SPEC_OK)
+      st = launch(sv::beam_rows_stream_kernel<E>, grid, kStreamSmem, prm, stream, true);
+  } else {
+    st = launch(sv::beam_rows_kernel<E>, prm.items, 0, prm, stream, true);
+  }
   if (st != SPEC_OK) return st;
-  return launch(sv::grow_topk_stream_kernel<E, true>, grid, kStreamSmem, prm, stream, true);
+  const int nruns = prm.nchunks * sv::kBeamRuns;
+  constexpr size_t kMost = (size_t)sv::kBeamMaxK * sv::kBeamMaxM * 12 +
+                           (size_t)sv::kBeamWarps * sv::kBeamStage * sizeof(float);
+  const size_t smem = (size_t)prm.K * prm.M * 12 +
+                      (nruns <= sv::kBeamStage
+                           ? (size_t)std::min(prm.K, sv::kBeamWarps) * nruns * sizeof(float) : 0);
+  if (vec) {
+    st = ensure_smem<sv::beam_select_kernel<E, true>>(kMost);
+    if (st != SPEC_OK) return st;
+    return launch(sv::beam_select_kernel<E, true>, prm.B, smem, prm, stream, true, 1, sv::kBeamThreads);
+  }
+  st = ensure_smem<sv::beam_select_kernel<E, false>>(kMost);
+  if (st != SPEC_OK) return st;
+  return launch(sv::beam_select_kernel<E, false>, prm.B, smem, prm, stream, true, 1, sv::kBeamThreads);
 }
 
 }  // namespace
@@ -1566,7 +1586,6 @@ spec_status_t spec_tree_grow(const void* draft_logits, int dtype, float temperat
   prm.flags = reinterpret_cast<unsigned*>(ws);
   // every draft row the growth reads, reduced in one streaming launch
   prm.rows_per_tree = 1 + (D - 1) * K;
-  prm.slots = K;
   if ((long long)B * prm.rows_per_tree * prm.nchunks > INT32_MAX) return SPEC_ERR_INVALID_ARG;
   prm.items = B * prm.rows_per_tree * prm.nchunks;
   const bool vec = vec_ok(draft_logits, V, dtype);  // whole 16-byte vectors per row
@@ -1877,40 +1896,27 @@ spec_status_t spec_beam_select(const void* logits, int dtype, const float* score
   char* ws = static_cast<char*>(workspace);
   sv::BeamParams prm;
   std::memset(&prm, 0, sizeof prm);
-  prm.rows.logits = logits;
-  prm.rows.scale = (float)(1.4426950408889634 / (double)temperature);
-  prm.rows.B = B * K;
-  prm.rows.D = 1;
-  prm.rows.K = M;
-  prm.rows.V = V;
-  prm.rows.nchunks = L.nchunks;
-  prm.rows.rows_per_tree = 1;
-  prm.rows.slots = 1;
-  prm.rows.items = B * K * L.nchunks;
-  prm.rows.rec = reinterpret_cast<sv::GrowRec*>(ws + kDataOffset);
-  prm.rows.flags = reinterpret_cast<unsigned*>(ws);
+  prm.logits = logits;
   prm.score = scores;
   prm.finished = finished;
+  prm.part = reinterpret_cast<float2*>(ws + kDataOffset);
+  prm.runs = reinterpret_cast<float*>(ws + L.off_runs);
   prm.out_score = out_scores;
   prm.out_parent = out_parents;
   prm.out_token = out_tokens;
   prm.out_finished = out_finished;
+  prm.flags = reinterpret_cast<unsigned*>(ws);
+  prm.scale = (float)(1.4426950408889634 / (double)temperature);
   prm.B = B;
   prm.K = K;
+  prm.V = V;
   prm.M = M;
   prm.eos = eos;
+  prm.nchunks = L.nchunks;
+  prm.items = B * K * L.nchunks;
   const bool vec = vec_ok(logits, V, dtype);
-  const spec_status_t st = dtype == SPEC_DTYPE_BF16
-                               ? run_beam_rows<sv::BF16>(prm.rows, vec, stream)
-                               : run_beam_rows<sv::F32>(prm.rows, vec, stream);
-  if (st != SPEC_OK) return st;
-  const int off = (int)(((size_t)K * M * 12 + (size_t)sv::kBeamWarps * L.nchunks + 15) / 16 * 16);
-  // a row's candidates in shared memory, where all warps' fit beside the rest
-  const bool staged = off + (size_t)sv::kBeamWarps * L.nchunks * M * 8 <= 48 << 10;
-  prm.off_stage = off;
-  prm.stage = staged ? L.nchunks * M : 0;
-  const size_t smem = off + (size_t)sv::kBeamWarps * prm.stage * 8;
-  return launch(sv::beam_select_kernel, B, smem, prm, stream, true, 1, sv::kBeamThreads);
+  return dtype == SPEC_DTYPE_BF16 ? run_beam<sv::BF16>(prm, vec, stream)
+                                  : run_beam<sv::F32>(prm, vec, stream);
 }
 
 spec_status_t spec_verify_read_flags(void* workspace, uint32_t* host_flags, int clear,

@@ -54,7 +54,6 @@ struct GrowParams {
   float scale;         // log2(e) / T
   int B, D, K, V, M, nchunks;
   int rows_per_tree;   // draft rows read per tree: 1 + (D - 1) K
-  int slots;           // row slots of a layer: K
   int items;           // B rows_per_tree nchunks
   GrowRec* rec;        // [B, rows_per_tree, nchunks]
   double* nval;        // [B, kGrowMaxNodes]
@@ -101,7 +100,7 @@ __device__ __forceinline__ size_t grow_row_offset(const GrowParams& p, int rowi)
   const int b = rowi / p.rows_per_tree, q = rowi - b * p.rows_per_tree;
   const int layer = q == 0 ? 0 : 1 + (q - 1) / p.K;
   const int slot = q == 0 ? 0 : (q - 1) - (layer - 1) * p.K;
-  return (((size_t)b * p.D + layer) * p.slots + slot) * (size_t)p.V;
+  return (((size_t)b * p.D + layer) * p.K + slot) * (size_t)p.V;
 }
 
 // Streaming top-k over row segments.  A CTA walks contiguous items (row,
@@ -340,20 +339,6 @@ __device__ __noinline__ void grow_seg_merge(const GrowParams& p, GrowSegSmem& sh
   }
 }
 
-// stats_chunk with each chunk's own reference: a row's sum is then the same (to
-// the 2^-44 of the double-float sums) wherever the row is cut between CTAs.
-template <typename E>
-__device__ __forceinline__ void stats_chunk_fixed(const uint4 (&raw)[kVecPerThread], float s,
-                                                  StatsState& st, float m) {
-  StatsState c;
-  stats_chunk<E>(raw, s, c, m);
-  if (c.ref > st.ref) {
-    st.acc.scale(pow2i_f(st.ref - c.ref));
-    st.ref = c.ref;
-  }
-  st.acc.add(c.acc.hi * pow2i_f(c.ref - st.ref));
-}
-
 // One item for the whole CTA (every thread calls it with the same flags):
 // the softmax partial runs on in st; the warp appends its candidates.  A
 // segment's state lives in slot seg % kGrowSlots.  first: the item opens a
@@ -365,7 +350,7 @@ __device__ __forceinline__ void stats_chunk_fixed(const uint4 (&raw)[kVecPerThre
 // the next segment's barrier, and no warp runs more than kStages items
 // ahead of the slowest, so kGrowSlots slots cover every segment in use.
 // Otherwise one warp writes the item's empty record.
-template <typename E, bool kFixed>
+template <typename E>
 __device__ __forceinline__ void grow_seg_item(const GrowParams& p,
                                               const uint4 (&raw)[kVecPerThread], int item, int c,
                                               bool first, bool last, StatsState& st, float& thr,
@@ -398,10 +383,7 @@ __device__ __forceinline__ void grow_seg_item(const GrowParams& p,
   int n = grow_warp_append<E>(sh, raw, vm, j0, j1, K, nb, thr, &sh.thr_key[slot]);
   // the softmax partial after the candidates, so that the vector maxima are
   // no longer live across its arithmetic
-  if constexpr (kFixed)
-    stats_chunk_fixed<E>(raw, p.scale, st, tmax);
-  else
-    stats_chunk<E>(raw, p.scale, st, tmax);
+  stats_chunk<E>(raw, p.scale, st, tmax);
   GrowRec* out = p.rec + item;  // item = row * nchunks + chunk
   if (!last) {
     if (warp == item % kWarps) {
@@ -444,7 +426,7 @@ __device__ __forceinline__ void grow_seg_item(const GrowParams& p,
 }
 
 // One CTA per item, plain loads (any row size and alignment).
-template <typename E, bool kVec, bool kFixed = false>
+template <typename E, bool kVec>
 __global__ void __launch_bounds__(kThreads, 2) grow_topk_kernel(const GrowParams p) {
   using St = typename E::storage;
   __shared__ GrowSegSmem sh;
@@ -463,13 +445,13 @@ __global__ void __launch_bounds__(kThreads, 2) grow_topk_kernel(const GrowParams
   StatsState st;
   float thr = -INFINITY;
   int seg = 0;
-  grow_seg_item<E, kFixed>(p, raw, item, c, true, true, st, thr, sh, seg);
+  grow_seg_item<E>(p, raw, item, c, true, true, st, thr, sh, seg);
 }
 
 // Persistent CTAs over contiguous item ranges, the chunks streamed through
 // the bulk-copy ring of the verification kernels (rows of whole 16-byte
 // vectors).  Within a row segment the loop has no CTA barrier.
-template <typename E, bool kFixed = false>
+template <typename E>
 __global__ void __launch_bounds__(kThreads, 2) grow_topk_stream_kernel(const GrowParams p) {
   extern __shared__ __align__(128) uint8_t stage_mem[];
   __shared__ Ring ring;
@@ -509,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, 2) grow_topk_stream_kernel(const Gro
     uint4 raw[kVecPerThread];
     ring_take<E>(ring, stage_mem, slot, par, (j1 - j0) / E::kEPV, p.flags, raw);
     // an aborted CTA ranks -inf: its flag is set
-    grow_seg_item<E, kFixed>(p, raw, it, c, it == i0 || c == 0, c + 1 == C || it + 1 == i1, st, thr,
+    grow_seg_item<E>(p, raw, it, c, it == i0 || c == 0, c + 1 == C || it + 1 == i1, st, thr,
                      sh, seg);
     // the refill after the item's work, when the other warps have usually
     // released the slot (before it, warp 0 waits for them: 0.7 us slower)
