@@ -710,7 +710,7 @@ SPEC_API spec_status_t spec_kv_pages_compact(void* pages, int planes, long long 
  * parent was finished, or the token is eos).  Places without a candidate:
  * -inf, -1, -1, 1.
  * Totals are ordered in float64 from float32 exponentials: they are off by less
- * than 2^-21 (1 + |z_v / T|); within a beam the order is that of the logits,
+ * than 2^-19 (1 + |z_v / T|); within a beam the order is that of the logits,
  * and beams with the same logits and scores tie.
  * Two launches.  Workspace: spec_beam_select_workspace_bytes() bytes.
  */

@@ -678,7 +678,7 @@ bool kv4_shape_ok(long long n_pages, int page_size, int Hkv, int D, int W) {
 struct Attn4Plan {
   bool tiles = false;  // more rows than the kernel for few serves
   AttnPlan t;          // tiles: items and slots as spec_tree_attention's
-  int nt = 1, rows = 0, groups = 0;
+  int nt = 1, rows = 0;
   size_t off_ml = 0, off_part = 0, bytes = 0;
 };
 constexpr int kA4MaxRows = 24;
@@ -693,21 +693,13 @@ Attn4Plan attn4_plan(int B, int N, int Hq, int Hkv, int D) {
     return a;
   }
   a.nt = all <= 8 ? 1 : all <= 16 ? 2 : 3;
-  a.groups = (int)((all + 8 * a.nt - 1) / (8 * a.nt));
-  a.rows = (int)std::min<long long>(all, 8 * a.nt);
-  const size_t items = (size_t)B * Hkv * a.groups;
+  a.rows = (int)all;
+  const size_t items = (size_t)B * Hkv;
   const size_t rows = (size_t)2 * sv::kA4MaxCtas * a.rows;
   a.off_ml = align_up(kDataOffset + items * sizeof(int2));
   a.off_part = align_up(a.off_ml + rows * sizeof(float2));
   a.bytes = align_up(a.off_part + rows * D * sizeof(float));
   return a;
-}
-
-bool attn4_shape_ok(int B, int N, int Hq, int Hkv, int D) {
-  if (B < 0 || N < 1 || N > SPEC_ATTN_MAX_NODES || Hkv < 1 || Hq < Hkv || Hq > 65536 ||
-      Hq % Hkv || (D != 64 && D != 128) || Hq / Hkv > 128)
-    return false;
-  return (long long)B * N * Hq * (D / 4) <= (long long)INT32_MAX * 128;
 }
 
 template <int D, int NT>
@@ -1707,7 +1699,7 @@ spec_status_t spec_kv4_read(const void* pages, int layers, long long n_pages, in
 }
 
 size_t spec_tree_attention_kv4_workspace_bytes(int B, int N, int Hq, int Hkv, int D) {
-  if (!attn4_shape_ok(B, N, Hq, Hkv, D)) return 0;
+  if (!attn_shape_ok(B, N, Hq, Hkv, D, 0)) return 0;
   return attn4_plan(B, N, Hq, Hkv, D).bytes;
 }
 
@@ -1718,7 +1710,7 @@ spec_status_t spec_tree_attention_kv4(const void* q, const void* pages, long lon
                                       const int32_t* kv_exp, int B, int N, int Hq, int Hkv, int D,
                                       float scale, void* out, float* lse, void* workspace,
                                       size_t workspace_bytes, void* stream) {
-  if (!attn4_shape_ok(B, N, Hq, Hkv, D) || !kv4_shape_ok(n_pages, page_size, Hkv, D, W) ||
+  if (!attn_shape_ok(B, N, Hq, Hkv, D, 0) || !kv4_shape_ok(n_pages, page_size, Hkv, D, W) ||
       (long long)W * page_size > INT32_MAX - 256 || !(scale > 0.0f) ||
       !(scale < 1.7014118e38f))  // 2^127: scale * log2(e) stays finite
     return SPEC_ERR_INVALID_ARG;
@@ -1822,7 +1814,6 @@ spec_status_t spec_tree_attention_kv4(const void* q, const void* pages, long lon
   prm.Wm = (N + 31) / 32;
   prm.lg = log2_of(page_size);
   prm.rows = plan.rows;
-  prm.groups = plan.groups;
   return D == 128 ? run_attn4<128>(prm, plan.nt, sms, stream)
                   : run_attn4<64>(prm, plan.nt, sms, stream);
 }

@@ -35,8 +35,7 @@ struct Attn4Params {
   long long n_pages;
   float scale_log2;         // scale * log2(e)
   int B, N, Hq, Hkv, G, W, Wm, lg;
-  int rows;                 // rows of an item (at most 8 NT)
-  int groups;               // items per key-value head and sequence
+  int rows;                 // N G, at most 8 NT: rows of an item (a sequence's key-value head)
   int nctas;
 };
 
@@ -54,7 +53,7 @@ __device__ __forceinline__ int attn4_units(const Attn4Params& p, int base) {
 
 // A CTA's run of units is cut into segments, one per item it meets.
 struct Attn4Seg {
-  int b, h, row0, nrows;  // sequence, key-value head, rows of the sequence's N G
+  int b, h;               // sequence, key-value head
   int t0, n, len;         // units, committed positions
   int slot, whole;        // partial's slot; whole: all units of the item
 };
@@ -63,7 +62,7 @@ struct Attn4Walk {
   int b;
   __device__ __forceinline__ bool next(const Attn4Params& p, Attn4Seg* s, bool writes) {
     if (pos >= hi) return false;
-    const int per = p.Hkv * p.groups;
+    const int per = p.Hkv;
     int base = p.base_len[b];
     int units = attn4_units(p, base);
     while (pos >= bstart + (long long)per * units) {
@@ -75,10 +74,7 @@ struct Attn4Walk {
     s->t0 = (int)(pos - bstart - (long long)it * units);
     s->n = (int)min((long long)(units - s->t0), hi - pos);
     s->b = b;
-    s->h = it / p.groups;
-    const int rg = it - s->h * p.groups;
-    s->row0 = rg * p.rows;
-    s->nrows = min(p.rows, p.N * p.G - s->row0);
+    s->h = it;
     s->len = base - 1;
     s->slot = 2 * blockIdx.x + (s->t0 == 0);
     s->whole = s->n == units;
@@ -184,7 +180,7 @@ __global__ void __launch_bounds__(kA4Threads, a4_per_sm<NT>())
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
   // the run [lo, hi) of this CTA and the sequence it starts in
-  const int per = p.Hkv * p.groups;
+  const int per = p.Hkv;
   int mine = (int)threadIdx.x < p.B ? attn4_units(p, p.base_len[threadIdx.x]) : 0;
   long long sum = mine;
   for (int b = threadIdx.x + kA4Threads; b < p.B; b += kA4Threads)
@@ -305,14 +301,13 @@ __global__ void __launch_bounds__(kA4Threads, a4_per_sm<NT>())
     // queries as fp16, each row times a power of two that brings its largest
     // element to [2^14, 2^15)
     for (int r = warp; r < NT * 8; r += kA4Warps) {
-      const int rr = seg.row0 + r;
-      const bool in = r < seg.nrows;
-      const int v = rr / p.G;
+      const bool in = r < p.rows;
+      const int v = r / p.G;
       uint32_t x[D / 64];
 #pragma unroll
       for (int j = 0; j < D / 64; ++j)
         x[j] = in ? *reinterpret_cast<const uint32_t*>(
-                        p.q + (((size_t)seg.b * p.N + v) * p.Hq + seg.h * p.G + (rr - v * p.G)) * D +
+                        p.q + (((size_t)seg.b * p.N + v) * p.Hq + seg.h * p.G + (r - v * p.G)) * D +
                         j * 64 + lane * 2)
                   : 0u;
       uint32_t a = 0;
@@ -346,7 +341,7 @@ __global__ void __launch_bounds__(kA4Threads, a4_per_sm<NT>())
         fac[i][c] = s_fac[8 * i + 2 * t + c];
         m[i][c] = -1e30f;
         l[i][c] = 0.0f;
-        vis[i][c] = (seg.row0 + min(8 * i + 2 * t + c, seg.nrows - 1)) / p.G;
+        vis[i][c] = min(8 * i + 2 * t + c, p.rows - 1) / p.G;
       }
     }
     // products of 16 entries a time (rows g, g + 8), hidden ones -inf, to weights;
@@ -405,8 +400,7 @@ __global__ void __launch_bounds__(kA4Threads, a4_per_sm<NT>())
       {
         // ---- 16 nodes ----
         const int u0 = u * 128 + warp * 16;
-        const int last = (seg.row0 + seg.nrows - 1) / p.G;  // the item's last node
-        if (u0 < p.N && (p.mask || u0 <= last)) {
+        if (u0 < p.N) {
           const size_t node0 = (size_t)seg.b * p.N;
           const size_t stride = (size_t)p.Hkv * D;
           float s[1][NT][4];
@@ -679,11 +673,11 @@ __global__ void __launch_bounds__(kA4Threads, a4_per_sm<NT>())
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           const int r = 8 * i + 2 * t + c;
-          if (r >= seg.nrows) continue;
+          if (r >= p.rows) continue;
           if (seg.whole) {
             const float norm = attn_norm(l[i][c]) * vscale;
-            const int rr = seg.row0 + r, v = rr / p.G;
-            const size_t orow = ((size_t)seg.b * p.N + v) * p.Hq + seg.h * p.G + (rr - v * p.G);
+            const int v = r / p.G;
+            const size_t orow = ((size_t)seg.b * p.N + v) * p.Hq + seg.h * p.G + (r - v * p.G);
             uint32_t x[kCv / 2];
 #pragma unroll
             for (int j = 0; j < kSteps; ++j) x[j] = pack_bf16(o[i][j][c] * norm, o[i][j][c + 2] * norm);
@@ -733,8 +727,8 @@ __global__ void __launch_bounds__(256) kv4_attn_finish_kernel(const Attn4Params 
   float m = -1e30f, l = 0.0f;
   float4 acc = make_float4(0, 0, 0, 0);
   if (attn4_len(p, p.base_len[b]) >= 0) {
-    const int rg = rr / p.rows, r = rr - rg * p.rows;
-    int2 span = p.span[bh * p.groups + rg];
+    const int r = rr;
+    int2 span = p.span[bh];
     if (span.x == span.y) return;  // written by its only CTA
     // slots of the workspace, whatever an overlapping call made of the span
     span.x = max(span.x, 0);
