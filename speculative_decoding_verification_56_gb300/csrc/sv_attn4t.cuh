@@ -60,6 +60,12 @@ __device__ __forceinline__ void atq_put(int pair, int n, int i, int* t, int* is_
   }
 }
 
+// True in one thread of the (converged) warp, the same each time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(one));
+  return one != 0;
+}
 // Whether a phase is complete, without waiting.
 __device__ __forceinline__ bool mbar_test(uint64_t* bar, unsigned parity) {
   uint32_t done;
@@ -163,11 +169,13 @@ __global__ void __launch_bounds__(kAtqThreads, 1)
       mbar_init(&seg_empty[s], 14);  // copies, MMAs, eight softmax warps, four that unpack
     }
     mbar_init(&drain, 1);
+    for (int s = 0; s < kAtqTurns; ++s) s_hole[s] = 0;
     s_abort = 0;
     s_b = 0;
     s_bstart = 0;
     mbar_init_fence();
   }
+  if (threadIdx.x < kAtqTurns * 8) (&s_bad[0][0][0])[threadIdx.x] = 0;
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_addr(&tmem_holder)),
@@ -328,119 +336,136 @@ __global__ void __launch_bounds__(kAtqThreads, 1)
       mbar_wait_bounded(&raw_full[j % kRaw], (unsigned)((j / kRaw) & 1));
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
-      // ---------------- MMAs ----------------
-      const uint32_t id_qk = umma_idesc_f16_f32(kAtRows, kAtKeys);
-      const uint32_t id_pv = umma_idesc_f16_f32(kAtRows, D) | (1u << 16);  // V: MN-major
-      const uint64_t qdesc = umma_desc_sw128(smem_addr(smem));
-      const uint64_t kdesc = umma_desc_sw128(smem_addr(ring));
-      const uint64_t vdesc = umma_desc_mn_sw128(smem_addr(ring));
-      int stage = 0;
-      unsigned phase = 0, nq = 0, np = 0, np1 = 0;
-      bool ok = true;
-      auto wait = [&](uint64_t* bar, unsigned parity) {
-        if (!atq_wait(p, bar, parity & 1, abort)) {
-          ok = false;
-          fail();
-        }
-        tmem_fence_after();
-        return ok;
-      };
-      auto advance = [&]() {
-        if (++stage == S) {
-          stage = 0;
-          phase ^= 1u;
-        }
-      };
-      // scores of half w from the K tile in stage st, query tile qt
-      auto scores = [&](int w, int qt, int st) {
-        const uint64_t a = qdesc + (uint64_t)(qt * kTile >> 4);
-        const uint64_t b = kdesc + (uint64_t)(st * kTile >> 4);
+    // ---------------- MMAs ----------------
+    // The whole warp walks along and one elected thread issues, so that what the
+    // products are issued with stands in uniform registers (one thread on its own
+    // took 3900 clocks a tile to issue 2048 clocks of products).
+    const uint32_t id_qk = umma_idesc_f16_f32(kAtRows, kAtKeys);
+    const uint32_t id_pv = umma_idesc_f16_f32(kAtRows, D) | (1u << 16);  // V: MN-major
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint64_t qdesc = umma_desc_sw128(smem_addr(smem));
+    const uint64_t kdesc = umma_desc_sw128(smem_addr(ring));
+    const uint64_t vdesc = umma_desc_mn_sw128(smem_addr(ring));
+    int stage = 0;
+    unsigned phase = 0, nq = 0, np = 0, np1 = 0;
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, unsigned parity) {
+      if (!atq_wait_warp(p, bar, parity & 1, abort)) {
+        ok = false;
+        if (lane == 0) fail();
+      }
+      tmem_fence_after();
+      return ok;
+    };
+    auto advance = [&]() {
+      if (++stage == S) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    };
+    auto commit = [&](uint64_t* bar) {
+      if (elect_one()) umma_commit(bar);
+      __syncwarp();
+    };
+    // scores of half w from the K tile in stage st, query tile qt
+    auto scores = [&](int w, int qt, int st) {
+      const uint64_t a = qdesc + (uint64_t)(qt * kTile >> 4);
+      const uint64_t b = kdesc + (uint64_t)(st * kTile >> 4);
+      const uint32_t d = tm + w * kAtKeys;
+      if (elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint64_t o = (uint64_t)((kk >> 2) * (kAtKeys * 128 >> 4) + (kk & 3) * 2);
-          umma_ss(tmem + w * kAtKeys, a + o, b + o, id_qk, kk ? 1u : 0u);
+          umma_ss(d, a + o, b + o, id_qk, kk ? 1u : 0u);
         }
         umma_commit(&s_full[w]);
         mbar_arrive(&s_full[w]);
-      };
-      // output of half w from the V tile in stage st
-      auto output = [&](int w, int st, bool first) {
-        const uint64_t b = vdesc + (uint64_t)(st * kTile >> 4);
+      }
+      __syncwarp();
+    };
+    // output of half w from the V tile in stage st
+    auto output = [&](int w, int st, bool first) {
+      const uint64_t b = vdesc + (uint64_t)(st * kTile >> 4);
+      const uint32_t d = tm + 2 * kAtKeys + w * D, a = tm + w * kAtKeys;
+      if (elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < kAtKeys / 16; ++kk)
-          umma_ts(tmem + 2 * kAtKeys + w * D, tmem + w * kAtKeys + kk * 8,
-                  b + (uint64_t)(kk * (2048 >> 4)), id_pv, (!first || kk) ? 1u : 0u);
-      };
-      while (ok) {
-        const unsigned at = nq % kAtSegs;
-        if (!wait(&seg_full[at], nq / kAtSegs)) break;
-        const int n = s_seg[at].n, pair = s_seg[at].pair;
-        mbar_arrive(&seg_empty[at]);
-        if (n == 0 || !wait(&q_full, nq++)) break;
-        if (pair) {
-          // ring: K0, V0, K1, V1, ...; each tile is waited for as late as its use
-          // allows, and where the tensor cores have work
-          if (!wait(&full[stage], phase)) break;
+          umma_ts(d, a + kk * 8, b + (uint64_t)(kk * (2048 >> 4)), id_pv, (!first || kk) ? 1u : 0u);
+      }
+      __syncwarp();
+    };
+    while (ok) {
+      const unsigned at = nq % kAtSegs;
+      if (!wait(&seg_full[at], nq / kAtSegs)) break;
+      const int n = __shfl_sync(0xffffffffu, s_seg[at].n, 0);
+      const int pair = __shfl_sync(0xffffffffu, s_seg[at].pair, 0);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&seg_empty[at]);
+      if (n == 0 || !wait(&q_full, nq++)) break;
+      if (pair) {
+        // ring: K0, V0, K1, V1, ...; each tile is waited for as late as its use
+        // allows, and where the tensor cores have work
+        if (!wait(&full[stage], phase)) break;
+        scores(0, 0, stage);
+        scores(1, 1, stage);
+        if (n == 1) commit(&q_empty);
+        advance();
+        int vst = stage;
+        if (!wait(&full[stage], phase)) break;
+        advance();
 #pragma unroll 1
-          for (int w = 0; w < 2; ++w) scores(w, w, stage);
-          if (n == 1) umma_commit(&q_empty);
-          advance();
-          int vst = stage;
-          if (!wait(&full[stage], phase)) break;
-          advance();
-#pragma unroll 1
-          for (int t = 0; ok && t < n; ++t, ++np) {
-            const bool more = t + 1 < n;
-            const int v = vst, k = stage;
-            if (more && !wait(&full[stage], phase)) break;
-#pragma unroll 1
-            for (int w = 0; w < 2; ++w) {
-              if (!wait(&p_full[w], np)) break;
-              output(w, v, t == 0);
-              if (more)
-                scores(w, w, k);
-              else
-                umma_commit(&o_full[w]);
-              if (more && w == 0) {
-                advance();
-                vst = stage;
-                if (!wait(&full[stage], phase)) break;
-                advance();
-              }
-            }
-            if (t + 2 == n) umma_commit(&q_empty);
-          }
-          np1 = np;
-        } else {
-          for (int t = 0; t < min(2, n); ++t) {
-            if (!wait(&full[stage], phase)) break;
-            scores(t, 0, stage);
-            if (t + 1 == n) umma_commit(&q_empty);
+        for (int t = 0; t < n; ++t, ++np) {
+          const bool more = t + 1 < n;
+          const int v = vst, k = stage;
+          if (more && !wait(&full[stage], phase)) break;
+          if (!wait(&p_full[0], np)) break;
+          output(0, v, t == 0);
+          if (more) {
+            scores(0, 0, k);
             advance();
-          }
-#pragma unroll 1
-          for (int t = 0; ok && t < n; ++t) {
-            const int w = t & 1, vst = stage;
+            vst = stage;
             if (!wait(&full[stage], phase)) break;
             advance();
-            if (!wait(&p_full[w], w ? np1++ : np++)) break;
-            output(w, vst, t < 2);
-            if (t + 2 < n) {
-              if (!wait(&full[stage], phase)) break;
-              scores(w, 0, stage);
-              if (t + 3 == n) umma_commit(&q_empty);
-              advance();
-            } else {
-              umma_commit(&o_full[w]);
-            }
+          } else {
+            commit(&o_full[0]);
+          }
+          if (!wait(&p_full[1], np)) break;
+          output(1, v, t == 0);
+          if (more) {
+            scores(1, 1, k);
+            if (t + 2 == n) commit(&q_empty);
+          } else {
+            commit(&o_full[1]);
+          }
+        }
+      } else {
+        for (int t = 0; t < min(2, n); ++t) {
+          if (!wait(&full[stage], phase)) break;
+          scores(t, 0, stage);
+          if (t + 1 == n) commit(&q_empty);
+          advance();
+        }
+#pragma unroll 1
+        for (int t = 0; ok && t < n; ++t) {
+          const int w = t & 1, vst = stage;
+          if (!wait(&full[stage], phase)) break;
+          advance();
+          if (!wait(&p_full[w], w ? np1++ : np++)) break;
+          output(w, vst, t < 2);
+          if (t + 2 < n) {
+            if (!wait(&full[stage], phase)) break;
+            scores(w, 0, stage);
+            if (t + 3 == n) commit(&q_empty);
+            advance();
+          } else {
+            commit(&o_full[w]);
           }
         }
       }
-      // every MMA has completed before tensor memory is freed
-      umma_commit(&drain);
-      mbar_wait_bounded(&drain, 0);
     }
+    // every MMA has completed before tensor memory is freed
+    commit(&drain);
+    mbar_wait_bounded(&drain, 0);
     __syncwarp();
   }
   } else if (warp >= 12) {
@@ -451,8 +476,9 @@ __global__ void __launch_bounds__(kAtqThreads, 1)
     const int r = (int)threadIdx.x - 384;
     const int kexp = kv4_exp(p.exps, 0);
     const float kinv = pow2_small(-kexp), vinv = pow2_small(-kv4_exp(p.exps, 1));
-    int rst = 0;
-    unsigned rphase = 0, use = 0, nput = 0, kput = 0, vput = 0;  // ring uses, node tiles, K and V tiles so far
+    int rst = 0, stage = 0;
+    unsigned rphase = 0, phase = 0, nput = 0, kput = 0, vput = 0;  // node tiles, K and V tiles so far
+    unsigned noted = 0;           // turns whose words in s_bad and s_hole are not 0
     unsigned nq = 0, nasked = 0;  // thread 384: queries and node tiles asked for
     bool ok = true;
     // the tiles' rows of 128 bytes: 16-byte chunk c of row r stands at c ^ (r & 7)
@@ -531,16 +557,20 @@ __global__ void __launch_bounds__(kAtqThreads, 1)
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_full);
-      int asked = 0;  // puts of the segment whose nodes are asked for
+      // the first put with nodes: the K tile of the first such tile
+      const int t_nodes = max(0, seg.plen / kAtKeys - seg.t0);
+      int asked = t_nodes >= seg.n ? 2 * seg.n : seg.pair ? 2 * t_nodes : max(t_nodes, 2 * t_nodes - 1);
 #pragma unroll 1
-      for (int i = 0; i < 2 * seg.n; ++i, ++use) {
-        if (threadIdx.x == 384) {  // this put's nodes, and the next one's if its place is free
+      for (int i = 0; i < 2 * seg.n; ++i) {
+        if (i + 1 >= asked && threadIdx.x == 384) {  // this put's nodes, and the next one's if its place is free
           for (; asked <= i + 1 && asked < 2 * seg.n; ++asked) {
             int t, is_v;
             atq_put(seg.pair, seg.n, asked, &t, &is_v);
             const int node0 = (seg.t0 + t) * kAtKeys - seg.plen;
             if (node0 + kAtKeys <= 0) continue;
-            const unsigned u = use + (asked - i), st = u % S, par = ((u / S) & 1) ^ 1u;
+            const bool wraps = asked > i && stage + 1 == S;
+            const int st = wraps ? 0 : stage + (asked - i);
+            const unsigned par = wraps ? phase : phase ^ 1u;
             if (asked > i && !mbar_test(&empty[st], par)) break;
             if (!atq_wait(p, &empty[st], par, abort)) {
               fail();
@@ -557,12 +587,11 @@ __global__ void __launch_bounds__(kAtqThreads, 1)
         int t, is_v;
         atq_put(seg.pair, seg.n, i, &t, &is_v);
         const int key0 = (seg.t0 + t) * kAtKeys, key = key0 + r;
-        const int stage = use % S;
         uint8_t* tile = ring + stage * kTile;
         // a tile with nodes: they are in it already (and 0 behind the last)
         const bool nodes = key0 + kAtKeys > seg.plen, paged = key0 < seg.plen;
         if (!(nodes ? atq_wait_warp(p, &node_full[nput % kAtqTurns], (nput / kAtqTurns) & 1, abort)
-                    : atq_wait_warp(p, &empty[stage], ((use / S) & 1) ^ 1u, abort))) {
+                    : atq_wait_warp(p, &empty[stage], phase ^ 1u, abort))) {
           ok = false;
           break;
         }
@@ -608,6 +637,8 @@ __global__ void __launch_bounds__(kAtqThreads, 1)
             uint32_t two[32 / kRows];
 #pragma unroll
             for (int j = 0; j < 32 / kRows; ++j) load(j, x[j], two[j]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&raw_empty[rst]);  // (all that is needed of it is in registers)
 #pragma unroll
             for (int j = 0; j < 32 / kRows; ++j) unpack(j, x[j], two[j]);
           } else if (paged) {
@@ -641,17 +672,25 @@ __global__ void __launch_bounds__(kAtqThreads, 1)
 #pragma unroll 1
             for (int c = 0; c < D / 8; ++c) *chunk(tile, c) = make_uint4(0, 0, 0, 0);
         }
-        const unsigned any = __ballot_sync(0xffffffffu, bad);
         const unsigned turn = (is_v ? vput++ : kput++) % kAtqTurns;
-        if (lane == 0) {
-          s_bad[turn][is_v][warp - 12] = any;
-          if (warp == 12 && !is_v) s_hole[turn] = hole;
+        const unsigned bit = 1u << (2 * turn + is_v);
+        if (nodes || hole || (noted & bit)) {  // (0 where nothing was noted before)
+          const unsigned any = __ballot_sync(0xffffffffu, bad);
+          if (lane == 0) {
+            s_bad[turn][is_v][warp - 12] = any;
+            if (warp == 12 && !is_v) s_hole[turn] = hole;
+          }
+          noted = any || hole ? noted | bit : noted & ~bit;
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(&full[stage]);
-          if (paged) mbar_arrive(&raw_empty[rst]);
+          if (paged && (nodes || hole)) mbar_arrive(&raw_empty[rst]);
+        }
+        if (++stage == S) {
+          stage = 0;
+          phase ^= 1u;
         }
         if (paged && ++rst == kRaw) {
           rst = 0;
