@@ -16,8 +16,8 @@
 
 namespace sv {
 
-constexpr int kAtqThreads = 512;  // copies, MMAs, segments, an idle warp; 2 x 4 softmax warps;
-                                  // 4 that unpack
+constexpr int kAtqThreads = 640;  // copies, MMAs, segments, an idle warp; 2 x 4 softmax warps;
+                                  // 2 x 4 that unpack
 constexpr int kAtqTurns = 16;
 constexpr float kAtqLazy = 32768.0f;  // largest sum of a row's weights in 32 entries before its
                                       // reference is renewed: 2^8 times 2^kA4Off, within fp16
@@ -66,18 +66,6 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(one));
   return one != 0;
 }
-// Whether a phase is complete, without waiting.
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, unsigned parity) {
-  uint32_t done;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-      " selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(done)
-      : "r"(smem_addr(bar)), "r"(parity)
-      : "memory");
-  return done != 0;
-}
-
 // Waits between the roles: a number of tries that sleep in the instruction until
 // the phase completes, so that a wait is a few instructions (what the roles
 // share here is the instruction caches, see below).
@@ -121,7 +109,7 @@ __global__ void __launch_bounds__(kAtqThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem[];
   static_assert(atq_tiles<D>() - 1 <= kAtMaxStages, "ring barriers");
   __shared__ uint64_t full[kAtMaxStages], empty[kAtMaxStages];
-  __shared__ uint64_t raw_full[kRaw], raw_empty[kRaw], node_full[kAtqTurns], q_raw;
+  __shared__ uint64_t raw_full[kRaw], raw_empty[kRaw], node_full[2][kAtqTurns], q_raw;
   __shared__ uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], drain;
   __shared__ uint64_t seg_full[kAtSegs], seg_empty[kAtSegs], pair_bar;
   __shared__ AttnSeg s_seg[kAtSegs];
@@ -154,9 +142,9 @@ __global__ void __launch_bounds__(kAtqThreads, 1)
       mbar_init(&raw_full[s], 1);
       mbar_init(&raw_empty[s], 4);
     }
-    for (int s = 0; s < kAtqTurns; ++s) mbar_init(&node_full[s], 1);
+    for (int s = 0; s < 2 * kAtqTurns; ++s) mbar_init(&node_full[0][s], 1);
     mbar_init(&q_raw, 1);
-    mbar_init(&q_full, 4);
+    mbar_init(&q_full, 8);
     mbar_init(&q_empty, 1);
     for (int w = 0; w < 2; ++w) {
       mbar_init(&s_full[w], 2);  // the products, and the issuing thread for what it has waited for
@@ -166,7 +154,7 @@ __global__ void __launch_bounds__(kAtqThreads, 1)
     mbar_init(&pair_bar, 8);
     for (int s = 0; s < kAtSegs; ++s) {
       mbar_init(&seg_full[s], 1);
-      mbar_init(&seg_empty[s], 14);  // copies, MMAs, eight softmax warps, four that unpack
+      mbar_init(&seg_empty[s], 18);  // copies, MMAs, eight softmax warps, eight that unpack
     }
     mbar_init(&drain, 1);
     for (int s = 0; s < kAtqTurns; ++s) s_hole[s] = 0;
@@ -244,9 +232,9 @@ __global__ void __launch_bounds__(kAtqThreads, 1)
     set_flag(p.flags, kFlagTimeout);
   };
 
-  // registers: 128 a thread at launch, 512 over the four warpgroups
+  // registers: 96 a thread at launch, 480 over the five warpgroups
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
   if (warp == 2) {
     if (lane == 0) {
       // ---------------- segments ----------------
@@ -469,32 +457,39 @@ __global__ void __launch_bounds__(kAtqThreads, 1)
     __syncwarp();
   }
   } else if (warp >= 12) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     // ---------------- unpacking ----------------
-    // thread r: query row r of each half, and node r of each tile.  (One copy of
-    // the code for keys and values: five roles share the instruction caches.)
-    const int r = (int)threadIdx.x - 384;
+    // thread r of a group of four warps: query row r of its half, and node r of its
+    // tiles.  (One copy of the code for keys and values: the roles share the
+    // instruction caches.)
+    const int r = (int)threadIdx.x & 127;
     const int kexp = kv4_exp(p.exps, 0);
     const float kinv = pow2_small(-kexp), vinv = pow2_small(-kv4_exp(p.exps, 1));
     int rst = 0, stage = 0;
-    unsigned rphase = 0, phase = 0, nput = 0, kput = 0, vput = 0;  // node tiles, K and V tiles so far
+    unsigned rphase = 0, phase = 0, nput = 0, tput = 0;  // node tiles and tiles so far
     unsigned noted = 0;           // turns whose words in s_bad and s_hole are not 0
-    unsigned nq = 0, nasked = 0;  // thread 384: queries and node tiles asked for
+    unsigned nq = 0, nasked = 0;  // (one thread's:) queries and node tiles asked for
     bool ok = true;
     // the tiles' rows of 128 bytes: 16-byte chunk c of row r stands at c ^ (r & 7)
-    auto chunk = [&](uint8_t* tile, int c) {  // of D / 8
+    auto chunk = [&](uint8_t* tile, int r, int c) {  // of D / 8
       return reinterpret_cast<uint4*>(tile + (c >> 3) * (kAtRows * 128) + r * 128 +
                                       (((c & 7) ^ (r & 7)) << 4));
     };
-    // Unpacking: lane 4 s + c (D = 64: 2 s + c) takes channels 32 c .. of entries s,
-    // s + kRows, ..: 16 bytes of codes, four chunks of fp16, which start at chunk
-    // 4 (c & 1) of column block c >> 1 and lie at places xor s & 7.  Lanes of the
-    // second column block store their chunks in the order 2 3 0 1.
+    // Warps 12 to 15 unpack K tiles, 16 to 19 V tiles, so that from a free place to
+    // a full one it is short (four warps for both: 16 trees of 60 nodes
+    // 91 us, now 87).
+    // A warp takes 32 entries: lane 4 s + c (D = 64: 2 s + c) takes
+    // channels 32 c .. of entries s, s + kRows, ..: 16 bytes of codes, four chunks of
+    // fp16, which start at chunk 4 (c & 1) of column block c >> 1 and lie at places
+    // xor s & 7.  Lanes of the second column block store their chunks in the order
+    // 2 3 0 1.
     constexpr int kRows = 32 * 32 / D;
+    const int is_v = (warp - 12) >> 2, row0 = (warp & 3) * 32;
     const int ucc = lane % (D / 32), usub = lane / (D / 32);
     const bool uswap = ucc >= 2;
-    const int udst = (ucc >> 1) * (kAtRows * 128) + ((warp - 12) * 32 + usub) * 128;
+    const int udst = (ucc >> 1) * (kAtRows * 128) + (row0 + usub) * 128;
     const int ulow = ((4 * (ucc & 1) + (uswap ? 2 : 0)) ^ (usub & 7)) * 16;
+    const bool asks = (threadIdx.x & 127) == 0;
     for (unsigned k = 0; ok; ++k) {
       const unsigned at = k % kAtSegs;
       if (!atq_wait_warp(p, &seg_full[at], (k / kAtSegs) & 1, abort)) {
@@ -526,14 +521,13 @@ __global__ void __launch_bounds__(kAtqThreads, 1)
         ok = false;
         break;
       }
-#pragma unroll 1
-      for (int w = 0; w <= seg.pair; ++w) {
-        if (r >= p.tok * p.G) continue;  // (rows of no node: whatever the copy brought)
+      if (is_v <= seg.pair && r < p.tok * p.G) {  // (rows of no node: whatever the copy brought)
+        const int w = is_v;  // half
         uint8_t* tile = smem + w * kTile;
         uint32_t a = 0;
 #pragma unroll 4
         for (int c = 0; c < D / 8; ++c) {
-          const uint4 x = lds128(chunk(tile, c));
+          const uint4 x = lds128(chunk(tile, r, c));
           const uint32_t y[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) a = max(a, max(y[e] & 0x7FFFu, (y[e] >> 16) & 0x7FFFu));
@@ -544,7 +538,7 @@ __global__ void __launch_bounds__(kAtqThreads, 1)
         const float f0 = pow2_small(e2 / 2), f1 = pow2_small(e2 - e2 / 2);  // (2^e2 may overflow)
 #pragma unroll 2
         for (int c = 0; c < D / 8; ++c) {
-          uint4* at_c = chunk(tile, c);
+          uint4* at_c = chunk(tile, r, c);
           const uint4 x = lds128(at_c);
           const uint32_t y[4] = {x.x, x.y, x.z, x.w};
           uint32_t z[4];
@@ -557,61 +551,50 @@ __global__ void __launch_bounds__(kAtqThreads, 1)
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_full);
-      // the first put with nodes: the K tile of the first such tile
-      const int t_nodes = max(0, seg.plen / kAtKeys - seg.t0);
-      int asked = t_nodes >= seg.n ? 2 * seg.n : seg.pair ? 2 * t_nodes : max(t_nodes, 2 * t_nodes - 1);
+      const int t_nodes = max(0, seg.plen / kAtKeys - seg.t0);  // the first tile with nodes
+      int asked = t_nodes;  // this group's tiles whose nodes are asked for, or that have none
+      int t = 0;
 #pragma unroll 1
       for (int i = 0; i < 2 * seg.n; ++i) {
-        if (i + 1 >= asked && threadIdx.x == 384) {  // this put's nodes, and the next one's if its place is free
-          for (; asked <= i + 1 && asked < 2 * seg.n; ++asked) {
-            int t, is_v;
-            atq_put(seg.pair, seg.n, asked, &t, &is_v);
-            const int node0 = (seg.t0 + t) * kAtKeys - seg.plen;
-            if (node0 + kAtKeys <= 0) continue;
-            const bool wraps = asked > i && stage + 1 == S;
-            const int st = wraps ? 0 : stage + (asked - i);
-            const unsigned par = wraps ? phase : phase ^ 1u;
-            if (asked > i && !mbar_test(&empty[st], par)) break;
-            if (!atq_wait(p, &empty[st], par, abort)) {
-              fail();
-              break;
-            }
-            uint64_t* bar = &node_full[nasked++ % kAtqTurns];
-            mbar_expect_tx(bar, kTile);
-            for (int c = 0; c < kSub; ++c)
-              tma_load_4d(ring + st * kTile + c * (kAtKeys * 128), is_v ? &p.map_v : &p.map_k, c * 64,
-                          seg.h, node0, seg.b, bar);
-          }
-        }
-        __syncwarp();
-        int t, is_v;
-        atq_put(seg.pair, seg.n, i, &t, &is_v);
-        const int key0 = (seg.t0 + t) * kAtKeys, key = key0 + r;
-        uint8_t* tile = ring + stage * kTile;
+        int ti, vi;
+        atq_put(seg.pair, seg.n, i, &ti, &vi);
+        const int key0 = (seg.t0 + ti) * kAtKeys;
         // a tile with nodes: they are in it already (and 0 behind the last)
-        const bool nodes = key0 + kAtKeys > seg.plen, paged = key0 < seg.plen;
-        if (!(nodes ? atq_wait_warp(p, &node_full[nput % kAtqTurns], (nput / kAtqTurns) & 1, abort)
-                    : atq_wait_warp(p, &empty[stage], phase ^ 1u, abort))) {
-          ok = false;
-          break;
-        }
-        nput += nodes;
-        unsigned hole = 0;
-        if (paged) {
-          if (!atq_wait_warp(p, &raw_full[rst], rphase, abort)) {
+        const bool nodes = ti >= t_nodes, paged = key0 < seg.plen;
+        if (vi == is_v) {
+          t = ti;
+          uint8_t* tile = ring + stage * kTile;
+          if (nodes && asks && asked <= t) {
+            if (atq_wait(p, &empty[stage], phase ^ 1u, abort)) {
+              uint64_t* bar = &node_full[is_v][nasked++ % kAtqTurns];
+              mbar_expect_tx(bar, kTile);
+              for (int c = 0; c < kSub; ++c)
+                tma_load_4d(tile + c * (kAtKeys * 128), is_v ? &p.map_v : &p.map_k, c * 64, seg.h,
+                            key0 - seg.plen, seg.b, bar);
+            } else {
+              fail();
+            }
+            asked = t + 1;
+          }
+          __syncwarp();
+          if (!(nodes ? atq_wait_warp(p, &node_full[is_v][nput % kAtqTurns], (nput / kAtqTurns) & 1, abort)
+                      : atq_wait_warp(p, &empty[stage], phase ^ 1u, abort))) {
             ok = false;
             break;
           }
-          hole = s_nopage[rst];
-        }
-        // the warp's 32 entries, kRows at a time: every load is of whole groups and
-        // every store meets other banks
-        {
-          const uint8_t* src = raw + rst * kHalf + (warp - 12) * (kHalf / 4);
+          nput += nodes;
+          unsigned hole = 0;
+          if (paged) {
+            if (!atq_wait_warp(p, &raw_full[rst], rphase, abort)) {
+              ok = false;
+              break;
+            }
+            hole = s_nopage[rst];
+          }
+          const uint8_t* src = raw + rst * kHalf + (row0 >> 4) * (kHalf / 8);
           const uint8_t* codes = src + usub * (D / 2) + ucc * 16;
           const uint8_t* scales = src + 8 * D + usub * (D / 16) + ucc * 2;
           uint8_t* dst = tile + udst;
-          const int left = seg.plen - key0 - (warp - 12) * 32 - usub;  // positions from this one on
           auto load = [&](int j, uint4& x, uint32_t& two) {
             const int group = j * kRows / 16, place = j * kRows % 16;
             x = lds128(codes + group * (kHalf / 8) + place * (D / 2));
@@ -632,61 +615,61 @@ __global__ void __launch_bounds__(kAtqThreads, 1)
                   make_uint4(hmul2(h[0], s), hmul2(h[1], s), hmul2(h[2], s), hmul2(h[3], s));
             }
           };
+          constexpr int kSteps = 32 / kRows;
           if (!nodes && !hole) {  // all of them: loads first, and no branches between
-            uint4 x[32 / kRows];
-            uint32_t two[32 / kRows];
+            uint4 x[kSteps];
+            uint32_t two[kSteps];
 #pragma unroll
-            for (int j = 0; j < 32 / kRows; ++j) load(j, x[j], two[j]);
+            for (int j = 0; j < kSteps; ++j) load(j, x[j], two[j]);
             __syncwarp();
             if (lane == 0) mbar_arrive(&raw_empty[rst]);  // (all that is needed of it is in registers)
 #pragma unroll
-            for (int j = 0; j < 32 / kRows; ++j) unpack(j, x[j], two[j]);
-          } else if (paged) {
+            for (int j = 0; j < kSteps; ++j) unpack(j, x[j], two[j]);
+          } else {
+            const int left = seg.plen - key0 - row0 - usub;  // positions from this lane's first on
+            if (paged)
 #pragma unroll 1
-            for (int j = 0; j < 32 / kRows; ++j) {
-              if (j * kRows >= left || ((hole >> ((warp - 12) * 2 + j * kRows / 16)) & 1)) continue;
-              uint4 x;
-              uint32_t two;
-              load(j, x, two);
-              unpack(j, x, two);
-            }
+              for (int j = 0; j < kSteps; ++j) {
+                if (j * kRows >= left || ((hole >> ((row0 + j * kRows) >> 4)) & 1)) continue;
+                uint4 x;
+                uint32_t two;
+                load(j, x, two);
+                unpack(j, x, two);
+              }
           }
-        }
-        const bool mine = key < seg.plen;
-        bool bad = false;
-        if (nodes || hole) {
-          // nodes, bf16 to fp16 in place; 0 if an element is not finite, and where
-          // there is no page
-          bool zero = mine && ((hole >> (r >> 4)) & 1);
-          if (!mine && key < seg.kvlen) {
-            const float f = is_v ? vinv : kinv;
+          const unsigned turn = tput++ % kAtqTurns;
+          if (nodes || hole || ((noted >> turn) & 1)) {
+            // nodes, bf16 to fp16 in place; 0 if an element is not finite, and where
+            // there is no page
+            const int row = row0 + lane, key = key0 + row;
+            const bool mine = key < seg.plen;
+            bool bad = false;
+            if (!mine && key < seg.kvlen) {
+              const float f = is_v ? vinv : kinv;
 #pragma unroll 2
-            for (int c = 0; c < D / 8; ++c) {
-              uint4* at_c = chunk(tile, c);
-              const uint4 x = lds128(at_c);
-              *at_c = make_uint4(node_half2(x.x, f, bad), node_half2(x.y, f, bad),
-                                 node_half2(x.z, f, bad), node_half2(x.w, f, bad));
+              for (int c = 0; c < D / 8; ++c) {
+                uint4* at_c = chunk(tile, row, c);
+                const uint4 x = lds128(at_c);
+                *at_c = make_uint4(node_half2(x.x, f, bad), node_half2(x.y, f, bad),
+                                   node_half2(x.z, f, bad), node_half2(x.w, f, bad));
+              }
             }
-          }
-          if (zero || bad)
+            if (bad || (mine && ((hole >> (row >> 4)) & 1)))
 #pragma unroll 1
-            for (int c = 0; c < D / 8; ++c) *chunk(tile, c) = make_uint4(0, 0, 0, 0);
-        }
-        const unsigned turn = (is_v ? vput++ : kput++) % kAtqTurns;
-        const unsigned bit = 1u << (2 * turn + is_v);
-        if (nodes || hole || (noted & bit)) {  // (0 where nothing was noted before)
-          const unsigned any = __ballot_sync(0xffffffffu, bad);
-          if (lane == 0) {
-            s_bad[turn][is_v][warp - 12] = any;
-            if (warp == 12 && !is_v) s_hole[turn] = hole;
+              for (int c = 0; c < D / 8; ++c) *chunk(tile, row, c) = make_uint4(0, 0, 0, 0);
+            const unsigned any = __ballot_sync(0xffffffffu, bad);
+            if (lane == 0) {  // (0 where nothing was noted before)
+              s_bad[turn][is_v][row0 >> 5] = any;
+              if (warp == 12) s_hole[turn] = hole;
+            }
+            noted = any || hole ? noted | (1u << turn) : noted & ~(1u << turn);
           }
-          noted = any || hole ? noted | bit : noted & ~bit;
-        }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&full[stage]);
-          if (paged && (nodes || hole)) mbar_arrive(&raw_empty[rst]);
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&full[stage]);
+            if (paged && (nodes || hole)) mbar_arrive(&raw_empty[rst]);
+          }
         }
         if (++stage == S) {
           stage = 0;
@@ -699,14 +682,14 @@ __global__ void __launch_bounds__(kAtqThreads, 1)
       }
     }
     if (!ok && lane == 0) fail();
-    if (threadIdx.x == 384) {  // every copy has landed before the CTA can leave
+    if (asks) {  // every copy has landed before the CTA can leave
       for (unsigned j = nasked > kAtqTurns ? nasked - kAtqTurns : 0; j < nasked; ++j)
-        mbar_wait_bounded(&node_full[j % kAtqTurns], (j / kAtqTurns) & 1);
+        mbar_wait_bounded(&node_full[is_v][j % kAtqTurns], (j / kAtqTurns) & 1);
       if (nq) mbar_wait_bounded(&q_raw, (nq - 1) & 1);
     }
     __syncwarp();
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 136;");
     // ---------------- softmax ----------------
     const int w = (warp - 4) >> 2;                // half
     const int quad = warp & 3;                    // tensor-memory lanes 32 quad ..
