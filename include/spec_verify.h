@@ -624,7 +624,7 @@ SPEC_API spec_status_t spec_kv4_read(const void* pages, int layers, long long n_
  * brings a head's largest element to 2^14, weights at 2^7: both have at least
  * bf16's 8 bits down to 2^-24 of the largest), the cached values are exact in
  * fp16, sums are float32.  Limits as spec_tree_attention (D 64 or 128, G at most
- * 128, N at most SPEC_ATTN_MAX_NODES); W * page_size at most 2^31 - 257.  Two
+ * 128, N at most SPEC_ATTN_MAX_NODES); W * page_size + N at most 2^31 - 257.  Two
  * launches; the cut of the work, and so the last bits, depend on base_len and
  * the number of SMs alone.  Workspace: at least
  * spec_tree_attention_kv4_workspace_bytes() bytes.
@@ -665,7 +665,8 @@ SPEC_API spec_status_t spec_tree_attention_kv4(const void* q, const void* pages,
  * copy (SPEC_FLAG_BAD_PAGE); a parent outside [-1, B) counts as -1
  * (SPEC_FLAG_BAD_PARENT); a length outside its range counts as 0, a need beyond
  * W page_size as that (SPEC_FLAG_BAD_PATH).
- * Two launches.  Workspace: spec_kv_pages_workspace_bytes(n_pages, B2) bytes.
+ * B2 = 0 frees all pages (used = 0).  Two launches.  Workspace:
+ * spec_kv_pages_workspace_bytes(n_pages, B2) bytes.
  */
 SPEC_API size_t spec_kv_pages_workspace_bytes(long long n_pages, int rows);
 SPEC_API spec_status_t spec_kv_pages_fork(void* pages, int planes, long long plane_stride,
@@ -745,14 +746,15 @@ SPEC_API uint64_t spec_verify_launch_count(void);
  * Diagnostic control of the bounded waits (no counterpart in the pages).
  *
  * Every wait of the verification kernels on their own bulk copies, and every
- * wait between the roles of a CTA of spec_tree_attention (copies, products,
- * softmax), gives up after a limit (0.2 s by default): the CTA then sets
+ * wait between the roles of a CTA of spec_tree_attention and of
+ * spec_tree_attention_kv4 (copies, products, softmax), gives up after a limit
+ * (0.2 s by default): the CTA then sets
  * SPEC_FLAG_TIMEOUT, stops copying, waits (with the default limit) for the
  * copies and products it has in flight and finishes its control flow, so the
  * call completes with unspecified outputs and the flag raised instead of
  * hanging.  This sets the limit used by calls of spec_verify_sample,
- * spec_verify_greedy, spec_verify_tree_greedy, spec_verify_greedy_noalloc and
- * spec_tree_attention enqueued afterwards, process-wide; limit_ns = 0 restores
+ * spec_verify_greedy, spec_verify_tree_greedy, spec_verify_greedy_noalloc,
+ * spec_tree_attention and spec_tree_attention_kv4 enqueued afterwards, process-wide; limit_ns = 0 restores
  * the default.  limit_ns = 1 gives up whenever a copy has not landed (a role
  * has not answered) at the first look, which is how a test exercises that path
  * (other limits below a microsecond are rounded up by the resolution of the
