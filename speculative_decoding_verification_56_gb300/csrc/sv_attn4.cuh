@@ -1,5 +1,33 @@
 // sv_attn4.cuh -- attention of drafted trees over a 4-bit cache in pages, for
 // few rows (a node's query heads of one key-value head) per sequence.
+//
+//   out = sum_j w_j v_j / sum_j w_j,  w_j = exp(scale q . k_j),
+//
+// over the committed positions in the pages and the nodes that the mask names.
+// S = K Q^T and O = V^T P are matrix instructions of 16 entries (channels) by 8
+// rows from registers: with 8 to 24 rows, tiles of 128 would be mostly padding,
+// and entries would be written to shared memory and read back.  Both operands of
+// codes are unpacked into registers from the packed bytes, whose 16 positions of a
+// group are placed so that the thread that reads a 4- or 8-byte piece holds what
+// its fragment needs; what a product sums over (channels for S, positions for O)
+// may come in any order that both its operands share.  P becomes the second
+// product's operand by one transposition in registers.
+//
+// The work is cut into equal runs of 256 positions over two CTAs an SM (one for
+// more than 8 rows), whatever the lengths; in a CTA each warp has its own 32
+// positions of a run's step, its own ring of bulk copies (nobody waits for a
+// producer), reference, sum and output, joined at the item's end; items that
+// several CTAs share leave float32 partials for kv4_attn_finish_kernel.  The
+// softmax reference is renewed only when a score passes it by 2^kA4Lazy.  Sums,
+// references and outputs are float32; weights are rounded to fp16 (2^-11 of a
+// weight, or 2^-32 of the largest), queries, brought into its range by a power of
+// two per row, lose bits only in elements below 2^-31 of the row's largest.
+//
+// Bound: instructions, about 700 for a warp's 32 positions at D = 128 (unpacking,
+// scaling and products).  Measured: decoding 64 sequences of up to 4096 positions,
+// 32 heads of 8, 70-72 us where the packed bytes (229 MB) take 34 at the copy rate
+// and the bf16 cache takes its kernel 134; 16 positions a step 104 us, 32 with more
+// registers 77.  One chain of 5 over 300 positions: 10.6 us of kernels.
 #pragma once
 
 #include "sv_attn.cuh"

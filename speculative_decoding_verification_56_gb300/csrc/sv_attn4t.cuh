@@ -5,11 +5,25 @@
 // The same tiles, roles and softmax as the attention over a bf16 cache
 // (sv_attn.cuh: segments, half tiles, references, hand-overs), with two
 // differences.  Entries do not come as tiles that a product can read: a warp
-// copies the packed groups of a tile, and four warps unpack them, an entry a
-// thread, to fp16 tiles in the layout that a TMA copy would have given (K-major
-// and, for the values, MN-major rows of 128 swizzled bytes).  And the products
-// are of fp16, in which codes times scales are exact: queries are brought into
-// its range by a power of two per row, weights by 2^kA4Off.
+// copies the packed groups of a tile, and two groups of four warps, one for keys
+// and one for values, unpack them to fp16 tiles in the layout that a TMA copy
+// would have given (K-major and, for the values, MN-major rows of 128 swizzled
+// bytes).  And the products are of fp16, in which codes times scales are exact:
+// queries are brought into its range by a power of two per row, weights by
+// 2^kA4Off (they are rounded to fp16: 2^-11 of a weight, or 2^-32 of the largest).
+//
+// Bound: products, 4 N Hq D len operations (2048 clocks a pair of half tiles at
+// D = 128), more than the pages' bytes.  Measured (D = 128, 8 key-value heads):
+// 16 trees of 60 nodes, 32 heads, up to 4096 positions 87-91 us (products 25 us at
+// the library's rate, the bf16 kernel 69); 3 trees of 33, 40 heads, up to 65536
+// positions 158-175 us (52; bf16 129).  About 5000 clocks a tile: what is waited
+// for is the hand-over of a place of the ring, from the products that free it by
+// the packed copy's and the unpacking's latency to the products that read it;
+// query and unpacked tiles are 32 KB each, so four or five places are all there is.
+// What was gained on the way from 143 / 234 us: queries and nodes by TMA,
+// converted in place (115 / 222); no per-entry branches, and loops small enough
+// for the instruction caches, which five roles share (96 / 169); the issuing warp
+// as a whole (91); eight warps that unpack instead of four (87).
 #pragma once
 
 #include "sv_attn4.cuh"
@@ -235,227 +249,227 @@ __global__ void __launch_bounds__(kAtqThreads, 1)
   // registers: 96 a thread at launch, 480 over the five warpgroups
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-  if (warp == 2) {
-    if (lane == 0) {
-      // ---------------- segments ----------------
-      AttnWalk walk{lo, hi, s_bstart, s_b};
-      for (unsigned k = 0;; ++k) {
-        AttnSeg seg;
-        walk.next(p, &seg);
-        const unsigned at = k % kAtSegs;
-        // (the only wait that lasts as long as an item: until the one four before
-        // this is begun, so up to the run's length)
-        if (!atq_wait(p, &seg_empty[at], ((k / kAtSegs) & 1) ^ 1u, abort,
-                      (int)min(hi - lo, 1000000ll))) {
-          fail();
-          break;
+    if (warp == 2) {
+      if (lane == 0) {
+        // ---------------- segments ----------------
+        AttnWalk walk{lo, hi, s_bstart, s_b};
+        for (unsigned k = 0;; ++k) {
+          AttnSeg seg;
+          walk.next(p, &seg);
+          const unsigned at = k % kAtSegs;
+          // (the only wait that lasts as long as an item: until the one four before
+          // this is begun, so up to the run's length)
+          if (!atq_wait(p, &seg_empty[at], ((k / kAtSegs) & 1) ^ 1u, abort,
+                        (int)min(hi - lo, 1000000ll))) {
+            fail();
+            break;
+          }
+          s_seg[at] = seg;
+          mbar_arrive(&seg_full[at]);
+          if (seg.n == 0) break;
         }
-        s_seg[at] = seg;
-        mbar_arrive(&seg_full[at]);
-        if (seg.n == 0) break;
       }
-    }
-    __syncwarp();
-  } else if (warp == 0) {
-    // ---------------- copies ----------------
-    // lane j < 8 brings in the keys or values of positions 16 j .. of a tile
-    int stage = 0, issued = 0;
-    unsigned phase = 0;
-    bool ok = true;
-    const int page = 1 << p.lg;
-    for (unsigned k = 0; ok; ++k) {
-      const unsigned at = k % kAtSegs;
-      if (!atq_wait_warp(p, &seg_full[at], (k / kAtSegs) & 1, abort)) {
-        ok = false;
-        break;
-      }
-      const AttnSeg seg = s_seg[at];
       __syncwarp();
-      if (lane == 0) mbar_arrive(&seg_empty[at]);
-      if (seg.n == 0) break;
-      const int32_t* row = p.table + (size_t)seg.b * p.Wt;
-      auto page_of = [&](int i) {  // of this lane's positions of put i: -2 none wanted, -1 no page
-        if (lane >= 8 || i >= 2 * seg.n) return -2;
-        int t, is_v;
-        atq_put(seg.pair, seg.n, i, &t, &is_v);
-        const int pos = (seg.t0 + t) * kAtKeys + lane * 16;
-        if (pos >= seg.plen) return -2;
-        const int id = row[pos >> p.lg];
-        return id >= 0 && id < p.n_pages ? id : -1;
-      };
-      // (pages are looked up two puts early)
-      int id0 = page_of(0), id1 = page_of(1);
-#pragma unroll 1
-      for (int i = 0; i < 2 * seg.n; ++i) {
-        int t, is_v;
-        atq_put(seg.pair, seg.n, i, &t, &is_v);
-        const int id = id0;
-        id0 = id1;
-        id1 = page_of(i + 2);
-        const int key0 = (seg.t0 + t) * kAtKeys;
-        if (key0 >= seg.plen) continue;  // nodes alone: not in the pages
-        if (!atq_wait_warp(p, &raw_empty[stage], phase ^ 1u, abort)) {
+    } else if (warp == 0) {
+      // ---------------- copies ----------------
+      // lane j < 8 brings in the keys or values of positions 16 j .. of a tile
+      int stage = 0, issued = 0;
+      unsigned phase = 0;
+      bool ok = true;
+      const int page = 1 << p.lg;
+      for (unsigned k = 0; ok; ++k) {
+        const unsigned at = k % kAtSegs;
+        if (!atq_wait_warp(p, &seg_full[at], (k / kAtSegs) & 1, abort)) {
           ok = false;
           break;
         }
-        const unsigned some = __ballot_sync(0xffffffffu, id >= 0);
-        const unsigned none = __ballot_sync(0xffffffffu, id == -1);
-        if (lane == 0) {
-          if (none) set_flag(p.flags, kFlagBadPage);
-          s_nopage[stage] = none;
-          mbar_expect_tx(&raw_full[stage], (unsigned)__popc(some) * (kHalf / 8));
-        }
+        const AttnSeg seg = s_seg[at];
         __syncwarp();
-        if (id >= 0)
-          bulk_g2s(raw + stage * kHalf + lane * (kHalf / 8),
-                   p.pages + ((size_t)id * p.Hkv + seg.h) * kv4_block(page, D) +
-                       kv4_half((key0 + lane * 16) & (page - 1), is_v, D),
-                   kHalf / 8, &raw_full[stage]);
-        ++issued;
-        if (++stage == kRaw) {
+        if (lane == 0) mbar_arrive(&seg_empty[at]);
+        if (seg.n == 0) break;
+        const int32_t* row = p.table + (size_t)seg.b * p.Wt;
+        auto page_of = [&](int i) {  // of this lane's positions of put i: -2 none wanted, -1 no page
+          if (lane >= 8 || i >= 2 * seg.n) return -2;
+          int t, is_v;
+          atq_put(seg.pair, seg.n, i, &t, &is_v);
+          const int pos = (seg.t0 + t) * kAtKeys + lane * 16;
+          if (pos >= seg.plen) return -2;
+          const int id = row[pos >> p.lg];
+          return id >= 0 && id < p.n_pages ? id : -1;
+        };
+        // (pages are looked up two puts early)
+        int id0 = page_of(0), id1 = page_of(1);
+#pragma unroll 1
+        for (int i = 0; i < 2 * seg.n; ++i) {
+          int t, is_v;
+          atq_put(seg.pair, seg.n, i, &t, &is_v);
+          const int id = id0;
+          id0 = id1;
+          id1 = page_of(i + 2);
+          const int key0 = (seg.t0 + t) * kAtKeys;
+          if (key0 >= seg.plen) continue;  // nodes alone: not in the pages
+          if (!atq_wait_warp(p, &raw_empty[stage], phase ^ 1u, abort)) {
+            ok = false;
+            break;
+          }
+          const unsigned some = __ballot_sync(0xffffffffu, id >= 0);
+          const unsigned none = __ballot_sync(0xffffffffu, id == -1);
+          if (lane == 0) {
+            if (none) set_flag(p.flags, kFlagBadPage);
+            s_nopage[stage] = none;
+            mbar_expect_tx(&raw_full[stage], (unsigned)__popc(some) * (kHalf / 8));
+          }
+          __syncwarp();
+          if (id >= 0)
+            bulk_g2s(raw + stage * kHalf + lane * (kHalf / 8),
+                     p.pages + ((size_t)id * p.Hkv + seg.h) * kv4_block(page, D) +
+                         kv4_half((key0 + lane * 16) & (page - 1), is_v, D),
+                     kHalf / 8, &raw_full[stage]);
+          ++issued;
+          if (++stage == kRaw) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (!ok && lane == 0) fail();
+      // every copy has landed before the CTA can leave
+      for (int j = max(0, issued - kRaw); j < issued; ++j)
+        mbar_wait_bounded(&raw_full[j % kRaw], (unsigned)((j / kRaw) & 1));
+      __syncwarp();
+    } else if (warp == 1) {
+      // ---------------- MMAs ----------------
+      // The whole warp walks along and one elected thread issues, so that what the
+      // products are issued with stands in uniform registers (one thread on its own
+      // took 3900 clocks a tile to issue 2048 clocks of products).
+      const uint32_t id_qk = umma_idesc_f16_f32(kAtRows, kAtKeys);
+      const uint32_t id_pv = umma_idesc_f16_f32(kAtRows, D) | (1u << 16);  // V: MN-major
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      const uint64_t qdesc = umma_desc_sw128(smem_addr(smem));
+      const uint64_t kdesc = umma_desc_sw128(smem_addr(ring));
+      const uint64_t vdesc = umma_desc_mn_sw128(smem_addr(ring));
+      int stage = 0;
+      unsigned phase = 0, nq = 0, np = 0, np1 = 0;
+      bool ok = true;
+      auto wait = [&](uint64_t* bar, unsigned parity) {
+        if (!atq_wait_warp(p, bar, parity & 1, abort)) {
+          ok = false;
+          if (lane == 0) fail();
+        }
+        tmem_fence_after();
+        return ok;
+      };
+      auto advance = [&]() {
+        if (++stage == S) {
           stage = 0;
           phase ^= 1u;
         }
-      }
-    }
-    if (!ok && lane == 0) fail();
-    // every copy has landed before the CTA can leave
-    for (int j = max(0, issued - kRaw); j < issued; ++j)
-      mbar_wait_bounded(&raw_full[j % kRaw], (unsigned)((j / kRaw) & 1));
-    __syncwarp();
-  } else if (warp == 1) {
-    // ---------------- MMAs ----------------
-    // The whole warp walks along and one elected thread issues, so that what the
-    // products are issued with stands in uniform registers (one thread on its own
-    // took 3900 clocks a tile to issue 2048 clocks of products).
-    const uint32_t id_qk = umma_idesc_f16_f32(kAtRows, kAtKeys);
-    const uint32_t id_pv = umma_idesc_f16_f32(kAtRows, D) | (1u << 16);  // V: MN-major
-    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-    const uint64_t qdesc = umma_desc_sw128(smem_addr(smem));
-    const uint64_t kdesc = umma_desc_sw128(smem_addr(ring));
-    const uint64_t vdesc = umma_desc_mn_sw128(smem_addr(ring));
-    int stage = 0;
-    unsigned phase = 0, nq = 0, np = 0, np1 = 0;
-    bool ok = true;
-    auto wait = [&](uint64_t* bar, unsigned parity) {
-      if (!atq_wait_warp(p, bar, parity & 1, abort)) {
-        ok = false;
-        if (lane == 0) fail();
-      }
-      tmem_fence_after();
-      return ok;
-    };
-    auto advance = [&]() {
-      if (++stage == S) {
-        stage = 0;
-        phase ^= 1u;
-      }
-    };
-    auto commit = [&](uint64_t* bar) {
-      if (elect_one()) umma_commit(bar);
-      __syncwarp();
-    };
-    // scores of half w from the K tile in stage st, query tile qt
-    auto scores = [&](int w, int qt, int st) {
-      const uint64_t a = qdesc + (uint64_t)(qt * kTile >> 4);
-      const uint64_t b = kdesc + (uint64_t)(st * kTile >> 4);
-      const uint32_t d = tm + w * kAtKeys;
-      if (elect_one()) {
+      };
+      auto commit = [&](uint64_t* bar) {
+        if (elect_one()) umma_commit(bar);
+        __syncwarp();
+      };
+      // scores of half w from the K tile in stage st, query tile qt
+      auto scores = [&](int w, int qt, int st) {
+        const uint64_t a = qdesc + (uint64_t)(qt * kTile >> 4);
+        const uint64_t b = kdesc + (uint64_t)(st * kTile >> 4);
+        const uint32_t d = tm + w * kAtKeys;
+        if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint64_t o = (uint64_t)((kk >> 2) * (kAtKeys * 128 >> 4) + (kk & 3) * 2);
-          umma_ss(d, a + o, b + o, id_qk, kk ? 1u : 0u);
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint64_t o = (uint64_t)((kk >> 2) * (kAtKeys * 128 >> 4) + (kk & 3) * 2);
+            umma_ss(d, a + o, b + o, id_qk, kk ? 1u : 0u);
+          }
+          umma_commit(&s_full[w]);
+          mbar_arrive(&s_full[w]);
         }
-        umma_commit(&s_full[w]);
-        mbar_arrive(&s_full[w]);
-      }
-      __syncwarp();
-    };
-    // output of half w from the V tile in stage st
-    auto output = [&](int w, int st, bool first) {
-      const uint64_t b = vdesc + (uint64_t)(st * kTile >> 4);
-      const uint32_t d = tm + 2 * kAtKeys + w * D, a = tm + w * kAtKeys;
-      if (elect_one()) {
+        __syncwarp();
+      };
+      // output of half w from the V tile in stage st
+      auto output = [&](int w, int st, bool first) {
+        const uint64_t b = vdesc + (uint64_t)(st * kTile >> 4);
+        const uint32_t d = tm + 2 * kAtKeys + w * D, a = tm + w * kAtKeys;
+        if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < kAtKeys / 16; ++kk)
-          umma_ts(d, a + kk * 8, b + (uint64_t)(kk * (2048 >> 4)), id_pv, (!first || kk) ? 1u : 0u);
-      }
-      __syncwarp();
-    };
-    while (ok) {
-      const unsigned at = nq % kAtSegs;
-      if (!wait(&seg_full[at], nq / kAtSegs)) break;
-      const int n = __shfl_sync(0xffffffffu, s_seg[at].n, 0);
-      const int pair = __shfl_sync(0xffffffffu, s_seg[at].pair, 0);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&seg_empty[at]);
-      if (n == 0 || !wait(&q_full, nq++)) break;
-      if (pair) {
-        // ring: K0, V0, K1, V1, ...; each tile is waited for as late as its use
-        // allows, and where the tensor cores have work
-        if (!wait(&full[stage], phase)) break;
-        scores(0, 0, stage);
-        scores(1, 1, stage);
-        if (n == 1) commit(&q_empty);
-        advance();
-        int vst = stage;
-        if (!wait(&full[stage], phase)) break;
-        advance();
-#pragma unroll 1
-        for (int t = 0; t < n; ++t, ++np) {
-          const bool more = t + 1 < n;
-          const int v = vst, k = stage;
-          if (more && !wait(&full[stage], phase)) break;
-          if (!wait(&p_full[0], np)) break;
-          output(0, v, t == 0);
-          if (more) {
-            scores(0, 0, k);
-            advance();
-            vst = stage;
-            if (!wait(&full[stage], phase)) break;
-            advance();
-          } else {
-            commit(&o_full[0]);
-          }
-          if (!wait(&p_full[1], np)) break;
-          output(1, v, t == 0);
-          if (more) {
-            scores(1, 1, k);
-            if (t + 2 == n) commit(&q_empty);
-          } else {
-            commit(&o_full[1]);
-          }
+          for (int kk = 0; kk < kAtKeys / 16; ++kk)
+            umma_ts(d, a + kk * 8, b + (uint64_t)(kk * (2048 >> 4)), id_pv, (!first || kk) ? 1u : 0u);
         }
-      } else {
-        for (int t = 0; t < min(2, n); ++t) {
+        __syncwarp();
+      };
+      while (ok) {
+        const unsigned at = nq % kAtSegs;
+        if (!wait(&seg_full[at], nq / kAtSegs)) break;
+        const int n = __shfl_sync(0xffffffffu, s_seg[at].n, 0);
+        const int pair = __shfl_sync(0xffffffffu, s_seg[at].pair, 0);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&seg_empty[at]);
+        if (n == 0 || !wait(&q_full, nq++)) break;
+        if (pair) {
+          // ring: K0, V0, K1, V1, ...; each tile is waited for as late as its use
+          // allows, and where the tensor cores have work
           if (!wait(&full[stage], phase)) break;
-          scores(t, 0, stage);
-          if (t + 1 == n) commit(&q_empty);
+          scores(0, 0, stage);
+          scores(1, 1, stage);
+          if (n == 1) commit(&q_empty);
           advance();
-        }
-#pragma unroll 1
-        for (int t = 0; ok && t < n; ++t) {
-          const int w = t & 1, vst = stage;
+          int vst = stage;
           if (!wait(&full[stage], phase)) break;
           advance();
-          if (!wait(&p_full[w], w ? np1++ : np++)) break;
-          output(w, vst, t < 2);
-          if (t + 2 < n) {
+#pragma unroll 1
+          for (int t = 0; t < n; ++t, ++np) {
+            const bool more = t + 1 < n;
+            const int v = vst, k = stage;
+            if (more && !wait(&full[stage], phase)) break;
+            if (!wait(&p_full[0], np)) break;
+            output(0, v, t == 0);
+            if (more) {
+              scores(0, 0, k);
+              advance();
+              vst = stage;
+              if (!wait(&full[stage], phase)) break;
+              advance();
+            } else {
+              commit(&o_full[0]);
+            }
+            if (!wait(&p_full[1], np)) break;
+            output(1, v, t == 0);
+            if (more) {
+              scores(1, 1, k);
+              if (t + 2 == n) commit(&q_empty);
+            } else {
+              commit(&o_full[1]);
+            }
+          }
+        } else {
+          for (int t = 0; t < min(2, n); ++t) {
             if (!wait(&full[stage], phase)) break;
-            scores(w, 0, stage);
-            if (t + 3 == n) commit(&q_empty);
+            scores(t, 0, stage);
+            if (t + 1 == n) commit(&q_empty);
             advance();
-          } else {
-            commit(&o_full[w]);
+          }
+#pragma unroll 1
+          for (int t = 0; ok && t < n; ++t) {
+            const int w = t & 1, vst = stage;
+            if (!wait(&full[stage], phase)) break;
+            advance();
+            if (!wait(&p_full[w], w ? np1++ : np++)) break;
+            output(w, vst, t < 2);
+            if (t + 2 < n) {
+              if (!wait(&full[stage], phase)) break;
+              scores(w, 0, stage);
+              if (t + 3 == n) commit(&q_empty);
+              advance();
+            } else {
+              commit(&o_full[w]);
+            }
           }
         }
       }
+      // every MMA has completed before tensor memory is freed
+      commit(&drain);
+      mbar_wait_bounded(&drain, 0);
+      __syncwarp();
     }
-    // every MMA has completed before tensor memory is freed
-    commit(&drain);
-    mbar_wait_bounded(&drain, 0);
-    __syncwarp();
-  }
   } else if (warp >= 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     // ---------------- unpacking ----------------

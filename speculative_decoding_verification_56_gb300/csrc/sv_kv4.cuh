@@ -14,6 +14,11 @@
 // Codes have 2 significant bits and scales 4, so a value is exact in bf16 and,
 // without 2^e, in fp16; and x / (s 2^e) next to a border of two codes is
 // decided exactly in float32 (x has 8 bits, border times scale at most 7).
+//
+// Commit reads 4 D bytes of an entry's head and writes 9 D / 8, read the other
+// way round.  Measured with 5 prompts of up to 1000 tokens, 8 layers, 8 heads of
+// 128: commit 55 us (instructions: scales and quotients), read 54 us (5.3 TB/s);
+// before the lanes of a warp shared an entry the two took 119 us.
 #pragma once
 
 #include "sv_rope.cuh"
