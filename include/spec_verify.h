@@ -567,6 +567,7 @@ SPEC_API spec_status_t spec_tree_qkv_rope_nodes(const void* qkv, const void* q_n
  * (SPEC_FLAG_BAD_PATH) or a needed table entry that names no page
  * (SPEC_FLAG_BAD_PAGE) is left untouched, with new_len = max(base_len - 1, 0).
  * Elements that are not finite give unspecified values of their scale's 16.
+ * new_len must not overlap the inputs (SPEC_ERR_INVALID_ARG).
  * One launch.  Workspace: spec_verify_workspace_bytes(SPEC_MODE_KV4, ...) bytes
  * (the flag header).  D is 64 or 128, N at most SPEC_MAX_TREE_NODES, W at most
  * SPEC_KV_MAX_TABLE.
@@ -623,7 +624,8 @@ SPEC_API spec_status_t spec_kv4_read(const void* pages, int layers, long long n_
  * Queries and weights are rounded to fp16 (queries at a power of two that
  * brings a head's largest element to 2^14, weights at 2^7: both have at least
  * bf16's 8 bits down to 2^-24 of the largest), the cached values are exact in
- * fp16, sums are float32.  Limits as spec_tree_attention (D 64 or 128, G at most
+ * fp16, sums are float32.  out must not overlap q, node_k or node_v
+ * (SPEC_ERR_INVALID_ARG).  Limits as spec_tree_attention (D 64 or 128, G at most
  * 128, N at most SPEC_ATTN_MAX_NODES); W * page_size + N at most 2^31 - 257.  Two
  * launches; the cut of the work, and so the last bits, depend on base_len and
  * the number of SMs alone.  Workspace: at least
@@ -659,8 +661,8 @@ SPEC_API spec_status_t spec_tree_attention_kv4(const void* q, const void* pages,
  *   parent      int32 [B2], or NULL (j's own, B2 <= B: growth alone)
  *   need        int32 [B2], or NULL (new_len)
  * Outputs: new_table int32 [B2, W] (-1 behind a sequence's pages), new_len
- * int32 [B2], used int32 [1] (pages held).  new_table and new_len must not
- * overlap the inputs.  No page left: -1 (SPEC_FLAG_NO_PAGE).  A needed entry
+ * int32 [B2], used int32 [1] (pages held).  Outputs must not overlap the inputs
+ * (SPEC_ERR_INVALID_ARG).  No page left: -1 (SPEC_FLAG_NO_PAGE).  A needed entry
  * that names no page stays -1, an unfinished one gets a fresh page without a
  * copy (SPEC_FLAG_BAD_PAGE); a parent outside [-1, B) counts as -1
  * (SPEC_FLAG_BAD_PARENT); a length outside its range counts as 0, a need beyond
@@ -683,7 +685,8 @@ SPEC_API spec_status_t spec_kv_pages_fork(void* pages, int planes, long long pla
  * move to the free places below n, in ascending order both.
  *   page_table  int32 [B, W], negative: no page (others outside [0, n_pages)
  *               become -1, SPEC_FLAG_BAD_PAGE)
- * Outputs: new_table int32 [B, W] (may be page_table itself), used int32 [1] (n).
+ * Outputs: new_table int32 [B, W] (may be page_table itself, not a part of it),
+ * used int32 [1] (n).
  * Two launches.  Other arguments as spec_kv_pages_fork; workspace:
  * spec_kv_pages_workspace_bytes(n_pages, B) bytes.
  */
@@ -712,7 +715,9 @@ SPEC_API spec_status_t spec_kv_pages_compact(void* pages, int planes, long long 
  * -inf, -1, -1, 1.
  * Totals are ordered in float64 from float32 exponentials: they are off by less
  * than 2^-19 (1 + |z_v / T|); within a beam the order is that of the logits,
- * and beams with the same logits and scores tie.
+ * and beams with the same logits and scores tie.  A logit that is NaN or +inf
+ * makes what its request gets unspecified.  Outputs must not overlap scores or
+ * finished (SPEC_ERR_INVALID_ARG).
  * Two launches.  Workspace: spec_beam_select_workspace_bytes() bytes.
  */
 SPEC_API size_t spec_beam_select_workspace_bytes(int B, int K, int V, int M, int dtype);

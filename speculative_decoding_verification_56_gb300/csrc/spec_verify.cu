@@ -12,6 +12,7 @@
 #include <cstdint>
 #include <cstring>
 #include <mutex>
+#include <utility>
 
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -182,6 +183,12 @@ bool make_layout(int mode, int B, int kN, int V, int dtype, Layout* L) {
 }
 
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
+
+// Whether two arrays (null: none) share bytes.
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+  return a && b && x < y + nb && y < x + na;
+}
 
 // 16-byte vector path: base aligned and every row a whole number of vectors.
 bool vec_ok(const void* p, int V, int dtype) {
@@ -1632,6 +1639,12 @@ spec_status_t spec_kv4_commit_path(void* pages, int layers, long long n_pages, i
     return SPEC_ERR_ALIGNMENT;
   if (!workspace || workspace_bytes < kHeaderBytes) return SPEC_ERR_WORKSPACE;
   if (!aligned(workspace, kAlign)) return SPEC_ERR_ALIGNMENT;
+  // (many CTAs read a sequence's inputs, one writes its new length)
+  const size_t seqs = 4 * (size_t)B;
+  if (overlap(new_len, seqs, base_len, seqs) || overlap(new_len, seqs, accepted_len, seqs) ||
+      overlap(new_len, seqs, path_nodes, path_nodes ? seqs * (max_depth + 1) : 0) ||
+      overlap(new_len, seqs, page_table, seqs * W))
+    return SPEC_ERR_INVALID_ARG;
   sv::Kv4Params prm;
   std::memset(&prm, 0, sizeof prm);
   prm.pages = static_cast<uint8_t*>(pages);
@@ -1729,6 +1742,10 @@ spec_status_t spec_tree_attention_kv4(const void* q, const void* pages, long lon
   if (!aligned(workspace, kAlign)) return SPEC_ERR_ALIGNMENT;
   const Attn4Plan plan = attn4_plan(B, N, Hq, Hkv, D);
   if (workspace_bytes < plan.bytes) return SPEC_ERR_WORKSPACE;
+  const size_t heads = 2 * (size_t)B * N * D;  // bytes of a head of all nodes
+  if (overlap(out, heads * Hq, q, heads * Hq) || overlap(out, heads * Hq, node_k, heads * Hkv) ||
+      overlap(out, heads * Hq, node_v, heads * Hkv))
+    return SPEC_ERR_INVALID_ARG;
   int sms = 0;
   const spec_status_t st = sm_count(&sms);
   if (st != SPEC_OK) return st;
@@ -1844,6 +1861,11 @@ spec_status_t spec_kv_pages_fork(void* pages, int planes, long long plane_stride
   if ((B > 0 && !length) || (B2 > 0 && !new_len)) return SPEC_ERR_INVALID_ARG;
   if (!aligned(length, 4) || !aligned(parent, 4) || !aligned(need, 4) || !aligned(new_len, 4))
     return SPEC_ERR_ALIGNMENT;
+  const size_t rows = 4 * (size_t)B, rows2 = 4 * (size_t)B2;
+  for (const auto& o : {std::pair<const void*, size_t>(new_table, rows2 * W), {new_len, rows2}, {used, 4}})
+    if (overlap(o.first, o.second, page_table, rows * W) || overlap(o.first, o.second, length, rows) ||
+        overlap(o.first, o.second, parent, rows2) || overlap(o.first, o.second, need, rows2))
+      return SPEC_ERR_INVALID_ARG;
   prm.length = length;
   prm.parent = parent;
   prm.need = need;
@@ -1862,6 +1884,10 @@ spec_status_t spec_kv_pages_compact(void* pages, int planes, long long plane_str
                                         page_table, B, B, W, new_table, used, workspace,
                                         workspace_bytes, &prm);
   if (st != SPEC_OK) return st;
+  const size_t bytes = 4 * (size_t)B * W;
+  if ((new_table != page_table && overlap(new_table, bytes, page_table, bytes)) ||
+      overlap(used, 4, page_table, bytes))
+    return SPEC_ERR_INVALID_ARG;
   return run_pages(false, prm, stream);
 }
 
@@ -1888,6 +1914,10 @@ spec_status_t spec_beam_select(const void* logits, int dtype, const float* score
     return SPEC_ERR_ALIGNMENT;
   if (!workspace || workspace_bytes < L.bytes) return SPEC_ERR_WORKSPACE;
   if (!aligned(workspace, kAlign)) return SPEC_ERR_ALIGNMENT;
+  const size_t in = 4 * (size_t)B * K, picked = 4 * (size_t)B * M;
+  for (const void* o : {(const void*)out_scores, (const void*)out_parents, (const void*)out_tokens,
+                        (const void*)out_finished})
+    if (overlap(o, picked, scores, in) || overlap(o, picked, finished, in)) return SPEC_ERR_INVALID_ARG;
   char* ws = static_cast<char*>(workspace);
   sv::BeamParams prm;
   std::memset(&prm, 0, sizeof prm);

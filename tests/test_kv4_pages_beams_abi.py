@@ -119,6 +119,38 @@ def test_beam_validation(lib):
     assert call(B=0, z=None) == OK
 
 
+def test_outputs_over_inputs(lib):
+    far = [FAKE + (i << 30) for i in range(1, 10)]
+    call = caller(lib.spec_kv4_commit_path, pages=far[0], layers=2, n_pages=9, page=16, Hkv=2, D=64, table=far[1], W=3,
+                  nk=far[2], nv=far[3], base=far[4], acc=far[5], path=far[6], md=4, exps=None, B=2, N=8, new=far[7],
+                  ws=far[8], wsb=256, stream=None)
+    for over in (far[4], far[4] + 4, far[5], far[6] + 36, far[1] + 20):
+        assert call(new=over) == INVALID, over
+    for N in (1, 60):
+        n = sv.spec_tree_attention_kv4_workspace_bytes(2, N, 8, 2, 64)
+        call = caller(lib.spec_tree_attention_kv4, q=far[0], pages=far[1], n_pages=9, page=16, table=far[2], W=3, nk=far[3],
+                      nv=far[4], mask=None, base=far[5], exps=None, B=2, N=N, Hq=8, Hkv=2, D=64, scale=0.1, out=far[6],
+                      lse=None, ws=far[7], wsb=n, stream=None)
+        for over in (far[0], far[0] + 2 * 2 * N * 8 * 64 - 16, far[0] - 2 * 2 * N * 8 * 64 + 16, far[3], far[4]):
+            assert call(out=over) == INVALID, over
+    n = sv.spec_kv_pages_workspace_bytes(9, 4)
+    fork = caller(lib.spec_kv_pages_fork, pages=far[0], planes=2, ps=9 * 64, n_pages=9, pb=64, page=16, table=far[1],
+                  len=far[2], B=3, parent=far[3], need=far[4], B2=4, W=3, new=far[5], nl=far[6], used=far[7], ws=far[8],
+                  wsb=n, stream=None)
+    for over in (dict(new=far[1]), dict(new=far[1] + 32), dict(new=far[2]), dict(nl=far[2]), dict(nl=far[3]),
+                 dict(nl=far[4] + 12), dict(used=far[1]), dict(used=far[2] + 8)):
+        assert fork(**over) == INVALID, over
+    compact = caller(lib.spec_kv_pages_compact, pages=far[0], planes=2, ps=9 * 64, n_pages=9, pb=64, table=far[1], B=3, W=3,
+                     new=far[5], used=far[7], ws=far[8], wsb=n, stream=None)
+    for over in (dict(new=far[1] + 4), dict(new=far[1] - 4), dict(used=far[1] + 32)):
+        assert compact(**over) == INVALID, over
+    n = sv.spec_beam_select_workspace_bytes(2, 4, 1000, 4, 1)
+    call = caller(lib.spec_beam_select, z=far[0], dtype=1, s=far[1], fin=far[2], eos=2, T=1.0, B=2, K=4, V=1000, M=4,
+                  os=far[3], op=far[4], ot=far[5], of=far[6], ws=far[7], wsb=n, stream=None)
+    for over in (dict(os=far[1]), dict(op=far[1] + 28), dict(ot=far[2]), dict(of=far[2])):
+        assert call(**over) == INVALID, over
+
+
 def test_rope_nodes_validation(lib):
     call = caller(lib.spec_tree_qkv_rope_nodes, qkv=FAKE, qn=None, kn=None, eps=1e-6, freq=FAKE, rot=64, inter=0, off=0,
                   base=FAKE, depth=None, B=2, N=8, Hq=8, Hkv=2, D=64, q=FAKE, k=FAKE, v=FAKE, ws=FAKE, wsb=256, stream=None)
