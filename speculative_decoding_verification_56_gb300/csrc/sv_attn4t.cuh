@@ -16,14 +16,16 @@
 // D = 128), more than the pages' bytes.  Measured (D = 128, 8 key-value heads):
 // 16 trees of 60 nodes, 32 heads, up to 4096 positions 87-91 us (products 25 us at
 // the library's rate, the bf16 kernel 69); 3 trees of 33, 40 heads, up to 65536
-// positions 158-175 us (52; bf16 129).  About 5000 clocks a tile: what is waited
-// for is the hand-over of a place of the ring, from the products that free it by
-// the packed copy's and the unpacking's latency to the products that read it;
-// query and unpacked tiles are 32 KB each, so four or five places are all there is.
+// positions 154-165 us (52; bf16 129).  About 4700 clocks a tile, two chains of
+// scores (512), softmax (2050-2400 beside the warps that unpack) and output (512)
+// with their hand-overs; and the hand-over of a place of the ring, 2300 clocks
+// from the products that free it to the products that read it: query and unpacked
+// tiles are 32 KB each, so four or five places are all there is.
 // What was gained on the way from 143 / 234 us: queries and nodes by TMA,
 // converted in place (115 / 222); no per-entry branches, and loops small enough
 // for the instruction caches, which five roles share (96 / 169); the issuing warp
-// as a whole (91); eight warps that unpack instead of four (87).
+// as a whole (91); eight warps that unpack instead of four (87, long 173); every
+// tile waited for right before its use (87-90, long 157).
 #pragma once
 
 #include "sv_attn4.cuh"
@@ -405,28 +407,23 @@ __global__ void __launch_bounds__(kAtqThreads, 1)
         if (lane == 0) mbar_arrive(&seg_empty[at]);
         if (n == 0 || !wait(&q_full, nq++)) break;
         if (pair) {
-          // ring: K0, V0, K1, V1, ...; each tile is waited for as late as its use
-          // allows, and where the tensor cores have work
+          // ring: K0, V0, K1, V1, ...; each tile is waited for right before its use
           if (!wait(&full[stage], phase)) break;
           scores(0, 0, stage);
           scores(1, 1, stage);
           if (n == 1) commit(&q_empty);
           advance();
-          int vst = stage;
-          if (!wait(&full[stage], phase)) break;
-          advance();
 #pragma unroll 1
           for (int t = 0; t < n; ++t, ++np) {
             const bool more = t + 1 < n;
-            const int v = vst, k = stage;
-            if (more && !wait(&full[stage], phase)) break;
-            if (!wait(&p_full[0], np)) break;
+            const int v = stage;
+            if (!wait(&p_full[0], np) || !wait(&full[stage], phase)) break;
             output(0, v, t == 0);
+            advance();
+            const int k = stage;
             if (more) {
-              scores(0, 0, k);
-              advance();
-              vst = stage;
               if (!wait(&full[stage], phase)) break;
+              scores(0, 0, k);
               advance();
             } else {
               commit(&o_full[0]);
