@@ -12,13 +12,13 @@
 // both rounded to nearest even (codes saturate at 6), channel 2 i in the low
 // half of byte i; e is one exponent per layer for keys and one for values.
 // Codes have 2 significant bits and scales 4, so a value is exact in bf16 and,
-// without 2^e, in fp16; and x / (s 2^e) next to a border of two codes is
-// decided exactly in float32 (x has 8 bits, border times scale at most 7).
+// without 2^e, in fp16; and a / 6 and x / (s 2^e) next to a border are decided
+// exactly in float32 (see the commit).
 //
 // Commit reads 4 D bytes of an entry's head and writes 9 D / 8, read the other
 // way round.  Measured with 5 prompts of up to 1000 tokens, 8 layers, 8 heads of
-// 128: commit 55 us (instructions: scales and quotients), read 54 us (5.3 TB/s);
-// before the lanes of a warp shared an entry the two took 119 us.
+// 128: commit 44 us, read 54-58 us (5 TB/s); commit took 55 with divisions and
+// rounding by integers, and both 119 before the lanes of a warp shared an entry.
 #pragma once
 
 #include "sv_rope.cuh"
@@ -75,13 +75,21 @@ __device__ __forceinline__ uint32_t to_e4m3(float x) {
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.0f), "f"(x));
   return r & 0xFFu;
 }
-// a byte of two codes, lo in the low half, to nearest even, saturating
-__device__ __forceinline__ uint32_t to_e2m1x2(float hi, float lo) {
+// 8 codes (a word), channels in order from the low end, to nearest even, saturating
+__device__ __forceinline__ uint32_t to_e2m1x8(const float (&x)[8]) {
   uint32_t r;
-  asm("{\n .reg .b8 t;\n cvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n mov.b32 %0, {t, t, t, t};\n}\n"
+  asm("{\n .reg .b8 a, b, c, d;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n"
+      " mov.b32 %0, {a, b, c, d};\n}\n"
       : "=r"(r)
-      : "f"(hi), "f"(lo));
-  return r & 0xFFu;
+      : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
+  return r;
+}
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
 
 struct Kv4Params {
@@ -167,8 +175,7 @@ __global__ void __launch_bounds__(kKv4Threads) kv4_commit_kernel(const Kv4Params
   if (layer == 0 && part == 0 && threadIdx.x == 0)
     p.new_len[b] = count ? base - 1 + count : max(base - 1, 0);
   const int blocks = p.Hkv * kBlocks, page = 1 << p.lg;
-  const float unit[2] = {pow2_small(kv4_exp(p.exps, 2 * layer)),
-                         pow2_small(kv4_exp(p.exps, 2 * layer + 1))};
+  const int e[2] = {kv4_exp(p.exps, 2 * layer), kv4_exp(p.exps, 2 * layer + 1)};
   const Kv4Lanes w(p, part);
   for (int at = w.first; at < count; at += w.step) {
     const int node = p.path ? p.path[(size_t)b * (p.max_depth + 1) + at] : at;
@@ -191,23 +198,36 @@ __global__ void __launch_bounds__(kKv4Threads) kv4_commit_kernel(const Kv4Params
       for (int v = 0; v < 2; ++v) {
         const uint32_t x[8] = {x4[v][0].x, x4[v][0].y, x4[v][0].z, x4[v][0].w,
                                x4[v][1].x, x4[v][1].y, x4[v][1].z, x4[v][1].w};
-        uint32_t a = 0;  // largest magnitude, as bits
+        uint32_t a2 = 0;  // largest magnitudes of even and odd channels, as bits
 #pragma unroll
-        for (int j = 0; j < 8; ++j) a = max(a, max(x[j] & 0x7FFFu, (x[j] >> 16) & 0x7FFFu));
-        const uint32_t sb = to_e4m3(fminf(__fdiv_rn(__uint_as_float(a << 16), 6.0f) / unit[v], 448.0f));
-        const float step = half2_to_float2(kv4_scales(sb)).x * unit[v];
-        // x / step, to 12 bits: a quotient on the border of two codes is exactly
-        // that (borders have 3 bits), and others are further from it than 2^-8 of
-        // it: with whole numbers X < 2^8 and m < 2^4 (of x and s), X against
-        // border x m < 2^7
-        const float inv = step > 0.0f ? 1.0f / step : 0.0f;
-        auto quotient = [&](float y) {
-          return __uint_as_float((__float_as_uint(y * inv) + 0x800u) & 0xFFFFF000u);
-        };
-        uint32_t code[2] = {0, 0};
+        for (int j = 0; j < 8; ++j) a2 = max_u16x2(a2, x[j] & 0x7FFF7FFFu);
+        const float a = __uint_as_float(max(a2 & 0xFFFF0000u, a2 << 16));
+        // Quotients a / 6 and x / step, by reciprocals (off by 2^-22 of themselves)
+        // and rounded so far that those on a border of two scales or codes are
+        // exactly that, while the others, further from a border than 2^-8 of it,
+        // stay on their side.  (With whole numbers X < 2^8 of a or x, m < 2^4 of the
+        // step: X against borders times 6 or m, below 2^8.)  a / 6 to 12 bits; x /
+        // step, whose borders are 1/4 and more, to multiples of 2^-11 (by at most a
+        // quarter of that distance).
+        const float sixth = __uint_as_float((__float_as_uint(a * (1.0f / 6.0f)) + 0x800u) & 0xFFFFF000u);
+        const uint32_t sb = to_e4m3(fminf(sixth * pow2_small(-e[v]), 448.0f));
+        const float step = half2_to_float2(kv4_scales(sb)).x * pow2_small(e[v]);
+        float inv;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(step));
+        if (sb == 0) inv = 0.0f;
+        constexpr float kGrid = 6144.0f;  // 1.5 2^12, whose last place is 2^-11
+        const unsigned long long inv2 = f2pack(inv, inv), up = f2pack(kGrid, kGrid),
+                                 down = f2pack(-kGrid, -kGrid);
+        uint32_t code[2];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          code[j >> 2] |= to_e2m1x2(quotient(bf16_hi(x[j])), quotient(bf16_lo(x[j]))) << (8 * (j & 3));
+        for (int j = 0; j < 2; ++j) {
+          float q[8];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            f2unpack(add2(fma2(f2pack(bf16_lo(x[4 * j + i]), bf16_hi(x[4 * j + i])), inv2, up), down),
+                     q[2 * i], q[2 * i + 1]);
+          code[j] = to_e2m1x8(q);
+        }
         uint8_t* block = dst + (size_t)h * kv4_block(page, D) + v * (kv4_group(D) / 2);
         *reinterpret_cast<uint2*>(block + place * (D / 2) + c * 8) = make_uint2(code[0], code[1]);
         block[8 * D + place * kBlocks + c] = (uint8_t)sb;

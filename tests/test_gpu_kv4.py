@@ -438,6 +438,32 @@ def test_rounding_errors_of_the_format():
     assert (np.abs(z)[~inside] == (6 * step * np.ones_like(y))[~inside]).all()
 
 
+@pytest.mark.parametrize("e", [0, -20, 33])
+def test_commit_on_the_borders_of_codes_and_scales(e):
+    """Every bf16 magnitude of 25 binades as a block's largest, with the seven borders
+    of its codes and a bf16 neighbour of each beside it: bit by bit what exact
+    arithmetic gives.  (The 25 binades hold all scales, those below 2^-6 and 448 too.)"""
+    a = np.arange(115 << 7, 140 << 7, dtype=np.uint32)  # bf16 bits of 2^-12 .. 2^13
+    largest = (a << 16).view(np.float32).astype(np.float64)
+    _, s = ref.rounded(np.repeat(largest[:, None], 16, 1))
+    borders = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0]) * ref.SCALES[s].reshape(-1, 1)
+    exact = torch.tensor(borders).to(torch.bfloat16)
+    assert (exact.double().numpy() == borders).all()  # (7 bits at most)
+    bits = exact.view(torch.int16).numpy().astype(np.int32)
+    beside = np.maximum(bits + np.where(np.arange(a.size)[:, None] % 2, 1, -1), 0)
+    x = np.concatenate([a[:, None], bits, beside, np.zeros((a.size, 1))], 1).astype(np.int64)
+    x = np.where(x > a[:, None], a[:, None], x)  # (none beyond the largest)
+    x |= np.random.default_rng(5).integers(0, 2, x.shape) << 15
+    x = (x - (x >> 15 << 16)).astype(np.int16).reshape(2, 1, 1, 200, 2, 64)
+    k, v = (torch.from_numpy(y).cuda().view(torch.bfloat16) * 2.0 ** e for y in x)
+    pages, table = sv.alloc_kv4_pages(1, 4, 2, 64, 64), cuda(np.arange(4, dtype=np.int32)[None])
+    exps = cuda(np.full((1, 2), e, np.int32))
+    n = sv.kv4_commit_path(pages, table, k, v, cuda(np.ones(1, np.int32)), kv_exp=exps)
+    for got, y in zip(sv.kv4_read(pages, table, n, 200, 64, kv_exp=exps), (k, v)):
+        want, _ = ref.rounded(host(y), e)
+        assert np.array_equal(host(got), want)
+
+
 def test_commit_of_malformed_sequences():
     """They are left as they were, with the flag of what is wrong; the others are
     written."""
