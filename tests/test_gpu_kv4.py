@@ -522,6 +522,31 @@ def test_read_lengths_pages_and_strides():
     assert (big[:, B] == 7).all() and (big[:, :, L:] == 7).all()
 
 
+@pytest.mark.parametrize("first,gap,D", [(0, 0, 64), (8, 0, 64), (0, 8, 128), (16, 16, 64), (8, 24, 128)])
+def test_read_into_outputs_of_every_alignment(first, gap, D):
+    """Outputs that begin at, and sequences that lie apart by, odd multiples of 16
+    bytes and multiples of 32: one result, and nothing beside it is written."""
+    rng = np.random.default_rng(7)
+    layers, B, page, Hkv, W, L = 2, 3, 16, 3, 2, 27
+    table = rng.permutation(B * W).reshape(B, W).astype(np.int32)
+    raw = np.stack([random_pages(rng, B * W, Hkv, page, D) for _ in range(layers)])
+    row = L * Hkv * D
+    flat = [torch.full((layers * B * (row + gap) + 64,), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    k, v = (x[first:].as_strided((layers, B, L, Hkv, D), (B * (row + gap), row + gap, Hkv * D, D, 1), x[first:].storage_offset())
+            for x in flat)
+    ws = sv.alloc_workspace(sv.SPEC_MODE_KV4, B, 1, 1, sv.SPEC_DTYPE_BF16)
+    sv.spec_kv4_read(cuda(raw), cuda(table), cuda(np.array([L, 5, L - 1], np.int32)), k, v, ws)
+    assert flags_of(ws) == 0
+    for layer in range(layers):
+        for b, n in ((0, L), (1, 5), (2, L - 1)):
+            for got, w in zip((k, v), ref.unpack(raw[layer], table[b], n, page, D)):
+                g = host(got[layer, b])
+                assert np.array_equal(g[:n], w) and (g[n:] == 7).all()
+    for x, y in zip(flat, (k, v)):
+        y.fill_(7.0)
+        assert (x == 7).all()
+
+
 # ---------------------------------------------------------------------------
 # the calls together
 # ---------------------------------------------------------------------------
