@@ -14,7 +14,7 @@
 //
 // Bound: products, 4 N Hq D len operations (2048 clocks a pair of half tiles at
 // D = 128), more than the pages' bytes.  Measured (D = 128, 8 key-value heads):
-// 16 trees of 60 nodes, 32 heads, up to 4096 positions 87-91 us (products 25 us at
+// 16 trees of 60 nodes, 32 heads, up to 4096 positions 87-92 us (products 25 us at
 // the library's rate, the bf16 kernel 69); 3 trees of 33, 40 heads, up to 65536
 // positions 154-165 us (52; bf16 129).  About 4700 clocks a tile, two chains of
 // scores (512), softmax (2050-2400 beside the warps that unpack) and output (512)

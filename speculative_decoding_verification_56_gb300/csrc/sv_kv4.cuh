@@ -17,7 +17,7 @@
 //
 // Commit reads 4 D bytes of an entry's head and writes 9 D / 8, read the other
 // way round.  Measured with 5 prompts of up to 1000 tokens, 8 layers, 8 heads of
-// 128: commit 44 us, read 43 us (6.6 TB/s); commit took 55 with divisions and
+// 128: commit 42-44 us, read 43-46 us (6.3-6.6 TB/s); commit took 55 with divisions and
 // rounding by integers, and both 119 before the lanes of a warp shared an entry.
 #pragma once
 

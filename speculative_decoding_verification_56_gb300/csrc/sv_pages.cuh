@@ -9,7 +9,7 @@
 // carries the copies out over all planes.
 //
 // Bound: the copies, where there are many (compaction of 24 sequences in 32 planes
-// of 64 positions, 993 MB read and written: 144-149 us, 98% of the rate of a plain
+// of 64 positions, 993 MB read and written: 144-152 us, up to 98% of the rate of a plain
 // copy); else the plan's chain of dependent loads.
 #pragma once
 
