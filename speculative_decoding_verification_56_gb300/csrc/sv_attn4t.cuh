@@ -16,7 +16,7 @@
 // D = 128), more than the pages' bytes.  Measured (D = 128, 8 key-value heads):
 // 16 trees of 60 nodes, 32 heads, up to 4096 positions 87-92 us (products 25 us at
 // the library's rate, the bf16 kernel 69); 3 trees of 33, 40 heads, up to 65536
-// positions 154-165 us (52; bf16 129).  About 4700 clocks a tile, two chains of
+// positions 154-184 us (52; bf16 129).  About 4700 clocks a tile, two chains of
 // scores (512), softmax (2050-2400 beside the warps that unpack) and output (512)
 // with their hand-overs; and the hand-over of a place of the ring, 2300 clocks
 // from the products that free it to the products that read it: query and unpacked
@@ -25,7 +25,7 @@
 // converted in place (115 / 222); no per-entry branches, and loops small enough
 // for the instruction caches, which five roles share (96 / 169); the issuing warp
 // as a whole (91); eight warps that unpack instead of four (87, long 173); every
-// tile waited for right before its use (87-90, long 157).
+// tile waited for right before its use (87-92, long 173 -> 157 in turns).
 #pragma once
 
 #include "sv_attn4.cuh"
