@@ -702,7 +702,8 @@ SPEC_API spec_status_t spec_kv_pages_compact(void* pages, int planes, long long 
  * V tokens,
  *   total[b, k, v] = scores[b, k] + z_v / T - ln sum_j exp(z_j / T),
  * z = logits[b, k, :]; a finished beam has the single candidate (eos, its
- * score).  Larger totals first, then lower beams, then lower tokens.
+ * score).  Larger totals first, then lower beams, then lower tokens (logits -0 and
+ * +0 are the same).
  *   logits    [B, K, V] dtype; -inf is a token of probability 0
  *   scores    float [B, K]; -inf (or NaN): the beam has no candidate
  *   finished  int32 [B, K] (not 0: finished) or NULL

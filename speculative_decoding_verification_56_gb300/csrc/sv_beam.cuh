@@ -190,9 +190,10 @@ __device__ __forceinline__ double beam_unkey(unsigned long long k) {
   return __longlong_as_double((long long)((k >> 63) ? (k & 0x7FFFFFFFFFFFFFFFull) : ~k));
 }
 
-// Warp argmax over lanes of (v, i), lower i first; the winner to every lane.
+// Warp argmax over lanes of (v, i), lower i first; the winner to every lane.  (-0
+// becomes +0: keys are equal exactly where floats are, as the other compares here.)
 __device__ __forceinline__ void beam_warp_best(float& v, int& i) {
-  const unsigned key = grow_fkey(v);
+  const unsigned key = grow_fkey(v == 0.0f ? 0.0f : v);
   const unsigned top = __reduce_max_sync(0xffffffffu, key);
   i = (int)__reduce_min_sync(0xffffffffu, key == top ? (unsigned)i : 0x7FFFFFFFu);
   v = grow_funkey(top);
