@@ -13,6 +13,7 @@
 // copy); else the plan's chain of dependent loads.
 #pragma once
 
+#include "spec_verify.h"
 #include "sv_kv4.cuh"
 
 namespace sv {
@@ -89,6 +90,18 @@ __device__ __forceinline__ void pg_hold(const PagesParams& p, int id) {
 __device__ __forceinline__ bool pg_held(const PagesParams& p, int id) {
   return (__ldcg(p.bits + (id >> 5)) >> (id & 31)) & 1;
 }
+// What the sequences want in all may be more than 2^31 pages (2^20 sequences of 2^20);
+// that more than the pool's pages are wanted is all that counts then.  So the sum of
+// the turns before, of kPgThreads sequences each, stops at kPgMany, above any pool,
+// and the place of a sequence's page (the turns before, at most a turn's pages before
+// it, its own) stays below 2^31.
+constexpr int kPgMany = 2 * SPEC_KV_MAX_PAGES;
+static_assert((long long)kPgMany + (long long)kPgThreads * SPEC_KV_MAX_TABLE + SPEC_KV_MAX_TABLE <= 0x7FFFFFFF,
+              "places of fresh pages fit 32 bits");
+__host__ __device__ constexpr int pg_many(int before, int sum) {
+  return before + sum < kPgMany ? before + sum : kPgMany;
+}
+
 // bits of word w that stand for pages
 __device__ __forceinline__ uint32_t pg_valid(const PagesParams& p, int w) {
   const int left = p.n_pages - 32 * w;
@@ -210,7 +223,7 @@ __global__ void __launch_bounds__(kPgThreads) pages_fork_kernel(const PagesParam
     const int x = j < p.B2 ? __ldcg(p.off + j) : 0;
     int sum;
     const int before = nfresh + pg_scan(x >> 1, &sum, s_warp);
-    nfresh += sum;
+    nfresh = pg_many(nfresh, sum);
     s_before[threadIdx.x] = before;
     s_keep[threadIdx.x] = x & 1;
     __syncthreads();
