@@ -754,17 +754,19 @@ SPEC_API uint64_t spec_verify_launch_count(void);
  * Every wait of the verification kernels on their own bulk copies, and every
  * wait between the roles of a CTA of spec_tree_attention and of
  * spec_tree_attention_kv4 (copies, products, softmax), gives up after a limit
- * (0.2 s by default): the CTA then sets
- * SPEC_FLAG_TIMEOUT, stops copying, waits (with the default limit) for the
- * copies and products it has in flight and finishes its control flow, so the
- * call completes with unspecified outputs and the flag raised instead of
- * hanging.  This sets the limit used by calls of spec_verify_sample,
- * spec_verify_greedy, spec_verify_tree_greedy, spec_verify_greedy_noalloc,
- * spec_tree_attention and spec_tree_attention_kv4 enqueued afterwards, process-wide; limit_ns = 0 restores
- * the default.  limit_ns = 1 gives up whenever a copy has not landed (a role
- * has not answered) at the first look, which is how a test exercises that path
- * (other limits below a microsecond are rounded up by the resolution of the
- * GPU's global timer).  Not for production use.
+ * (0.2 s by default; the one role that lists a CTA's work ahead may wait 20 us
+ * longer for each tile of it): the CTA then sets SPEC_FLAG_TIMEOUT, stops
+ * copying, waits (with the default limit) for the copies and products it has
+ * in flight and finishes its control flow, so the call completes with
+ * unspecified outputs and the flag raised instead of hanging.  This sets the
+ * limit used by calls of spec_verify_sample, spec_verify_greedy,
+ * spec_verify_tree_greedy, spec_verify_greedy_noalloc, spec_tree_attention and
+ * spec_tree_attention_kv4 enqueued afterwards, process-wide; limit_ns = 0
+ * restores the default.  limit_ns = 1 gives up whenever a copy has not landed
+ * (a role has not answered) at the first look, which is how a test exercises
+ * that path.  Between two looks at the GPU's clock a wait sleeps for about 4 us
+ * at least (shorter limits are rounded up) and 1 ms at most.  Not for
+ * production use.
  */
 SPEC_API void spec_verify_set_wait_limit_ns(uint64_t limit_ns);
 

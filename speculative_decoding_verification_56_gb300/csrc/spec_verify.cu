@@ -1779,10 +1779,7 @@ spec_status_t spec_tree_attention_kv4(const void* q, const void* pages, long lon
     t.span = reinterpret_cast<int2*>(ws + kDataOffset);
     t.ml = reinterpret_cast<float2*>(ws + plan.t.off_ml);
     t.opart = reinterpret_cast<float*>(ws + plan.t.off_part);
-    const uint64_t limit = g_wait_limit_ns.load(std::memory_order_relaxed);
-    t.sleep_ns = (unsigned)std::min<uint64_t>(limit, sv::kSuspendHintNs);
-    t.polls = limit > 1 ? 128 : 1;
-    t.tries = limit > 1 ? (int)std::min<uint64_t>(limit / 10000 + 1, 1000000) : 1;
+    sv::atq_limit(&t, g_wait_limit_ns.load(std::memory_order_relaxed));
     t.pages = static_cast<const uint8_t*>(pages);
     t.table = page_table;
     {

@@ -14,7 +14,7 @@
 //
 // Bound: products, 4 N Hq D len operations (2048 clocks a pair of half tiles at
 // D = 128), more than the pages' bytes.  Measured (D = 128, 8 key-value heads):
-// 16 trees of 60 nodes, 32 heads, up to 4096 positions 87-92 us (products 25 us at
+// 16 trees of 60 nodes, 32 heads, up to 4096 positions 87-91 us (products 25 us at
 // the library's rate, the bf16 kernel 69); 3 trees of 33, 40 heads, up to 65536
 // positions 154-184 us (52; bf16 129).  About 4700 clocks a tile, two chains of
 // scores (512), softmax (2050-2400 beside the warps that unpack) and output (512)
@@ -56,9 +56,16 @@ struct AttnQParams : AttnParams {
   const int32_t* exps;   // [2] or null
   long long n_pages;
   int Wt, lg;            // the table's width; log2 of the page size
-  int tries, polls;      // a wait is given up after tries x polls tests, each a sleep of up to
-  unsigned sleep_ns;     // this (of which the hardware takes some hundred ns)
+  unsigned sleep_ns;     // longest sleep of one test of a wait
 };
+
+// The limit of the waits between the roles.  A wait ends at most one test behind it,
+// so a test sleeps an eighth of it at most (3.9 us, measured, whatever it is told).
+__host__ inline void atq_limit(AttnQParams* p, uint64_t limit_ns) {
+  const uint64_t eighth = limit_ns / 8;
+  p->wait_ns = limit_ns < (1ull << 62) ? limit_ns : 1ull << 62;
+  p->sleep_ns = (unsigned)(eighth < 1 ? 1 : eighth < kSuspendHintNs ? eighth : kSuspendHintNs);
+}
 
 // Put i of a segment of n tiles into the ring, in the order of use: pairs K0 V0
 // K1 V1 .., else K0 K1 V0 K2 V1 K3 .. (see the softmax's k_use and v_use).
@@ -82,29 +89,34 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(one));
   return one != 0;
 }
-// Waits between the roles: a number of tries that sleep in the instruction until
-// the phase completes, so that a wait is a few instructions (what the roles
-// share here is the instruction caches, see below).
+// Waits between the roles: tests that sleep in the instruction until the phase
+// completes, and after each a look at whether another role has given up and at the
+// clock (a wait is a few instructions, since what the roles share here is the
+// instruction caches, see below).  end: when the wait is given up, set at the first
+// look; a limit of 1 ns gives up there.
+__device__ __forceinline__ bool atq_late(const AttnQParams& p, uint64_t& end, uint64_t more_ns) {
+  const uint64_t now = global_ns();
+  if (end == 0) end = now + p.wait_ns - 1 + more_ns;
+  return now >= end;
+}
 __device__ __forceinline__ bool atq_wait(const AttnQParams& p, uint64_t* bar, unsigned parity,
-                                         const int* abort, int more = 0) {
+                                         const int* abort, uint64_t more_ns = 0) {
+  uint64_t end = 0;
 #pragma unroll 1
-  for (int i = p.tries + more; i > 0; --i) {
-#pragma unroll 1
-    for (int j = p.polls; j > 0; --j)
-      if (mbar_try_wait(bar, parity, p.sleep_ns)) return true;
-    if (*(const volatile int*)abort) break;
+  for (unsigned i = 1u << 30; i > 0; --i) {
+    if (mbar_try_wait(bar, parity, p.sleep_ns)) return true;
+    if (*(const volatile int*)abort || atq_late(p, end, more_ns)) break;
   }
   return false;
 }
 // the same for a whole warp, with one answer
 __device__ __forceinline__ bool atq_wait_warp(const AttnQParams& p, uint64_t* bar, unsigned parity,
                                               const int* abort) {
+  uint64_t end = 0;
 #pragma unroll 1
-  for (int i = p.tries; i > 0; --i) {
-#pragma unroll 1
-    for (int j = p.polls; j > 0; --j)
-      if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity, p.sleep_ns))) return true;
-    if (__any_sync(0xffffffffu, *(const volatile int*)abort)) break;
+  for (unsigned i = 1u << 30; i > 0; --i) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity, p.sleep_ns))) return true;
+    if (__any_sync(0xffffffffu, *(const volatile int*)abort || atq_late(p, end, 0))) break;
   }
   return false;
 }
@@ -262,7 +274,7 @@ __global__ void __launch_bounds__(kAtqThreads, 1)
           // (the only wait that lasts as long as an item: until the one four before
           // this is begun, so up to the run's length)
           if (!atq_wait(p, &seg_empty[at], ((k / kAtSegs) & 1) ^ 1u, abort,
-                        (int)min(hi - lo, 1000000ll))) {
+                        (uint64_t)(hi - lo) * kAtTileNs)) {
             fail();
             break;
           }
