@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(kKv4Threads) kv4_commit_kernel(const Kv4Params
   const int count = kv4_commit_count(p, b);
   const int base = p.base_len[b];
   if (layer == 0 && part == 0 && threadIdx.x == 0)
-    p.new_len[b] = count ? base - 1 + count : max(base - 1, 0);
+    p.new_len[b] = count ? base - 1 + count : max(base, 1) - 1;
   const int blocks = p.Hkv * kBlocks, page = 1 << p.lg;
   const int e[2] = {kv4_exp(p.exps, 2 * layer), kv4_exp(p.exps, 2 * layer + 1)};
   const Kv4Lanes w(p, part);
