@@ -624,7 +624,7 @@ SPEC_API spec_status_t spec_kv4_read(const void* pages, int layers, long long n_
  * Queries and weights are rounded to fp16 (queries at a power of two that
  * brings a head's largest element to 2^14, weights at 2^7: both have at least
  * bf16's 8 bits down to 2^-24 of the largest), the cached values are exact in
- * fp16, sums are float32.  out must not overlap q, node_k or node_v
+ * fp16, sums are float32.  out and lse must not overlap the inputs
  * (SPEC_ERR_INVALID_ARG).  Limits as spec_tree_attention (D 64 or 128, G at most
  * 128, N at most SPEC_ATTN_MAX_NODES); W * page_size + N at most 2^31 - 257.  Two
  * launches; the cut of the work, and so the last bits, depend on base_len and
@@ -717,8 +717,8 @@ SPEC_API spec_status_t spec_kv_pages_compact(void* pages, int planes, long long 
  * Totals are ordered in float64 from float32 exponentials: they are off by less
  * than 2^-19 (1 + |z_v / T|); within a beam the order is that of the logits,
  * and beams with the same logits and scores tie.  A logit that is NaN or +inf
- * makes what its request gets unspecified.  Outputs must not overlap scores or
- * finished (SPEC_ERR_INVALID_ARG).
+ * makes what its request gets unspecified.  Outputs must not overlap the inputs
+ * (SPEC_ERR_INVALID_ARG).
  * Two launches.  Workspace: spec_beam_select_workspace_bytes() bytes.
  */
 SPEC_API size_t spec_beam_select_workspace_bytes(int B, int K, int V, int M, int dtype);

@@ -1640,10 +1640,11 @@ spec_status_t spec_kv4_commit_path(void* pages, int layers, long long n_pages, i
   if (!workspace || workspace_bytes < kHeaderBytes) return SPEC_ERR_WORKSPACE;
   if (!aligned(workspace, kAlign)) return SPEC_ERR_ALIGNMENT;
   // (many CTAs read a sequence's inputs, one writes its new length)
-  const size_t seqs = 4 * (size_t)B;
+  const size_t seqs = 4 * (size_t)B, nodes = 2 * (size_t)layers * B * N * Hkv * D;
   if (overlap(new_len, seqs, base_len, seqs) || overlap(new_len, seqs, accepted_len, seqs) ||
       overlap(new_len, seqs, path_nodes, path_nodes ? seqs * (max_depth + 1) : 0) ||
-      overlap(new_len, seqs, page_table, seqs * W))
+      overlap(new_len, seqs, page_table, seqs * W) || overlap(new_len, seqs, kv_exp, 8 * (size_t)layers) ||
+      overlap(new_len, seqs, node_k, nodes) || overlap(new_len, seqs, node_v, nodes))
     return SPEC_ERR_INVALID_ARG;
   sv::Kv4Params prm;
   std::memset(&prm, 0, sizeof prm);
@@ -1742,10 +1743,16 @@ spec_status_t spec_tree_attention_kv4(const void* q, const void* pages, long lon
   if (!aligned(workspace, kAlign)) return SPEC_ERR_ALIGNMENT;
   const Attn4Plan plan = attn4_plan(B, N, Hq, Hkv, D);
   if (workspace_bytes < plan.bytes) return SPEC_ERR_WORKSPACE;
-  const size_t heads = 2 * (size_t)B * N * D;  // bytes of a head of all nodes
-  if (overlap(out, heads * Hq, q, heads * Hq) || overlap(out, heads * Hq, node_k, heads * Hkv) ||
-      overlap(out, heads * Hq, node_v, heads * Hkv))
-    return SPEC_ERR_INVALID_ARG;
+  // (CTAs that share a sequence's or a node's inputs write their outputs at different times)
+  const size_t rows = (size_t)B * N, heads = 2 * rows * D;  // heads: bytes of a head of all nodes
+  const std::pair<const void*, size_t> outs[] = {{out, heads * Hq}, {lse, 4 * rows * Hq}};
+  const std::pair<const void*, size_t> ins[] = {
+      {q, heads * Hq}, {node_k, heads * Hkv}, {node_v, heads * Hkv},
+      {pages, (size_t)n_pages * Hkv * sv::kv4_block(page_size, D)}, {page_table, 4 * (size_t)B * W},
+      {mask, 4 * rows * ((N + 31) / 32)}, {base_len, 4 * (size_t)B}, {kv_exp, 8}};
+  for (const auto& o : outs)
+    for (const auto& i : ins)
+      if (overlap(o.first, o.second, i.first, i.second)) return SPEC_ERR_INVALID_ARG;
   int sms = 0;
   const spec_status_t st = sm_count(&sms);
   if (st != SPEC_OK) return st;
@@ -1914,7 +1921,9 @@ spec_status_t spec_beam_select(const void* logits, int dtype, const float* score
   const size_t in = 4 * (size_t)B * K, picked = 4 * (size_t)B * M;
   for (const void* o : {(const void*)out_scores, (const void*)out_parents, (const void*)out_tokens,
                         (const void*)out_finished})
-    if (overlap(o, picked, scores, in) || overlap(o, picked, finished, in)) return SPEC_ERR_INVALID_ARG;
+    if (overlap(o, picked, scores, in) || overlap(o, picked, finished, in) ||
+        overlap(o, picked, logits, (size_t)B * K * V * elem_bytes(dtype)))
+      return SPEC_ERR_INVALID_ARG;
   char* ws = static_cast<char*>(workspace);
   sv::BeamParams prm;
   std::memset(&prm, 0, sizeof prm);
