@@ -610,8 +610,11 @@ SPEC_API spec_status_t spec_kv4_read(const void* pages, int layers, long long n_
  *     whose keys and values are still bf16.
  *   q, out          bf16 [B, N, Hq, D];  lse float [B, N, Hq] or NULL
  *   pages           uint8 [n_pages, Hkv, block] (one layer, see above)
- *   node_k, node_v  bf16 [B, N, Hkv, D]; magnitudes beyond 65504 * 2^e count as
- *                   that (the cache itself holds up to 2688 * 2^e)
+ *   node_k, node_v  bf16 [B, N, Hkv, D], taken as fp16 in units of 2^e (kv_exp's of
+ *                   keys, of values): exact from 2^-17 * 2^e to 65504 * 2^e,
+ *                   larger magnitudes count as that, smaller ones are rounded
+ *                   to multiples of 2^-24 * 2^e (the cache itself holds up to
+ *                   2688 * 2^e, in steps of 2^-10 * 2^e at least)
  *   mask, base_len, scale  as spec_tree_attention;  kv_exp int32 [2] or NULL
  * N = 1 without a mask is plain decoding.  A node that sees nothing gets out = 0
  * and lse = -inf.  Entries that a node does not see are never used, whatever
