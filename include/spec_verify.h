@@ -707,7 +707,8 @@ SPEC_API spec_status_t spec_kv_pages_compact(void* pages, int planes, long long 
  * z = logits[b, k, :]; a finished beam has the single candidate (eos, its
  * score).  Larger totals first, then lower beams, then lower tokens (logits -0 and
  * +0 are the same).
- *   logits    [B, K, V] dtype; -inf is a token of probability 0
+ *   logits    [B, K, V] dtype, of any magnitude; -inf is a token of probability 0
+ *             (a row of the type's lowest value alone is a flat one)
  *   scores    float [B, K]; -inf (or NaN): the beam has no candidate
  *   finished  int32 [B, K] (not 0: finished) or NULL
  *   eos       the token that ends a beam, or -1

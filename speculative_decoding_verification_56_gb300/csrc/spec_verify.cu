@@ -1937,7 +1937,8 @@ spec_status_t spec_beam_select(const void* logits, int dtype, const float* score
   prm.out_token = out_tokens;
   prm.out_finished = out_finished;
   prm.flags = reinterpret_cast<unsigned*>(ws);
-  prm.scale = (float)(1.4426950408889634 / (double)temperature);
+  // (finite, so that 0 times it is 0: temperatures below 2^-127 count as that)
+  prm.scale = (float)std::min(1.4426950408889634 / (double)temperature, 3.4028234663852886e38);
   prm.B = B;
   prm.K = K;
   prm.V = V;

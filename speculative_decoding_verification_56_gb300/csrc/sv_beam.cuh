@@ -54,6 +54,16 @@ struct BeamParams {
   int B, K, V, M, eos, nchunks, items;
 };
 
+// A warp's sum of 2^(z scale) relative to its reference, the next whole number from
+// its largest logit m's power on.  Beyond 2^30 there are no such numbers, and powers of
+// two float logits are 64 or more apart (2^30 2^-24): the sum is then the number of
+// logits equal to m, relative to m itself, and the reference says so.
+constexpr float kBeamFar = 1073741824.0f;
+constexpr int kBeamFarRef = 0x7FFFFFFF;
+__device__ __forceinline__ bool beam_far(float m, float scale) {
+  return !(fabsf(ceilf(m * scale)) < kBeamFar);
+}
+
 // A chunk's records, from its logits in registers.
 template <typename E>
 __device__ __forceinline__ void beam_chunk(const BeamParams& p, const uint4 (&raw)[kVecPerThread],
@@ -63,27 +73,41 @@ __device__ __forceinline__ void beam_chunk(const BeamParams& p, const uint4 (&ra
 #pragma unroll
   for (int q = 0; q < kVecPerThread; ++q)
     top[q] = grow_funkey(__reduce_max_sync(0xffffffffu, grow_fkey(grow_vec_max<E>(raw[q]))));
-  const int ref = exp_ref(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), p.scale);
-  const unsigned long long s2 = f2pack(p.scale, p.scale);
-  const unsigned long long n2 = f2pack(-(float)ref, -(float)ref);
-  constexpr int kP = E::kEPV / 2;
-  unsigned long long sum[2] = {0, 0};
+  const float m = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+  int bits = kRefEmpty;
+  float total = 0.0f;
+  if (!beam_far(m, p.scale)) {
+    const float ref = ceilf(m * p.scale);
+    const unsigned long long s2 = f2pack(p.scale, p.scale);
+    const unsigned long long n2 = f2pack(-ref, -ref);
+    constexpr int kP = E::kEPV / 2;
+    unsigned long long sum[2] = {0, 0};
 #pragma unroll
-  for (int q = 0; q < kVecPerThread; ++q) {
-    unsigned long long pr[kP];
-    vec_pairs<E>(raw[q], pr);
+    for (int q = 0; q < kVecPerThread; ++q) {
+      unsigned long long pr[kP];
+      vec_pairs<E>(raw[q], pr);
 #pragma unroll
-    for (int h = 0; h < kP; ++h) {
-      float x0, x1;
-      f2unpack(fma2(pr[h], s2, n2), x0, x1);
-      sum[h & 1] = add2(sum[h & 1], f2pack(ex2(x0), ex2(x1)));
+      for (int h = 0; h < kP; ++h) {
+        float x0, x1;
+        f2unpack(fma2(pr[h], s2, n2), x0, x1);
+        sum[h & 1] = add2(sum[h & 1], f2pack(ex2(x0), ex2(x1)));
+      }
     }
+    float a0, a1;
+    f2unpack(add2(sum[0], sum[1]), a0, a1);
+    total = warp_sum_f(a0 + a1);
+    bits = (int)ref;
+  } else if (m > -INFINITY) {
+    int n = 0;
+#pragma unroll
+    for (int q = 0; q < kVecPerThread; ++q)
+#pragma unroll
+      for (int e = 0; e < E::kEPV; ++e) n += E::elem(raw[q], e) == m ? 1 : 0;
+    total = (float)__reduce_add_sync(0xffffffffu, n);
+    bits = kBeamFarRef;
   }
-  float a0, a1;
-  f2unpack(add2(sum[0], sum[1]), a0, a1);
-  const float total = warp_sum_f(a0 + a1);
   if (lane == 0) {
-    p.part[(size_t)item * kWarps + warp] = make_float2(__int_as_float(ref), total);
+    p.part[(size_t)item * kWarps + warp] = make_float2(__int_as_float(bits), total);
     float* run = p.runs + (size_t)item * kBeamRuns + warp;  // (their order is the tokens')
 #pragma unroll
     for (int q = 0; q < kVecPerThread; ++q) run[q * kWarps] = top[q];
@@ -286,15 +310,38 @@ __global__ void __launch_bounds__(kBeamThreads) beam_select_kernel(const BeamPar
     const float2* part = p.part + row * C * kWarps;
     int lref = kRefEmpty;
     FSum acc = FSum::zero();
+    bool some_far = false;
 #pragma unroll 4
     for (int i = lane; i < C * kWarps; i += 32) {
       const float2 x = __ldcg(part + i);
       const int ref = __float_as_int(x.x);
+      if (ref == kBeamFarRef) {  // 2^-64 and less of the others' sums, unless it is the row's largest
+        some_far = true;
+        continue;
+      }
       if (ref > lref) {
         acc.scale(pow2i_f(lref - ref));
         lref = ref;
       }
       acc.add(x.y * pow2i_f(ref - lref));
+    }
+    float top = 0.0f;  // what the sum is relative to, besides its reference: 0 or the row's largest logit
+    if (__any_sync(0xffffffffu, some_far)) {
+      float m = -INFINITY;
+      for (int r = lane; r < nruns; r += 32) m = fmaxf(m, __ldcg(gruns + r));
+      m = grow_funkey(__reduce_max_sync(0xffffffffu, grow_fkey(m)));
+      if (beam_far(m, p.scale)) {
+        top = m;
+        lref = 0;
+        acc = FSum::zero();
+        for (int i = lane; i < C * kWarps; i += 32) {  // the warps whose largest it is
+          const float* run = gruns + i / kWarps * kBeamRuns + i % kWarps;
+          float w = -INFINITY;
+#pragma unroll
+          for (int q = 0; q < kVecPerThread; ++q) w = fmaxf(w, __ldcg(run + q * kWarps));
+          if (w == top) acc.add(__ldcg(part + i).y);
+        }
+      }
     }
     // this lane's best run that is left
     float rv = -INFINITY;
@@ -434,7 +481,7 @@ __global__ void __launch_bounds__(kBeamThreads) beam_select_kernel(const BeamPar
     const double ln2 = 0.6931471805599453;
     const double lse = rint(beam_ln(S, R) * 4294967296.0) * (1.0 / 4294967296.0);
     if (lane < M) {
-      const double x = (double)score + ((double)best.v * (double)p.scale * ln2 - lse);
+      const double x = (double)score + (((double)best.v - (double)top) * (double)p.scale * ln2 - lse);
       tot[lane] = grow_key(best.i < p.V && x > -INFINITY ? x : -INFINITY);
       tok[lane] = best.i;
     }

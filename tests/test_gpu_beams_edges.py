@@ -1,4 +1,5 @@
-"""Beam selection on the GPU where logits tie: zeros of both signs."""
+"""Beam selection on the GPU where logits tie (zeros of both signs), and where they lie
+far from zero or from one another."""
 import numpy as np
 import pytest
 import torch
@@ -65,3 +66,95 @@ def test_beams_whose_zeros_differ_in_sign_tie(dtype):
     z[0, 1, ::2] = -0.0
     parents, tokens = select(z, 16, dtype)
     assert (parents == 0).all() and tokens[0].tolist() == list(range(16))
+
+
+def check(z, scores, M, dtype, T=1.0, finished=None, eos=-1):
+    """Every place against totals in 64 bits, whatever lies close together: within a
+    beam exactly its largest logits, lower tokens first; a place's score is its
+    candidate's total to 2^-18 + 2^-24 of what its logit lies below the row's largest
+    (over T) and half a step of float32; no place and no candidate left out has a
+    total that is smaller (larger) than a later place's (the last one's) by more."""
+    z = torch.from_numpy(z.astype(np.float32)).to(torch.bfloat16 if dtype == "bf16" else torch.float32).cuda()
+    B, K, V = z.shape
+    got = {n: x.cpu().numpy() for n, x in sv.beam_select(
+        z, cuda(scores.astype(np.float32)), M, None if finished is None else cuda(finished.astype(np.int32)), eos, T).items()}
+    z, T = z.double().cpu().numpy(), float(np.float32(T))
+    scores = scores.astype(np.float32).astype(np.float64)
+    for b in range(B):
+        rows = []  # of each beam: its candidates in order, as (total, token, bound)
+        for k in range(K):
+            if not scores[b, k] > -np.inf:
+                rows.append([])
+            elif finished is not None and finished[b, k]:
+                rows.append([(scores[b, k], eos, 0.0)])
+            else:
+                top = z[b, k].max()
+                if top == -np.inf:
+                    rows.append([])
+                    continue
+                y = (z[b, k] - top) / T
+                total = scores[b, k] + (y - np.log(np.exp(y).sum()))
+                order = np.lexsort((np.arange(V), -z[b, k]))[: M + 1]
+                rows.append([(total[i], int(i), 2.0 ** -18 + 2.0 ** -24 * -y[i]) for i in order if z[b, k, i] > -np.inf])
+        n = min(M, sum(len(r) for r in rows))
+        assert (got["parents"][b, n:] == -1).all() and (got["tokens"][b, n:] == -1).all()
+        assert (got["scores"][b, n:] == -np.inf).all() and (got["finished"][b, n:] == 1).all()
+        at, places = [0] * K, []
+        for i in range(n):
+            k = int(got["parents"][b, i]) - b * K
+            assert 0 <= k < K and at[k] < len(rows[k]), (b, i, k)
+            total, token, bound = rows[k][at[k]]
+            at[k] += 1
+            assert got["tokens"][b, i] == token, (b, i, k)
+            with np.errstate(over="ignore"):
+                want = np.float32(total)
+            off = abs(float(got["scores"][b, i]) - total)
+            assert got["scores"][b, i] == want or off <= bound + 2.0 ** -24 * abs(total), (b, i, off, bound)
+            done = finished is not None and finished[b, k]
+            assert got["finished"][b, i] == int(bool(done) or token == eos)
+            places.append((total, bound))
+        left = [r[a] for r, a in zip(rows, at) if a < len(r)]
+        for (x, bx), (y, by) in zip(places, places[1:]):
+            assert x + bx >= y - by
+        for y, _, by in left:
+            assert places[-1][0] + places[-1][1] >= y - by, b
+    return got
+
+
+@pytest.mark.parametrize("V", [1000, 1003, 40000])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_logits_far_from_zero(V, dtype):
+    """Rows masked with the type's lowest value, in all places or in most, and rows of
+    huge logits of either sign: totals are relative to the row's largest logit."""
+    rng = np.random.default_rng(V)
+    low = torch.finfo(torch.bfloat16 if dtype == "bf16" else torch.float32).min
+    z = rng.standard_normal((9, 3, V)) * 2
+    z[0, 1] = low                                  # a beam whose every token is masked
+    z[1] = low                                     # all beams
+    z[2, :, 5:] = low                              # five tokens left
+    z[3, 0] = -1e30
+    z[3, 1, : V // 2] = -1e38                      # chunks of other maxima, all far below
+    z[3, 1, V // 2:] = -1e31
+    z[4, 0] = 1e30
+    z[4, 1, ::3] = 1e35
+    z[5, 2] = np.where(rng.random(V) < 0.01, 3e38, -3e38)
+    z[6] *= 1e9
+    z[7] = z[7] * 1e8 - 3e9
+    z[8, 0, : V - 1] = -np.inf                     # one token a beam, huge
+    z[8, 0, V - 1] = -1e33
+    scores = -rng.random((9, 3)) * 10
+    for M in (1, 4, 16):
+        check(z, scores, M, dtype)
+        check(z, scores, M, dtype, T=0.3)
+
+
+@pytest.mark.parametrize("T", [1e-3, 1e-6, 1e-9, 1e-20, 1e-38, 1e6, 1e30])
+def test_temperatures_far_from_one(T):
+    rng = np.random.default_rng(4)
+    z = rng.standard_normal((3, 4, 5000)) * 3
+    z[1, 2] = 0.0
+    z[2, 1, 100:200] = z[2, 1].max() + 1
+    for dtype in ("bf16", "f32"):
+        check(z, -rng.random((3, 4)) * 5, 8, dtype, T=T)
+        check(z * min(T * 1e9, 1e30), -rng.random((3, 4)) * 5, 8, dtype, T=T)  # (about 2^30 of it)
+        check(z * min(T, 1e30), -rng.random((3, 4)) * 5, 8, dtype, T=T)
