@@ -719,10 +719,11 @@ SPEC_API spec_status_t spec_kv_pages_compact(void* pages, int planes, long long 
  * parent was finished, or the token is eos).  Places without a candidate:
  * -inf, -1, -1, 1.
  * Totals are ordered in float64 from float32 exponentials: they are off by less
- * than 2^-19 (1 + |z_v / T|); within a beam the order is that of the logits,
- * and beams with the same logits and scores tie.  A logit that is NaN or +inf
- * makes what its request gets unspecified.  Outputs must not overlap the inputs
- * (SPEC_ERR_INVALID_ARG).
+ * than 2^-18 + 2^-24 (z_max - z_v) / T, z_max the row's largest logit (and
+ * out_scores rounds them to float); within a beam the order is that of the
+ * logits, and beams with the same logits and scores tie.  A logit that is NaN
+ * or +inf makes what its request gets unspecified.  Outputs must not overlap
+ * the inputs (SPEC_ERR_INVALID_ARG).
  * Two launches.  Workspace: spec_beam_select_workspace_bytes() bytes.
  */
 SPEC_API size_t spec_beam_select_workspace_bytes(int B, int K, int V, int M, int dtype);

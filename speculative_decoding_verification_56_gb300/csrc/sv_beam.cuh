@@ -24,7 +24,12 @@
 //
 // Totals are float64.  A row's ln sum is rounded to 2^-32, and its sum depends
 // on its logits alone (references and order are the chunks' own), so equal rows
-// have equal totals.
+// have equal totals.  What a total is off by: of the sum, the exponents' rounding
+// 2^-24 of themselves (27 ln 2 on the weights' average, the entropy of 2^26 tokens),
+// the exponential 2^-22, 15 additions in float32 2^-24 each; and the scale's rounding,
+// 2^-24 of what z_v / T lies from the weights' average, itself within ln V <= 18 of
+// the largest: 2^-24 (18.7 + 4 + 15 + 18) < 2^-18, and 2^-24 of the distance from
+// the largest.
 #pragma once
 
 #include "sv_grow.cuh"

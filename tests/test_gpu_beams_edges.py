@@ -158,3 +158,36 @@ def test_temperatures_far_from_one(T):
         check(z, -rng.random((3, 4)) * 5, 8, dtype, T=T)
         check(z * min(T * 1e9, 1e30), -rng.random((3, 4)) * 5, 8, dtype, T=T)  # (about 2^30 of it)
         check(z * min(T, 1e30), -rng.random((3, 4)) * 5, 8, dtype, T=T)
+
+
+@pytest.mark.parametrize("T", [1.0, 0.9, 0.7, 1.3])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_totals_of_candidates_far_below_the_largest(T, dtype):
+    """Rows of few tokens with 10 to 1000 between them, so that the places go far
+    down; and peaked, flat and long rows."""
+    rng = np.random.default_rng(int(10 * T))
+    z = np.full((8, 3, 3000), -np.inf)
+    for b in range(4):
+        n = 6
+        z[b, :, rng.choice(3000, n, replace=False)] = rng.random((n, 3)) * 10.0 ** b
+    z[4] = rng.standard_normal((3, 3000)) * 30
+    z[5] = rng.standard_normal((3, 3000)) * 0.01
+    z[6] = np.log(rng.random((3, 3000)))
+    z[7, :, :16] = -np.arange(16) * 100.0 * T + np.array([[0.0], [1.0], [500.0]])
+    for M in (3, 16):
+        check(z, -rng.random((8, 3)) * 3, M, dtype, T=T)
+    check(rng.standard_normal((2, 2, 151936)) * 3, -rng.random((2, 2)), 16, dtype, T=T)
+
+
+@pytest.mark.parametrize("V", [500, 4099, 128256])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_every_place_holds_the_candidate_it_names(V, dtype):
+    """Many close totals: parents and tokens are checked against their own totals,
+    with finished beams, beams without a score, and an end token."""
+    rng = np.random.default_rng(V)
+    z = rng.standard_normal((4, 8, V))
+    scores = -rng.random((4, 8)) * 0.5
+    scores[1, 3] = -np.inf
+    finished = rng.random((4, 8)) < 0.25
+    for T in (1.0, 0.6):
+        check(z, scores, 16, dtype, T=T, finished=finished, eos=min(7, V - 1))
