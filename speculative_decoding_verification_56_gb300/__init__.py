@@ -1192,7 +1192,8 @@ def tree_attention_kv4(q, pages, page_table, node_k, node_v, mask, base_len, sca
 
 def alloc_kv_pages_workspace(pages, rows: int, W: int = 1):
     """Workspace of :func:`spec_kv_pages_fork` and :func:`spec_kv_pages_compact`
-    for tables of up to ``rows`` sequences (of any width)."""
+    for tables of up to ``rows`` sequences of any width (``W``, so that a table's
+    shape can be passed, is not looked at)."""
     return _alloc_flagged(spec_kv_pages_workspace_bytes(pages.shape[1], rows), pages.device)
 
 

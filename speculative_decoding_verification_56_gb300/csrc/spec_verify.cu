@@ -693,6 +693,7 @@ struct Attn4Plan {
 // D = 128, 8 rows 72 us against 186, 16 rows 113 / 187, 24 rows 146 / 190; D = 64,
 // 52 / 158, 86 / 157, 104 / 158; 2 sequences of 22000, D = 128, 24 rows 48 / 58.
 constexpr int kA4MaxRows = 24;
+static_assert(kA4MaxRows <= 16 * sv::kA4Warps, "an item's nodes are its first unit's");
 
 Attn4Plan attn4_plan(int B, int N, int Hq, int Hkv, int D) {
   Attn4Plan a;

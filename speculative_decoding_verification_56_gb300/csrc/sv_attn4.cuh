@@ -25,7 +25,7 @@
 //
 // Bound: instructions, about 700 for a warp's 32 positions at D = 128 (unpacking,
 // scaling and products).  Measured: decoding 64 sequences of up to 4096 positions,
-// 32 heads of 8, 70-72 us where the packed bytes (229 MB) take 34 at the copy rate
+// 32 heads of 8, 69-72 us where the packed bytes (229 MB) take 34 at the copy rate
 // and the bf16 cache takes its kernel 134; 16 positions a step 104 us, 32 with more
 // registers 77.  One chain of 5 over 300 positions: 10.6 us of kernels.
 #pragma once
@@ -71,12 +71,11 @@ struct Attn4Params {
 __device__ __forceinline__ int attn4_len(const Attn4Params& p, int base) {
   return base >= 1 && (long long)base - 1 <= ((long long)p.W << p.lg) ? base - 1 : -1;
 }
-// Units of work of an item: the first tiles of nodes alone, the last of them
-// together with the first tile of committed positions, the other tiles.
-__device__ __forceinline__ int attn4_node_tiles(const Attn4Params& p) { return (p.N + 127) >> 7; }
+// Units of work of an item: tiles of committed positions, the first of them together
+// with the nodes (kA4Warps times 16 at most).
 __device__ __forceinline__ int attn4_units(const Attn4Params& p, int base) {
   const int len = attn4_len(p, base);
-  return len < 0 ? 0 : attn4_node_tiles(p) - 1 + max(1, len / kA4Tile + (len % kA4Tile != 0));
+  return len < 0 ? 0 : max(1, len / kA4Tile + (len % kA4Tile != 0));
 }
 
 // A CTA's run of units is cut into segments, one per item it meets.
@@ -251,7 +250,6 @@ __global__ void __launch_bounds__(kA4Threads, a4_per_sm<NT>())
     }
   }
   __syncthreads();
-  const int lead = attn4_node_tiles(p) - 1;  // units before the first tile of positions
   const int page = 1 << p.lg;
 
   // ---------------- copies ----------------
@@ -275,8 +273,8 @@ __global__ void __launch_bounds__(kA4Threads, a4_per_sm<NT>())
     Attn4Seg s;
     bool some = false;
     while (!some && w.next(p, &s, warp == 0 && lane == 0)) {
-      c_at = max(s.t0 - lead, 0) * kA4Tile + warp * kA4Step;
-      c_end = min(s.len, (s.t0 + s.n - lead) * kA4Tile);
+      c_at = s.t0 * kA4Tile + warp * kA4Step;
+      c_end = min(s.len, (s.t0 + s.n) * kA4Tile);
       c_h = s.h;
       c_row = p.table + (size_t)s.b * p.W;
       some = c_at < c_end;
@@ -423,98 +421,93 @@ __global__ void __launch_bounds__(kA4Threads, a4_per_sm<NT>())
         }
     };
 
-#pragma unroll 1
-    for (int u = seg.t0; u < min(seg.t0 + seg.n, lead + 1); ++u) {
+    // ---- 16 nodes ----
+    const int u0 = warp * 16;
+    if (seg.t0 == 0 && u0 < p.N) {
+      const size_t node0 = (size_t)seg.b * p.N;
+      const size_t stride = (size_t)p.Hkv * D;
+      float s[1][NT][4];
+#pragma unroll
+      for (int i = 0; i < NT; ++i) s[0][i][0] = s[0][i][1] = s[0][i][2] = s[0][i][3] = 0.0f;
+      const int n0 = u0 + pi, n1 = n0 + 8;
+      bool bad0 = false, bad1 = false;
       {
-        // ---- 16 nodes ----
-        const int u0 = u * 128 + warp * 16;
-        if (u0 < p.N) {
-          const size_t node0 = (size_t)seg.b * p.N;
-          const size_t stride = (size_t)p.Hkv * D;
-          float s[1][NT][4];
+        const uint16_t* k0 = p.nk + (node0 + min(n0, p.N - 1)) * stride + seg.h * D + kCh * t;
+        const uint16_t* k1 = p.nk + (node0 + min(n1, p.N - 1)) * stride + seg.h * D + kCh * t;
 #pragma unroll
-          for (int i = 0; i < NT; ++i) s[0][i][0] = s[0][i][1] = s[0][i][2] = s[0][i][3] = 0.0f;
-          const int n0 = u0 + pi, n1 = n0 + 8;
-          bool bad0 = false, bad1 = false;
-          {
-            const uint16_t* k0 = p.nk + (node0 + min(n0, p.N - 1)) * stride + seg.h * D + kCh * t;
-            const uint16_t* k1 = p.nk + (node0 + min(n1, p.N - 1)) * stride + seg.h * D + kCh * t;
+        for (int j = 0; j < kSteps; j += 2) {
+          const uint4 x = *reinterpret_cast<const uint4*>(k0 + 4 * j);
+          const uint4 y = *reinterpret_cast<const uint4*>(k1 + 4 * j);
+          const uint32_t a0[4] = {node_half2(x.x, kinv, bad0), node_half2(y.x, kinv, bad1),
+                                  node_half2(x.y, kinv, bad0), node_half2(y.y, kinv, bad1)};
+          const uint32_t a1[4] = {node_half2(x.z, kinv, bad0), node_half2(y.z, kinv, bad1),
+                                  node_half2(x.w, kinv, bad0), node_half2(y.w, kinv, bad1)};
 #pragma unroll
-            for (int j = 0; j < kSteps; j += 2) {
-              const uint4 x = *reinterpret_cast<const uint4*>(k0 + 4 * j);
-              const uint4 y = *reinterpret_cast<const uint4*>(k1 + 4 * j);
-              const uint32_t a0[4] = {node_half2(x.x, kinv, bad0), node_half2(y.x, kinv, bad1),
-                                      node_half2(x.y, kinv, bad0), node_half2(y.y, kinv, bad1)};
-              const uint32_t a1[4] = {node_half2(x.z, kinv, bad0), node_half2(y.z, kinv, bad1),
-                                      node_half2(x.w, kinv, bad0), node_half2(y.w, kinv, bad1)};
-#pragma unroll
-              for (int i = 0; i < NT; ++i) {
-                mma_16816(s[0][i], a0, qf[i][j][0], qf[i][j][1]);
-                mma_16816(s[0][i], a1, qf[i][j + 1][0], qf[i][j + 1][1]);
-              }
-            }
+          for (int i = 0; i < NT; ++i) {
+            mma_16816(s[0][i], a0, qf[i][j][0], qf[i][j][1]);
+            mma_16816(s[0][i], a1, qf[i][j + 1][0], qf[i][j + 1][1]);
           }
-          // values: this thread's four nodes 4 i + t of the 16, channels kCv g ..;
-          // looked at first, and loaded once more for their product
-          const uint16_t* vrow[4];
-          unsigned badv = 0;
+        }
+      }
+      // values: this thread's four nodes 4 i + t of the 16, channels kCv g ..;
+      // looked at first, and loaded once more for their product
+      const uint16_t* vrow[4];
+      unsigned badv = 0;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            vrow[i] = p.nv + (node0 + min(u0 + 4 * i + t, p.N - 1)) * stride + seg.h * D + kCv * g;
-            bool bad = false;
+      for (int i = 0; i < 4; ++i) {
+        vrow[i] = p.nv + (node0 + min(u0 + 4 * i + t, p.N - 1)) * stride + seg.h * D + kCv * g;
+        bool bad = false;
 #pragma unroll
-            for (int c = 0; c < kCv; c += 8) {
-              const uint4 x = *reinterpret_cast<const uint4*>(vrow[i] + c);
-              bad |= bf16_inf(x.x) || bf16_inf(x.y) || bf16_inf(x.z) || bf16_inf(x.w);
-            }
-            badv |= bad ? 1u << (4 * i + t) : 0u;
-          }
-          // entries with an element that is not finite: their values count as 0
-          // here, and the scores of the rows that see them become NaN
-          badv |= (bad0 ? 1u << pi : 0u) | (bad1 ? 1u << (pi + 8) : 0u);
-          badv = __reduce_or_sync(0xffffffffu, badv);
+        for (int c = 0; c < kCv; c += 8) {
+          const uint4 x = *reinterpret_cast<const uint4*>(vrow[i] + c);
+          bad |= bf16_inf(x.x) || bf16_inf(x.y) || bf16_inf(x.z) || bf16_inf(x.w);
+        }
+        badv |= bad ? 1u << (4 * i + t) : 0u;
+      }
+      // entries with an element that is not finite: their values count as 0
+      // here, and the scores of the rows that see them become NaN
+      badv |= (bad0 ? 1u << pi : 0u) | (bad1 ? 1u << (pi + 8) : 0u);
+      badv = __reduce_or_sync(0xffffffffu, badv);
 #pragma unroll
-          for (int i = 0; i < NT; ++i)
+      for (int i = 0; i < NT; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int v = vis[i][e & 1], nn = e < 2 ? n0 : n1;
-              bool see = nn < p.N;
-              if (see)
-                see = p.mask ? (p.mask[(node0 + v) * p.Wm + (nn >> 5)] >> (nn & 31)) & 1 : nn <= v;
-              const bool bad = (badv >> (e < 2 ? pi : pi + 8)) & 1;
-              if (!see || bad) s[0][i][e] = see ? __int_as_float(0x7FC00000) : -INFINITY;
-            }
-          uint32_t w[1][NT][2];
-          weights(s, w);
+        for (int e = 0; e < 4; ++e) {
+          const int v = vis[i][e & 1], nn = e < 2 ? n0 : n1;
+          bool see = nn < p.N;
+          if (see)
+            see = p.mask ? (p.mask[(node0 + v) * p.Wm + (nn >> 5)] >> (nn & 31)) & 1 : nn <= v;
+          const bool bad = (badv >> (e < 2 ? pi : pi + 8)) & 1;
+          if (!see || bad) s[0][i][e] = see ? __int_as_float(0x7FC00000) : -INFINITY;
+        }
+      uint32_t w[1][NT][2];
+      weights(s, w);
 #pragma unroll
-          for (int c = 0; c < kCv; c += 8) {
-            uint32_t h[4][4];
+      for (int c = 0; c < kCv; c += 8) {
+        uint32_t h[4][4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint4 x = *reinterpret_cast<const uint4*>(vrow[i] + c);
-              if ((badv >> (4 * i + t)) & 1) x = make_uint4(0, 0, 0, 0);
-              bool dummy = false;
-              h[i][0] = node_half2(x.x, vinv, dummy);
-              h[i][1] = node_half2(x.y, vinv, dummy);
-              h[i][2] = node_half2(x.z, vinv, dummy);
-              h[i][3] = node_half2(x.w, vinv, dummy);
-            }
+        for (int i = 0; i < 4; ++i) {
+          uint4 x = *reinterpret_cast<const uint4*>(vrow[i] + c);
+          if ((badv >> (4 * i + t)) & 1) x = make_uint4(0, 0, 0, 0);
+          bool dummy = false;
+          h[i][0] = node_half2(x.x, vinv, dummy);
+          h[i][1] = node_half2(x.y, vinv, dummy);
+          h[i][2] = node_half2(x.z, vinv, dummy);
+          h[i][3] = node_half2(x.w, vinv, dummy);
+        }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const uint32_t a[4] = {prmt(h[0][j], h[1][j], 0x5410), prmt(h[0][j], h[1][j], 0x7632),
-                                     prmt(h[2][j], h[3][j], 0x5410), prmt(h[2][j], h[3][j], 0x7632)};
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t a[4] = {prmt(h[0][j], h[1][j], 0x5410), prmt(h[0][j], h[1][j], 0x7632),
+                                 prmt(h[2][j], h[3][j], 0x5410), prmt(h[2][j], h[3][j], 0x7632)};
 #pragma unroll
-              for (int i = 0; i < NT; ++i) mma_16816(o[i][c / 2 + j], a, w[0][i][0], w[0][i][1]);
-            }
-          }
+          for (int i = 0; i < NT; ++i) mma_16816(o[i][c / 2 + j], a, w[0][i][0], w[0][i][1]);
         }
       }
     }
 
     // ---- 32 committed positions ----
-    const int len = seg.len, end = min(len, (seg.t0 + seg.n - lead) * kA4Tile);
+    const int len = seg.len, end = min(len, (seg.t0 + seg.n) * kA4Tile);
 #pragma unroll 1
-    for (int at = max(seg.t0 - lead, 0) * kA4Tile + warp * kA4Step; at < end && !dead; at += kA4Tile) {
+    for (int at = seg.t0 * kA4Tile + warp * kA4Step; at < end && !dead; at += kA4Tile) {
       if (!__all_sync(0xffffffffu, mbar_wait_bounded(&full[warp][stage], phase, p.wait_ns))) {
         dead = true;
         if (lane == 0) set_flag(p.flags, kFlagTimeout);

@@ -575,8 +575,6 @@ __global__ void __launch_bounds__(kAtqThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_full);
       const int t_nodes = max(0, seg.plen / kAtKeys - seg.t0);  // the first tile with nodes
-      int asked = t_nodes;  // this group's tiles whose nodes are asked for, or that have none
-      int t = 0;
 #pragma unroll 1
       for (int i = 0; i < 2 * seg.n; ++i) {
         int ti, vi;
@@ -585,9 +583,8 @@ __global__ void __launch_bounds__(kAtqThreads, 1)
         // a tile with nodes: they are in it already (and 0 behind the last)
         const bool nodes = ti >= t_nodes, paged = key0 < seg.plen;
         if (vi == is_v) {
-          t = ti;
           uint8_t* tile = ring + stage * kTile;
-          if (nodes && asks && asked <= t) {
+          if (nodes && asks) {
             if (atq_wait(p, &empty[stage], phase ^ 1u, abort)) {
               uint64_t* bar = &node_full[is_v][nasked++ % kAtqTurns];
               mbar_expect_tx(bar, kTile);
@@ -597,7 +594,6 @@ __global__ void __launch_bounds__(kAtqThreads, 1)
             } else {
               fail();
             }
-            asked = t + 1;
           }
           __syncwarp();
           if (!(nodes ? atq_wait_warp(p, &node_full[is_v][nput % kAtqTurns], (nput / kAtqTurns) & 1, abort)
