@@ -690,8 +690,8 @@ struct Attn4Plan {
 };
 // Few rows (matrix instructions from registers, no unpacked tiles) against the
 // tensor cores' tiles, 64 sequences of about 3000 positions, 8 key-value heads:
-// D = 128, 8 rows 72 us against 186, 16 rows 113 / 187, 24 rows 146 / 190; D = 64,
-// 52 / 158, 86 / 157, 104 / 158; 2 sequences of 22000, D = 128, 24 rows 48 / 58.
+// D = 128, 8 rows 71 us against 186, 16 rows 113 / 187, 24 rows 140-146 / 190; D = 64,
+// 53 / 158, 87 / 157, 105 / 158; 2 sequences of 22000, D = 128, 24 rows 48 / 58.
 constexpr int kA4MaxRows = 24;
 static_assert(kA4MaxRows <= 16 * sv::kA4Warps, "an item's nodes are its first unit's");
 

@@ -23,11 +23,19 @@
 // weight, or 2^-32 of the largest), queries, brought into its range by a power of
 // two per row, lose bits only in elements below 2^-31 of the row's largest.
 //
-// Bound: instructions, about 700 for a warp's 32 positions at D = 128 (unpacking,
-// scaling and products).  Measured: decoding 64 sequences of up to 4096 positions,
-// 32 heads of 8, 69-72 us where the packed bytes (229 MB) take 34 at the copy rate
-// and the bf16 cache takes its kernel 134; 16 positions a step 104 us, 32 with more
-// registers 77.  One chain of 5 over 300 positions: 10.6 us of kernels.
+// Bound: latency.  A warp's 32 positions are about 700 instructions at D = 128
+// (unpacking, scaling and products), one chain of wait, unpack, product, exponentials,
+// unpack, product, and registers leave four warps a scheduler to overlap them (two
+// from 9 rows on).  Decoding, while an SM is busy: 54% of the issue slots, the integer
+// and logic unit, the busiest, 48%, DRAM 43%; of 6.9 cycles between a warp's
+// instructions 1.5 are waits for results of fixed latency, 1.0 barriers of the joins,
+// 0.8 a busy unit, 0.5 loads; and SMs are busy for 84% of the kernel's time.
+// Measured: decoding 64 sequences of up to 4096 positions, 32 heads of 8, 69-72 us
+// where the packed bytes (229 MB) take 34 at the copy rate and the bf16 cache takes
+// its kernel 134 (D = 64: 52, 17 and 110); 16 positions a step 104 us, 32 with more
+// registers 77.  Chains of 3 and 4 nodes (12 and 16 rows) 113 us, of 5 and 6 (20 and
+// 24) 140 (the bf16 cache 136 and 138; D = 64: 87 and 105, 112 and 113).  One chain of 5
+// over 300 positions: 10.6 us of kernels.
 #pragma once
 
 #include "sv_attn.cuh"

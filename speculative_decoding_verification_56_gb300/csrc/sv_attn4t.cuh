@@ -15,8 +15,11 @@
 // Bound: products, 4 N Hq D len operations (2048 clocks a pair of half tiles at
 // D = 128), more than the pages' bytes.  Measured (D = 128, 8 key-value heads):
 // 16 trees of 60 nodes, 32 heads, up to 4096 positions 87-91 us (products 25 us at
-// the library's rate, the bf16 kernel 69); 3 trees of 33, 40 heads, up to 65536
-// positions 154-184 us (52; bf16 129).  About 4700 clocks a tile, two chains of
+// the library's rate, the bf16 kernel 68; D = 64: 69, 13 and 57); 3 trees of 33, 40
+// heads, up to 65536 positions 154-184 us (52; bf16 129; D = 64: 142, 23 and 109); 64
+// chains of 8 nodes 183 us (35, the bytes; bf16 141).  A chunk of 1000 nodes behind
+// each of 4 prompts of up to 4096, D = 128: 402 us (121; bf16 290), of which a chain's
+// tiles of nodes that its rows do not see are computed all the same; alone 62.  About 4700 clocks a tile, two chains of
 // scores (512), softmax (2050-2400 beside the warps that unpack) and output (512)
 // with their hand-overs; and the hand-over of a place of the ring, 2300 clocks
 // from the products that free it to the products that read it: query and unpacked
@@ -25,7 +28,8 @@
 // converted in place (115 / 222); no per-entry branches, and loops small enough
 // for the instruction caches, which five roles share (96 / 169); the issuing warp
 // as a whole (91); eight warps that unpack instead of four (87, long 173); every
-// tile waited for right before its use (87-92, long 173 -> 157 in turns).
+// tile waited for right before its use (87-92, long 173 -> 157 in turns); waits of one
+// loop, by the clock (90.5 -> 88.8, long 177 -> 173 in turns).
 #pragma once
 
 #include "sv_attn4.cuh"

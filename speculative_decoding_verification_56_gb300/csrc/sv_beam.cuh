@@ -18,7 +18,8 @@
 //
 // Measured: 64 requests of 8 beams, V = 128256 bf16 (115 MB of live beams), 38 us:
 // rows 26-27 (4.3 TB/s, instructions), select 11 (a chain of dependent loads and
-// exchanges); 4 beams of one request 10.4 us.  The sorted lists of tree growth, one
+// exchanges); 4 beams of one request 10.4-11.4 us.  float32 (230 MB) 56; V = 128255 of
+// bf16, no whole number of vectors, 69 (a CTA a chunk and plain loads; float32 56).  The sorted lists of tree growth, one
 // per thread, took 40.6 us for the rows; a selection that reads the best runs one
 // after the other 24 us, and all of a row's M at once 18.
 //
